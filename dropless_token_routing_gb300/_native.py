@@ -65,6 +65,18 @@ class LayerGrads(ctypes.Structure):
                 ("dws2", c_void_p), ("dw_r", c_void_p), ("dlogits", c_void_p)]
 
 
+class LinearDims(ctypes.Structure):
+    _fields_ = [("M", c_int64), ("N", c_int32), ("K", c_int32), ("act", c_int32), ("dtype", c_int32),
+                ("ld_x", c_int64), ("ld_w", c_int64), ("ld_y", c_int64), ("ld_res", c_int64)]
+
+
+class VerifyDims(ctypes.Structure):
+    _fields_ = [("B", c_int64), ("n", c_int32), ("V", c_int32), ("dtype", c_int32), ("ld_draft", c_int64),
+                ("ld_target", c_int64)]
+
+
+ACTS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}   # enum moe_act
+
 P = c_void_p
 _SIGS = {
     "moe_status_string": (ctypes.c_char_p, [c_int]),
@@ -96,6 +108,14 @@ _SIGS = {
                               ctypes.POINTER(LayerSaved), P, P, c_size_t, P]),
     "moe_layer_bwd": (c_int, [ctypes.POINTER(LayerParams), ctypes.POINTER(LayerSaved), P, P,
                               ctypes.POINTER(MoeDims), ctypes.POINTER(LayerGrads), P, c_size_t, P]),
+    "moe_op_workspace_init": (c_int, [P, c_size_t, P]),
+    "moe_decode_workspace_bytes": (c_size_t, [ctypes.POINTER(MoeDims)]),
+    "moe_layer_decode": (c_int, [ctypes.POINTER(LayerParams), P, P, P, ctypes.POINTER(MoeDims), P, P, P, P, c_size_t,
+                                 P]),
+    "moe_linear_workspace_bytes": (c_size_t, [ctypes.POINTER(LinearDims)]),
+    "moe_linear_fwd": (c_int, [P, P, P, P, ctypes.POINTER(LinearDims), P, P, P, c_size_t, P]),
+    "moe_linear_bwd": (c_int, [P, P, P, P, ctypes.POINTER(LinearDims), P, P, P, P, c_size_t, P]),
+    "moe_verify_draft": (c_int, [P, P, P, P, P, P, ctypes.POINTER(VerifyDims), P, P, P]),
     "moe_debug_timeout_probe": (c_int, [P, c_size_t, c_uint64, P]),
     "moe_trace_enable": (c_int, [c_int]),
     "moe_trace_read": (c_int, [ctypes.POINTER(TraceEntry), c_int, ctypes.POINTER(c_int)]),

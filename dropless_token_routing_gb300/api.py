@@ -12,7 +12,8 @@ from . import _native as N
 
 __all__ = ["make_dims", "Workspace", "router_logits", "route_topk", "permute", "permute_rows",
            "grouped_swiglu_fwd", "unpermute_combine", "grouped_bwd_dx", "grouped_bwd_dw",
-           "route_topk_bwd", "LayerParams", "MoELayer", "get_device_error", "debug_timeout_probe"]
+           "route_topk_bwd", "LayerParams", "MoELayer", "get_device_error", "debug_timeout_probe",
+           "OpWorkspace", "MoEDecodeLayer", "Linear", "DraftVerifier"]
 
 
 def _p(t: Optional[torch.Tensor]):
@@ -254,3 +255,189 @@ class MoELayer:
                                       ctypes.byref(self.dims), ctypes.byref(gc), self.ws.ptr,
                                       self.ws.nbytes, _s(stream)), "moe_layer_bwd")
         return g
+
+
+# ------------------------------------------------------------------ few-token operators
+class OpWorkspace:
+    """Device workspace of a few-token operator: its header is zeroed once, here."""
+
+    def __init__(self, nbytes: int, call: str, device="cuda", stream=None):
+        if nbytes == 0:
+            raise N.MoeError(N.STATUS_CODE["MOE_ERR_BAD_DIMS"], call)
+        self.nbytes = int(nbytes)
+        self.buf = torch.empty(self.nbytes + 256, dtype=torch.uint8, device=device)
+        self.ptr = self.buf.data_ptr() + (-self.buf.data_ptr()) % 256
+        N.check(N.lib().moe_op_workspace_init(self.ptr, self.nbytes, _s(stream)), "moe_op_workspace_init")
+
+
+def _matrix(t, name, dtype, rows, cols):
+    """Checks a [rows, cols] operand with contiguous rows; returns the stride between them."""
+    if t.dtype != dtype or t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols:
+        raise ValueError(f"{name}: expected [{rows}, {cols}] of {dtype}, got {list(t.shape)} of {t.dtype}")
+    if cols > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name}: the elements of a row must be contiguous")
+    return t.stride(0) if rows > 1 else max(cols, t.stride(0))
+
+
+def _dense(t, name, dtype, shape):
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise ValueError(f"{name}: expected contiguous {list(shape)} of {dtype}, got {list(t.shape)} of {t.dtype}")
+
+
+class MoEDecodeLayer:
+    """The whole MoE layer for a few tokens: moe_layer_decode on a kept workspace.
+
+    ``forward(x, residual=None)`` takes 0 to ``max_tokens`` (at most 64) tokens and returns
+    y [T, d], the layer's own buffer (overwritten by the next call) unless ``out`` is given
+    (x and residual are allowed). ``topk_idx`` and ``topk_w`` hold the last call's selection.
+    One instance serves one stream at a time.
+    """
+
+    def __init__(self, params: LayerParams, max_tokens, d, E, k, f, S=0, f_s=0, dtype=torch.bfloat16,
+                 device="cuda", stream=None):
+        self.params, self.dtype, self.max_tokens, self.d, self.E, self.k = params, dtype, max_tokens, d, E, k
+        self.dims = make_dims(max_tokens, d, E, k, f, S, f_s, dtype)
+        self.ws = OpWorkspace(N.lib().moe_decode_workspace_bytes(ctypes.byref(self.dims)), "moe_decode_workspace_bytes",
+                              device, stream)
+        self._idx = torch.empty(max_tokens, k, dtype=torch.int32, device=device)
+        self._w = torch.empty(max_tokens, k, dtype=torch.float32, device=device)
+        self._y = torch.empty(max_tokens, d, dtype=dtype, device=device)
+        self._c = params.c()
+        self._T = 0
+
+    @property
+    def topk_idx(self):
+        return self._idx[:self._T]
+
+    @property
+    def topk_w(self):
+        return self._w[:self._T]
+
+    def forward(self, x, residual=None, logits_in=None, out=None, stream=None):
+        T, d, dt = x.shape[0], self.d, self.dtype
+        if T > self.max_tokens:
+            raise ValueError(f"x: {T} tokens, the layer was made for {self.max_tokens}")
+        _dense(x, "x", dt, (T, d))
+        if residual is not None:
+            _dense(residual, "residual", dt, (T, d))
+        if logits_in is not None:
+            _dense(logits_in, "logits_in", torch.float32, (T, self.E))
+        if out is None:
+            out = self._y[:T]
+        else:
+            _dense(out, "out", dt, (T, d))
+        self._T = self.dims.T = T
+        N.check(N.lib().moe_layer_decode(ctypes.byref(self._c), x.data_ptr(), _p(logits_in), _p(residual),
+                                         ctypes.byref(self.dims), self._idx.data_ptr(), self._w.data_ptr(),
+                                         out.data_ptr(), self.ws.ptr, self.ws.nbytes, _s(stream)), "moe_layer_decode")
+        return out
+
+
+class Linear:
+    """y = act(x W^T + b) + residual and its gradients: moe_linear_fwd / moe_linear_bwd on a kept
+    workspace for up to ``max_rows`` rows. ``w`` [N, K] may have strided rows.
+
+    ``forward(x, residual=None, save=False)`` returns y [M, N], the layer's own buffer
+    (overwritten by the next call) unless ``out`` is given; with ``save=True`` it keeps x and the
+    pre-activation for ``backward(dy)``, which returns dict(dx, dw, db) (own buffers too; ``need``
+    names those to compute). The residual's gradient is dy itself.
+    """
+
+    def __init__(self, w, bias=None, act="none", max_rows=1, device=None, stream=None):
+        self.w, self.bias, self.dtype, self.max_rows = w, bias, w.dtype, max_rows
+        self.N, self.K = w.shape
+        self.act = N.ACTS[act]
+        dev = self.device = device if device is not None else w.device
+        ld_w = _matrix(w, "w", w.dtype, self.N, self.K)
+        if bias is not None:
+            _dense(bias, "bias", w.dtype, (self.N,))
+        self.dims = N.LinearDims(int(max_rows), self.N, self.K, self.act, _dt(w.dtype), 0, ld_w, 0, 0)
+        self.ws = OpWorkspace(N.lib().moe_linear_workspace_bytes(ctypes.byref(self.dims)), "moe_linear_workspace_bytes",
+                              dev, stream)
+        self._x = None
+        self._bufs = {}
+
+    def _own(self, name, rows, cols):
+        """The layer's buffer ``name``, made at its first use."""
+        t = self._bufs.get(name)
+        if t is None:
+            t = self._bufs[name] = torch.empty(rows, cols, dtype=self.dtype, device=self.device)
+        return t
+
+    def _rows(self, M):
+        if M > self.max_rows:
+            raise ValueError(f"{M} rows, the layer was made for {self.max_rows}")
+
+    def forward(self, x, residual=None, save=False, out=None, stream=None):
+        M, D = x.shape[0], self.dims
+        self._rows(M)
+        D.M, D.ld_x = M, _matrix(x, "x", self.dtype, M, self.K)
+        D.ld_res = _matrix(residual, "residual", self.dtype, M, self.N) if residual is not None else 0
+        if out is None:
+            out = self._own("y", self.max_rows, self.N)[:M]
+        D.ld_y = _matrix(out, "out", self.dtype, M, self.N)
+        z = self._own("z", self.max_rows, self.N) if save and self.act != 0 else None
+        self._x = x if save else None
+        N.check(N.lib().moe_linear_fwd(x.data_ptr(), self.w.data_ptr(), _p(self.bias), _p(residual), ctypes.byref(D),
+                                       _p(z), out.data_ptr(), self.ws.ptr, self.ws.nbytes, _s(stream)),
+                "moe_linear_fwd")
+        return out
+
+    def backward(self, dy, need=("dx", "dw", "db"), stream=None):
+        x, D = self._x, self.dims
+        if x is None:
+            raise ValueError("backward: the last forward did not save (save=True)")
+        M = x.shape[0]
+        D.M, D.ld_x, D.ld_res = M, _matrix(x, "x", self.dtype, M, self.K), 0
+        D.ld_y = _matrix(dy, "dy", self.dtype, M, self.N)
+        ld_w = D.ld_w
+        dx = dw = db = None
+        if "dx" in need:   # rows of dx are as far apart as those of x
+            dx = self._own(("dx", D.ld_x), self.max_rows, D.ld_x)[:M, :self.K]
+        if "dw" in need:
+            dw = self._own(("dw", ld_w), self.N, ld_w)[:, :self.K]
+        if "db" in need and self.bias is not None:
+            db = self._own("db", 1, self.N)[0]
+        z = self._own("z", self.max_rows, self.N) if self.act != 0 else None
+        N.check(N.lib().moe_linear_bwd(x.data_ptr(), self.w.data_ptr(), _p(z), dy.data_ptr(), ctypes.byref(D), _p(dx),
+                                       _p(dw), _p(db), self.ws.ptr, self.ws.nbytes, _s(stream)), "moe_linear_bwd")
+        return dict(dx=dx, dw=dw, db=db)
+
+
+class DraftVerifier:
+    """Verification of drafted tokens (moe_verify_draft) for up to ``max_batch`` sequences of
+    ``n`` drafted tokens each; returns (tokens [B, n+1], accepted [B]), own buffers."""
+
+    def __init__(self, max_batch, n, V, dtype=torch.float32, device="cuda"):
+        self.max_batch, self.n, self.V, self.dtype = max_batch, n, V, dtype
+        self.dims = N.VerifyDims(0, n, V, _dt(dtype), 0, 0)
+        self._tokens = torch.empty(max_batch, n + 1, dtype=torch.int32, device=device)
+        self._accepted = torch.empty(max_batch, dtype=torch.int32, device=device)
+
+    def _rows(self, t, name, B, rows):
+        if t.dtype != self.dtype or tuple(t.shape) != (B, rows, self.V):
+            raise ValueError(f"{name}: expected [{B}, {rows}, {self.V}] of {self.dtype}, got {list(t.shape)} of {t.dtype}")
+        ld = t.stride(1) if rows > 1 else (t.stride(0) if B > 1 else self.V)
+        if (self.V > 1 and t.stride(2) != 1) or (B > 1 and rows > 0 and t.stride(0) != rows * ld) or ld < self.V:
+            raise ValueError(f"{name}: rows must be contiguous and evenly spaced")
+        return ld
+
+    def verify(self, draft_tokens, draft_probs, target_probs, u_accept, u_sample, draft_len=None, stream=None):
+        B, n = draft_tokens.shape[0], self.n
+        if B > self.max_batch:
+            raise ValueError(f"{B} sequences, made for {self.max_batch}")
+        _dense(draft_tokens, "draft_tokens", torch.int32, (B, n))
+        _dense(u_accept, "u_accept", torch.float32, (B, n))
+        _dense(u_sample, "u_sample", torch.float32, (B,))
+        if draft_len is not None:
+            _dense(draft_len, "draft_len", torch.int32, (B,))
+        D = self.dims
+        D.B = B
+        D.ld_draft = self._rows(draft_probs, "draft_probs", B, n)
+        D.ld_target = self._rows(target_probs, "target_probs", B, n + 1)
+        tokens, accepted = self._tokens[:B], self._accepted[:B]
+        N.check(N.lib().moe_verify_draft(draft_tokens.data_ptr(), _p(draft_len), draft_probs.data_ptr(),
+                                         target_probs.data_ptr(), u_accept.data_ptr(), u_sample.data_ptr(),
+                                         ctypes.byref(D), tokens.data_ptr(), accepted.data_ptr(), _s(stream)),
+                "moe_verify_draft")
+        return tokens, accepted

@@ -216,6 +216,10 @@ int dgate_tiles(const moe_dims* d) {
 }  // namespace
 }  // namespace moe
 
+namespace moe {
+int check_layer_dims(const moe_dims* dims) { return check_dims(dims); }
+}  // namespace moe
+
 using namespace moe;
 
 extern "C" {

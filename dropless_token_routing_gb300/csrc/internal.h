@@ -61,6 +61,9 @@ struct WsLayout {
 
 WsLayout ws_layout(const moe_dims& d);
 
+// The argument checks every layer call makes of its dims (MOE_OK or the status).
+int check_layer_dims(const moe_dims* dims);
+
 // launchers (return the launch's cudaError_t)
 cudaError_t launch_router_logits(const void* x, const float* w_r, const moe_dims& dm, float* logits,
                                  cudaStream_t st);

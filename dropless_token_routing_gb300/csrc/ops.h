@@ -1,0 +1,81 @@
+// Host-side internals of the few-token operators: workspace layouts and kernel launchers.
+#pragma once
+
+#include "internal.h"
+
+namespace moe {
+
+constexpr size_t kOpHeader = 4096;    // error word, launch counters and flags
+constexpr int kDecodeMaxT = 64;       // tokens of moe_layer_decode
+
+inline size_t round256(size_t x) { return (x + 255) & ~size_t(255); }
+
+// ------------------------------------------------------------------ decode
+struct DecodeLayout {
+  size_t logits;     // [T][E] fp32
+  size_t idx;        // [T][k] int32
+  size_t gate;       // [T][k] fp32
+  size_t counts;     // [E] int32
+  size_t h;          // [T*k][f] then [S*T][f_s] fp32: hidden rows times their gates
+  size_t total;
+};
+DecodeLayout decode_layout(const moe_dims& d);
+
+struct DecodeArgs {
+  const void *x, *residual;
+  const float *w_r, *bias, *logits_in;
+  const void *w13, *w2, *ws13, *ws2;
+  int32_t* idx_out;
+  float* gate_out;
+  void* y;
+  uint8_t* ws;
+  DecodeLayout L;
+  moe_dims dm;
+};
+int launch_decode_simt(const DecodeArgs& a, int num_sms, cudaStream_t st);
+
+// ------------------------------------------------------------------ linear
+struct LinearLayout {
+  size_t dz;         // [M][ld_dz] the pre-activation's gradient, dims->dtype
+  size_t db_part;    // [kDbSplit][N] fp32
+  int64_t ld_dz;
+  size_t total;
+};
+constexpr int kDbSplit = 64;
+LinearLayout linear_layout(const moe_linear_dims& d);
+
+// C [M, N] = A B^T, A (m, k) at a[m * am + k * ak], B (n, k) at b[n * bn + k * bk], one of the two
+// strides of each being 1; C (m, n) at c[m * ldc + n].
+struct GemmArgs {
+  const void *a, *b;
+  int64_t am, ak, bn, bk;
+  int64_t M;
+  int N;
+  int64_t K;
+  // epilogue: z = acc + bias[n]; z_out [M][N]; c = act(z) + res
+  const void* bias;
+  const void* res;
+  int64_t ld_res;
+  int act;
+  void* z_out;
+  void* c;
+  int64_t ldc;
+  int dtype;
+};
+cudaError_t launch_gemm_simt(const GemmArgs& g, cudaStream_t st);
+// dz = dy * act'(z) (dz may be NULL: sums only) and db (may be NULL)
+cudaError_t launch_linear_dz(const void* dy, int64_t ld_dy, const void* z, int act, int64_t M, int N,
+                             int dtype, void* dz, int64_t ld_dz, float* db_part, void* db, cudaStream_t st);
+
+// ------------------------------------------------------------------ verify
+struct VerifyArgs {
+  const int32_t *tokens, *len;
+  const void *q, *p;
+  const float *u_accept, *u_sample;
+  int32_t *out, *accepted;
+  int64_t B, ld_q, ld_p;
+  int n, V, dtype;
+};
+cudaError_t launch_verify(const VerifyArgs& v, int num_sms, cudaStream_t st);
+
+}  // namespace moe

@@ -13,7 +13,8 @@ const char* kPhaseNames[TP_COUNT] = {
     "router_gemm", "route_topk",  "permute_hist", "permute_scan", "permute_scatter",
     "gemm_fwd1",   "gemm_fwd2",   "combine",      "permute_rows", "gemm_bwd2t",
     "route_bwd",   "gemm_bwd1t",  "transpose",    "combine_bwd",  "gemm_dw2",
-    "gemm_dw13",   "dwr",         "misc"};
+    "gemm_dw13",   "dwr",         "misc",         "decode",       "linear",
+    "linear_dz",   "verify"};
 
 struct Rec {
   int phase;

@@ -25,6 +25,10 @@ enum TracePhase : int {
   TP_GEMM_DW13,
   TP_DWR,
   TP_MISC,
+  TP_DECODE,
+  TP_LINEAR,
+  TP_LINEAR_DZ,
+  TP_VERIFY,
   TP_COUNT
 };
 

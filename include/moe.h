@@ -341,6 +341,96 @@ int moe_layer_bwd(const moe_layer_params* params, const moe_layer_saved* saved, 
                   const void* dy, const moe_dims* dims, const moe_layer_grads* grads,
                   void* ws, size_t ws_bytes, moe_stream_t stream);
 
+/* ---------------------------------------------------------------- few-token operators */
+/* The calls below answer with a trained layer: a few tokens (one per user, or each user's drafted
+ * ones) pass through the dense projections and the layer, and the drafted ones are verified. The
+ * pages name serving the layer only in passing; the formulas are written out here. */
+
+/* Zero the 4 KB header (error word, launch counters and flags) of a workspace of the calls below
+ * (async). Once after allocating it; the calls leave the counters zeroed themselves. A workspace
+ * belongs to one call at a time: calls that share one have to be ordered on one stream.
+ * moe_get_device_error reads its error word. ws: 256-byte aligned, ws_bytes >= 4096. */
+int moe_op_workspace_init(void* ws, size_t ws_bytes, moe_stream_t stream);
+
+/* The whole layer for 0 <= dims->T <= 64 tokens (router, top-k, selected experts, shared experts,
+ * weighted sum), reading the weights of the selected experts only:
+ *   y_t = sum_{e in S_t} w_te SwiGLU_e(x_t) + sum_s SwiGLU_s(x_t) (+ residual_t)
+ * with the scores, S_t and w of moe_router_logits / moe_route_topk (fp32, ties to the lower
+ * index; scores must be finite). dims->capacity and dims->rearrange must be 0 (MOE_ERR_BAD_DIMS).
+ * x, residual (or NULL) -> y [T, d]; y may be the buffer of x or of residual.
+ * logits_in [T][E] fp32 replaces x W_r when given (w_r is not read then).
+ * topk_idx [T][k] int32 and topk_w [T][k] fp32 receive the selection (NULL: not returned).
+ * bf16 rounds h (times its gate) and y; fp32 rounds nothing. Sums are fp32 in a fixed order. */
+size_t moe_decode_workspace_bytes(const moe_dims* dims);
+int moe_layer_decode(const moe_layer_params* params, const void* x, const float* logits_in,
+                     const void* residual, const moe_dims* dims, int32_t* topk_idx, float* topk_w,
+                     void* y, void* ws, size_t ws_bytes, moe_stream_t stream);
+
+enum moe_act {
+  MOE_ACT_NONE = 0,
+  MOE_ACT_RELU = 1,     /* max(z, 0); derivative 0 at 0 */
+  MOE_ACT_SILU = 2,     /* z / (1 + exp(-z)) */
+  MOE_ACT_GELU = 3,     /* z (1 + erf(z / sqrt 2)) / 2 */
+  MOE_ACT_GELU_TANH = 4 /* z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))) / 2 */
+};
+
+typedef struct moe_linear_dims {
+  int64_t M;        /* rows (tokens), >= 0 */
+  int32_t N, K;     /* output and input width, >= 1; any value */
+  int32_t act;      /* enum moe_act */
+  int32_t dtype;    /* enum moe_dtype: x, w, bias, residual, y, z and every gradient */
+  int64_t ld_x;     /* elements between rows of x and dx (>= K), 0 = K */
+  int64_t ld_w;     /* ... of w and dw (>= K), 0 = K */
+  int64_t ld_y;     /* ... of y and dy (>= N), 0 = N */
+  int64_t ld_res;   /* ... of residual (>= N), 0 = N */
+} moe_linear_dims;
+
+/* Matrix product with bias, activation and residual in its epilogue:
+ *   z = x W^T + b,   y = act(z) + r        x [M, K], w [N][K], bias [N] or NULL, residual [M, N]
+ * or NULL, z [M][N] (contiguous) receives the pre-activation for the backward, or NULL.
+ * fp32 accumulation, y rounded once (not from the rounded z). residual may be the buffer of y
+ * (y updated in place) when their strides agree. Base pointers are 16-byte aligned; strides and
+ * widths may be odd. M == 0 is a no-op. */
+size_t moe_linear_workspace_bytes(const moe_linear_dims* dims);
+int moe_linear_fwd(const void* x, const void* w, const void* bias, const void* residual,
+                   const moe_linear_dims* dims, void* z, void* y, void* ws, size_t ws_bytes,
+                   moe_stream_t stream);
+
+/* Its gradients from dy [M, N]:
+ *   dz = dy * act'(z),  dx = dz W,  dw = dz^T x,  db = sum_m dz   (the residual's gradient is dy)
+ * z as written by moe_linear_fwd (required unless act is MOE_ACT_NONE). dx [M, K], dw [N][K],
+ * db [N]: each may be NULL (not computed); w is needed for dx, x for dw. With M == 0 dw and db
+ * are zeroed. bf16 rounds dz once before the two products; db sums the unrounded dz in fp32. */
+int moe_linear_bwd(const void* x, const void* w, const void* z, const void* dy,
+                   const moe_linear_dims* dims, void* dx, void* dw, void* db, void* ws,
+                   size_t ws_bytes, moe_stream_t stream);
+
+typedef struct moe_verify_dims {
+  int64_t B;         /* sequences, >= 0 */
+  int32_t n;         /* drafted tokens per sequence, 0 <= n <= 1024 */
+  int32_t V;         /* vocabulary, 1 <= V <= 2^22 */
+  int32_t dtype;     /* enum moe_dtype of both probability tensors */
+  int64_t ld_draft;  /* elements between rows of draft_probs (>= V), 0 = V */
+  int64_t ld_target; /* ... of target_probs */
+} moe_verify_dims;
+
+/* Verification of drafted tokens against the target's probabilities from given random numbers
+ * (the kept tokens are distributed as the target's own samples). Per sequence:
+ *   drafted token x_i is kept while u_i q_i(x_i) < p_i(x_i) (product rounded to fp32) and i < len;
+ *   after the first refusal, at a, one token is drawn from max(p_a - q_a, 0), after the last kept
+ *   token (a = len) from p_a: the smallest j with m_0 + .. + m_j > floor(u 2^24) M / 2^24, where
+ *   m_j are the fp32 weights clamped to [0, 1] (NaN: 0) and truncated to multiples of 2^-40, M
+ *   their sum: whole numbers, so no result depends on an order of summation.
+ * Without any weight in max(p - q, 0) the token is drawn from p_a; without any in p_a it is -1.
+ * draft_tokens [B][n] int32 (a token outside [0, V) is refused), draft_len [B] int32 or NULL (n
+ * for all; clamped to [0, n]), draft_probs [B][n][ld_draft], target_probs [B][n+1][ld_target],
+ * u_accept [B][n], u_sample [B] fp32 in [0, 1) -> tokens [B][n+1] int32 (kept tokens, the drawn
+ * one, then -1), accepted [B] int32 (kept drafted tokens). Tensors of size 0 may be NULL. */
+int moe_verify_draft(const int32_t* draft_tokens, const int32_t* draft_len, const void* draft_probs,
+                     const void* target_probs, const float* u_accept, const float* u_sample,
+                     const moe_verify_dims* dims, int32_t* tokens, int32_t* accepted,
+                     moe_stream_t stream);
+
 /* ---------------------------------------------------------------- tracing */
 /* Per-phase launch timing: while enabled, every kernel launch of the library is bracketed by
  * a pair of CUDA events on its stream (a few microseconds of host work per launch, no device

@@ -1,0 +1,141 @@
+"""Host-side refusals and workspace sizes of the few-token operators (CPU only: every call here
+fails validation or has nothing to do, so no CUDA API is touched)."""
+import ctypes
+import os
+
+import pytest
+
+from dropless_token_routing_gb300 import builder as B
+
+if not os.path.exists(B.LIB):
+    B.build()
+
+from dropless_token_routing_gb300 import _native as N  # noqa: E402
+
+L = N.lib()
+BAD, GOOD = 0x1008, 0x10000   # fake addresses, never dereferenced
+C = N.STATUS_CODE
+REF = ctypes.byref
+
+
+def layer_dims(**kw):
+    base = dict(T=4, d=512, E=8, k=2, f=256, S=0, f_s=0, dtype=N.MOE_BF16, capacity=0, rearrange=0)
+    base.update(kw)
+    return N.MoeDims(*base.values())
+
+
+def linear_dims(**kw):
+    base = dict(M=4, N=96, K=64, act=0, dtype=N.MOE_BF16, ld_x=0, ld_w=0, ld_y=0, ld_res=0)
+    base.update(kw)
+    return N.LinearDims(*base.values())
+
+
+def verify_dims(**kw):
+    base = dict(B=2, n=3, V=100, dtype=N.MOE_F32, ld_draft=0, ld_target=0)
+    base.update(kw)
+    return N.VerifyDims(*base.values())
+
+
+def test_workspace_init_is_checked():
+    assert L.moe_op_workspace_init(None, 4096, None) == C["MOE_ERR_NULL_POINTER"]
+    assert L.moe_op_workspace_init(GOOD + 16, 4096, None) == C["MOE_ERR_MISALIGNED"]
+    assert L.moe_op_workspace_init(GOOD, 4095, None) == C["MOE_ERR_WORKSPACE_TOO_SMALL"]
+
+
+@pytest.mark.parametrize("bad", [dict(T=65), dict(T=-1), dict(k=9), dict(d=96), dict(E=1025), dict(capacity=4),
+                                 dict(rearrange=1), dict(dtype=5), dict(S=9, f_s=64), dict(S=1, f_s=0)])
+def test_decode_dims(bad):
+    d = layer_dims(**bad)
+    assert L.moe_decode_workspace_bytes(REF(d)) == 0
+    p = N.LayerParams(GOOD, None, GOOD, GOOD, GOOD, GOOD)
+    assert L.moe_layer_decode(REF(p), GOOD, None, None, REF(d), None, None, GOOD, GOOD, 1 << 40, None) < 0
+
+
+def test_decode_workspace_grows_with_every_size():
+    base = dict(T=8, d=512, E=16, k=2, f=256, S=1, f_s=128)
+    n0 = L.moe_decode_workspace_bytes(REF(layer_dims(**base)))
+    assert n0 >= 4096
+    for name, v in (("T", 64), ("E", 1024), ("k", 8), ("f", 4096), ("S", 8), ("f_s", 4096)):
+        assert L.moe_decode_workspace_bytes(REF(layer_dims(**{**base, name: v}))) >= n0
+    assert L.moe_decode_workspace_bytes(REF(layer_dims(T=0))) >= 4096
+
+
+def test_decode_pointers():
+    d = layer_dims(S=1, f_s=64)
+    n = L.moe_decode_workspace_bytes(REF(d))
+    full = dict(w_r=GOOD, bias=None, w13=GOOD, w2=GOOD, ws13=GOOD, ws2=GOOD)
+
+    def call(x=GOOD, logits=None, res=None, idx=None, w=None, y=GOOD, ws=GOOD, nb=n, dims=d, **kw):
+        p = N.LayerParams(*{**full, **kw}.values())
+        return L.moe_layer_decode(REF(p), x, logits, res, REF(dims), idx, w, y, ws, nb, None)
+
+    null, mis = C["MOE_ERR_NULL_POINTER"], C["MOE_ERR_MISALIGNED"]
+    for name in ("x", "y", "w_r", "w13", "w2", "ws13", "ws2", "ws"):
+        assert call(**{name: None}) == null, name
+    for name in ("x", "logits", "res", "idx", "w", "y", "w_r", "bias", "w13", "w2", "ws13", "ws2"):
+        assert call(**{name: BAD}) == mis, name
+    assert call(ws=GOOD + 16) == mis
+    assert call(nb=n - 1) == C["MOE_ERR_WORKSPACE_TOO_SMALL"]
+    assert L.moe_layer_decode(None, GOOD, None, None, REF(d), None, None, GOOD, GOOD, n, None) == null
+    assert call(x=None, y=None, dims=layer_dims(T=0, S=1, f_s=64)) == 0   # nothing to do
+
+
+@pytest.mark.parametrize("bad,status", [
+    (dict(M=-1), "MOE_ERR_BAD_DIMS"), (dict(N=0), "MOE_ERR_BAD_DIMS"), (dict(K=0), "MOE_ERR_BAD_DIMS"),
+    (dict(act=5), "MOE_ERR_BAD_DIMS"), (dict(act=-1), "MOE_ERR_BAD_DIMS"), (dict(ld_x=63), "MOE_ERR_BAD_DIMS"),
+    (dict(ld_w=10), "MOE_ERR_BAD_DIMS"), (dict(ld_y=95), "MOE_ERR_BAD_DIMS"), (dict(ld_res=1), "MOE_ERR_BAD_DIMS"),
+    (dict(M=2**31), "MOE_ERR_BAD_DIMS"), (dict(dtype=2), "MOE_ERR_UNSUPPORTED_DTYPE")])
+def test_linear_dims(bad, status):
+    d = linear_dims(**bad)
+    assert L.moe_linear_workspace_bytes(REF(d)) == 0
+    assert L.moe_linear_fwd(GOOD, GOOD, None, None, REF(d), None, GOOD, GOOD, 1 << 40, None) == C[status]
+    assert L.moe_linear_bwd(GOOD, GOOD, GOOD, GOOD, REF(d), GOOD, GOOD, GOOD, GOOD, 1 << 40, None) == C[status]
+
+
+def test_linear_pointers():
+    d = linear_dims(act=N.ACTS["gelu"])
+    n = L.moe_linear_workspace_bytes(REF(d))
+    null, mis = C["MOE_ERR_NULL_POINTER"], C["MOE_ERR_MISALIGNED"]
+
+    def fwd(x=GOOD, w=GOOD, b=None, r=None, z=None, y=GOOD, ws=GOOD, nb=n, dims=d):
+        return L.moe_linear_fwd(x, w, b, r, REF(dims), z, y, ws, nb, None)
+
+    def bwd(x=GOOD, w=GOOD, z=GOOD, dy=GOOD, dx=GOOD, dw=GOOD, db=GOOD, ws=GOOD, nb=n, dims=d):
+        return L.moe_linear_bwd(x, w, z, dy, REF(dims), dx, dw, db, ws, nb, None)
+
+    for name in ("x", "w", "y", "ws"):
+        assert fwd(**{name: None}) == null, name
+    for name in ("x", "w", "b", "r", "z", "y"):
+        assert fwd(**{name: BAD}) == mis, name
+    for name in ("x", "w", "z", "dy", "ws"):
+        assert bwd(**{name: None}) == null, name
+    for name in ("x", "w", "z", "dy", "dx", "dw", "db"):
+        assert bwd(**{name: BAD}) == mis, name
+    assert fwd(nb=n - 1) == C["MOE_ERR_WORKSPACE_TOO_SMALL"] and bwd(nb=n - 1) == C["MOE_ERR_WORKSPACE_TOO_SMALL"]
+    assert fwd(x=None, y=None, dims=linear_dims(M=0)) == 0
+    assert bwd(x=None, z=None, dy=None, dx=None, dw=None, db=None, dims=linear_dims(M=0)) == 0
+
+
+@pytest.mark.parametrize("bad", [dict(B=-1), dict(n=-1), dict(n=1025), dict(V=0), dict(V=2**22 + 1), dict(ld_draft=99),
+                                 dict(ld_target=50)])
+def test_verify_dims(bad):
+    d = verify_dims(**bad)
+    assert L.moe_verify_draft(GOOD, None, GOOD, GOOD, GOOD, GOOD, REF(d), GOOD, GOOD, None) == C["MOE_ERR_BAD_DIMS"]
+
+
+def test_verify_pointers():
+    null, mis = C["MOE_ERR_NULL_POINTER"], C["MOE_ERR_MISALIGNED"]
+    order = ("tokens", "length", "q", "p", "u", "us")
+
+    def call(dims, out=GOOD, acc=GOOD, **kw):
+        a = {**dict.fromkeys(order, GOOD), "length": None, **kw}
+        return L.moe_verify_draft(*[a[k] for k in order], REF(dims), out, acc, None)
+
+    d = verify_dims()
+    for name in ("tokens", "q", "p", "u", "us", "out", "acc"):
+        assert call(d, **{name: None}) == null, name
+    for name in order + ("out", "acc"):
+        assert call(d, **{name: BAD}) == mis, name
+    assert call(verify_dims(dtype=9)) == C["MOE_ERR_UNSUPPORTED_DTYPE"]
+    assert call(verify_dims(n=0), tokens=None, q=None, u=None, p=None) == null
+    assert call(verify_dims(B=0), **dict.fromkeys(("tokens", "q", "p", "u", "us", "out", "acc"))) == 0

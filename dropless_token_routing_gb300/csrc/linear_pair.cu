@@ -1,0 +1,517 @@
+// The linear layer's large bf16 products on CTA pairs (sm_103a), C [Mo, No] = A B^T over Ko:
+//   forward  y  = act(x W^T + b) + r    A = x  (K-major),  B = W (K-major)
+//   dX       dx = dz W                  A = dz (K-major),  B = W (MN-major: W's rows run along Ko)
+//   dW       dw = dz^T x                A = dz (MN-major), B = x (MN-major)
+//
+// The two CTAs of a cluster compute one 256 x 256 tile with tcgen05.mma.cta_group::2: each
+// stages its own 128 rows of A and 128 columns of B per 64-deep K block (32 KB, six stages) and
+// holds its 128 x 256 fp32 half of the tile in tensor memory, two tiles deep. Both CTAs' loads
+// complete on the even CTA's full_bar, whose warp 1 issues the MMAs.
+//   warp 0     TMA producer of this CTA's halves
+//   warp 1     TMEM owner; in the even CTA one thread issues the MMAs
+//   warps 2..9 epilogue: two warps per TMEM lane quarter, 128 columns each
+// Ragged edges need no code in the main loop: the TMA fills what lies outside with zeros.
+//
+// Tiles beyond the last whole round of the pairs are divided along K instead of leaving pairs
+// idle: each pair takes an equal run of their K blocks. A run's part of a tile that ends in
+// another run is left as fp32 partial sums in the workspace; the run that holds the tile's last
+// K block adds them in the order of the pairs (so results repeat bit for bit). A pair works on
+// its run's last part first, so that what it waits for was begun before its own part was; it
+// only waits for pairs of a lower index, which were started before it.
+//
+// Every wait is bounded (1 s): MOE_ERR_DEVICE_TIMEOUT is recorded and the pair winds down.
+#include <string.h>
+
+#include <mutex>
+
+#include "act.cuh"
+#include "ops.h"
+#include "tc_common.cuh"
+#include "trace.h"
+
+namespace moe {
+namespace {
+
+using namespace tc;
+
+constexpr int TM = 256, HM = 128, TN = 256, HN = 128, BK = 64;
+constexpr int STAGES = 6, EW = 8;
+constexpr int A_BYTES = HM * BK * 2, B_BYTES = HN * BK * 2, STAGE_BYTES = A_BYTES + B_BYTES;
+constexpr int SLAB = 64 * 128;                    // 64 x 64 elements, 128-byte swizzle
+constexpr int PITCH = 80;                         // staging row: 32 bf16 + 16 bytes (no bank conflicts)
+constexpr int EPI_BYTES = 32 * PITCH;
+constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + EW * EPI_BYTES + 1024;
+constexpr int THREADS = 32 * (2 + EW);
+constexpr int PANEL = 8;                          // M tiles walked together per N tile
+
+struct PairGemm {
+  CUtensorMap a, b;
+  int64_t Mo;
+  int No, nkb, tiles_m, tiles_n;
+  int sk_tiles;          // the first sk_tiles tiles are divided along K
+  int sk_pairs;          // over this many pairs (each gets at least kMinRun K blocks)
+  const __nv_bfloat16 *bias, *res;
+  __nv_bfloat16 *z, *c;
+  int64_t ld_res, ldc;
+  bool vec;              // rows of c, res and z hold whole 16-byte vectors
+  uint32_t* header;      // error word, epoch, exit count
+  uint32_t* flags;       // [CTA][EW]
+  float* part;           // [CTA][EW][128 columns][32 rows]
+};
+
+// K blocks [k0, k1) of tile t; part: others hold the rest
+struct Seg {
+  int t, k0, k1;
+};
+
+// The segments of pair `p` of `np`: its share of the divided tiles, last part first, then whole
+// tiles.
+struct SegCursor {
+  int nkb, tiles, np, p;
+  int64_t u0, u;       // divided units still to do: [u0, u)
+  int t;               // next whole tile
+  Seg s;
+  __device__ SegCursor(const PairGemm& g, int pair, int npairs) {
+    nkb = g.nkb;
+    tiles = g.tiles_m * g.tiles_n;
+    np = npairs;
+    p = pair;
+    const int64_t units = (int64_t)g.sk_tiles * nkb;
+    u0 = u = 0;
+    if (pair < g.sk_pairs) {
+      u0 = units * pair / g.sk_pairs;
+      u = units * (pair + 1) / g.sk_pairs;
+    }
+    t = g.sk_tiles + pair;
+  }
+  __device__ bool next() {
+    if (u > u0) {
+      s.t = (int)((u - 1) / nkb);
+      const int64_t first = (int64_t)s.t * nkb;
+      s.k1 = (int)(u - first);
+      s.k0 = u0 > first ? (int)(u0 - first) : 0;
+      u = first + s.k0;
+      return true;
+    }
+    if (t >= tiles) return false;
+    s.t = t;
+    s.k0 = 0;
+    s.k1 = nkb;
+    t += np;
+    return true;
+  }
+};
+
+__device__ __forceinline__ void tile_coord(const PairGemm& g, int t, int& mi, int& ni) {
+  const int per = PANEL * g.tiles_n, panel = t / per, r = t - panel * per;
+  const int rows = min(PANEL, g.tiles_m - panel * PANEL);
+  ni = r / rows;
+  mi = panel * PANEL + r - ni * rows;
+}
+
+// A TMA load whose bytes complete on a barrier of either CTA of the pair.
+__device__ __forceinline__ void tma2d_pair(uint32_t dst, const CUtensorMap* map, uint32_t bar, int c0, int c1) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1)
+      : "memory");
+}
+
+__device__ __forceinline__ uint32_t ld_acquire(const uint32_t* p) {
+  uint32_t v;
+  asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+  return v;
+}
+__device__ __forceinline__ void st_release(uint32_t* p, uint32_t v) {
+  asm volatile("st.release.gpu.global.u32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
+}
+
+// Lane 0 waits for *flag == value; the answer is the same in all lanes.
+__device__ __forceinline__ bool flag_wait(const uint32_t* flag, uint32_t value, int lane, volatile int* abort, int* err) {
+  bool ok = true;
+  if (lane == 0 && ld_acquire(flag) != value) {
+    const uint64_t t0 = global_ns();
+    while (ld_acquire(flag) != value) {
+      if (*abort) { ok = false; break; }
+      if (global_ns() - t0 > kWaitLimitNs) {
+        record_error(err, MOE_ERR_DEVICE_TIMEOUT);
+        *abort = 1;
+        ok = false;
+        break;
+      }
+    }
+  }
+  ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+  __syncwarp();
+  return ok;
+}
+
+// 32 rows x 32 columns of `src` (or of the staging buffer to `dst`), 64 bytes per row.
+__device__ __forceinline__ void load_rows(uint8_t* stage, const __nv_bfloat16* src, int64_t ld, int rows, int cols, bool vec,
+                                          int lane) {
+  if (vec) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = i * 8 + (lane >> 2), q = lane & 3;
+      if (r < rows && q * 8 < cols)
+        *reinterpret_cast<uint4*>(stage + r * PITCH + q * 16) = *reinterpret_cast<const uint4*>(src + r * ld + q * 8);
+    }
+  } else if (lane < cols) {
+    for (int r = 0; r < rows; ++r)
+      *reinterpret_cast<__nv_bfloat16*>(stage + r * PITCH + lane * 2) = src[r * ld + lane];
+  }
+}
+__device__ __forceinline__ void store_rows(const uint8_t* stage, __nv_bfloat16* dst, int64_t ld, int rows, int cols,
+                                           bool vec, int lane) {
+  if (vec) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = i * 8 + (lane >> 2), q = lane & 3;
+      if (r < rows && q * 8 < cols)
+        *reinterpret_cast<uint4*>(dst + r * ld + q * 8) = *reinterpret_cast<const uint4*>(stage + r * PITCH + q * 16);
+    }
+  } else if (lane < cols) {
+    for (int r = 0; r < rows; ++r)
+      dst[r * ld + lane] = *reinterpret_cast<const __nv_bfloat16*>(stage + r * PITCH + lane * 2);
+  }
+}
+
+__device__ __forceinline__ void pack_row(uint8_t* stage, int lane, const float (&v)[32]) {
+  uint4* row = reinterpret_cast<uint4*>(stage + lane * PITCH);
+#pragma unroll
+  for (int q = 0; q < 4; ++q)
+    row[q] = make_uint4(pack_bf16x2(v[8 * q], v[8 * q + 1]), pack_bf16x2(v[8 * q + 2], v[8 * q + 3]),
+                        pack_bf16x2(v[8 * q + 4], v[8 * q + 5]), pack_bf16x2(v[8 * q + 6], v[8 * q + 7]));
+}
+
+// bias, z, activation and residual of this lane's 32 columns, and their way out. m0: the warp's
+// first row, rows of its 32 are inside; n: the first column, cols of the 32 are inside.
+template <int ACT>
+__device__ __forceinline__ void finish_chunk(const PairGemm& g, uint8_t* stage, int lane, float (&v)[32], int64_t m0, int rows,
+                                             int n, int cols) {
+  if (g.bias != nullptr) {
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] += i < cols ? __bfloat162float(g.bias[n + i]) : 0.f;
+  }
+  if (g.z != nullptr) {
+    pack_row(stage, lane, v);
+    __syncwarp();
+    store_rows(stage, g.z + m0 * g.No + n, g.No, rows, cols, g.vec, lane);
+    __syncwarp();
+  }
+#pragma unroll
+  for (int i = 0; i < 32; ++i) v[i] = act_f<ACT>(v[i]);
+  if (g.res != nullptr) {
+    load_rows(stage, g.res + m0 * g.ld_res + n, g.ld_res, rows, cols, g.vec, lane);
+    __syncwarp();
+    const uint4* row = reinterpret_cast<const uint4*>(stage + lane * PITCH);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const uint4 u = row[q];
+      const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 t = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w[i]));
+        v[8 * q + 2 * i] += t.x;
+        v[8 * q + 2 * i + 1] += t.y;
+      }
+    }
+    __syncwarp();
+  }
+  pack_row(stage, lane, v);
+  __syncwarp();
+  store_rows(stage, g.c + m0 * g.ldc + n, g.ldc, rows, cols, g.vec, lane);
+  __syncwarp();
+}
+
+template <bool A_MN, bool B_MN, int ACT>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
+    linear_pair_kernel(const __grid_constant__ PairGemm g) {
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ __align__(8) uint64_t full_bar[STAGES], empty_bar[STAGES], tfull_bar[2], tempty_bar[2], final_bar;
+  __shared__ uint32_t tmem_base_sh;
+  __shared__ volatile int abort_flag;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_rank();
+  const bool leader = rank == 0;
+  const int pair = (int)cluster_id(), npairs = (int)cluster_count();
+  int* err = reinterpret_cast<int*>(g.header);
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t smem_base = smem_u32(smem);
+
+  if (threadIdx.x == 0) {
+    abort_flag = 0;
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(smem_u32(&full_bar[s]), 1);
+      mbar_init(smem_u32(&empty_bar[s]), 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(smem_u32(&tfull_bar[b]), 1);
+      mbar_init(smem_u32(&tempty_bar[b]), 2 * EW);   // the epilogue warps of both CTAs
+    }
+    mbar_init(smem_u32(&final_bar), 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tmem_base_sh)),
+                 "r"(512)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    tc_fence_before();
+  }
+  __syncthreads();
+  cluster_sync_all();   // the peer's barriers are initialised before any remote arrival
+  tc_fence_after();
+  const uint32_t tmem_base = tmem_base_sh;
+  const uint32_t epoch = *reinterpret_cast<volatile uint32_t*>(g.header + 1) + 1;
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ TMA producer (both CTAs)
+    if (lane == 0) {
+      int stage = 0;
+      uint32_t phase = 0, pending = 0, pend_par = 0;
+      bool ok = true;
+      SegCursor cur(g, pair, npairs);
+      while (ok && cur.next()) {
+        int mi, ni;
+        tile_coord(g, cur.s.t, mi, ni);
+        const int m0 = mi * TM + HM * (int)rank, n0 = ni * TN + HN * (int)rank;
+        for (int kb = cur.s.k0; kb < cur.s.k1; ++kb) {
+          if (!mbar_wait_bounded(smem_u32(&empty_bar[stage]), phase ^ 1u, &abort_flag, err, kWaitLimitNs)) {
+            ok = false;
+            break;
+          }
+          const uint32_t a_s = smem_base + stage * STAGE_BYTES, b_s = a_s + A_BYTES;
+          if (leader) mbar_arrive_expect_tx(smem_u32(&full_bar[stage]), 2 * STAGE_BYTES);
+          const uint32_t bar = peer_addr(smem_u32(&full_bar[stage]), 0);
+          const int k0 = kb * BK;
+          if (A_MN) {
+            tma2d_pair(a_s, &g.a, bar, m0, k0);
+            tma2d_pair(a_s + SLAB, &g.a, bar, m0 + 64, k0);
+          } else {
+            tma2d_pair(a_s, &g.a, bar, k0, m0);
+          }
+          if (B_MN) {
+            tma2d_pair(b_s, &g.b, bar, n0, k0);
+            tma2d_pair(b_s + SLAB, &g.b, bar, n0 + 64, k0);
+          } else {
+            tma2d_pair(b_s, &g.b, bar, k0, n0);
+          }
+          pending |= 1u << stage;
+          pend_par = (pend_par & ~(1u << stage)) | (phase << stage);
+          if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+        }
+      }
+      // drain: no TMA load may still be writing shared memory when the pair exits
+      if (leader)
+        for (int s = 0; s < STAGES; ++s)
+          if ((pending >> s) & 1u)
+            mbar_wait_bounded(smem_u32(&full_bar[s]), (pend_par >> s) & 1u, nullptr, err, kWaitLimitNs);
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA issuer (even CTA)
+    if (leader && lane == 0) {
+      constexpr uint32_t idesc = idesc_bf16(TM, TN, A_MN, B_MN);
+      int stage = 0, it = 0;
+      uint32_t phase = 0;
+      bool ok = true, issued = false;
+      SegCursor cur(g, pair, npairs);
+      for (; ok && cur.next(); ++it) {
+        const int b = it & 1;
+        if (!mbar_wait_bounded(smem_u32(&tempty_bar[b]), ((it >> 1) & 1) ^ 1, &abort_flag, err, kWaitLimitNs)) break;
+        tc_fence_after();
+        const uint32_t d_tmem = tmem_base + (uint32_t)(b * TN);
+        for (int kb = cur.s.k0; kb < cur.s.k1; ++kb) {
+          if (!mbar_wait_bounded(smem_u32(&full_bar[stage]), phase, &abort_flag, err, kWaitLimitNs)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t a_s = smem_base + stage * STAGE_BYTES, b_s = a_s + A_BYTES;
+#pragma unroll
+          for (int kk = 0; kk < BK / 16; ++kk) {
+            const uint64_t ad = A_MN ? sdesc(a_s + kk * 2048, SLAB, 1024) : sdesc(a_s + kk * 32, 16, 1024);
+            const uint64_t bd = B_MN ? sdesc(b_s + kk * 2048, SLAB, 1024) : sdesc(b_s + kk * 32, 16, 1024);
+            umma_pair(d_tmem, ad, bd, idesc, (kb != cur.s.k0 || kk != 0) ? 1u : 0u);
+          }
+          issued = true;
+          umma_commit_mc(smem_u32(&empty_bar[stage]), 0x3);
+          if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+        }
+        if (!ok) break;
+        umma_commit_mc(smem_u32(&tfull_bar[b]), 0x3);
+      }
+      if (issued) {   // every MMA retired before the tensor memory is released
+        umma_commit_mc(smem_u32(&final_bar), 0x1);
+        mbar_wait_bounded(smem_u32(&final_bar), 0, nullptr, err, kWaitLimitNs);
+      }
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------------ epilogue (both CTAs)
+    const int ew = warp - 2, lg = warp & 3, col0 = (ew >> 2) * 128;
+    uint8_t* stage = smem + STAGES * STAGE_BYTES + ew * EPI_BYTES;
+    const int slot = (int)blockIdx.x * EW + ew;
+    int it = 0;
+    SegCursor cur(g, pair, npairs);
+    for (; cur.next(); ++it) {
+      const int b = it & 1;
+      int mi, ni;
+      tile_coord(g, cur.s.t, mi, ni);
+      const int64_t m0 = (int64_t)mi * TM + HM * (int)rank + lg * 32;
+      const int rows = (int)min((int64_t)32, g.Mo - m0), n0 = ni * TN + col0;
+      const bool got = mbar_wait_bounded(smem_u32(&tfull_bar[b]), (it >> 1) & 1, &abort_flag, err, kWaitLimitNs);
+      if (!__all_sync(0xffffffffu, got)) break;   // warp-uniform: tcgen05.ld is .sync.aligned
+      tc_fence_after();
+      const uint32_t acc = tmem_base + ((uint32_t)(lg * 32) << 16) + (uint32_t)(b * TN + col0);
+      const bool live = rows > 0 && n0 < g.No;    // the same for every part of the tile
+      bool ok = true;
+      if (live && cur.s.k1 < g.nkb) {
+        // the tile ends in a later pair's run: leave the partial sums to it
+        float* out = g.part + (int64_t)slot * 128 * 32 + lane;
+#pragma unroll
+        for (int c = 0; c < 128; c += 32) {
+          uint32_t u[32];
+          tmem_ld32(acc + c, u);
+          tmem_ld_wait();
+#pragma unroll
+          for (int i = 0; i < 32; ++i) __stcg(out + (c + i) * 32, __uint_as_float(u[i]));
+        }
+        __threadfence();
+        __syncwarp();
+        if (lane == 0) st_release(g.flags + slot, epoch);
+      } else if (live) {
+        // first and last pair before this one whose runs hold parts of the tile
+        const int64_t units = (int64_t)g.sk_tiles * g.nkb, first = (int64_t)cur.s.t * g.nkb;
+        int q0 = pair;
+        if (cur.s.k0 > 0) {
+          q0 = (int)(first * g.sk_pairs / units);
+          while (units * (q0 + 1) / g.sk_pairs <= first) ++q0;
+          for (int q = q0; ok && q < pair; ++q)
+            ok = flag_wait(g.flags + (q * 2 + (int)rank) * EW + ew, epoch, lane, &abort_flag, err);
+        }
+        if (ok) {
+#pragma unroll 1
+          for (int c = 0; c < 128; c += 32) {
+            if (n0 + c >= g.No) break;
+            uint32_t u[32];
+            float v[32];
+            tmem_ld32(acc + c, u);
+            tmem_ld_wait();
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(u[i]);
+            for (int q = q0; q < pair; ++q) {
+              const float* in = g.part + ((int64_t)((q * 2 + (int)rank) * EW + ew) * 128 + c) * 32 + lane;
+#pragma unroll
+              for (int i = 0; i < 32; ++i) v[i] += __ldcg(in + i * 32);
+            }
+            finish_chunk<ACT>(g, stage, lane, v, m0, rows, n0 + c, min(32, g.No - n0 - c));
+          }
+        }
+      }
+      if (!ok) break;
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_remote(peer_addr(smem_u32(&tempty_bar[b]), 0));
+    }
+  }
+  __syncthreads();
+  cluster_sync_all();   // neither CTA releases its tensor memory while the pair still uses it
+  if (warp == 1) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(512) : "memory");
+  }
+  // the last CTA to leave makes this call's flags stale
+  if (g.sk_tiles > 0 && threadIdx.x == 0) {
+    __threadfence();
+    if (atomicAdd(g.header + 2, 1u) == gridDim.x - 1) {
+      g.header[2] = 0;
+      g.header[1] = epoch;
+    }
+  }
+}
+
+template <bool A_MN, bool B_MN, int ACT>
+int launch_pair(PairGemm& g, int num_sms, cudaStream_t st) {
+  auto kernel = linear_pair_kernel<A_MN, B_MN, ACT>;
+  // per device, once (under a lock): the shared-memory attribute and the pairs resident at once
+  static std::mutex mu;
+  static int occ_dev[kMaxDevices];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return MOE_ERR_CUDA;
+  int pairs;
+  {
+    std::lock_guard<std::mutex> lk(mu);
+    if (occ_dev[dev] == 0) {
+      if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES) != cudaSuccess)
+        return MOE_ERR_CUDA;
+      cudaLaunchConfig_t cfg = {};
+      cfg.gridDim = dim3((unsigned)(num_sms & ~1));
+      cfg.blockDim = dim3(THREADS);
+      cfg.dynamicSmemBytes = SMEM_BYTES;
+      int n = 0;
+      if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n <= 0) return MOE_ERR_CUDA;
+      occ_dev[dev] = n < kMaxPairs ? n : kMaxPairs;
+    }
+    pairs = occ_dev[dev];
+  }
+  const int64_t tiles = (int64_t)g.tiles_m * g.tiles_n;
+  const int rem = (int)(tiles % pairs);
+  g.sk_tiles = g.sk_pairs = 0;
+  const int64_t most = (int64_t)rem * g.nkb / kMinRun;   // pairs that the divided tiles can feed
+  const int run_pairs = most < pairs ? (int)most : pairs;
+  if (tiles < pairs) {
+    if (run_pairs > tiles) {
+      g.sk_tiles = (int)tiles;
+      g.sk_pairs = pairs = run_pairs;
+    } else {
+      pairs = (int)tiles;
+    }
+  } else if (run_pairs > rem && (int64_t)rem * g.nkb / run_pairs + kJoinBlocks < g.nkb) {
+    g.sk_tiles = rem;
+    g.sk_pairs = run_pairs;
+  }
+  TraceScope ts(TP_LINEAR, st);
+  kernel<<<2 * pairs, THREADS, SMEM_BYTES, st>>>(g);
+  return cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_LAUNCH;
+}
+
+}  // namespace
+
+size_t linear_pair_part_bytes() { return (size_t)2 * kMaxPairs * EW * 128 * 32 * 4; }
+
+int launch_linear_pair(int kind, const GemmArgs& a, uint8_t* ws, size_t part, int num_sms, cudaStream_t st) {
+  PairGemm g;
+  memset(&g, 0, sizeof(g));
+  g.Mo = a.M;
+  g.No = a.N;
+  g.nkb = (int)((a.K + BK - 1) / BK);
+  g.tiles_m = (int)((a.M + TM - 1) / TM);
+  g.tiles_n = (a.N + TN - 1) / TN;
+  g.bias = static_cast<const __nv_bfloat16*>(a.bias);
+  g.res = static_cast<const __nv_bfloat16*>(a.res);
+  g.z = static_cast<__nv_bfloat16*>(a.z_out);
+  g.c = static_cast<__nv_bfloat16*>(a.c);
+  g.ld_res = a.ld_res;
+  g.ldc = a.ldc;
+  g.vec = a.N % 8 == 0 && a.ldc % 8 == 0 && (a.res == nullptr || a.ld_res % 8 == 0);
+  g.header = reinterpret_cast<uint32_t*>(ws);
+  g.flags = g.header + 256;
+  g.part = reinterpret_cast<float*>(ws + part);
+  // K-major: box 64 along K x 128 rows; MN-major: box 64 along the rows x 64 of K
+  bool ok = a.ak == 1 ? map2d_ld(&g.a, a.a, a.K, a.M, a.am, BK, HM) : map2d_ld(&g.a, a.a, a.M, a.K, a.ak, 64, BK);
+  ok = ok && (a.bk == 1 ? map2d_ld(&g.b, a.b, a.K, a.N, a.bn, BK, HN) : map2d_ld(&g.b, a.b, a.N, a.K, a.bk, 64, BK));
+  if (!ok) return MOE_ERR_CUDA;
+  if (kind == LINEAR_DX) return launch_pair<false, true, MOE_ACT_NONE>(g, num_sms, st);
+  if (kind == LINEAR_DW) return launch_pair<true, true, MOE_ACT_NONE>(g, num_sms, st);
+#define MOE_P(A) return launch_pair<false, false, A>(g, num_sms, st)
+  MOE_ACT_SWITCH(a.act, MOE_P)
+#undef MOE_P
+  return MOE_OK;
+}
+
+}  // namespace moe

@@ -5,7 +5,7 @@
 
 namespace moe {
 
-constexpr size_t kOpHeader = 4096;    // error word, launch counters and flags
+constexpr size_t kOpHeader = 8192;    // error word, launch counters, and from byte 1024 flags
 constexpr int kDecodeMaxT = 64;       // tokens of moe_layer_decode
 
 inline size_t round256(size_t x) { return (x + 255) & ~size_t(255); }
@@ -38,10 +38,12 @@ int launch_decode_simt(const DecodeArgs& a, int num_sms, cudaStream_t st);
 struct LinearLayout {
   size_t dz;         // [M][ld_dz] the pre-activation's gradient, dims->dtype
   size_t db_part;    // [kDbSplit][N] fp32
+  size_t part;       // partial tiles of the products on CTA pairs (bf16)
   int64_t ld_dz;
   size_t total;
 };
 constexpr int kDbSplit = 64;
+constexpr int kMaxWidth = 65535 * 64;   // N and K of a linear layer
 LinearLayout linear_layout(const moe_linear_dims& d);
 
 // C [M, N] = A B^T, A (m, k) at a[m * am + k * ak], B (n, k) at b[n * bn + k * bk], one of the two
@@ -63,6 +65,14 @@ struct GemmArgs {
   int dtype;
 };
 cudaError_t launch_gemm_simt(const GemmArgs& g, cudaStream_t st);
+// The bf16 products on CTA pairs. LINEAR_FWD: A and B K-major; DX: B MN-major; DW: both. Base
+// pointers 16-byte aligned, row strides multiples of 8 elements.
+enum LinearKind { LINEAR_FWD = 0, LINEAR_DX, LINEAR_DW };
+constexpr int kMaxPairs = 80;     // clusters of two CTAs
+constexpr int kMinRun = 4;        // K blocks of a pair's run when there are fewer tiles than pairs
+constexpr int kJoinBlocks = 8;    // K blocks that the division of a tile costs
+size_t linear_pair_part_bytes();
+int launch_linear_pair(int kind, const GemmArgs& a, uint8_t* ws, size_t part, int num_sms, cudaStream_t st);
 // dz = dy * act'(z) (dz may be NULL: sums only) and db (may be NULL)
 cudaError_t launch_linear_dz(const void* dy, int64_t ld_dy, const void* z, int act, int64_t M, int N,
                              int dtype, void* dz, int64_t ld_dz, float* db_part, void* db, cudaStream_t st);

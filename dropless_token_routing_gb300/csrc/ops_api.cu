@@ -28,7 +28,8 @@ LinearLayout linear_layout(const moe_linear_dims& d) {
   L.ld_dz = (d.N + 7) & ~7ll;
   L.dz = kOpHeader;
   L.db_part = L.dz + round256((size_t)d.M * L.ld_dz * elt_bytes(d.dtype));
-  L.total = L.db_part + round256(4 * (size_t)kDbSplit * d.N);
+  L.part = L.db_part + round256(4 * (size_t)kDbSplit * d.N);
+  L.total = L.part + (d.dtype == MOE_BF16 ? linear_pair_part_bytes() : 0);
   return L;
 }
 
@@ -69,7 +70,7 @@ int resolve_linear(const moe_linear_dims* in, moe_linear_dims* d) {
   if (in == nullptr) return MOE_ERR_NULL_POINTER;
   *d = *in;
   if (d->dtype != MOE_F32 && d->dtype != MOE_BF16) return MOE_ERR_UNSUPPORTED_DTYPE;
-  if (d->M < 0 || d->M > 0x7fffffff || d->N < 1 || d->K < 1 || d->N > (1 << 22) || d->K > (1 << 22)) return MOE_ERR_BAD_DIMS;
+  if (d->M < 0 || d->M > (1 << 30) || d->N < 1 || d->K < 1 || d->N > kMaxWidth || d->K > kMaxWidth) return MOE_ERR_BAD_DIMS;
   if (d->act < MOE_ACT_NONE || d->act > MOE_ACT_GELU_TANH) return MOE_ERR_BAD_DIMS;
   if (d->ld_x == 0) d->ld_x = d->K;
   if (d->ld_w == 0) d->ld_w = d->K;
@@ -80,6 +81,14 @@ int resolve_linear(const moe_linear_dims* in, moe_linear_dims* d) {
       d->ld_y > most || d->ld_res > most)
     return MOE_ERR_BAD_DIMS;
   return MOE_OK;
+}
+
+// One product of the layer. bf16 with row strides that the TMA takes (whole 16-byte vectors) goes
+// to the tensor cores, everything else to the FMA pipes.
+int run_gemm(int kind, const GemmArgs& g, uint8_t* ws, const LinearLayout& L, int sms, cudaStream_t st) {
+  const int64_t lda = g.ak == 1 ? g.am : g.ak, ldb = g.bk == 1 ? g.bn : g.bk;
+  if (g.dtype == MOE_BF16 && lda % 8 == 0 && ldb % 8 == 0) return launch_linear_pair(kind, g, ws, L.part, sms, st);
+  return launch_gemm_simt(g, st) == cudaSuccess ? MOE_OK : MOE_ERR_LAUNCH;
 }
 
 }  // namespace
@@ -149,7 +158,8 @@ int moe_linear_fwd(const void* x, const void* w, const void* bias, const void* r
                    void* z, void* y, void* ws, size_t ws_bytes, moe_stream_t stream) {
   moe_linear_dims d;
   OP_TRY(resolve_linear(dims, &d));
-  OP_TRY(check_op_ws(ws, ws_bytes, linear_layout(d).total));
+  const LinearLayout L = linear_layout(d);
+  OP_TRY(check_op_ws(ws, ws_bytes, L.total));
   const bool some = d.M > 0;
   OP_TRY(req_if(x, some));
   OP_TRY(req(w));
@@ -159,7 +169,9 @@ int moe_linear_fwd(const void* x, const void* w, const void* bias, const void* r
   OP_TRY(req_if(y, some));
   if (!some) return MOE_OK;
   GemmArgs g = {x, w, d.ld_x, 1, d.ld_w, 1, d.M, d.N, d.K, bias, residual, d.ld_res, d.act, z, y, d.ld_y, d.dtype};
-  return launch_gemm_simt(g, (cudaStream_t)stream) == cudaSuccess ? MOE_OK : MOE_ERR_LAUNCH;
+  const int sms = num_sms();
+  if (sms == 0) return MOE_ERR_CUDA;
+  return run_gemm(LINEAR_FWD, g, static_cast<uint8_t*>(ws), L, sms, (cudaStream_t)stream);
 }
 
 int moe_linear_bwd(const void* x, const void* w, const void* z, const void* dy, const moe_linear_dims* dims, void* dx,
@@ -184,8 +196,11 @@ int moe_linear_bwd(const void* x, const void* w, const void* z, const void* dy, 
     return MOE_OK;
   }
   uint8_t* base = static_cast<uint8_t*>(ws);
+  const int sms = num_sms();
+  if (sms == 0) return MOE_ERR_CUDA;
   const bool products = dx != nullptr || dw != nullptr;
-  const bool own_dz = products && d.act != MOE_ACT_NONE;
+  // without an activation dz is dy itself, unless dy's rows are not whole 16-byte vectors (bf16)
+  const bool own_dz = products && (d.act != MOE_ACT_NONE || (d.dtype == MOE_BF16 && d.ld_y % 8 != 0));
   const void* dz = own_dz ? base + L.dz : dy;
   const int64_t ld_dz = own_dz ? L.ld_dz : d.ld_y;
   if (own_dz || db != nullptr) {
@@ -195,11 +210,11 @@ int moe_linear_bwd(const void* x, const void* w, const void* z, const void* dy, 
   }
   if (dx != nullptr) {   // dx [M, K] = dz W: contraction over N
     GemmArgs g = {dz, w, ld_dz, 1, 1, d.ld_w, d.M, d.K, d.N, nullptr, nullptr, 0, MOE_ACT_NONE, nullptr, dx, d.ld_x, d.dtype};
-    if (launch_gemm_simt(g, st) != cudaSuccess) return MOE_ERR_LAUNCH;
+    OP_TRY(run_gemm(LINEAR_DX, g, base, L, sms, st));
   }
   if (dw != nullptr) {   // dw [N, K] = dz^T x: contraction over M
     GemmArgs g = {dz, x, 1, ld_dz, 1, d.ld_x, d.N, d.K, d.M, nullptr, nullptr, 0, MOE_ACT_NONE, nullptr, dw, d.ld_w, d.dtype};
-    if (launch_gemm_simt(g, st) != cudaSuccess) return MOE_ERR_LAUNCH;
+    OP_TRY(run_gemm(LINEAR_DW, g, base, L, sms, st));
   }
   return MOE_OK;
 }

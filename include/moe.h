@@ -346,10 +346,10 @@ int moe_layer_bwd(const moe_layer_params* params, const moe_layer_saved* saved, 
  * ones) pass through the dense projections and the layer, and the drafted ones are verified. The
  * pages name serving the layer only in passing; the formulas are written out here. */
 
-/* Zero the 4 KB header (error word, launch counters and flags) of a workspace of the calls below
+/* Zero the header (error word, launch counters and flags) of a workspace of the calls below
  * (async). Once after allocating it; the calls leave the counters zeroed themselves. A workspace
  * belongs to one call at a time: calls that share one have to be ordered on one stream.
- * moe_get_device_error reads its error word. ws: 256-byte aligned, ws_bytes >= 4096. */
+ * moe_get_device_error reads its error word. ws: 256-byte aligned, ws_bytes >= 8192. */
 int moe_op_workspace_init(void* ws, size_t ws_bytes, moe_stream_t stream);
 
 /* The whole layer for 0 <= dims->T <= 64 tokens (router, top-k, selected experts, shared experts,
@@ -375,8 +375,8 @@ enum moe_act {
 };
 
 typedef struct moe_linear_dims {
-  int64_t M;        /* rows (tokens), >= 0 */
-  int32_t N, K;     /* output and input width, >= 1; any value */
+  int64_t M;        /* rows (tokens), 0 <= M <= 2^30 */
+  int32_t N, K;     /* output and input width, 1 .. 4194240 (65535 * 64) */
   int32_t act;      /* enum moe_act */
   int32_t dtype;    /* enum moe_dtype: x, w, bias, residual, y, z and every gradient */
   int64_t ld_x;     /* elements between rows of x and dx (>= K), 0 = K */

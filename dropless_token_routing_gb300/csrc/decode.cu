@@ -1,4 +1,4 @@
-// The whole MoE layer for a few tokens on the FMA pipes: the scores and the selection by the
+// The whole MoE layer for a few tokens in fp32, on the FMA pipes: the scores and the selection by the
 // router's kernels, then one warp per hidden row and one per output row.
 #include "common.cuh"
 #include "ops.h"
@@ -42,7 +42,7 @@ __global__ void __launch_bounds__(256) decode_hidden_kernel(const DecodeArgs a) 
   const T* x = static_cast<const T*>(a.x) + t * D.d;
   const float g = warp_dot(w13 + (int64_t)j * D.d, x, D.d, lane);
   const float u = warp_dot(w13 + (int64_t)(f + j) * D.d, x, D.d, lane);
-  float* h = reinterpret_cast<float*>(a.ws + a.L.h) + (sh ? Tk * D.f + (q - Tk) * f : q * f);
+  float* h = reinterpret_cast<float*>(a.ws + (sh ? a.L.hs : a.L.h)) + (sh ? q - Tk : q) * f;
   if (lane == 0) h[j] = w * silu_f(g) * u;
 }
 
@@ -51,9 +51,10 @@ template <typename T>
 __global__ void __launch_bounds__(256) decode_output_kernel(const DecodeArgs a) {
   const moe_dims& D = a.dm;
   const int lane = threadIdx.x & 31, n = blockIdx.x * 8 + (threadIdx.x >> 5);
-  const int64_t t = blockIdx.y, Tk = D.T * D.k;
+  const int64_t t = blockIdx.y;
   if (n >= D.d) return;
   const float* h = reinterpret_cast<const float*>(a.ws + a.L.h);
+  const float* hs = reinterpret_cast<const float*>(a.ws + a.L.hs);
   float y = 0.f;
   for (int j = 0; j < D.k; ++j) {
     const int64_t q = t * D.k + j;
@@ -62,7 +63,7 @@ __global__ void __launch_bounds__(256) decode_output_kernel(const DecodeArgs a) 
   }
   for (int s = 0; s < D.S; ++s)
     y += warp_dot(static_cast<const T*>(a.ws2) + ((int64_t)s * D.d + n) * D.f_s,
-                  h + Tk * D.f + (s * D.T + t) * D.f_s, D.f_s, lane);
+                  hs + (s * D.T + t) * D.f_s, D.f_s, lane);
   if (lane == 0) {
     if (a.residual != nullptr) y += to_f32(static_cast<const T*>(a.residual)[t * D.d + n]);
     static_cast<T*>(a.y)[t * D.d + n] = from_f32<T>(y);
@@ -97,7 +98,7 @@ int launch_decode_simt(const DecodeArgs& a, int num_sms, cudaStream_t st) {
   if (a.gate_out != nullptr && cudaMemcpyAsync(a.gate_out, gate, n, cudaMemcpyDeviceToDevice, st) != cudaSuccess)
     return MOE_ERR_CUDA;
   TraceScope ts(TP_DECODE, st);
-  const cudaError_t e = D.dtype == MOE_F32 ? run_ffn<float>(a, st) : run_ffn<__nv_bfloat16>(a, st);
+  const cudaError_t e = run_ffn<float>(a, st);
   return e == cudaSuccess ? MOE_OK : MOE_ERR_LAUNCH;
 }
 

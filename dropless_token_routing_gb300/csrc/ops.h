@@ -10,13 +10,22 @@ constexpr int kDecodeMaxT = 64;       // tokens of moe_layer_decode
 
 inline size_t round256(size_t x) { return (x + 255) & ~size_t(255); }
 
+constexpr int kMaxStreamCtas = 160;   // CTAs of a weight stream
+constexpr int kMinStreamRun = 2;      // K blocks of a CTA's run
+
 // ------------------------------------------------------------------ decode
 struct DecodeLayout {
-  size_t logits;     // [T][E] fp32
   size_t idx;        // [T][k] int32
   size_t gate;       // [T][k] fp32
+  // fp32 layers
+  size_t logits;     // [T][E] fp32
   size_t counts;     // [E] int32
-  size_t h;          // [T*k][f] then [S*T][f_s] fp32: hidden rows times their gates
+  // bf16 layers
+  size_t score_part; // [T][slabs * groups][E] fp32 partial scores
+  size_t part;       // [3][CTA][token columns][128] fp32 partial tiles
+  // hidden rows times their gates: fp32 [T*k][f] and [S*T][f_s]; bf16 [slot][token columns][f]
+  // and [S][token columns][f_s]
+  size_t h, hs;
   size_t total;
 };
 DecodeLayout decode_layout(const moe_dims& d);
@@ -32,6 +41,10 @@ struct DecodeArgs {
   DecodeLayout L;
   moe_dims dm;
 };
+int decode_token_columns(int64_t T);   // MMA columns that T tokens take
+// slots of the hidden rows: experts that T tokens can select
+inline int64_t decode_slots(const moe_dims& d) { return d.T * d.k < d.E ? d.T * d.k : d.E; }
+int launch_decode_tc(const DecodeArgs& a, int num_sms, cudaStream_t st);
 int launch_decode_simt(const DecodeArgs& a, int num_sms, cudaStream_t st);
 
 // ------------------------------------------------------------------ linear
@@ -73,6 +86,10 @@ constexpr int kMinRun = 4;        // K blocks of a pair's run when there are few
 constexpr int kJoinBlocks = 8;    // K blocks that the division of a tile costs
 size_t linear_pair_part_bytes();
 int launch_linear_pair(int kind, const GemmArgs& a, uint8_t* ws, size_t part, int num_sms, cudaStream_t st);
+// The forward product for at most kStreamRows rows, as a stream of the weights.
+constexpr int kStreamRows = 256;
+size_t linear_stream_part_bytes(int64_t M);
+int launch_linear_stream(const GemmArgs& a, uint8_t* ws, size_t part, int num_sms, cudaStream_t st);
 // dz = dy * act'(z) (dz may be NULL: sums only) and db (may be NULL)
 cudaError_t launch_linear_dz(const void* dy, int64_t ld_dy, const void* z, int act, int64_t M, int N,
                              int dtype, void* dz, int64_t ld_dz, float* db_part, void* db, cudaStream_t st);

@@ -13,12 +13,19 @@ DecodeLayout decode_layout(const moe_dims& d) {
     o = round256(o + bytes);
     return r;
   };
-  const size_t T = (size_t)d.T;
-  L.logits = take(4 * T * d.E);
+  const size_t T = (size_t)d.T, E = (size_t)d.E;
+  const bool tc = d.dtype == MOE_BF16;
+  const size_t nt = tc ? decode_token_columns(d.T) : 0;
   L.idx = take(4 * T * d.k);
   L.gate = take(4 * T * d.k);
-  L.counts = take(4 * (size_t)d.E);
-  L.h = take(4 * T * ((size_t)d.k * d.f + (size_t)d.S * d.f_s));
+  L.logits = take(tc ? 0 : 4 * T * E);
+  L.counts = take(tc ? 0 : 4 * E);
+  // a CTA's share of the scores: one row per group of threads, at most 256 values per token
+  // (E with more experts)
+  L.score_part = take(tc ? 4 * T * kMaxStreamCtas * (E < 256 ? 256 : E) : 0);
+  L.part = take(tc ? 4 * 3 * kMaxStreamCtas * nt * 128 : 0);
+  L.h = take(tc ? 2 * (size_t)decode_slots(d) * nt * d.f : 4 * T * d.k * d.f);
+  L.hs = take(tc ? 2 * (size_t)d.S * nt * d.f_s : 4 * T * d.S * d.f_s);
   L.total = o;
   return L;
 }
@@ -29,7 +36,12 @@ LinearLayout linear_layout(const moe_linear_dims& d) {
   L.dz = kOpHeader;
   L.db_part = L.dz + round256((size_t)d.M * L.ld_dz * elt_bytes(d.dtype));
   L.part = L.db_part + round256(4 * (size_t)kDbSplit * d.N);
-  L.total = L.part + (d.dtype == MOE_BF16 ? linear_pair_part_bytes() : 0);
+  size_t part = 0;
+  if (d.dtype == MOE_BF16) {
+    const size_t a = linear_pair_part_bytes(), b = linear_stream_part_bytes(d.M);
+    part = a > b ? a : b;
+  }
+  L.total = L.part + part;
   return L;
 }
 
@@ -87,7 +99,10 @@ int resolve_linear(const moe_linear_dims* in, moe_linear_dims* d) {
 // to the tensor cores, everything else to the FMA pipes.
 int run_gemm(int kind, const GemmArgs& g, uint8_t* ws, const LinearLayout& L, int sms, cudaStream_t st) {
   const int64_t lda = g.ak == 1 ? g.am : g.ak, ldb = g.bk == 1 ? g.bn : g.bk;
-  if (g.dtype == MOE_BF16 && lda % 8 == 0 && ldb % 8 == 0) return launch_linear_pair(kind, g, ws, L.part, sms, st);
+  if (g.dtype == MOE_BF16 && lda % 8 == 0 && ldb % 8 == 0) {
+    if (kind == LINEAR_FWD && g.M <= kStreamRows) return launch_linear_stream(g, ws, L.part, sms, st);
+    return launch_linear_pair(kind, g, ws, L.part, sms, st);
+  }
   return launch_gemm_simt(g, st) == cudaSuccess ? MOE_OK : MOE_ERR_LAUNCH;
 }
 
@@ -146,7 +161,7 @@ int moe_layer_decode(const moe_layer_params* params, const void* x, const float*
   a.y = y;
   a.ws = static_cast<uint8_t*>(ws);
   a.dm = *dims;
-  return launch_decode_simt(a, sms, (cudaStream_t)stream);
+  return dims->dtype == MOE_BF16 ? launch_decode_tc(a, sms, (cudaStream_t)stream) : launch_decode_simt(a, sms, (cudaStream_t)stream);
 }
 
 size_t moe_linear_workspace_bytes(const moe_linear_dims* dims) {

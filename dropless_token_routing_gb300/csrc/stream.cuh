@@ -1,0 +1,320 @@
+// Products of a weight stream with a few token rows (sm_103a): the pieces that the few-token
+// layer (decode_tc.cu) and the linear layer's serving form (linear_stream.cu) share.
+//
+// With few tokens a product is a stream of weights out of HBM, and everything here serves that
+// stream. The weights are the MMA's A operand, 128 weight rows by 64 of K per stage; the tokens
+// are B, NT (16 .. 256) rows; the transposed result, 128 weight rows by NT tokens, accumulates in
+// tensor memory, two accumulators deep. One thread issues TMA loads into a ring that fills the
+// shared memory (about 190 KB in flight per SM, four times what the HBM's latency needs), one
+// thread issues tcgen05.mma, eight warps take the results out.
+//
+// The K blocks of all tiles are divided evenly over the CTAs whatever the tile count (a "run" of
+// blocks each), so that every SM streams the same number of bytes. A run's part of a tile that
+// ends in a later run is left as fp32 partial sums in the workspace; the run that holds the
+// tile's last K block adds them in the order of the CTAs (results repeat bit for bit). A CTA works
+// on its run's last part first, so that what another CTA waits for is done first, and only waits
+// for CTAs of a lower index.
+//
+// Every wait is bounded (1 s); the warps that take results out leave together (a barrier carries
+// the verdict), so that none is left at a barrier.
+#pragma once
+
+#include "ops.h"
+#include "tc_common.cuh"
+
+namespace moe {
+namespace stream {
+
+using namespace tc;
+
+constexpr int BM = 128, BK = 64;
+constexpr int A_BYTES = BM * BK * 2;
+constexpr int CW = 8, CT = CW * 32;          // warps and threads that take results out
+constexpr int THREADS = 64 + CT;
+constexpr int PITCH = BM + 4;                // floats between token columns of the staged result
+constexpr int MAX_STAGES = 12;
+
+template <int NT> struct Cfg {
+  static constexpr int STAGE = A_BYTES + NT * BK * 2;
+  static constexpr int CHUNK = NT < 64 ? NT : 64;                 // token columns staged at once
+  static constexpr int ACC_BYTES = CHUNK * PITCH * 4;
+  static constexpr int TMEM = 2 * NT < 32 ? 32 : 2 * NT;          // NT is a power of two
+  // stages that fit beside the staged result and `extra` bytes of tables
+  static constexpr int stages(int extra) {
+    const int n = (227 * 1024 - 2048 - ACC_BYTES - extra) / STAGE;
+    return n < MAX_STAGES ? n : MAX_STAGES;
+  }
+  static constexpr int smem(int extra) { return 1024 + stages(extra) * STAGE + ACC_BYTES + extra; }
+};
+
+struct Bars {
+  uint64_t full[MAX_STAGES], empty[MAX_STAGES], tfull[2], tempty[2], final, list;
+  uint32_t tmem;
+  volatile int abort;
+};
+
+__device__ __forceinline__ uint32_t ld_acquire(const uint32_t* p) {
+  uint32_t v;
+  asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+  return v;
+}
+__device__ __forceinline__ void st_release(uint32_t* p, uint32_t v) {
+  asm volatile("st.release.gpu.global.u32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
+}
+__device__ __forceinline__ void add_release(uint32_t* p, uint32_t v) {
+  asm volatile("red.release.gpu.global.add.u32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
+}
+
+// One thread waits until the word holds `value` (equal) or at least `value` (!equal).
+__device__ __forceinline__ bool word_wait(const uint32_t* p, uint32_t value, bool equal, volatile int* abort, int* err) {
+  auto there = [&]() {
+    const uint32_t v = ld_acquire(p);
+    return equal ? v == value : v >= value;
+  };
+  if (there()) return true;
+  const uint64_t t0 = global_ns();
+  while (!there()) {
+    if (*abort) return false;
+    if (global_ns() - t0 > kWaitLimitNs) {
+      record_error(err, MOE_ERR_DEVICE_TIMEOUT);
+      *abort = 1;
+      return false;
+    }
+  }
+  return true;
+}
+
+// Barrier of the CT threads that take results out.
+__device__ __forceinline__ void ct_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+// The same, and true in all of them if `bad` is true in any.
+__device__ __forceinline__ bool ct_any(bool bad) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+      "barrier.cta.red.or.pred q, 1, 256, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(bad ? 1u : 0u)
+      : "memory");
+  return r != 0;
+}
+
+__device__ __forceinline__ void umma1(uint32_t d_tmem, uint64_t ad, uint64_t bd, uint32_t idesc, uint32_t accum) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(ad), "l"(bd), "r"(idesc), "r"(accum)
+      : "memory");
+}
+__device__ __forceinline__ void umma1_commit(uint32_t bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr));
+}
+
+// K blocks [k0, k1) of tile t
+struct Seg {
+  int64_t t;
+  int k0, k1;
+};
+
+// CTA `c` of `n` works on its run of the tiles' K blocks, the last part first. With few blocks
+// only as many CTAs as get kMinStreamRun of them take part, so no run among them is empty.
+struct Run {
+  int64_t units, u0, u;
+  int nkb, n;
+  Seg s;
+  __device__ Run(int64_t tiles, int nkb_, int c, int n_cta) {
+    nkb = nkb_;
+    units = tiles * nkb;
+    n = (int)min((int64_t)n_cta, max((int64_t)1, units / kMinStreamRun));
+    u0 = c < n ? units * c / n : 0;
+    u = c < n ? units * (c + 1) / n : 0;
+  }
+  __device__ bool next() {
+    if (u <= u0) return false;
+    s.t = (u - 1) / nkb;
+    const int64_t first = s.t * nkb;
+    s.k1 = (int)(u - first);
+    s.k0 = u0 > first ? (int)(u0 - first) : 0;
+    u = first + s.k0;
+    return true;
+  }
+  // the first CTA whose run holds a part of the current tile
+  __device__ int first_cta() const {
+    const int64_t first = s.t * nkb;
+    int q = (int)(first * n / units);
+    while (units * (q + 1) / n <= first) ++q;
+    return q;
+  }
+};
+
+// Position in the ring of stages.
+template <int STAGES> struct Ring {
+  int stage = 0;
+  uint32_t phase = 0;
+  __device__ __forceinline__ void step() {
+    if (++stage == STAGES) {
+      stage = 0;
+      phase ^= 1u;
+    }
+  }
+};
+
+// Set-up by all threads: barriers, tensor memory. Ends with __syncthreads.
+template <int NT, int STAGES>
+__device__ __forceinline__ void setup(Bars& b, int warp) {
+  if (threadIdx.x == 0) {
+    b.abort = 0;
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(smem_u32(&b.full[s]), 1);
+      mbar_init(smem_u32(&b.empty[s]), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_u32(&b.tfull[i]), 1);
+      mbar_init(smem_u32(&b.tempty[i]), CW);
+    }
+    mbar_init(smem_u32(&b.final), 1);
+    mbar_init(smem_u32(&b.list), 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&b.tmem)),
+                 "r"(Cfg<NT>::TMEM)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    tc_fence_before();
+  }
+  __syncthreads();
+  tc_fence_after();
+}
+
+template <int NT> __device__ __forceinline__ void teardown(Bars& b, int warp) {
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(b.tmem), "r"(Cfg<NT>::TMEM) : "memory");
+  }
+}
+
+// Wait for the loads that are still in flight (the producer, before it leaves).
+template <int STAGES> __device__ __forceinline__ void drain(Bars& b, const Ring<STAGES>& r, int64_t loaded, int* err) {
+  // the last min(loaded, STAGES) loads end just before the ring's position
+  Ring<STAGES> q = r;
+  const int n = loaded < STAGES ? (int)loaded : STAGES;
+  for (int i = 0; i < n; ++i) {
+    if (q.stage == 0) {
+      q.stage = STAGES;
+      q.phase ^= 1u;
+    }
+    --q.stage;
+    mbar_wait_bounded(smem_u32(&b.full[q.stage]), q.phase, nullptr, err, kWaitLimitNs);
+  }
+}
+
+// The MMA thread's part of a run; `it` counts the segments of the launch.
+template <int NT, int STAGES>
+__device__ __forceinline__ bool mma_run(Bars& b, uint32_t smem_base, Run run, Ring<STAGES>& ring, int& it, int* err) {
+  constexpr uint32_t idesc = idesc_bf16(BM, NT, false, false);
+  for (; run.next(); ++it) {
+    const int buf = it & 1;
+    if (!mbar_wait_bounded(smem_u32(&b.tempty[buf]), ((it >> 1) & 1) ^ 1, &b.abort, err, kWaitLimitNs)) return false;
+    tc_fence_after();
+    const uint32_t d_tmem = b.tmem + (uint32_t)(buf * NT);
+    for (int kb = run.s.k0; kb < run.s.k1; ++kb) {
+      if (!mbar_wait_bounded(smem_u32(&b.full[ring.stage]), ring.phase, &b.abort, err, kWaitLimitNs)) return false;
+      tc_fence_after();
+      const uint32_t a_s = smem_base + ring.stage * Cfg<NT>::STAGE, b_s = a_s + A_BYTES;
+#pragma unroll
+      for (int kk = 0; kk < BK / 16; ++kk)
+        umma1(d_tmem, sdesc(a_s + kk * 32, 16, 1024), sdesc(b_s + kk * 32, 16, 1024), idesc,
+              (kb != run.s.k0 || kk != 0) ? 1u : 0u);
+      umma1_commit(smem_u32(&b.empty[ring.stage]));
+      ring.step();
+    }
+    umma1_commit(smem_u32(&b.tfull[buf]));
+  }
+  return true;
+}
+
+// The part of the CT threads in a run. `flags` and `part` are this run's (one word, NT * 128
+// floats per CTA). f.prepare(t) runs before, f.finish(t, c0, acc) after token columns
+// [c0, c0 + CHUNK) of tile t are staged: acc[(column - c0) * PITCH + weight row].
+template <int NT, class F>
+__device__ __forceinline__ bool take_run(Bars& b, Run run, int& it, int cta, uint32_t* flags, uint32_t epoch, float* part,
+                                         float* acc, int* err, F& f) {
+  constexpr int CHUNK = Cfg<NT>::CHUNK, HALF = CHUNK / 2;
+  const int cw = (threadIdx.x >> 5) - 2, lane = threadIdx.x & 31, lg = (threadIdx.x >> 5) & 3;
+  const int row = lg * 32 + lane, col0 = (cw >> 2) * HALF;
+  for (; run.next(); ++it) {
+    const int buf = it & 1;
+    const bool owner = run.s.k1 == run.nkb;
+    bool ok = mbar_wait_bounded(smem_u32(&b.tfull[buf]), (it >> 1) & 1, &b.abort, err, kWaitLimitNs);
+    const int q0 = owner && run.s.k0 > 0 ? run.first_cta() : cta;
+    if (ok && lane == 0)
+      for (int q = q0; ok && q < cta; ++q) ok = word_wait(flags + q, epoch, true, &b.abort, err);
+    if (owner) f.prepare(run.s.t);
+    if (ct_any(!ok)) return false;
+    tc_fence_after();
+    const uint32_t t_base = b.tmem + ((uint32_t)(lg * 32) << 16) + (uint32_t)(buf * NT);
+#pragma unroll 1
+    for (int c0 = 0; c0 < NT; c0 += CHUNK) {
+#pragma unroll
+      for (int c = 0; c < HALF; c += 8) {
+        const int col = c0 + col0 + c;
+        uint32_t u[8];
+        float v[8];
+        tmem_ld8(t_base + col, u);
+        tmem_ld_wait();
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(u[i]);
+        if (owner) {
+          for (int q = q0; q < cta; ++q) {
+            const float* in = part + ((int64_t)q * NT + col) * BM + row;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] += __ldcg(in + i * BM);
+          }
+#pragma unroll
+          for (int i = 0; i < 8; ++i) acc[(col0 + c + i) * PITCH + row] = v[i];
+        } else {
+          float* out = part + ((int64_t)cta * NT + col) * BM + row;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) __stcg(out + i * BM, v[i]);
+        }
+      }
+      if (c0 + CHUNK >= NT) {   // the accumulator is read: the next part may use it
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&b.tempty[buf]));
+      }
+      if (owner) {
+        ct_sync();
+        f.finish(run.s.t, c0, acc);
+        ct_sync();
+      }
+    }
+    if (!owner) {
+      __threadfence();
+      ct_sync();
+      if (threadIdx.x == 64) st_release(flags + cta, epoch);
+    }
+  }
+  return true;
+}
+
+// The last CTA of the launch to leave zeroes the counters and makes the flags stale.
+__device__ __forceinline__ void leave(uint32_t* header, uint32_t epoch) {
+  if (threadIdx.x == 0) {
+    __threadfence();
+    if (atomicAdd(header + 2, 1u) == gridDim.x - 1) {
+      for (int i = 2; i < 8; ++i) header[i] = 0;
+      header[1] = epoch;
+    }
+  }
+}
+
+}  // namespace stream
+}  // namespace moe

@@ -33,6 +33,17 @@ template <int ACT> __device__ __forceinline__ float act_slope(float z) {
   return 1.f;
 }
 
+// The activation by a value that is the same in the whole launch.
+__device__ __forceinline__ float act_any(int act, float z) {
+  switch (act) {
+    case MOE_ACT_RELU: return act_f<MOE_ACT_RELU>(z);
+    case MOE_ACT_SILU: return act_f<MOE_ACT_SILU>(z);
+    case MOE_ACT_GELU: return act_f<MOE_ACT_GELU>(z);
+    case MOE_ACT_GELU_TANH: return act_f<MOE_ACT_GELU_TANH>(z);
+    default: return z;
+  }
+}
+
 // CALL(ACT) with the activation `act` (validated by the caller) as a constant.
 #define MOE_ACT_SWITCH(act, CALL)                                    \
   switch (act) {                                                     \

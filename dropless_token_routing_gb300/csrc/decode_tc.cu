@@ -33,20 +33,28 @@ constexpr int RT = 128;            // rows of W_r that a CTA takes at a time
 // tables behind the staged result: selected experts, and the tokens' selections
 constexpr int kSlots = kMaxE * 2;                       // uint16 expert of each slot
 constexpr int kIdx = kDecodeMaxT * kMaxK * 2;           // uint16 [T][k]
-constexpr int kGate = kDecodeMaxT * kMaxK * 4;          // fp32 [T][k]
+constexpr int kGate = kDecodeMaxT * kMaxK * 4;          // fp32 [T][k]; first the bias
+static_assert(kGate >= kMaxE * 4, "the bias waits in the table of gates");
 constexpr int kExtra = kSlots + kIdx + kGate;
 
 struct DecodeTc {
   CUtensorMap w13, w2, ws13, ws2, x, h, hs;
   DecodeArgs a;
   int n_slab, slab;      // CTAs that take a slab of W_r, rows of each
-  int groups;            // row groups of a slab (threads side by side)
-  uint32_t* header;      // error, epoch, leave count, scores / tokens / hidden arrivals
-  uint32_t* flags;       // [3][CTA]
-  float* part;           // [3][CTA][NT][128]
-  float* score_part;     // [T][n_slab * groups][E]
+  uint32_t* header;      // error, epoch, leave count, counters (enum)
+  uint32_t* flags;       // [kDecodeRuns][CTA]
+  float* part;           // [kDecodeRuns][CTA][NT][128]
+  float* score_part;     // [T][n_slab][E]
+  uint64_t* chosen;      // [T][k] selections
   __nv_bfloat16 *hbuf, *hsbuf;   // [slot][NT][f], [S][NT][f_s]
 };
+
+enum Counter { SCORES = 3, ROWS };   // words of the header
+// A selection is one 64-bit word: gate (32 bits), expert (kTagShift bits) and the launch's tag
+// (22 bits, from the epoch, never 0). The words are cleared before the tags start again.
+constexpr int kTagShift = 10;
+constexpr uint32_t kTagMask = (1u << (32 - kTagShift)) - 1;
+static_assert(kMaxE == 1 << kTagShift, "");
 
 struct Tables {
   uint16_t* slots;
@@ -55,79 +63,76 @@ struct Tables {
 };
 
 // ------------------------------------------------------------------ scores and selection
-// Partial scores of this CTA's slab. Thread (group, column): groups of threads take every
-// groups-th row. xs: [RT][NT] floats of shared memory.
+__device__ __forceinline__ void gate_open() { asm volatile("bar.arrive 2, 288;" ::: "memory"); }
+__device__ __forceinline__ void gate_wait() { asm volatile("bar.sync 2, 288;" ::: "memory"); }
+
+// `n` floats global -> shared by the result warps, 16 bytes at a time where both ends allow.
+__device__ __forceinline__ void copy_floats(float* dst, const float* src, int n, bool vec) {
+  const int tid = threadIdx.x - 64;
+  if (vec) {
+#pragma unroll 4
+    for (int i = tid * 4; i < n; i += CT * 4) cp_async16(smem_u32(dst + i), src + i);
+  } else {
+#pragma unroll 4
+    for (int i = tid; i < n; i += CT)
+      asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst + i)), "l"(src + i) : "memory");
+  }
+}
+__device__ __forceinline__ void copies_landed() {
+  asm volatile("cp.async.wait_all;" ::: "memory");
+  ct_sync();
+}
+
+// Partial scores of this CTA's slab. xs: [rows][NT] floats, ws: `cap` floats of shared memory (stages of the ring that
+// the producer leaves alone until slab_free). The first part of W_r is asked for before anything
+// else: behind the weight stream's loads it would wait for all of those, so the producer starts
+// once it is on its way (gate_open). W_r goes through shared memory, not registers: the loop
+// stays a few instructions long (unrolled over 64 register loads it took 8 us, most of it
+// instruction fetches).
 template <int NT>
-__device__ __forceinline__ void partial_scores(const DecodeTc& p, int cta, float* xs) {
+__device__ __forceinline__ void partial_scores(const DecodeTc& p, int cta, float* xs, float* ws, int cap) {
+  constexpr int TS = 8;   // tokens at a time in registers
   const moe_dims& D = p.a.dm;
   const int T = (int)D.T, E = D.E, d = D.d, tid = threadIdx.x - 64;
   const int d0 = cta * p.slab, d1 = min(d, d0 + p.slab);
   const __nv_bfloat16* x = static_cast<const __nv_bfloat16*>(p.a.x);
-  const int cols = min(E, CT), group = tid / cols, rows = p.n_slab * p.groups;
-  for (int e0 = 0; e0 < E; e0 += CT) {
-    const int e = e0 + tid % cols;
-    float s[NT];
+  const int at_once = min(RT, cap / E);   // rows of W_r
+  for (int r0 = d0; r0 < d1; r0 += at_once) {
+    const int n = min(at_once, d1 - r0);
+    copy_floats(ws, p.a.w_r + (int64_t)r0 * E, n * E, E % 4 == 0);
+    if (r0 == d0) gate_open();
+    for (int i = tid; i < n * NT; i += CT) {
+      const int t = i / n, r = i - t * n;
+      xs[r * NT + t] = t < T ? __bfloat162float(x[(int64_t)t * d + r0 + r]) : 0.f;
+    }
+    copies_landed();
+    // one expert and TS tokens at a time
+#pragma unroll 1
+    for (int i = tid; i < E * ((T + TS - 1) / TS); i += CT) {
+      const int e = i % E, t0 = i / E * TS;
+      float* out = p.score_part + ((int64_t)t0 * p.n_slab + cta) * E + e;
+      float s[TS];
 #pragma unroll
-    for (int t = 0; t < NT; ++t) s[t] = 0.f;
-    for (int r0 = d0; r0 < d1; r0 += RT) {
-      const int n = min(RT, d1 - r0);
-      ct_sync();
-      for (int i = tid; i < n * T; i += CT) {
-        const int t = i / n, r = i - t * n;
-        xs[r * NT + t] = __bfloat162float(x[(int64_t)t * d + r0 + r]);
-      }
-      for (int i = tid; i < n * (NT - T); i += CT) xs[(i / (NT - T)) * NT + T + i % (NT - T)] = 0.f;
-      ct_sync();
-      if (group < p.groups && e < E) {
-#pragma unroll 8
-        for (int r = group; r < n; r += p.groups) {
-          const float w = __ldg(p.a.w_r + (int64_t)(r0 + r) * E + e);
-          const float4* xr = reinterpret_cast<const float4*>(xs + r * NT);
+      for (int t = 0; t < TS; ++t) s[t] = r0 > d0 && t0 + t < T ? __ldcg(out + (int64_t)t * p.n_slab * E) : 0.f;
+#pragma unroll 4
+      for (int r = 0; r < n; ++r) {
+        const float w = ws[r * E + e];
+        const float4* xr = reinterpret_cast<const float4*>(xs + r * NT + t0);
 #pragma unroll
-          for (int t = 0; t < NT; t += 4) {
-            const float4 v = xr[t / 4];
-            s[t] = fmaf(v.x, w, s[t]);
-            s[t + 1] = fmaf(v.y, w, s[t + 1]);
-            s[t + 2] = fmaf(v.z, w, s[t + 2]);
-            s[t + 3] = fmaf(v.w, w, s[t + 3]);
-          }
+        for (int t = 0; t < TS; t += 4) {
+          const float4 v = xr[t / 4];
+          s[t] = fmaf(v.x, w, s[t]);
+          s[t + 1] = fmaf(v.y, w, s[t + 1]);
+          s[t + 2] = fmaf(v.z, w, s[t + 2]);
+          s[t + 3] = fmaf(v.w, w, s[t + 3]);
         }
       }
-    }
-    if (group < p.groups && e < E) {
 #pragma unroll
-      for (int t = 0; t < NT; ++t)
-        if (t < T) __stcg(p.score_part + ((int64_t)t * rows + cta * p.groups + group) * E + e, s[t]);
+      for (int t = 0; t < TS; ++t)
+        if (t0 + t < T) __stcg(out + (int64_t)t * p.n_slab * E, s[t]);
     }
+    ct_sync();
   }
-}
-
-// Token t's scores into `scores` (shared memory, [E]); `tmp`: [CT] floats of shared memory.
-__device__ __forceinline__ void sum_scores(const DecodeTc& p, int t, float* scores, float* tmp) {
-  const int E = p.a.dm.E, tid = threadIdx.x - 64;
-  if (p.a.logits_in != nullptr) {
-    for (int e = tid; e < E; e += CT) scores[e] = p.a.logits_in[(int64_t)t * E + e];
-  } else {
-    const int rows = p.n_slab * p.groups;
-    const float* in = p.score_part + (int64_t)t * rows * E;
-    for (int e0 = 0; e0 < E; e0 += CT) {
-      // `ng` threads share a column, each summing every ng-th row in order
-      const int cols = min(E - e0, CT), ng = CT / cols, g = tid / cols, e = e0 + tid % cols;
-      float s = 0.f;
-      if (g < ng) {
-#pragma unroll 16
-        for (int r = g; r < rows; r += ng) s += __ldcg(in + (int64_t)r * E + e);
-      }
-      ct_sync();
-      tmp[tid] = s;
-      ct_sync();
-      if (tid < cols) {
-        for (int i = 1; i < ng; ++i) s += tmp[i * cols + tid];
-        scores[e0 + tid] = s;
-      }
-    }
-  }
-  ct_sync();
 }
 
 // Order-preserving map of a float to uint32, above 0 for every finite one; NaN is ranked last.
@@ -136,66 +141,115 @@ __device__ __forceinline__ uint32_t rank_key(float x) {
   const uint32_t u = __float_as_uint(x + 0.f);   // -0 ranks as +0
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
+__device__ __forceinline__ float key_value(uint32_t key) {
+  return __uint_as_float((key & 0x80000000u) ? (key & 0x7fffffffu) : ~key);
+}
 
-// The k largest of `scores` (+ bias), descending, ties to the lower index, and their gates
-// (softmax over the k): one warp. Element i of a lane is expert lane + 32 i, so a lane's first
-// largest is its lowest expert.
-__device__ __forceinline__ void select_topk(const DecodeTc& p, int t, const float* scores, uint32_t* keys, int lane) {
+// Token t's scores, ranked. Shared memory: buf [cap] floats (the ring, idle in a CTA with a token),
+// through which the partial rows come, all of them in flight; tmp [CT]; keys [E], a multiple of 4
+// readable; top [2 * kMaxK]; bias [E].
+// An expert's rank is the number of experts before it (larger key, or the same and a lower index),
+// which every thread counts for its own: no rounds over k. All loops are short on purpose: this is
+// code that a CTA runs once, and fetching it is what it costs.
+__device__ __forceinline__ void select_experts(const DecodeTc& p, int t, float* buf, int cap, float* tmp, uint32_t* keys,
+                                               uint32_t* top, const float* bias, uint32_t tag) {
   const moe_dims& D = p.a.dm;
-  const int E = D.E, k = D.k;
-  for (int e = lane; e < E; e += 32) {
-    float s = scores[e];
-    if (p.a.bias != nullptr) s = s + p.a.bias[e];   // one fp32 rounding, as in the routing kernel
-    keys[e] = rank_key(s);
-  }
-  uint32_t my_key = 0, my_e = 0;
-  for (int j = 0; j < k; ++j) {
-    uint32_t kb = 0, eb = 0xffffffffu;
-    for (int e = lane; e < E; e += 32) {
-      const uint32_t key = keys[e];
-      if (key > kb) {
-        kb = key;
-        eb = e;
+  const int E = D.E, k = D.k, tid = threadIdx.x - 64;
+  const bool given = p.a.logits_in != nullptr;
+  const int rows = given ? 1 : p.n_slab, at_once = cap / E;
+  const float* in = given ? p.a.logits_in + (int64_t)t * E : p.score_part + (int64_t)t * rows * E;
+  for (int i = tid; i < ((E + 3) & ~3); i += CT) keys[i] = 0u;
+  for (int r0 = 0; r0 < rows; r0 += at_once) {
+    const int n = min(at_once, rows - r0);
+    copy_floats(buf, in + (int64_t)r0 * E, n * E, E % 4 == 0);
+    copies_landed();
+#pragma unroll 1
+    for (int e0 = 0; e0 < E; e0 += CT) {
+      // ng threads share a column, each summing every ng-th row
+      const int cols = min(E - e0, CT), ng = CT / cols, g = tid / cols, c = e0 + tid % cols;
+      float s = 0.f;
+      if (g < ng) {
+#pragma unroll 4
+        for (int r = g; r < n; r += ng) s += buf[r * E + c];
       }
+      tmp[tid] = s;
+      ct_sync();
+      if (tid < cols) {
+        for (int i = cols; i < ng * cols; i += cols) s += tmp[tid + i];
+        if (r0 > 0) s += __uint_as_float(keys[c]);   // the sum so far
+        if (r0 + n < rows) keys[c] = __float_as_uint(s);
+        else keys[c] = rank_key(p.a.bias != nullptr ? s + bias[c] : s);   // one fp32 rounding
+      }
+      ct_sync();
     }
-    const uint32_t km = __reduce_max_sync(0xffffffffu, kb);
-    const uint32_t em = __reduce_min_sync(0xffffffffu, kb == km ? eb : 0xffffffffu);
-    if ((em & 31u) == (uint32_t)lane) keys[em] = 0u;   // taken
-    if (j == lane) {
-      my_key = km;
-      my_e = em;
-    }
-    __syncwarp();
   }
-  const float v = __uint_as_float((my_key & 0x80000000u) ? (my_key & 0x7fffffffu) : ~my_key);
-  const float top = __shfl_sync(0xffffffffu, v, 0);
-  float w = lane < k ? expf(v - top) : 0.f, sum = w;
+#pragma unroll 1
+  for (int e = tid; e < E; e += CT) {
+    const uint32_t key = keys[e];
+    int rank = 0;
+#pragma unroll 2
+    for (int i = 0; i < E; i += 4) {   // keys past E are 0, below every other
+      const uint4 v = *reinterpret_cast<const uint4*>(keys + i);
+      rank += (v.x > key || (v.x == key && i < e)) + (v.y > key || (v.y == key && i + 1 < e)) +
+              (v.z > key || (v.z == key && i + 2 < e)) + (v.w > key || (v.w == key && i + 3 < e));
+    }
+    if (rank < k) {
+      top[rank] = e;
+      top[kMaxK + rank] = key;
+    }
+  }
+  ct_sync();
+  if (tid < 32) {
+    const float v = key_value(top[kMaxK + min(tid, k - 1)]);
+    const float largest = __shfl_sync(0xffffffffu, v, 0);   // by all lanes
+    float w = tid < k ? expf(v - largest) : 0.f, sum = w;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  w /= sum;
-  if (lane < k) {
-    const int64_t q = (int64_t)t * k + lane;
-    __stcg(reinterpret_cast<int32_t*>(p.a.ws + p.a.L.idx) + q, (int32_t)my_e);
-    __stcg(reinterpret_cast<float*>(p.a.ws + p.a.L.gate) + q, w);
-    if (p.a.idx_out != nullptr) p.a.idx_out[q] = (int32_t)my_e;
-    if (p.a.gate_out != nullptr) p.a.gate_out[q] = w;
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    w /= sum;
+    if (tid < k) {
+      const int64_t q = (int64_t)t * k + tid;
+      const int32_t e = (int32_t)top[tid];
+      // expert, gate and the launch in one word: whoever reads it needs no other signal
+      asm volatile("st.relaxed.gpu.global.u64 [%0], %1;" ::"l"(p.chosen + q),
+                   "l"((uint64_t)(tag << kTagShift | (uint32_t)e) << 32 | __float_as_uint(w))
+                   : "memory");
+      if (p.a.idx_out != nullptr) p.a.idx_out[q] = e;
+      if (p.a.gate_out != nullptr) p.a.gate_out[q] = w;
+    }
   }
 }
 
-// The selected experts in ascending order, and the tokens' selections. Returns their number.
+// The selected experts in ascending order, and the tokens' selections, once they are all there
+// (their words carry this launch's tag). Returns their number, 0 when the wait ran out.
 // bits: kMaxE / 32 words, count: one int of shared memory.
-__device__ __forceinline__ int build_tables(const DecodeTc& p, const Tables& tb, uint32_t* bits, int* count) {
+__device__ __forceinline__ int build_tables(const DecodeTc& p, const Tables& tb, uint32_t tag, uint32_t* bits, int* count,
+                                            volatile int* abort, int* err) {
   const moe_dims& D = p.a.dm;
   const int n = (int)D.T * D.k, tid = threadIdx.x - 64;
   if (tid < kMaxE / 32) bits[tid] = 0u;
   ct_sync();
-  for (int i = tid; i < n; i += CT) {
-    const int e = __ldcg(reinterpret_cast<const int32_t*>(p.a.ws + p.a.L.idx) + i);
+  const uint64_t t0 = global_ns();
+  bool ok = true;
+#pragma unroll 1
+  for (int i = tid; ok && i < n; i += CT) {
+    uint64_t w;
+    while (true) {
+      asm volatile("ld.relaxed.gpu.global.u64 %0, [%1];" : "=l"(w) : "l"(p.chosen + i) : "memory");
+      if ((uint32_t)(w >> (32 + kTagShift)) == tag) break;
+      if (*abort || global_ns() - t0 > kWaitLimitNs) {
+        if (!*abort) record_error(err, MOE_ERR_DEVICE_TIMEOUT);
+        *abort = 1;
+        ok = false;
+        break;
+      }
+    }
+    if (!ok) break;
+    const int e = (int)(w >> 32) & (kMaxE - 1);
     tb.idx[i] = (uint16_t)e;
-    tb.gate[i] = __ldcg(reinterpret_cast<const float*>(p.a.ws + p.a.L.gate) + i);
+    tb.gate[i] = __uint_as_float((uint32_t)w);
     atomicOr(bits + (e >> 5), 1u << (e & 31));
   }
-  ct_sync();
+  if (ct_any(!ok)) return 0;
   if (tid < 32) {   // lane i: word i of the bitmap
     const uint32_t w = bits[tid];
     int c = __popc(w);
@@ -213,66 +267,117 @@ __device__ __forceinline__ int build_tables(const DecodeTc& p, const Tables& tb,
   return *count;
 }
 
+// ------------------------------------------------------------------ the runs
+// In the order in which every CTA works on them. (Dividing the output's K into a first part that
+// needs no rows of the slower CTAs, to keep the stream going meanwhile, measured no better: the
+// joins of a further run cost what it hides.)
+enum RunId { SHARED = 0, HIDDEN, OUTPUT };
+static_assert(OUTPUT + 1 == kDecodeRuns, "");
+
+struct Plan {
+  int per_h, per_s, k_sh, nkb_d, tiles_out;   // tiles of an expert, K blocks of the shared ones
+  int cta, n_cta, T;
+  int total;                                  // routed hidden tiles (after the selection)
+  __device__ Plan(const moe_dims& D, int cta_, int n_cta_) {
+    per_h = D.f / 64;
+    per_s = D.S > 0 ? D.f_s / 64 : 1;
+    k_sh = D.S * per_s;
+    nkb_d = D.d / 64;
+    tiles_out = (D.d + BM - 1) / BM;
+    cta = cta_;
+    n_cta = n_cta_;
+    T = (int)D.T;
+    total = 0;
+  }
+  __device__ void select(int active) { total = active * per_h; }
+  // The CTAs that select for a token leave the shared experts to the others: behind a stream's
+  // loads their own would wait.
+  __device__ Run run(int r) const {
+    const int tiles = r == SHARED ? k_sh : r == HIDDEN ? total : tiles_out;
+    const int nkb = r == OUTPUT ? k_sh + total : nkb_d;
+    const int skip = r == SHARED ? T : 0;
+    return Run(tiles, nkb, cta - skip, n_cta - skip);
+  }
+};
+
+// Consecutive K blocks of the output: the shared experts' first, then the selected ones'.
+struct Blocks {
+  bool shared;
+  int slot, at, per;   // block `at` of the `per` of an expert
+  __device__ Blocks(const Plan& plan, int kb) {
+    shared = kb < plan.k_sh;
+    per = shared ? plan.per_s : plan.per_h;
+    if (!shared) kb -= plan.k_sh;
+    slot = kb / per;
+    at = kb - slot * per;
+  }
+  __device__ void step(const Plan& plan) {
+    if (++at < per) return;
+    at = 0;
+    ++slot;
+    if (shared && slot * per == plan.k_sh) {
+      shared = false;
+      slot = 0;
+      per = plan.per_h;
+    }
+  }
+};
+
 // ------------------------------------------------------------------ results
-// A hidden tile: rows 0..63 gate, 64..127 up. slots == nullptr: shared experts (weight 1).
-template <int NT> struct HiddenFinish {
+// What becomes of a tile: SHARED, HIDDEN: rows 0..63 gate, 64..127 up -> hidden rows; OUTPUT: y.
+template <int NT> struct Finish {
   const DecodeTc& p;
   const Tables& tb;
-  const bool shared;
-  const int per;                   // tiles of an expert
-  float* wt;                       // [NT] weights of the tile's expert
+  const Plan& plan;
+  float* wt;                       // [NT] weights of a hidden tile's expert
+  int r;
   __device__ void prepare(int64_t tile) {
     const int t = threadIdx.x - 64, k = p.a.dm.k;
-    if (t < (int)p.a.dm.T) {
-      float w = shared ? 1.f : 0.f;
-      if (!shared) {
-        const int e = tb.slots[tile / per];
-        for (int j = 0; j < k; ++j)
-          if (tb.idx[t * k + j] == e) w = tb.gate[t * k + j];
+    if (r != OUTPUT && t < plan.T) {
+      float w = r == SHARED ? 1.f : 0.f;
+      if (r != SHARED) {
+        const int e = tb.slots[(int)tile / plan.per_h];
+#pragma unroll 1
+        for (int j = t * k; j < t * k + k; ++j)
+          if (tb.idx[j] == e) w = tb.gate[j];
       }
       wt[t] = w;
     }
   }
   __device__ void finish(int64_t tile, int, const float* acc) {
-    const int T = (int)p.a.dm.T, f = shared ? p.a.dm.f_s : p.a.dm.f;
-    const int64_t slot = tile / per;
-    const int j0 = (int)(tile - slot * per) * 64, c = ((threadIdx.x - 64) & 31) * 2;
-    __nv_bfloat16* out = (shared ? p.hsbuf : p.hbuf) + slot * NT * f + j0 + c;
-    for (int t = (threadIdx.x - 64) >> 5; t < T; t += CW) {
-      const float w = wt[t];
-      float h[2] = {0.f, 0.f};
-      if (w != 0.f) {
-        const float2 g = *reinterpret_cast<const float2*>(acc + t * PITCH + c);
-        const float2 u = *reinterpret_cast<const float2*>(acc + t * PITCH + 64 + c);
-        h[0] = w * (silu_f(g.x) * u.x);
-        h[1] = w * (silu_f(g.y) * u.y);
+    const int T = plan.T, tid = threadIdx.x - 64;
+    if (r != OUTPUT) {
+      const int f = r == SHARED ? p.a.dm.f_s : p.a.dm.f, per = r == SHARED ? plan.per_s : plan.per_h;
+      const int at = (int)tile, slot = at / per, c = (tid & 31) * 2;
+      __nv_bfloat16* out = (r == SHARED ? p.hsbuf : p.hbuf) + (int64_t)slot * NT * f + (at - slot * per) * 64 + c;
+#pragma unroll 1
+      for (int t = tid >> 5; t < T; t += CW) {
+        const float w = wt[t];
+        float h0 = 0.f, h1 = 0.f;
+        if (w != 0.f) {
+          const float2 g = *reinterpret_cast<const float2*>(acc + t * PITCH + c);
+          const float2 u = *reinterpret_cast<const float2*>(acc + t * PITCH + 64 + c);
+          h0 = w * (silu_f(g.x) * u.x);
+          h1 = w * (silu_f(g.y) * u.y);
+        }
+        *reinterpret_cast<uint32_t*>(out + (int64_t)t * f) = pack_bf16x2(h0, h1);
       }
-      *reinterpret_cast<uint32_t*>(out + (int64_t)t * f) = pack_bf16x2(h[0], h[1]);
-    }
-  }
-};
-
-struct OutputFinish {
-  const DecodeTc& p;
-  __device__ void prepare(int64_t) {}
-  __device__ void finish(int64_t tile, int, const float* acc) {
-    const int T = (int)p.a.dm.T, d = p.a.dm.d, tid = threadIdx.x - 64;
-    const int q = (tid & 15) * 8, n = (int)tile * BM + q;
-    if (n >= d) return;   // d is a multiple of 64
-    for (int t = tid >> 4; t < T; t += 16) {
-      float v[8], r[8];
-      *reinterpret_cast<float4*>(v) = *reinterpret_cast<const float4*>(acc + t * PITCH + q);
-      *reinterpret_cast<float4*>(v + 4) = *reinterpret_cast<const float4*>(acc + t * PITCH + q + 4);
-      Vec8<__nv_bfloat16> b;
-      const int64_t at = (int64_t)t * d + n;
-      if (p.a.residual != nullptr) {   // may be y's own buffer
-        b.v = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.a.residual) + at);
-        b.to_float(r);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] += r[i];
+    } else {
+      const int d = p.a.dm.d, q = (tid & 31) * 4, n = (int)tile * BM + q;
+      if (n >= d) return;   // d is a multiple of 64
+#pragma unroll 1
+      for (int t = tid >> 5; t < T; t += CW) {
+        float4 v = *reinterpret_cast<const float4*>(acc + t * PITCH + q);
+        const int64_t at = (int64_t)t * d + n;
+        if (p.a.residual != nullptr) {   // may be y's own buffer
+          const uint2 u = *reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(p.a.residual) + at);
+          const float2 a = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&u.x));
+          const float2 b = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&u.y));
+          v = make_float4(v.x + a.x, v.y + a.y, v.z + b.x, v.w + b.y);
+        }
+        *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.a.y) + at) =
+            make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
       }
-      b.from_float(v);
-      b.store(static_cast<__nv_bfloat16*>(p.a.y) + at);
     }
   }
 };
@@ -280,13 +385,14 @@ struct OutputFinish {
 // ------------------------------------------------------------------ the kernel
 template <int NT>
 __global__ void __launch_bounds__(THREADS, 1) decode_kernel(const __grid_constant__ DecodeTc p) {
-  constexpr int STAGES = Cfg<NT>::stages(kExtra), STAGE = Cfg<NT>::STAGE;
+  constexpr int STAGES = Cfg<NT>::stages(kExtra), STAGE = Cfg<NT>::STAGE, SLAB0 = STAGES - 3;
   static_assert(RT * NT * 4 <= Cfg<NT>::ACC_BYTES, "the slab of x is staged where the result is");
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) Bars b;
   __shared__ uint32_t s_bits[kMaxE / 32];
   __shared__ int s_active;
   __shared__ float s_wt[NT];
+  __shared__ uint32_t s_top[2 * kMaxK];
   const moe_dims& D = p.a.dm;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -296,109 +402,94 @@ __global__ void __launch_bounds__(THREADS, 1) decode_kernel(const __grid_constan
   const Tables tb = {reinterpret_cast<uint16_t*>(tables), reinterpret_cast<uint16_t*>(tables + kSlots),
                      reinterpret_cast<float*>(tables + kSlots + kIdx)};
   int* err = reinterpret_cast<int*>(p.header);
-  const int cta = (int)blockIdx.x, n_cta = (int)gridDim.x, T = (int)D.T;
+  const int cta = (int)blockIdx.x, n_cta = (int)gridDim.x, T = (int)D.T;   // T < n_cta
   setup<NT, STAGES>(b, warp);
   const uint32_t epoch = *reinterpret_cast<volatile uint32_t*>(p.header + 1) + 1;
-  uint32_t* arrived = p.header + 3;   // scores, tokens, hidden
 
-  const int per_h = D.f / 64, per_s = D.S > 0 ? D.f_s / 64 : 0, nkb_d = D.d / 64;
-  const int tiles_out = (D.d + BM - 1) / BM;
-  auto shared_run = [&]() { return Run((int64_t)D.S * per_s, nkb_d, cta, n_cta); };
-  auto hidden_run = [&](int active) { return Run((int64_t)active * per_h, nkb_d, cta, n_cta); };
-  auto output_run = [&](int active) { return Run(tiles_out, active * per_h + D.S * per_s, cta, n_cta); };
+  const uint32_t tag = 1 + epoch % kTagMask;
+  const bool scores = p.a.logits_in == nullptr && cta < p.n_slab;
+  Plan plan(D, cta, n_cta);
 
   if (warp == 0) {
     // ------------------------------------------------------------ producer
+    if (scores) gate_wait();
     if (lane == 0) {
       Ring<STAGES> ring;
       int64_t loaded = 0;
       bool ok = true;
-      auto acquire = [&]() {
-        ok = mbar_wait_bounded(smem_u32(&b.empty[ring.stage]), ring.phase ^ 1u, &b.abort, err, kWaitLimitNs);
-        if (ok) mbar_arrive_expect_tx(smem_u32(&b.full[ring.stage]), STAGE);
-        return ok;
+      // the token rows of an output block, into stage q
+      auto rows = [&](const Ring<STAGES>& q, const Blocks& k) {
+        tma2d(smem_base + q.stage * STAGE + A_BYTES, k.shared ? &p.hs : &p.h, smem_u32(&b.full[q.stage]), k.at * BK,
+              k.slot * NT);
       };
-      // 64 gate and 64 up rows of one expert, and the tokens
-      auto hidden = [&](Run run, bool shared) {
-        const CUtensorMap* wm = shared ? &p.ws13 : &p.w13;
-        const int per = shared ? per_s : per_h, f = shared ? D.f_s : D.f;
-        while (ok && run.next()) {
-          const int slot = (int)(run.s.t / per), j0 = (int)(run.s.t - (int64_t)slot * per) * 64;
-          const int e = shared ? slot : tb.slots[slot];
-          for (int kb = run.s.k0; kb < run.s.k1 && acquire(); ++kb) {
-            const uint32_t a_s = smem_base + ring.stage * STAGE, bar = smem_u32(&b.full[ring.stage]);
-            tma3d(a_s, wm, bar, kb * BK, j0, e);
-            tma3d(a_s + A_BYTES / 2, wm, bar, kb * BK, f + j0, e);
-            tma2d(a_s + A_BYTES, &p.x, bar, kb * BK, 0);
-            ring.step();
-            ++loaded;
-          }
+#pragma unroll 1
+      for (int r = D.S > 0 ? SHARED : HIDDEN; ok && r <= OUTPUT; ++r) {
+        if (r == HIDDEN) {
+          ok = bar_wait(&b.list, 0, &b.abort, err);
+          if (!ok) break;
+          plan.select(s_active);
         }
-      };
-      if (D.S > 0) hidden(shared_run(), true);
-      ok = ok && mbar_wait_bounded(smem_u32(&b.list), 0, &b.abort, err, kWaitLimitNs);
-      if (ok) {
-        const int active = s_active;
-        hidden(hidden_run(active), false);
-        // the output's weights at once, its tokens' hidden rows once every CTA has written its own
-        const int routed = active * per_h;
-        Run run = output_run(active), tokens = run;
-        auto weights = [&](int64_t tile, int kb) {
-          const uint32_t a_s = smem_base + ring.stage * STAGE, bar = smem_u32(&b.full[ring.stage]);
-          if (kb < routed) {
-            const int slot = kb / per_h;
-            tma3d(a_s, &p.w2, bar, (kb - slot * per_h) * BK, (int)tile * BM, tb.slots[slot]);
-          } else {
-            const int s = (kb - routed) / per_s;
-            tma3d(a_s, &p.ws2, bar, (kb - routed - s * per_s) * BK, (int)tile * BM, s);
-          }
-        };
-        auto rows = [&](const Ring<STAGES>& r, int kb) {
-          const uint32_t b_s = smem_base + r.stage * STAGE + A_BYTES, bar = smem_u32(&b.full[r.stage]);
-          if (kb < routed) {
-            const int slot = kb / per_h;
-            tma2d(b_s, &p.h, bar, (kb - slot * per_h) * BK, slot * NT);
-          } else {
-            const int s = (kb - routed) / per_s;
-            tma2d(b_s, &p.hs, bar, (kb - routed - s * per_s) * BK, s * NT);
-          }
-        };
-        Ring<STAGES> behind = ring;   // the first stage whose tokens are still to be loaded
+        Run run = plan.run(r), tokens = run;
+        // The output's weights are loaded at once, its tokens' hidden rows when every CTA has written
+        // its own: `ahead` stages, from `behind` on, lack them.
+        bool have_rows = r != OUTPUT;
+        Ring<STAGES> behind = ring;
         int ahead = 0;
-        bool waited = false;
-        auto wait_hidden = [&]() {
-          ok = word_wait(arrived + 2, (uint32_t)n_cta, false, &b.abort, err);
+        auto wait_rows = [&]() {
+          ok = word_wait(p.header + ROWS, (uint32_t)n_cta, &b.abort, err);
           asm volatile("fence.proxy.async;" ::: "memory");   // generic writes of other CTAs, read by TMA
-          waited = true;
-        };
-        auto catch_up = [&]() {
-          // the same blocks again, from the run's start, for their tokens
-          int left = ahead;
-          while (left > 0 && tokens.next())
-            for (int kb = tokens.s.k0; kb < tokens.s.k1 && left > 0; ++kb, --left) {
-              rows(behind, kb);
+          have_rows = true;
+          while (ok && ahead > 0 && tokens.next()) {   // the same blocks again, from the run's start
+            Blocks k(plan, tokens.s.k0);
+            for (int kb = tokens.s.k0; kb < tokens.s.k1 && ahead > 0; ++kb, --ahead) {
+              rows(behind, k);
               behind.step();
+              k.step(plan);
             }
+          }
         };
+        // the next stage, or false
+        auto acquire = [&]() {
+          if (loaded == SLAB0 && scores)   // the ring's last stages hold W_r first
+            ok = ok && bar_wait(&b.slab_free, 0, &b.abort, err);
+          ok = ok && bar_wait(&b.empty[ring.stage], ring.phase ^ 1u, &b.abort, err);
+          if (ok) mbar_arrive_expect_tx(smem_u32(&b.full[ring.stage]), STAGE);
+          return ok;
+        };
+#pragma unroll 1
         while (ok && run.next()) {
-          for (int kb = run.s.k0; kb < run.s.k1 && ok; ++kb) {
-            if (!waited && ahead == STAGES) {   // the ring is full of weights
-              wait_hidden();
-              if (!ok) break;
-              catch_up();
+          if (r != OUTPUT) {   // 64 gate and the 64 up rows beside them
+            const int per = r == SHARED ? plan.per_s : plan.per_h, f = r == SHARED ? D.f_s : D.f;
+            const int tile = (int)run.s.t, slot = tile / per, j0 = (tile - slot * per) * 64;
+            const int e = r == SHARED ? slot : tb.slots[slot];
+            const CUtensorMap* m = r == SHARED ? &p.ws13 : &p.w13;
+#pragma unroll 1
+            for (int kb = run.s.k0; kb < run.s.k1 && acquire(); ++kb) {
+              const uint32_t a_s = smem_base + ring.stage * STAGE, bar = smem_u32(&b.full[ring.stage]);
+              tma3d(a_s, m, bar, kb * BK, j0, e);
+              tma3d(a_s + A_BYTES / 2, m, bar, kb * BK, f + j0, e);
+              tma2d(a_s + A_BYTES, &p.x, bar, kb * BK, 0);
+              ring.step();
+              ++loaded;
             }
-            if (!acquire()) break;
-            weights(run.s.t, kb);
-            if (waited) rows(ring, kb);
-            else ++ahead;
-            ring.step();
-            ++loaded;
+          } else {
+            Blocks k(plan, run.s.k0);
+            const int n0 = (int)run.s.t * BM;
+#pragma unroll 1
+            for (int kb = run.s.k0; kb < run.s.k1; ++kb) {
+              if (!have_rows && ahead == STAGES) wait_rows();   // the ring is full of weights
+              if (!acquire()) break;
+              tma3d(smem_base + ring.stage * STAGE, k.shared ? &p.ws2 : &p.w2, smem_u32(&b.full[ring.stage]), k.at * BK, n0,
+                    k.shared ? k.slot : tb.slots[k.slot]);
+              if (have_rows) rows(ring, k);
+              else ++ahead;
+              ring.step();
+              ++loaded;
+              k.step(plan);
+            }
           }
         }
-        if (ok && !waited) {
-          wait_hidden();
-          if (ok) catch_up();
-        }
+        if (ok && !have_rows && ahead > 0) wait_rows();
       }
       drain<STAGES>(b, ring, loaded, err);
     }
@@ -409,70 +500,73 @@ __global__ void __launch_bounds__(THREADS, 1) decode_kernel(const __grid_constan
       Ring<STAGES> ring;
       int it = 0;
       bool ok = true;
-      if (D.S > 0) ok = mma_run<NT, STAGES>(b, smem_base, shared_run(), ring, it, err);
-      ok = ok && mbar_wait_bounded(smem_u32(&b.list), 0, &b.abort, err, kWaitLimitNs);
-      if (ok) {
-        const int active = s_active;
-        ok = mma_run<NT, STAGES>(b, smem_base, hidden_run(active), ring, it, err) &&
-             mma_run<NT, STAGES>(b, smem_base, output_run(active), ring, it, err);
+#pragma unroll 1
+      for (int r = D.S > 0 ? SHARED : HIDDEN; ok && r <= OUTPUT; ++r) {
+        if (r == HIDDEN) {
+          ok = bar_wait(&b.list, 0, &b.abort, err);
+          if (!ok) break;
+          plan.select(s_active);
+        }
+        ok = mma_run<NT, STAGES>(b, smem_base, plan.run(r), ring, it, err);
       }
       umma1_commit(smem_u32(&b.final));   // every MMA retired before the tensor memory is released
-      mbar_wait_bounded(smem_u32(&b.final), 0, nullptr, err, kWaitLimitNs);
+      bar_wait(&b.final, 0, nullptr, err);
     }
     __syncwarp();
   } else {
     // ------------------------------------------------------------ scores, selection, results
-    const int64_t part_run = (int64_t)n_cta * NT * BM;
     int it = 0;
     bool ok = true;
-    if (p.a.logits_in == nullptr && cta < p.n_slab) {
-      partial_scores<NT>(p, cta, acc);
+    // the bias waits in the table of gates, which is filled later (read when it is needed, it would
+    // come from HBM behind the stream)
+    if (cta < T && p.a.bias != nullptr) copy_floats(tb.gate, p.a.bias, D.E, D.E % 4 == 0);
+    if (scores) {
+      partial_scores<NT>(p, cta, acc, reinterpret_cast<float*>(smem + SLAB0 * STAGE), (STAGES - SLAB0) * STAGE / 4);
       __threadfence();
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // the stages become the TMA's again
       ct_sync();
-      if (threadIdx.x == 64) add_release(arrived, 1u);
+      if (threadIdx.x == 64) {
+        add_release(p.header + SCORES, 1u);
+        mbar_arrive(smem_u32(&b.slab_free));
+      }
     }
     if (cta < T) {
       if (p.a.logits_in == nullptr) {
-        if (threadIdx.x == 64) ok = word_wait(arrived, (uint32_t)p.n_slab, false, &b.abort, err);
+        if (threadIdx.x == 64) ok = word_wait(p.header + SCORES, (uint32_t)p.n_slab, &b.abort, err);
         ok = !ct_any(!ok);
       }
-      for (int t = cta; ok && t < T; t += n_cta) {
-        ct_sync();
-        sum_scores(p, t, acc, acc + kMaxE);
-        if (warp == 2) {
-          select_topk(p, t, acc, reinterpret_cast<uint32_t*>(acc), lane);
-          __threadfence();
-          __syncwarp();
-          if (lane == 0) add_release(arrived + 1, 1u);
-        }
-      }
+      if (ok)
+        select_experts(p, cta, reinterpret_cast<float*>(smem), STAGES * STAGE / 4, acc + kMaxE,
+                       reinterpret_cast<uint32_t*>(acc), s_top, tb.gate, tag);
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // the ring held partial scores
       ct_sync();
     }
-    if (ok && D.S > 0) {
-      HiddenFinish<NT> f{p, tb, true, per_s, s_wt};
-      ok = take_run<NT>(b, shared_run(), it, cta, p.flags, epoch, p.part, acc, err, f);
-    }
-    if (ok) {
-      if (threadIdx.x == 64) ok = word_wait(arrived + 1, (uint32_t)T, false, &b.abort, err);
-      ok = !ct_any(!ok);
-    }
-    if (ok) {
-      const int active = build_tables(p, tb, s_bits, &s_active);
-      if (threadIdx.x == 64) mbar_arrive(smem_u32(&b.list));
-      HiddenFinish<NT> f{p, tb, false, per_h, s_wt};
-      ok = take_run<NT>(b, hidden_run(active), it, cta, p.flags + n_cta, epoch, p.part + part_run, acc, err, f);
-      if (ok) {
+    Finish<NT> f{p, tb, plan, s_wt, 0};
+#pragma unroll 1
+    for (int r = D.S > 0 ? SHARED : HIDDEN; ok && r <= OUTPUT; ++r) {
+      if (r == HIDDEN) {
+        const int active = build_tables(p, tb, tag, s_bits, &s_active, &b.abort, err);
+        ok = active > 0;
+        if (!ok) break;
+        plan.select(active);
+        if (threadIdx.x == 64) mbar_arrive(smem_u32(&b.list));
+      }
+      f.r = r;
+      ok = take_run<NT>(b, plan.run(r), it, r == SHARED ? cta - T : cta, p.flags + r * n_cta, epoch,
+                        p.part + (int64_t)r * n_cta * NT * BM, acc, err, f);
+      if (ok && r == HIDDEN) {
+        // this CTA's hidden rows are written, for the TMA of any CTA
         __threadfence();
         asm volatile("fence.proxy.async;" ::: "memory");
         ct_sync();
-        if (threadIdx.x == 64) add_release(arrived + 2, 1u);
-        OutputFinish o{p};
-        take_run<NT>(b, output_run(active), it, cta, p.flags + 2 * n_cta, epoch, p.part + 2 * part_run, acc, err, o);
+        if (threadIdx.x == 64) add_release(p.header + ROWS, 1u);
       }
     }
   }
   teardown<NT>(b, warp);
-  leave(p.header, epoch);
+  // the tags start again after this launch: no word may still hold one
+  if (leave(p.header, epoch) && tag == kTagMask)
+    for (int i = 0; i < kDecodeMaxT * kMaxK; ++i) p.chosen[i] = 0;
 }
 
 template <int NT>
@@ -512,6 +606,7 @@ int launch_decode_tc(const DecodeArgs& a, int num_sms, cudaStream_t st) {
   const moe_dims& D = a.dm;
   const int nt = decode_token_columns(D.T);
   if (num_sms > kMaxStreamCtas) num_sms = kMaxStreamCtas;
+  if (num_sms <= kDecodeMaxT) return MOE_ERR_UNSUPPORTED_DEVICE;
   DecodeTc p;
   memset(&p, 0, sizeof(p));
   p.a = a;
@@ -519,11 +614,11 @@ int launch_decode_tc(const DecodeArgs& a, int num_sms, cudaStream_t st) {
   p.slab = (D.d + num_sms - 1) / num_sms;
   if (p.slab < 8) p.slab = 8;
   p.n_slab = (D.d + p.slab - 1) / p.slab;
-  p.groups = D.E < CT ? CT / D.E : 1;
   p.header = reinterpret_cast<uint32_t*>(a.ws);
   p.flags = p.header + 256;
   p.part = reinterpret_cast<float*>(a.ws + a.L.part);
   p.score_part = reinterpret_cast<float*>(a.ws + a.L.score_part);
+  p.chosen = reinterpret_cast<uint64_t*>(a.ws + kOpFlags);
   p.hbuf = reinterpret_cast<__nv_bfloat16*>(a.ws + a.L.h);
   p.hsbuf = reinterpret_cast<__nv_bfloat16*>(a.ws + a.L.hs);
   const int64_t slots = decode_slots(D);

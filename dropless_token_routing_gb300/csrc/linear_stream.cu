@@ -1,6 +1,12 @@
 // The linear layer's serving form: y = act(x W^T + b) + r for few rows, bf16, as one stream of W
 // (stream.cuh). The result leaves the tensor memory transposed (lanes are outputs), so that each
-// token's 128 outputs of a tile are contiguous.
+// token's outputs of a tile are contiguous.
+//
+// W's rows are divided evenly: a cluster of 1, 2, 4 or 8 CTAs takes tiles of R <= 128 rows, R such
+// that all clusters have the same number of tiles, and its CTAs each a share of K. They join their
+// sums through distributed shared memory, each CTA finishing a share of the token columns: a
+// join through global memory costs fences, flags and loads of about 2 us each behind the stream.
+// The host picks the cluster size that gives a CTA the fewest bytes to load (weights and tokens).
 #include <string.h>
 
 #include <mutex>
@@ -16,166 +22,270 @@ using namespace stream;
 
 struct LinearStream {
   CUtensorMap w, x;
-  int M, N, nkb, tiles;
+  int M, N, nkb, tiles, rows;   // rows of W in a tile
+  int act;
   const __nv_bfloat16 *bias, *res;
   __nv_bfloat16 *z, *y;
   int64_t ld_res, ld_y;
-  bool vec;             // rows of y, res and z hold whole 16-byte vectors
-  uint32_t* header;
-  float* part;          // [CTA][NT][128]
+  bool vec;             // rows of y, res and z hold whole 16-byte vectors, and so do tiles
+  int* err;
 };
 
-template <int ACT> struct Finish {
-  const LinearStream& g;
-  __device__ void prepare(int64_t) {}
-  // 8 outputs of one token per thread and step
-  __device__ void finish(int64_t tile, int c0, const float* acc) {
-    const int n0 = (int)tile * BM, tid = threadIdx.x - 64;
-    const int q = (tid & 15) * 8, n = n0 + q;
-    if (n >= g.N) return;
-    const int cols = min(8, g.N - n);
-    float b[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) b[i] = g.bias != nullptr && i < cols ? __bfloat162float(g.bias[n + i]) : 0.f;
-    for (int c = tid >> 4; c < 64 && c0 + c < g.M; c += 16) {
-      const int64_t m = c0 + c;
-      float v[8], r[8];
-      *reinterpret_cast<float4*>(v) = *reinterpret_cast<const float4*>(acc + c * PITCH + q);
-      *reinterpret_cast<float4*>(v + 4) = *reinterpret_cast<const float4*>(acc + c * PITCH + q + 4);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        v[i] += b[i];
-        r[i] = 0.f;
-      }
-      Vec8<__nv_bfloat16> p;
-      if (g.vec) {
-        if (g.res != nullptr) {
-          p.v = *reinterpret_cast<const uint4*>(g.res + m * g.ld_res + n);   // may be y's own buffer
-          p.to_float(r);
-        }
-        if (g.z != nullptr) {
-          p.from_float(v);
-          p.store(g.z + m * g.N + n);
-        }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = act_f<ACT>(v[i]) + r[i];
-        p.from_float(v);
-        p.store(g.y + m * g.ld_y + n);
-      } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          if (i >= cols) break;
-          const float res = g.res != nullptr ? __bfloat162float(g.res[m * g.ld_res + n + i]) : 0.f;
-          if (g.z != nullptr) g.z[m * g.N + n + i] = __float2bfloat16_rn(v[i]);
-          g.y[m * g.ld_y + n + i] = __float2bfloat16_rn(act_f<ACT>(v[i]) + res);
-        }
-      }
+__device__ __forceinline__ float4 peer_ld4(uint32_t a) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a) : "memory");
+  return v;
+}
+// One arrival on this barrier of every CTA of the cluster.
+__device__ __forceinline__ void arrive_all(uint64_t* bar, int cluster) {
+  for (int i = 0; i < cluster; ++i)
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(peer_addr(smem_u32(bar), i)) : "memory");
+}
+// The wait for the other CTAs' arrivals (their shared memory may be read, or written over, after).
+static __device__ __noinline__ bool peers_wait(uint64_t* bar, uint32_t parity, volatile int* abort, int* err) {
+  const uint64_t t0 = global_ns();
+  while (true) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    if (ok) return true;
+    if (*abort) return false;
+    if (global_ns() - t0 > kWaitLimitNs) {
+      record_error(err, MOE_ERR_DEVICE_TIMEOUT);
+      *abort = 1;
+      return false;
     }
   }
-};
+}
 
-template <int NT, int ACT>
+// 8 outputs (n .. n + 7, `cols` of them inside the tile) of token m.
+__device__ __forceinline__ void finish8(const LinearStream& g, float (&v)[8], const float (&b)[8], int64_t m, int n, int cols) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] += b[i];
+  if (g.vec) {
+    float r[8] = {};
+    Vec8<__nv_bfloat16> p;
+    if (g.res != nullptr) {
+      p.v = *reinterpret_cast<const uint4*>(g.res + m * g.ld_res + n);   // may be y's own buffer
+      p.to_float(r);
+    }
+    if (g.z != nullptr) {
+      p.from_float(v);
+      p.store(g.z + m * g.N + n);
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = act_any(g.act, v[i]) + r[i];
+    p.from_float(v);
+    p.store(g.y + m * g.ld_y + n);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (i >= cols) break;
+      const float res = g.res != nullptr ? __bfloat162float(g.res[m * g.ld_res + n + i]) : 0.f;
+      if (g.z != nullptr) g.z[m * g.N + n + i] = __float2bfloat16_rn(v[i]);
+      g.y[m * g.ld_y + n + i] = __float2bfloat16_rn(act_any(g.act, v[i]) + res);
+    }
+  }
+}
+
+template <int NT>
 __global__ void __launch_bounds__(THREADS, 1) linear_stream_kernel(const __grid_constant__ LinearStream g) {
-  constexpr int STAGES = Cfg<NT>::stages(0);
+  constexpr int STAGES = Cfg<NT>::stages(0), STAGE = Cfg<NT>::STAGE, CHUNK = Cfg<NT>::CHUNK;
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) Bars b;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t smem_base = smem_u32(smem);
-  float* acc = reinterpret_cast<float*>(smem + STAGES * Cfg<NT>::STAGE);
-  int* err = reinterpret_cast<int*>(g.header);
-  const int cta = (int)blockIdx.x, n_cta = (int)gridDim.x;
-  setup<NT, STAGES>(b, warp);
-  const uint32_t epoch = *reinterpret_cast<volatile uint32_t*>(g.header + 1) + 1;
-  Run run(g.tiles, g.nkb, cta, n_cta);
+  float* acc = reinterpret_cast<float*>(smem + STAGES * STAGE);
+  uint32_t cl, rank;
+  asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(cl));
+  rank = cluster_rank();
+  const int tile0 = (int)cluster_id(), step = (int)cluster_count();
+  const int k0 = (int)((int64_t)g.nkb * rank / cl), k1 = (int)((int64_t)g.nkb * (rank + 1) / cl);
+  setup<NT, STAGES>(b, warp, (int)cl);
+  if (cl > 1) cluster_sync_all();   // the peers' barriers are initialised before any arrival
 
   if (warp == 0) {
     if (lane == 0) {
       Ring<STAGES> ring;
       int64_t loaded = 0;
       bool ok = true;
-      while (ok && run.next()) {
-        const int n0 = (int)run.s.t * BM;
-        for (int kb = run.s.k0; kb < run.s.k1; ++kb) {
-          if (!mbar_wait_bounded(smem_u32(&b.empty[ring.stage]), ring.phase ^ 1u, &b.abort, err, kWaitLimitNs)) {
-            ok = false;
-            break;
-          }
-          const uint32_t a_s = smem_base + ring.stage * Cfg<NT>::STAGE, bar = smem_u32(&b.full[ring.stage]);
-          mbar_arrive_expect_tx(bar, Cfg<NT>::STAGE);
-          tma2d(a_s, &g.w, bar, kb * BK, n0);
+      const uint32_t bytes = (uint32_t)(g.rows + NT) * BK * 2;
+      for (int tile = tile0; ok && tile < g.tiles; tile += step) {
+        for (int kb = k0; kb < k1; ++kb) {
+          ok = bar_wait(&b.empty[ring.stage], ring.phase ^ 1u, &b.abort, g.err);
+          if (!ok) break;
+          const uint32_t a_s = smem_base + ring.stage * STAGE, bar = smem_u32(&b.full[ring.stage]);
+          mbar_arrive_expect_tx(bar, bytes);
+          tma2d(a_s, &g.w, bar, kb * BK, tile * g.rows);   // rows past the tile keep what was there
           tma2d(a_s + A_BYTES, &g.x, bar, kb * BK, 0);
           ring.step();
           ++loaded;
         }
       }
-      drain<STAGES>(b, ring, loaded, err);
+      drain<STAGES>(b, ring, loaded, g.err);
     }
     __syncwarp();
   } else if (warp == 1) {
     if (lane == 0) {
       Ring<STAGES> ring;
       int it = 0;
-      mma_run<NT, STAGES>(b, smem_base, run, ring, it, err);
+      for (int tile = tile0; tile < g.tiles; tile += step, ++it)
+        if (!mma_tile<NT, STAGES>(b, smem_base, k1 - k0, ring, it, g.err)) break;
       umma1_commit(smem_u32(&b.final));   // every MMA retired before the tensor memory is released
-      mbar_wait_bounded(smem_u32(&b.final), 0, nullptr, err, kWaitLimitNs);
+      bar_wait(&b.final, 0, nullptr, g.err);
     }
     __syncwarp();
   } else {
-    int it = 0;
-    Finish<ACT> f{g};
-    take_run<NT>(b, run, it, cta, g.header + 256, epoch, g.part, acc, err, f);
-  }
-  teardown<NT>(b, warp);
-  leave(g.header, epoch);
-}
-
-template <int NT, int ACT>
-int launch_nt(LinearStream& g, const GemmArgs& a, int num_sms, cudaStream_t st) {
-  constexpr int SMEM = Cfg<NT>::smem(0);
-  auto kernel = linear_stream_kernel<NT, ACT>;
-  static std::mutex mu;   // the shared-memory attribute is set once per device
-  static bool attr_set[kMaxDevices];
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return MOE_ERR_CUDA;
-  {
-    std::lock_guard<std::mutex> lk(mu);
-    if (!attr_set[dev]) {
-      if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM) != cudaSuccess) return MOE_ERR_CUDA;
-      attr_set[dev] = true;
+    constexpr int HALF = CHUNK / 2;
+    const int lg = warp & 3, row = lg * 32 + lane, col0 = ((warp - 2) >> 2) * HALF, tid = threadIdx.x - 64;
+    const int q = (tid & 15) * 8;   // this thread's 8 rows of W in a tile
+    // its share of a chunk's token columns
+    const int c_lo = CHUNK * (int)rank / (int)cl, c_hi = CHUNK * ((int)rank + 1) / (int)cl;
+    uint32_t parity = 0;
+    bool ok = true;
+    for (int tile = tile0, it = 0; ok && tile < g.tiles; tile += step, ++it) {
+      const int buf = it & 1, n = tile * g.rows + q;
+      const int cols = min(8, min(g.rows - q, g.N - n));
+      float bias[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) bias[i] = g.bias != nullptr && i < cols ? __bfloat162float(g.bias[n + i]) : 0.f;
+      ok = bar_wait(&b.tfull[buf], (it >> 1) & 1, &b.abort, g.err);
+      if (ct_any(!ok)) break;
+      __syncwarp();
+      tc_fence_after();
+      const uint32_t t_base = b.tmem + ((uint32_t)(lg * 32) << 16) + (uint32_t)(buf * NT);
+#pragma unroll 1
+      for (int c0 = 0; c0 < NT && c0 < g.M; c0 += CHUNK) {
+#pragma unroll
+        for (int c = 0; c < HALF; c += 8) {
+          uint32_t u[8];
+          tmem_ld8(t_base + c0 + col0 + c, u);
+          tmem_ld_wait();
+#pragma unroll
+          for (int i = 0; i < 8; ++i) acc[(col0 + c + i) * PITCH + row] = __uint_as_float(u[i]);
+        }
+        ct_sync();
+        if (cl > 1) {
+          if (tid == 0) arrive_all(&b.peers_ready, (int)cl);
+          ok = !ct_any(!peers_wait(&b.peers_ready, parity, &b.abort, g.err));
+          if (!ok) break;
+        }
+        for (int c = c_lo + (tid >> 4); c < c_hi && c0 + c < g.M; c += 16) {
+          float v[8] = {};
+          for (uint32_t r = 0; r < cl; ++r) {   // in the order of the ranks
+            const uint32_t at = peer_addr(smem_u32(acc + c * PITCH + q), r);
+            const float4 lo = peer_ld4(at), hi = peer_ld4(at + 16);
+            v[0] += lo.x; v[1] += lo.y; v[2] += lo.z; v[3] += lo.w;
+            v[4] += hi.x; v[5] += hi.y; v[6] += hi.z; v[7] += hi.w;
+          }
+          if (cols > 0) finish8(g, v, bias, c0 + c, n, cols);
+        }
+        ct_sync();
+        if (cl > 1) {   // the peers have read this CTA's sums before they are written over
+          if (tid == 0) arrive_all(&b.peers_done, (int)cl);
+          ok = !ct_any(!peers_wait(&b.peers_done, parity, &b.abort, g.err));
+          if (!ok) break;
+          parity ^= 1u;
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&b.tempty[buf]));
     }
   }
-  if (!map2d_ld(&g.w, a.b, a.K, a.N, a.bn, BK, BM) || !map2d_ld(&g.x, a.a, a.K, a.M, a.am, BK, NT)) return MOE_ERR_CUDA;
-  const int64_t units = (int64_t)g.tiles * g.nkb;
-  int ctas = num_sms < kMaxStreamCtas ? num_sms : kMaxStreamCtas;
-  if (units / kMinStreamRun < ctas) ctas = units < kMinStreamRun ? 1 : (int)(units / kMinStreamRun);
-  TraceScope ts(TP_LINEAR, st);
-  kernel<<<ctas, THREADS, SMEM, st>>>(g);
-  return cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_LAUNCH;
+  teardown<NT>(b, warp);
+  if (cl > 1) cluster_sync_all();   // no CTA leaves while a peer may still reach its shared memory
+}
+
+// Clusters of `c` CTAs that can be resident at once (c = 1: the SMs).
+template <int NT>
+int resident(int c, int num_sms) {
+  constexpr int SMEM = Cfg<NT>::smem(0);
+  auto kernel = linear_stream_kernel<NT>;
+  static std::mutex mu;   // per device, once: the shared-memory attribute and the counts
+  static int count[kMaxDevices][4];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return 0;
+  const int i = c == 1 ? 0 : c == 2 ? 1 : c == 4 ? 2 : 3;
+  std::lock_guard<std::mutex> lk(mu);
+  if (count[dev][0] == 0) {
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM) != cudaSuccess) return 0;
+    count[dev][0] = num_sms;
+  }
+  if (count[dev][i] == 0) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(num_sms / c * c));
+    cfg.blockDim = dim3(THREADS);
+    cfg.dynamicSmemBytes = SMEM;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = c;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n <= 0) return 0;
+    count[dev][i] = n;
+  }
+  return count[dev][i];
 }
 
 template <int NT>
-int launch_act(LinearStream& g, const GemmArgs& a, int num_sms, cudaStream_t st) {
-#define MOE_S(A) return launch_nt<NT, A>(g, a, num_sms, st)
-  MOE_ACT_SWITCH(a.act, MOE_S)
-#undef MOE_S
-  return MOE_OK;
+int launch_nt(LinearStream& g, const GemmArgs& a, int num_sms, cudaStream_t st) {
+  // The cluster size that leaves a CTA the least to load. A join costs about as much as kJoin bytes.
+  constexpr int64_t kJoin = 48 << 10;
+  int best = 0, best_rows = 0, best_tiles = 0, best_clusters = 0;
+  int64_t best_cost = 0;
+  for (int c = 1; c <= 8; c *= 2) {
+    if (c > 1 && g.nkb / c < 4) break;
+    const int ncl = resident<NT>(c, num_sms);
+    if (ncl == 0) return MOE_ERR_CUDA;
+    const int per = (g.N + ncl * BM - 1) / (ncl * BM);           // tiles of a cluster
+    int rows = (g.N + ncl * per - 1) / (ncl * per);
+    rows = (rows + 7) & ~7;                                      // whole vectors of outputs
+    const int tiles = (g.N + rows - 1) / rows;
+    const int64_t cost = (int64_t)per * ((g.nkb + c - 1) / c * (int64_t)(rows + NT) * BK * 2 + (c > 1 ? kJoin : 0));
+    if (best == 0 || cost < best_cost) {
+      best = c;
+      best_cost = cost;
+      best_rows = rows;
+      best_tiles = tiles;
+      best_clusters = ncl < tiles ? ncl : tiles;
+    }
+  }
+  g.rows = best_rows;
+  g.tiles = best_tiles;
+  if (!map2d_ld(&g.w, a.b, a.K, a.N, a.bn, BK, best_rows) || !map2d_ld(&g.x, a.a, a.K, a.M, a.am, BK, NT)) return MOE_ERR_CUDA;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(best_clusters * best));
+  cfg.blockDim = dim3(THREADS);
+  cfg.dynamicSmemBytes = Cfg<NT>::smem(0);
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = best;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  TraceScope ts(TP_LINEAR, st);
+  return cudaLaunchKernelEx(&cfg, linear_stream_kernel<NT>, g) == cudaSuccess ? MOE_OK : MOE_ERR_LAUNCH;
 }
 
 }  // namespace
 
-size_t linear_stream_part_bytes(int64_t M) {
-  const int nt = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : M <= 128 ? 128 : 256;
-  return (size_t)kMaxStreamCtas * nt * BM * 4;
-}
-
-int launch_linear_stream(const GemmArgs& a, uint8_t* ws, size_t part, int num_sms, cudaStream_t st) {
+int launch_linear_stream(const GemmArgs& a, uint8_t* ws, int num_sms, cudaStream_t st) {
   LinearStream g;
   memset(&g, 0, sizeof(g));
   g.M = (int)a.M;
   g.N = a.N;
   g.nkb = (int)((a.K + BK - 1) / BK);
-  g.tiles = (a.N + BM - 1) / BM;
+  g.act = a.act;
   g.bias = static_cast<const __nv_bfloat16*>(a.bias);
   g.res = static_cast<const __nv_bfloat16*>(a.res);
   g.z = static_cast<__nv_bfloat16*>(a.z_out);
@@ -183,13 +293,12 @@ int launch_linear_stream(const GemmArgs& a, uint8_t* ws, size_t part, int num_sm
   g.ld_res = a.ld_res;
   g.ld_y = a.ldc;
   g.vec = a.N % 8 == 0 && a.ldc % 8 == 0 && (a.res == nullptr || a.ld_res % 8 == 0);
-  g.header = reinterpret_cast<uint32_t*>(ws);
-  g.part = reinterpret_cast<float*>(ws + part);
-  if (a.M <= 16) return launch_act<16>(g, a, num_sms, st);
-  if (a.M <= 32) return launch_act<32>(g, a, num_sms, st);
-  if (a.M <= 64) return launch_act<64>(g, a, num_sms, st);
-  if (a.M <= 128) return launch_act<128>(g, a, num_sms, st);
-  return launch_act<256>(g, a, num_sms, st);
+  g.err = reinterpret_cast<int*>(ws);
+  if (a.M <= 16) return launch_nt<16>(g, a, num_sms, st);
+  if (a.M <= 32) return launch_nt<32>(g, a, num_sms, st);
+  if (a.M <= 64) return launch_nt<64>(g, a, num_sms, st);
+  if (a.M <= 128) return launch_nt<128>(g, a, num_sms, st);
+  return launch_nt<256>(g, a, num_sms, st);
 }
 
 }  // namespace moe

@@ -5,8 +5,10 @@
 
 namespace moe {
 
-constexpr size_t kOpHeader = 8192;    // error word, launch counters, and from byte 1024 flags
+constexpr size_t kOpFlags = 8192;     // error word, launch counters, and from byte 1024 flags
+constexpr size_t kOpHeader = kOpFlags + 8 * 64 * kMaxK;   // and the selections of 64 tokens
 constexpr int kDecodeMaxT = 64;       // tokens of moe_layer_decode
+static_assert(kOpHeader == kOpFlags + 8 * kDecodeMaxT * kMaxK, "");
 
 inline size_t round256(size_t x) { return (x + 255) & ~size_t(255); }
 
@@ -14,15 +16,16 @@ constexpr int kMaxStreamCtas = 160;   // CTAs of a weight stream
 constexpr int kMinStreamRun = 2;      // K blocks of a CTA's run
 
 // ------------------------------------------------------------------ decode
+constexpr int kDecodeRuns = 3;   // shared, hidden, output
 struct DecodeLayout {
+  // fp32 layers
   size_t idx;        // [T][k] int32
   size_t gate;       // [T][k] fp32
-  // fp32 layers
   size_t logits;     // [T][E] fp32
   size_t counts;     // [E] int32
   // bf16 layers
-  size_t score_part; // [T][slabs * groups][E] fp32 partial scores
-  size_t part;       // [3][CTA][token columns][128] fp32 partial tiles
+  size_t score_part; // [T][slabs][E] fp32 partial scores
+  size_t part;       // [kDecodeRuns][CTA][token columns][128] fp32 partial tiles
   // hidden rows times their gates: fp32 [T*k][f] and [S*T][f_s]; bf16 [slot][token columns][f]
   // and [S][token columns][f_s]
   size_t h, hs;
@@ -88,8 +91,7 @@ size_t linear_pair_part_bytes();
 int launch_linear_pair(int kind, const GemmArgs& a, uint8_t* ws, size_t part, int num_sms, cudaStream_t st);
 // The forward product for at most kStreamRows rows, as a stream of the weights.
 constexpr int kStreamRows = 256;
-size_t linear_stream_part_bytes(int64_t M);
-int launch_linear_stream(const GemmArgs& a, uint8_t* ws, size_t part, int num_sms, cudaStream_t st);
+int launch_linear_stream(const GemmArgs& a, uint8_t* ws, int num_sms, cudaStream_t st);
 // dz = dy * act'(z) (dz may be NULL: sums only) and db (may be NULL)
 cudaError_t launch_linear_dz(const void* dy, int64_t ld_dy, const void* z, int act, int64_t M, int N,
                              int dtype, void* dz, int64_t ld_dz, float* db_part, void* db, cudaStream_t st);

@@ -16,14 +16,12 @@ DecodeLayout decode_layout(const moe_dims& d) {
   const size_t T = (size_t)d.T, E = (size_t)d.E;
   const bool tc = d.dtype == MOE_BF16;
   const size_t nt = tc ? decode_token_columns(d.T) : 0;
-  L.idx = take(4 * T * d.k);
-  L.gate = take(4 * T * d.k);
+  L.idx = take(tc ? 0 : 4 * T * d.k);
+  L.gate = take(tc ? 0 : 4 * T * d.k);
   L.logits = take(tc ? 0 : 4 * T * E);
   L.counts = take(tc ? 0 : 4 * E);
-  // a CTA's share of the scores: one row per group of threads, at most 256 values per token
-  // (E with more experts)
-  L.score_part = take(tc ? 4 * T * kMaxStreamCtas * (E < 256 ? 256 : E) : 0);
-  L.part = take(tc ? 4 * 3 * kMaxStreamCtas * nt * 128 : 0);
+  L.score_part = take(tc ? 4 * T * kMaxStreamCtas * E : 0);
+  L.part = take(tc ? 4 * (size_t)kDecodeRuns * kMaxStreamCtas * nt * 128 : 0);
   L.h = take(tc ? 2 * (size_t)decode_slots(d) * nt * d.f : 4 * T * d.k * d.f);
   L.hs = take(tc ? 2 * (size_t)d.S * nt * d.f_s : 4 * T * d.S * d.f_s);
   L.total = o;
@@ -36,12 +34,7 @@ LinearLayout linear_layout(const moe_linear_dims& d) {
   L.dz = kOpHeader;
   L.db_part = L.dz + round256((size_t)d.M * L.ld_dz * elt_bytes(d.dtype));
   L.part = L.db_part + round256(4 * (size_t)kDbSplit * d.N);
-  size_t part = 0;
-  if (d.dtype == MOE_BF16) {
-    const size_t a = linear_pair_part_bytes(), b = linear_stream_part_bytes(d.M);
-    part = a > b ? a : b;
-  }
-  L.total = L.part + part;
+  L.total = L.part + (d.dtype == MOE_BF16 ? linear_pair_part_bytes() : 0);
   return L;
 }
 
@@ -100,7 +93,7 @@ int resolve_linear(const moe_linear_dims* in, moe_linear_dims* d) {
 int run_gemm(int kind, const GemmArgs& g, uint8_t* ws, const LinearLayout& L, int sms, cudaStream_t st) {
   const int64_t lda = g.ak == 1 ? g.am : g.ak, ldb = g.bk == 1 ? g.bn : g.bk;
   if (g.dtype == MOE_BF16 && lda % 8 == 0 && ldb % 8 == 0) {
-    if (kind == LINEAR_FWD && g.M <= kStreamRows) return launch_linear_stream(g, ws, L.part, sms, st);
+    if (kind == LINEAR_FWD && g.M <= kStreamRows) return launch_linear_stream(g, ws, sms, st);
     return launch_linear_pair(kind, g, ws, L.part, sms, st);
   }
   return launch_gemm_simt(g, st) == cudaSuccess ? MOE_OK : MOE_ERR_LAUNCH;

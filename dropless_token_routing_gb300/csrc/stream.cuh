@@ -1,5 +1,6 @@
 // Products of a weight stream with a few token rows (sm_103a): the pieces that the few-token
-// layer (decode_tc.cu) and the linear layer's serving form (linear_stream.cu) share.
+// layer (decode_tc.cu) and the linear layer's serving form (linear_stream.cu) share. Runs and their
+// joins through the workspace are the layer's; the linear layer joins inside a cluster.
 //
 // With few tokens a product is a stream of weights out of HBM, and everything here serves that
 // stream. The weights are the MMA's A operand, 128 weight rows by 64 of K per stage; the tokens
@@ -48,16 +49,11 @@ template <int NT> struct Cfg {
 };
 
 struct Bars {
-  uint64_t full[MAX_STAGES], empty[MAX_STAGES], tfull[2], tempty[2], final, list;
+  uint64_t full[MAX_STAGES], empty[MAX_STAGES], tfull[2], tempty[2], final, list, slab_free, peers_ready, peers_done;
   uint32_t tmem;
   volatile int abort;
 };
 
-__device__ __forceinline__ uint32_t ld_acquire(const uint32_t* p) {
-  uint32_t v;
-  asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
-  return v;
-}
 __device__ __forceinline__ void st_release(uint32_t* p, uint32_t v) {
   asm volatile("st.release.gpu.global.u32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
 }
@@ -65,15 +61,26 @@ __device__ __forceinline__ void add_release(uint32_t* p, uint32_t v) {
   asm volatile("red.release.gpu.global.add.u32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
 }
 
-// One thread waits until the word holds `value` (equal) or at least `value` (!equal).
-__device__ __forceinline__ bool word_wait(const uint32_t* p, uint32_t value, bool equal, volatile int* abort, int* err) {
-  auto there = [&]() {
-    const uint32_t v = ld_acquire(p);
-    return equal ? v == value : v >= value;
-  };
-  if (there()) return true;
+// The slow sides of the waits are calls: the kernels' cold code stays short (an instruction line
+// that is not cached costs about 0.4 us while the stream saturates the L2).
+static __device__ __noinline__ bool bar_wait_slow(uint32_t bar, uint32_t parity, volatile int* abort, int* err) {
+  return mbar_wait_bounded(bar, parity, abort, err, kWaitLimitNs);
+}
+__device__ __forceinline__ bool bar_wait(uint64_t* bar, uint32_t parity, volatile int* abort, int* err) {
+  return mbar_try_wait(smem_u32(bar), parity) || bar_wait_slow(smem_u32(bar), parity, abort, err);
+}
+
+__device__ __forceinline__ uint32_t ld_relaxed(const uint32_t* p) {
+  uint32_t v;
+  asm volatile("ld.relaxed.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+  return v;
+}
+__device__ __forceinline__ void fence_acquire() { asm volatile("fence.acq_rel.gpu;" ::: "memory"); }
+
+// One thread waits until the word holds at least `value`.
+static __device__ __noinline__ bool word_wait(const uint32_t* p, uint32_t value, volatile int* abort, int* err) {
   const uint64_t t0 = global_ns();
-  while (!there()) {
+  while (ld_relaxed(p) < value) {
     if (*abort) return false;
     if (global_ns() - t0 > kWaitLimitNs) {
       record_error(err, MOE_ERR_DEVICE_TIMEOUT);
@@ -81,6 +88,26 @@ __device__ __forceinline__ bool word_wait(const uint32_t* p, uint32_t value, boo
       return false;
     }
   }
+  fence_acquire();
+  return true;
+}
+
+// A warp waits until every lane's flag holds `value`; lanes without one pass nullptr. All flags are
+// polled at once: behind a saturated L2 a poll takes about 2 us.
+static __device__ __noinline__ bool flags_wait(const uint32_t* p, uint32_t value, volatile int* abort, int* err) {
+  const uint64_t t0 = global_ns();
+  while (true) {
+    bool there = true;
+    if (p != nullptr) there = ld_relaxed(p) == value;
+    if (__all_sync(0xffffffffu, there)) break;
+    if (__any_sync(0xffffffffu, *abort != 0)) return false;
+    if (__any_sync(0xffffffffu, global_ns() - t0 > kWaitLimitNs)) {
+      record_error(err, MOE_ERR_DEVICE_TIMEOUT);
+      *abort = 1;
+      return false;
+    }
+  }
+  fence_acquire();
   return true;
 }
 
@@ -130,8 +157,9 @@ struct Run {
     nkb = nkb_;
     units = tiles * nkb;
     n = (int)min((int64_t)n_cta, max((int64_t)1, units / kMinStreamRun));
-    u0 = c < n ? units * c / n : 0;
-    u = c < n ? units * (c + 1) / n : 0;
+    const bool in = c >= 0 && c < n;
+    u0 = in ? units * c / n : 0;
+    u = in ? units * (c + 1) / n : 0;
   }
   __device__ bool next() {
     if (u <= u0) return false;
@@ -165,7 +193,7 @@ template <int STAGES> struct Ring {
 
 // Set-up by all threads: barriers, tensor memory. Ends with __syncthreads.
 template <int NT, int STAGES>
-__device__ __forceinline__ void setup(Bars& b, int warp) {
+__device__ __forceinline__ void setup(Bars& b, int warp, int cluster = 1) {
   if (threadIdx.x == 0) {
     b.abort = 0;
     for (int s = 0; s < STAGES; ++s) {
@@ -178,6 +206,9 @@ __device__ __forceinline__ void setup(Bars& b, int warp) {
     }
     mbar_init(smem_u32(&b.final), 1);
     mbar_init(smem_u32(&b.list), 1);
+    mbar_init(smem_u32(&b.slab_free), 1);
+    mbar_init(smem_u32(&b.peers_ready), cluster);
+    mbar_init(smem_u32(&b.peers_done), cluster);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   }
@@ -211,32 +242,37 @@ template <int STAGES> __device__ __forceinline__ void drain(Bars& b, const Ring<
       q.phase ^= 1u;
     }
     --q.stage;
-    mbar_wait_bounded(smem_u32(&b.full[q.stage]), q.phase, nullptr, err, kWaitLimitNs);
+    bar_wait(&b.full[q.stage], q.phase, nullptr, err);
   }
 }
 
-// The MMA thread's part of a run; `it` counts the segments of the launch.
+// The MMAs of `blocks` K blocks into accumulator it & 1 (`it` counts the tiles of the launch).
+template <int NT, int STAGES>
+__device__ __forceinline__ bool mma_tile(Bars& b, uint32_t smem_base, int blocks, Ring<STAGES>& ring, int it, int* err) {
+  constexpr uint32_t idesc = idesc_bf16(BM, NT, false, false);
+  const int buf = it & 1;
+  if (!bar_wait(&b.tempty[buf], ((it >> 1) & 1) ^ 1, &b.abort, err)) return false;
+  tc_fence_after();
+  const uint32_t d_tmem = b.tmem + (uint32_t)(buf * NT);
+  for (int kb = 0; kb < blocks; ++kb) {
+    if (!bar_wait(&b.full[ring.stage], ring.phase, &b.abort, err)) return false;
+    tc_fence_after();
+    const uint32_t a_s = smem_base + ring.stage * Cfg<NT>::STAGE, b_s = a_s + A_BYTES;
+#pragma unroll
+    for (int kk = 0; kk < BK / 16; ++kk)
+      umma1(d_tmem, sdesc(a_s + kk * 32, 16, 1024), sdesc(b_s + kk * 32, 16, 1024), idesc, (kb | kk) != 0 ? 1u : 0u);
+    umma1_commit(smem_u32(&b.empty[ring.stage]));
+    ring.step();
+  }
+  umma1_commit(smem_u32(&b.tfull[buf]));
+  return true;
+}
+
+// The MMA thread's part of a run.
 template <int NT, int STAGES>
 __device__ __forceinline__ bool mma_run(Bars& b, uint32_t smem_base, Run run, Ring<STAGES>& ring, int& it, int* err) {
-  constexpr uint32_t idesc = idesc_bf16(BM, NT, false, false);
-  for (; run.next(); ++it) {
-    const int buf = it & 1;
-    if (!mbar_wait_bounded(smem_u32(&b.tempty[buf]), ((it >> 1) & 1) ^ 1, &b.abort, err, kWaitLimitNs)) return false;
-    tc_fence_after();
-    const uint32_t d_tmem = b.tmem + (uint32_t)(buf * NT);
-    for (int kb = run.s.k0; kb < run.s.k1; ++kb) {
-      if (!mbar_wait_bounded(smem_u32(&b.full[ring.stage]), ring.phase, &b.abort, err, kWaitLimitNs)) return false;
-      tc_fence_after();
-      const uint32_t a_s = smem_base + ring.stage * Cfg<NT>::STAGE, b_s = a_s + A_BYTES;
-#pragma unroll
-      for (int kk = 0; kk < BK / 16; ++kk)
-        umma1(d_tmem, sdesc(a_s + kk * 32, 16, 1024), sdesc(b_s + kk * 32, 16, 1024), idesc,
-              (kb != run.s.k0 || kk != 0) ? 1u : 0u);
-      umma1_commit(smem_u32(&b.empty[ring.stage]));
-      ring.step();
-    }
-    umma1_commit(smem_u32(&b.tfull[buf]));
-  }
+  for (; run.next(); ++it)
+    if (!mma_tile<NT, STAGES>(b, smem_base, run.s.k1 - run.s.k0, ring, it, err)) return false;
   return true;
 }
 
@@ -252,12 +288,14 @@ __device__ __forceinline__ bool take_run(Bars& b, Run run, int& it, int cta, uin
   for (; run.next(); ++it) {
     const int buf = it & 1;
     const bool owner = run.s.k1 == run.nkb;
-    bool ok = mbar_wait_bounded(smem_u32(&b.tfull[buf]), (it >> 1) & 1, &b.abort, err, kWaitLimitNs);
+    bool ok = bar_wait(&b.tfull[buf], (it >> 1) & 1, &b.abort, err);
     const int q0 = owner && run.s.k0 > 0 ? run.first_cta() : cta;
-    if (ok && lane == 0)
-      for (int q = q0; ok && q < cta; ++q) ok = word_wait(flags + q, epoch, true, &b.abort, err);
+    ok = __all_sync(0xffffffffu, ok);
+    if (owner)   // the flags of the tile's other CTAs
+      for (int q = q0; ok && q < cta; q += 32) ok = flags_wait(q + lane < cta ? flags + q + lane : nullptr, epoch, &b.abort, err);
     if (owner) f.prepare(run.s.t);
     if (ct_any(!ok)) return false;
+    __syncwarp();   // the TMEM loads are for whole warps
     tc_fence_after();
     const uint32_t t_base = b.tmem + ((uint32_t)(lg * 32) << 16) + (uint32_t)(buf * NT);
 #pragma unroll 1
@@ -272,10 +310,18 @@ __device__ __forceinline__ bool take_run(Bars& b, Run run, int& it, int cta, uin
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(u[i]);
         if (owner) {
-          for (int q = q0; q < cta; ++q) {
+#pragma unroll 1
+          for (int q = q0; q < cta; q += 4) {   // four CTAs' parts in flight, added in order
             const float* in = part + ((int64_t)q * NT + col) * BM + row;
+            float w[4][8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] += __ldcg(in + i * BM);
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+              for (int i = 0; i < 8; ++i) w[j][i] = q + j < cta ? __ldcg(in + (j * NT + i) * BM) : 0.f;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+              for (int i = 0; i < 8; ++i) v[i] += w[j][i];
           }
 #pragma unroll
           for (int i = 0; i < 8; ++i) acc[(col0 + c + i) * PITCH + row] = v[i];
@@ -305,15 +351,15 @@ __device__ __forceinline__ bool take_run(Bars& b, Run run, int& it, int cta, uin
   return true;
 }
 
-// The last CTA of the launch to leave zeroes the counters and makes the flags stale.
-__device__ __forceinline__ void leave(uint32_t* header, uint32_t epoch) {
-  if (threadIdx.x == 0) {
-    __threadfence();
-    if (atomicAdd(header + 2, 1u) == gridDim.x - 1) {
-      for (int i = 2; i < 8; ++i) header[i] = 0;
-      header[1] = epoch;
-    }
-  }
+// The last CTA of the launch to leave zeroes the counters and makes the flags stale; true in its
+// thread 0.
+__device__ __forceinline__ bool leave(uint32_t* header, uint32_t epoch) {
+  if (threadIdx.x != 0) return false;
+  __threadfence();
+  if (atomicAdd(header + 2, 1u) != gridDim.x - 1) return false;
+  for (int i = 2; i < 8; ++i) header[i] = 0;
+  header[1] = epoch;
+  return true;
 }
 
 }  // namespace stream

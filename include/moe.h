@@ -349,7 +349,7 @@ int moe_layer_bwd(const moe_layer_params* params, const moe_layer_saved* saved, 
 /* Zero the header (error word, launch counters and flags) of a workspace of the calls below
  * (async). Once after allocating it; the calls leave the counters zeroed themselves. A workspace
  * belongs to one call at a time: calls that share one have to be ordered on one stream.
- * moe_get_device_error reads its error word. ws: 256-byte aligned, ws_bytes >= 8192. */
+ * moe_get_device_error reads its error word. ws: 256-byte aligned, ws_bytes >= 24576. */
 int moe_op_workspace_init(void* ws, size_t ws_bytes, moe_stream_t stream);
 
 /* The whole layer for 0 <= dims->T <= 64 tokens (router, top-k, selected experts, shared experts,

@@ -496,19 +496,20 @@ __global__ void __launch_bounds__(THREADS, 1) decode_kernel(const __grid_constan
     __syncwarp();
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA
-    if (lane == 0) {
-      Ring<STAGES> ring;
-      int it = 0;
-      bool ok = true;
+    Ring<STAGES> ring;
+    int it = 0;
+    bool ok = true;
+    const bool one = elect_one();
 #pragma unroll 1
-      for (int r = D.S > 0 ? SHARED : HIDDEN; ok && r <= OUTPUT; ++r) {
-        if (r == HIDDEN) {
-          ok = bar_wait(&b.list, 0, &b.abort, err);
-          if (!ok) break;
-          plan.select(s_active);
-        }
-        ok = mma_run<NT, STAGES>(b, smem_base, plan.run(r), ring, it, err);
+    for (int r = D.S > 0 ? SHARED : HIDDEN; ok && r <= OUTPUT; ++r) {
+      if (r == HIDDEN) {
+        ok = warp_bar_wait(smem_u32(&b.list), 0, &b.abort, err);
+        if (!ok) break;
+        plan.select(s_active);
       }
+      ok = mma_run<NT, STAGES>(b, smem_base, plan.run(r), ring, it, one, err);
+    }
+    if (one) {
       umma1_commit(smem_u32(&b.final));   // every MMA retired before the tensor memory is released
       bar_wait(&b.final, 0, nullptr, err);
     }

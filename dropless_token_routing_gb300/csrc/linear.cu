@@ -71,51 +71,105 @@ void gemm_simt(const GemmArgs& g, cudaStream_t st) {
   else gemm_simt_kernel<T, ACT, false, false><<<grid, 256, 0, st>>>(g);
 }
 
-// dz = dy * act'(z) for 64 columns and a share of the rows, and the shares' column sums: block
-// (x, y) takes columns 64 x .. and the rows congruent to y in blocks of 4.
-template <typename T, int ACT>
+// dz = dy * act'(z), and its column sums. A block takes 256 columns and every gridDim.y-th group of
+// 8 rows: 8 columns per lane, a row per warp. Its warps' sums are added in order into one row of
+// `part` per block. (8-element vectors where the rows allow, else element by element.)
+template <typename T, int ACT, bool VEC>
 __global__ void __launch_bounds__(256) linear_dz_kernel(const T* __restrict__ dy, int64_t ld_dy,
                                                         const T* __restrict__ z, int64_t M, int N,
                                                         T* __restrict__ dz, int64_t ld_dz,
                                                         float* __restrict__ part) {
-  __shared__ float s[4][64];
-  const int col = threadIdx.x & 63, r = threadIdx.x >> 6;
-  const int n = blockIdx.x * 64 + col;
-  float sum = 0.f;
-  if (n < N) {
-    for (int64_t m = blockIdx.y * 4 + r; m < M; m += (int64_t)gridDim.y * 4) {
-      float v = to_f32(dy[m * ld_dy + n]);
-      if constexpr (ACT != MOE_ACT_NONE) v *= act_slope<ACT>(to_f32(z[m * N + n]));
-      if (dz != nullptr) dz[m * ld_dz + n] = from_f32<T>(v);
-      sum += v;
+  __shared__ float s[8][256 + 8];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int n = blockIdx.x * 256 + lane * 8, cols = min(8, N - n);
+  float sum[8] = {};
+  auto load = [&](const T* p, float (&v)[8]) {
+    if (VEC) {
+      Vec8<T> u;
+      u.load(p);
+      u.to_float(v);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = i < cols ? to_f32(p[i]) : 0.f;
+    }
+  };
+  if (cols > 0) {
+#pragma unroll 4
+    for (int64_t m = (int64_t)blockIdx.y * 8 + warp; m < M; m += (int64_t)gridDim.y * 8) {
+      float v[8], zv[8];
+      load(dy + m * ld_dy + n, v);
+      if constexpr (ACT != MOE_ACT_NONE) {
+        load(z + m * N + n, zv);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] *= sizeof(T) == 2 ? act_slope_fast<ACT>(zv[i]) : act_slope<ACT>(zv[i]);
+      }
+      if (dz != nullptr) {
+        T* out = dz + m * ld_dz + n;
+        if (VEC) {
+          Vec8<T> u;
+          u.from_float(v);
+          u.store(out);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (i < cols) out[i] = from_f32<T>(v[i]);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sum[i] += v[i];
     }
   }
-  s[r][col] = sum;
+  if (part == nullptr) return;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) s[warp][lane * 8 + i] = sum[i];
   __syncthreads();
-  if (r == 0 && n < N && part != nullptr)
-    part[(int64_t)blockIdx.y * N + n] = (s[0][col] + s[1][col]) + (s[2][col] + s[3][col]);
+  const int c = blockIdx.x * 256 + threadIdx.x;
+  if (c < N) {
+    float t = 0.f;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) t += s[w][threadIdx.x];
+    part[(int64_t)blockIdx.y * N + c] = t;
+  }
 }
 
+// db = the sum of n_part rows: 32 columns per block, 8 threads each, added in order.
 template <typename T>
-__global__ void linear_db_kernel(const float* __restrict__ part, int n_part, int N, T* __restrict__ db) {
-  const int n = blockIdx.x * blockDim.x + threadIdx.x;
-  if (n >= N) return;
-  float s = 0.f;
-  for (int i = 0; i < n_part; ++i) s += part[(int64_t)i * N + n];
-  db[n] = from_f32<T>(s);
+__global__ void __launch_bounds__(256) linear_db_kernel(const float* __restrict__ part, int n_part, int N, T* __restrict__ db) {
+  __shared__ float s[8][33];
+  const int col = threadIdx.x & 31, r = threadIdx.x >> 5, n = blockIdx.x * 32 + col;
+  float t = 0.f;
+  if (n < N) {
+#pragma unroll 8
+    for (int i = r; i < n_part; i += 8) t += part[(int64_t)i * N + n];
+  }
+  s[r][col] = t;
+  __syncthreads();
+  if (r == 0 && n < N) {
+#pragma unroll
+    for (int i = 1; i < 8; ++i) t += s[i][col];
+    db[n] = from_f32<T>(t);
+  }
 }
 
 template <typename T>
 cudaError_t linear_dz(const void* dy, int64_t ld_dy, const void* z, int act, int64_t M, int N, void* dz,
                       int64_t ld_dz, float* part, void* db, cudaStream_t st) {
-  const int split = (int)(M < 4 * kDbSplit ? (M + 3) / 4 : kDbSplit);
-  const dim3 grid((N + 63) / 64, split);
-#define MOE_DZ(A)                                                                                       \
-  linear_dz_kernel<T, A><<<grid, 256, 0, st>>>(static_cast<const T*>(dy), ld_dy, static_cast<const T*>(z), M, N, \
-                                               static_cast<T*>(dz), ld_dz, db != nullptr ? part : nullptr)
+  // about 1200 blocks (8 on an SM), of at least 32 rows
+  const int nx = (N + 255) / 256;
+  int64_t split = (1216 + nx - 1) / nx;
+  if (split > (M + 31) / 32) split = (M + 31) / 32;
+  if (split > kDbSplit) split = kDbSplit;
+  const dim3 grid(nx, (unsigned)split);
+  const bool vec = N % 8 == 0 && ld_dy % 8 == 0;   // ld_dz is a multiple of 8
+  const T *dyp = static_cast<const T*>(dy), *zp = static_cast<const T*>(z);
+  T* dzp = static_cast<T*>(dz);
+  float* pp = db != nullptr ? part : nullptr;
+#define MOE_DZ(A)                                                                                   \
+  if (vec) linear_dz_kernel<T, A, true><<<grid, 256, 0, st>>>(dyp, ld_dy, zp, M, N, dzp, ld_dz, pp); \
+  else linear_dz_kernel<T, A, false><<<grid, 256, 0, st>>>(dyp, ld_dy, zp, M, N, dzp, ld_dz, pp)
   MOE_ACT_SWITCH(act, MOE_DZ)
 #undef MOE_DZ
-  if (db != nullptr) linear_db_kernel<T><<<(N + 255) / 256, 256, 0, st>>>(part, split, N, static_cast<T*>(db));
+  if (db != nullptr) linear_db_kernel<T><<<(N + 31) / 32, 256, 0, st>>>(part, (int)split, N, static_cast<T*>(db));
   return cudaGetLastError();
 }
 

@@ -3,21 +3,22 @@
 //   dX       dx = dz W                  A = dz (K-major),  B = W (MN-major: W's rows run along Ko)
 //   dW       dw = dz^T x                A = dz (MN-major), B = x (MN-major)
 //
-// The two CTAs of a cluster compute one 256 x 256 tile with tcgen05.mma.cta_group::2: each
-// stages its own 128 rows of A and 128 columns of B per 64-deep K block (32 KB, six stages) and
-// holds its 128 x 256 fp32 half of the tile in tensor memory, two tiles deep. Both CTAs' loads
+// The two CTAs of a cluster compute one 256 x TN tile (TN <= 256, chosen by the host for
+// the shape) with tcgen05.mma.cta_group::2: each stages its own 128 rows of A and TN / 2 columns of
+// B per 64-deep K block (up to 32 KB, six stages) and holds its 128 x TN fp32 half of the tile in
+// tensor memory, two tiles deep. Both CTAs' loads
 // complete on the even CTA's full_bar, whose warp 1 issues the MMAs.
 //   warp 0     TMA producer of this CTA's halves
-//   warp 1     TMEM owner; in the even CTA one thread issues the MMAs
-//   warps 2..9 epilogue: two warps per TMEM lane quarter, 128 columns each
+//   warp 1     TMEM owner; in the even CTA it issues the MMAs
+//   warps 2..9 epilogue: two warps per TMEM lane quarter, half of the columns each
 // Ragged edges need no code in the main loop: the TMA fills what lies outside with zeros.
 //
-// Tiles beyond the last whole round of the pairs are divided along K instead of leaving pairs
-// idle: each pair takes an equal run of their K blocks. A run's part of a tile that ends in
+// Where the tiles do not make whole rounds of the pairs, the last ones are divided along K instead
+// of leaving pairs idle: each pair takes an equal run of their K blocks. A run's part of a tile that ends in
 // another run is left as fp32 partial sums in the workspace; the run that holds the tile's last
 // K block adds them in the order of the pairs (so results repeat bit for bit). A pair works on
-// its run's last part first, so that what it waits for was begun before its own part was; it
-// only waits for pairs of a lower index, which were started before it.
+// its run's last part first, which is what another may wait for; it only waits for pairs of a lower
+// index, which were started before it.
 //
 // Every wait is bounded (1 s): MOE_ERR_DEVICE_TIMEOUT is recorded and the pair winds down.
 #include <string.h>
@@ -34,9 +35,10 @@ namespace {
 
 using namespace tc;
 
-constexpr int TM = 256, HM = 128, TN = 256, HN = 128, BK = 64;
+constexpr int TM = 256, HM = 128, BK = 64;
+constexpr int MAX_TN = 256, MAX_HN = MAX_TN / 2;   // tile columns, and those of B that a CTA stages
 constexpr int STAGES = 6, EW = 8;
-constexpr int A_BYTES = HM * BK * 2, B_BYTES = HN * BK * 2, STAGE_BYTES = A_BYTES + B_BYTES;
+constexpr int A_BYTES = HM * BK * 2, STAGE_BYTES = A_BYTES + MAX_HN * BK * 2;
 constexpr int SLAB = 64 * 128;                    // 64 x 64 elements, 128-byte swizzle
 constexpr int PITCH = 80;                         // staging row: 32 bf16 + 16 bytes (no bank conflicts)
 constexpr int EPI_BYTES = 32 * PITCH;
@@ -48,6 +50,8 @@ struct PairGemm {
   CUtensorMap a, b;
   int64_t Mo;
   int No, nkb, tiles_m, tiles_n;
+  int tn;                // tile columns: 32 .. 256, a multiple of 32
+  uint32_t idesc, stage_tx;   // MMA shape; bytes that both CTAs load per K block
   int sk_tiles;          // the first sk_tiles tiles are divided along K
   int sk_pairs;          // over this many pairs (each gets at least kMinRun K blocks)
   const __nv_bfloat16 *bias, *res;
@@ -56,7 +60,7 @@ struct PairGemm {
   bool vec;              // rows of c, res and z hold whole 16-byte vectors
   uint32_t* header;      // error word, epoch, exit count
   uint32_t* flags;       // [CTA][EW]
-  float* part;           // [CTA][EW][128 columns][32 rows]
+  float* part;           // [CTA][EW][128 / 4][32 rows][4 columns]
 };
 
 // K blocks [k0, k1) of tile t; part: others hold the rest
@@ -64,39 +68,62 @@ struct Seg {
   int t, k0, k1;
 };
 
-// The segments of pair `p` of `np`: its share of the divided tiles, last part first, then whole
-// tiles.
+// The segments of a pair: its run of the divided tiles (the last part, which another pair may wait
+// for, then the first, which may wait for another, then the whole tiles between, whose MMAs hide
+// that wait), then whole tiles.
 struct SegCursor {
-  int nkb, tiles, np, p;
-  int64_t u0, u;       // divided units still to do: [u0, u)
+  int nkb, tiles, np;
+  int64_t u0, u1;      // the run's K blocks
+  int next_mid, mid;   // its whole tiles left: [next_mid, mid)
   int t;               // next whole tile
+  int state;
   Seg s;
   __device__ SegCursor(const PairGemm& g, int pair, int npairs) {
     nkb = g.nkb;
     tiles = g.tiles_m * g.tiles_n;
     np = npairs;
-    p = pair;
     const int64_t units = (int64_t)g.sk_tiles * nkb;
-    u0 = u = 0;
+    u0 = u1 = 0;
     if (pair < g.sk_pairs) {
       u0 = units * pair / g.sk_pairs;
-      u = units * (pair + 1) / g.sk_pairs;
+      u1 = units * (pair + 1) / g.sk_pairs;
     }
+    next_mid = mid = 0;
     t = g.sk_tiles + pair;
+    state = u1 > u0 ? 0 : 2;
   }
   __device__ bool next() {
-    if (u > u0) {
-      s.t = (int)((u - 1) / nkb);
+    if (state == 0) {
+      state = 1;
+      s.t = (int)((u1 - 1) / nkb);
       const int64_t first = (int64_t)s.t * nkb;
-      s.k1 = (int)(u - first);
+      s.k1 = (int)(u1 - first);
       s.k0 = u0 > first ? (int)(u0 - first) : 0;
-      u = first + s.k0;
+      u1 = first + s.k0;
+      return true;
+    }
+    if (state == 1) {
+      state = 2;
+      if (u1 > u0) {
+        s.t = (int)(u0 / nkb);
+        s.k0 = (int)(u0 - (int64_t)s.t * nkb);
+        s.k1 = nkb;
+        mid = (int)(u1 / nkb);
+        next_mid = s.t;
+        if (s.k0 > 0) {
+          ++next_mid;
+          return true;
+        }
+      }
+    }
+    s.k0 = 0;
+    s.k1 = nkb;
+    if (next_mid < mid) {
+      s.t = next_mid++;
       return true;
     }
     if (t >= tiles) return false;
     s.t = t;
-    s.k0 = 0;
-    s.k1 = nkb;
     t += np;
     return true;
   }
@@ -147,35 +174,42 @@ __device__ __forceinline__ bool flag_wait(const uint32_t* flag, uint32_t value, 
   return ok;
 }
 
-// 32 rows x 32 columns of `src` (or of the staging buffer to `dst`), 64 bytes per row.
-__device__ __forceinline__ void load_rows(uint8_t* stage, const __nv_bfloat16* src, int64_t ld, int rows, int cols, bool vec,
-                                          int lane) {
-  if (vec) {
+// A warp's 32 rows x 32 columns between global memory and its staging buffer, 64 bytes per row:
+// eight rows per instruction where rows hold whole 16-byte vectors, else row by row.
+struct Chunk {
+  int64_t m0;
+  int n, rows, cols;
+  bool vec;
+  __device__ __forceinline__ void load(uint4 (&v)[4], const __nv_bfloat16* p, int64_t ld, int lane) const {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const int r = i * 8 + (lane >> 2), q = lane & 3;
-      if (r < rows && q * 8 < cols)
-        *reinterpret_cast<uint4*>(stage + r * PITCH + q * 16) = *reinterpret_cast<const uint4*>(src + r * ld + q * 8);
+      const int r = i * 8 + (lane >> 2), q = (lane & 3) * 8;
+      if (r < rows && q < cols) v[i] = *reinterpret_cast<const uint4*>(p + (m0 + r) * ld + n + q);
     }
-  } else if (lane < cols) {
-    for (int r = 0; r < rows; ++r)
-      *reinterpret_cast<__nv_bfloat16*>(stage + r * PITCH + lane * 2) = src[r * ld + lane];
   }
-}
-__device__ __forceinline__ void store_rows(const uint8_t* stage, __nv_bfloat16* dst, int64_t ld, int rows, int cols,
-                                           bool vec, int lane) {
-  if (vec) {
+  __device__ __forceinline__ void stage(uint8_t* buf, const uint4 (&v)[4], int lane) const {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int r = i * 8 + (lane >> 2), q = lane & 3;
-      if (r < rows && q * 8 < cols)
-        *reinterpret_cast<uint4*>(dst + r * ld + q * 8) = *reinterpret_cast<const uint4*>(stage + r * PITCH + q * 16);
-    }
-  } else if (lane < cols) {
-    for (int r = 0; r < rows; ++r)
-      dst[r * ld + lane] = *reinterpret_cast<const __nv_bfloat16*>(stage + r * PITCH + lane * 2);
+    for (int i = 0; i < 4; ++i) *reinterpret_cast<uint4*>(buf + (i * 8 + (lane >> 2)) * PITCH + (lane & 3) * 16) = v[i];
   }
-}
+  __device__ __forceinline__ void stage_scalar(uint8_t* buf, const __nv_bfloat16* p, int64_t ld, int lane) const {
+    if (lane < cols)
+#pragma unroll 4
+      for (int r = 0; r < rows; ++r) *reinterpret_cast<__nv_bfloat16*>(buf + r * PITCH + lane * 2) = p[(m0 + r) * ld + n + lane];
+  }
+  __device__ __forceinline__ void store(const uint8_t* buf, __nv_bfloat16* p, int64_t ld, int lane) const {
+    if (vec) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int r = i * 8 + (lane >> 2), q = lane & 3;
+        if (r < rows && q * 8 < cols)
+          *reinterpret_cast<uint4*>(p + (m0 + r) * ld + n + q * 8) = *reinterpret_cast<const uint4*>(buf + r * PITCH + q * 16);
+      }
+    } else if (lane < cols) {
+#pragma unroll 4
+      for (int r = 0; r < rows; ++r) p[(m0 + r) * ld + n + lane] = *reinterpret_cast<const __nv_bfloat16*>(buf + r * PITCH + lane * 2);
+    }
+  }
+};
 
 __device__ __forceinline__ void pack_row(uint8_t* stage, int lane, const float (&v)[32]) {
   uint4* row = reinterpret_cast<uint4*>(stage + lane * PITCH);
@@ -184,44 +218,54 @@ __device__ __forceinline__ void pack_row(uint8_t* stage, int lane, const float (
     row[q] = make_uint4(pack_bf16x2(v[8 * q], v[8 * q + 1]), pack_bf16x2(v[8 * q + 2], v[8 * q + 3]),
                         pack_bf16x2(v[8 * q + 4], v[8 * q + 5]), pack_bf16x2(v[8 * q + 6], v[8 * q + 7]));
 }
-
-// bias, z, activation and residual of this lane's 32 columns, and their way out. m0: the warp's
-// first row, rows of its 32 are inside; n: the first column, cols of the 32 are inside.
-template <int ACT>
-__device__ __forceinline__ void finish_chunk(const PairGemm& g, uint8_t* stage, int lane, float (&v)[32], int64_t m0, int rows,
-                                             int n, int cols) {
-  if (g.bias != nullptr) {
+// v += 32 bf16 at p (16-byte aligned)
+__device__ __forceinline__ void add_row(float (&v)[32], const void* p) {
+  const uint4* row = static_cast<const uint4*>(p);
 #pragma unroll
-    for (int i = 0; i < 32; ++i) v[i] += i < cols ? __bfloat162float(g.bias[n + i]) : 0.f;
+  for (int q = 0; q < 4; ++q) {
+    const uint4 u = row[q];
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 t = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w[i]));
+      v[8 * q + 2 * i] += t.x;
+      v[8 * q + 2 * i + 1] += t.y;
+    }
+  }
+}
+
+// bias, z, activation and residual of this lane's 32 columns, and their way out. `res`: the chunk's
+// residual (vec), loaded ahead; `next` and `load_next`: the chunk to load into it.
+template <int ACT>
+__device__ __forceinline__ void finish_chunk(const PairGemm& g, uint8_t* stage, int lane, float (&v)[32], const Chunk& c,
+                                             uint4 (&res)[4], const Chunk& next, bool load_next) {
+  if (g.bias != nullptr) {
+    if (c.cols == 32) {
+      add_row(v, g.bias + c.n);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 32; ++i) v[i] += i < c.cols ? __bfloat162float(g.bias[c.n + i]) : 0.f;
+    }
   }
   if (g.z != nullptr) {
     pack_row(stage, lane, v);
     __syncwarp();
-    store_rows(stage, g.z + m0 * g.No + n, g.No, rows, cols, g.vec, lane);
+    c.store(stage, g.z, g.No, lane);
     __syncwarp();
   }
 #pragma unroll
-  for (int i = 0; i < 32; ++i) v[i] = act_f<ACT>(v[i]);
+  for (int i = 0; i < 32; ++i) v[i] = act_fast<ACT>(v[i]);
   if (g.res != nullptr) {
-    load_rows(stage, g.res + m0 * g.ld_res + n, g.ld_res, rows, cols, g.vec, lane);
+    if (c.vec) c.stage(stage, res, lane);
+    else c.stage_scalar(stage, g.res, g.ld_res, lane);
     __syncwarp();
-    const uint4* row = reinterpret_cast<const uint4*>(stage + lane * PITCH);
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const uint4 u = row[q];
-      const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float2 t = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w[i]));
-        v[8 * q + 2 * i] += t.x;
-        v[8 * q + 2 * i + 1] += t.y;
-      }
-    }
+    if (c.vec && load_next) next.load(res, g.res, g.ld_res, lane);
+    add_row(v, stage + lane * PITCH);
     __syncwarp();
   }
   pack_row(stage, lane, v);
   __syncwarp();
-  store_rows(stage, g.c + m0 * g.ldc + n, g.ldc, rows, cols, g.vec, lane);
+  c.store(stage, g.c, g.ldc, lane);
   __syncwarp();
 }
 
@@ -278,14 +322,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       while (ok && cur.next()) {
         int mi, ni;
         tile_coord(g, cur.s.t, mi, ni);
-        const int m0 = mi * TM + HM * (int)rank, n0 = ni * TN + HN * (int)rank;
+        const int hn = g.tn / 2, m0 = mi * TM + HM * (int)rank, n0 = ni * g.tn + hn * (int)rank;
         for (int kb = cur.s.k0; kb < cur.s.k1; ++kb) {
           if (!mbar_wait_bounded(smem_u32(&empty_bar[stage]), phase ^ 1u, &abort_flag, err, kWaitLimitNs)) {
             ok = false;
             break;
           }
           const uint32_t a_s = smem_base + stage * STAGE_BYTES, b_s = a_s + A_BYTES;
-          if (leader) mbar_arrive_expect_tx(smem_u32(&full_bar[stage]), 2 * STAGE_BYTES);
+          if (leader) mbar_arrive_expect_tx(smem_u32(&full_bar[stage]), g.stage_tx);
           const uint32_t bar = peer_addr(smem_u32(&full_bar[stage]), 0);
           const int k0 = kb * BK;
           if (A_MN) {
@@ -296,7 +340,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
           }
           if (B_MN) {
             tma2d_pair(b_s, &g.b, bar, n0, k0);
-            tma2d_pair(b_s + SLAB, &g.b, bar, n0 + 64, k0);
+            if (hn > 64) tma2d_pair(b_s + SLAB, &g.b, bar, n0 + 64, k0);
           } else {
             tma2d_pair(b_s, &g.b, bar, k0, n0);
           }
@@ -314,38 +358,39 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     __syncwarp();
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer (even CTA)
-    if (leader && lane == 0) {
-      constexpr uint32_t idesc = idesc_bf16(TM, TN, A_MN, B_MN);
+    if (leader) {
+      const uint32_t idesc = g.idesc;
+      constexpr uint32_t hi = sdesc_hi(1024), a_step = A_MN ? 2048 / 16 : 32 / 16, b_step = B_MN ? 2048 / 16 : 32 / 16;
+      const uint32_t a0 = sdesc_lo(smem_base, A_MN ? SLAB : 16), b0 = sdesc_lo(smem_base + A_BYTES, B_MN ? SLAB : 16);
+      const bool one = elect_one();
       int stage = 0, it = 0;
       uint32_t phase = 0;
-      bool ok = true, issued = false;
+      bool ok = true;
       SegCursor cur(g, pair, npairs);
       for (; ok && cur.next(); ++it) {
         const int b = it & 1;
-        if (!mbar_wait_bounded(smem_u32(&tempty_bar[b]), ((it >> 1) & 1) ^ 1, &abort_flag, err, kWaitLimitNs)) break;
+        ok = warp_bar_wait(smem_u32(&tempty_bar[b]), ((it >> 1) & 1) ^ 1, &abort_flag, err);
+        if (!ok) break;
         tc_fence_after();
-        const uint32_t d_tmem = tmem_base + (uint32_t)(b * TN);
-        for (int kb = cur.s.k0; kb < cur.s.k1; ++kb) {
-          if (!mbar_wait_bounded(smem_u32(&full_bar[stage]), phase, &abort_flag, err, kWaitLimitNs)) {
-            ok = false;
-            break;
-          }
+        const uint32_t d_tmem = tmem_base + (uint32_t)(b * MAX_TN);
+        const int blocks = cur.s.k1 - cur.s.k0;
+        for (int kb = 0; kb < blocks; ++kb) {
+          ok = warp_bar_wait(smem_u32(&full_bar[stage]), phase, &abort_flag, err);
+          if (!ok) break;
           tc_fence_after();
-          const uint32_t a_s = smem_base + stage * STAGE_BYTES, b_s = a_s + A_BYTES;
+          const uint32_t a_lo = a0 + stage * (STAGE_BYTES / 16), b_lo = b0 + stage * (STAGE_BYTES / 16);
+          if (one) {
 #pragma unroll
-          for (int kk = 0; kk < BK / 16; ++kk) {
-            const uint64_t ad = A_MN ? sdesc(a_s + kk * 2048, SLAB, 1024) : sdesc(a_s + kk * 32, 16, 1024);
-            const uint64_t bd = B_MN ? sdesc(b_s + kk * 2048, SLAB, 1024) : sdesc(b_s + kk * 32, 16, 1024);
-            umma_pair(d_tmem, ad, bd, idesc, (kb != cur.s.k0 || kk != 0) ? 1u : 0u);
+            for (int kk = 0; kk < BK / 16; ++kk)
+              umma_lo<2>(d_tmem, a_lo + kk * a_step, hi, b_lo + kk * b_step, hi, idesc, (kb | kk) != 0 ? 1u : 0u);
+            umma_commit_mc(smem_u32(&empty_bar[stage]), 0x3);
           }
-          issued = true;
-          umma_commit_mc(smem_u32(&empty_bar[stage]), 0x3);
           if (++stage == STAGES) { stage = 0; phase ^= 1u; }
         }
         if (!ok) break;
-        umma_commit_mc(smem_u32(&tfull_bar[b]), 0x3);
+        if (one) umma_commit_mc(smem_u32(&tfull_bar[b]), 0x3);
       }
-      if (issued) {   // every MMA retired before the tensor memory is released
+      if (one) {   // every MMA retired before the tensor memory is released
         umma_commit_mc(smem_u32(&final_bar), 0x1);
         mbar_wait_bounded(smem_u32(&final_bar), 0, nullptr, err, kWaitLimitNs);
       }
@@ -353,7 +398,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     __syncwarp();
   } else {
     // ------------------------------------------------------------ epilogue (both CTAs)
-    const int ew = warp - 2, lg = warp & 3, col0 = (ew >> 2) * 128;
+    const int ew = warp - 2, lg = warp & 3, hn = g.tn / 2, col0 = (ew >> 2) * hn;
     uint8_t* stage = smem + STAGES * STAGE_BYTES + ew * EPI_BYTES;
     const int slot = (int)blockIdx.x * EW + ew;
     int it = 0;
@@ -363,32 +408,38 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       int mi, ni;
       tile_coord(g, cur.s.t, mi, ni);
       const int64_t m0 = (int64_t)mi * TM + HM * (int)rank + lg * 32;
-      const int rows = (int)min((int64_t)32, g.Mo - m0), n0 = ni * TN + col0;
+      const int rows = (int)min((int64_t)32, g.Mo - m0), n0 = ni * g.tn + col0;
+      const bool live = rows > 0 && n0 < g.No;    // the same for every part of the tile
+      const bool owner = cur.s.k1 == g.nkb;
+      auto chunk = [&](int c) { return Chunk{m0, n0 + c, rows, min(32, min(hn - c, g.No - n0 - c)), g.vec}; };
+      uint4 res[4];
+      if (live && owner && g.res != nullptr && g.vec) chunk(0).load(res, g.res, g.ld_res, lane);
       const bool got = mbar_wait_bounded(smem_u32(&tfull_bar[b]), (it >> 1) & 1, &abort_flag, err, kWaitLimitNs);
       if (!__all_sync(0xffffffffu, got)) break;   // warp-uniform: tcgen05.ld is .sync.aligned
       tc_fence_after();
-      const uint32_t acc = tmem_base + ((uint32_t)(lg * 32) << 16) + (uint32_t)(b * TN + col0);
-      const bool live = rows > 0 && n0 < g.No;    // the same for every part of the tile
+      const uint32_t acc = tmem_base + ((uint32_t)(lg * 32) << 16) + (uint32_t)(b * MAX_TN + col0);
       bool ok = true;
-      if (live && cur.s.k1 < g.nkb) {
+      if (live && !owner) {
         // the tile ends in a later pair's run: leave the partial sums to it
-        float* out = g.part + (int64_t)slot * 128 * 32 + lane;
-#pragma unroll
-        for (int c = 0; c < 128; c += 32) {
+        float4* out = reinterpret_cast<float4*>(g.part) + (int64_t)slot * 32 * 32 + lane;
+#pragma unroll 1
+        for (int c = 0; c < hn; c += 32) {
           uint32_t u[32];
           tmem_ld32(acc + c, u);
           tmem_ld_wait();
 #pragma unroll
-          for (int i = 0; i < 32; ++i) __stcg(out + (c + i) * 32, __uint_as_float(u[i]));
+          for (int i = 0; i < 8; ++i)
+            __stcg(out + (c / 4 + i) * 32, make_float4(__uint_as_float(u[4 * i]), __uint_as_float(u[4 * i + 1]),
+                                                       __uint_as_float(u[4 * i + 2]), __uint_as_float(u[4 * i + 3])));
         }
         __threadfence();
         __syncwarp();
         if (lane == 0) st_release(g.flags + slot, epoch);
       } else if (live) {
-        // first and last pair before this one whose runs hold parts of the tile
-        const int64_t units = (int64_t)g.sk_tiles * g.nkb, first = (int64_t)cur.s.t * g.nkb;
+        // the first pair whose run holds a part of the tile, and the wait for all up to this one
         int q0 = pair;
         if (cur.s.k0 > 0) {
+          const int64_t units = (int64_t)g.sk_tiles * g.nkb, first = (int64_t)cur.s.t * g.nkb;
           q0 = (int)(first * g.sk_pairs / units);
           while (units * (q0 + 1) / g.sk_pairs <= first) ++q0;
           for (int q = q0; ok && q < pair; ++q)
@@ -396,7 +447,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         }
         if (ok) {
 #pragma unroll 1
-          for (int c = 0; c < 128; c += 32) {
+          for (int c = 0; c < hn; c += 32) {
             if (n0 + c >= g.No) break;
             uint32_t u[32];
             float v[32];
@@ -404,12 +455,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
             tmem_ld_wait();
 #pragma unroll
             for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(u[i]);
+#pragma unroll 1
             for (int q = q0; q < pair; ++q) {
-              const float* in = g.part + ((int64_t)((q * 2 + (int)rank) * EW + ew) * 128 + c) * 32 + lane;
+              const float4* in =
+                  reinterpret_cast<const float4*>(g.part) + ((int64_t)((q * 2 + (int)rank) * EW + ew) * 32 + c / 4) * 32 + lane;
+              float4 w[8];
 #pragma unroll
-              for (int i = 0; i < 32; ++i) v[i] += __ldcg(in + i * 32);
+              for (int i = 0; i < 8; ++i) w[i] = __ldcg(in + i * 32);
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                v[4 * i] += w[i].x;
+                v[4 * i + 1] += w[i].y;
+                v[4 * i + 2] += w[i].z;
+                v[4 * i + 3] += w[i].w;
+              }
             }
-            finish_chunk<ACT>(g, stage, lane, v, m0, rows, n0 + c, min(32, g.No - n0 - c));
+            finish_chunk<ACT>(g, stage, lane, v, chunk(c), res, chunk(c + 32), c + 32 < hn && n0 + c + 32 < g.No);
           }
         }
       }
@@ -435,8 +496,61 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   }
 }
 
+// Columns of a tile and the divided tiles, by the time that the slowest pair takes (us): a K block
+// of a 256 x TN tile takes the longer of its MMAs (kMma at 256 columns) and its loads (16 KB of A,
+// 64 TN bytes of B at kLoad KB/us for an SM); a launch kStart, the last tile's way out kOut at 256
+// columns; a tile's division kJoin (its fp32 parts go through L2) and kPart more for each part.
+// Whole rounds of narrower tiles beat divided ones of 256 where some width fits the pairs:
+// 4096 x 2816 x 2048 in 208 columns, 2816 x 2048 x 4096 in 160; with few tiles and a long K only a
+// division uses the pairs. Returns the pairs to launch.
+constexpr double kMma = 0.335, kLoad = 105.0, kStart = 3.0, kOut = 4.0, kJoin = 9.0, kPart = 1.5;
+
+int plan(PairGemm& g, int pairs) {
+  double best = 1e30;
+  int used = pairs;
+  for (int tn = 256; tn >= 32; tn -= 32) {
+    const int64_t tiles = (int64_t)g.tiles_m * ((g.No + tn - 1) / tn);
+    const double mma = kMma * tn / 256, load = (16.0 + tn / 16.0) / kLoad;
+    const double block = mma > load ? mma : load, out = kOut * tn / 256;
+    const int64_t rounds = (tiles + pairs - 1) / pairs;
+    double cost = kStart + rounds * g.nkb * block + out;
+    int sk_tiles = 0, sk_pairs = 0, use = (int)(tiles < pairs ? tiles : pairs);
+    const int64_t rem = tiles % pairs;
+    if (rem > 0) {
+      // with fewer tiles than pairs all are divided; else the incomplete round's and one round more,
+      // so that a run is longer than a tile
+      const int64_t divided = tiles < pairs ? tiles : rem + pairs;
+      int64_t over = divided * g.nkb / kMinRun;
+      if (over > pairs) over = pairs;
+      const double parts = over > divided ? (double)over / divided : 1.0;
+      const double c = kStart + ((tiles - divided) / pairs * g.nkb + (double)divided * g.nkb / over) * block + out + kJoin * tn / 256 +
+                       kPart * parts;
+      if (over > rem && c < cost) {
+        cost = c;
+        sk_tiles = (int)divided;
+        sk_pairs = (int)over;
+        use = tiles < pairs ? (int)over : pairs;
+      }
+    }
+    if (cost < best) {
+      best = cost;
+      g.tn = tn;
+      g.sk_tiles = sk_tiles;
+      g.sk_pairs = sk_pairs;
+      used = use;
+    }
+  }
+  g.tiles_n = (g.No + g.tn - 1) / g.tn;
+  return used;
+}
+
+// B's tensor map: K-major in boxes of 64 along K x half a tile, MN-major of 64 columns x 64 of K.
+bool map_b(PairGemm& g, const GemmArgs& a) {
+  return a.bk == 1 ? map2d_ld(&g.b, a.b, a.K, a.N, a.bn, BK, g.tn / 2) : map2d_ld(&g.b, a.b, a.N, a.K, a.bk, 64, BK);
+}
+
 template <bool A_MN, bool B_MN, int ACT>
-int launch_pair(PairGemm& g, int num_sms, cudaStream_t st) {
+int launch_pair(PairGemm& g, const GemmArgs& a, int num_sms, cudaStream_t st) {
   auto kernel = linear_pair_kernel<A_MN, B_MN, ACT>;
   // per device, once (under a lock): the shared-memory attribute and the pairs resident at once
   static std::mutex mu;
@@ -459,22 +573,10 @@ int launch_pair(PairGemm& g, int num_sms, cudaStream_t st) {
     }
     pairs = occ_dev[dev];
   }
-  const int64_t tiles = (int64_t)g.tiles_m * g.tiles_n;
-  const int rem = (int)(tiles % pairs);
-  g.sk_tiles = g.sk_pairs = 0;
-  const int64_t most = (int64_t)rem * g.nkb / kMinRun;   // pairs that the divided tiles can feed
-  const int run_pairs = most < pairs ? (int)most : pairs;
-  if (tiles < pairs) {
-    if (run_pairs > tiles) {
-      g.sk_tiles = (int)tiles;
-      g.sk_pairs = pairs = run_pairs;
-    } else {
-      pairs = (int)tiles;
-    }
-  } else if (run_pairs > rem && (int64_t)rem * g.nkb / run_pairs + kJoinBlocks < g.nkb) {
-    g.sk_tiles = rem;
-    g.sk_pairs = run_pairs;
-  }
+  pairs = plan(g, pairs);
+  g.idesc = idesc_bf16(TM, g.tn, A_MN, B_MN);
+  g.stage_tx = 2 * (A_BYTES + (B_MN ? (g.tn > 128 ? 2 : 1) * SLAB : g.tn / 2 * BK * 2));
+  if (!map_b(g, a)) return MOE_ERR_CUDA;
   TraceScope ts(TP_LINEAR, st);
   kernel<<<2 * pairs, THREADS, SMEM_BYTES, st>>>(g);
   return cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_LAUNCH;
@@ -491,7 +593,6 @@ int launch_linear_pair(int kind, const GemmArgs& a, uint8_t* ws, size_t part, in
   g.No = a.N;
   g.nkb = (int)((a.K + BK - 1) / BK);
   g.tiles_m = (int)((a.M + TM - 1) / TM);
-  g.tiles_n = (a.N + TN - 1) / TN;
   g.bias = static_cast<const __nv_bfloat16*>(a.bias);
   g.res = static_cast<const __nv_bfloat16*>(a.res);
   g.z = static_cast<__nv_bfloat16*>(a.z_out);
@@ -502,13 +603,12 @@ int launch_linear_pair(int kind, const GemmArgs& a, uint8_t* ws, size_t part, in
   g.header = reinterpret_cast<uint32_t*>(ws);
   g.flags = g.header + 256;
   g.part = reinterpret_cast<float*>(ws + part);
-  // K-major: box 64 along K x 128 rows; MN-major: box 64 along the rows x 64 of K
-  bool ok = a.ak == 1 ? map2d_ld(&g.a, a.a, a.K, a.M, a.am, BK, HM) : map2d_ld(&g.a, a.a, a.M, a.K, a.ak, 64, BK);
-  ok = ok && (a.bk == 1 ? map2d_ld(&g.b, a.b, a.K, a.N, a.bn, BK, HN) : map2d_ld(&g.b, a.b, a.N, a.K, a.bk, 64, BK));
+  // A: K-major in boxes of 64 along K x 128 rows; MN-major of 64 rows x 64 of K
+  const bool ok = a.ak == 1 ? map2d_ld(&g.a, a.a, a.K, a.M, a.am, BK, HM) : map2d_ld(&g.a, a.a, a.M, a.K, a.ak, 64, BK);
   if (!ok) return MOE_ERR_CUDA;
-  if (kind == LINEAR_DX) return launch_pair<false, true, MOE_ACT_NONE>(g, num_sms, st);
-  if (kind == LINEAR_DW) return launch_pair<true, true, MOE_ACT_NONE>(g, num_sms, st);
-#define MOE_P(A) return launch_pair<false, false, A>(g, num_sms, st)
+  if (kind == LINEAR_DX) return launch_pair<false, true, MOE_ACT_NONE>(g, a, num_sms, st);
+  if (kind == LINEAR_DW) return launch_pair<true, true, MOE_ACT_NONE>(g, a, num_sms, st);
+#define MOE_P(ACT) return launch_pair<false, false, ACT>(g, a, num_sms, st)
   MOE_ACT_SWITCH(a.act, MOE_P)
 #undef MOE_P
   return MOE_OK;

@@ -79,7 +79,7 @@ __device__ __forceinline__ void finish8(const LinearStream& g, float (&v)[8], co
       p.store(g.z + m * g.N + n);
     }
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = act_any(g.act, v[i]) + r[i];
+    for (int i = 0; i < 8; ++i) v[i] = act_any_fast(g.act, v[i]) + r[i];
     p.from_float(v);
     p.store(g.y + m * g.ld_y + n);
   } else {
@@ -88,7 +88,7 @@ __device__ __forceinline__ void finish8(const LinearStream& g, float (&v)[8], co
       if (i >= cols) break;
       const float res = g.res != nullptr ? __bfloat162float(g.res[m * g.ld_res + n + i]) : 0.f;
       if (g.z != nullptr) g.z[m * g.N + n + i] = __float2bfloat16_rn(v[i]);
-      g.y[m * g.ld_y + n + i] = __float2bfloat16_rn(act_any(g.act, v[i]) + res);
+      g.y[m * g.ld_y + n + i] = __float2bfloat16_rn(act_any_fast(g.act, v[i]) + res);
     }
   }
 }
@@ -132,11 +132,12 @@ __global__ void __launch_bounds__(THREADS, 1) linear_stream_kernel(const __grid_
     }
     __syncwarp();
   } else if (warp == 1) {
-    if (lane == 0) {
-      Ring<STAGES> ring;
-      int it = 0;
-      for (int tile = tile0; tile < g.tiles; tile += step, ++it)
-        if (!mma_tile<NT, STAGES>(b, smem_base, k1 - k0, ring, it, g.err)) break;
+    Ring<STAGES> ring;
+    int it = 0;
+    const bool one = elect_one();
+    for (int tile = tile0; tile < g.tiles; tile += step, ++it)
+      if (!mma_tile<NT, STAGES>(b, smem_base, k1 - k0, ring, it, one, g.err)) break;
+    if (one) {
       umma1_commit(smem_u32(&b.final));   // every MMA retired before the tensor memory is released
       bar_wait(&b.final, 0, nullptr, g.err);
     }
@@ -297,8 +298,7 @@ int launch_linear_stream(const GemmArgs& a, uint8_t* ws, int num_sms, cudaStream
   if (a.M <= 16) return launch_nt<16>(g, a, num_sms, st);
   if (a.M <= 32) return launch_nt<32>(g, a, num_sms, st);
   if (a.M <= 64) return launch_nt<64>(g, a, num_sms, st);
-  if (a.M <= 128) return launch_nt<128>(g, a, num_sms, st);
-  return launch_nt<256>(g, a, num_sms, st);
+  return launch_nt<128>(g, a, num_sms, st);
 }
 
 }  // namespace moe

@@ -58,7 +58,7 @@ struct LinearLayout {
   int64_t ld_dz;
   size_t total;
 };
-constexpr int kDbSplit = 64;
+constexpr int kDbSplit = 256;
 constexpr int kMaxWidth = 65535 * 64;   // N and K of a linear layer
 LinearLayout linear_layout(const moe_linear_dims& d);
 
@@ -86,11 +86,10 @@ cudaError_t launch_gemm_simt(const GemmArgs& g, cudaStream_t st);
 enum LinearKind { LINEAR_FWD = 0, LINEAR_DX, LINEAR_DW };
 constexpr int kMaxPairs = 80;     // clusters of two CTAs
 constexpr int kMinRun = 4;        // K blocks of a pair's run when there are fewer tiles than pairs
-constexpr int kJoinBlocks = 8;    // K blocks that the division of a tile costs
 size_t linear_pair_part_bytes();
 int launch_linear_pair(int kind, const GemmArgs& a, uint8_t* ws, size_t part, int num_sms, cudaStream_t st);
 // The forward product for at most kStreamRows rows, as a stream of the weights.
-constexpr int kStreamRows = 256;
+constexpr int kStreamRows = 128;
 int launch_linear_stream(const GemmArgs& a, uint8_t* ws, int num_sms, cudaStream_t st);
 // dz = dy * act'(z) (dz may be NULL: sums only) and db (may be NULL)
 cudaError_t launch_linear_dz(const void* dy, int64_t ld_dy, const void* z, int act, int64_t M, int N,

@@ -4,7 +4,7 @@
 //
 // With few tokens a product is a stream of weights out of HBM, and everything here serves that
 // stream. The weights are the MMA's A operand, 128 weight rows by 64 of K per stage; the tokens
-// are B, NT (16 .. 256) rows; the transposed result, 128 weight rows by NT tokens, accumulates in
+// are B, NT (16 .. 128) rows; the transposed result, 128 weight rows by NT tokens, accumulates in
 // tensor memory, two accumulators deep. One thread issues TMA loads into a ring that fills the
 // shared memory (about 190 KB in flight per SM, four times what the HBM's latency needs), one
 // thread issues tcgen05.mma, eight warps take the results out.
@@ -125,13 +125,6 @@ __device__ __forceinline__ bool ct_any(bool bad) {
   return r != 0;
 }
 
-__device__ __forceinline__ void umma1(uint32_t d_tmem, uint64_t ad, uint64_t bd, uint32_t idesc, uint32_t accum) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "l"(ad), "l"(bd), "r"(idesc), "r"(accum)
-      : "memory");
-}
 __device__ __forceinline__ void umma1_commit(uint32_t bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
 }
@@ -246,33 +239,38 @@ template <int STAGES> __device__ __forceinline__ void drain(Bars& b, const Ring<
   }
 }
 
-// The MMAs of `blocks` K blocks into accumulator it & 1 (`it` counts the tiles of the launch).
+// The MMAs of `blocks` K blocks into accumulator it & 1 (`it` counts the tiles of the launch), by
+// the whole warp; `one`: this lane issues.
 template <int NT, int STAGES>
-__device__ __forceinline__ bool mma_tile(Bars& b, uint32_t smem_base, int blocks, Ring<STAGES>& ring, int it, int* err) {
-  constexpr uint32_t idesc = idesc_bf16(BM, NT, false, false);
+__device__ __forceinline__ bool mma_tile(Bars& b, uint32_t smem_base, int blocks, Ring<STAGES>& ring, int it, bool one, int* err) {
+  constexpr uint32_t idesc = idesc_bf16(BM, NT, false, false), hi = sdesc_hi(1024);
+  const uint32_t a0 = sdesc_lo(smem_base, 16);
   const int buf = it & 1;
-  if (!bar_wait(&b.tempty[buf], ((it >> 1) & 1) ^ 1, &b.abort, err)) return false;
+  if (!warp_bar_wait(smem_u32(&b.tempty[buf]), ((it >> 1) & 1) ^ 1, &b.abort, err)) return false;
   tc_fence_after();
   const uint32_t d_tmem = b.tmem + (uint32_t)(buf * NT);
   for (int kb = 0; kb < blocks; ++kb) {
-    if (!bar_wait(&b.full[ring.stage], ring.phase, &b.abort, err)) return false;
+    if (!warp_bar_wait(smem_u32(&b.full[ring.stage]), ring.phase, &b.abort, err)) return false;
     tc_fence_after();
-    const uint32_t a_s = smem_base + ring.stage * Cfg<NT>::STAGE, b_s = a_s + A_BYTES;
+    const uint32_t a_lo = a0 + ring.stage * (Cfg<NT>::STAGE / 16);
+    if (one) {
 #pragma unroll
-    for (int kk = 0; kk < BK / 16; ++kk)
-      umma1(d_tmem, sdesc(a_s + kk * 32, 16, 1024), sdesc(b_s + kk * 32, 16, 1024), idesc, (kb | kk) != 0 ? 1u : 0u);
-    umma1_commit(smem_u32(&b.empty[ring.stage]));
+      for (int kk = 0; kk < BK / 16; ++kk)
+        umma_lo<1>(d_tmem, a_lo + kk * 2, hi, a_lo + A_BYTES / 16 + kk * 2, hi, idesc, (kb | kk) != 0 ? 1u : 0u);
+      umma1_commit(smem_u32(&b.empty[ring.stage]));
+    }
     ring.step();
   }
-  umma1_commit(smem_u32(&b.tfull[buf]));
+  if (one) umma1_commit(smem_u32(&b.tfull[buf]));
   return true;
 }
 
-// The MMA thread's part of a run.
+// The MMA warp's part of a run.
 template <int NT, int STAGES>
-__device__ __forceinline__ bool mma_run(Bars& b, uint32_t smem_base, Run run, Ring<STAGES>& ring, int& it, int* err) {
+__device__ __forceinline__ bool mma_run(Bars& b, uint32_t smem_base, Run run, Ring<STAGES>& ring, int& it, bool one,
+                                        int* err) {
   for (; run.next(); ++it)
-    if (!mma_tile<NT, STAGES>(b, smem_base, run.s.k1 - run.s.k0, ring, it, err)) return false;
+    if (!mma_tile<NT, STAGES>(b, smem_base, run.s.k1 - run.s.k0, ring, it, one, err)) return false;
   return true;
 }
 

@@ -128,6 +128,49 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float a, float b) {
   return *reinterpret_cast<uint32_t*>(&h);
 }
 
+// ------------------------------------------------------------------ issuing MMAs from a whole warp
+// A tcgen05.mma takes its descriptors from uniform registers. In code that one lane alone runs
+// the compiler has to move them there for every instruction: four MMAs and their bookkeeping took
+// 700 cycles, more than a 256 x 256 x 64 block needs in the tensor cores. The linear and few-token
+// kernels' issuing warp therefore stays together, with warp-uniform loops and waits, and only the
+// instruction itself is one lane's (elect_one).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r));
+  return r != 0;
+}
+// The upper word of sdesc (fixed for a layout); the lower is (address >> 4) | lbo.
+__host__ __device__ constexpr uint32_t sdesc_hi(uint32_t sbo) { return (sbo >> 4) | (1u << 14) | (2u << 29); }
+__device__ __forceinline__ uint32_t sdesc_lo(uint32_t saddr, uint32_t lbo) {
+  return ((saddr & 0x3FFFFu) >> 4) | ((lbo >> 4) << 16);
+}
+template <int GROUP>
+__device__ __forceinline__ void umma_lo(uint32_t d_tmem, uint32_t a_lo, uint32_t a_hi, uint32_t b_lo, uint32_t b_hi, uint32_t idesc,
+                                        uint32_t accum) {
+  if (GROUP == 2)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\tmov.b64 a, {%1, %2};\n\tmov.b64 b, {%3, %4};\n\tsetp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], a, b, %5, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_lo), "r"(a_hi), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(accum)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\tmov.b64 a, {%1, %2};\n\tmov.b64 b, {%3, %4};\n\tsetp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %5, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_lo), "r"(a_hi), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(accum)
+        : "memory");
+}
+// Wait of a whole warp; the answer is uniform.
+static __device__ __noinline__ bool warp_bar_wait_slow(uint32_t bar, uint32_t parity, volatile int* abort, int* err) {
+  return mbar_wait_bounded(bar, parity, abort, err, kWaitLimitNs);
+}
+__device__ __forceinline__ bool warp_bar_wait(uint32_t bar, uint32_t parity, volatile int* abort, int* err) {
+  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+  return __all_sync(0xffffffffu, warp_bar_wait_slow(bar, parity, abort, err));
+}
+
 // ------------------------------------------------------------------ cluster / pair PTX
 __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;

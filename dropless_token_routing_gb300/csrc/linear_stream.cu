@@ -111,25 +111,28 @@ __global__ void __launch_bounds__(THREADS, 1) linear_stream_kernel(const __grid_
   if (cl > 1) cluster_sync_all();   // the peers' barriers are initialised before any arrival
 
   if (warp == 0) {
-    if (lane == 0) {
-      Ring<STAGES> ring;
-      int64_t loaded = 0;
-      bool ok = true;
-      const uint32_t bytes = (uint32_t)(g.rows + NT) * BK * 2;
-      for (int tile = tile0; ok && tile < g.tiles; tile += step) {
-        for (int kb = k0; kb < k1; ++kb) {
-          ok = bar_wait(&b.empty[ring.stage], ring.phase ^ 1u, &b.abort, g.err);
-          if (!ok) break;
+    // the whole warp, one lane issuing (see tc_common.cuh)
+    const bool one = elect_one();
+    Ring<STAGES> ring;
+    int64_t loaded = 0;
+    bool ok = true;
+    const uint32_t bytes = (uint32_t)(g.rows + NT) * BK * 2;
+    for (int tile = tile0; ok && tile < g.tiles; tile += step) {
+      const int n0 = tile * g.rows;   // rows past the tile keep what was in the stage
+      for (int kb = k0; kb < k1; ++kb) {
+        ok = warp_bar_wait(smem_u32(&b.empty[ring.stage]), ring.phase ^ 1u, &b.abort, g.err);
+        if (!ok) break;
+        if (one) {
           const uint32_t a_s = smem_base + ring.stage * STAGE, bar = smem_u32(&b.full[ring.stage]);
           mbar_arrive_expect_tx(bar, bytes);
-          tma2d(a_s, &g.w, bar, kb * BK, tile * g.rows);   // rows past the tile keep what was there
+          tma2d(a_s, &g.w, bar, kb * BK, n0);
           tma2d(a_s + A_BYTES, &g.x, bar, kb * BK, 0);
-          ring.step();
-          ++loaded;
         }
+        ring.step();
+        ++loaded;
       }
-      drain<STAGES>(b, ring, loaded, g.err);
     }
+    if (one) drain<STAGES>(b, ring, loaded, g.err);
     __syncwarp();
   } else if (warp == 1) {
     Ring<STAGES> ring;

@@ -270,18 +270,39 @@ class OpWorkspace:
         N.check(N.lib().moe_op_workspace_init(self.ptr, self.nbytes, _s(stream)), "moe_op_workspace_init")
 
 
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream(stream, device_index):
+    """The stream's handle; the current one's without making a Stream object where torch can."""
+    if stream is not None:
+        return stream.cuda_stream
+    return _raw_stream(device_index) if _raw_stream is not None else torch.cuda.current_stream(device_index).cuda_stream
+
+
+def _refuse(name, dtype, shape, t):
+    raise ValueError(f"{name}: expected contiguous {list(shape)} of {dtype}, got {list(t.shape)} of {t.dtype}, "
+                     f"strides {t.stride()}")
+
+
 def _matrix(t, name, dtype, rows, cols):
     """Checks a [rows, cols] operand with contiguous rows; returns the stride between them."""
-    if t.dtype != dtype or t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols:
+    if t.dtype != dtype or t.shape != (rows, cols):
         raise ValueError(f"{name}: expected [{rows}, {cols}] of {dtype}, got {list(t.shape)} of {t.dtype}")
-    if cols > 1 and t.stride(1) != 1:
+    ld, inner = t.stride()
+    if inner != 1 and cols > 1:
         raise ValueError(f"{name}: the elements of a row must be contiguous")
-    return t.stride(0) if rows > 1 else max(cols, t.stride(0))
+    return ld if rows > 1 or ld > cols else cols
 
 
 def _dense(t, name, dtype, shape):
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
-        raise ValueError(f"{name}: expected contiguous {list(shape)} of {dtype}, got {list(t.shape)} of {t.dtype}")
+    if t.dtype != dtype or t.shape != shape or not t.is_contiguous():
+        _refuse(name, dtype, shape, t)
+
+
+def _device_index(device):
+    d = torch.device(device)
+    return d.index if d.index is not None else torch.cuda.current_device()
 
 
 class MoEDecodeLayer:
@@ -302,7 +323,11 @@ class MoEDecodeLayer:
         self._idx = torch.empty(max_tokens, k, dtype=torch.int32, device=device)
         self._w = torch.empty(max_tokens, k, dtype=torch.float32, device=device)
         self._y = torch.empty(max_tokens, d, dtype=dtype, device=device)
+        self._views = {}            # y's first T rows
+        self._device = _device_index(device)
         self._c = params.c()
+        self._call = N.lib().moe_layer_decode
+        self._refs = (ctypes.byref(self._c), ctypes.byref(self.dims), self._idx.data_ptr(), self._w.data_ptr())
         self._T = 0
 
     @property
@@ -314,22 +339,28 @@ class MoEDecodeLayer:
         return self._w[:self._T]
 
     def forward(self, x, residual=None, logits_in=None, out=None, stream=None):
-        T, d, dt = x.shape[0], self.d, self.dtype
+        T = x.shape[0]
+        shape = (T, self.d)
         if T > self.max_tokens:
             raise ValueError(f"x: {T} tokens, the layer was made for {self.max_tokens}")
-        _dense(x, "x", dt, (T, d))
+        _dense(x, "x", self.dtype, shape)
         if residual is not None:
-            _dense(residual, "residual", dt, (T, d))
+            _dense(residual, "residual", self.dtype, shape)
         if logits_in is not None:
             _dense(logits_in, "logits_in", torch.float32, (T, self.E))
         if out is None:
-            out = self._y[:T]
+            out = self._views.get(T)
+            if out is None:
+                out = self._views[T] = self._y[:T]
         else:
-            _dense(out, "out", dt, (T, d))
+            _dense(out, "out", self.dtype, shape)
         self._T = self.dims.T = T
-        N.check(N.lib().moe_layer_decode(ctypes.byref(self._c), x.data_ptr(), _p(logits_in), _p(residual),
-                                         ctypes.byref(self.dims), self._idx.data_ptr(), self._w.data_ptr(),
-                                         out.data_ptr(), self.ws.ptr, self.ws.nbytes, _s(stream)), "moe_layer_decode")
+        c, dims, idx, w = self._refs
+        st = self._call(c, x.data_ptr(), None if logits_in is None else logits_in.data_ptr(),
+                        None if residual is None else residual.data_ptr(), dims, idx, w, out.data_ptr(), self.ws.ptr,
+                        self.ws.nbytes, _stream(stream, self._device))
+        if st:
+            N.check(st, "moe_layer_decode")
         return out
 
 
@@ -355,7 +386,11 @@ class Linear:
         self.ws = OpWorkspace(N.lib().moe_linear_workspace_bytes(ctypes.byref(self.dims)), "moe_linear_workspace_bytes",
                               dev, stream)
         self._x = None
-        self._bufs = {}
+        self._bufs, self._views = {}, {}
+        self._device = _device_index(dev)
+        self._dims_ref = ctypes.byref(self.dims)
+        self._w_ptr, self._b_ptr = w.data_ptr(), _p(bias)
+        self._fwd, self._bwd = N.lib().moe_linear_fwd, N.lib().moe_linear_bwd
 
     def _own(self, name, rows, cols):
         """The layer's buffer ``name``, made at its first use."""
@@ -364,23 +399,31 @@ class Linear:
             t = self._bufs[name] = torch.empty(rows, cols, dtype=self.dtype, device=self.device)
         return t
 
-    def _rows(self, M):
-        if M > self.max_rows:
-            raise ValueError(f"{M} rows, the layer was made for {self.max_rows}")
+    def _view(self, name, rows, cols, M, width):
+        """[M, width] of the buffer ``name`` [rows, cols]."""
+        key = (name, M, width)
+        t = self._views.get(key)
+        if t is None:
+            t = self._views[key] = self._own(name, rows, cols)[:M, :width]
+        return t
 
     def forward(self, x, residual=None, save=False, out=None, stream=None):
         M, D = x.shape[0], self.dims
-        self._rows(M)
+        if M > self.max_rows:
+            raise ValueError(f"{M} rows, the layer was made for {self.max_rows}")
         D.M, D.ld_x = M, _matrix(x, "x", self.dtype, M, self.K)
         D.ld_res = _matrix(residual, "residual", self.dtype, M, self.N) if residual is not None else 0
         if out is None:
-            out = self._own("y", self.max_rows, self.N)[:M]
-        D.ld_y = _matrix(out, "out", self.dtype, M, self.N)
-        z = self._own("z", self.max_rows, self.N) if save and self.act != 0 else None
+            out = self._view("y", self.max_rows, self.N, M, self.N)
+            D.ld_y = self.N
+        else:
+            D.ld_y = _matrix(out, "out", self.dtype, M, self.N)
+        z = self._own("z", self.max_rows, self.N).data_ptr() if save and self.act != 0 else None
         self._x = x if save else None
-        N.check(N.lib().moe_linear_fwd(x.data_ptr(), self.w.data_ptr(), _p(self.bias), _p(residual), ctypes.byref(D),
-                                       _p(z), out.data_ptr(), self.ws.ptr, self.ws.nbytes, _s(stream)),
-                "moe_linear_fwd")
+        st = self._fwd(x.data_ptr(), self._w_ptr, self._b_ptr, None if residual is None else residual.data_ptr(),
+                       self._dims_ref, z, out.data_ptr(), self.ws.ptr, self.ws.nbytes, _stream(stream, self._device))
+        if st:
+            N.check(st, "moe_linear_fwd")
         return out
 
     def backward(self, dy, need=("dx", "dw", "db"), stream=None):
@@ -393,14 +436,16 @@ class Linear:
         ld_w = D.ld_w
         dx = dw = db = None
         if "dx" in need:   # rows of dx are as far apart as those of x
-            dx = self._own(("dx", D.ld_x), self.max_rows, D.ld_x)[:M, :self.K]
+            dx = self._view(("dx", D.ld_x), self.max_rows, D.ld_x, M, self.K)
         if "dw" in need:
-            dw = self._own(("dw", ld_w), self.N, ld_w)[:, :self.K]
+            dw = self._view("dw", self.N, ld_w, self.N, self.K)
         if "db" in need and self.bias is not None:
             db = self._own("db", 1, self.N)[0]
-        z = self._own("z", self.max_rows, self.N) if self.act != 0 else None
-        N.check(N.lib().moe_linear_bwd(x.data_ptr(), self.w.data_ptr(), _p(z), dy.data_ptr(), ctypes.byref(D), _p(dx),
-                                       _p(dw), _p(db), self.ws.ptr, self.ws.nbytes, _s(stream)), "moe_linear_bwd")
+        z = self._own("z", self.max_rows, self.N).data_ptr() if self.act != 0 else None
+        st = self._bwd(x.data_ptr(), self._w_ptr, z, dy.data_ptr(), self._dims_ref, _p(dx), _p(dw), _p(db), self.ws.ptr,
+                       self.ws.nbytes, _stream(stream, self._device))
+        if st:
+            N.check(st, "moe_linear_bwd")
         return dict(dx=dx, dw=dw, db=db)
 
 
@@ -413,12 +458,16 @@ class DraftVerifier:
         self.dims = N.VerifyDims(0, n, V, _dt(dtype), 0, 0)
         self._tokens = torch.empty(max_batch, n + 1, dtype=torch.int32, device=device)
         self._accepted = torch.empty(max_batch, dtype=torch.int32, device=device)
+        self._views = {}
+        self._device = _device_index(device)
+        self._call, self._dims_ref = N.lib().moe_verify_draft, ctypes.byref(self.dims)
 
     def _rows(self, t, name, B, rows):
-        if t.dtype != self.dtype or tuple(t.shape) != (B, rows, self.V):
+        if t.dtype != self.dtype or t.shape != (B, rows, self.V):
             raise ValueError(f"{name}: expected [{B}, {rows}, {self.V}] of {self.dtype}, got {list(t.shape)} of {t.dtype}")
-        ld = t.stride(1) if rows > 1 else (t.stride(0) if B > 1 else self.V)
-        if (self.V > 1 and t.stride(2) != 1) or (B > 1 and rows > 0 and t.stride(0) != rows * ld) or ld < self.V:
+        s0, s1, s2 = t.stride()
+        ld = s1 if rows > 1 else (s0 if B > 1 else self.V)
+        if (self.V > 1 and s2 != 1) or (B > 1 and rows > 0 and s0 != rows * ld) or ld < self.V:
             raise ValueError(f"{name}: rows must be contiguous and evenly spaced")
         return ld
 
@@ -435,9 +484,13 @@ class DraftVerifier:
         D.B = B
         D.ld_draft = self._rows(draft_probs, "draft_probs", B, n)
         D.ld_target = self._rows(target_probs, "target_probs", B, n + 1)
-        tokens, accepted = self._tokens[:B], self._accepted[:B]
-        N.check(N.lib().moe_verify_draft(draft_tokens.data_ptr(), _p(draft_len), draft_probs.data_ptr(),
-                                         target_probs.data_ptr(), u_accept.data_ptr(), u_sample.data_ptr(),
-                                         ctypes.byref(D), tokens.data_ptr(), accepted.data_ptr(), _s(stream)),
-                "moe_verify_draft")
+        out = self._views.get(B)
+        if out is None:
+            out = self._views[B] = (self._tokens[:B], self._accepted[:B])
+        tokens, accepted = out
+        st = self._call(draft_tokens.data_ptr(), None if draft_len is None else draft_len.data_ptr(),
+                        draft_probs.data_ptr(), target_probs.data_ptr(), u_accept.data_ptr(), u_sample.data_ptr(),
+                        self._dims_ref, tokens.data_ptr(), accepted.data_ptr(), _stream(stream, self._device))
+        if st:
+            N.check(st, "moe_verify_draft")
         return tokens, accepted

@@ -94,7 +94,7 @@ __global__ void __launch_bounds__(256) linear_dz_kernel(const T* __restrict__ dy
     }
   };
   if (cols > 0) {
-#pragma unroll 4
+#pragma unroll(ACT == MOE_ACT_NONE ? 8 : 4)
     for (int64_t m = (int64_t)blockIdx.y * 8 + warp; m < M; m += (int64_t)gridDim.y * 8) {
       float v[8], zv[8];
       load(dy + m * ld_dy + n, v);

@@ -498,22 +498,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   }
 }
 
-// Columns of a tile and the divided tiles, by the time that the slowest pair takes (us): a K block
-// of a 256 x TN tile takes the longer of its MMAs (kMma at 256 columns) and its loads (16 KB of A,
-// 64 TN bytes of B at kLoad KB/us for an SM); a launch kStart, the last tile's way out kOut at 256
-// columns; a tile's division kJoin (its fp32 parts go through L2) and kPart more for each part.
-// Whole rounds of narrower tiles beat divided ones of 256 where some width fits the pairs:
-// 4096 x 2816 x 2048 in 208 columns, 2816 x 2048 x 4096 in 160; with few tiles and a long K only a
-// division uses the pairs. Returns the pairs to launch.
-constexpr double kMma = 0.335, kLoad = 105.0, kStart = 3.0, kOut = 4.0, kJoin = 9.0, kPart = 1.5;
+// Columns of a tile and the divided tiles, by the time that the slowest pair takes (us). Measured: a
+// K block of a 256 x TN tile takes 0.318 / 0.283 / 0.251 / 0.219 / 0.194 / 0.182 / 0.171 us at TN =
+// 256 / 224 / 192 / 160 / 128 / 96 / 64 (block_us); a launch kStart; the last tile's way out kOut at
+// 256 columns; the division of tiles kJoin at 256 columns (their fp32 parts go through L2) and
+// kPart for each part of a tile. Whole rounds of narrower tiles beat divided ones of 256 where some
+// width fits the pairs (4096 x 2816 x 2048: 32 us in 160 or 224 columns, 34 in 256, 37 divided);
+// 8192 x 2048 x 7680 is divided (141 us, 157 whole); with few tiles and a long K only a division
+// uses the pairs.
+constexpr double kStart = 4.5, kOut = 3.0, kJoin = 4.0, kPart = 1.5;
+inline double block_us(int tn) {
+  const double wide = 0.0625 + 0.001 * tn, narrow = 0.17 + 0.0004 * (tn - 64);
+  return wide > narrow ? wide : narrow;
+}
 
 int plan(PairGemm& g, int pairs) {
   double best = 1e30;
   int used = pairs;
   for (int tn = 256; tn >= 32; tn -= 32) {
     const int64_t tiles = (int64_t)g.tiles_m * ((g.No + tn - 1) / tn);
-    const double mma = kMma * tn / 256, load = (16.0 + tn / 16.0) / kLoad;
-    const double block = mma > load ? mma : load, out = kOut * tn / 256;
+    const double block = block_us(tn), out = kOut * tn / 256;
     const int64_t rounds = (tiles + pairs - 1) / pairs;
     double cost = kStart + rounds * g.nkb * block + out;
     int sk_tiles = 0, sk_pairs = 0, use = (int)(tiles < pairs ? tiles : pairs);

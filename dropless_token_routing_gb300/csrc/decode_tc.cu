@@ -21,251 +21,23 @@
 
 #include <mutex>
 
-#include "stream.cuh"
+#include "decode_select.cuh"
 #include "trace.h"
 
 namespace moe {
 namespace {
 
-using namespace stream;
-
-constexpr int RT = 128;            // rows of W_r that a CTA takes at a time
-// tables behind the staged result: selected experts, and the tokens' selections
-constexpr int kSlots = kMaxE * 2;                       // uint16 expert of each slot
-constexpr int kIdx = kDecodeMaxT * kMaxK * 2;           // uint16 [T][k]
-constexpr int kGate = kDecodeMaxT * kMaxK * 4;          // fp32 [T][k]; first the bias
-static_assert(kGate >= kMaxE * 4, "the bias waits in the table of gates");
-constexpr int kExtra = kSlots + kIdx + kGate;
+using namespace decode;
 
 struct DecodeTc {
   CUtensorMap w13, w2, ws13, ws2, x, h, hs;
   DecodeArgs a;
-  int n_slab, slab;      // CTAs that take a slab of W_r, rows of each
+  Select s;
   uint32_t* header;      // error, epoch, leave count, counters (enum)
   uint32_t* flags;       // [kDecodeRuns][CTA]
   float* part;           // [kDecodeRuns][CTA][NT][128]
-  float* score_part;     // [T][n_slab][E]
-  uint64_t* chosen;      // [T][k] selections
   __nv_bfloat16 *hbuf, *hsbuf;   // [slot][NT][f], [S][NT][f_s]
 };
-
-enum Counter { SCORES = 3, ROWS };   // words of the header
-// A selection is one 64-bit word: gate (32 bits), expert (kTagShift bits) and the launch's tag
-// (22 bits, from the epoch, never 0). The words are cleared before the tags start again.
-constexpr int kTagShift = 10;
-constexpr uint32_t kTagMask = (1u << (32 - kTagShift)) - 1;
-static_assert(kMaxE == 1 << kTagShift, "");
-
-struct Tables {
-  uint16_t* slots;
-  uint16_t* idx;
-  float* gate;
-};
-
-// ------------------------------------------------------------------ scores and selection
-__device__ __forceinline__ void gate_open() { asm volatile("bar.arrive 2, 288;" ::: "memory"); }
-__device__ __forceinline__ void gate_wait() { asm volatile("bar.sync 2, 288;" ::: "memory"); }
-
-// `n` floats global -> shared by the result warps, 16 bytes at a time where both ends allow.
-__device__ __forceinline__ void copy_floats(float* dst, const float* src, int n, bool vec) {
-  const int tid = threadIdx.x - 64;
-  if (vec) {
-#pragma unroll 4
-    for (int i = tid * 4; i < n; i += CT * 4) cp_async16(smem_u32(dst + i), src + i);
-  } else {
-#pragma unroll 4
-    for (int i = tid; i < n; i += CT)
-      asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst + i)), "l"(src + i) : "memory");
-  }
-}
-__device__ __forceinline__ void copies_landed() {
-  asm volatile("cp.async.wait_all;" ::: "memory");
-  ct_sync();
-}
-
-// Partial scores of this CTA's slab. xs: [rows][NT] floats, ws: `cap` floats of shared memory (stages of the ring that
-// the producer leaves alone until slab_free). The first part of W_r is asked for before anything
-// else: behind the weight stream's loads it would wait for all of those, so the producer starts
-// once it is on its way (gate_open). W_r goes through shared memory, not registers: the loop
-// stays a few instructions long (unrolled over 64 register loads it took 8 us, most of it
-// instruction fetches).
-template <int NT>
-__device__ __forceinline__ void partial_scores(const DecodeTc& p, int cta, float* xs, float* ws, int cap) {
-  constexpr int TS = 8;   // tokens at a time in registers
-  const moe_dims& D = p.a.dm;
-  const int T = (int)D.T, E = D.E, d = D.d, tid = threadIdx.x - 64;
-  const int d0 = cta * p.slab, d1 = min(d, d0 + p.slab);
-  const __nv_bfloat16* x = static_cast<const __nv_bfloat16*>(p.a.x);
-  const int at_once = min(RT, cap / E);   // rows of W_r
-  for (int r0 = d0; r0 < d1; r0 += at_once) {
-    const int n = min(at_once, d1 - r0);
-    copy_floats(ws, p.a.w_r + (int64_t)r0 * E, n * E, E % 4 == 0);
-    if (r0 == d0) gate_open();
-    for (int i = tid; i < n * NT; i += CT) {
-      const int t = i / n, r = i - t * n;
-      xs[r * NT + t] = t < T ? __bfloat162float(x[(int64_t)t * d + r0 + r]) : 0.f;
-    }
-    copies_landed();
-    // one expert and TS tokens at a time
-#pragma unroll 1
-    for (int i = tid; i < E * ((T + TS - 1) / TS); i += CT) {
-      const int e = i % E, t0 = i / E * TS;
-      float* out = p.score_part + ((int64_t)t0 * p.n_slab + cta) * E + e;
-      float s[TS];
-#pragma unroll
-      for (int t = 0; t < TS; ++t) s[t] = r0 > d0 && t0 + t < T ? __ldcg(out + (int64_t)t * p.n_slab * E) : 0.f;
-#pragma unroll 4
-      for (int r = 0; r < n; ++r) {
-        const float w = ws[r * E + e];
-        const float4* xr = reinterpret_cast<const float4*>(xs + r * NT + t0);
-#pragma unroll
-        for (int t = 0; t < TS; t += 4) {
-          const float4 v = xr[t / 4];
-          s[t] = fmaf(v.x, w, s[t]);
-          s[t + 1] = fmaf(v.y, w, s[t + 1]);
-          s[t + 2] = fmaf(v.z, w, s[t + 2]);
-          s[t + 3] = fmaf(v.w, w, s[t + 3]);
-        }
-      }
-#pragma unroll
-      for (int t = 0; t < TS; ++t)
-        if (t0 + t < T) __stcg(out + (int64_t)t * p.n_slab * E, s[t]);
-    }
-    ct_sync();
-  }
-}
-
-// Order-preserving map of a float to uint32, above 0 for every finite one; NaN is ranked last.
-__device__ __forceinline__ uint32_t rank_key(float x) {
-  if (!(x == x)) return 1u;
-  const uint32_t u = __float_as_uint(x + 0.f);   // -0 ranks as +0
-  return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
-}
-__device__ __forceinline__ float key_value(uint32_t key) {
-  return __uint_as_float((key & 0x80000000u) ? (key & 0x7fffffffu) : ~key);
-}
-
-// Token t's scores, ranked. Shared memory: buf [cap] floats (the ring, idle in a CTA with a token),
-// through which the partial rows come, all of them in flight; tmp [CT]; keys [E], a multiple of 4
-// readable; top [2 * kMaxK]; bias [E].
-// An expert's rank is the number of experts before it (larger key, or the same and a lower index),
-// which every thread counts for its own: no rounds over k. All loops are short on purpose: this is
-// code that a CTA runs once, and fetching it is what it costs.
-__device__ __forceinline__ void select_experts(const DecodeTc& p, int t, float* buf, int cap, float* tmp, uint32_t* keys,
-                                               uint32_t* top, const float* bias, uint32_t tag) {
-  const moe_dims& D = p.a.dm;
-  const int E = D.E, k = D.k, tid = threadIdx.x - 64;
-  const bool given = p.a.logits_in != nullptr;
-  const int rows = given ? 1 : p.n_slab, at_once = cap / E;
-  const float* in = given ? p.a.logits_in + (int64_t)t * E : p.score_part + (int64_t)t * rows * E;
-  for (int i = tid; i < ((E + 3) & ~3); i += CT) keys[i] = 0u;
-  for (int r0 = 0; r0 < rows; r0 += at_once) {
-    const int n = min(at_once, rows - r0);
-    copy_floats(buf, in + (int64_t)r0 * E, n * E, E % 4 == 0);
-    copies_landed();
-#pragma unroll 1
-    for (int e0 = 0; e0 < E; e0 += CT) {
-      // ng threads share a column, each summing every ng-th row
-      const int cols = min(E - e0, CT), ng = CT / cols, g = tid / cols, c = e0 + tid % cols;
-      float s = 0.f;
-      if (g < ng) {
-#pragma unroll 4
-        for (int r = g; r < n; r += ng) s += buf[r * E + c];
-      }
-      tmp[tid] = s;
-      ct_sync();
-      if (tid < cols) {
-        for (int i = cols; i < ng * cols; i += cols) s += tmp[tid + i];
-        if (r0 > 0) s += __uint_as_float(keys[c]);   // the sum so far
-        if (r0 + n < rows) keys[c] = __float_as_uint(s);
-        else keys[c] = rank_key(p.a.bias != nullptr ? s + bias[c] : s);   // one fp32 rounding
-      }
-      ct_sync();
-    }
-  }
-#pragma unroll 1
-  for (int e = tid; e < E; e += CT) {
-    const uint32_t key = keys[e];
-    int rank = 0;
-#pragma unroll 2
-    for (int i = 0; i < E; i += 4) {   // keys past E are 0, below every other
-      const uint4 v = *reinterpret_cast<const uint4*>(keys + i);
-      rank += (v.x > key || (v.x == key && i < e)) + (v.y > key || (v.y == key && i + 1 < e)) +
-              (v.z > key || (v.z == key && i + 2 < e)) + (v.w > key || (v.w == key && i + 3 < e));
-    }
-    if (rank < k) {
-      top[rank] = e;
-      top[kMaxK + rank] = key;
-    }
-  }
-  ct_sync();
-  if (tid < 32) {
-    const float v = key_value(top[kMaxK + min(tid, k - 1)]);
-    const float largest = __shfl_sync(0xffffffffu, v, 0);   // by all lanes
-    float w = tid < k ? expf(v - largest) : 0.f, sum = w;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    w /= sum;
-    if (tid < k) {
-      const int64_t q = (int64_t)t * k + tid;
-      const int32_t e = (int32_t)top[tid];
-      // expert, gate and the launch in one word: whoever reads it needs no other signal
-      asm volatile("st.relaxed.gpu.global.u64 [%0], %1;" ::"l"(p.chosen + q),
-                   "l"((uint64_t)(tag << kTagShift | (uint32_t)e) << 32 | __float_as_uint(w))
-                   : "memory");
-      if (p.a.idx_out != nullptr) p.a.idx_out[q] = e;
-      if (p.a.gate_out != nullptr) p.a.gate_out[q] = w;
-    }
-  }
-}
-
-// The selected experts in ascending order, and the tokens' selections, once they are all there
-// (their words carry this launch's tag). Returns their number, 0 when the wait ran out.
-// bits: kMaxE / 32 words, count: one int of shared memory.
-__device__ __forceinline__ int build_tables(const DecodeTc& p, const Tables& tb, uint32_t tag, uint32_t* bits, int* count,
-                                            volatile int* abort, int* err) {
-  const moe_dims& D = p.a.dm;
-  const int n = (int)D.T * D.k, tid = threadIdx.x - 64;
-  if (tid < kMaxE / 32) bits[tid] = 0u;
-  ct_sync();
-  const uint64_t t0 = global_ns();
-  bool ok = true;
-#pragma unroll 1
-  for (int i = tid; ok && i < n; i += CT) {
-    uint64_t w;
-    while (true) {
-      asm volatile("ld.relaxed.gpu.global.u64 %0, [%1];" : "=l"(w) : "l"(p.chosen + i) : "memory");
-      if ((uint32_t)(w >> (32 + kTagShift)) == tag) break;
-      if (*abort || global_ns() - t0 > kWaitLimitNs) {
-        if (!*abort) record_error(err, MOE_ERR_DEVICE_TIMEOUT);
-        *abort = 1;
-        ok = false;
-        break;
-      }
-    }
-    if (!ok) break;
-    const int e = (int)(w >> 32) & (kMaxE - 1);
-    tb.idx[i] = (uint16_t)e;
-    tb.gate[i] = __uint_as_float((uint32_t)w);
-    atomicOr(bits + (e >> 5), 1u << (e & 31));
-  }
-  if (ct_any(!ok)) return 0;
-  if (tid < 32) {   // lane i: word i of the bitmap
-    const uint32_t w = bits[tid];
-    int c = __popc(w);
-    int inc = c;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int v = __shfl_up_sync(0xffffffffu, inc, o);
-      if (tid >= o) inc += v;
-    }
-    int at = inc - c;
-    for (uint32_t m = w; m != 0u; m &= m - 1u) tb.slots[at++] = (uint16_t)(tid * 32 + __ffs((int)m) - 1);
-    if (tid == 31) *count = inc;
-  }
-  ct_sync();
-  return *count;
-}
 
 // ------------------------------------------------------------------ the runs
 // In the order in which every CTA works on them. (Dividing the output's K into a first part that
@@ -407,7 +179,7 @@ __global__ void __launch_bounds__(THREADS, 1) decode_kernel(const __grid_constan
   const uint32_t epoch = *reinterpret_cast<volatile uint32_t*>(p.header + 1) + 1;
 
   const uint32_t tag = 1 + epoch % kTagMask;
-  const bool scores = p.a.logits_in == nullptr && cta < p.n_slab;
+  const bool scores = p.a.logits_in == nullptr && cta < p.s.n_slab;
   Plan plan(D, cta, n_cta);
 
   if (warp == 0) {
@@ -522,7 +294,7 @@ __global__ void __launch_bounds__(THREADS, 1) decode_kernel(const __grid_constan
     // come from HBM behind the stream)
     if (cta < T && p.a.bias != nullptr) copy_floats(tb.gate, p.a.bias, D.E, D.E % 4 == 0);
     if (scores) {
-      partial_scores<NT>(p, cta, acc, reinterpret_cast<float*>(smem + SLAB0 * STAGE), (STAGES - SLAB0) * STAGE / 4);
+      partial_scores<NT, __nv_bfloat16, true>(p.s, cta, acc, reinterpret_cast<float*>(smem + SLAB0 * STAGE), (STAGES - SLAB0) * STAGE / 4);
       __threadfence();
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // the stages become the TMA's again
       ct_sync();
@@ -533,11 +305,11 @@ __global__ void __launch_bounds__(THREADS, 1) decode_kernel(const __grid_constan
     }
     if (cta < T) {
       if (p.a.logits_in == nullptr) {
-        if (threadIdx.x == 64) ok = word_wait(p.header + SCORES, (uint32_t)p.n_slab, &b.abort, err);
+        if (threadIdx.x == 64) ok = word_wait(p.header + SCORES, (uint32_t)p.s.n_slab, &b.abort, err);
         ok = !ct_any(!ok);
       }
       if (ok)
-        select_experts(p, cta, reinterpret_cast<float*>(smem), STAGES * STAGE / 4, acc + kMaxE,
+        select_experts(p.s, cta, reinterpret_cast<float*>(smem), STAGES * STAGE / 4, acc + kMaxE,
                        reinterpret_cast<uint32_t*>(acc), s_top, tb.gate, tag);
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // the ring held partial scores
       ct_sync();
@@ -546,7 +318,7 @@ __global__ void __launch_bounds__(THREADS, 1) decode_kernel(const __grid_constan
 #pragma unroll 1
     for (int r = D.S > 0 ? SHARED : HIDDEN; ok && r <= OUTPUT; ++r) {
       if (r == HIDDEN) {
-        const int active = build_tables(p, tb, tag, s_bits, &s_active, &b.abort, err);
+        const int active = build_tables(p.s, tb, tag, s_bits, &s_active, &b.abort, err);
         ok = active > 0;
         if (!ok) break;
         plan.select(active);
@@ -567,7 +339,7 @@ __global__ void __launch_bounds__(THREADS, 1) decode_kernel(const __grid_constan
   teardown<NT>(b, warp);
   // the tags start again after this launch: no word may still hold one
   if (leave(p.header, epoch) && tag == kTagMask)
-    for (int i = 0; i < kDecodeMaxT * kMaxK; ++i) p.chosen[i] = 0;
+    for (int i = 0; i < kDecodeMaxT * kMaxK; ++i) p.s.chosen[i] = 0;
 }
 
 template <int NT>
@@ -611,15 +383,10 @@ int launch_decode_tc(const DecodeArgs& a, int num_sms, cudaStream_t st) {
   DecodeTc p;
   memset(&p, 0, sizeof(p));
   p.a = a;
-  // slabs of at least 8 rows of W_r
-  p.slab = (D.d + num_sms - 1) / num_sms;
-  if (p.slab < 8) p.slab = 8;
-  p.n_slab = (D.d + p.slab - 1) / p.slab;
+  p.s = select_args(a, num_sms);
   p.header = reinterpret_cast<uint32_t*>(a.ws);
   p.flags = p.header + 256;
   p.part = reinterpret_cast<float*>(a.ws + a.L.part);
-  p.score_part = reinterpret_cast<float*>(a.ws + a.L.score_part);
-  p.chosen = reinterpret_cast<uint64_t*>(a.ws + kOpFlags);
   p.hbuf = reinterpret_cast<__nv_bfloat16*>(a.ws + a.L.h);
   p.hsbuf = reinterpret_cast<__nv_bfloat16*>(a.ws + a.L.hs);
   const int64_t slots = decode_slots(D);

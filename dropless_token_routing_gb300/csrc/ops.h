@@ -18,15 +18,9 @@ constexpr int kMinStreamRun = 2;      // K blocks of a CTA's run
 // ------------------------------------------------------------------ decode
 constexpr int kDecodeRuns = 3;   // shared, hidden, output
 struct DecodeLayout {
-  // fp32 layers
-  size_t idx;        // [T][k] int32
-  size_t gate;       // [T][k] fp32
-  size_t logits;     // [T][E] fp32
-  size_t counts;     // [E] int32
-  // bf16 layers
   size_t score_part; // [T][slabs][E] fp32 partial scores
-  size_t part;       // [kDecodeRuns][CTA][token columns][128] fp32 partial tiles
-  // hidden rows times their gates: fp32 [T*k][f] and [S*T][f_s]; bf16 [slot][token columns][f]
+  size_t part;       // bf16: [kDecodeRuns][CTA][token columns][128] fp32 partial tiles
+  // hidden rows times their gates: fp32 [slot][T][f] and [S][T][f_s]; bf16 [slot][token columns][f]
   // and [S][token columns][f_s]
   size_t h, hs;
   size_t total;

@@ -16,14 +16,11 @@ DecodeLayout decode_layout(const moe_dims& d) {
   const size_t T = (size_t)d.T, E = (size_t)d.E;
   const bool tc = d.dtype == MOE_BF16;
   const size_t nt = tc ? decode_token_columns(d.T) : 0;
-  L.idx = take(tc ? 0 : 4 * T * d.k);
-  L.gate = take(tc ? 0 : 4 * T * d.k);
-  L.logits = take(tc ? 0 : 4 * T * E);
-  L.counts = take(tc ? 0 : 4 * E);
-  L.score_part = take(tc ? 4 * T * kMaxStreamCtas * E : 0);
+  L.score_part = take(4 * T * kMaxStreamCtas * E);
   L.part = take(tc ? 4 * (size_t)kDecodeRuns * kMaxStreamCtas * nt * 128 : 0);
-  L.h = take(tc ? 2 * (size_t)decode_slots(d) * nt * d.f : 4 * T * d.k * d.f);
-  L.hs = take(tc ? 2 * (size_t)d.S * nt * d.f_s : 4 * T * d.S * d.f_s);
+  const size_t rows = tc ? 2 * nt : 4 * T;   // bytes of a column of hidden rows
+  L.h = take(rows * (size_t)decode_slots(d) * d.f);
+  L.hs = take(rows * (size_t)d.S * d.f_s);
   L.total = o;
   return L;
 }

@@ -111,7 +111,8 @@ static __device__ __noinline__ bool flags_wait(const uint32_t* p, uint32_t value
   return true;
 }
 
-// Barrier of the CT threads that take results out.
+// Index among the CT threads that take results out (a block's last ones), and their barrier.
+__device__ __forceinline__ int ct_tid() { return (int)threadIdx.x - (int)(blockDim.x - CT); }
 __device__ __forceinline__ void ct_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
 // The same, and true in all of them if `bad` is true in any.
 __device__ __forceinline__ bool ct_any(bool bad) {

@@ -78,7 +78,16 @@ template <int ACT> __device__ __forceinline__ float act_slope_fast(float z) {
   return act_slope<ACT>(z);
 }
 
-// The activation by a value that is the same in the whole launch.
+// The activations by a value that is the same in the whole launch.
+__device__ __forceinline__ float act_any(int act, float z) {
+  switch (act) {
+    case MOE_ACT_RELU: return act_f<MOE_ACT_RELU>(z);
+    case MOE_ACT_SILU: return act_f<MOE_ACT_SILU>(z);
+    case MOE_ACT_GELU: return act_f<MOE_ACT_GELU>(z);
+    case MOE_ACT_GELU_TANH: return act_f<MOE_ACT_GELU_TANH>(z);
+    default: return z;
+  }
+}
 __device__ __forceinline__ float act_any_fast(int act, float z) {
   switch (act) {
     case MOE_ACT_RELU: return act_fast<MOE_ACT_RELU>(z);

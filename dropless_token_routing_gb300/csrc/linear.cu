@@ -7,68 +7,167 @@
 namespace moe {
 namespace {
 
-constexpr int GM = 64, GN = 64, GK = 16;
+constexpr int GM = 128, GN = 64, GK = 16, GT = 128;
 
-// One 64 x 64 tile of C = act(A B^T + bias) + res per block, 4 x 4 of it per thread. AK / BK:
-// k is the contiguous index of A / B (else the row is), so that the tile loads coalesce.
-template <typename T, int ACT, bool AK, bool BK>
-__global__ void __launch_bounds__(256) gemm_simt_kernel(const GemmArgs g) {
-  __shared__ float As[GK][GM + 4];
-  __shared__ float Bs[GK][GN + 4];
-  const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
+// bias, z, activation, residual of one element and its way out.
+template <typename T>
+__device__ __forceinline__ void finish_element(const GemmArgs& g, int64_t m, int n, float v) {
+  if (g.bias != nullptr) v += to_f32(static_cast<const T*>(g.bias)[n]);
+  if (g.z_out != nullptr) static_cast<T*>(g.z_out)[m * g.N + n] = from_f32<T>(v);
+  v = act_any(g.act, v);
+  if (g.res != nullptr) v += to_f32(static_cast<const T*>(g.res)[m * g.ld_res + n]);
+  static_cast<T*>(g.c)[m * g.ldc + n] = from_f32<T>(v);
+}
+
+// Two fp32 FMAs in one instruction (1024 x 1024 x 1024: 63 us, 68 with single ones).
+__device__ __forceinline__ uint64_t pair_of(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void fma_pair(uint64_t& d, uint64_t a, uint64_t b) {
+  asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(d) : "l"(a), "l"(b));
+}
+
+// A thread's share of an R x 16 operand tile: single elements, which any stride and alignment
+// allows. KC: k is the contiguous index (16 lanes along k, rows 8 apart), else the row is (64 lanes
+// along the rows, k two apart).
+template <typename T, bool KC, int R> struct Operand {
+  static constexpr int N = R * GK / GT, H = R / 64;   // elements; rows of a lane where rows are contiguous
+  const T* p;          // this thread's first element at the present k
+  int64_t rs, ks;
+  int row0, k;         // its first row in the tile, its first k in the block
+  int rows;            // rows of the tile that exist
+  __device__ Operand(const void* base, int64_t row, int64_t k0, int64_t rs_, int64_t ks_, int64_t total, int tid) {
+    row0 = KC ? tid / GK : tid % 64;
+    k = KC ? tid % GK : tid / 64;
+    rows = (int)(total - row < R ? total - row : R);
+    rs = rs_;
+    ks = ks_;
+    p = static_cast<const T*>(base) + (row + row0) * rs + (k0 + k) * ks;
+  }
+  __device__ __forceinline__ static int row_of(int i) { return KC ? 8 * i : i % H * 64; }
+  __device__ __forceinline__ static int k_of(int i) { return KC ? 0 : i / H * 2; }
+  // left: k's of this block that exist
+  __device__ __forceinline__ void load(float (&r)[N], int64_t left) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const bool in = row0 + row_of(i) < rows && k + k_of(i) < left;
+      r[i] = in ? to_f32(p[row_of(i) * rs + k_of(i) * ks]) : 0.f;
+    }
+    p += GK * ks;
+  }
+  __device__ __forceinline__ void stage(float (*s)[R + 4], const float (&r)[N]) const {
+#pragma unroll
+    for (int i = 0; i < N; ++i) s[k + k_of(i)][row0 + row_of(i)] = r[i];
+  }
+};
+
+// One 128 x 64 tile of A B^T per block (or a share of its K: blockIdx.z of gridDim.z, into fp32
+// partial sums), 8 x 8 of it per thread in quarters of 4 x 4: 4 shared-memory vectors per 64 FMAs
+// (with 8 x 4 the shared memory was the limit). The next 16 of K are loaded into registers while
+// the present ones are multiplied.
+template <typename T, bool AK, bool BK, bool SPLIT>
+__global__ void __launch_bounds__(GT) gemm_simt_kernel(const GemmArgs g, float* part) {
+  __shared__ __align__(16) float As[2][GK][GM + 4];
+  __shared__ __align__(16) float Bs[2][GK][GN + 4];
+  const int tid = threadIdx.x, ty = tid >> 3, tx = tid & 7;
   const int64_t m0 = (int64_t)blockIdx.x * GM;
   const int n0 = blockIdx.y * GN;
-  const T* A = static_cast<const T*>(g.a);
-  const T* B = static_cast<const T*>(g.b);
-  float acc[4][4] = {};
-  for (int64_t k0 = 0; k0 < g.K; k0 += GK) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int s = tid + 256 * i;
-      const int ar = AK ? s / GK : s % GM, ac = AK ? s % GK : s / GM;
-      const int br = BK ? s / GK : s % GN, bc = BK ? s % GK : s / GN;
-      As[ac][ar] = m0 + ar < g.M && k0 + ac < g.K ? to_f32(A[(m0 + ar) * g.am + (k0 + ac) * g.ak]) : 0.f;
-      Bs[bc][br] = n0 + br < g.N && k0 + bc < g.K ? to_f32(B[(n0 + br) * g.bn + (k0 + bc) * g.bk]) : 0.f;
+  int64_t k_lo = 0, k_hi = g.K;
+  if (SPLIT) {
+    const int64_t per = ((g.K + gridDim.z - 1) / gridDim.z + GK - 1) / GK * GK;
+    k_lo = per * blockIdx.z < g.K ? per * blockIdx.z : g.K;
+    k_hi = k_lo + per < g.K ? k_lo + per : g.K;
+  }
+  Operand<T, AK, GM> A(g.a, m0, k_lo, g.am, g.ak, g.M, tid);
+  Operand<T, BK, GN> B(g.b, n0, k_lo, g.bn, g.bk, g.N, tid);
+  float ra[A.N], rb[B.N];
+  uint64_t acc[8][4] = {};   // pairs of columns
+  A.load(ra, k_hi - k_lo);
+  B.load(rb, k_hi - k_lo);
+  A.stage(As[0], ra);
+  B.stage(Bs[0], rb);
+  __syncthreads();
+  int buf = 0;
+  for (int64_t k0 = k_lo; k0 < k_hi; k0 += GK, buf ^= 1) {
+    const int64_t left = k_hi - k0 - GK;
+    if (left > 0) {
+      A.load(ra, left);
+      B.load(rb, left);
     }
-    __syncthreads();
 #pragma unroll
     for (int k = 0; k < GK; ++k) {
-      const float4 a4 = *reinterpret_cast<const float4*>(&As[k][ty * 4]);
-      const float4 b4 = *reinterpret_cast<const float4*>(&Bs[k][tx * 4]);
-      const float av[4] = {a4.x, a4.y, a4.z, a4.w}, bv[4] = {b4.x, b4.y, b4.z, b4.w};
+      float av[8];
+      alignas(16) float bv[8];
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+      for (int h = 0; h < 2; ++h) {
+        *reinterpret_cast<float4*>(av + 4 * h) = *reinterpret_cast<const float4*>(&As[buf][k][64 * h + ty * 4]);
+        *reinterpret_cast<float4*>(bv + 4 * h) = *reinterpret_cast<const float4*>(&Bs[buf][k][32 * h + tx * 4]);
+      }
+      const uint64_t* b2 = reinterpret_cast<const uint64_t*>(bv);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(av[i], bv[j], acc[i][j]);
+      for (int i = 0; i < 8; ++i) {
+        const uint64_t a2 = pair_of(av[i], av[i]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) fma_pair(acc[i][j], a2, b2[j]);
+      }
     }
-    __syncthreads();
+    if (left > 0) {   // the other buffer was last read before the previous barrier
+      A.stage(As[buf ^ 1], ra);
+      B.stage(Bs[buf ^ 1], rb);
+      __syncthreads();
+    }
   }
-  const T* bias = static_cast<const T*>(g.bias);
-  const T* res = static_cast<const T*>(g.res);
-  T* z = static_cast<T*>(g.z_out);
-  T* c = static_cast<T*>(g.c);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int64_t m = m0 + ty * 4 + i;
+  for (int i = 0; i < 8; ++i) {
+    const int64_t m = m0 + i / 4 * 64 + ty * 4 + i % 4;
     if (m >= g.M) continue;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int n = n0 + tx * 4 + j;
+    for (int j = 0; j < 8; ++j) {
+      const int n = n0 + j / 4 * 32 + tx * 4 + j % 4;
       if (n >= g.N) continue;
-      const float v = acc[i][j] + (bias != nullptr ? to_f32(bias[n]) : 0.f);
-      if (z != nullptr) z[m * g.N + n] = from_f32<T>(v);
-      c[m * g.ldc + n] = from_f32<T>(act_f<ACT>(v) + (res != nullptr ? to_f32(res[m * g.ld_res + n]) : 0.f));
+      const float v = __uint_as_float((uint32_t)(acc[i][j / 2] >> (j % 2 * 32)));
+      if (SPLIT) part[((int64_t)blockIdx.z * g.M + m) * g.N + n] = v;
+      else finish_element<T>(g, m, n, v);
     }
   }
 }
 
-template <typename T, int ACT>
-void gemm_simt(const GemmArgs& g, cudaStream_t st) {
-  const dim3 grid((unsigned)((g.M + GM - 1) / GM), (unsigned)((g.N + GN - 1) / GN));
-  if (g.ak == 1 && g.bk == 1) gemm_simt_kernel<T, ACT, true, true><<<grid, 256, 0, st>>>(g);
-  else if (g.ak == 1) gemm_simt_kernel<T, ACT, true, false><<<grid, 256, 0, st>>>(g);
-  else if (g.bk == 1) gemm_simt_kernel<T, ACT, false, true><<<grid, 256, 0, st>>>(g);
-  else gemm_simt_kernel<T, ACT, false, false><<<grid, 256, 0, st>>>(g);
+// The shares of a divided K, added in order.
+template <typename T>
+__global__ void __launch_bounds__(256) gemm_join_kernel(const GemmArgs g, const float* __restrict__ part, int split) {
+  const int64_t all = g.M * g.N;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < all; i += (int64_t)gridDim.x * 256) {
+    float v = 0.f;
+    for (int s = 0; s < split; ++s) v += part[s * all + i];
+    finish_element<T>(g, i / g.N, (int)(i % g.N), v);
+  }
+}
+
+// The layouts of the layer's products: forward (both operands along k), dX, dW.
+template <typename T, bool SPLIT>
+void gemm_layouts(const GemmArgs& g, float* part, const dim3& grid, cudaStream_t st) {
+  if (g.ak == 1 && g.bk == 1) gemm_simt_kernel<T, true, true, SPLIT><<<grid, GT, 0, st>>>(g, part);
+  else if (g.ak == 1) gemm_simt_kernel<T, true, false, SPLIT><<<grid, GT, 0, st>>>(g, part);
+  else gemm_simt_kernel<T, false, false, SPLIT><<<grid, GT, 0, st>>>(g, part);
+}
+
+template <typename T>
+void gemm_simt(const GemmArgs& g, float* part, int num_sms, cudaStream_t st) {
+  const int64_t tm = (g.M + GM - 1) / GM, tn = (g.N + GN - 1) / GN, tiles = tm * tn;
+  // One block leaves an SM's FMA pipes waiting for its loads; K is divided until there are about
+  // kBlocks on each, with at least 64 of K.
+  int64_t split = (int64_t)kBlocks * (num_sms < kMaxStreamCtas ? num_sms : kMaxStreamCtas) / tiles;
+  if (split > g.K / 64) split = g.K / 64;
+  if (split > kMaxSplit) split = kMaxSplit;
+  if (split <= 1) {
+    gemm_layouts<T, false>(g, nullptr, dim3((unsigned)tm, (unsigned)tn), st);
+    return;
+  }
+  gemm_layouts<T, true>(g, part, dim3((unsigned)tm, (unsigned)tn, (unsigned)split), st);
+  const int64_t blocks = (g.M * g.N + 1023) / 1024;
+  gemm_join_kernel<T><<<(unsigned)(blocks < 8 * num_sms ? blocks : 8 * num_sms), 256, 0, st>>>(g, part, (int)split);
 }
 
 // dz = dy * act'(z), and its column sums. A block takes 256 columns and every gridDim.y-th group of
@@ -175,17 +274,10 @@ cudaError_t linear_dz(const void* dy, int64_t ld_dy, const void* z, int act, int
 
 }  // namespace
 
-cudaError_t launch_gemm_simt(const GemmArgs& g, cudaStream_t st) {
+cudaError_t launch_gemm_simt(const GemmArgs& g, float* part, int num_sms, cudaStream_t st) {
   TraceScope ts(TP_LINEAR, st);
-  if (g.dtype == MOE_F32) {
-#define MOE_G(A) gemm_simt<float, A>(g, st)
-    MOE_ACT_SWITCH(g.act, MOE_G)
-#undef MOE_G
-  } else {
-#define MOE_G(A) gemm_simt<__nv_bfloat16, A>(g, st)
-    MOE_ACT_SWITCH(g.act, MOE_G)
-#undef MOE_G
-  }
+  if (g.dtype == MOE_F32) gemm_simt<float>(g, part, num_sms, st);
+  else gemm_simt<__nv_bfloat16>(g, part, num_sms, st);
   return cudaGetLastError();
 }
 

@@ -48,7 +48,7 @@ int launch_decode_simt(const DecodeArgs& a, int num_sms, cudaStream_t st);
 struct LinearLayout {
   size_t dz;         // [M][ld_dz] the pre-activation's gradient, dims->dtype
   size_t db_part;    // [kDbSplit][N] fp32
-  size_t part;       // partial tiles of the products on CTA pairs (bf16)
+  size_t part;       // partial sums of products with a divided K
   int64_t ld_dz;
   size_t total;
 };
@@ -74,7 +74,9 @@ struct GemmArgs {
   int64_t ldc;
   int dtype;
 };
-cudaError_t launch_gemm_simt(const GemmArgs& g, cudaStream_t st);
+constexpr int kMaxSplit = 16, kBlocks = 3;   // of the FMA products: shares of a divided K, blocks for an SM
+inline size_t gemm_simt_part_bytes() { return (size_t)kBlocks * kMaxStreamCtas * 128 * 64 * 4; }
+cudaError_t launch_gemm_simt(const GemmArgs& g, float* part, int num_sms, cudaStream_t st);
 // The bf16 products on CTA pairs. LINEAR_FWD: A and B K-major; DX: B MN-major; DW: both. Base
 // pointers 16-byte aligned, row strides multiples of 8 elements.
 enum LinearKind { LINEAR_FWD = 0, LINEAR_DX, LINEAR_DW };

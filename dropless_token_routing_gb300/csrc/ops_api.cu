@@ -31,7 +31,8 @@ LinearLayout linear_layout(const moe_linear_dims& d) {
   L.dz = kOpHeader;
   L.db_part = L.dz + round256((size_t)d.M * L.ld_dz * elt_bytes(d.dtype));
   L.part = L.db_part + round256(4 * (size_t)kDbSplit * d.N);
-  L.total = L.part + (d.dtype == MOE_BF16 ? linear_pair_part_bytes() : 0);
+  const size_t simt = gemm_simt_part_bytes(), pair = d.dtype == MOE_BF16 ? linear_pair_part_bytes() : 0;
+  L.total = L.part + (simt > pair ? simt : pair);
   return L;
 }
 
@@ -93,7 +94,7 @@ int run_gemm(int kind, const GemmArgs& g, uint8_t* ws, const LinearLayout& L, in
     if (kind == LINEAR_FWD && g.M <= kStreamRows) return launch_linear_stream(g, ws, sms, st);
     return launch_linear_pair(kind, g, ws, L.part, sms, st);
   }
-  return launch_gemm_simt(g, st) == cudaSuccess ? MOE_OK : MOE_ERR_LAUNCH;
+  return launch_gemm_simt(g, reinterpret_cast<float*>(ws + L.part), sms, st) == cudaSuccess ? MOE_OK : MOE_ERR_LAUNCH;
 }
 
 }  // namespace

@@ -1,6 +1,7 @@
 // The linear layer on the FMA pipes: products of any type, size, stride and alignment, and the
 // elementwise half of its backward.
 #include "act.cuh"
+#include "launch.cuh"
 #include "ops.h"
 #include "trace.h"
 
@@ -72,6 +73,7 @@ __global__ void __launch_bounds__(GT) gemm_simt_kernel(const GemmArgs g, float* 
   __shared__ __align__(16) float As[2][GK][GM + 4];
   __shared__ __align__(16) float Bs[2][GK][GN + 4];
   const int tid = threadIdx.x, ty = tid >> 3, tx = tid & 7;
+  pdl_wait();
   const int64_t m0 = (int64_t)blockIdx.x * GM;
   const int n0 = blockIdx.y * GN;
   int64_t k_lo = 0, k_hi = g.K;
@@ -119,6 +121,7 @@ __global__ void __launch_bounds__(GT) gemm_simt_kernel(const GemmArgs g, float* 
       __syncthreads();
     }
   }
+  pdl_start();   // (earlier, the next kernel's blocks slow these down: 115 -> 118 us for a step of three)
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const int64_t m = m0 + i / 4 * 64 + ty * 4 + i % 4;
@@ -138,6 +141,8 @@ __global__ void __launch_bounds__(GT) gemm_simt_kernel(const GemmArgs g, float* 
 template <typename T>
 __global__ void __launch_bounds__(256) gemm_join_kernel(const GemmArgs g, const float* __restrict__ part, int split) {
   const int64_t all = g.M * g.N;
+  pdl_start();
+  pdl_wait();
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < all; i += (int64_t)gridDim.x * 256) {
     float v = 0.f;
     for (int s = 0; s < split; ++s) v += part[s * all + i];
@@ -148,9 +153,9 @@ __global__ void __launch_bounds__(256) gemm_join_kernel(const GemmArgs g, const 
 // The layouts of the layer's products: forward (both operands along k), dX, dW.
 template <typename T, bool SPLIT>
 void gemm_layouts(const GemmArgs& g, float* part, const dim3& grid, cudaStream_t st) {
-  if (g.ak == 1 && g.bk == 1) gemm_simt_kernel<T, true, true, SPLIT><<<grid, GT, 0, st>>>(g, part);
-  else if (g.ak == 1) gemm_simt_kernel<T, true, false, SPLIT><<<grid, GT, 0, st>>>(g, part);
-  else gemm_simt_kernel<T, false, false, SPLIT><<<grid, GT, 0, st>>>(g, part);
+  if (g.ak == 1 && g.bk == 1) launch_pdl(gemm_simt_kernel<T, true, true, SPLIT>, grid, GT, 0, 1, st, g, part);
+  else if (g.ak == 1) launch_pdl(gemm_simt_kernel<T, true, false, SPLIT>, grid, GT, 0, 1, st, g, part);
+  else launch_pdl(gemm_simt_kernel<T, false, false, SPLIT>, grid, GT, 0, 1, st, g, part);
 }
 
 template <typename T>
@@ -167,67 +172,85 @@ void gemm_simt(const GemmArgs& g, float* part, int num_sms, cudaStream_t st) {
   }
   gemm_layouts<T, true>(g, part, dim3((unsigned)tm, (unsigned)tn, (unsigned)split), st);
   const int64_t blocks = (g.M * g.N + 1023) / 1024;
-  gemm_join_kernel<T><<<(unsigned)(blocks < 8 * num_sms ? blocks : 8 * num_sms), 256, 0, st>>>(g, part, (int)split);
+  launch_pdl(gemm_join_kernel<T>, dim3((unsigned)(blocks < 8 * num_sms ? blocks : 8 * num_sms)), 256, 0, 1, st, g, part, (int)split);
 }
 
-// dz = dy * act'(z), and its column sums. A block takes 256 columns and every gridDim.y-th group of
-// 8 rows: 8 columns per lane, a row per warp. Its warps' sums are added in order into one row of
-// `part` per block. (8-element vectors where the rows allow, else element by element.)
+// dz = dy * act'(z), and its column sums. 8 columns per thread, `lx` threads side by side (a row's
+// 16 lx bytes at a time, for the HBM's sake), 256 / lx rows; the block takes every gridDim.y-th such
+// group of rows and adds its rows' sums in order into one row of `part`. (8-element vectors where
+// the rows allow, else element by element.)
 template <typename T, int ACT, bool VEC>
 __global__ void __launch_bounds__(256) linear_dz_kernel(const T* __restrict__ dy, int64_t ld_dy,
                                                         const T* __restrict__ z, int64_t M, int N,
                                                         T* __restrict__ dz, int64_t ld_dz,
-                                                        float* __restrict__ part) {
-  __shared__ float s[8][256 + 8];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int n = blockIdx.x * 256 + lane * 8, cols = min(8, N - n);
+                                                        float* __restrict__ part, int lx) {
+  constexpr int U = 4;   // rows in flight
+  __shared__ float s[256 * 9];                     // 8 sums a thread, 9 apart
+  pdl_start();
+  pdl_wait();
+  const int ly = 256 / lx, c = threadIdx.x % lx, r = threadIdx.x / lx;
+  const int n = (blockIdx.x * lx + c) * 8, cols = min(8, N - n);
+  const int64_t step = (int64_t)gridDim.y * ly;
   float sum[8] = {};
-  auto load = [&](const T* p, float (&v)[8]) {
+  auto load = [&](const T* p, Vec8<T>& u, float (&v)[8]) {
     if (VEC) {
-      Vec8<T> u;
       u.load(p);
-      u.to_float(v);
     } else {
 #pragma unroll
       for (int i = 0; i < 8; ++i) v[i] = i < cols ? to_f32(p[i]) : 0.f;
     }
   };
   if (cols > 0) {
-#pragma unroll(ACT == MOE_ACT_NONE ? 8 : 4)
-    for (int64_t m = (int64_t)blockIdx.y * 8 + warp; m < M; m += (int64_t)gridDim.y * 8) {
-      float v[8], zv[8];
-      load(dy + m * ld_dy + n, v);
-      if constexpr (ACT != MOE_ACT_NONE) {
-        load(z + m * N + n, zv);
+    for (int64_t m0 = (int64_t)blockIdx.y * ly + r; m0 < M; m0 += U * step) {
+      Vec8<T> a[U], b[U];
+      float av[U][8], bv[U][8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] *= sizeof(T) == 2 ? act_slope_fast<ACT>(zv[i]) : act_slope<ACT>(zv[i]);
-      }
-      if (dz != nullptr) {
-        T* out = dz + m * ld_dz + n;
-        if (VEC) {
-          Vec8<T> u;
-          u.from_float(v);
-          u.store(out);
-        } else {
-#pragma unroll
-          for (int i = 0; i < 8; ++i)
-            if (i < cols) out[i] = from_f32<T>(v[i]);
+      for (int u = 0; u < U; ++u) {
+        const int64_t m = m0 + u * step;
+        if (m < M) {
+          load(dy + m * ld_dy + n, a[u], av[u]);
+          if (ACT != MOE_ACT_NONE) load(z + m * N + n, b[u], bv[u]);
         }
       }
 #pragma unroll
-      for (int i = 0; i < 8; ++i) sum[i] += v[i];
+      for (int u = 0; u < U; ++u) {
+        const int64_t m = m0 + u * step;
+        if (m >= M) break;
+        if (VEC) {
+          a[u].to_float(av[u]);
+          if (ACT != MOE_ACT_NONE) b[u].to_float(bv[u]);
+        }
+        if constexpr (ACT != MOE_ACT_NONE) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) av[u][i] *= sizeof(T) == 2 ? act_slope_fast<ACT>(bv[u][i]) : act_slope<ACT>(bv[u][i]);
+        }
+        if (dz != nullptr) {
+          T* out = dz + m * ld_dz + n;
+          if (VEC) {
+            Vec8<T> o;
+            o.from_float(av[u]);
+            o.store(out);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              if (i < cols) out[i] = from_f32<T>(av[u][i]);
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sum[i] += av[u][i];
+      }
     }
   }
   if (part == nullptr) return;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) s[warp][lane * 8 + i] = sum[i];
+  for (int i = 0; i < 8; ++i) s[threadIdx.x * 9 + i] = sum[i];
   __syncthreads();
-  const int c = blockIdx.x * 256 + threadIdx.x;
-  if (c < N) {
+  for (int i = threadIdx.x; i < lx * 8; i += 256) {
+    const int at = blockIdx.x * lx * 8 + i;
+    if (at >= N) break;
     float t = 0.f;
-#pragma unroll
-    for (int w = 0; w < 8; ++w) t += s[w][threadIdx.x];
-    part[(int64_t)blockIdx.y * N + c] = t;
+    for (int w = 0; w < ly; ++w) t += s[(w * lx + i / 8) * 9 + i % 8];
+    part[(int64_t)blockIdx.y * N + at] = t;
   }
 }
 
@@ -237,6 +260,8 @@ __global__ void __launch_bounds__(256) linear_db_kernel(const float* __restrict_
   __shared__ float s[8][33];
   const int col = threadIdx.x & 31, r = threadIdx.x >> 5, n = blockIdx.x * 32 + col;
   float t = 0.f;
+  pdl_start();
+  pdl_wait();
   if (n < N) {
 #pragma unroll 8
     for (int i = r; i < n_part; i += 8) t += part[(int64_t)i * N + n];
@@ -253,10 +278,12 @@ __global__ void __launch_bounds__(256) linear_db_kernel(const float* __restrict_
 template <typename T>
 cudaError_t linear_dz(const void* dy, int64_t ld_dy, const void* z, int act, int64_t M, int N, void* dz,
                       int64_t ld_dz, float* part, void* db, cudaStream_t st) {
-  // about 1200 blocks (8 on an SM), of at least 32 rows
-  const int nx = (N + 255) / 256;
-  int64_t split = (1216 + nx - 1) / nx;
-  if (split > (M + 31) / 32) split = (M + 31) / 32;
+  // About 600 blocks (4 on an SM), each with at least 8 rows for a thread. Sums alone in rows of 2 KB
+  // (8192 x 7680: 24 us, 31 in rows of 512 bytes and 1200 blocks); with a derivative to compute in
+  // rows of 512 (4096 x 2816 SiLU: 12.5 us, 13.9).
+  const int lx = act == MOE_ACT_NONE && N > 512 ? 128 : 32, ly = 256 / lx, nx = (N + lx * 8 - 1) / (lx * 8);
+  int64_t split = (608 + nx - 1) / nx;
+  if (split > (M + 8 * ly - 1) / (8 * ly)) split = (M + 8 * ly - 1) / (8 * ly);
   if (split > kDbSplit) split = kDbSplit;
   const dim3 grid(nx, (unsigned)split);
   const bool vec = N % 8 == 0 && ld_dy % 8 == 0;   // ld_dz is a multiple of 8
@@ -264,11 +291,11 @@ cudaError_t linear_dz(const void* dy, int64_t ld_dy, const void* z, int act, int
   T* dzp = static_cast<T*>(dz);
   float* pp = db != nullptr ? part : nullptr;
 #define MOE_DZ(A)                                                                                   \
-  if (vec) linear_dz_kernel<T, A, true><<<grid, 256, 0, st>>>(dyp, ld_dy, zp, M, N, dzp, ld_dz, pp); \
-  else linear_dz_kernel<T, A, false><<<grid, 256, 0, st>>>(dyp, ld_dy, zp, M, N, dzp, ld_dz, pp)
+  if (vec) launch_pdl(linear_dz_kernel<T, A, true>, grid, 256, 0, 1, st, dyp, ld_dy, zp, M, N, dzp, ld_dz, pp, lx); \
+  else launch_pdl(linear_dz_kernel<T, A, false>, grid, 256, 0, 1, st, dyp, ld_dy, zp, M, N, dzp, ld_dz, pp, lx)
   MOE_ACT_SWITCH(act, MOE_DZ)
 #undef MOE_DZ
-  if (db != nullptr) linear_db_kernel<T><<<(N + 31) / 32, 256, 0, st>>>(part, (int)split, N, static_cast<T*>(db));
+  if (db != nullptr) launch_pdl(linear_db_kernel<T>, dim3((N + 31) / 32), 256, 0, 1, st, part, (int)split, N, static_cast<T*>(db));
   return cudaGetLastError();
 }
 

@@ -26,6 +26,7 @@
 #include <mutex>
 
 #include "act.cuh"
+#include "launch.cuh"
 #include "ops.h"
 #include "tc_common.cuh"
 #include "trace.h"
@@ -285,6 +286,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t smem_base = smem_u32(smem);
 
+  pdl_start();
   if (threadIdx.x == 0) {
     abort_flag = 0;
     for (int s = 0; s < STAGES; ++s) {
@@ -309,6 +311,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   __syncthreads();
   cluster_sync_all();   // the peer's barriers are initialised before any remote arrival
   tc_fence_after();
+  pdl_wait();
   const uint32_t tmem_base = tmem_base_sh;
   const uint32_t epoch = *reinterpret_cast<volatile uint32_t*>(g.header + 1) + 1;
 
@@ -584,8 +587,7 @@ int launch_pair(PairGemm& g, const GemmArgs& a, int num_sms, cudaStream_t st) {
   g.stage_tx = 2 * (A_BYTES + (B_MN ? (g.tn > 128 ? 2 : 1) * SLAB : g.tn / 2 * BK * 2));
   if (!map_b(g, a)) return MOE_ERR_CUDA;
   TraceScope ts(TP_LINEAR, st);
-  kernel<<<2 * pairs, THREADS, SMEM_BYTES, st>>>(g);
-  return cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_LAUNCH;
+  return launch_pdl(kernel, dim3((unsigned)(2 * pairs)), THREADS, SMEM_BYTES, 1, st, g) == cudaSuccess ? MOE_OK : MOE_ERR_LAUNCH;
 }
 
 }  // namespace

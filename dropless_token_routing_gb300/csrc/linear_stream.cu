@@ -12,6 +12,7 @@
 #include <mutex>
 
 #include "act.cuh"
+#include "launch.cuh"
 #include "stream.cuh"
 #include "trace.h"
 
@@ -107,8 +108,10 @@ __global__ void __launch_bounds__(THREADS, 1) linear_stream_kernel(const __grid_
   rank = cluster_rank();
   const int tile0 = (int)cluster_id(), step = (int)cluster_count();
   const int k0 = (int)((int64_t)g.nkb * rank / cl), k1 = (int)((int64_t)g.nkb * (rank + 1) / cl);
+  pdl_start();
   setup<NT, STAGES>(b, warp, (int)cl);
   if (cl > 1) cluster_sync_all();   // the peers' barriers are initialised before any arrival
+  pdl_wait();
 
   if (warp == 0) {
     // the whole warp, one lane issuing (see tc_common.cuh)
@@ -266,19 +269,11 @@ int launch_nt(LinearStream& g, const GemmArgs& a, int num_sms, cudaStream_t st) 
   g.rows = best_rows;
   g.tiles = best_tiles;
   if (!map2d_ld(&g.w, a.b, a.K, a.N, a.bn, BK, best_rows) || !map2d_ld(&g.x, a.a, a.K, a.M, a.am, BK, NT)) return MOE_ERR_CUDA;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(best_clusters * best));
-  cfg.blockDim = dim3(THREADS);
-  cfg.dynamicSmemBytes = Cfg<NT>::smem(0);
-  cfg.stream = st;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = best;
-  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
   TraceScope ts(TP_LINEAR, st);
-  return cudaLaunchKernelEx(&cfg, linear_stream_kernel<NT>, g) == cudaSuccess ? MOE_OK : MOE_ERR_LAUNCH;
+  return launch_pdl(linear_stream_kernel<NT>, dim3((unsigned)(best_clusters * best)), THREADS, Cfg<NT>::smem(0), best, st, g) ==
+                 cudaSuccess
+             ? MOE_OK
+             : MOE_ERR_LAUNCH;
 }
 
 }  // namespace

@@ -6,6 +6,7 @@
 // multiples of 2^-40 and are summed as 64-bit integers, so the sums, and with them the drawn
 // token, do not depend on how the row is split over threads and CTAs.
 #include "common.cuh"
+#include "launch.cuh"
 #include "ops.h"
 #include "trace.h"
 
@@ -167,6 +168,8 @@ __global__ void __launch_bounds__(VT, 2) verify_kernel(const VerifyArgs v) {
   __shared__ long long s_sum[2][VW];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = ctarank(), nrank = nctarank();
+  pdl_start();
+  pdl_wait();
   const int64_t b = blockIdx.x / nrank;
   const int n = v.n, V = v.V;
   const T* q0 = static_cast<const T*>(v.q) + b * n * v.ld_q;
@@ -269,21 +272,12 @@ cudaError_t launch_verify(const VerifyArgs& v, int num_sms, cudaStream_t st) {
   // 16-byte loads: rows that start and lie on whole vectors
   const int64_t w = v.dtype == MOE_F32 ? 4 : 8;
   const bool vec = v.ld_p % w == 0 && v.ld_q % w == 0;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(v.B * c));
-  cfg.blockDim = dim3(VT);
-  cfg.stream = st;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = c;
-  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
+  const dim3 grid((unsigned)(v.B * c));
   TraceScope ts(TP_VERIFY, st);
   if (v.dtype == MOE_F32)
-    return vec ? cudaLaunchKernelEx(&cfg, verify_kernel<float, true>, v) : cudaLaunchKernelEx(&cfg, verify_kernel<float, false>, v);
-  return vec ? cudaLaunchKernelEx(&cfg, verify_kernel<__nv_bfloat16, true>, v)
-             : cudaLaunchKernelEx(&cfg, verify_kernel<__nv_bfloat16, false>, v);
+    return vec ? launch_pdl(verify_kernel<float, true>, grid, VT, 0, c, st, v) : launch_pdl(verify_kernel<float, false>, grid, VT, 0, c, st, v);
+  return vec ? launch_pdl(verify_kernel<__nv_bfloat16, true>, grid, VT, 0, c, st, v)
+             : launch_pdl(verify_kernel<__nv_bfloat16, false>, grid, VT, 0, c, st, v);
 }
 
 }  // namespace moe

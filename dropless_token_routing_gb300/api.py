@@ -418,7 +418,7 @@ class Linear:
             D.ld_y = self.N
         else:
             D.ld_y = _matrix(out, "out", self.dtype, M, self.N)
-        z = self._own("z", self.max_rows, self.N).data_ptr() if save and self.act != 0 else None
+        z = self._own("z", self.max_rows, self.N + 7 & ~7).data_ptr() if save and self.act != 0 else None
         self._x = x if save else None
         st = self._fwd(x.data_ptr(), self._w_ptr, self._b_ptr, None if residual is None else residual.data_ptr(),
                        self._dims_ref, z, out.data_ptr(), self.ws.ptr, self.ws.nbytes, _stream(stream, self._device))
@@ -441,7 +441,7 @@ class Linear:
             dw = self._view("dw", self.N, ld_w, self.N, self.K)
         if "db" in need and self.bias is not None:
             db = self._own("db", 1, self.N)[0]
-        z = self._own("z", self.max_rows, self.N).data_ptr() if self.act != 0 else None
+        z = self._own("z", self.max_rows, self.N + 7 & ~7).data_ptr() if self.act != 0 else None
         st = self._bwd(x.data_ptr(), self._w_ptr, z, dy.data_ptr(), self._dims_ref, _p(dx), _p(dw), _p(db), self.ws.ptr,
                        self.ws.nbytes, _stream(stream, self._device))
         if st:

@@ -66,6 +66,39 @@ template <> struct Vec8<float> {
   }
 };
 
+// 8 consecutive elements from an address that is aligned to the element only: the aligned 16-byte
+// vectors around them, shifted into place (element by element where those reach past `end`, the
+// tensor's end; its beginning is 16-byte aligned).
+template <typename T>
+__device__ __forceinline__ void load8_unaligned(Vec8<T>& r, const T* p, const T* end, int n) {
+  constexpr int W = 2 * sizeof(T);   // 32-bit words of the 8 elements
+  const uintptr_t at = reinterpret_cast<uintptr_t>(p), base = at & ~uintptr_t(15);
+  if (base + W * 4 + 16 <= reinterpret_cast<uintptr_t>(end)) {
+    uint32_t w[W + 4];
+#pragma unroll
+    for (int i = 0; i < W / 4 + 1; ++i) {
+      const uint4 v = __ldg(reinterpret_cast<const uint4*>(base) + i);
+      w[4 * i] = v.x;
+      w[4 * i + 1] = v.y;
+      w[4 * i + 2] = v.z;
+      w[4 * i + 3] = v.w;
+    }
+    if (at & 8)
+#pragma unroll
+      for (int i = 0; i < W + 2; ++i) w[i] = w[i + 2];
+    if (at & 4)
+#pragma unroll
+      for (int i = 0; i < W + 1; ++i) w[i] = w[i + 1];
+    uint32_t* out = reinterpret_cast<uint32_t*>(&r);
+#pragma unroll
+    for (int i = 0; i < W; ++i) out[i] = at & 2 ? __funnelshift_r(w[i], w[i + 1], 16) : w[i];
+  } else {
+    T* out = reinterpret_cast<T*>(&r);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) out[i] = i < n ? p[i] : T(0.f);
+  }
+}
+
 __device__ __forceinline__ float to_f32(float v) { return v; }
 __device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
 template <typename T> __device__ __forceinline__ T from_f32(float v);

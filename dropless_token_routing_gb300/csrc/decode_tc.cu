@@ -21,6 +21,7 @@
 
 #include <mutex>
 
+#include "act.cuh"
 #include "decode_select.cuh"
 #include "trace.h"
 
@@ -109,7 +110,7 @@ template <int NT> struct Finish {
       float w = r == SHARED ? 1.f : 0.f;
       if (r != SHARED) {
         const int e = tb.slots[(int)tile / plan.per_h];
-#pragma unroll 1
+#pragma unroll 4
         for (int j = t * k; j < t * k + k; ++j)
           if (tb.idx[j] == e) w = tb.gate[j];
       }
@@ -122,15 +123,15 @@ template <int NT> struct Finish {
       const int f = r == SHARED ? p.a.dm.f_s : p.a.dm.f, per = r == SHARED ? plan.per_s : plan.per_h;
       const int at = (int)tile, slot = at / per, c = (tid & 31) * 2;
       __nv_bfloat16* out = (r == SHARED ? p.hsbuf : p.hbuf) + (int64_t)slot * NT * f + (at - slot * per) * 64 + c;
-#pragma unroll 1
+#pragma unroll 4
       for (int t = tid >> 5; t < T; t += CW) {
         const float w = wt[t];
         float h0 = 0.f, h1 = 0.f;
         if (w != 0.f) {
           const float2 g = *reinterpret_cast<const float2*>(acc + t * PITCH + c);
           const float2 u = *reinterpret_cast<const float2*>(acc + t * PITCH + 64 + c);
-          h0 = w * (silu_f(g.x) * u.x);
-          h1 = w * (silu_f(g.y) * u.y);
+          h0 = w * (act_fast<MOE_ACT_SILU>(g.x) * u.x);
+          h1 = w * (act_fast<MOE_ACT_SILU>(g.y) * u.y);
         }
         *reinterpret_cast<uint32_t*>(out + (int64_t)t * f) = pack_bf16x2(h0, h1);
       }

@@ -14,7 +14,7 @@ constexpr int GM = 128, GN = 64, GK = 16, GT = 128;
 template <typename T>
 __device__ __forceinline__ void finish_element(const GemmArgs& g, int64_t m, int n, float v) {
   if (g.bias != nullptr) v += to_f32(static_cast<const T*>(g.bias)[n]);
-  if (g.z_out != nullptr) static_cast<T*>(g.z_out)[m * g.N + n] = from_f32<T>(v);
+  if (g.z_out != nullptr) static_cast<T*>(g.z_out)[m * g.ld_z + n] = from_f32<T>(v);
   v = act_any(g.act, v);
   if (g.res != nullptr) v += to_f32(static_cast<const T*>(g.res)[m * g.ld_res + n]);
   static_cast<T*>(g.c)[m * g.ldc + n] = from_f32<T>(v);
@@ -177,8 +177,8 @@ void gemm_simt(const GemmArgs& g, float* part, int num_sms, cudaStream_t st) {
 
 // dz = dy * act'(z), and its column sums. 8 columns per thread, `lx` threads side by side (a row's
 // 16 lx bytes at a time, for the HBM's sake), 256 / lx rows; the block takes every gridDim.y-th such
-// group of rows and adds its rows' sums in order into one row of `part`. (8-element vectors where
-// the rows allow, else element by element.)
+// group of rows and adds its rows' sums in order into one row of `part`. VEC: dy's rows hold whole
+// 16-byte vectors.
 template <typename T, int ACT, bool VEC>
 __global__ void __launch_bounds__(256) linear_dz_kernel(const T* __restrict__ dy, int64_t ld_dy,
                                                         const T* __restrict__ z, int64_t M, int N,
@@ -192,52 +192,37 @@ __global__ void __launch_bounds__(256) linear_dz_kernel(const T* __restrict__ dy
   const int n = (blockIdx.x * lx + c) * 8, cols = min(8, N - n);
   const int64_t step = (int64_t)gridDim.y * ly;
   float sum[8] = {};
-  auto load = [&](const T* p, Vec8<T>& u, float (&v)[8]) {
-    if (VEC) {
-      u.load(p);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = i < cols ? to_f32(p[i]) : 0.f;
-    }
-  };
+  const T* dy_end = dy + (M - 1) * ld_dy + N;
   if (cols > 0) {
     for (int64_t m0 = (int64_t)blockIdx.y * ly + r; m0 < M; m0 += U * step) {
       Vec8<T> a[U], b[U];
-      float av[U][8], bv[U][8];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int64_t m = m0 + u * step;
         if (m < M) {
-          load(dy + m * ld_dy + n, a[u], av[u]);
-          if (ACT != MOE_ACT_NONE) load(z + m * N + n, b[u], bv[u]);
+          if (VEC) a[u].load(dy + m * ld_dy + n);
+          else load8_unaligned(a[u], dy + m * ld_dy + n, dy_end, cols);
+          if (ACT != MOE_ACT_NONE) b[u].load(z + m * ld_dz + n);
         }
       }
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int64_t m = m0 + u * step;
         if (m >= M) break;
-        if (VEC) {
-          a[u].to_float(av[u]);
-          if (ACT != MOE_ACT_NONE) b[u].to_float(bv[u]);
-        }
+        float v[8], zv[8];
+        a[u].to_float(v);
         if constexpr (ACT != MOE_ACT_NONE) {
+          b[u].to_float(zv);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) av[u][i] *= sizeof(T) == 2 ? act_slope_fast<ACT>(bv[u][i]) : act_slope<ACT>(bv[u][i]);
+          for (int i = 0; i < 8; ++i) v[i] *= sizeof(T) == 2 ? act_slope_fast<ACT>(zv[i]) : act_slope<ACT>(zv[i]);
         }
-        if (dz != nullptr) {
-          T* out = dz + m * ld_dz + n;
-          if (VEC) {
-            Vec8<T> o;
-            o.from_float(av[u]);
-            o.store(out);
-          } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-              if (i < cols) out[i] = from_f32<T>(av[u][i]);
-          }
+        if (dz != nullptr) {   // whole vectors: what lies past N is never read
+          Vec8<T> o;
+          o.from_float(v);
+          o.store(dz + m * ld_dz + n);
         }
 #pragma unroll
-        for (int i = 0; i < 8; ++i) sum[i] += av[u][i];
+        for (int i = 0; i < 8; ++i) sum[i] += v[i];
       }
     }
   }
@@ -286,7 +271,7 @@ cudaError_t linear_dz(const void* dy, int64_t ld_dy, const void* z, int act, int
   if (split > (M + 8 * ly - 1) / (8 * ly)) split = (M + 8 * ly - 1) / (8 * ly);
   if (split > kDbSplit) split = kDbSplit;
   const dim3 grid(nx, (unsigned)split);
-  const bool vec = N % 8 == 0 && ld_dy % 8 == 0;   // ld_dz is a multiple of 8
+  const bool vec = N % 8 == 0 && ld_dy % 8 == 0;   // z's and dz's stride is a multiple of 8
   const T *dyp = static_cast<const T*>(dy), *zp = static_cast<const T*>(z);
   T* dzp = static_cast<T*>(dz);
   float* pp = db != nullptr ? part : nullptr;

@@ -57,8 +57,8 @@ struct PairGemm {
   int sk_pairs;          // over this many pairs (each gets at least kMinRun K blocks)
   const __nv_bfloat16 *bias, *res;
   __nv_bfloat16 *z, *c;
-  int64_t ld_res, ldc;
-  bool vec;              // rows of c, res and z hold whole 16-byte vectors
+  int64_t ld_res, ldc, ld_z;
+  bool vec, vec_res;     // rows of c, of res, hold whole 16-byte vectors (z's do)
   uint32_t* header;      // error word, epoch, exit count
   uint32_t* flags;       // [CTA][EW]
   float* part;           // [CTA][EW][128 / 4][32 rows][4 columns]
@@ -175,29 +175,34 @@ __device__ __forceinline__ bool flag_wait(const uint32_t* flag, uint32_t value, 
   return ok;
 }
 
-// A warp's 32 rows x 32 columns between global memory and its staging buffer, 64 bytes per row:
-// eight rows per instruction where rows hold whole 16-byte vectors, else row by row.
+// A warp's 32 rows x 32 columns between global memory and its staging buffer, 64 bytes per row,
+// eight rows per instruction; rows that do not hold whole 16-byte vectors are loaded shifted and
+// stored element by element, a row per instruction.
 struct Chunk {
   int64_t m0;
   int n, rows, cols;
-  bool vec;
-  __device__ __forceinline__ void load(uint4 (&v)[4], const __nv_bfloat16* p, int64_t ld, int lane) const {
+  __device__ __forceinline__ void load(uint4 (&v)[4], const __nv_bfloat16* p, int64_t ld, bool vec, const __nv_bfloat16* end,
+                                       int lane) const {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int r = i * 8 + (lane >> 2), q = (lane & 3) * 8;
-      if (r < rows && q < cols) v[i] = *reinterpret_cast<const uint4*>(p + (m0 + r) * ld + n + q);
+      if (r < rows && q < cols) {
+        const __nv_bfloat16* at = p + (m0 + r) * ld + n + q;
+        if (vec) {
+          v[i] = *reinterpret_cast<const uint4*>(at);
+        } else {
+          Vec8<__nv_bfloat16> u;
+          load8_unaligned(u, at, end, cols - q);
+          v[i] = u.v;
+        }
+      }
     }
   }
   __device__ __forceinline__ void stage(uint8_t* buf, const uint4 (&v)[4], int lane) const {
 #pragma unroll
     for (int i = 0; i < 4; ++i) *reinterpret_cast<uint4*>(buf + (i * 8 + (lane >> 2)) * PITCH + (lane & 3) * 16) = v[i];
   }
-  __device__ __forceinline__ void stage_scalar(uint8_t* buf, const __nv_bfloat16* p, int64_t ld, int lane) const {
-    if (lane < cols)
-#pragma unroll 4
-      for (int r = 0; r < rows; ++r) *reinterpret_cast<__nv_bfloat16*>(buf + r * PITCH + lane * 2) = p[(m0 + r) * ld + n + lane];
-  }
-  __device__ __forceinline__ void store(const uint8_t* buf, __nv_bfloat16* p, int64_t ld, int lane) const {
+  __device__ __forceinline__ void store(const uint8_t* buf, __nv_bfloat16* p, int64_t ld, bool vec, int lane) const {
     if (vec) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -206,7 +211,7 @@ struct Chunk {
           *reinterpret_cast<uint4*>(p + (m0 + r) * ld + n + q * 8) = *reinterpret_cast<const uint4*>(buf + r * PITCH + q * 16);
       }
     } else if (lane < cols) {
-#pragma unroll 4
+#pragma unroll 8
       for (int r = 0; r < rows; ++r) p[(m0 + r) * ld + n + lane] = *reinterpret_cast<const __nv_bfloat16*>(buf + r * PITCH + lane * 2);
     }
   }
@@ -235,8 +240,10 @@ __device__ __forceinline__ void add_row(float (&v)[32], const void* p) {
   }
 }
 
+__device__ __forceinline__ const __nv_bfloat16* res_end(const PairGemm& g) { return g.res + (g.Mo - 1) * g.ld_res + g.No; }
+
 // bias, z, activation and residual of this lane's 32 columns, and their way out. `res`: the chunk's
-// residual (vec), loaded ahead; `next` and `load_next`: the chunk to load into it.
+// residual, loaded ahead; `next` and `load_next`: the chunk to load into it.
 template <int ACT>
 __device__ __forceinline__ void finish_chunk(const PairGemm& g, uint8_t* stage, int lane, float (&v)[32], const Chunk& c,
                                              uint4 (&res)[4], const Chunk& next, bool load_next) {
@@ -251,22 +258,21 @@ __device__ __forceinline__ void finish_chunk(const PairGemm& g, uint8_t* stage, 
   if (g.z != nullptr) {
     pack_row(stage, lane, v);
     __syncwarp();
-    c.store(stage, g.z, g.No, lane);
+    c.store(stage, g.z, g.ld_z, true, lane);
     __syncwarp();
   }
 #pragma unroll
   for (int i = 0; i < 32; ++i) v[i] = act_fast<ACT>(v[i]);
   if (g.res != nullptr) {
-    if (c.vec) c.stage(stage, res, lane);
-    else c.stage_scalar(stage, g.res, g.ld_res, lane);
+    c.stage(stage, res, lane);
     __syncwarp();
-    if (c.vec && load_next) next.load(res, g.res, g.ld_res, lane);
+    if (load_next) next.load(res, g.res, g.ld_res, g.vec_res, res_end(g), lane);
     add_row(v, stage + lane * PITCH);
     __syncwarp();
   }
   pack_row(stage, lane, v);
   __syncwarp();
-  c.store(stage, g.c, g.ldc, lane);
+  c.store(stage, g.c, g.ldc, g.vec, lane);
   __syncwarp();
 }
 
@@ -416,9 +422,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       const int rows = (int)min((int64_t)32, g.Mo - m0), n0 = ni * g.tn + col0;
       const bool live = rows > 0 && n0 < g.No;    // the same for every part of the tile
       const bool owner = cur.s.k1 == g.nkb;
-      auto chunk = [&](int c) { return Chunk{m0, n0 + c, rows, min(32, min(hn - c, g.No - n0 - c)), g.vec}; };
+      auto chunk = [&](int c) { return Chunk{m0, n0 + c, rows, min(32, min(hn - c, g.No - n0 - c))}; };
       uint4 res[4];
-      if (live && owner && g.res != nullptr && g.vec) chunk(0).load(res, g.res, g.ld_res, lane);
+      if (live && owner && g.res != nullptr) chunk(0).load(res, g.res, g.ld_res, g.vec_res, res_end(g), lane);
       const bool got = mbar_wait_bounded(smem_u32(&tfull_bar[b]), (it >> 1) & 1, &abort_flag, err, kWaitLimitNs);
       if (!__all_sync(0xffffffffu, got)) break;   // warp-uniform: tcgen05.ld is .sync.aligned
       tc_fence_after();
@@ -607,7 +613,9 @@ int launch_linear_pair(int kind, const GemmArgs& a, uint8_t* ws, size_t part, in
   g.c = static_cast<__nv_bfloat16*>(a.c);
   g.ld_res = a.ld_res;
   g.ldc = a.ldc;
-  g.vec = a.N % 8 == 0 && a.ldc % 8 == 0 && (a.res == nullptr || a.ld_res % 8 == 0);
+  g.ld_z = a.ld_z;
+  g.vec = a.N % 8 == 0 && a.ldc % 8 == 0;
+  g.vec_res = a.N % 8 == 0 && a.ld_res % 8 == 0;
   g.header = reinterpret_cast<uint32_t*>(ws);
   g.flags = g.header + 256;
   g.part = reinterpret_cast<float*>(ws + part);

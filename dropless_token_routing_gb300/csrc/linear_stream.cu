@@ -27,14 +27,19 @@ struct LinearStream {
   int act;
   const __nv_bfloat16 *bias, *res;
   __nv_bfloat16 *z, *y;
-  int64_t ld_res, ld_y;
-  bool vec;             // rows of y, res and z hold whole 16-byte vectors, and so do tiles
+  int64_t ld_res, ld_y, ld_z;
+  bool vec;             // rows of y and res hold whole 16-byte vectors (z's and tiles do)
   int* err;
 };
 
 __device__ __forceinline__ float4 peer_ld4(uint32_t a) {
   float4 v;
   asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ float peer_ld1(uint32_t a) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
   return v;
 }
 // One arrival on this barrier of every CTA of the cluster.
@@ -64,34 +69,24 @@ static __device__ __noinline__ bool peers_wait(uint64_t* bar, uint32_t parity, v
   }
 }
 
-// 8 outputs (n .. n + 7, `cols` of them inside the tile) of token m.
-__device__ __forceinline__ void finish8(const LinearStream& g, float (&v)[8], const float (&b)[8], int64_t m, int n, int cols) {
+// 8 outputs (n .. n + 7) of token m.
+__device__ __forceinline__ void finish8(const LinearStream& g, float (&v)[8], const float (&b)[8], int64_t m, int n) {
+  float r[8] = {};
+  Vec8<__nv_bfloat16> p;
+  if (g.res != nullptr) {
+    p.v = *reinterpret_cast<const uint4*>(g.res + m * g.ld_res + n);   // may be y's own buffer
+    p.to_float(r);
+  }
 #pragma unroll
   for (int i = 0; i < 8; ++i) v[i] += b[i];
-  if (g.vec) {
-    float r[8] = {};
-    Vec8<__nv_bfloat16> p;
-    if (g.res != nullptr) {
-      p.v = *reinterpret_cast<const uint4*>(g.res + m * g.ld_res + n);   // may be y's own buffer
-      p.to_float(r);
-    }
-    if (g.z != nullptr) {
-      p.from_float(v);
-      p.store(g.z + m * g.N + n);
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = act_any_fast(g.act, v[i]) + r[i];
+  if (g.z != nullptr) {
     p.from_float(v);
-    p.store(g.y + m * g.ld_y + n);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      if (i >= cols) break;
-      const float res = g.res != nullptr ? __bfloat162float(g.res[m * g.ld_res + n + i]) : 0.f;
-      if (g.z != nullptr) g.z[m * g.N + n + i] = __float2bfloat16_rn(v[i]);
-      g.y[m * g.ld_y + n + i] = __float2bfloat16_rn(act_any_fast(g.act, v[i]) + res);
-    }
+    p.store(g.z + m * g.ld_z + n);
   }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = act_any_fast(g.act, v[i]) + r[i];
+  p.from_float(v);
+  p.store(g.y + m * g.ld_y + n);
 }
 
 template <int NT>
@@ -157,11 +152,17 @@ __global__ void __launch_bounds__(THREADS, 1) linear_stream_kernel(const __grid_
     uint32_t parity = 0;
     bool ok = true;
     for (int tile = tile0, it = 0; ok && tile < g.tiles; tile += step, ++it) {
-      const int buf = it & 1, n = tile * g.rows + q;
-      const int cols = min(8, min(g.rows - q, g.N - n));
-      float bias[8];
+      const int buf = it & 1, n0 = tile * g.rows;
+      // this thread's outputs: n0 + q .. + 7 where rows hold whole vectors, else n0 + lane + 32 i
+      const int cols = min(g.rows, g.N - n0);
+      float bias[8] = {};
+      if (g.bias != nullptr) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) bias[i] = g.bias != nullptr && i < cols ? __bfloat162float(g.bias[n + i]) : 0.f;
+        for (int i = 0; i < 8; ++i) {
+          const int at = g.vec ? q + i : lane + 32 * i;
+          if (at < cols && (g.vec || i < 4)) bias[i] = __bfloat162float(g.bias[n0 + at]);
+        }
+      }
       ok = bar_wait(&b.tfull[buf], (it >> 1) & 1, &b.abort, g.err);
       if (ct_any(!ok)) break;
       __syncwarp();
@@ -183,15 +184,37 @@ __global__ void __launch_bounds__(THREADS, 1) linear_stream_kernel(const __grid_
           ok = !ct_any(!peers_wait(&b.peers_ready, parity, &b.abort, g.err));
           if (!ok) break;
         }
-        for (int c = c_lo + (tid >> 4); c < c_hi && c0 + c < g.M; c += 16) {
-          float v[8] = {};
-          for (uint32_t r = 0; r < cl; ++r) {   // in the order of the ranks
-            const uint32_t at = peer_addr(smem_u32(acc + c * PITCH + q), r);
-            const float4 lo = peer_ld4(at), hi = peer_ld4(at + 16);
-            v[0] += lo.x; v[1] += lo.y; v[2] += lo.z; v[3] += lo.w;
-            v[4] += hi.x; v[5] += hi.y; v[6] += hi.z; v[7] += hi.w;
+        if (g.vec) {
+          for (int c = c_lo + (tid >> 4); c < c_hi && c0 + c < g.M; c += 16) {
+            float v[8] = {};
+            for (uint32_t r = 0; r < cl; ++r) {   // in the order of the ranks
+              const uint32_t at = peer_addr(smem_u32(acc + c * PITCH + q), r);
+              const float4 lo = peer_ld4(at), hi = peer_ld4(at + 16);
+              v[0] += lo.x; v[1] += lo.y; v[2] += lo.z; v[3] += lo.w;
+              v[4] += hi.x; v[5] += hi.y; v[6] += hi.z; v[7] += hi.w;
+            }
+            if (q < cols) finish8(g, v, bias, c0 + c, n0 + q);
           }
-          if (cols > 0) finish8(g, v, bias, c0 + c, n, cols);
+        } else {   // a token per warp, so that single elements still make whole sectors
+          for (int c = c_lo + warp - 2; c < c_hi && c0 + c < g.M; c += CW) {
+            const int64_t m = c0 + c;
+            float v[4] = {}, res[4] = {};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int at = lane + 32 * i;
+              if (at >= cols) break;
+              if (g.res != nullptr) res[i] = __bfloat162float(g.res[m * g.ld_res + n0 + at]);
+              for (uint32_t r = 0; r < cl; ++r) v[i] += peer_ld1(peer_addr(smem_u32(acc + c * PITCH + at), r));
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int at = lane + 32 * i;
+              if (at >= cols) break;
+              const float z = v[i] + bias[i];
+              if (g.z != nullptr) g.z[m * g.ld_z + n0 + at] = __float2bfloat16_rn(z);
+              g.y[m * g.ld_y + n0 + at] = __float2bfloat16_rn(act_any_fast(g.act, z) + res[i]);
+            }
+          }
         }
         ct_sync();
         if (cl > 1) {   // the peers have read this CTA's sums before they are written over
@@ -291,6 +314,7 @@ int launch_linear_stream(const GemmArgs& a, uint8_t* ws, int num_sms, cudaStream
   g.y = static_cast<__nv_bfloat16*>(a.c);
   g.ld_res = a.ld_res;
   g.ld_y = a.ldc;
+  g.ld_z = a.ld_z;
   g.vec = a.N % 8 == 0 && a.ldc % 8 == 0 && (a.res == nullptr || a.ld_res % 8 == 0);
   g.err = reinterpret_cast<int*>(ws);
   if (a.M <= 16) return launch_nt<16>(g, a, num_sms, st);

@@ -64,12 +64,13 @@ struct GemmArgs {
   int64_t M;
   int N;
   int64_t K;
-  // epilogue: z = acc + bias[n]; z_out [M][N]; c = act(z) + res
+  // epilogue: z = acc + bias[n]; z_out [M][ld_z]; c = act(z) + res
   const void* bias;
   const void* res;
   int64_t ld_res;
   int act;
   void* z_out;
+  int64_t ld_z;      // N rounded up to a multiple of 8
   void* c;
   int64_t ldc;
   int dtype;
@@ -87,7 +88,8 @@ int launch_linear_pair(int kind, const GemmArgs& a, uint8_t* ws, size_t part, in
 // The forward product for at most kStreamRows rows, as a stream of the weights.
 constexpr int kStreamRows = 128;
 int launch_linear_stream(const GemmArgs& a, uint8_t* ws, int num_sms, cudaStream_t st);
-// dz = dy * act'(z) (dz may be NULL: sums only) and db (may be NULL)
+// dz = dy * act'(z) (dz may be NULL: sums only) and db (may be NULL); z and dz have ld_dz = N rounded
+// up to a multiple of 8 elements between rows
 cudaError_t launch_linear_dz(const void* dy, int64_t ld_dy, const void* z, int act, int64_t M, int N,
                              int dtype, void* dz, int64_t ld_dz, float* db_part, void* db, cudaStream_t st);
 

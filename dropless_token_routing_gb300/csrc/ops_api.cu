@@ -174,7 +174,7 @@ int moe_linear_fwd(const void* x, const void* w, const void* bias, const void* r
   OP_TRY(opt(z));
   OP_TRY(req_if(y, some));
   if (!some) return MOE_OK;
-  GemmArgs g = {x, w, d.ld_x, 1, d.ld_w, 1, d.M, d.N, d.K, bias, residual, d.ld_res, d.act, z, y, d.ld_y, d.dtype};
+  GemmArgs g = {x, w, d.ld_x, 1, d.ld_w, 1, d.M, d.N, d.K, bias, residual, d.ld_res, d.act, z, L.ld_dz, y, d.ld_y, d.dtype};
   const int sms = num_sms();
   if (sms == 0) return MOE_ERR_CUDA;
   return run_gemm(LINEAR_FWD, g, static_cast<uint8_t*>(ws), L, sms, (cudaStream_t)stream);
@@ -215,11 +215,11 @@ int moe_linear_bwd(const void* x, const void* w, const void* z, const void* dy, 
       return MOE_ERR_LAUNCH;
   }
   if (dx != nullptr) {   // dx [M, K] = dz W: contraction over N
-    GemmArgs g = {dz, w, ld_dz, 1, 1, d.ld_w, d.M, d.K, d.N, nullptr, nullptr, 0, MOE_ACT_NONE, nullptr, dx, d.ld_x, d.dtype};
+    GemmArgs g = {dz, w, ld_dz, 1, 1, d.ld_w, d.M, d.K, d.N, nullptr, nullptr, 0, MOE_ACT_NONE, nullptr, 0, dx, d.ld_x, d.dtype};
     OP_TRY(run_gemm(LINEAR_DX, g, base, L, sms, st));
   }
   if (dw != nullptr) {   // dw [N, K] = dz^T x: contraction over M
-    GemmArgs g = {dz, x, 1, ld_dz, 1, d.ld_x, d.N, d.K, d.M, nullptr, nullptr, 0, MOE_ACT_NONE, nullptr, dw, d.ld_w, d.dtype};
+    GemmArgs g = {dz, x, 1, ld_dz, 1, d.ld_x, d.N, d.K, d.M, nullptr, nullptr, 0, MOE_ACT_NONE, nullptr, 0, dw, d.ld_w, d.dtype};
     OP_TRY(run_gemm(LINEAR_DW, g, base, L, sms, st));
   }
   return MOE_OK;

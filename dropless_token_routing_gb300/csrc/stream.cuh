@@ -299,15 +299,16 @@ __device__ __forceinline__ bool take_run(Bars& b, Run run, int& it, int cta, uin
     const uint32_t t_base = b.tmem + ((uint32_t)(lg * 32) << 16) + (uint32_t)(buf * NT);
 #pragma unroll 1
     for (int c0 = 0; c0 < NT; c0 += CHUNK) {
+      uint32_t u[HALF / 8][8];
+#pragma unroll
+      for (int c = 0; c < HALF / 8; ++c) tmem_ld8(t_base + c0 + col0 + 8 * c, u[c]);
+      tmem_ld_wait();
 #pragma unroll
       for (int c = 0; c < HALF; c += 8) {
         const int col = c0 + col0 + c;
-        uint32_t u[8];
         float v[8];
-        tmem_ld8(t_base + col, u);
-        tmem_ld_wait();
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(u[i]);
+        for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(u[c / 8][i]);
         if (owner) {
 #pragma unroll 1
           for (int q = q0; q < cta; q += 4) {   // four CTAs' parts in flight, added in order

@@ -387,7 +387,8 @@ typedef struct moe_linear_dims {
 
 /* Matrix product with bias, activation and residual in its epilogue:
  *   z = x W^T + b,   y = act(z) + r        x [M, K], w [N][K], bias [N] or NULL, residual [M, N]
- * or NULL, z [M][N] (contiguous) receives the pre-activation for the backward, or NULL.
+ * or NULL, z [M][N rounded up to a multiple of 8] receives the pre-activation for the backward, or
+ * NULL.
  * fp32 accumulation, y rounded once (not from the rounded z). residual may be the buffer of y
  * (y updated in place) when their strides agree. Base pointers are 16-byte aligned; strides and
  * widths may be odd. M == 0 is a no-op. */

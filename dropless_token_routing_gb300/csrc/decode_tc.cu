@@ -35,8 +35,8 @@ struct DecodeTc {
   DecodeArgs a;
   Select s;
   uint32_t* header;      // error, epoch, leave count, counters (enum)
-  uint32_t* flags;       // [kDecodeRuns][CTA]
-  float* part;           // [kDecodeRuns][CTA][NT][128]
+  uint32_t* flags;       // [kDecodeRuns + 1][CTA]: the output has two parts per CTA
+  float* part;           // [kDecodeRuns + 1][CTA][NT][128]
   __nv_bfloat16 *hbuf, *hsbuf;   // [slot][NT][f], [S][NT][f_s]
 };
 
@@ -45,6 +45,10 @@ struct DecodeTc {
 // needs no rows of the slower CTAs, to keep the stream going meanwhile, measured no better: the
 // joins of a further run cost what it hides.)
 enum RunId { SHARED = 0, HIDDEN, OUTPUT };
+// An output tile with parts in kScatter or more CTAs is joined by all of them, with 32 columns and
+// more: T = 57, d = 448: 39 us, 48 by one CTA. With 16 columns one CTA is done sooner (T = 5, d =
+// 2048: 91 us, 93 by all), and with fewer parts there is no difference.
+constexpr int kScatter = 4;
 static_assert(OUTPUT + 1 == kDecodeRuns, "");
 
 struct Plan {
@@ -69,7 +73,7 @@ struct Plan {
     const int tiles = r == SHARED ? k_sh : r == HIDDEN ? total : tiles_out;
     const int nkb = r == OUTPUT ? k_sh + total : nkb_d;
     const int skip = r == SHARED ? T : 0;
-    return Run(tiles, nkb, cta - skip, n_cta - skip);
+    return Run(tiles, nkb, cta - skip, n_cta - skip, r != OUTPUT);
   }
 };
 
@@ -136,22 +140,24 @@ template <int NT> struct Finish {
         *reinterpret_cast<uint32_t*>(out + (int64_t)t * f) = pack_bf16x2(h0, h1);
       }
     } else {
-      const int d = p.a.dm.d, q = (tid & 31) * 4, n = (int)tile * BM + q;
-      if (n >= d) return;   // d is a multiple of 64
 #pragma unroll 1
-      for (int t = tid >> 5; t < T; t += CW) {
-        float4 v = *reinterpret_cast<const float4*>(acc + t * PITCH + q);
-        const int64_t at = (int64_t)t * d + n;
-        if (p.a.residual != nullptr) {   // may be y's own buffer
-          const uint2 u = *reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(p.a.residual) + at);
-          const float2 a = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&u.x));
-          const float2 b = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&u.y));
-          v = make_float4(v.x + a.x, v.y + a.y, v.z + b.x, v.w + b.y);
-        }
-        *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.a.y) + at) =
-            make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
-      }
+      for (int t = tid >> 5; t < T; t += CW)
+        out4(tile, t, (tid & 31) * 4, *reinterpret_cast<const float4*>(acc + t * PITCH + (tid & 31) * 4));
     }
+  }
+  __device__ int columns() const { return plan.T; }
+  // outputs q .. q + 3 of a tile, token t
+  __device__ void out4(int64_t tile, int t, int q, float4 v) {
+    const int d = p.a.dm.d, n = (int)tile * BM + q;
+    if (n >= d) return;   // d is a multiple of 64
+    const int64_t at = (int64_t)t * d + n;
+    if (p.a.residual != nullptr) {   // may be y's own buffer
+      const uint2 u = *reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(p.a.residual) + at);
+      const float2 a = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&u.x));
+      const float2 b = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&u.y));
+      v = make_float4(v.x + a.x, v.y + a.y, v.z + b.x, v.w + b.y);
+    }
+    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.a.y) + at) = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
   }
 };
 
@@ -327,7 +333,7 @@ __global__ void __launch_bounds__(THREADS, 1) decode_kernel(const __grid_constan
       }
       f.r = r;
       ok = take_run<NT>(b, plan.run(r), it, r == SHARED ? cta - T : cta, p.flags + r * n_cta, epoch,
-                        p.part + (int64_t)r * n_cta * NT * BM, acc, err, f);
+                        p.part + (int64_t)r * n_cta * NT * BM, acc, err, f, NT > 16 && r == OUTPUT && plan.tiles_out * kScatter <= n_cta);
       if (ok && r == HIDDEN) {
         // this CTA's hidden rows are written, for the TMA of any CTA
         __threadfence();

@@ -14,12 +14,13 @@ inline size_t round256(size_t x) { return (x + 255) & ~size_t(255); }
 
 constexpr int kMaxStreamCtas = 160;   // CTAs of a weight stream
 constexpr int kMinStreamRun = 2;      // K blocks of a CTA's run
+constexpr int kWholeTiles = 16;       // K blocks that a join costs (6, 16: 42, 40 us with 19 tokens, d = 2112; 0: 45)
 
 // ------------------------------------------------------------------ decode
 constexpr int kDecodeRuns = 3;   // shared, hidden, output
 struct DecodeLayout {
   size_t score_part; // [T][slabs][E] fp32 partial scores
-  size_t part;       // bf16: [kDecodeRuns][CTA][token columns][128] fp32 partial tiles
+  size_t part;       // bf16: [kDecodeRuns + 1][CTA][token columns][128] fp32 partial tiles
   // hidden rows times their gates: fp32 [slot][T][f] and [S][T][f_s]; bf16 [slot][token columns][f]
   // and [S][token columns][f_s]
   size_t h, hs;

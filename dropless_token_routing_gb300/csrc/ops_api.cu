@@ -17,7 +17,7 @@ DecodeLayout decode_layout(const moe_dims& d) {
   const bool tc = d.dtype == MOE_BF16;
   const size_t nt = tc ? decode_token_columns(d.T) : 0;
   L.score_part = take(4 * T * kMaxStreamCtas * E);
-  L.part = take(tc ? 4 * (size_t)kDecodeRuns * kMaxStreamCtas * nt * 128 : 0);
+  L.part = take(tc ? 4 * (size_t)(kDecodeRuns + 1) * kMaxStreamCtas * nt * 128 : 0);
   const size_t rows = tc ? 2 * nt : 4 * T;   // bytes of a column of hidden rows
   L.h = take(rows * (size_t)decode_slots(d) * d.f);
   L.hs = take(rows * (size_t)d.S * d.f_s);

@@ -142,18 +142,21 @@ struct Seg {
 };
 
 // CTA `c` of `n` works on its run of the tiles' K blocks, the last part first. With few blocks
-// only as many CTAs as get kMinStreamRun of them take part, so no run among them is empty.
+// only as many CTAs as get kMinStreamRun of them take part, so no run among them is empty. Where
+// whole tiles leave the busiest CTA at most kWholeTiles blocks more than an even share (a join costs
+// about as many), the runs end at tiles (`whole`).
 struct Run {
   int64_t units, u0, u;
   int nkb, n;
   Seg s;
-  __device__ Run(int64_t tiles, int nkb_, int c, int n_cta) {
+  __device__ Run(int64_t tiles, int nkb_, int c, int n_cta, bool whole) {
     nkb = nkb_;
     units = tiles * nkb;
-    n = (int)min((int64_t)n_cta, max((int64_t)1, units / kMinStreamRun));
+    whole = whole && (tiles + n_cta - 1) / n_cta * nkb - units / n_cta <= kWholeTiles;
+    n = (int)min((int64_t)n_cta, max((int64_t)1, whole ? tiles : units / kMinStreamRun));
     const bool in = c >= 0 && c < n;
-    u0 = in ? units * c / n : 0;
-    u = in ? units * (c + 1) / n : 0;
+    u0 = !in ? 0 : whole ? tiles * c / n * nkb : units * c / n;
+    u = !in ? 0 : whole ? tiles * (c + 1) / n * nkb : units * (c + 1) / n;
   }
   __device__ bool next() {
     if (u <= u0) return false;
@@ -164,11 +167,10 @@ struct Run {
     u = first + s.k0;
     return true;
   }
-  // the first CTA whose run holds a part of the current tile
-  __device__ int first_cta() const {
-    const int64_t first = s.t * nkb;
-    int q = (int)(first * n / units);
-    while (units * (q + 1) / n <= first) ++q;
+  // the CTA whose run holds K block `at` of all (of a divided tile)
+  __device__ int holder(int64_t at) const {
+    int q = (int)(at * n / units);
+    while (units * (q + 1) / n <= at) ++q;
     return q;
   }
 };
@@ -276,19 +278,27 @@ __device__ __forceinline__ bool mma_run(Bars& b, uint32_t smem_base, Run run, Ri
 }
 
 // The part of the CT threads in a run. `flags` and `part` are this run's (one word, NT * 128
-// floats per CTA). f.prepare(t) runs before, f.finish(t, c0, acc) after token columns
+// floats per CTA; with `scatter` two of each). f.prepare(t) runs before, f.finish(t, c0, acc) after token columns
 // [c0, c0 + CHUNK) of tile t are staged: acc[(column - c0) * PITCH + weight row].
+// scatter: tiles that many CTAs share (an output's, few and with a long K) are joined by all of them,
+// each a share of the result (f.out4(t, column, row, sum of 4 rows)): one CTA adding up 37 others'
+// parts took 25 us.
 template <int NT, class F>
 __device__ __forceinline__ bool take_run(Bars& b, Run run, int& it, int cta, uint32_t* flags, uint32_t epoch, float* part,
-                                         float* acc, int* err, F& f) {
+                                         float* acc, int* err, F& f, bool scatter) {
   constexpr int CHUNK = Cfg<NT>::CHUNK, HALF = CHUNK / 2;
   const int cw = (threadIdx.x >> 5) - 2, lane = threadIdx.x & 31, lg = (threadIdx.x >> 5) & 3;
   const int row = lg * 32 + lane, col0 = (cw >> 2) * HALF;
+  int64_t shared_tile[2];   // divided tiles of this CTA (scatter): a run has two at most
+  int n_shared = 0;
+  const int stride = scatter ? 2 : 1;
   for (; run.next(); ++it) {
     const int buf = it & 1;
-    const bool owner = run.s.k1 == run.nkb;
+    const bool divided = run.s.k0 > 0 || run.s.k1 < run.nkb;
+    const bool owner = scatter ? !divided : run.s.k1 == run.nkb;
+    const int slot = cta * stride + (scatter && run.s.k0 > 0 ? 1 : 0);
     bool ok = bar_wait(&b.tfull[buf], (it >> 1) & 1, &b.abort, err);
-    const int q0 = owner && run.s.k0 > 0 ? run.first_cta() : cta;
+    const int q0 = owner && divided ? run.holder(run.s.t * run.nkb) : cta;
     ok = __all_sync(0xffffffffu, ok);
     if (owner)   // the flags of the tile's other CTAs
       for (int q = q0; ok && q < cta; q += 32) ok = flags_wait(q + lane < cta ? flags + q + lane : nullptr, epoch, &b.abort, err);
@@ -326,7 +336,7 @@ __device__ __forceinline__ bool take_run(Bars& b, Run run, int& it, int cta, uin
 #pragma unroll
           for (int i = 0; i < 8; ++i) acc[(col0 + c + i) * PITCH + row] = v[i];
         } else {
-          float* out = part + ((int64_t)cta * NT + col) * BM + row;
+          float* out = part + ((int64_t)slot * NT + col) * BM + row;
 #pragma unroll
           for (int i = 0; i < 8; ++i) __stcg(out + i * BM, v[i]);
         }
@@ -345,7 +355,40 @@ __device__ __forceinline__ bool take_run(Bars& b, Run run, int& it, int cta, uin
     if (!owner) {
       __threadfence();
       ct_sync();
-      if (threadIdx.x == 64) st_release(flags + cta, epoch);
+      if (threadIdx.x == 64) st_release(flags + slot, epoch);
+      if (scatter) {
+        if (n_shared == 0) shared_tile[0] = run.s.t;
+        else shared_tile[1] = run.s.t;
+        ++n_shared;
+      }
+    }
+  }
+#pragma unroll 1
+  for (int i = 0; i < n_shared; ++i) {
+    const int64_t t = i == 0 ? shared_tile[0] : shared_tile[1];
+    // CTAs q0 .. q1 hold parts of it, the first in its slot 0, the others in their slot 1
+    const int q0 = run.holder(t * run.nkb), q1 = run.holder((t + 1) * run.nkb - 1), n = q1 - q0 + 1;
+    bool ok = true;
+    for (int q = q0; ok && q <= q1; q += 32)
+      ok = flags_wait(q + lane <= q1 ? flags + (q + lane) * 2 + (q + lane > q0 ? 1 : 0) : nullptr, epoch, &b.abort, err);
+    if (ct_any(!ok)) return false;
+    const int all = f.columns() * (BM / 4), lo = all * (cta - q0) / n, hi = all * (cta - q0 + 1) / n;
+#pragma unroll 1
+    for (int u = lo + ct_tid(); u < hi; u += CT) {
+      const int col = u / (BM / 4), r4 = u % (BM / 4) * 4;
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+      for (int q = q0; q <= q1; q += 8) {   // eight CTAs' parts in flight, added in order
+        float4 w[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          w[j] = q + j <= q1 ? __ldcg(reinterpret_cast<const float4*>(
+                                   part + ((int64_t)((q + j) * 2 + (q + j > q0 ? 1 : 0)) * NT + col) * BM + r4))
+                             : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v = make_float4(v.x + w[j].x, v.y + w[j].y, v.z + w[j].z, v.w + w[j].w);
+      }
+      f.out4(t, col, r4, v);
     }
   }
   return true;

@@ -147,8 +147,6 @@ __global__ void __launch_bounds__(THREADS, 1) linear_stream_kernel(const __grid_
     constexpr int HALF = CHUNK / 2;
     const int lg = warp & 3, row = lg * 32 + lane, col0 = ((warp - 2) >> 2) * HALF, tid = threadIdx.x - 64;
     const int q = (tid & 15) * 8;   // this thread's 8 rows of W in a tile
-    // its share of a chunk's token columns
-    const int c_lo = CHUNK * (int)rank / (int)cl, c_hi = CHUNK * ((int)rank + 1) / (int)cl;
     uint32_t parity = 0;
     bool ok = true;
     for (int tile = tile0, it = 0; ok && tile < g.tiles; tile += step, ++it) {
@@ -178,6 +176,8 @@ __global__ void __launch_bounds__(THREADS, 1) linear_stream_kernel(const __grid_
 #pragma unroll
           for (int i = 0; i < 8; ++i) acc[(col0 + c + i) * PITCH + row] = __uint_as_float(u[i]);
         }
+        // this CTA's share of the chunk's tokens
+        const int here = min(CHUNK, g.M - c0), c_lo = here * (int)rank / (int)cl, c_hi = here * ((int)rank + 1) / (int)cl;
         ct_sync();
         if (cl > 1) {
           if (tid == 0) arrive_all(&b.peers_ready, (int)cl);
@@ -185,26 +185,48 @@ __global__ void __launch_bounds__(THREADS, 1) linear_stream_kernel(const __grid_
           if (!ok) break;
         }
         if (g.vec) {
-          for (int c = c_lo + (tid >> 4); c < c_hi && c0 + c < g.M; c += 16) {
+          for (int c = c_lo + (tid >> 4); c < c_hi; c += 16) {
             float v[8] = {};
-            for (uint32_t r = 0; r < cl; ++r) {   // in the order of the ranks
-              const uint32_t at = peer_addr(smem_u32(acc + c * PITCH + q), r);
-              const float4 lo = peer_ld4(at), hi = peer_ld4(at + 16);
-              v[0] += lo.x; v[1] += lo.y; v[2] += lo.z; v[3] += lo.w;
-              v[4] += hi.x; v[5] += hi.y; v[6] += hi.z; v[7] += hi.w;
+            for (uint32_t r0 = 0; r0 < cl; r0 += 4) {   // in the order of the ranks, four in flight
+              float4 w[4][2];
+#pragma unroll
+              for (uint32_t r = 0; r < 4; ++r) {
+                if (r0 + r >= cl) break;
+                const uint32_t at = peer_addr(smem_u32(acc + c * PITCH + q), r0 + r);
+                w[r][0] = peer_ld4(at);
+                w[r][1] = peer_ld4(at + 16);
+              }
+#pragma unroll
+              for (uint32_t r = 0; r < 4; ++r) {
+                if (r0 + r >= cl) break;
+                v[0] += w[r][0].x; v[1] += w[r][0].y; v[2] += w[r][0].z; v[3] += w[r][0].w;
+                v[4] += w[r][1].x; v[5] += w[r][1].y; v[6] += w[r][1].z; v[7] += w[r][1].w;
+              }
             }
             if (q < cols) finish8(g, v, bias, c0 + c, n0 + q);
           }
         } else {   // a token per warp, so that single elements still make whole sectors
-          for (int c = c_lo + warp - 2; c < c_hi && c0 + c < g.M; c += CW) {
+          for (int c = c_lo + warp - 2; c < c_hi; c += CW) {
             const int64_t m = c0 + c;
             float v[4] = {}, res[4] = {};
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int at = lane + 32 * i;
-              if (at >= cols) break;
-              if (g.res != nullptr) res[i] = __bfloat162float(g.res[m * g.ld_res + n0 + at]);
-              for (uint32_t r = 0; r < cl; ++r) v[i] += peer_ld1(peer_addr(smem_u32(acc + c * PITCH + at), r));
+            for (int i = 0; i < 4; ++i)
+              if (g.res != nullptr && lane + 32 * i < cols) res[i] = __bfloat162float(g.res[m * g.ld_res + n0 + lane + 32 * i]);
+            for (uint32_t r0 = 0; r0 < cl; r0 += 4) {
+              float w[4][4];
+#pragma unroll
+              for (uint32_t r = 0; r < 4; ++r) {
+                if (r0 + r >= cl) break;
+                const uint32_t at = peer_addr(smem_u32(acc + c * PITCH + lane), r0 + r);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) w[r][i] = peer_ld1(at + 128 * i);
+              }
+#pragma unroll
+              for (uint32_t r = 0; r < 4; ++r) {
+                if (r0 + r >= cl) break;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) v[i] += w[r][i];
+              }
             }
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -217,7 +239,8 @@ __global__ void __launch_bounds__(THREADS, 1) linear_stream_kernel(const __grid_
           }
         }
         ct_sync();
-        if (cl > 1) {   // the peers have read this CTA's sums before they are written over
+        // the peers have read this CTA's sums before they are written over (the last ones are not)
+        if (cl > 1 && (tile + step < g.tiles || c0 + CHUNK < g.M)) {
           if (tid == 0) arrive_all(&b.peers_done, (int)cl);
           ok = !ct_any(!peers_wait(&b.peers_done, parity, &b.abort, g.err));
           if (!ok) break;

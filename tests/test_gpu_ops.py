@@ -531,3 +531,109 @@ def test_draft_block_example():
     ref, racc = _verify64(tokens.cpu().numpy(), None, probs.cpu().numpy(), target.cpu().numpy(), u.cpu().numpy(),
                           us.cpu().numpy())
     assert np.array_equal(got.cpu().numpy(), ref) and np.array_equal(acc.cpu().numpy(), racc)
+
+
+# ------------------------------------------------------------------ large and odd memory
+def test_linear_output_past_32_bit_offsets():
+    """y holds more than 2^31 elements; the last rows and some between are compared."""
+    A = _api()
+    M, N, K = 70001, 32768, 64
+    g = torch.Generator(device="cuda").manual_seed(1)
+    w = torch.randn(N, K, generator=g, device="cuda", dtype=torch.bfloat16) * 0.1
+    x = torch.randn(M, K, generator=g, device="cuda", dtype=torch.bfloat16)
+    y = A.Linear(w, None, max_rows=M).forward(x)
+    rows = torch.tensor([0, 1, 255, 256, 32767, 65535, 65536, 65599, 69999, 70000], device="cuda")
+    _close(y[rows], x[rows].cpu().double() @ w.cpu().double().T, torch.bfloat16)
+
+
+def test_verify_probabilities_past_32_bit_offsets():
+    """Row n of the target starts past element 2^31."""
+    n, V, ld = 1024, 1000, 1 << 21
+    p = torch.zeros(1, n + 1, ld, dtype=torch.bfloat16, device="cuda")[..., :V]
+    q = torch.zeros(1, n, V, dtype=torch.bfloat16, device="cuda")
+    tokens = torch.randint(0, V, (1, n), generator=_gen(2)).to(torch.int32)
+    at = tokens.long().cuda().unsqueeze(-1)
+    p[:, :n].scatter_(2, at, 1.0)            # every drafted token is kept
+    q.scatter_(2, at, 1.0)
+    p[0, n, 777] = 1.0                       # and the one after them is certain
+    u, us = torch.full((1, n), 0.5), torch.tensor([0.25])
+    got, acc = _api().DraftVerifier(1, n, V, torch.bfloat16).verify(tokens.cuda(), q, p, u.cuda(), us.cuda())
+    assert int(acc) == n and got[0, :n].tolist() == tokens[0].tolist() and int(got[0, n]) == 777
+
+
+@pytest.mark.parametrize("M", [5, 40, 100, 300])
+@pytest.mark.parametrize("N", [264, 301])
+def test_linear_rows_with_nan_and_inf_stay_alone(M, N):
+    """A row of x that is not finite spoils no other row of y, and no other row of dx."""
+    A = _api()
+    K = 136
+    g = _gen(M + N)
+    w, x = _rand(g, N, K, std=0.1, dtype=torch.bfloat16), _rand(g, M, K, dtype=torch.bfloat16)
+    r, dy = _rand(g, M, N, dtype=torch.bfloat16), _rand(g, M, N, dtype=torch.bfloat16)
+    y, ref = _linear64(x, w, None, r, "silu", dy)
+    bad, bad_dy = x.clone(), dy.clone()
+    bad[1] = float("nan")
+    bad[M - 1, 7] = float("inf")
+    bad_dy[1] = float("nan")
+    lin = A.Linear(w.cuda(), None, act="silu", max_rows=M)
+    keep = [i for i in range(M) if i not in (1, M - 1)]
+    _close(lin.forward(bad.cuda(), residual=r.cuda(), save=True)[keep], y[keep], torch.bfloat16)
+    _close(lin.backward(bad_dy.cuda(), need=("dx",))["dx"][keep], ref["dx"][keep], torch.bfloat16)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_linear_long_contractions_divided(dtype):
+    """Few outputs and a long K: the sums of many partial ones."""
+    A = _api()
+    for M, N, K in ((300, 64, 8192), (260, 130, 5000), (20, 40, 9000)):
+        g = _gen(K)
+        x, w = _rand(g, M, K, dtype=dtype), _rand(g, N, K, std=K ** -0.5, dtype=dtype)
+        dy = _rand(g, M, N, dtype=dtype)
+        lin = A.Linear(w.cuda(), None, max_rows=M)
+        y, ref = _linear64(x, w, None, None, "none", dy)
+        _close(lin.forward(x.cuda(), save=True), y, dtype)
+        grads = lin.backward(dy.cuda())
+        _close(grads["dx"], ref["dx"], dtype)
+        _close(grads["dw"], ref["dw"], dtype)
+
+
+def test_workspaces_report_no_error_after_use():
+    A = _api()
+    g = _gen(0)
+    lin = A.Linear(_rand(g, 500, 256, std=0.1, dtype=torch.bfloat16).cuda(), None, act="gelu", max_rows=400)
+    x = _rand(g, 400, 256, dtype=torch.bfloat16).cuda()
+    lin.forward(x, save=True)
+    lin.backward(lin.forward(x, save=True).clone())
+    assert A.get_device_error(lin.ws) == 0
+
+
+def test_wrappers_refuse_what_does_not_fit():
+    A = _api()
+    w = torch.zeros(32, 64, dtype=torch.bfloat16, device="cuda")
+    lin = A.Linear(w, None, max_rows=4)
+    x = torch.zeros(4, 64, dtype=torch.bfloat16, device="cuda")
+    for bad in (x.float(), x[:, :32], torch.zeros(5, 64, dtype=torch.bfloat16, device="cuda"), x.t().contiguous().t()):
+        with pytest.raises(ValueError):
+            lin.forward(bad)
+    with pytest.raises(ValueError):
+        lin.backward(torch.zeros(4, 32, dtype=torch.bfloat16, device="cuda"))   # nothing saved
+    with pytest.raises(ValueError):
+        lin.forward(x, residual=x)
+    with pytest.raises(KeyError):
+        A.Linear(w, None, act="tanh")
+    wl, xl, _ = _layer(4, 128, 8, 2, 64, 0, 0, torch.bfloat16)
+    layer = _decode_layer(wl, 4, 128, 8, 2, 64, 0, 0, torch.bfloat16)
+    for bad in (xl.float().cuda(), torch.zeros(5, 128, dtype=torch.bfloat16, device="cuda"), xl[:, :64].cuda()):
+        with pytest.raises(ValueError):
+            layer.forward(bad)
+    with pytest.raises(A.N.MoeError):
+        _decode_layer(wl, 65, 128, 8, 2, 64, 0, 0, torch.bfloat16)
+    ver = A.DraftVerifier(2, 3, 16)
+    good = dict(draft_tokens=torch.zeros(2, 3, dtype=torch.int32).cuda(), draft_probs=torch.zeros(2, 3, 16).cuda(),
+                target_probs=torch.zeros(2, 4, 16).cuda(), u_accept=torch.zeros(2, 3).cuda(), u_sample=torch.zeros(2).cuda())
+    ver.verify(**good)
+    for name, bad in (("draft_tokens", torch.zeros(2, 3).cuda()), ("target_probs", torch.zeros(2, 3, 16).cuda()),
+                      ("draft_probs", torch.zeros(2, 3, 16).bfloat16().cuda()), ("u_sample", torch.zeros(3).cuda()),
+                      ("draft_probs", torch.zeros(2, 16, 3).cuda().transpose(1, 2))):
+        with pytest.raises(ValueError):
+            ver.verify(**{**good, name: bad})

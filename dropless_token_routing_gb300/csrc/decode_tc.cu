@@ -121,7 +121,7 @@ template <int NT> struct Finish {
       wt[t] = w;
     }
   }
-  __device__ void finish(int64_t tile, int, const float* acc) {
+  __device__ void finish(int64_t tile, const float* acc) {
     const int T = plan.T, tid = threadIdx.x - 64;
     if (r != OUTPUT) {
       const int f = r == SHARED ? p.a.dm.f_s : p.a.dm.f, per = r == SHARED ? plan.per_s : plan.per_h;

@@ -64,8 +64,8 @@ template <typename T, bool KC, int R> struct Operand {
   }
 };
 
-// One 128 x 64 tile of A B^T per block (or a share of its K: blockIdx.z of gridDim.z, into fp32
-// partial sums), 8 x 8 of it per thread in quarters of 4 x 4: 4 shared-memory vectors per 64 FMAs
+// One 128 x 64 tile of A B^T per block (or a share of its K: blockIdx.z of gridDim.z, into `part`, whole
+// tiles of fp32 sums), 8 x 8 of it per thread in quarters of 4 x 4: 4 shared-memory vectors per 64 FMAs
 // (with 8 x 4 the shared memory was the limit). The next 16 of K are loaded into registers while
 // the present ones are multiplied.
 template <typename T, bool AK, bool BK, bool SPLIT>
@@ -121,7 +121,16 @@ __global__ void __launch_bounds__(GT) gemm_simt_kernel(const GemmArgs g, float* 
       __syncthreads();
     }
   }
-  pdl_start();   // (earlier, the next kernel's blocks slow these down: 115 -> 118 us for a step of three)
+  if (SPLIT) {
+    float* out = part + (((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * gridDim.z + blockIdx.z) * (GM * GN);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        *reinterpret_cast<ulonglong2*>(out + (i / 4 * 64 + ty * 4 + i % 4) * GN + h * 32 + tx * 4) =
+            make_ulonglong2(acc[i][2 * h], acc[i][2 * h + 1]);
+    return;
+  }
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const int64_t m = m0 + i / 4 * 64 + ty * 4 + i % 4;
@@ -130,24 +139,38 @@ __global__ void __launch_bounds__(GT) gemm_simt_kernel(const GemmArgs g, float* 
     for (int j = 0; j < 8; ++j) {
       const int n = n0 + j / 4 * 32 + tx * 4 + j % 4;
       if (n >= g.N) continue;
-      const float v = __uint_as_float((uint32_t)(acc[i][j / 2] >> (j % 2 * 32)));
-      if (SPLIT) part[((int64_t)blockIdx.z * g.M + m) * g.N + n] = v;
-      else finish_element<T>(g, m, n, v);
+      finish_element<T>(g, m, n, __uint_as_float((uint32_t)(acc[i][j / 2] >> (j % 2 * 32))));
     }
   }
 }
 
-// The shares of a divided K, added in order.
+// The shares of a divided K, added in order: a tile's row per warp. (Neither this kernel nor the product
+// lets the next one start early: its blocks would then fill the SMs that are free first, several on
+// one. 256 x 256 x 1024: 8.0 us, 16.4 if this one does.)
+constexpr int JR = 8;   // rows of a block
 template <typename T>
-__global__ void __launch_bounds__(256) gemm_join_kernel(const GemmArgs g, const float* __restrict__ part, int split) {
-  const int64_t all = g.M * g.N;
-  pdl_start();
+__global__ void __launch_bounds__(32 * JR) gemm_join_kernel(const GemmArgs g, const float* __restrict__ part, int split) {
+  const int lane = threadIdx.x & 31, r = blockIdx.z * JR + (threadIdx.x >> 5);
+  const int64_t m = (int64_t)blockIdx.x * GM + r;
+  const int n = blockIdx.y * GN + lane;
+  const float* in = part + ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * split * (GM * GN) + r * GN + lane;
   pdl_wait();
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < all; i += (int64_t)gridDim.x * 256) {
-    float v = 0.f;
-    for (int s = 0; s < split; ++s) v += part[s * all + i];
-    finish_element<T>(g, i / g.N, (int)(i % g.N), v);
+  if (m >= g.M) return;
+  float v[2] = {};
+  for (int s0 = 0; s0 < split; s0 += 16) {   // 16 shares in flight
+    float w[16][2];
+#pragma unroll
+    for (int s = 0; s < 16; ++s)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) w[s][h] = s0 + s < split ? __ldcg(in + (s0 + s) * (GM * GN) + 32 * h) : 0.f;
+#pragma unroll
+    for (int s = 0; s < 16; ++s)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) v[h] += w[s][h];
   }
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+    if (n + 32 * h < g.N) finish_element<T>(g, m, n + 32 * h, v[h]);
 }
 
 // The layouts of the layer's products: forward (both operands along k), dX, dW.
@@ -158,21 +181,34 @@ void gemm_layouts(const GemmArgs& g, float* part, const dim3& grid, cudaStream_t
   else launch_pdl(gemm_simt_kernel<T, false, false, SPLIT>, grid, GT, 0, 1, st, g, part);
 }
 
+// The shares of K, by the time of the busiest SM (us). Measured: 16 of K of one block take 1.33 us, of two
+// on an SM 0.89 each, of more 0.82 each (there is no load latency left to hide); a join takes 2.5 and
+// 0.0055 for each share of a tile, whose sums go through the L2, the way out of undivided tiles 6. 512 x 1000 x 768: 7 shares 22 us, one
+// 68, 16 23; 2048 x 2048 x 512: 2 shares 101 us, one 114, 8 115.
+int simt_split(int64_t tiles, int64_t K, int num_sms) {
+  int best = 1;
+  double least = 0;
+  for (int s = 1; s <= kMaxSplit && (s == 1 || (K / s >= 2 * GK && tiles * s <= kMaxShares)); ++s) {
+    const int64_t blocks = (tiles * s + num_sms - 1) / num_sms, steps = (K + (int64_t)s * GK - 1) / (s * GK);
+    const double t = (double)blocks * steps * (blocks == 1 ? 1.33 : blocks == 2 ? 0.89 : 0.82) + (s > 1 ? 2.5 + 0.0055 * tiles * s : 6);
+    if (s == 1 || t < least) {
+      least = t;
+      best = s;
+    }
+  }
+  return best;
+}
+
 template <typename T>
 void gemm_simt(const GemmArgs& g, float* part, int num_sms, cudaStream_t st) {
   const int64_t tm = (g.M + GM - 1) / GM, tn = (g.N + GN - 1) / GN, tiles = tm * tn;
-  // One block leaves an SM's FMA pipes waiting for its loads; K is divided until there are about
-  // kBlocks on each, with at least 64 of K.
-  int64_t split = (int64_t)kBlocks * (num_sms < kMaxStreamCtas ? num_sms : kMaxStreamCtas) / tiles;
-  if (split > g.K / 64) split = g.K / 64;
-  if (split > kMaxSplit) split = kMaxSplit;
+  const int split = simt_split(tiles, g.K, num_sms);
   if (split <= 1) {
     gemm_layouts<T, false>(g, nullptr, dim3((unsigned)tm, (unsigned)tn), st);
     return;
   }
-  gemm_layouts<T, true>(g, part, dim3((unsigned)tm, (unsigned)tn, (unsigned)split), st);
-  const int64_t blocks = (g.M * g.N + 1023) / 1024;
-  launch_pdl(gemm_join_kernel<T>, dim3((unsigned)(blocks < 8 * num_sms ? blocks : 8 * num_sms)), 256, 0, 1, st, g, part, (int)split);
+  gemm_layouts<T, true>(g, part, dim3((unsigned)tm, (unsigned)tn, split), st);
+  launch_pdl(gemm_join_kernel<T>, dim3((unsigned)tm, (unsigned)tn, GM / JR), 32 * JR, 0, 1, st, g, part, split);
 }
 
 // dz = dy * act'(z), and its column sums. 8 columns per thread, `lx` threads side by side (a row's
@@ -263,12 +299,12 @@ __global__ void __launch_bounds__(256) linear_db_kernel(const float* __restrict_
 template <typename T>
 cudaError_t linear_dz(const void* dy, int64_t ld_dy, const void* z, int act, int64_t M, int N, void* dz,
                       int64_t ld_dz, float* part, void* db, cudaStream_t st) {
-  // About 600 blocks (4 on an SM), each with at least 8 rows for a thread. Sums alone in rows of 2 KB
+  // About 600 blocks (4 on an SM), each with at least 2 rows for a thread. Sums alone in rows of 2 KB
   // (8192 x 7680: 24 us, 31 in rows of 512 bytes and 1200 blocks); with a derivative to compute in
   // rows of 512 (4096 x 2816 SiLU: 12.5 us, 13.9).
   const int lx = act == MOE_ACT_NONE && N > 512 ? 128 : 32, ly = 256 / lx, nx = (N + lx * 8 - 1) / (lx * 8);
   int64_t split = (608 + nx - 1) / nx;
-  if (split > (M + 8 * ly - 1) / (8 * ly)) split = (M + 8 * ly - 1) / (8 * ly);
+  if (split > (M + 2 * ly - 1) / (2 * ly)) split = (M + 2 * ly - 1) / (2 * ly);
   if (split > kDbSplit) split = kDbSplit;
   const dim3 grid(nx, (unsigned)split);
   const bool vec = N % 8 == 0 && ld_dy % 8 == 0;   // z's and dz's stride is a multiple of 8
@@ -285,6 +321,12 @@ cudaError_t linear_dz(const void* dy, int64_t ld_dy, const void* z, int act, int
 }
 
 }  // namespace
+
+size_t gemm_simt_part_bytes(int64_t M, int64_t N, int64_t K) {
+  const int64_t tiles = ((M + GM - 1) / GM) * ((N + GN - 1) / GN), most = K / (2 * GK) < kMaxSplit ? K / (2 * GK) : kMaxSplit;
+  if (most < 2 || 2 * tiles > kMaxShares) return 0;
+  return (size_t)(tiles * most < kMaxShares ? tiles * most : kMaxShares) * GM * GN * 4;
+}
 
 cudaError_t launch_gemm_simt(const GemmArgs& g, float* part, int num_sms, cudaStream_t st) {
   TraceScope ts(TP_LINEAR, st);

@@ -91,7 +91,7 @@ __device__ __forceinline__ void finish8(const LinearStream& g, float (&v)[8], co
 
 template <int NT>
 __global__ void __launch_bounds__(THREADS, 1) linear_stream_kernel(const __grid_constant__ LinearStream g) {
-  constexpr int STAGES = Cfg<NT>::stages(0), STAGE = Cfg<NT>::STAGE, CHUNK = Cfg<NT>::CHUNK;
+  constexpr int STAGES = Cfg<NT>::stages(0), STAGE = Cfg<NT>::STAGE;
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) Bars b;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -144,7 +144,7 @@ __global__ void __launch_bounds__(THREADS, 1) linear_stream_kernel(const __grid_
     }
     __syncwarp();
   } else {
-    constexpr int HALF = CHUNK / 2;
+    constexpr int HALF = NT / 2;
     const int lg = warp & 3, row = lg * 32 + lane, col0 = ((warp - 2) >> 2) * HALF, tid = threadIdx.x - 64;
     const int q = (tid & 15) * 8;   // this thread's 8 rows of W in a tile
     uint32_t parity = 0;
@@ -166,86 +166,83 @@ __global__ void __launch_bounds__(THREADS, 1) linear_stream_kernel(const __grid_
       __syncwarp();
       tc_fence_after();
       const uint32_t t_base = b.tmem + ((uint32_t)(lg * 32) << 16) + (uint32_t)(buf * NT);
-#pragma unroll 1
-      for (int c0 = 0; c0 < NT && c0 < g.M; c0 += CHUNK) {
 #pragma unroll
-        for (int c = 0; c < HALF; c += 8) {
-          uint32_t u[8];
-          tmem_ld8(t_base + c0 + col0 + c, u);
-          tmem_ld_wait();
+      for (int c = 0; c < HALF; c += 8) {
+        uint32_t u[8];
+        tmem_ld8(t_base + col0 + c, u);
+        tmem_ld_wait();
 #pragma unroll
-          for (int i = 0; i < 8; ++i) acc[(col0 + c + i) * PITCH + row] = __uint_as_float(u[i]);
-        }
-        // this CTA's share of the chunk's tokens
-        const int here = min(CHUNK, g.M - c0), c_lo = here * (int)rank / (int)cl, c_hi = here * ((int)rank + 1) / (int)cl;
-        ct_sync();
-        if (cl > 1) {
-          if (tid == 0) arrive_all(&b.peers_ready, (int)cl);
-          ok = !ct_any(!peers_wait(&b.peers_ready, parity, &b.abort, g.err));
-          if (!ok) break;
-        }
-        if (g.vec) {
-          for (int c = c_lo + (tid >> 4); c < c_hi; c += 16) {
-            float v[8] = {};
-            for (uint32_t r0 = 0; r0 < cl; r0 += 4) {   // in the order of the ranks, four in flight
-              float4 w[4][2];
+        for (int i = 0; i < 8; ++i) acc[(col0 + c + i) * PITCH + row] = __uint_as_float(u[i]);
+      }
+      // this CTA's share of the tokens
+      const int c_lo = g.M * (int)rank / (int)cl, c_hi = g.M * ((int)rank + 1) / (int)cl;
+      ct_sync();
+      if (cl > 1) {
+        if (tid == 0) arrive_all(&b.peers_ready, (int)cl);
+        ok = !ct_any(!peers_wait(&b.peers_ready, parity, &b.abort, g.err));
+        if (!ok) break;
+      }
+      if (g.vec) {
+        for (int c = c_lo + (tid >> 4); c < c_hi; c += 16) {
+          float v[8] = {};
+          for (uint32_t r0 = 0; r0 < cl; r0 += 4) {   // in the order of the ranks, four in flight
+            float4 w[4][2];
 #pragma unroll
-              for (uint32_t r = 0; r < 4; ++r) {
-                if (r0 + r >= cl) break;
-                const uint32_t at = peer_addr(smem_u32(acc + c * PITCH + q), r0 + r);
-                w[r][0] = peer_ld4(at);
-                w[r][1] = peer_ld4(at + 16);
-              }
-#pragma unroll
-              for (uint32_t r = 0; r < 4; ++r) {
-                if (r0 + r >= cl) break;
-                v[0] += w[r][0].x; v[1] += w[r][0].y; v[2] += w[r][0].z; v[3] += w[r][0].w;
-                v[4] += w[r][1].x; v[5] += w[r][1].y; v[6] += w[r][1].z; v[7] += w[r][1].w;
-              }
-            }
-            if (q < cols) finish8(g, v, bias, c0 + c, n0 + q);
-          }
-        } else {   // a token per warp, so that single elements still make whole sectors
-          for (int c = c_lo + warp - 2; c < c_hi; c += CW) {
-            const int64_t m = c0 + c;
-            float v[4] = {}, res[4] = {};
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              if (g.res != nullptr && lane + 32 * i < cols) res[i] = __bfloat162float(g.res[m * g.ld_res + n0 + lane + 32 * i]);
-            for (uint32_t r0 = 0; r0 < cl; r0 += 4) {
-              float w[4][4];
-#pragma unroll
-              for (uint32_t r = 0; r < 4; ++r) {
-                if (r0 + r >= cl) break;
-                const uint32_t at = peer_addr(smem_u32(acc + c * PITCH + lane), r0 + r);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) w[r][i] = peer_ld1(at + 128 * i);
-              }
-#pragma unroll
-              for (uint32_t r = 0; r < 4; ++r) {
-                if (r0 + r >= cl) break;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) v[i] += w[r][i];
-              }
+            for (uint32_t r = 0; r < 4; ++r) {
+              if (r0 + r >= cl) break;
+              const uint32_t at = peer_addr(smem_u32(acc + c * PITCH + q), r0 + r);
+              w[r][0] = peer_ld4(at);
+              w[r][1] = peer_ld4(at + 16);
             }
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int at = lane + 32 * i;
-              if (at >= cols) break;
-              const float z = v[i] + bias[i];
-              if (g.z != nullptr) g.z[m * g.ld_z + n0 + at] = __float2bfloat16_rn(z);
-              g.y[m * g.ld_y + n0 + at] = __float2bfloat16_rn(act_any_fast(g.act, z) + res[i]);
+            for (uint32_t r = 0; r < 4; ++r) {
+              if (r0 + r >= cl) break;
+              v[0] += w[r][0].x; v[1] += w[r][0].y; v[2] += w[r][0].z; v[3] += w[r][0].w;
+              v[4] += w[r][1].x; v[5] += w[r][1].y; v[6] += w[r][1].z; v[7] += w[r][1].w;
             }
           }
+          if (q < cols) finish8(g, v, bias, c, n0 + q);
         }
-        ct_sync();
-        // the peers have read this CTA's sums before they are written over (the last ones are not)
-        if (cl > 1 && (tile + step < g.tiles || c0 + CHUNK < g.M)) {
-          if (tid == 0) arrive_all(&b.peers_done, (int)cl);
-          ok = !ct_any(!peers_wait(&b.peers_done, parity, &b.abort, g.err));
-          if (!ok) break;
-          parity ^= 1u;
+      } else {   // a token per warp, so that single elements still make whole sectors
+        for (int c = c_lo + warp - 2; c < c_hi; c += CW) {
+          const int64_t m = c;
+          float v[4] = {}, res[4] = {};
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (g.res != nullptr && lane + 32 * i < cols) res[i] = __bfloat162float(g.res[m * g.ld_res + n0 + lane + 32 * i]);
+          for (uint32_t r0 = 0; r0 < cl; r0 += 4) {
+            float w[4][4];
+#pragma unroll
+            for (uint32_t r = 0; r < 4; ++r) {
+              if (r0 + r >= cl) break;
+              const uint32_t at = peer_addr(smem_u32(acc + c * PITCH + lane), r0 + r);
+#pragma unroll
+              for (int i = 0; i < 4; ++i) w[r][i] = peer_ld1(at + 128 * i);
+            }
+#pragma unroll
+            for (uint32_t r = 0; r < 4; ++r) {
+              if (r0 + r >= cl) break;
+#pragma unroll
+              for (int i = 0; i < 4; ++i) v[i] += w[r][i];
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int at = lane + 32 * i;
+            if (at >= cols) break;
+            const float z = v[i] + bias[i];
+            if (g.z != nullptr) g.z[m * g.ld_z + n0 + at] = __float2bfloat16_rn(z);
+            g.y[m * g.ld_y + n0 + at] = __float2bfloat16_rn(act_any_fast(g.act, z) + res[i]);
+          }
         }
+      }
+      ct_sync();
+      // the peers have read this CTA's sums before they are written over (the last ones are not)
+      if (cl > 1 && tile + step < g.tiles) {
+        if (tid == 0) arrive_all(&b.peers_done, (int)cl);
+        ok = !ct_any(!peers_wait(&b.peers_done, parity, &b.abort, g.err));
+        if (!ok) break;
+        parity ^= 1u;
       }
       tc_fence_before();
       __syncwarp();
@@ -291,8 +288,10 @@ int resident(int c, int num_sms) {
 
 template <int NT>
 int launch_nt(LinearStream& g, const GemmArgs& a, int num_sms, cudaStream_t st) {
-  // The cluster size that leaves a CTA the least to load. A join costs about as much as kJoin bytes.
-  constexpr int64_t kJoin = 48 << 10;
+  // The cluster size with the least time for a CTA, in bytes of its share of the stream (45 a ns): a K
+  // block takes as long as kBlock bytes at least (0.16 us), a join as long as kJoin (1.7 us).
+  // M = 8, 2048 x 2048: 6.4 us by 8 CTAs, 8.1 by one; M = 1, N = 7680, K = 2048: 9.5 by 2, 8.9 by one.
+  constexpr int64_t kBlock = 7 << 10, kJoin = 76 << 10;
   int best = 0, best_rows = 0, best_tiles = 0, best_clusters = 0;
   int64_t best_cost = 0;
   for (int c = 1; c <= 8; c *= 2) {
@@ -303,7 +302,8 @@ int launch_nt(LinearStream& g, const GemmArgs& a, int num_sms, cudaStream_t st) 
     int rows = (g.N + ncl * per - 1) / (ncl * per);
     rows = (rows + 7) & ~7;                                      // whole vectors of outputs
     const int tiles = (g.N + rows - 1) / rows;
-    const int64_t cost = (int64_t)per * ((g.nkb + c - 1) / c * (int64_t)(rows + NT) * BK * 2 + (c > 1 ? kJoin : 0));
+    const int64_t block = (int64_t)(rows + NT) * BK * 2;
+    const int64_t cost = per * ((g.nkb + c - 1) / c * (block > kBlock ? block : kBlock) + (c > 1 ? kJoin : 0));
     if (best == 0 || cost < best_cost) {
       best = c;
       best_cost = cost;

@@ -49,7 +49,7 @@ int launch_decode_simt(const DecodeArgs& a, int num_sms, cudaStream_t st);
 struct LinearLayout {
   size_t dz;         // [M][ld_dz] the pre-activation's gradient, dims->dtype
   size_t db_part;    // [kDbSplit][N] fp32
-  size_t part;       // partial sums of products with a divided K
+  size_t part;       // fp32 partial sums of products with a divided K
   int64_t ld_dz;
   size_t total;
 };
@@ -76,8 +76,9 @@ struct GemmArgs {
   int64_t ldc;
   int dtype;
 };
-constexpr int kMaxSplit = 16, kBlocks = 3;   // of the FMA products: shares of a divided K, blocks for an SM
-inline size_t gemm_simt_part_bytes() { return (size_t)kBlocks * kMaxStreamCtas * 128 * 64 * 4; }
+// The FMA products: shares of a divided K, and of all tiles; fp32 partial sums [tile][share][128][64].
+constexpr int kMaxSplit = 32, kMaxShares = 1024;
+size_t gemm_simt_part_bytes(int64_t M, int64_t N, int64_t K);
 cudaError_t launch_gemm_simt(const GemmArgs& g, float* part, int num_sms, cudaStream_t st);
 // The bf16 products on CTA pairs. LINEAR_FWD: A and B K-major; DX: B MN-major; DW: both. Base
 // pointers 16-byte aligned, row strides multiples of 8 elements.
@@ -86,8 +87,10 @@ constexpr int kMaxPairs = 80;     // clusters of two CTAs
 constexpr int kMinRun = 4;        // K blocks of a pair's run when there are fewer tiles than pairs
 size_t linear_pair_part_bytes();
 int launch_linear_pair(int kind, const GemmArgs& a, uint8_t* ws, size_t part, int num_sms, cudaStream_t st);
-// The forward product for at most kStreamRows rows, as a stream of the weights.
-constexpr int kStreamRows = 128;
+// The forward product for at most kStreamRows rows, as a stream of the weights (N = 7680, K = 2048, 64
+// rows: 11.1 us, 12.4 on pairs; N = 32768, K = 1024, 128 rows: 23.4, 20.3), for up to kStreamRowsLong if
+// K is kStreamLong or more (N = K = 7680, 128 rows: 29.3, 35.4; N = 2048, K = 2816: 11.8, 12.1).
+constexpr int kStreamRows = 64, kStreamRowsLong = 128, kStreamLong = 2800;
 int launch_linear_stream(const GemmArgs& a, uint8_t* ws, int num_sms, cudaStream_t st);
 // dz = dy * act'(z) (dz may be NULL: sums only) and db (may be NULL); z and dz have ld_dz = N rounded
 // up to a multiple of 8 elements between rows

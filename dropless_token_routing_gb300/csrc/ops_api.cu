@@ -31,8 +31,11 @@ LinearLayout linear_layout(const moe_linear_dims& d) {
   L.dz = kOpHeader;
   L.db_part = L.dz + round256((size_t)d.M * L.ld_dz * elt_bytes(d.dtype));
   L.part = L.db_part + round256(4 * (size_t)kDbSplit * d.N);
-  const size_t simt = gemm_simt_part_bytes(), pair = d.dtype == MOE_BF16 ? linear_pair_part_bytes() : 0;
-  L.total = L.part + (simt > pair ? simt : pair);
+  size_t part = d.dtype == MOE_BF16 ? linear_pair_part_bytes() : 0;
+  const size_t simt[3] = {gemm_simt_part_bytes(d.M, d.N, d.K), gemm_simt_part_bytes(d.M, d.K, d.N),
+                          gemm_simt_part_bytes(d.N, d.K, d.M)};   // y, dx, dw
+  for (size_t s : simt) part = s > part ? s : part;
+  L.total = L.part + part;
   return L;
 }
 
@@ -91,7 +94,7 @@ int resolve_linear(const moe_linear_dims* in, moe_linear_dims* d) {
 int run_gemm(int kind, const GemmArgs& g, uint8_t* ws, const LinearLayout& L, int sms, cudaStream_t st) {
   const int64_t lda = g.ak == 1 ? g.am : g.ak, ldb = g.bk == 1 ? g.bn : g.bk;
   if (g.dtype == MOE_BF16 && lda % 8 == 0 && ldb % 8 == 0) {
-    if (kind == LINEAR_FWD && g.M <= kStreamRows) return launch_linear_stream(g, ws, sms, st);
+    if (kind == LINEAR_FWD && g.M <= (g.K >= kStreamLong ? kStreamRowsLong : kStreamRows)) return launch_linear_stream(g, ws, sms, st);
     return launch_linear_pair(kind, g, ws, L.part, sms, st);
   }
   return launch_gemm_simt(g, reinterpret_cast<float*>(ws + L.part), sms, st) == cudaSuccess ? MOE_OK : MOE_ERR_LAUNCH;

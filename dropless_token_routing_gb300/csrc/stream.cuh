@@ -37,9 +37,8 @@ constexpr int MAX_STAGES = 12;
 
 template <int NT> struct Cfg {
   static constexpr int STAGE = A_BYTES + NT * BK * 2;
-  static constexpr int CHUNK = NT < 64 ? NT : 64;                 // token columns staged at once
-  static constexpr int ACC_BYTES = CHUNK * PITCH * 4;
-  static constexpr int TMEM = 2 * NT < 32 ? 32 : 2 * NT;          // NT is a power of two
+  static constexpr int ACC_BYTES = NT * PITCH * 4;
+  static constexpr int TMEM = 2 * NT;                             // NT is a power of two, 16 at least
   // stages that fit beside the staged result and `extra` bytes of tables
   static constexpr int stages(int extra) {
     const int n = (227 * 1024 - 2048 - ACC_BYTES - extra) / STAGE;
@@ -278,15 +277,15 @@ __device__ __forceinline__ bool mma_run(Bars& b, uint32_t smem_base, Run run, Ri
 }
 
 // The part of the CT threads in a run. `flags` and `part` are this run's (one word, NT * 128
-// floats per CTA; with `scatter` two of each). f.prepare(t) runs before, f.finish(t, c0, acc) after token columns
-// [c0, c0 + CHUNK) of tile t are staged: acc[(column - c0) * PITCH + weight row].
+// floats per CTA; with `scatter` two of each). f.prepare(t) runs before, f.finish(t, acc) after tile t is
+// staged: acc[column * PITCH + weight row].
 // scatter: tiles that many CTAs share (an output's, few and with a long K) are joined by all of them,
 // each a share of the result (f.out4(t, column, row, sum of 4 rows)): one CTA adding up 37 others'
 // parts took 25 us.
 template <int NT, class F>
 __device__ __forceinline__ bool take_run(Bars& b, Run run, int& it, int cta, uint32_t* flags, uint32_t epoch, float* part,
                                          float* acc, int* err, F& f, bool scatter) {
-  constexpr int CHUNK = Cfg<NT>::CHUNK, HALF = CHUNK / 2;
+  constexpr int HALF = NT / 2;
   const int cw = (threadIdx.x >> 5) - 2, lane = threadIdx.x & 31, lg = (threadIdx.x >> 5) & 3;
   const int row = lg * 32 + lane, col0 = (cw >> 2) * HALF;
   int64_t shared_tile[2];   // divided tiles of this CTA (scatter): a run has two at most
@@ -307,52 +306,47 @@ __device__ __forceinline__ bool take_run(Bars& b, Run run, int& it, int cta, uin
     __syncwarp();   // the TMEM loads are for whole warps
     tc_fence_after();
     const uint32_t t_base = b.tmem + ((uint32_t)(lg * 32) << 16) + (uint32_t)(buf * NT);
-#pragma unroll 1
-    for (int c0 = 0; c0 < NT; c0 += CHUNK) {
-      uint32_t u[HALF / 8][8];
+    uint32_t u[HALF / 8][8];
 #pragma unroll
-      for (int c = 0; c < HALF / 8; ++c) tmem_ld8(t_base + c0 + col0 + 8 * c, u[c]);
-      tmem_ld_wait();
+    for (int c = 0; c < HALF / 8; ++c) tmem_ld8(t_base + col0 + 8 * c, u[c]);
+    tmem_ld_wait();
 #pragma unroll
-      for (int c = 0; c < HALF; c += 8) {
-        const int col = c0 + col0 + c;
-        float v[8];
+    for (int c = 0; c < HALF; c += 8) {
+      const int col = col0 + c;
+      float v[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(u[c / 8][i]);
-        if (owner) {
-#pragma unroll 1
-          for (int q = q0; q < cta; q += 4) {   // four CTAs' parts in flight, added in order
-            const float* in = part + ((int64_t)q * NT + col) * BM + row;
-            float w[4][8];
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-#pragma unroll
-              for (int i = 0; i < 8; ++i) w[j][i] = q + j < cta ? __ldcg(in + (j * NT + i) * BM) : 0.f;
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-#pragma unroll
-              for (int i = 0; i < 8; ++i) v[i] += w[j][i];
-          }
-#pragma unroll
-          for (int i = 0; i < 8; ++i) acc[(col0 + c + i) * PITCH + row] = v[i];
-        } else {
-          float* out = part + ((int64_t)slot * NT + col) * BM + row;
-#pragma unroll
-          for (int i = 0; i < 8; ++i) __stcg(out + i * BM, v[i]);
-        }
-      }
-      if (c0 + CHUNK >= NT) {   // the accumulator is read: the next part may use it
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&b.tempty[buf]));
-      }
+      for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(u[c / 8][i]);
       if (owner) {
-        ct_sync();
-        f.finish(run.s.t, c0, acc);
-        ct_sync();
+#pragma unroll 1
+        for (int q = q0; q < cta; q += 4) {   // four CTAs' parts in flight, added in order
+          const float* in = part + ((int64_t)q * NT + col) * BM + row;
+          float w[4][8];
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) w[j][i] = q + j < cta ? __ldcg(in + (j * NT + i) * BM) : 0.f;
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] += w[j][i];
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) acc[(col + i) * PITCH + row] = v[i];
+      } else {
+        float* out = part + ((int64_t)slot * NT + col) * BM + row;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) __stcg(out + i * BM, v[i]);
       }
     }
-    if (!owner) {
+    // the accumulator is read: the next part may use it
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_u32(&b.tempty[buf]));
+    if (owner) {
+      ct_sync();
+      f.finish(run.s.t, acc);
+      ct_sync();
+    } else {
       __threadfence();
       ct_sync();
       if (threadIdx.x == 64) st_release(flags + slot, epoch);

@@ -1,5 +1,4 @@
-// The linear layer on the FMA pipes: products of any type, size, stride and alignment, and the
-// elementwise half of its backward.
+// The linear layer's fp32 products, on the FMA pipes, and the elementwise half of its backward.
 #include "act.cuh"
 #include "launch.cuh"
 #include "ops.h"
@@ -11,13 +10,12 @@ namespace {
 constexpr int GM = 128, GN = 64, GK = 16, GT = 128;
 
 // bias, z, activation, residual of one element and its way out.
-template <typename T>
 __device__ __forceinline__ void finish_element(const GemmArgs& g, int64_t m, int n, float v) {
-  if (g.bias != nullptr) v += to_f32(static_cast<const T*>(g.bias)[n]);
-  if (g.z_out != nullptr) static_cast<T*>(g.z_out)[m * g.ld_z + n] = from_f32<T>(v);
+  if (g.bias != nullptr) v += static_cast<const float*>(g.bias)[n];
+  if (g.z_out != nullptr) static_cast<float*>(g.z_out)[m * g.ld_z + n] = v;
   v = act_any(g.act, v);
-  if (g.res != nullptr) v += to_f32(static_cast<const T*>(g.res)[m * g.ld_res + n]);
-  static_cast<T*>(g.c)[m * g.ldc + n] = from_f32<T>(v);
+  if (g.res != nullptr) v += static_cast<const float*>(g.res)[m * g.ld_res + n];
+  static_cast<float*>(g.c)[m * g.ldc + n] = v;
 }
 
 // Two fp32 FMAs in one instruction (1024 x 1024 x 1024: 63 us, 68 with single ones).
@@ -33,9 +31,9 @@ __device__ __forceinline__ void fma_pair(uint64_t& d, uint64_t a, uint64_t b) {
 // A thread's share of an R x 16 operand tile: single elements, which any stride and alignment
 // allows. KC: k is the contiguous index (16 lanes along k, rows 8 apart), else the row is (64 lanes
 // along the rows, k two apart).
-template <typename T, bool KC, int R> struct Operand {
+template <bool KC, int R> struct Operand {
   static constexpr int N = R * GK / GT, H = R / 64;   // elements; rows of a lane where rows are contiguous
-  const T* p;          // this thread's first element at the present k
+  const float* p;      // this thread's first element at the present k
   int64_t rs, ks;
   int row0, k;         // its first row in the tile, its first k in the block
   int rows;            // rows of the tile that exist
@@ -45,7 +43,7 @@ template <typename T, bool KC, int R> struct Operand {
     rows = (int)(total - row < R ? total - row : R);
     rs = rs_;
     ks = ks_;
-    p = static_cast<const T*>(base) + (row + row0) * rs + (k0 + k) * ks;
+    p = static_cast<const float*>(base) + (row + row0) * rs + (k0 + k) * ks;
   }
   __device__ __forceinline__ static int row_of(int i) { return KC ? 8 * i : i % H * 64; }
   __device__ __forceinline__ static int k_of(int i) { return KC ? 0 : i / H * 2; }
@@ -54,7 +52,7 @@ template <typename T, bool KC, int R> struct Operand {
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       const bool in = row0 + row_of(i) < rows && k + k_of(i) < left;
-      r[i] = in ? to_f32(p[row_of(i) * rs + k_of(i) * ks]) : 0.f;
+      r[i] = in ? p[row_of(i) * rs + k_of(i) * ks] : 0.f;
     }
     p += GK * ks;
   }
@@ -68,7 +66,7 @@ template <typename T, bool KC, int R> struct Operand {
 // tiles of fp32 sums), 8 x 8 of it per thread in quarters of 4 x 4: 4 shared-memory vectors per 64 FMAs
 // (with 8 x 4 the shared memory was the limit). The next 16 of K are loaded into registers while
 // the present ones are multiplied.
-template <typename T, bool AK, bool BK, bool SPLIT>
+template <bool AK, bool BK, bool SPLIT>
 __global__ void __launch_bounds__(GT) gemm_simt_kernel(const GemmArgs g, float* part) {
   __shared__ __align__(16) float As[2][GK][GM + 4];
   __shared__ __align__(16) float Bs[2][GK][GN + 4];
@@ -82,8 +80,8 @@ __global__ void __launch_bounds__(GT) gemm_simt_kernel(const GemmArgs g, float* 
     k_lo = per * blockIdx.z < g.K ? per * blockIdx.z : g.K;
     k_hi = k_lo + per < g.K ? k_lo + per : g.K;
   }
-  Operand<T, AK, GM> A(g.a, m0, k_lo, g.am, g.ak, g.M, tid);
-  Operand<T, BK, GN> B(g.b, n0, k_lo, g.bn, g.bk, g.N, tid);
+  Operand<AK, GM> A(g.a, m0, k_lo, g.am, g.ak, g.M, tid);
+  Operand<BK, GN> B(g.b, n0, k_lo, g.bn, g.bk, g.N, tid);
   float ra[A.N], rb[B.N];
   uint64_t acc[8][4] = {};   // pairs of columns
   A.load(ra, k_hi - k_lo);
@@ -139,7 +137,7 @@ __global__ void __launch_bounds__(GT) gemm_simt_kernel(const GemmArgs g, float* 
     for (int j = 0; j < 8; ++j) {
       const int n = n0 + j / 4 * 32 + tx * 4 + j % 4;
       if (n >= g.N) continue;
-      finish_element<T>(g, m, n, __uint_as_float((uint32_t)(acc[i][j / 2] >> (j % 2 * 32))));
+      finish_element(g, m, n, __uint_as_float((uint32_t)(acc[i][j / 2] >> (j % 2 * 32))));
     }
   }
 }
@@ -148,7 +146,6 @@ __global__ void __launch_bounds__(GT) gemm_simt_kernel(const GemmArgs g, float* 
 // lets the next one start early: its blocks would then fill the SMs that are free first, several on
 // one. 256 x 256 x 1024: 8.0 us, 16.4 if this one does.)
 constexpr int JR = 8;   // rows of a block
-template <typename T>
 __global__ void __launch_bounds__(32 * JR) gemm_join_kernel(const GemmArgs g, const float* __restrict__ part, int split) {
   const int lane = threadIdx.x & 31, r = blockIdx.z * JR + (threadIdx.x >> 5);
   const int64_t m = (int64_t)blockIdx.x * GM + r;
@@ -170,15 +167,15 @@ __global__ void __launch_bounds__(32 * JR) gemm_join_kernel(const GemmArgs g, co
   }
 #pragma unroll
   for (int h = 0; h < 2; ++h)
-    if (n + 32 * h < g.N) finish_element<T>(g, m, n + 32 * h, v[h]);
+    if (n + 32 * h < g.N) finish_element(g, m, n + 32 * h, v[h]);
 }
 
 // The layouts of the layer's products: forward (both operands along k), dX, dW.
-template <typename T, bool SPLIT>
+template <bool SPLIT>
 void gemm_layouts(const GemmArgs& g, float* part, const dim3& grid, cudaStream_t st) {
-  if (g.ak == 1 && g.bk == 1) launch_pdl(gemm_simt_kernel<T, true, true, SPLIT>, grid, GT, 0, 1, st, g, part);
-  else if (g.ak == 1) launch_pdl(gemm_simt_kernel<T, true, false, SPLIT>, grid, GT, 0, 1, st, g, part);
-  else launch_pdl(gemm_simt_kernel<T, false, false, SPLIT>, grid, GT, 0, 1, st, g, part);
+  if (g.ak == 1 && g.bk == 1) launch_pdl(gemm_simt_kernel<true, true, SPLIT>, grid, GT, 0, 1, st, g, part);
+  else if (g.ak == 1) launch_pdl(gemm_simt_kernel<true, false, SPLIT>, grid, GT, 0, 1, st, g, part);
+  else launch_pdl(gemm_simt_kernel<false, false, SPLIT>, grid, GT, 0, 1, st, g, part);
 }
 
 // The shares of K, by the time of the busiest SM (us). Measured: 16 of K of one block take 1.33 us, of two
@@ -197,18 +194,6 @@ int simt_split(int64_t tiles, int64_t K, int num_sms) {
     }
   }
   return best;
-}
-
-template <typename T>
-void gemm_simt(const GemmArgs& g, float* part, int num_sms, cudaStream_t st) {
-  const int64_t tm = (g.M + GM - 1) / GM, tn = (g.N + GN - 1) / GN, tiles = tm * tn;
-  const int split = simt_split(tiles, g.K, num_sms);
-  if (split <= 1) {
-    gemm_layouts<T, false>(g, nullptr, dim3((unsigned)tm, (unsigned)tn), st);
-    return;
-  }
-  gemm_layouts<T, true>(g, part, dim3((unsigned)tm, (unsigned)tn, split), st);
-  launch_pdl(gemm_join_kernel<T>, dim3((unsigned)tm, (unsigned)tn, GM / JR), 32 * JR, 0, 1, st, g, part, split);
 }
 
 // dz = dy * act'(z), and its column sums. 8 columns per thread, `lx` threads side by side (a row's
@@ -324,14 +309,20 @@ cudaError_t linear_dz(const void* dy, int64_t ld_dy, const void* z, int act, int
 
 size_t gemm_simt_part_bytes(int64_t M, int64_t N, int64_t K) {
   const int64_t tiles = ((M + GM - 1) / GM) * ((N + GN - 1) / GN), most = K / (2 * GK) < kMaxSplit ? K / (2 * GK) : kMaxSplit;
-  if (most < 2 || 2 * tiles > kMaxShares) return 0;
+  if (most < 2) return 0;
   return (size_t)(tiles * most < kMaxShares ? tiles * most : kMaxShares) * GM * GN * 4;
 }
 
 cudaError_t launch_gemm_simt(const GemmArgs& g, float* part, int num_sms, cudaStream_t st) {
+  const int64_t tm = (g.M + GM - 1) / GM, tn = (g.N + GN - 1) / GN;
+  const int split = simt_split(tm * tn, g.K, num_sms);
   TraceScope ts(TP_LINEAR, st);
-  if (g.dtype == MOE_F32) gemm_simt<float>(g, part, num_sms, st);
-  else gemm_simt<__nv_bfloat16>(g, part, num_sms, st);
+  if (split <= 1) {
+    gemm_layouts<false>(g, nullptr, dim3((unsigned)tm, (unsigned)tn), st);
+  } else {
+    gemm_layouts<true>(g, part, dim3((unsigned)tm, (unsigned)tn, split), st);
+    launch_pdl(gemm_join_kernel, dim3((unsigned)tm, (unsigned)tn, GM / JR), 32 * JR, 0, 1, st, g, part, split);
+  }
   return cudaGetLastError();
 }
 

@@ -50,7 +50,8 @@ struct LinearLayout {
   size_t dz;         // [M][ld_dz] the pre-activation's gradient, dims->dtype
   size_t db_part;    // [kDbSplit][N] fp32
   size_t part;       // fp32 partial sums of products with a divided K
-  int64_t ld_dz;
+  size_t x_copy, w_copy;   // bf16 [M][ld_copy], [N][ld_copy] for rows that are not whole vectors
+  int64_t ld_dz, ld_copy;
   size_t total;
 };
 constexpr int kDbSplit = 256;
@@ -76,9 +77,9 @@ struct GemmArgs {
   int64_t ldc;
   int dtype;
 };
-// The FMA products: shares of a divided K, and of all tiles; fp32 partial sums [tile][share][128][64].
+// The FMA products (fp32): shares of a divided K, and of all tiles; fp32 partial sums [tile][share][128][64].
 constexpr int kMaxSplit = 32, kMaxShares = 1024;
-size_t gemm_simt_part_bytes(int64_t M, int64_t N, int64_t K);
+size_t gemm_simt_part_bytes(int64_t M, int64_t N, int64_t K);   // enough for smaller ones too
 cudaError_t launch_gemm_simt(const GemmArgs& g, float* part, int num_sms, cudaStream_t st);
 // The bf16 products on CTA pairs. LINEAR_FWD: A and B K-major; DX: B MN-major; DW: both. Base
 // pointers 16-byte aligned, row strides multiples of 8 elements.

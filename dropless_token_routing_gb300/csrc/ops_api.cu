@@ -31,11 +31,19 @@ LinearLayout linear_layout(const moe_linear_dims& d) {
   L.dz = kOpHeader;
   L.db_part = L.dz + round256((size_t)d.M * L.ld_dz * elt_bytes(d.dtype));
   L.part = L.db_part + round256(4 * (size_t)kDbSplit * d.N);
-  size_t part = d.dtype == MOE_BF16 ? linear_pair_part_bytes() : 0;
-  const size_t simt[3] = {gemm_simt_part_bytes(d.M, d.N, d.K), gemm_simt_part_bytes(d.M, d.K, d.N),
-                          gemm_simt_part_bytes(d.N, d.K, d.M)};   // y, dx, dw
-  for (size_t s : simt) part = s > part ? s : part;
-  L.total = L.part + part;
+  if (d.dtype == MOE_BF16) {
+    L.ld_copy = (d.K + 7) & ~7ll;
+    L.x_copy = L.part + round256(linear_pair_part_bytes());
+    L.w_copy = L.x_copy + round256(2 * (size_t)d.M * L.ld_copy);   // a call's x may have any stride
+    L.total = L.w_copy + (d.ld_w % 8 != 0 ? round256(2 * (size_t)d.N * L.ld_copy) : 0);
+  } else {
+    size_t part = 0;
+    const size_t simt[3] = {gemm_simt_part_bytes(d.M, d.N, d.K), gemm_simt_part_bytes(d.M, d.K, d.N),
+                            gemm_simt_part_bytes(d.N, d.K, d.M)};   // y, dx, dw
+    for (size_t s : simt) part = s > part ? s : part;
+    L.ld_copy = 0;
+    L.x_copy = L.w_copy = L.total = L.part + part;
+  }
   return L;
 }
 
@@ -89,11 +97,22 @@ int resolve_linear(const moe_linear_dims* in, moe_linear_dims* d) {
   return MOE_OK;
 }
 
-// One product of the layer. bf16 with row strides that the TMA takes (whole 16-byte vectors) goes
-// to the tensor cores, everything else to the FMA pipes.
+// x or w with a row stride that the TMA takes: bf16 rows that are not whole 16-byte vectors are copied
+// to such first (300 x 700 x 1001: 10.6 us, 17.9 with single elements on the FMA pipes; 4096 x 2816 x
+// 2047: 41 us, 1043).
+int whole_vectors(const void** p, int64_t* ld, int64_t rows, const moe_linear_dims& d, int64_t ld_copy, uint8_t* copy,
+                  cudaStream_t st) {
+  if (d.dtype != MOE_BF16 || *ld % 8 == 0) return MOE_OK;
+  if (launch_linear_dz(*p, *ld, nullptr, MOE_ACT_NONE, rows, d.K, d.dtype, copy, ld_copy, nullptr, nullptr, st) != cudaSuccess)
+    return MOE_ERR_LAUNCH;
+  *p = copy;
+  *ld = ld_copy;
+  return MOE_OK;
+}
+
+// One product of the layer: bf16 on the tensor cores, fp32 on the FMA pipes.
 int run_gemm(int kind, const GemmArgs& g, uint8_t* ws, const LinearLayout& L, int sms, cudaStream_t st) {
-  const int64_t lda = g.ak == 1 ? g.am : g.ak, ldb = g.bk == 1 ? g.bn : g.bk;
-  if (g.dtype == MOE_BF16 && lda % 8 == 0 && ldb % 8 == 0) {
+  if (g.dtype == MOE_BF16) {
     if (kind == LINEAR_FWD && g.M <= (g.K >= kStreamLong ? kStreamRowsLong : kStreamRows)) return launch_linear_stream(g, ws, sms, st);
     return launch_linear_pair(kind, g, ws, L.part, sms, st);
   }
@@ -177,10 +196,15 @@ int moe_linear_fwd(const void* x, const void* w, const void* bias, const void* r
   OP_TRY(opt(z));
   OP_TRY(req_if(y, some));
   if (!some) return MOE_OK;
-  GemmArgs g = {x, w, d.ld_x, 1, d.ld_w, 1, d.M, d.N, d.K, bias, residual, d.ld_res, d.act, z, L.ld_dz, y, d.ld_y, d.dtype};
   const int sms = num_sms();
   if (sms == 0) return MOE_ERR_CUDA;
-  return run_gemm(LINEAR_FWD, g, static_cast<uint8_t*>(ws), L, sms, (cudaStream_t)stream);
+  uint8_t* base = static_cast<uint8_t*>(ws);
+  const cudaStream_t st = (cudaStream_t)stream;
+  int64_t ld_x = d.ld_x, ld_w = d.ld_w;
+  OP_TRY(whole_vectors(&x, &ld_x, d.M, d, L.ld_copy, base + L.x_copy, st));
+  OP_TRY(whole_vectors(&w, &ld_w, d.N, d, L.ld_copy, base + L.w_copy, st));
+  GemmArgs g = {x, w, ld_x, 1, ld_w, 1, d.M, d.N, d.K, bias, residual, d.ld_res, d.act, z, L.ld_dz, y, d.ld_y, d.dtype};
+  return run_gemm(LINEAR_FWD, g, base, L, sms, st);
 }
 
 int moe_linear_bwd(const void* x, const void* w, const void* z, const void* dy, const moe_linear_dims* dims, void* dx,
@@ -218,11 +242,15 @@ int moe_linear_bwd(const void* x, const void* w, const void* z, const void* dy, 
       return MOE_ERR_LAUNCH;
   }
   if (dx != nullptr) {   // dx [M, K] = dz W: contraction over N
-    GemmArgs g = {dz, w, ld_dz, 1, 1, d.ld_w, d.M, d.K, d.N, nullptr, nullptr, 0, MOE_ACT_NONE, nullptr, 0, dx, d.ld_x, d.dtype};
+    int64_t ld_w = d.ld_w;
+    OP_TRY(whole_vectors(&w, &ld_w, d.N, d, L.ld_copy, base + L.w_copy, st));
+    GemmArgs g = {dz, w, ld_dz, 1, 1, ld_w, d.M, d.K, d.N, nullptr, nullptr, 0, MOE_ACT_NONE, nullptr, 0, dx, d.ld_x, d.dtype};
     OP_TRY(run_gemm(LINEAR_DX, g, base, L, sms, st));
   }
   if (dw != nullptr) {   // dw [N, K] = dz^T x: contraction over M
-    GemmArgs g = {dz, x, 1, ld_dz, 1, d.ld_x, d.N, d.K, d.M, nullptr, nullptr, 0, MOE_ACT_NONE, nullptr, 0, dw, d.ld_w, d.dtype};
+    int64_t ld_x = d.ld_x;
+    OP_TRY(whole_vectors(&x, &ld_x, d.M, d, L.ld_copy, base + L.x_copy, st));
+    GemmArgs g = {dz, x, 1, ld_dz, 1, ld_x, d.N, d.K, d.M, nullptr, nullptr, 0, MOE_ACT_NONE, nullptr, 0, dw, d.ld_w, d.dtype};
     OP_TRY(run_gemm(LINEAR_DW, g, base, L, sms, st));
   }
   return MOE_OK;

@@ -391,7 +391,9 @@ typedef struct moe_linear_dims {
  * NULL.
  * fp32 accumulation, y rounded once (not from the rounded z). residual may be the buffer of y
  * (y updated in place) when their strides agree. Base pointers are 16-byte aligned; strides and
- * widths may be odd. M == 0 is a no-op. */
+ * widths may be odd (bf16 rows of x and w that are not whole 16-byte vectors are copied in every
+ * call). M == 0 is a no-op. A workspace for M rows serves fewer rows, any act and any stride of x, y
+ * and residual. */
 size_t moe_linear_workspace_bytes(const moe_linear_dims* dims);
 int moe_linear_fwd(const void* x, const void* w, const void* bias, const void* residual,
                    const moe_linear_dims* dims, void* z, void* y, void* ws, size_t ws_bytes,

@@ -637,3 +637,19 @@ def test_wrappers_refuse_what_does_not_fit():
                       ("draft_probs", torch.zeros(2, 16, 3).cuda().transpose(1, 2))):
         with pytest.raises(ValueError):
             ver.verify(**{**good, name: bad})
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_linear_made_for_many_rows_used_with_few(dtype):
+    A = _api()
+    N, K = 1500, 333
+    g = _gen(9)
+    w = _rand(g, N, K, std=K ** -0.5, dtype=dtype)
+    lin = A.Linear(w.cuda(), None, act="relu", max_rows=6000)
+    for M in (100, 1, 6000, 700):
+        x, dy = _rand(g, M, K, dtype=dtype), _rand(g, M, N, dtype=dtype)
+        y, ref = _linear64(x, w, None, None, "relu", dy)
+        _close(lin.forward(x.cuda(), save=True), y, dtype)
+        grads = lin.backward(dy.cuda())
+        _close(grads["dw"], ref["dw"], dtype)
+        _close(grads["dx"], ref["dx"], dtype)

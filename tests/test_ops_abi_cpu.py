@@ -139,3 +139,17 @@ def test_verify_pointers():
     assert call(verify_dims(dtype=9)) == C["MOE_ERR_UNSUPPORTED_DTYPE"]
     assert call(verify_dims(n=0), tokens=None, q=None, u=None, p=None) == null
     assert call(verify_dims(B=0), **dict.fromkeys(("tokens", "q", "p", "u", "us", "out", "acc"))) == 0
+
+
+@pytest.mark.parametrize("dtype", [N.MOE_F32, N.MOE_BF16])
+@pytest.mark.parametrize("width", [(64, 64), (1001, 777), (4096, 2048), (200, 100000)])
+def test_linear_workspace_serves_fewer_rows(dtype, width):
+    """A workspace for M rows is large enough for fewer, with any stride of x and y."""
+    last = 0
+    for M in (0, 1, 64, 65, 128, 129, 700, 1024, 5000, 9000, 100000):
+        dims = N.LinearDims(M, *width, 0, dtype, 0, 0, 0, 0)
+        need = L.moe_linear_workspace_bytes(ctypes.byref(dims))
+        odd = N.LinearDims(M, *width, 4, dtype, width[1] + 3, 0, width[0] + 1, 0)
+        assert need == L.moe_linear_workspace_bytes(ctypes.byref(odd))
+        assert need >= last > 0 or M == 0
+        last = need

@@ -16,7 +16,13 @@
 // hidden rows need; only their token operands wait.
 //
 // h times its gate is rounded to bf16 once (it is an MMA operand; the training path rounds the
-// same product for its dW), y once.
+// same product for its dW), y once. Scores, gates and all sums are fp32.
+//
+// Bound by the stream out of HBM, and with few bytes by the chain scores - selection - hidden rows -
+// output, whose steps each wait for all CTAs. Measured: T = 32, d = 7168, 81 experts read:
+// 7.16 GB in 1.06-1.10 ms, 6.5-6.7 TB/s (the copy rate is 6.8); T = 1, d = 7680, 9 experts:
+// 857 MB in 145 us, 5.9 TB/s; T = 5, d = 2048, 26 experts: 460 MB in 89 us, 5.2 TB/s; T = 10, d =
+// 448: 1.8 MB in 22 us, all of it the chain.
 #include <string.h>
 
 #include <mutex>

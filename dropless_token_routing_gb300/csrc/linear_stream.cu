@@ -6,7 +6,12 @@
 // that all clusters have the same number of tiles, and its CTAs each a share of K. They join their
 // sums through distributed shared memory, each CTA finishing a share of the token columns: a
 // join through global memory costs fences, flags and loads of about 2 us each behind the stream.
-// The host picks the cluster size that gives a CTA the fewest bytes to load (weights and tokens).
+// The host picks the cluster size with the least time for a CTA's share (launch_nt).
+//
+// z and y are rounded to bf16 from the fp32 sum, each once. Bound by HBM for large W, by the launch
+// and the join (5 us together) for small ones: M = 16, 7680 x 7680: 22.5 us, 5.3 TB/s; M = 37, N =
+// 4097, K = 7168: 15.4 us, 3.9 TB/s; M = 1, N = 7680, K = 2048: 8.6 us, 3.6 TB/s; M = 1, 1000 x 512:
+// 3.8 us.
 #include <string.h>
 
 #include <mutex>

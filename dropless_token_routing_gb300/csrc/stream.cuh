@@ -5,9 +5,9 @@
 // With few tokens a product is a stream of weights out of HBM, and everything here serves that
 // stream. The weights are the MMA's A operand, 128 weight rows by 64 of K per stage; the tokens
 // are B, NT (16 .. 128) rows; the transposed result, 128 weight rows by NT tokens, accumulates in
-// tensor memory, two accumulators deep. One thread issues TMA loads into a ring that fills the
+// tensor memory, two accumulators deep. One warp issues TMA loads into a ring that fills the
 // shared memory (about 190 KB in flight per SM, four times what the HBM's latency needs), one
-// thread issues tcgen05.mma, eight warps take the results out.
+// issues tcgen05.mma, eight warps take the results out.
 //
 // The K blocks of all tiles are divided evenly over the CTAs whatever the tile count (a "run" of
 // blocks each), so that every SM streams the same number of bytes. A run's part of a tile that

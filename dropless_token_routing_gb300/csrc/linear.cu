@@ -71,8 +71,10 @@ template <bool KC, int R> struct Operand {
 // tiles of fp32 sums), 8 x 8 of it per thread in quarters of 4 x 4: 4 shared-memory vectors per 64 FMAs
 // (with 8 x 4 the shared memory was the limit). The next 16 of K are loaded into registers while
 // the present ones are multiplied.
+// Four blocks fit on an SM; the gradients' forms need the limit for that (2048 x 2048 x 512: dw 91.8 us,
+// 96.7 with 154 registers), the forward one is there by itself.
 template <bool AK, bool BK, bool SPLIT>
-__global__ void __launch_bounds__(GT) gemm_simt_kernel(const GemmArgs g, float* part) {
+__global__ void __launch_bounds__(GT, BK ? 0 : 4) gemm_simt_kernel(const GemmArgs g, float* part) {
   __shared__ __align__(16) float As[2][GK][GM + 4];
   __shared__ __align__(16) float Bs[2][GK][GN + 4];
   const int tid = threadIdx.x, ty = tid >> 3, tx = tid & 7;
@@ -212,7 +214,7 @@ __global__ void __launch_bounds__(256) linear_dz_kernel(const T* __restrict__ dy
                                                         float* __restrict__ part, int lx) {
   constexpr int U = 4;   // rows in flight
   __shared__ float s[256 * 9];                     // 8 sums a thread, 9 apart
-  pdl_start();
+  if (sizeof(T) == 2) pdl_start();   // (before FMA products: see gemm_join_kernel)
   pdl_wait();
   const int ly = 256 / lx, c = threadIdx.x % lx, r = threadIdx.x / lx;
   const int n = (blockIdx.x * lx + c) * 8, cols = min(8, N - n);
@@ -271,7 +273,7 @@ __global__ void __launch_bounds__(256) linear_db_kernel(const float* __restrict_
   __shared__ float s[8][33];
   const int col = threadIdx.x & 31, r = threadIdx.x >> 5, n = blockIdx.x * 32 + col;
   float t = 0.f;
-  pdl_start();
+  if (sizeof(T) == 2) pdl_start();   // (before FMA products: see gemm_join_kernel)
   pdl_wait();
   if (n < N) {
 #pragma unroll 8

@@ -360,7 +360,10 @@ int moe_op_workspace_init(void* ws, size_t ws_bytes, moe_stream_t stream);
  * x, residual (or NULL) -> y [T, d]; y may be the buffer of x or of residual.
  * logits_in [T][E] fp32 replaces x W_r when given (w_r is not read then).
  * topk_idx [T][k] int32 and topk_w [T][k] fp32 receive the selection (NULL: not returned).
- * bf16 rounds h (times its gate) and y; fp32 rounds nothing. Sums are fp32 in a fixed order. */
+ * bf16 rounds h (times its gate) and y; fp32 rounds nothing. Sums are fp32 in a fixed order.
+ * In bf16 a weight that is not finite reaches every token of the call if any of them selects its
+ * expert (the others have it times zero); in fp32 only those that select it. A workspace for T tokens
+ * serves fewer. MOE_ERR_UNSUPPORTED_DEVICE: a device with no more than 64 SMs. */
 size_t moe_decode_workspace_bytes(const moe_dims* dims);
 int moe_layer_decode(const moe_layer_params* params, const void* x, const float* logits_in,
                      const void* residual, const moe_dims* dims, int32_t* topk_idx, float* topk_w,

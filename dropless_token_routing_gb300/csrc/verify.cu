@@ -6,7 +6,7 @@
 // multiples of 2^-40 and are summed as 64-bit integers, so the sums, and with them the drawn
 // token, do not depend on how the row is split over threads and CTAs.
 //
-// A sequence is a cluster: every warp finds the first refusal itself (that is cheaper than telling the
+// A sequence is a cluster: every CTA finds the first refusal itself (that is cheaper than telling the
 // others), the CTAs share the row and exchange their sums. Bound by latency for few sequences (tokens,
 // their probabilities, the row, the sums, the drawn chunk, each a wait for the one before), by HBM
 // for many: B = 1, V = 32000: 5.2 us; B = 16, V = 50001: 8.1 us; B = 128, V = 131072 in fp32: 134 MB in

@@ -286,13 +286,18 @@ def _refuse(name, dtype, shape, t):
 
 
 def _matrix(t, name, dtype, rows, cols):
-    """Checks a [rows, cols] operand with contiguous rows; returns the stride between them."""
+    """Checks a [rows, cols] operand with contiguous rows that do not overlap (an expanded one is
+    no matrix: the library takes stride 0 for the default); returns the stride between them."""
     if t.dtype != dtype or t.shape != (rows, cols):
         raise ValueError(f"{name}: expected [{rows}, {cols}] of {dtype}, got {list(t.shape)} of {t.dtype}")
     ld, inner = t.stride()
     if inner != 1 and cols > 1:
         raise ValueError(f"{name}: the elements of a row must be contiguous")
-    return ld if rows > 1 or ld > cols else cols
+    if ld < cols:
+        if rows > 1:
+            raise ValueError(f"{name}: rows of {cols} elements are {ld} apart (expanded? make it contiguous)")
+        return cols
+    return ld
 
 
 def _dense(t, name, dtype, shape):

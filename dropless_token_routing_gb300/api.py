@@ -285,11 +285,17 @@ def _refuse(name, dtype, shape, t):
                      f"strides {t.stride()}")
 
 
-def _matrix(t, name, dtype, rows, cols):
+def _elsewhere(name, device, t):
+    raise ValueError(f"{name}: expected on device {device}, got {t.device}")
+
+
+def _matrix(t, name, dtype, rows, cols, device):
     """Checks a [rows, cols] operand with contiguous rows that do not overlap (an expanded one is
     no matrix: the library takes stride 0 for the default); returns the stride between them."""
     if t.dtype != dtype or t.shape != (rows, cols):
         raise ValueError(f"{name}: expected [{rows}, {cols}] of {dtype}, got {list(t.shape)} of {t.dtype}")
+    if t.device != device:
+        _elsewhere(name, device, t)
     ld, inner = t.stride()
     if inner != 1 and cols > 1:
         raise ValueError(f"{name}: the elements of a row must be contiguous")
@@ -300,14 +306,17 @@ def _matrix(t, name, dtype, rows, cols):
     return ld
 
 
-def _dense(t, name, dtype, shape):
+def _dense(t, name, dtype, shape, device):
     if t.dtype != dtype or t.shape != shape or not t.is_contiguous():
         _refuse(name, dtype, shape, t)
+    if t.device != device:
+        _elsewhere(name, device, t)
 
 
-def _device_index(device):
-    d = torch.device(device)
-    return d.index if d.index is not None else torch.cuda.current_device()
+def _device(device):
+    """The device as its tensors name it, and its index."""
+    d = torch.empty(0, device=device).device
+    return d, d.index if d.index is not None else 0
 
 
 class MoEDecodeLayer:
@@ -323,17 +332,31 @@ class MoEDecodeLayer:
                  device="cuda", stream=None):
         self.params, self.dtype, self.max_tokens, self.d, self.E, self.k = params, dtype, max_tokens, d, E, k
         self.dims = make_dims(max_tokens, d, E, k, f, S, f_s, dtype)
+        self.device, self._index = _device(device)
+        self._weights = (("w13", dtype, E * 2 * f * d), ("w2", dtype, E * d * f), ("w_r", torch.float32, d * E),
+                         ("bias", torch.float32, E)) + (
+            (("ws13", dtype, S * 2 * f_s * d), ("ws2", dtype, S * d * f_s)) if S else ())
+        self._check_weights()
         self.ws = OpWorkspace(N.lib().moe_decode_workspace_bytes(ctypes.byref(self.dims)), "moe_decode_workspace_bytes",
                               device, stream)
         self._idx = torch.empty(max_tokens, k, dtype=torch.int32, device=device)
         self._w = torch.empty(max_tokens, k, dtype=torch.float32, device=device)
         self._y = torch.empty(max_tokens, d, dtype=dtype, device=device)
         self._views = {}            # y's first T rows
-        self._device = _device_index(device)
         self._c = params.c()
         self._call = N.lib().moe_layer_decode
         self._refs = (ctypes.byref(self._c), ctypes.byref(self.dims), self._idx.data_ptr(), self._w.data_ptr())
         self._T = 0
+
+    def _check_weights(self):
+        """The weights that are there have the layer's type, size and device (any shape of them)."""
+        for name, dtype, n in self._weights:
+            t = getattr(self.params, name)
+            if t is not None and (t.dtype != dtype or t.numel() != n or not t.is_contiguous()):
+                raise ValueError(f"{name}: expected {n} contiguous elements of {dtype}, got {list(t.shape)} of {t.dtype}, "
+                                 f"strides {t.stride()}")
+            if t is not None and t.device != self.device:
+                _elsewhere(name, self.device, t)
 
     @property
     def topk_idx(self):
@@ -344,26 +367,26 @@ class MoEDecodeLayer:
         return self._w[:self._T]
 
     def forward(self, x, residual=None, logits_in=None, out=None, stream=None):
-        T = x.shape[0]
+        T, dev = x.shape[0], self.device
         shape = (T, self.d)
         if T > self.max_tokens:
             raise ValueError(f"x: {T} tokens, the layer was made for {self.max_tokens}")
-        _dense(x, "x", self.dtype, shape)
+        _dense(x, "x", self.dtype, shape, dev)
         if residual is not None:
-            _dense(residual, "residual", self.dtype, shape)
+            _dense(residual, "residual", self.dtype, shape, dev)
         if logits_in is not None:
-            _dense(logits_in, "logits_in", torch.float32, (T, self.E))
+            _dense(logits_in, "logits_in", torch.float32, (T, self.E), dev)
         if out is None:
             out = self._views.get(T)
             if out is None:
                 out = self._views[T] = self._y[:T]
         else:
-            _dense(out, "out", self.dtype, shape)
+            _dense(out, "out", self.dtype, shape, dev)
         self._T = self.dims.T = T
         c, dims, idx, w = self._refs
         st = self._call(c, x.data_ptr(), None if logits_in is None else logits_in.data_ptr(),
                         None if residual is None else residual.data_ptr(), dims, idx, w, out.data_ptr(), self.ws.ptr,
-                        self.ws.nbytes, _stream(stream, self._device))
+                        self.ws.nbytes, _stream(stream, self._index))
         if st:
             N.check(st, "moe_layer_decode")
         return out
@@ -383,16 +406,16 @@ class Linear:
         self.w, self.bias, self.dtype, self.max_rows = w, bias, w.dtype, max_rows
         self.N, self.K = w.shape
         self.act = N.ACTS[act]
-        dev = self.device = device if device is not None else w.device
-        ld_w = _matrix(w, "w", w.dtype, self.N, self.K)
+        dev, self._index = _device(device if device is not None else w.device)
+        self.device = dev
+        ld_w = _matrix(w, "w", w.dtype, self.N, self.K, dev)
         if bias is not None:
-            _dense(bias, "bias", w.dtype, (self.N,))
+            _dense(bias, "bias", w.dtype, (self.N,), dev)
         self.dims = N.LinearDims(int(max_rows), self.N, self.K, self.act, _dt(w.dtype), 0, ld_w, 0, 0)
         self.ws = OpWorkspace(N.lib().moe_linear_workspace_bytes(ctypes.byref(self.dims)), "moe_linear_workspace_bytes",
                               dev, stream)
         self._x = None
         self._bufs, self._views = {}, {}
-        self._device = _device_index(dev)
         self._dims_ref = ctypes.byref(self.dims)
         self._w_ptr, self._b_ptr = w.data_ptr(), _p(bias)
         self._fwd, self._bwd = N.lib().moe_linear_fwd, N.lib().moe_linear_bwd
@@ -413,20 +436,20 @@ class Linear:
         return t
 
     def forward(self, x, residual=None, save=False, out=None, stream=None):
-        M, D = x.shape[0], self.dims
+        M, D, dev = x.shape[0], self.dims, self.device
         if M > self.max_rows:
             raise ValueError(f"{M} rows, the layer was made for {self.max_rows}")
-        D.M, D.ld_x = M, _matrix(x, "x", self.dtype, M, self.K)
-        D.ld_res = _matrix(residual, "residual", self.dtype, M, self.N) if residual is not None else 0
+        D.M, D.ld_x = M, _matrix(x, "x", self.dtype, M, self.K, dev)
+        D.ld_res = _matrix(residual, "residual", self.dtype, M, self.N, dev) if residual is not None else 0
         if out is None:
             out = self._view("y", self.max_rows, self.N, M, self.N)
             D.ld_y = self.N
         else:
-            D.ld_y = _matrix(out, "out", self.dtype, M, self.N)
+            D.ld_y = _matrix(out, "out", self.dtype, M, self.N, dev)
         z = self._own("z", self.max_rows, self.N + 7 & ~7).data_ptr() if save and self.act != 0 else None
         self._x = x if save else None
         st = self._fwd(x.data_ptr(), self._w_ptr, self._b_ptr, None if residual is None else residual.data_ptr(),
-                       self._dims_ref, z, out.data_ptr(), self.ws.ptr, self.ws.nbytes, _stream(stream, self._device))
+                       self._dims_ref, z, out.data_ptr(), self.ws.ptr, self.ws.nbytes, _stream(stream, self._index))
         if st:
             N.check(st, "moe_linear_fwd")
         return out
@@ -436,8 +459,8 @@ class Linear:
         if x is None:
             raise ValueError("backward: the last forward did not save (save=True)")
         M = x.shape[0]
-        D.M, D.ld_x, D.ld_res = M, _matrix(x, "x", self.dtype, M, self.K), 0
-        D.ld_y = _matrix(dy, "dy", self.dtype, M, self.N)
+        D.M, D.ld_x, D.ld_res = M, _matrix(x, "x", self.dtype, M, self.K, self.device), 0
+        D.ld_y = _matrix(dy, "dy", self.dtype, M, self.N, self.device)
         ld_w = D.ld_w
         dx = dw = db = None
         if "dx" in need:   # rows of dx are as far apart as those of x
@@ -448,7 +471,7 @@ class Linear:
             db = self._own("db", 1, self.N)[0]
         z = self._own("z", self.max_rows, self.N + 7 & ~7).data_ptr() if self.act != 0 else None
         st = self._bwd(x.data_ptr(), self._w_ptr, z, dy.data_ptr(), self._dims_ref, _p(dx), _p(dw), _p(db), self.ws.ptr,
-                       self.ws.nbytes, _stream(stream, self._device))
+                       self.ws.nbytes, _stream(stream, self._index))
         if st:
             N.check(st, "moe_linear_bwd")
         return dict(dx=dx, dw=dw, db=db)
@@ -464,12 +487,14 @@ class DraftVerifier:
         self._tokens = torch.empty(max_batch, n + 1, dtype=torch.int32, device=device)
         self._accepted = torch.empty(max_batch, dtype=torch.int32, device=device)
         self._views = {}
-        self._device = _device_index(device)
+        self.device, self._index = _device(device)
         self._call, self._dims_ref = N.lib().moe_verify_draft, ctypes.byref(self.dims)
 
     def _rows(self, t, name, B, rows):
         if t.dtype != self.dtype or t.shape != (B, rows, self.V):
             raise ValueError(f"{name}: expected [{B}, {rows}, {self.V}] of {self.dtype}, got {list(t.shape)} of {t.dtype}")
+        if t.device != self.device:
+            _elsewhere(name, self.device, t)
         s0, s1, s2 = t.stride()
         ld = s1 if rows > 1 else (s0 if B > 1 else self.V)
         if (self.V > 1 and s2 != 1) or (B > 1 and rows > 0 and s0 != rows * ld) or ld < self.V:
@@ -477,14 +502,14 @@ class DraftVerifier:
         return ld
 
     def verify(self, draft_tokens, draft_probs, target_probs, u_accept, u_sample, draft_len=None, stream=None):
-        B, n = draft_tokens.shape[0], self.n
+        B, n, dev = draft_tokens.shape[0], self.n, self.device
         if B > self.max_batch:
             raise ValueError(f"{B} sequences, made for {self.max_batch}")
-        _dense(draft_tokens, "draft_tokens", torch.int32, (B, n))
-        _dense(u_accept, "u_accept", torch.float32, (B, n))
-        _dense(u_sample, "u_sample", torch.float32, (B,))
+        _dense(draft_tokens, "draft_tokens", torch.int32, (B, n), dev)
+        _dense(u_accept, "u_accept", torch.float32, (B, n), dev)
+        _dense(u_sample, "u_sample", torch.float32, (B,), dev)
         if draft_len is not None:
-            _dense(draft_len, "draft_len", torch.int32, (B,))
+            _dense(draft_len, "draft_len", torch.int32, (B,), dev)
         D = self.dims
         D.B = B
         D.ld_draft = self._rows(draft_probs, "draft_probs", B, n)
@@ -495,7 +520,7 @@ class DraftVerifier:
         tokens, accepted = out
         st = self._call(draft_tokens.data_ptr(), None if draft_len is None else draft_len.data_ptr(),
                         draft_probs.data_ptr(), target_probs.data_ptr(), u_accept.data_ptr(), u_sample.data_ptr(),
-                        self._dims_ref, tokens.data_ptr(), accepted.data_ptr(), _stream(stream, self._device))
+                        self._dims_ref, tokens.data_ptr(), accepted.data_ptr(), _stream(stream, self._index))
         if st:
             N.check(st, "moe_verify_draft")
         return tokens, accepted

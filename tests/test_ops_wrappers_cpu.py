@@ -92,3 +92,78 @@ def test_linear_accepts_one_row_of_any_stride(lib):
     lin.forward(torch.zeros(64).expand(1, 64), residual=torch.zeros(32).expand(1, 32), stream=ST)
     dims = lib.last("moe_linear_fwd")[4]
     assert dims["M"] == 1 and dims["ld_x"] in (0, 64) and dims["ld_res"] in (0, 32)
+
+
+# ------------------------------------------------------------------ operands of another device
+DIMS = dict(d=64, E=4, k=2, f=64, S=1, f_s=64)
+
+
+def decode_params(dtype=torch.bfloat16, d=64, E=4, f=64, S=1, f_s=64, **kw):
+    p = dict(w13=torch.zeros(E, 2 * f, d, dtype=dtype), w2=torch.zeros(E, d, f, dtype=dtype), w_r=torch.zeros(d, E),
+             bias=torch.zeros(E), ws13=torch.zeros(S, 2 * f_s, d, dtype=dtype), ws2=torch.zeros(S, d, f_s, dtype=dtype))
+    return A.LayerParams(**{**p, **kw})
+
+
+def decode_layer(params=None, tokens=8, dtype=torch.bfloat16):
+    params = decode_params(dtype) if params is None else params
+    return A.MoEDecodeLayer(params, tokens, dtype=dtype, device=DEV, stream=ST, **DIMS)
+
+
+def drafts(B_=2, n=3, V=16):
+    return dict(draft_tokens=torch.zeros(B_, n, dtype=torch.int32), draft_probs=torch.zeros(B_, n, V),
+                target_probs=torch.zeros(B_, n + 1, V), u_accept=torch.zeros(B_, n), u_sample=torch.zeros(B_),
+                draft_len=torch.zeros(B_, dtype=torch.int32))
+
+
+def elsewhere(t):
+    return t.to("meta")
+
+
+def test_linear_refuses_operands_of_another_device(lib):
+    lin = linear()
+    x, y = torch.zeros(4, 64), torch.zeros(4, 32)
+    lin.forward(x, residual=y, save=True, stream=ST)
+    for bad in (dict(x=elsewhere(x)), dict(x=x, residual=elsewhere(y)), dict(x=x, out=elsewhere(y))):
+        with pytest.raises(ValueError, match="device"):
+            lin.forward(stream=ST, **bad)
+    lin.forward(x, save=True, stream=ST)
+    with pytest.raises(ValueError, match="device"):
+        lin.backward(elsewhere(y), stream=ST)
+    for w, b in ((torch.zeros(32, 64, device="meta"), None), (torch.zeros(32, 64), torch.zeros(32, device="meta"))):
+        with pytest.raises(ValueError, match="device"):
+            A.Linear(w, b, device=DEV, stream=ST)
+
+
+def test_decode_refuses_operands_of_another_device(lib):
+    layer = decode_layer()
+    x, s = torch.zeros(4, 64, dtype=torch.bfloat16), torch.zeros(4, 4)
+    layer.forward(x, residual=x, logits_in=s, stream=ST)
+    for bad in (dict(x=elsewhere(x)), dict(x=x, residual=elsewhere(x)), dict(x=x, logits_in=elsewhere(s)),
+                dict(x=x, out=elsewhere(x))):
+        with pytest.raises(ValueError, match="device"):
+            layer.forward(stream=ST, **bad)
+
+
+@pytest.mark.parametrize("name", ["w13", "w2", "w_r", "bias", "ws13", "ws2"])
+def test_decode_refuses_weights_that_do_not_fit(lib, name):
+    """The kernel would read past a smaller, narrower or strided tensor."""
+    good = getattr(decode_params(), name)
+    for bad in (elsewhere(good), good[:-1], good.to(torch.float64), torch.zeros(*good.shape, 2, dtype=good.dtype)[..., 0]):
+        with pytest.raises(ValueError, match=name):
+            decode_layer(decode_params(**{name: bad}))
+    decode_layer(decode_params(**{name: good.clone()}))
+
+
+def test_decode_weights_that_are_not_used_may_be_missing(lib):
+    p = decode_params(w_r=None, bias=None, ws13=None, ws2=None)
+    layer = A.MoEDecodeLayer(p, 4, 64, 4, 2, 64, device=DEV, stream=ST)
+    layer.forward(torch.zeros(2, 64, dtype=torch.bfloat16), logits_in=torch.zeros(2, 4), stream=ST)
+
+
+def test_verify_refuses_operands_of_another_device(lib):
+    ver = A.DraftVerifier(2, 3, 16, device=DEV)
+    good = drafts()
+    ver.verify(**good, stream=ST)
+    for name in good:
+        with pytest.raises(ValueError, match="device"):
+            ver.verify(**{**good, name: elsewhere(good[name])}, stream=ST)

@@ -3,6 +3,7 @@ every computation runs in libmoe's kernels.  Names follow include/moe.h."""
 from __future__ import annotations
 
 import ctypes
+import weakref
 from dataclasses import dataclass
 from typing import Optional
 
@@ -319,13 +320,25 @@ def _device(device):
     return d, d.index if d.index is not None else 0
 
 
+def _ref(t):
+    return None if t is None else weakref.ref(t)
+
+
+def _same(t, ref, ptr):
+    """t is the tensor that `ref` stands for, and lies where it did (None: neither)."""
+    if t is None or ref is None:
+        return t is None and ref is None
+    return ref() is t and t.data_ptr() == ptr
+
+
 class MoEDecodeLayer:
     """The whole MoE layer for a few tokens: moe_layer_decode on a kept workspace.
 
     ``forward(x, residual=None)`` takes 0 to ``max_tokens`` (at most 64) tokens and returns
     y [T, d], the layer's own buffer (overwritten by the next call) unless ``out`` is given
     (x and residual are allowed). ``topk_idx`` and ``topk_w`` hold the last call's selection.
-    One instance serves one stream at a time.
+    Every call takes the weights that ``params`` holds then (a captured graph those of the
+    capture). One instance serves one stream at a time.
     """
 
     def __init__(self, params: LayerParams, max_tokens, d, E, k, f, S=0, f_s=0, dtype=torch.bfloat16,
@@ -336,20 +349,28 @@ class MoEDecodeLayer:
         self._weights = (("w13", dtype, E * 2 * f * d), ("w2", dtype, E * d * f), ("w_r", torch.float32, d * E),
                          ("bias", torch.float32, E)) + (
             (("ws13", dtype, S * 2 * f_s * d), ("ws2", dtype, S * d * f_s)) if S else ())
-        self._check_weights()
+        self._c = N.LayerParams()
+        self._bind()
         self.ws = OpWorkspace(N.lib().moe_decode_workspace_bytes(ctypes.byref(self.dims)), "moe_decode_workspace_bytes",
                               device, stream)
         self._idx = torch.empty(max_tokens, k, dtype=torch.int32, device=device)
         self._w = torch.empty(max_tokens, k, dtype=torch.float32, device=device)
         self._y = torch.empty(max_tokens, d, dtype=dtype, device=device)
         self._views = {}            # y's first T rows
-        self._c = params.c()
         self._call = N.lib().moe_layer_decode
         self._refs = (ctypes.byref(self._c), ctypes.byref(self.dims), self._idx.data_ptr(), self._w.data_ptr())
         self._T = 0
 
-    def _check_weights(self):
-        """The weights that are there have the layer's type, size and device (any shape of them)."""
+    def _present(self):
+        p, r, c = self.params, self._bound, self._c
+        return (_same(p.w13, r[0], c.w13) and _same(p.w2, r[1], c.w2) and _same(p.w_r, r[2], c.w_r) and
+                _same(p.bias, r[3], c.bias) and _same(p.ws13, r[4], c.ws13) and _same(p.ws2, r[5], c.ws2))
+
+    def _bind(self):
+        """Takes the weights that params holds; those that are there have the layer's type, size and
+        device (any shape of them)."""
+        p, c = self.params, self._c
+        self._bound = (lambda: None,) * 6      # nothing, should a check fail
         for name, dtype, n in self._weights:
             t = getattr(self.params, name)
             if t is not None and (t.dtype != dtype or t.numel() != n or not t.is_contiguous()):
@@ -357,6 +378,9 @@ class MoEDecodeLayer:
                                  f"strides {t.stride()}")
             if t is not None and t.device != self.device:
                 _elsewhere(name, self.device, t)
+        for name, _ in c._fields_:
+            setattr(c, name, _p(getattr(p, name)))
+        self._bound = tuple(_ref(t) for t in (p.w13, p.w2, p.w_r, p.bias, p.ws13, p.ws2))
 
     @property
     def topk_idx(self):
@@ -382,6 +406,8 @@ class MoEDecodeLayer:
                 out = self._views[T] = self._y[:T]
         else:
             _dense(out, "out", self.dtype, shape, dev)
+        if not self._present():
+            self._bind()
         self._T = self.dims.T = T
         c, dims, idx, w = self._refs
         st = self._call(c, x.data_ptr(), None if logits_in is None else logits_in.data_ptr(),
@@ -394,7 +420,8 @@ class MoEDecodeLayer:
 
 class Linear:
     """y = act(x W^T + b) + residual and its gradients: moe_linear_fwd / moe_linear_bwd on a kept
-    workspace for up to ``max_rows`` rows. ``w`` [N, K] may have strided rows.
+    workspace for up to ``max_rows`` rows. ``w`` [N, K] may have strided rows; every call takes the
+    ``w`` and ``bias`` that the layer holds then.
 
     ``forward(x, residual=None, save=False)`` returns y [M, N], the layer's own buffer
     (overwritten by the next call) unless ``out`` is given; with ``save=True`` it keeps x and the
@@ -408,17 +435,32 @@ class Linear:
         self.act = N.ACTS[act]
         dev, self._index = _device(device if device is not None else w.device)
         self.device = dev
-        ld_w = _matrix(w, "w", w.dtype, self.N, self.K, dev)
-        if bias is not None:
-            _dense(bias, "bias", w.dtype, (self.N,), dev)
-        self.dims = N.LinearDims(int(max_rows), self.N, self.K, self.act, _dt(w.dtype), 0, ld_w, 0, 0)
-        self.ws = OpWorkspace(N.lib().moe_linear_workspace_bytes(ctypes.byref(self.dims)), "moe_linear_workspace_bytes",
-                              dev, stream)
+        self.dims = N.LinearDims(int(max_rows), self.N, self.K, self.act, _dt(w.dtype), 0, 0, 0, 0)
+        self._workspaces = []   # one that a wider W has outgrown may still be in use
+        self._bind(stream)
         self._x = None
         self._bufs, self._views = {}, {}
         self._dims_ref = ctypes.byref(self.dims)
-        self._w_ptr, self._b_ptr = w.data_ptr(), _p(bias)
         self._fwd, self._bwd = N.lib().moe_linear_fwd, N.lib().moe_linear_bwd
+
+    @property
+    def ws(self):
+        return self._workspaces[-1]
+
+    def _bind(self, stream):
+        """Takes the present w and bias; bf16 rows of w that are not whole vectors need a larger workspace."""
+        w, bias, D = self.w, self.bias, self.dims
+        self._w_ref = lambda: None      # nothing, should a check fail
+        ld_w = _matrix(w, "w", self.dtype, self.N, self.K, self.device)
+        if bias is not None:
+            _dense(bias, "bias", self.dtype, (self.N,), self.device)
+        most = N.LinearDims(int(self.max_rows), self.N, self.K, self.act, D.dtype, 0, ld_w, 0, 0)
+        need = N.lib().moe_linear_workspace_bytes(ctypes.byref(most))
+        if not self._workspaces or self.ws.nbytes < need:
+            self._workspaces.append(OpWorkspace(need, "moe_linear_workspace_bytes", self.device, stream))
+        D.ld_w = ld_w
+        self._w_ptr, self._b_ptr = w.data_ptr(), _p(bias)
+        self._w_ref, self._b_ref = _ref(w), _ref(bias)
 
     def _own(self, name, rows, cols):
         """The layer's buffer ``name``, made at its first use."""
@@ -447,6 +489,8 @@ class Linear:
         else:
             D.ld_y = _matrix(out, "out", self.dtype, M, self.N, dev)
         z = self._own("z", self.max_rows, self.N + 7 & ~7).data_ptr() if save and self.act != 0 else None
+        if not (_same(self.w, self._w_ref, self._w_ptr) and _same(self.bias, self._b_ref, self._b_ptr)):
+            self._bind(stream)
         self._x = x if save else None
         st = self._fwd(x.data_ptr(), self._w_ptr, self._b_ptr, None if residual is None else residual.data_ptr(),
                        self._dims_ref, z, out.data_ptr(), self.ws.ptr, self.ws.nbytes, _stream(stream, self._index))
@@ -459,6 +503,8 @@ class Linear:
         if x is None:
             raise ValueError("backward: the last forward did not save (save=True)")
         M = x.shape[0]
+        if not (_same(self.w, self._w_ref, self._w_ptr) and _same(self.bias, self._b_ref, self._b_ptr)):
+            self._bind(stream)
         D.M, D.ld_x, D.ld_res = M, _matrix(x, "x", self.dtype, M, self.K, self.device), 0
         D.ld_y = _matrix(dy, "dy", self.dtype, M, self.N, self.device)
         ld_w = D.ld_w
@@ -466,7 +512,7 @@ class Linear:
         if "dx" in need:   # rows of dx are as far apart as those of x
             dx = self._view(("dx", D.ld_x), self.max_rows, D.ld_x, M, self.K)
         if "dw" in need:
-            dw = self._view("dw", self.N, ld_w, self.N, self.K)
+            dw = self._view(("dw", ld_w), self.N, ld_w, self.N, self.K)
         if "db" in need and self.bias is not None:
             db = self._own("db", 1, self.N)[0]
         z = self._own("z", self.max_rows, self.N + 7 & ~7).data_ptr() if self.act != 0 else None

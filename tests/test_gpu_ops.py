@@ -653,3 +653,45 @@ def test_linear_made_for_many_rows_used_with_few(dtype):
         grads = lin.backward(dy.cuda())
         _close(grads["dw"], ref["dw"], dtype)
         _close(grads["dx"], ref["dx"], dtype)
+
+
+# ------------------------------------------------------------------ weights that are replaced
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_layers_use_replaced_weights(dtype):
+    """A weight that is replaced between two calls (the tensor, or its storage) is the one used."""
+    A = _api()
+    T, d, E, k, f, S, f_s = 6, 128, 8, 2, 64, 1, 64
+    w, x, _ = _layer(T, d, E, k, f, S, f_s, dtype, seed=31, bias=True)
+    other, _, _ = _layer(T, d, E, k, f, S, f_s, dtype, seed=32, bias=True)
+    layer = _decode_layer(w, T, d, E, k, f, S, f_s, dtype)
+    xc = x.cuda()
+    _close(layer.forward(xc), _decode64(w, x, None, k)[0], dtype)
+    for i, name in enumerate(("w2", "w13", "ws13", "ws2", "w_r", "bias")):
+        w[name] = other[name]
+        if i % 2:
+            getattr(layer.params, name).data = other[name].cuda()
+        else:
+            setattr(layer.params, name, other[name].cuda())
+        y = layer.forward(xc)
+        ref, idx, _ = _decode64(w, x, None, k)
+        assert torch.equal(layer.topk_idx.cpu(), idx), name
+        _close(y, ref, dtype, name)
+    M, n = 40, 72
+    g = _gen(33)
+    lin = A.Linear(_rand(g, n, d, std=0.1, dtype=dtype).cuda(), _rand(g, n, dtype=dtype).cuda(), act="silu", max_rows=M)
+    xl, dy = _rand(g, M, d, dtype=dtype), _rand(g, M, n, dtype=dtype)
+    lin.forward(xl.cuda(), save=True)
+    for pad in (0, 3, 8):
+        w2, b2 = _rand(g, n, d, std=0.1, dtype=dtype), _rand(g, n, dtype=dtype)
+        wide = torch.full((n, d + pad), 5.0, dtype=dtype)
+        wide[:, :d] = w2
+        if pad == 3:
+            lin.w.data, lin.bias.data = wide.cuda()[:, :d], b2.cuda()
+        else:
+            lin.w, lin.bias = wide.cuda()[:, :d], b2.cuda()
+        y, ref = _linear64(xl, w2, b2, None, "silu", dy)
+        _close(lin.forward(xl.cuda(), save=True), y, dtype, pad)
+        grads = lin.backward(dy.cuda())
+        for name in ("dx", "dw", "db"):
+            _close(grads[name], ref[name], dtype, (name, pad))
+    assert A.get_device_error(lin.ws) == 0 and A.get_device_error(layer.ws) == 0

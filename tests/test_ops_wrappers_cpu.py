@@ -167,3 +167,87 @@ def test_verify_refuses_operands_of_another_device(lib):
     for name in good:
         with pytest.raises(ValueError, match="device"):
             ver.verify(**{**good, name: elsewhere(good[name])}, stream=ST)
+
+
+# ------------------------------------------------------------------ weights that are replaced
+PARAM_FIELDS = [f for f, _ in N.LayerParams._fields_]
+
+
+@pytest.mark.parametrize("how", ["tensor", "storage"])
+@pytest.mark.parametrize("name", ["w13", "w2", "w_r", "bias", "ws13", "ws2"])
+def test_decode_reads_the_present_weights(lib, name, how):
+    """LayerParams may be changed (a training layer shares it): every call takes its present tensors."""
+    layer = decode_layer()
+    x = torch.zeros(2, 64, dtype=torch.bfloat16)
+    layer.forward(x, stream=ST)
+    old = getattr(layer.params, name)
+    new = old.clone()
+    if how == "tensor":
+        setattr(layer.params, name, new)
+    else:
+        old.data = new
+    layer.forward(x, stream=ST)
+    given = lib.last("moe_layer_decode")[0]
+    assert given[name] == new.data_ptr()
+    for field in PARAM_FIELDS:
+        assert given[field] == getattr(layer.params, field).data_ptr()
+    setattr(layer.params, name, new[:-1])
+    with pytest.raises(ValueError, match=name):
+        layer.forward(x, stream=ST)
+    setattr(layer.params, name, new)
+    layer.forward(x, stream=ST)
+
+
+def test_decode_reads_a_bias_that_comes_and_goes(lib):
+    layer = decode_layer(decode_params(bias=None))
+    x = torch.zeros(2, 64, dtype=torch.bfloat16)
+    layer.forward(x, stream=ST)
+    assert lib.last("moe_layer_decode")[0]["bias"] is None
+    layer.params.bias = torch.zeros(4)
+    layer.forward(x, stream=ST)
+    assert lib.last("moe_layer_decode")[0]["bias"] == layer.params.bias.data_ptr()
+    layer.params.bias = None
+    layer.forward(x, stream=ST)
+    assert lib.last("moe_layer_decode")[0]["bias"] is None
+
+
+@pytest.mark.parametrize("how", ["tensor", "storage"])
+def test_linear_reads_the_present_weights(lib, how):
+    lin = A.Linear(torch.zeros(32, 64), torch.zeros(32), max_rows=8, device=DEV, stream=ST)
+    x, dy = torch.zeros(4, 64), torch.zeros(4, 32)
+    lin.forward(x, save=True, stream=ST)
+    w, b = torch.zeros(32, 70)[:, :64], torch.zeros(32)
+    if how == "tensor":
+        lin.w, lin.bias = w, b
+    else:
+        lin.w.data, lin.bias.data = w, b
+    lin.forward(x, save=True, stream=ST)
+    given = lib.last("moe_linear_fwd")
+    assert given[1] == w.data_ptr() and given[2] == b.data_ptr() and given[4]["ld_w"] == 70
+    grads = lin.backward(dy, stream=ST)
+    given = lib.last("moe_linear_bwd")
+    assert given[1] == w.data_ptr() and given[4]["ld_w"] == 70
+    assert grads["dw"].stride() == (70, 1) and grads["db"] is not None
+    lin.bias = None
+    lin.forward(x, stream=ST)
+    assert lib.last("moe_linear_fwd")[2] is None
+    for bad in (torch.zeros(31, 64), torch.zeros(32, 64, dtype=torch.bfloat16), torch.zeros(64, 32).t()):
+        lin.w = bad
+        with pytest.raises(ValueError):
+            lin.forward(x, stream=ST)
+
+
+def test_linear_workspace_follows_the_weights_stride(lib):
+    """bf16 rows of W that are not whole vectors are copied into the workspace: it grows when such
+    a W replaces another."""
+    lin = A.Linear(torch.zeros(32, 64, dtype=torch.bfloat16), None, max_rows=8, device=DEV, stream=ST)
+    x = torch.zeros(4, 64, dtype=torch.bfloat16)
+    lin.w = torch.zeros(32, 67, dtype=torch.bfloat16)[:, :64]
+    lin.forward(x, save=True, stream=ST)
+    given = lib.last("moe_linear_fwd")
+    dims = N.LinearDims(8, 32, 64, 0, N.MOE_BF16, 0, 67, 0, 0)
+    import ctypes
+    assert given[8] >= lib.moe_linear_workspace_bytes(ctypes.byref(dims))
+    assert given[7] == lin.ws.ptr and given[8] == lin.ws.nbytes
+    inits = [values for n, values in lib.calls if n == "moe_op_workspace_init"]
+    assert [v[0] for v in inits].count(lin.ws.ptr) == 1

@@ -307,6 +307,25 @@ def _matrix(t, name, dtype, rows, cols, device):
     return ld
 
 
+def _overlap(a, ld_a, b, ld_b):
+    """Whether two matrices of contiguous rows, ld_a and ld_b elements apart, share an element."""
+    (Ma, ca), (Mb, cb), size = a.shape, b.shape, a.element_size()
+    if a.numel() == 0 or b.numel() == 0:
+        return False
+    d = b.data_ptr() - a.data_ptr()
+    ca, cb, la, lb = ca * size, cb * size, ld_a * size, ld_b * size
+    if (Ma - 1) * la + ca <= d or d + (Mb - 1) * lb + cb <= 0:
+        return False
+    if la == lb or Ma == 1 or Mb == 1:
+        # rows i of a and j of b meet where (i - j) l lies above d - ca and below d + cb
+        step = la if Mb == 1 else lb
+        return max((d - ca) // step + 1, 1 - Mb) <= min(-(-(d + cb) // step) - 1, Ma - 1)
+    # the last row of b that starts before a row of a ends is the one that reaches furthest
+    start = torch.arange(Ma) * la
+    j = ((start + ca - d - 1) // lb).clamp(max=Mb - 1)
+    return bool(((j >= 0) & (j * lb + d + cb > start)).any())
+
+
 def _dense(t, name, dtype, shape, device):
     if t.dtype != dtype or t.shape != shape or not t.is_contiguous():
         _refuse(name, dtype, shape, t)
@@ -424,15 +443,16 @@ class Linear:
     ``w`` and ``bias`` that the layer holds then.
 
     ``forward(x, residual=None, save=False)`` returns y [M, N], the layer's own buffer
-    (overwritten by the next call) unless ``out`` is given; with ``save=True`` it keeps x and the
+    (written by the next call, which may therefore not read it: a result that goes through the
+    layer again needs another ``out``) unless ``out`` is given; with ``save=True`` it keeps x and the
     pre-activation for ``backward(dy)``, which returns dict(dx, dw, db) (own buffers too; ``need``
-    names those to compute). The residual's gradient is dy itself.
+    names those to compute). The residual's gradient is dy itself. ``out`` may be the residual.
     """
 
     def __init__(self, w, bias=None, act="none", max_rows=1, device=None, stream=None):
         self.w, self.bias, self.dtype, self.max_rows = w, bias, w.dtype, max_rows
         self.N, self.K = w.shape
-        self.act = N.ACTS[act]
+        self.act, self._size = N.ACTS[act], w.element_size()
         dev, self._index = _device(device if device is not None else w.device)
         self.device = dev
         self.dims = N.LinearDims(int(max_rows), self.N, self.K, self.act, _dt(w.dtype), 0, 0, 0, 0)
@@ -483,17 +503,28 @@ class Linear:
             raise ValueError(f"{M} rows, the layer was made for {self.max_rows}")
         D.M, D.ld_x = M, _matrix(x, "x", self.dtype, M, self.K, dev)
         D.ld_res = _matrix(residual, "residual", self.dtype, M, self.N, dev) if residual is not None else 0
-        if out is None:
+        given = out is not None
+        if given:
+            D.ld_y = _matrix(out, "out", self.dtype, M, self.N, dev)
+        else:
             out = self._view("y", self.max_rows, self.N, M, self.N)
             D.ld_y = self.N
-        else:
-            D.ld_y = _matrix(out, "out", self.dtype, M, self.N, dev)
         z = self._own("z", self.max_rows, self.N + 7 & ~7).data_ptr() if save and self.act != 0 else None
         if not (_same(self.w, self._w_ref, self._w_ptr) and _same(self.bias, self._b_ref, self._b_ptr)):
             self._bind(stream)
+        xp, yp, rp = x.data_ptr(), out.data_ptr(), None if residual is None else residual.data_ptr()
+        # what is read may not lie where y is written, but for a residual in the same place
+        size, end = self._size, yp + M * D.ld_y * self._size
+        if xp < end and yp < xp + M * D.ld_x * size and _overlap(x, D.ld_x, out, D.ld_y):
+            raise ValueError("x: overlaps the output (a result of this layer? give it another out)")
+        if rp is not None and rp < end and yp < rp + M * D.ld_res * size and not (
+                rp == yp and (D.ld_res == D.ld_y or M == 1)) and _overlap(residual, D.ld_res, out, D.ld_y):
+            raise ValueError("residual: overlaps the output and does not lie where it does")
+        if given and (_overlap(self.w, D.ld_w, out, D.ld_y) or
+                      (self.bias is not None and _overlap(self.bias[None], self.N, out, D.ld_y))):
+            raise ValueError("out: overlaps the layer's weights")
         self._x = x if save else None
-        st = self._fwd(x.data_ptr(), self._w_ptr, self._b_ptr, None if residual is None else residual.data_ptr(),
-                       self._dims_ref, z, out.data_ptr(), self.ws.ptr, self.ws.nbytes, _stream(stream, self._index))
+        st = self._fwd(xp, self._w_ptr, self._b_ptr, rp, self._dims_ref, z, yp, self.ws.ptr, self.ws.nbytes, _stream(stream, self._index))
         if st:
             N.check(st, "moe_linear_fwd")
         return out
@@ -515,6 +546,17 @@ class Linear:
             dw = self._view(("dw", ld_w), self.N, ld_w, self.N, self.K)
         if "db" in need and self.bias is not None:
             db = self._own("db", 1, self.N)[0]
+        # dw's product reads x and dz last; dz is dy itself where it is not made first
+        size, own_dz = self._size, self.act != 0 or (D.dtype == N.MOE_BF16 and D.ld_y % 8 != 0)
+        for name, i, ld, read in (("dy", dy, D.ld_y, not own_dz), ("x", x, D.ld_x, dw is not None)):
+            if not read:
+                continue
+            lo = i.data_ptr()
+            end = lo + M * ld * size
+            for o, rows, ld_o in ((dx, M, D.ld_x), (dw, self.N, ld_w), (db, 1, self.N)):
+                if o is not None and lo < o.data_ptr() + rows * ld_o * size and o.data_ptr() < end and _overlap(
+                        i, ld, o if rows != 1 else o.view(1, -1), ld_o):
+                    raise ValueError(f"{name}: overlaps a result of this layer that is written first (pass a copy)")
         z = self._own("z", self.max_rows, self.N + 7 & ~7).data_ptr() if self.act != 0 else None
         st = self._bwd(x.data_ptr(), self._w_ptr, z, dy.data_ptr(), self._dims_ref, _p(dx), _p(dw), _p(db), self.ws.ptr,
                        self.ws.nbytes, _stream(stream, self._index))

@@ -393,7 +393,8 @@ typedef struct moe_linear_dims {
  * or NULL, z [M][N rounded up to a multiple of 8] receives the pre-activation for the backward, or
  * NULL.
  * fp32 accumulation, y rounded once (not from the rounded z). residual may be the buffer of y
- * (y updated in place) when their strides agree. Base pointers are 16-byte aligned; strides and
+ * (y updated in place) when their strides agree. y and z overlap no other input: the launch reads
+ * all of x and w while it writes them. Base pointers are 16-byte aligned; strides and
  * widths may be odd (bf16 rows of x and w that are not whole 16-byte vectors are copied in every
  * call). M == 0 is a no-op. A workspace for M rows serves fewer rows, any act and any stride of x, y
  * and residual. */
@@ -405,8 +406,9 @@ int moe_linear_fwd(const void* x, const void* w, const void* bias, const void* r
 /* Its gradients from dy [M, N]:
  *   dz = dy * act'(z),  dx = dz W,  dw = dz^T x,  db = sum_m dz   (the residual's gradient is dy)
  * z as written by moe_linear_fwd (required unless act is MOE_ACT_NONE). dx [M, K], dw [N][K],
- * db [N]: each may be NULL (not computed); w is needed for dx, x for dw. With M == 0 dw and db
- * are zeroed. bf16 rounds dz once before the two products; db sums the unrounded dz in fp32. */
+ * db [N]: each may be NULL (not computed); w is needed for dx, x for dw. None overlaps an input.
+ * With M == 0 dw and db are zeroed. bf16 rounds dz once before the two products; db sums the
+ * unrounded dz in fp32. */
 int moe_linear_bwd(const void* x, const void* w, const void* z, const void* dy,
                    const moe_linear_dims* dims, void* dx, void* dw, void* db, void* ws,
                    size_t ws_bytes, moe_stream_t stream);

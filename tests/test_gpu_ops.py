@@ -695,3 +695,31 @@ def test_layers_use_replaced_weights(dtype):
         for name in ("dx", "dw", "db"):
             _close(grads[name], ref[name], dtype, (name, pad))
     assert A.get_device_error(lin.ws) == 0 and A.get_device_error(layer.ws) == 0
+
+
+@pytest.mark.parametrize("M", [3, 200])
+def test_linear_applied_to_its_own_result(M):
+    """A square layer: its own y (dx) is refused as x (dy); through another buffer it is right."""
+    A = _api()
+    n = 128
+    g = _gen(41)
+    w, x = _rand(g, n, n, std=n ** -0.5), _rand(g, M, n)
+    lin = A.Linear(w.cuda(), None, max_rows=M)
+    y = lin.forward(x.cuda())
+    with pytest.raises(ValueError):
+        lin.forward(y)
+    twice = lin.forward(y, out=torch.empty(M, n, device="cuda"), save=True)
+    _close(twice, x.double() @ w.double().T @ w.double().T, torch.float32)
+    dx = lin.backward(x.cuda())["dx"]
+    with pytest.raises(ValueError):
+        lin.backward(dx)
+    _close(lin.backward(dx.clone())["dx"], x.double() @ w.double() @ w.double(), torch.float32)
+    # in and out side by side in the rows of one buffer
+    wide = torch.zeros(M, 3 * n, device="cuda")
+    wide[:, :n] = x.cuda()
+    lin.forward(wide[:, :n], out=wide[:, n:2 * n])
+    lin.forward(wide[:, n:2 * n], residual=wide[:, :n], out=wide[:, :n])
+    h = x.double() @ w.double().T
+    _close(wide[:, n:2 * n], h, torch.float32)
+    _close(wide[:, :n], h @ w.double().T + x.double(), torch.float32)
+    assert float(wide[:, 2 * n:].abs().max()) == 0.0

@@ -251,3 +251,102 @@ def test_linear_workspace_follows_the_weights_stride(lib):
     assert given[7] == lin.ws.ptr and given[8] == lin.ws.nbytes
     inits = [values for n, values in lib.calls if n == "moe_op_workspace_init"]
     assert [v[0] for v in inits].count(lin.ws.ptr) == 1
+
+
+# ------------------------------------------------------------------ inputs that lie on outputs
+def square(rows=8, act="none", **kw):
+    return linear(64, 64, rows, act=act, **kw)
+
+
+def test_linear_refuses_its_own_result_as_input(lib):
+    """y (dx) is written while x (dy) is still read."""
+    lin = square()
+    x = torch.zeros(4, 64)
+    y = lin.forward(x, stream=ST)
+    calls = len(lib.calls)
+    for bad in (y, y[1:], y[:1]):
+        with pytest.raises(ValueError, match="overlap"):
+            lin.forward(bad, stream=ST)
+    assert len(lib.calls) == calls
+    z = lin.forward(y, out=torch.zeros(4, 64), stream=ST)      # elsewhere: as before
+    lin.forward(z, stream=ST)
+    lin.forward(x, save=True, stream=ST)
+    grads = lin.backward(torch.zeros(4, 64), stream=ST)
+    calls = len(lib.calls)
+    with pytest.raises(ValueError, match="overlap"):
+        lin.backward(grads["dx"], stream=ST)
+    with pytest.raises(ValueError, match="overlap"):
+        lin.backward(grads["dw"][:4], stream=ST)
+    assert len(lib.calls) == calls
+    lin.backward(grads["dx"], need=("dw",), stream=ST)         # dx is not written
+    lin.backward(lin.forward(x, save=True, stream=ST), stream=ST)   # y is not written by the backward
+    # the saved x: read by dw's product, after dx is written
+    kept = grads["dx"]
+    lin.forward(kept, save=True, stream=ST)
+    with pytest.raises(ValueError, match="overlap"):
+        lin.backward(torch.zeros(4, 64), stream=ST)
+    lin.backward(torch.zeros(4, 64), need=("dx",), stream=ST)
+    lin.forward(grads["dw"][:4], save=True, stream=ST)
+    with pytest.raises(ValueError, match="overlap"):
+        lin.backward(torch.zeros(4, 64), need=("dw",), stream=ST)
+    with_db = A.Linear(torch.zeros(64, 64), torch.zeros(64), max_rows=4, device=DEV, stream=ST)
+    with_db.forward(x, save=True, stream=ST)
+    db = with_db.backward(torch.zeros(4, 64), stream=ST)["db"]
+    with_db.forward(db[None], save=True, stream=ST)
+    with pytest.raises(ValueError, match="overlap"):
+        with_db.backward(torch.zeros(1, 64), stream=ST)
+    # with an activation the gradient of z is made from dy before anything is written
+    act = square(act="silu")
+    act.forward(x, save=True, stream=ST)
+    act.backward(act.backward(torch.zeros(4, 64), stream=ST)["dx"], stream=ST)
+
+
+def test_linear_refuses_an_out_that_overlaps_an_input(lib):
+    lin = square()
+    buf = torch.zeros(16, 64)
+    with pytest.raises(ValueError, match="overlap"):
+        lin.forward(buf[:4], out=buf[3:7], stream=ST)
+    lin.forward(buf[:4], out=buf[4:8], stream=ST)
+    with pytest.raises(ValueError, match="overlap"):
+        lin.forward(buf[:4], residual=buf[4:8], out=buf[5:9], stream=ST)
+    lin.forward(buf[:4], residual=buf[4:8], out=buf[4:8], stream=ST)       # in place
+    with pytest.raises(ValueError, match="overlap"):
+        lin.forward(buf[:4], out=lin.w[8:12], stream=ST)
+    b = torch.zeros(2, 64)
+    with_bias = A.Linear(torch.zeros(64, 64), b[1], max_rows=4, device=DEV, stream=ST)
+    with pytest.raises(ValueError, match="overlap"):
+        with_bias.forward(buf[:2], out=b, stream=ST)
+    with_bias.forward(buf[:1], out=b[:1], stream=ST)
+    # columns of one buffer, side by side: rows lie between one another and share nothing
+    wide = torch.zeros(4, 200)
+    lin.forward(wide[:, :64], out=wide[:, 64:128], stream=ST)
+    lin.forward(wide[:, 100:164], residual=wide[:, :64], out=wide[:, :64], stream=ST)
+    with pytest.raises(ValueError, match="overlap"):
+        lin.forward(wide[:, :64], out=wide[:, 63:127], stream=ST)
+
+
+@pytest.mark.parametrize("seed", range(4))
+def test_overlap_of_strided_matrices(seed):
+    """Against the sets of elements, for equal and for different strides."""
+    g = torch.Generator().manual_seed(seed)
+    buf = torch.zeros(400)
+    at = torch.arange(400)
+    seen = set()
+
+    def draw(hi):
+        return int(torch.randint(0, hi, (1,), generator=g))
+
+    for _ in range(600):
+        shapes = []
+        for _ in range(2):
+            rows, cols = draw(5), 1 + draw(9)
+            ld = cols + draw(12)
+            shapes.append((draw(60), rows, cols, ld))
+        if draw(2):
+            shapes[1] = shapes[1][:3] + (max(shapes[0][3], shapes[1][2]),)
+        a, b = (buf.as_strided((r, c), (ld, 1), off) for off, r, c, ld in shapes)
+        ia, ib = (at.as_strided((r, c), (ld, 1), off) for off, r, c, ld in shapes)
+        want = bool(set(ia.reshape(-1).tolist()) & set(ib.reshape(-1).tolist()))
+        assert A._overlap(a, shapes[0][3], b, shapes[1][3]) == want, shapes
+        seen.add((want, shapes[0][3] == shapes[1][3]))
+    assert len(seen) == 4

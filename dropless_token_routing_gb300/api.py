@@ -355,9 +355,9 @@ class MoEDecodeLayer:
 
     ``forward(x, residual=None)`` takes 0 to ``max_tokens`` (at most 64) tokens and returns
     y [T, d], the layer's own buffer (overwritten by the next call) unless ``out`` is given
-    (x and residual are allowed). ``topk_idx`` and ``topk_w`` hold the last call's selection.
-    Every call takes the weights that ``params`` holds then (a captured graph those of the
-    capture). One instance serves one stream at a time.
+    (x and residual are allowed, a residual that only partly overlaps it is not). ``topk_idx`` and
+    ``topk_w`` hold the last call's selection. Every call takes the weights that ``params`` holds
+    then (a captured graph those of the capture). One instance serves one stream at a time.
     """
 
     def __init__(self, params: LayerParams, max_tokens, d, E, k, f, S=0, f_s=0, dtype=torch.bfloat16,
@@ -368,6 +368,7 @@ class MoEDecodeLayer:
         self._weights = (("w13", dtype, E * 2 * f * d), ("w2", dtype, E * d * f), ("w_r", torch.float32, d * E),
                          ("bias", torch.float32, E)) + (
             (("ws13", dtype, S * 2 * f_s * d), ("ws2", dtype, S * d * f_s)) if S else ())
+        self._row = d * torch.empty(0, dtype=dtype).element_size()   # bytes
         self._c = N.LayerParams()
         self._bind()
         self.ws = OpWorkspace(N.lib().moe_decode_workspace_bytes(ctypes.byref(self.dims)), "moe_decode_workspace_bytes",
@@ -427,11 +428,13 @@ class MoEDecodeLayer:
             _dense(out, "out", self.dtype, shape, dev)
         if not self._present():
             self._bind()
+        yp, rp = out.data_ptr(), None if residual is None else residual.data_ptr()
+        if rp is not None and rp != yp and abs(rp - yp) < T * self._row:
+            raise ValueError("residual: overlaps the output and does not lie where it does")
         self._T = self.dims.T = T
         c, dims, idx, w = self._refs
         st = self._call(c, x.data_ptr(), None if logits_in is None else logits_in.data_ptr(),
-                        None if residual is None else residual.data_ptr(), dims, idx, w, out.data_ptr(), self.ws.ptr,
-                        self.ws.nbytes, _stream(stream, self._index))
+                        rp, dims, idx, w, yp, self.ws.ptr, self.ws.nbytes, _stream(stream, self._index))
         if st:
             N.check(st, "moe_layer_decode")
         return out

@@ -357,7 +357,8 @@ int moe_op_workspace_init(void* ws, size_t ws_bytes, moe_stream_t stream);
  *   y_t = sum_{e in S_t} w_te SwiGLU_e(x_t) + sum_s SwiGLU_s(x_t) (+ residual_t)
  * with the scores, S_t and w of moe_router_logits / moe_route_topk (fp32, ties to the lower
  * index; scores must be finite). dims->capacity and dims->rearrange must be 0 (MOE_ERR_BAD_DIMS).
- * x, residual (or NULL) -> y [T, d]; y may be the buffer of x or of residual.
+ * x, residual (or NULL) -> y [T, d]; y may overlap x, and be the buffer of residual (the whole of
+ * it: element by element the residual is read where y is written).
  * logits_in [T][E] fp32 replaces x W_r when given (w_r is not read then).
  * topk_idx [T][k] int32 and topk_w [T][k] fp32 receive the selection (NULL: not returned).
  * bf16 rounds h (times its gate) and y; fp32 rounds nothing. Sums are fp32 in a fixed order.

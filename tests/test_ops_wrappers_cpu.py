@@ -350,3 +350,21 @@ def test_overlap_of_strided_matrices(seed):
         assert A._overlap(a, shapes[0][3], b, shapes[1][3]) == want, shapes
         seen.add((want, shapes[0][3] == shapes[1][3]))
     assert len(seen) == 4
+
+
+def test_decode_refuses_a_residual_that_partly_overlaps_the_output(lib):
+    """x is read before any output is written; the residual while others write theirs, so it lies
+    where the output does or elsewhere."""
+    layer = decode_layer()
+    x = torch.zeros(4, 64, dtype=torch.bfloat16)
+    y = layer.forward(x, residual=x, stream=ST)
+    assert layer.forward(y, residual=y, stream=ST) is y
+    layer.forward(y[:2], residual=y[:2], stream=ST)
+    layer.forward(y[1:3], residual=y[:2], stream=ST)
+    with pytest.raises(ValueError, match="residual"):
+        layer.forward(x[:2], residual=y[1:3], stream=ST)
+    buf = torch.zeros(8, 64, dtype=torch.bfloat16)
+    layer.forward(buf[:4], residual=buf[4:], out=buf[4:], stream=ST)
+    layer.forward(buf[:4], residual=buf[:4], out=buf[4:], stream=ST)
+    with pytest.raises(ValueError, match="residual"):
+        layer.forward(x, residual=buf[1:5], out=buf[4:], stream=ST)

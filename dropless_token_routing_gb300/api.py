@@ -609,9 +609,14 @@ class DraftVerifier:
         if out is None:
             out = self._views[B] = (self._tokens[:B], self._accepted[:B])
         tokens, accepted = out
-        st = self._call(draft_tokens.data_ptr(), None if draft_len is None else draft_len.data_ptr(),
-                        draft_probs.data_ptr(), target_probs.data_ptr(), u_accept.data_ptr(), u_sample.data_ptr(),
-                        self._dims_ref, tokens.data_ptr(), accepted.data_ptr(), _stream(stream, self._index))
+        # a result is written while other sequences, and later tokens of its own, are read
+        dp, tp, ap, lp = draft_tokens.data_ptr(), tokens.data_ptr(), accepted.data_ptr(), _p(draft_len)
+        if dp < tp + B * (n + 1) * 4 and tp < dp + B * n * 4 and not (B == 1 and dp == tp):
+            raise ValueError("draft_tokens: overlaps the result")
+        if lp is not None and lp != ap and abs(lp - ap) < B * 4:
+            raise ValueError("draft_len: overlaps the result and does not lie where it does")
+        st = self._call(dp, lp, draft_probs.data_ptr(), target_probs.data_ptr(), u_accept.data_ptr(), u_sample.data_ptr(),
+                        self._dims_ref, tp, ap, _stream(stream, self._index))
         if st:
             N.check(st, "moe_verify_draft")
         return tokens, accepted

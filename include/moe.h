@@ -434,7 +434,8 @@ typedef struct moe_verify_dims {
  * draft_tokens [B][n] int32 (a token outside [0, V) is refused), draft_len [B] int32 or NULL (n
  * for all; clamped to [0, n]), draft_probs [B][n][ld_draft], target_probs [B][n+1][ld_target],
  * u_accept [B][n], u_sample [B] fp32 in [0, 1) -> tokens [B][n+1] int32 (kept tokens, the drawn
- * one, then -1), accepted [B] int32 (kept drafted tokens). Tensors of size 0 may be NULL. */
+ * one, then -1), accepted [B] int32 (kept drafted tokens). Neither overlaps an input, but accepted may
+ * be draft_len and, for one sequence, tokens draft_tokens. Tensors of size 0 may be NULL. */
 int moe_verify_draft(const int32_t* draft_tokens, const int32_t* draft_len, const void* draft_probs,
                      const void* target_probs, const float* u_accept, const float* u_sample,
                      const moe_verify_dims* dims, int32_t* tokens, int32_t* accepted,

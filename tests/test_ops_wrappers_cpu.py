@@ -368,3 +368,23 @@ def test_decode_refuses_a_residual_that_partly_overlaps_the_output(lib):
     layer.forward(buf[:4], residual=buf[:4], out=buf[4:], stream=ST)
     with pytest.raises(ValueError, match="residual"):
         layer.forward(x, residual=buf[1:5], out=buf[4:], stream=ST)
+
+
+def test_verify_refuses_its_results_as_inputs(lib):
+    """Drafted tokens in the result's buffer: a sequence's results are written while another's (or
+    its own, shifted) are read. One sequence's own first n tokens may stay where they are."""
+    ver = A.DraftVerifier(4, 3, 16, device=DEV)
+    good = drafts(B_=4)
+    tokens, accepted = ver.verify(**good, stream=ST)
+    flat = tokens.view(-1)
+    for at in (0, 2, 4):
+        with pytest.raises(ValueError, match="draft_tokens"):
+            ver.verify(**{**good, "draft_tokens": flat[at:at + 12].view(4, 3)}, stream=ST)
+    one = drafts(B_=1)
+    got, n = ver.verify(**one, stream=ST)
+    ver.verify(**{**one, "draft_tokens": got[:, :3]}, stream=ST)
+    with pytest.raises(ValueError, match="draft_tokens"):
+        ver.verify(**{**one, "draft_tokens": got[:, 1:]}, stream=ST)
+    ver.verify(**{**good, "draft_len": accepted}, stream=ST)
+    with pytest.raises(ValueError, match="draft_len"):
+        ver.verify(**{**drafts(B_=2), "draft_len": accepted[1:3]}, stream=ST)

@@ -218,6 +218,12 @@ int dgate_tiles(const moe_dims* d) {
 
 namespace moe {
 int check_layer_dims(const moe_dims* dims) { return check_dims(dims); }
+int check_device(int* sms) {
+  const DevInfo di = dev_info();
+  if (di.sms == 0) return MOE_ERR_CUDA;
+  *sms = di.sms;
+  return di.cc == 103 ? MOE_OK : MOE_ERR_UNSUPPORTED_DEVICE;
+}
 }  // namespace moe
 
 using namespace moe;
@@ -235,7 +241,7 @@ const char* moe_status_string(int s) {
     case MOE_ERR_WORKSPACE_TOO_SMALL: return "workspace too small";
     case MOE_ERR_LAUNCH: return "kernel launch failed";
     case MOE_ERR_CUDA: return "CUDA call failed";
-    case MOE_ERR_UNSUPPORTED_DEVICE: return "bf16 grouped GEMM needs an sm_103 (GB300) device";
+    case MOE_ERR_UNSUPPORTED_DEVICE: return "bf16 grouped GEMM and the few-token operators need an sm_103 (GB300) device";
     case MOE_ERR_DEVICE_EXPERT_ID: return "device: expert id out of range or repeated in a row";
     case MOE_ERR_DEVICE_TIMEOUT: return "device: a bounded wait ran out";
     default: return "unknown status";

@@ -63,6 +63,9 @@ WsLayout ws_layout(const moe_dims& d);
 
 // The argument checks every layer call makes of its dims (MOE_OK or the status).
 int check_layer_dims(const moe_dims* dims);
+// The current device's SMs, and MOE_ERR_UNSUPPORTED_DEVICE where it is not an sm_103 (the library
+// holds code for no other).
+int check_device(int* sms);
 
 // launchers (return the launch's cudaError_t)
 cudaError_t launch_router_logits(const void* x, const float* w_r, const moe_dims& dm, float* logits,

@@ -66,12 +66,6 @@ int check_op_ws(const void* ws, size_t ws_bytes, size_t need) {
   return ws_bytes < need ? MOE_ERR_WORKSPACE_TOO_SMALL : MOE_OK;
 }
 
-int num_sms() {
-  int dev = 0, n = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
-  return cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess ? n : 0;
-}
-
 // A decode call's dims are the layer's, with few tokens and without the training variants.
 int check_decode(const moe_dims* d) {
   if (d == nullptr) return MOE_ERR_NULL_POINTER;
@@ -158,8 +152,8 @@ int moe_layer_decode(const moe_layer_params* params, const void* x, const float*
   OP_TRY(opt(topk_w));
   OP_TRY(req_if(y, some));
   if (!some) return MOE_OK;
-  const int sms = num_sms();
-  if (sms == 0) return MOE_ERR_CUDA;
+  int sms = 0;
+  OP_TRY(check_device(&sms));
   a.x = x;
   a.residual = residual;
   a.w_r = params->w_r;
@@ -196,8 +190,8 @@ int moe_linear_fwd(const void* x, const void* w, const void* bias, const void* r
   OP_TRY(opt(z));
   OP_TRY(req_if(y, some));
   if (!some) return MOE_OK;
-  const int sms = num_sms();
-  if (sms == 0) return MOE_ERR_CUDA;
+  int sms = 0;
+  OP_TRY(check_device(&sms));
   uint8_t* base = static_cast<uint8_t*>(ws);
   const cudaStream_t st = (cudaStream_t)stream;
   int64_t ld_x = d.ld_x, ld_w = d.ld_w;
@@ -229,8 +223,8 @@ int moe_linear_bwd(const void* x, const void* w, const void* z, const void* dy, 
     return MOE_OK;
   }
   uint8_t* base = static_cast<uint8_t*>(ws);
-  const int sms = num_sms();
-  if (sms == 0) return MOE_ERR_CUDA;
+  int sms = 0;
+  OP_TRY(check_device(&sms));
   const bool products = dx != nullptr || dw != nullptr;
   // without an activation dz is dy itself, unless dy's rows are not whole 16-byte vectors (bf16)
   const bool own_dz = products && (d.act != MOE_ACT_NONE || (d.dtype == MOE_BF16 && d.ld_y % 8 != 0));
@@ -275,8 +269,8 @@ int moe_verify_draft(const int32_t* draft_tokens, const int32_t* draft_len, cons
   OP_TRY(req_if(tokens, some));
   OP_TRY(req_if(accepted, some));
   if (!some) return MOE_OK;
-  const int sms = num_sms();
-  if (sms == 0) return MOE_ERR_CUDA;
+  int sms = 0;
+  OP_TRY(check_device(&sms));
   VerifyArgs v = {draft_tokens, draft_len, draft_probs, target_probs, u_accept, u_sample, tokens, accepted,
                   dims->B, dims->ld_draft != 0 ? dims->ld_draft : dims->V,
                   dims->ld_target != 0 ? dims->ld_target : dims->V, dims->n, dims->V, dims->dtype};

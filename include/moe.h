@@ -63,7 +63,7 @@ enum moe_status {
   MOE_ERR_WORKSPACE_TOO_SMALL = -6, /* ws_bytes < moe_workspace_bytes(dims) */
   MOE_ERR_LAUNCH = -7,              /* a kernel launch failed */
   MOE_ERR_CUDA = -8,                /* another CUDA runtime/driver call failed */
-  MOE_ERR_UNSUPPORTED_DEVICE = -9,  /* bf16 grouped GEMM needs an sm_103 (GB300) device */
+  MOE_ERR_UNSUPPORTED_DEVICE = -9,  /* bf16 grouped GEMM and the few-token operators: sm_103 (GB300) only */
   MOE_ERR_DEVICE_EXPERT_ID = -100,  /* device: expert id outside [0, E) or repeated in a row */
   MOE_ERR_DEVICE_TIMEOUT = -101     /* device: a bounded wait ran out */
 };

@@ -153,3 +153,51 @@ def test_linear_workspace_serves_fewer_rows(dtype, width):
         assert need == L.moe_linear_workspace_bytes(ctypes.byref(odd))
         assert need >= last > 0 or M == 0
         last = need
+
+
+FAKE_DEVICE = r"""
+/* a device of another architecture, as the CUDA runtime would report it */
+int cudaGetDevice(int* dev) { *dev = 0; return 0; }
+int cudaDeviceGetAttribute(int* value, int attr, int dev) {
+  *value = attr == 75 ? 9 : attr == 76 ? 0 : attr == 16 ? 132 : 1;   /* major, minor, SMs */
+  return dev;
+}
+"""
+
+
+@pytest.mark.parametrize("call", ["decode_bf16", "decode_f32", "linear_bf16", "linear_f32", "linear_bwd", "verify"])
+def test_other_devices_are_refused(tmp_path, call):
+    """The library holds sm_103 code alone: on another device a call is refused, not left to fail
+    at its launch. The runtime's answers about the device are faked in a child process."""
+    import shutil
+    import subprocess
+    import sys
+    cc = shutil.which("gcc") or shutil.which("cc")
+    if cc is None:
+        pytest.skip("no C compiler")
+    src, so = tmp_path / "fake.c", tmp_path / "fake.so"
+    src.write_text(FAKE_DEVICE)
+    subprocess.run([cc, "-shared", "-fPIC", "-o", str(so), str(src)], check=True)
+    code = f"""
+import ctypes, sys
+sys.path.insert(0, {os.path.dirname(os.path.dirname(os.path.abspath(__file__)))!r})
+from dropless_token_routing_gb300 import _native as N
+L, G, R = N.lib(), 0x10000, ctypes.byref
+def decode(dtype):
+    d = N.MoeDims(4, 512, 8, 2, 256, 0, 0, dtype, 0, 0)
+    p = N.LayerParams(G, None, G, G, None, None)
+    return L.moe_layer_decode(R(p), G, None, None, R(d), None, None, G, G, 1 << 40, None)
+def linear(dtype, bwd=False):
+    d = N.LinearDims(4, 96, 64, 0, dtype, 0, 0, 0, 0)
+    if bwd:
+        return L.moe_linear_bwd(G, G, None, G, R(d), G, G, G, G, 1 << 40, None)
+    return L.moe_linear_fwd(G, G, None, None, R(d), None, G, G, 1 << 40, None)
+print({{"decode_bf16": lambda: decode(N.MOE_BF16), "decode_f32": lambda: decode(N.MOE_F32),
+       "linear_bf16": lambda: linear(N.MOE_BF16), "linear_f32": lambda: linear(N.MOE_F32),
+       "linear_bwd": lambda: linear(N.MOE_BF16, True),
+       "verify": lambda: L.moe_verify_draft(G, None, G, G, G, G, R(N.VerifyDims(2, 3, 100, N.MOE_F32, 0, 0)), G, G, None),
+      }}[{call!r}]())
+"""
+    out = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, check=True,
+                         env={**os.environ, "LD_PRELOAD": str(so), "CUDA_VISIBLE_DEVICES": ""})
+    assert int(out.stdout) == C["MOE_ERR_UNSUPPORTED_DEVICE"], out.stdout

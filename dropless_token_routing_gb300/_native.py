@@ -117,6 +117,7 @@ _SIGS = {
     "moe_linear_bwd": (c_int, [P, P, P, P, ctypes.POINTER(LinearDims), P, P, P, P, c_size_t, P]),
     "moe_verify_draft": (c_int, [P, P, P, P, P, P, ctypes.POINTER(VerifyDims), P, P, P]),
     "moe_debug_timeout_probe": (c_int, [P, c_size_t, c_uint64, P]),
+    "moe_debug_decode_timeout_probe": (c_int, [ctypes.POINTER(LayerParams), P, ctypes.POINTER(MoeDims), P, P, c_size_t, P]),
     "moe_trace_enable": (c_int, [c_int]),
     "moe_trace_read": (c_int, [ctypes.POINTER(TraceEntry), c_int, ctypes.POINTER(c_int)]),
 }

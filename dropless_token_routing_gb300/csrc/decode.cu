@@ -247,7 +247,7 @@ __global__ void __launch_bounds__(FT, 1) decode_f32_kernel(const __grid_constant
     bool ok = true;
     if (threadIdx.x == 0) {
       add_release(header + ROWS, 1u);
-      ok = word_wait(header + ROWS, (uint32_t)n_cta, &s_abort, err);
+      ok = word_wait(header + ROWS, (uint32_t)n_cta + p.a.absent, &s_abort, err);
     }
     ok = !__syncthreads_or(!ok);
     if (ok) {

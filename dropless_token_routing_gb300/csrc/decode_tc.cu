@@ -221,10 +221,12 @@ __global__ void __launch_bounds__(THREADS, 1) decode_kernel(const __grid_constan
         Ring<STAGES> behind = ring;
         int ahead = 0;
         auto wait_rows = [&]() {
-          ok = word_wait(p.header + ROWS, (uint32_t)n_cta, &b.abort, err);
+          ok = ok && word_wait(p.header + ROWS, (uint32_t)n_cta + p.a.absent, &b.abort, err);
           asm volatile("fence.proxy.async;" ::: "memory");   // generic writes of other CTAs, read by TMA
           have_rows = true;
-          while (ok && ahead > 0 && tokens.next()) {   // the same blocks again, from the run's start
+          // the same blocks again, from the run's start. Also when the launch has failed: a stage that
+          // lacked its rows would never be full, and drain() would wait its whole limit for each
+          while (ahead > 0 && tokens.next()) {
             Blocks k(plan, tokens.s.k0);
             for (int kb = tokens.s.k0; kb < tokens.s.k1 && ahead > 0; ++kb, --ahead) {
               rows(behind, k);
@@ -274,7 +276,7 @@ __global__ void __launch_bounds__(THREADS, 1) decode_kernel(const __grid_constan
             }
           }
         }
-        if (ok && !have_rows && ahead > 0) wait_rows();
+        if (!have_rows && ahead > 0) wait_rows();
       }
       drain<STAGES>(b, ring, loaded, err);
     }

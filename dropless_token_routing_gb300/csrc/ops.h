@@ -36,6 +36,7 @@ struct DecodeArgs {
   float* gate_out;
   void* y;
   uint8_t* ws;
+  uint32_t absent;   // CTAs beyond the launch's that the hidden rows are waited for: 0, 1 lets the wait run out
   DecodeLayout L;
   moe_dims dm;
 };

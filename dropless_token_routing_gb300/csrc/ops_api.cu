@@ -113,25 +113,9 @@ int run_gemm(int kind, const GemmArgs& g, uint8_t* ws, const LinearLayout& L, in
   return launch_gemm_simt(g, reinterpret_cast<float*>(ws + L.part), sms, st) == cudaSuccess ? MOE_OK : MOE_ERR_LAUNCH;
 }
 
-}  // namespace
-}  // namespace moe
-
-using namespace moe;
-
-extern "C" {
-
-int moe_op_workspace_init(void* ws, size_t ws_bytes, moe_stream_t stream) {
-  OP_TRY(check_op_ws(ws, ws_bytes, kOpHeader));
-  return cudaMemsetAsync(ws, 0, kOpHeader, (cudaStream_t)stream) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
-}
-
-size_t moe_decode_workspace_bytes(const moe_dims* dims) {
-  return check_decode(dims) == MOE_OK ? decode_layout(*dims).total : 0;
-}
-
-int moe_layer_decode(const moe_layer_params* params, const void* x, const float* logits_in, const void* residual,
-                     const moe_dims* dims, int32_t* topk_idx, float* topk_w, void* y, void* ws, size_t ws_bytes,
-                     moe_stream_t stream) {
+int layer_decode(const moe_layer_params* params, const void* x, const float* logits_in, const void* residual,
+                 const moe_dims* dims, int32_t* topk_idx, float* topk_w, void* y, void* ws, size_t ws_bytes, uint32_t absent,
+                 cudaStream_t st) {
   OP_TRY(check_decode(dims));
   if (params == nullptr) return MOE_ERR_NULL_POINTER;
   DecodeArgs a;
@@ -167,8 +151,36 @@ int moe_layer_decode(const moe_layer_params* params, const void* x, const float*
   a.gate_out = topk_w;
   a.y = y;
   a.ws = static_cast<uint8_t*>(ws);
+  a.absent = absent;
   a.dm = *dims;
-  return dims->dtype == MOE_BF16 ? launch_decode_tc(a, sms, (cudaStream_t)stream) : launch_decode_simt(a, sms, (cudaStream_t)stream);
+  return dims->dtype == MOE_BF16 ? launch_decode_tc(a, sms, st) : launch_decode_simt(a, sms, st);
+}
+
+}  // namespace
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" {
+
+int moe_op_workspace_init(void* ws, size_t ws_bytes, moe_stream_t stream) {
+  OP_TRY(check_op_ws(ws, ws_bytes, kOpHeader));
+  return cudaMemsetAsync(ws, 0, kOpHeader, (cudaStream_t)stream) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}
+
+size_t moe_decode_workspace_bytes(const moe_dims* dims) {
+  return check_decode(dims) == MOE_OK ? decode_layout(*dims).total : 0;
+}
+
+int moe_layer_decode(const moe_layer_params* params, const void* x, const float* logits_in, const void* residual,
+                     const moe_dims* dims, int32_t* topk_idx, float* topk_w, void* y, void* ws, size_t ws_bytes,
+                     moe_stream_t stream) {
+  return layer_decode(params, x, logits_in, residual, dims, topk_idx, topk_w, y, ws, ws_bytes, 0, (cudaStream_t)stream);
+}
+
+int moe_debug_decode_timeout_probe(const moe_layer_params* params, const void* x, const moe_dims* dims, void* y, void* ws,
+                                   size_t ws_bytes, moe_stream_t stream) {
+  return layer_decode(params, x, nullptr, nullptr, dims, nullptr, nullptr, y, ws, ws_bytes, 1, (cudaStream_t)stream);
 }
 
 size_t moe_linear_workspace_bytes(const moe_linear_dims* dims) {

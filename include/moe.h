@@ -460,6 +460,12 @@ int moe_trace_read(moe_trace_entry* out, int max_entries, int* n_out);
  * and returns without hanging (read it with moe_get_device_error). */
 int moe_debug_timeout_probe(void* ws, size_t ws_bytes, uint64_t limit_ns, moe_stream_t stream);
 
+/* The same for the few-token layer: moe_layer_decode whose wait for all CTAs' hidden rows counts one
+ * CTA too many, so that it runs out (1 s) and the launch winds down. y is undefined; the workspace
+ * serves the next call. */
+int moe_debug_decode_timeout_probe(const moe_layer_params* params, const void* x, const moe_dims* dims, void* y,
+                                   void* ws, size_t ws_bytes, moe_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -723,3 +723,32 @@ def test_linear_applied_to_its_own_result(M):
     _close(wide[:, n:2 * n], h, torch.float32)
     _close(wide[:, :n], h @ w.double().T + x.double(), torch.float32)
     assert float(wide[:, 2 * n:].abs().max()) == 0.0
+
+
+# ------------------------------------------------------------------ a wait that runs out
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("T,d,E,k,f", [(5, 1024, 16, 6, 512), (40, 192, 9, 2, 64)])
+def test_decode_wait_that_runs_out(T, d, E, k, f, dtype):
+    """The hidden rows of a CTA that does not exist are waited for: after the limit of one second the
+    launch winds down at once (no stage of the weight ring is waited for any longer), the status
+    says so, and the next call on the workspace is right."""
+    import ctypes
+    import time
+    A = _api()
+    w, x, _ = _layer(T, d, E, k, f, 0, 0, dtype, seed=51)
+    layer = _decode_layer(w, T, d, E, k, f, 0, 0, dtype)
+    ref = _decode64(w, x, None, k)[0]
+    xc, y = x.cuda(), torch.zeros(T, d, dtype=dtype, device="cuda")
+    _close(layer.forward(xc), ref, dtype)
+    c, dims = layer.params.c(), A.make_dims(T, d, E, k, f, dtype=dtype)
+    torch.cuda.synchronize()
+    t0 = time.perf_counter()
+    st = A.N.lib().moe_debug_decode_timeout_probe(ctypes.byref(c), xc.data_ptr(), ctypes.byref(dims), y.data_ptr(),
+                                                  layer.ws.ptr, layer.ws.nbytes, torch.cuda.current_stream().cuda_stream)
+    assert st == 0
+    assert A.get_device_error(layer.ws) == A.N.STATUS_CODE["MOE_ERR_DEVICE_TIMEOUT"]
+    took = time.perf_counter() - t0
+    # the wait itself, and once more for a CTA that waits for one that gave up
+    assert 0.9 < took < 3.0, took
+    _close(layer.forward(xc), ref, dtype)
+    assert A.get_device_error(layer.ws) == 0

@@ -29,6 +29,8 @@ template <typename T> struct Vec8;
 template <> struct Vec8<__nv_bfloat16> {
   uint4 v;
   __device__ __forceinline__ void load(const __nv_bfloat16* p) { v = __ldg(reinterpret_cast<const uint4*>(p)); }
+  // for memory that may be written while the kernel lives (launch.cuh)
+  __device__ __forceinline__ void load_plain(const __nv_bfloat16* p) { v = *reinterpret_cast<const uint4*>(p); }
   __device__ __forceinline__ void store(__nv_bfloat16* p) const { *reinterpret_cast<uint4*>(p) = v; }
   __device__ __forceinline__ void to_float(float* f) const {
     const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&v);
@@ -51,6 +53,10 @@ template <> struct Vec8<float> {
   __device__ __forceinline__ void load(const float* p) {
     a = __ldg(reinterpret_cast<const float4*>(p));
     b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+  }
+  __device__ __forceinline__ void load_plain(const float* p) {
+    a = *reinterpret_cast<const float4*>(p);
+    b = *(reinterpret_cast<const float4*>(p) + 1);
   }
   __device__ __forceinline__ void store(float* p) const {
     reinterpret_cast<float4*>(p)[0] = a;
@@ -77,7 +83,7 @@ __device__ __forceinline__ void load8_unaligned(Vec8<T>& r, const T* p, const T*
     uint32_t w[W + 4];
 #pragma unroll
     for (int i = 0; i < W / 4 + 1; ++i) {
-      const uint4 v = __ldg(reinterpret_cast<const uint4*>(base) + i);
+      const uint4 v = *(reinterpret_cast<const uint4*>(base) + i);
       w[4 * i] = v.x;
       w[4 * i + 1] = v.y;
       w[4 * i + 2] = v.z;

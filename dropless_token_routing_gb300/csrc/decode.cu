@@ -82,8 +82,8 @@ __device__ __forceinline__ Group routed_group(const Tables& tb, int e, int g, in
 }
 
 // Hidden rows j .. j + HR - 1 of one expert for a group: h[t * f + j] = gate * silu(w1 . x_t) * (w3 . x_t).
-__device__ __forceinline__ void hidden_rows(const float* __restrict__ w1, const float* __restrict__ w3, const float* __restrict__ x,
-                                            int d, const Group& r, float* h, int f, int j, int lane) {
+__device__ __forceinline__ void hidden_rows(const float* __restrict__ w1, const float* __restrict__ w3, const float* x, int d,
+                                            const Group& r, float* h, int f, int j, int lane) {
   float g[HR][GROUP] = {}, u[HR][GROUP] = {};
 #pragma unroll 2
   for (int i = lane * 4; i < d; i += 128) {
@@ -96,7 +96,7 @@ __device__ __forceinline__ void hidden_rows(const float* __restrict__ w1, const 
 #pragma unroll
     for (int q = 0; q < GROUP; ++q) {
       if (q >= r.n) break;
-      const float4 v = __ldg(reinterpret_cast<const float4*>(x + (int64_t)r.t[q] * d + i));
+      const float4 v = *reinterpret_cast<const float4*>(x + (int64_t)r.t[q] * d + i);   // y may be x's buffer
 #pragma unroll
       for (int o = 0; o < HR; ++o) {
         g[o][q] = dot4(a[o], v, g[o][q]);

@@ -1,7 +1,9 @@
 // Launches whose set-up overlaps the end of the kernel before them on the stream (programmatic
 // dependent launch): a kernel starts with pdl_start(), which lets the next one's blocks in as soon
 // as its own leave room, and calls pdl_wait() before it first touches global memory, which returns
-// when the kernel before has finished and its writes are visible. In a row of launches one token's
+// when the kernel before has finished and its writes are visible. What it reads is then written
+// during its own lifetime, which rules out loads through the read-only path: no __ldg and no
+// const __restrict__ pointers in these kernels. In a row of launches one token's
 // 2048 x 7680 projection takes 9.3 us, 12.3 without.
 #pragma once
 

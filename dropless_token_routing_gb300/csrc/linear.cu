@@ -153,7 +153,7 @@ __global__ void __launch_bounds__(GT, BK ? 0 : 4) gemm_simt_kernel(const GemmArg
 // lets the next one start early: its blocks would then fill the SMs that are free first, several on
 // one. 256 x 256 x 1024: 8.0 us, 16.4 if this one does.)
 constexpr int JR = 8;   // rows of a block
-__global__ void __launch_bounds__(32 * JR) gemm_join_kernel(const GemmArgs g, const float* __restrict__ part, int split) {
+__global__ void __launch_bounds__(32 * JR) gemm_join_kernel(const GemmArgs g, const float* part, int split) {
   const int lane = threadIdx.x & 31, r = blockIdx.z * JR + (threadIdx.x >> 5);
   const int64_t m = (int64_t)blockIdx.x * GM + r;
   const int n = blockIdx.y * GN + lane;
@@ -208,10 +208,8 @@ int simt_split(int64_t tiles, int64_t K, int num_sms) {
 // group of rows and adds its rows' sums in order into one row of `part`. VEC: dy's rows hold whole
 // 16-byte vectors.
 template <typename T, int ACT, bool VEC>
-__global__ void __launch_bounds__(256) linear_dz_kernel(const T* __restrict__ dy, int64_t ld_dy,
-                                                        const T* __restrict__ z, int64_t M, int N,
-                                                        T* __restrict__ dz, int64_t ld_dz,
-                                                        float* __restrict__ part, int lx) {
+__global__ void __launch_bounds__(256) linear_dz_kernel(const T* dy, int64_t ld_dy, const T* z, int64_t M, int N, T* dz,
+                                                        int64_t ld_dz, float* part, int lx) {
   constexpr int U = 4;   // rows in flight
   __shared__ float s[256 * 9];                     // 8 sums a thread, 9 apart
   if (sizeof(T) == 2) pdl_start();   // (before FMA products: see gemm_join_kernel)
@@ -228,9 +226,9 @@ __global__ void __launch_bounds__(256) linear_dz_kernel(const T* __restrict__ dy
       for (int u = 0; u < U; ++u) {
         const int64_t m = m0 + u * step;
         if (m < M) {
-          if (VEC) a[u].load(dy + m * ld_dy + n);
+          if (VEC) a[u].load_plain(dy + m * ld_dy + n);
           else load8_unaligned(a[u], dy + m * ld_dy + n, dy_end, cols);
-          if (ACT != MOE_ACT_NONE) b[u].load(z + m * ld_dz + n);
+          if (ACT != MOE_ACT_NONE) b[u].load_plain(z + m * ld_dz + n);
         }
       }
 #pragma unroll
@@ -269,7 +267,7 @@ __global__ void __launch_bounds__(256) linear_dz_kernel(const T* __restrict__ dy
 
 // db = the sum of n_part rows: 32 columns per block, 8 threads each, added in order.
 template <typename T>
-__global__ void __launch_bounds__(256) linear_db_kernel(const float* __restrict__ part, int n_part, int N, T* __restrict__ db) {
+__global__ void __launch_bounds__(256) linear_db_kernel(const float* part, int n_part, int N, T* db) {
   __shared__ float s[8][33];
   const int col = threadIdx.x & 31, r = threadIdx.x >> 5, n = blockIdx.x * 32 + col;
   float t = 0.f;

@@ -67,7 +67,7 @@ template <typename T, bool VEC> struct Row {
     T p[W], q[W];
   };
   __device__ __forceinline__ static void load(T (&d)[W], const T* s) {
-    if constexpr (VEC) *reinterpret_cast<uint4*>(d) = __ldg(reinterpret_cast<const uint4*>(s));
+    if constexpr (VEC) *reinterpret_cast<uint4*>(d) = *reinterpret_cast<const uint4*>(s);
     else d[0] = s[0];
   }
   // elements j .. j + W - 1 (all of them past V count as 0; with VEC, V may end inside)

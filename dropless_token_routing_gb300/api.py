@@ -339,15 +339,18 @@ def _device(device):
     return d, d.index if d.index is not None else 0
 
 
+def _none():
+    return None
+
+
 def _ref(t):
-    return None if t is None else weakref.ref(t)
+    """Calls to the tensor, while it exists, or None."""
+    return _none if t is None else weakref.ref(t)
 
 
 def _same(t, ref, ptr):
-    """t is the tensor that `ref` stands for, and lies where it did (None: neither)."""
-    if t is None or ref is None:
-        return t is None and ref is None
-    return ref() is t and t.data_ptr() == ptr
+    """t is the tensor that `ref` stands for, and lies where it did (a freed one's ref gives None too)."""
+    return t is ref() and (t.data_ptr() if t is not None else None) == ptr
 
 
 class MoEDecodeLayer:
@@ -382,15 +385,18 @@ class MoEDecodeLayer:
         self._T = 0
 
     def _present(self):
-        p, r, c = self.params, self._bound, self._c
-        return (_same(p.w13, r[0], c.w13) and _same(p.w2, r[1], c.w2) and _same(p.w_r, r[2], c.w_r) and
-                _same(p.bias, r[3], c.bias) and _same(p.ws13, r[4], c.ws13) and _same(p.ws2, r[5], c.ws2))
+        p = self.params
+        for name, ref, ptr in self._bound:
+            t = getattr(p, name)
+            if t is not ref() or (t.data_ptr() if t is not None else None) != ptr:
+                return False
+        return True
 
     def _bind(self):
         """Takes the weights that params holds; those that are there have the layer's type, size and
         device (any shape of them)."""
         p, c = self.params, self._c
-        self._bound = (lambda: None,) * 6      # nothing, should a check fail
+        self._bound = (("w13", lambda: self, 0),)      # none of them, should a check fail
         for name, dtype, n in self._weights:
             t = getattr(self.params, name)
             if t is not None and (t.dtype != dtype or t.numel() != n or not t.is_contiguous()):
@@ -400,7 +406,7 @@ class MoEDecodeLayer:
                 _elsewhere(name, self.device, t)
         for name, _ in c._fields_:
             setattr(c, name, _p(getattr(p, name)))
-        self._bound = tuple(_ref(t) for t in (p.w13, p.w2, p.w_r, p.bias, p.ws13, p.ws2))
+        self._bound = tuple((name, _ref(getattr(p, name)), getattr(c, name)) for name, _, _ in self._weights)
 
     @property
     def topk_idx(self):
@@ -421,14 +427,16 @@ class MoEDecodeLayer:
         if logits_in is not None:
             _dense(logits_in, "logits_in", torch.float32, (T, self.E), dev)
         if out is None:
-            out = self._views.get(T)
-            if out is None:
-                out = self._views[T] = self._y[:T]
+            v = self._views.get(T)
+            if v is None:
+                v = self._views[T] = self._y[:T], self._y.data_ptr()
+            out, yp = v
         else:
             _dense(out, "out", self.dtype, shape, dev)
+            yp = out.data_ptr()
         if not self._present():
             self._bind()
-        yp, rp = out.data_ptr(), None if residual is None else residual.data_ptr()
+        rp = None if residual is None else residual.data_ptr()
         if rp is not None and rp != yp and abs(rp - yp) < T * self._row:
             raise ValueError("residual: overlaps the output and does not lie where it does")
         self._T = self.dims.T = T
@@ -459,16 +467,12 @@ class Linear:
         dev, self._index = _device(device if device is not None else w.device)
         self.device = dev
         self.dims = N.LinearDims(int(max_rows), self.N, self.K, self.act, _dt(w.dtype), 0, 0, 0, 0)
-        self._workspaces = []   # one that a wider W has outgrown may still be in use
+        self._workspaces, self.ws = [], None   # one that a wider W has outgrown may still be in use
         self._bind(stream)
         self._x = None
         self._bufs, self._views = {}, {}
         self._dims_ref = ctypes.byref(self.dims)
         self._fwd, self._bwd = N.lib().moe_linear_fwd, N.lib().moe_linear_bwd
-
-    @property
-    def ws(self):
-        return self._workspaces[-1]
 
     def _bind(self, stream):
         """Takes the present w and bias; bf16 rows of w that are not whole vectors need a larger workspace."""
@@ -479,8 +483,9 @@ class Linear:
             _dense(bias, "bias", self.dtype, (self.N,), self.device)
         most = N.LinearDims(int(self.max_rows), self.N, self.K, self.act, D.dtype, 0, ld_w, 0, 0)
         need = N.lib().moe_linear_workspace_bytes(ctypes.byref(most))
-        if not self._workspaces or self.ws.nbytes < need:
-            self._workspaces.append(OpWorkspace(need, "moe_linear_workspace_bytes", self.device, stream))
+        if self.ws is None or self.ws.nbytes < need:
+            self.ws = OpWorkspace(need, "moe_linear_workspace_bytes", self.device, stream)
+            self._workspaces.append(self.ws)
         D.ld_w = ld_w
         self._w_ptr, self._b_ptr = w.data_ptr(), _p(bias)
         self._w_ref, self._b_ref = _ref(w), _ref(bias)
@@ -493,79 +498,81 @@ class Linear:
         return t
 
     def _view(self, name, rows, cols, M, width):
-        """[M, width] of the buffer ``name`` [rows, cols]."""
+        """[M, width] of the buffer ``name`` [rows, cols], and its address."""
         key = (name, M, width)
-        t = self._views.get(key)
-        if t is None:
-            t = self._views[key] = self._own(name, rows, cols)[:M, :width]
-        return t
+        v = self._views.get(key)
+        if v is None:
+            t = self._own(name, rows, cols)[:M, :width]
+            v = self._views[key] = t, t.data_ptr()
+        return v
 
     def forward(self, x, residual=None, save=False, out=None, stream=None):
-        M, D, dev = x.shape[0], self.dims, self.device
+        M, D, dev, dtype, n, size = x.shape[0], self.dims, self.device, self.dtype, self.N, self._size
         if M > self.max_rows:
             raise ValueError(f"{M} rows, the layer was made for {self.max_rows}")
-        D.M, D.ld_x = M, _matrix(x, "x", self.dtype, M, self.K, dev)
-        D.ld_res = _matrix(residual, "residual", self.dtype, M, self.N, dev) if residual is not None else 0
-        given = out is not None
-        if given:
-            D.ld_y = _matrix(out, "out", self.dtype, M, self.N, dev)
+        ld_x, xp = _matrix(x, "x", dtype, M, self.K, dev), x.data_ptr()
+        if out is None:
+            y, yp = self._view("y", self.max_rows, n, M, n)
+            ld_y = n
         else:
-            out = self._view("y", self.max_rows, self.N, M, self.N)
-            D.ld_y = self.N
-        z = self._own("z", self.max_rows, self.N + 7 & ~7).data_ptr() if save and self.act != 0 else None
+            y, yp, ld_y = out, out.data_ptr(), _matrix(out, "out", dtype, M, n, dev)
         if not (_same(self.w, self._w_ref, self._w_ptr) and _same(self.bias, self._b_ref, self._b_ptr)):
             self._bind(stream)
-        xp, yp, rp = x.data_ptr(), out.data_ptr(), None if residual is None else residual.data_ptr()
         # what is read may not lie where y is written, but for a residual in the same place
-        size, end = self._size, yp + M * D.ld_y * self._size
-        if xp < end and yp < xp + M * D.ld_x * size and _overlap(x, D.ld_x, out, D.ld_y):
+        end = yp + M * ld_y * size
+        if xp < end and yp < xp + M * ld_x * size and _overlap(x, ld_x, y, ld_y):
             raise ValueError("x: overlaps the output (a result of this layer? give it another out)")
-        if rp is not None and rp < end and yp < rp + M * D.ld_res * size and not (
-                rp == yp and (D.ld_res == D.ld_y or M == 1)) and _overlap(residual, D.ld_res, out, D.ld_y):
-            raise ValueError("residual: overlaps the output and does not lie where it does")
-        if given and (_overlap(self.w, D.ld_w, out, D.ld_y) or
-                      (self.bias is not None and _overlap(self.bias[None], self.N, out, D.ld_y))):
+        if residual is None:
+            rp, ld_r = None, 0
+        else:
+            rp, ld_r = residual.data_ptr(), _matrix(residual, "residual", dtype, M, n, dev)
+            if rp < end and yp < rp + M * ld_r * size and not (
+                    rp == yp and (ld_r == ld_y or M == 1)) and _overlap(residual, ld_r, y, ld_y):
+                raise ValueError("residual: overlaps the output and does not lie where it does")
+        if out is not None and (_overlap(self.w, D.ld_w, y, ld_y) or
+                                (self.bias is not None and _overlap(self.bias[None], n, y, ld_y))):
             raise ValueError("out: overlaps the layer's weights")
+        z = self._own("z", self.max_rows, n + 7 & ~7).data_ptr() if save and self.act != 0 else None
         self._x = x if save else None
-        st = self._fwd(xp, self._w_ptr, self._b_ptr, rp, self._dims_ref, z, yp, self.ws.ptr, self.ws.nbytes, _stream(stream, self._index))
+        D.M, D.ld_x, D.ld_y, D.ld_res = M, ld_x, ld_y, ld_r
+        st = self._fwd(xp, self._w_ptr, self._b_ptr, rp, self._dims_ref, z, yp, self.ws.ptr, self.ws.nbytes,
+                       _stream(stream, self._index))
         if st:
             N.check(st, "moe_linear_fwd")
-        return out
+        return y
 
     def backward(self, dy, need=("dx", "dw", "db"), stream=None):
-        x, D = self._x, self.dims
+        x, D, n, size = self._x, self.dims, self.N, self._size
         if x is None:
             raise ValueError("backward: the last forward did not save (save=True)")
         M = x.shape[0]
         if not (_same(self.w, self._w_ref, self._w_ptr) and _same(self.bias, self._b_ref, self._b_ptr)):
             self._bind(stream)
-        D.M, D.ld_x, D.ld_res = M, _matrix(x, "x", self.dtype, M, self.K, self.device), 0
-        D.ld_y = _matrix(dy, "dy", self.dtype, M, self.N, self.device)
-        ld_w = D.ld_w
-        dx = dw = db = None
+        ld_x, xp, ld_w = _matrix(x, "x", self.dtype, M, self.K, self.device), x.data_ptr(), D.ld_w
+        ld_y, yp = _matrix(dy, "dy", self.dtype, M, n, self.device), dy.data_ptr()
+        dx = dw = db = dxp = dwp = dbp = None
         if "dx" in need:   # rows of dx are as far apart as those of x
-            dx = self._view(("dx", D.ld_x), self.max_rows, D.ld_x, M, self.K)
+            dx, dxp = self._view(("dx", ld_x), self.max_rows, ld_x, M, self.K)
         if "dw" in need:
-            dw = self._view(("dw", ld_w), self.N, ld_w, self.N, self.K)
+            dw, dwp = self._view(("dw", ld_w), n, ld_w, n, self.K)
         if "db" in need and self.bias is not None:
-            db = self._own("db", 1, self.N)[0]
+            db, dbp = self._view("db", 1, n, 1, n)
         # dw's product reads x and dz last; dz is dy itself where it is not made first
-        size, own_dz = self._size, self.act != 0 or (D.dtype == N.MOE_BF16 and D.ld_y % 8 != 0)
-        for name, i, ld, read in (("dy", dy, D.ld_y, not own_dz), ("x", x, D.ld_x, dw is not None)):
-            if not read:
+        own_dz = self.act != 0 or (size == 2 and ld_y % 8 != 0)
+        for o, op, rows, ld_o in ((dx, dxp, M, ld_x), (dw, dwp, n, ld_w), (db, dbp, 1, n)):
+            if o is None:
                 continue
-            lo = i.data_ptr()
-            end = lo + M * ld * size
-            for o, rows, ld_o in ((dx, M, D.ld_x), (dw, self.N, ld_w), (db, 1, self.N)):
-                if o is not None and lo < o.data_ptr() + rows * ld_o * size and o.data_ptr() < end and _overlap(
-                        i, ld, o if rows != 1 else o.view(1, -1), ld_o):
-                    raise ValueError(f"{name}: overlaps a result of this layer that is written first (pass a copy)")
-        z = self._own("z", self.max_rows, self.N + 7 & ~7).data_ptr() if self.act != 0 else None
-        st = self._bwd(x.data_ptr(), self._w_ptr, z, dy.data_ptr(), self._dims_ref, _p(dx), _p(dw), _p(db), self.ws.ptr,
-                       self.ws.nbytes, _stream(stream, self._index))
+            end = op + rows * ld_o * size
+            if (not own_dz and yp < end and op < yp + M * ld_y * size and _overlap(dy, ld_y, o, ld_o)) or (
+                    dw is not None and xp < end and op < xp + M * ld_x * size and _overlap(x, ld_x, o, ld_o)):
+                raise ValueError("dy or x: overlaps a result of this layer that is written before it is read (pass a copy)")
+        z = self._own("z", self.max_rows, n + 7 & ~7).data_ptr() if self.act != 0 else None
+        D.M, D.ld_x, D.ld_y, D.ld_res = M, ld_x, ld_y, 0
+        st = self._bwd(xp, self._w_ptr, z, yp, self._dims_ref, dxp, dwp, dbp, self.ws.ptr, self.ws.nbytes,
+                       _stream(stream, self._index))
         if st:
             N.check(st, "moe_linear_bwd")
-        return dict(dx=dx, dw=dw, db=db)
+        return dict(dx=dx, dw=dw, db=None if db is None else db[0])
 
 
 class DraftVerifier:
@@ -578,10 +585,12 @@ class DraftVerifier:
         self._tokens = torch.empty(max_batch, n + 1, dtype=torch.int32, device=device)
         self._accepted = torch.empty(max_batch, dtype=torch.int32, device=device)
         self._views = {}
+        self._ptrs = self._tokens.data_ptr(), self._accepted.data_ptr()
         self.device, self._index = _device(device)
         self._call, self._dims_ref = N.lib().moe_verify_draft, ctypes.byref(self.dims)
 
     def _rows(self, t, name, B, rows):
+        """Checks probabilities [B, rows, V] whose rows are contiguous and evenly spaced; returns their distance."""
         if t.dtype != self.dtype or t.shape != (B, rows, self.V):
             raise ValueError(f"{name}: expected [{B}, {rows}, {self.V}] of {self.dtype}, got {list(t.shape)} of {t.dtype}")
         if t.device != self.device:
@@ -593,30 +602,44 @@ class DraftVerifier:
         return ld
 
     def verify(self, draft_tokens, draft_probs, target_probs, u_accept, u_sample, draft_len=None, stream=None):
-        B, n, dev = draft_tokens.shape[0], self.n, self.device
-        if B > self.max_batch:
-            raise ValueError(f"{B} sequences, made for {self.max_batch}")
-        _dense(draft_tokens, "draft_tokens", torch.int32, (B, n), dev)
-        _dense(u_accept, "u_accept", torch.float32, (B, n), dev)
-        _dense(u_sample, "u_sample", torch.float32, (B,), dev)
-        if draft_len is not None:
-            _dense(draft_len, "draft_len", torch.int32, (B,), dev)
-        D = self.dims
-        D.B = B
-        D.ld_draft = self._rows(draft_probs, "draft_probs", B, n)
-        D.ld_target = self._rows(target_probs, "target_probs", B, n + 1)
-        out = self._views.get(B)
-        if out is None:
-            out = self._views[B] = (self._tokens[:B], self._accepted[:B])
-        tokens, accepted = out
+        B, n, dev, dt = draft_tokens.shape[0], self.n, self.device, self.dtype
+        v = self._views.get(B)
+        if v is None:
+            if B > self.max_batch:
+                raise ValueError(f"{B} sequences, made for {self.max_batch}")
+            v = self._views[B] = ((self._tokens[:B], self._accepted[:B]), (B, n), (B,), (B, n, self.V), (B, n + 1, self.V))
+        out, of_tokens, of_rows, of_q, of_p = v
+        # (checked here, and said there: a call's host time is near the kernel's own for one sequence)
+        t = draft_tokens
+        if t.dtype is not torch.int32 or t.shape != of_tokens or not t.is_contiguous() or t.device != dev:
+            _dense(t, "draft_tokens", torch.int32, of_tokens, dev)
+        t = u_accept
+        if t.dtype is not torch.float32 or t.shape != of_tokens or not t.is_contiguous() or t.device != dev:
+            _dense(t, "u_accept", torch.float32, of_tokens, dev)
+        t = u_sample
+        if t.dtype is not torch.float32 or t.shape != of_rows or not t.is_contiguous() or t.device != dev:
+            _dense(t, "u_sample", torch.float32, of_rows, dev)
+        ld_q = ld_p = self.V
+        t = draft_probs
+        if t.dtype is not dt or t.shape != of_q or not t.is_contiguous() or t.device != dev:
+            ld_q = self._rows(t, "draft_probs", B, n)
+        t = target_probs
+        if t.dtype is not dt or t.shape != of_p or not t.is_contiguous() or t.device != dev:
+            ld_p = self._rows(t, "target_probs", B, n + 1)
         # a result is written while other sequences, and later tokens of its own, are read
-        dp, tp, ap, lp = draft_tokens.data_ptr(), tokens.data_ptr(), accepted.data_ptr(), _p(draft_len)
+        dp, (tp, ap) = draft_tokens.data_ptr(), self._ptrs
         if dp < tp + B * (n + 1) * 4 and tp < dp + B * n * 4 and not (B == 1 and dp == tp):
             raise ValueError("draft_tokens: overlaps the result")
-        if lp is not None and lp != ap and abs(lp - ap) < B * 4:
-            raise ValueError("draft_len: overlaps the result and does not lie where it does")
+        lp = None
+        if draft_len is not None:
+            _dense(draft_len, "draft_len", torch.int32, of_rows, dev)
+            lp = draft_len.data_ptr()
+            if lp != ap and abs(lp - ap) < B * 4:
+                raise ValueError("draft_len: overlaps the result and does not lie where it does")
+        D = self.dims
+        D.B, D.ld_draft, D.ld_target = B, ld_q, ld_p
         st = self._call(dp, lp, draft_probs.data_ptr(), target_probs.data_ptr(), u_accept.data_ptr(), u_sample.data_ptr(),
                         self._dims_ref, tp, ap, _stream(stream, self._index))
         if st:
             N.check(st, "moe_verify_draft")
-        return tokens, accepted
+        return out

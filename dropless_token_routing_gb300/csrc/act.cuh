@@ -10,11 +10,16 @@ constexpr float kInvSqrt2Pi = 0.39894228040143268f;
 constexpr float kGeluC = 0.79788456080286536f;   // sqrt(2 / pi)
 constexpr float kGeluA = 0.044715f;
 
+// The fp32 forms keep their relative accuracy where the result is small (z well below 0): the normal
+// distribution's cumulative is erfc, the tanh form z times the logistic of 2 u. Written as 1 + erf and
+// 1 + tanh they cancel there (4 % off at z = -5, everything at -6).
+__device__ __forceinline__ float gelu_u(float z) { return kGeluC * (z + kGeluA * z * z * z); }
+
 template <int ACT> __device__ __forceinline__ float act_f(float z) {
   if constexpr (ACT == MOE_ACT_RELU) return z < 0.f ? 0.f : z;   // keeps NaN
   if constexpr (ACT == MOE_ACT_SILU) return silu_f(z);
-  if constexpr (ACT == MOE_ACT_GELU) return 0.5f * z * (1.f + erff(z * kSqrtHalf));
-  if constexpr (ACT == MOE_ACT_GELU_TANH) return 0.5f * z * (1.f + tanhf(kGeluC * (z + kGeluA * z * z * z)));
+  if constexpr (ACT == MOE_ACT_GELU) return 0.5f * z * erfcf(-z * kSqrtHalf);
+  if constexpr (ACT == MOE_ACT_GELU_TANH) return z / (1.f + expf(-2.f * gelu_u(z)));
   return z;
 }
 
@@ -25,19 +30,22 @@ template <int ACT> __device__ __forceinline__ float act_slope(float z) {
     return sg * (1.f + z * (1.f - sg));
   }
   if constexpr (ACT == MOE_ACT_GELU)
-    return 0.5f * (1.f + erff(z * kSqrtHalf)) + z * kInvSqrt2Pi * expf(-0.5f * z * z);
+    return 0.5f * erfcf(-z * kSqrtHalf) + z * kInvSqrt2Pi * expf(-0.5f * z * z);
   if constexpr (ACT == MOE_ACT_GELU_TANH) {
-    const float th = tanhf(kGeluC * (z + kGeluA * z * z * z));
-    return 0.5f * (1.f + th) + 0.5f * z * (1.f - th * th) * kGeluC * (1.f + 3.f * kGeluA * z * z);
+    // act = z s(2u), s' = s(2u) s(-2u)
+    const float u = 2.f * gelu_u(z), s = 1.f / (1.f + expf(-u)), r = 1.f / (1.f + expf(u));
+    return s + z * s * r * 2.f * kGeluC * (1.f + 3.f * kGeluA * z * z);
   }
   return 1.f;
 }
 
 // The forms for results that are rounded to bf16 (2^-9): the hardware's exponential and reciprocal,
 // a few 2^-22 off, take a third of the instructions; in the product kernels' epilogues the exact
-// forms cost a 4096 x 2816 x 2048 product 15 of 55 us. The tanh form is z times the logistic of
-// 2 u; the normal distribution's cumulative is erfc's five-term approximation 7.1.26 of Abramowitz
-// and Stegun, "Handbook of Mathematical Functions" (within 1.5e-7), on the side where it is small.
+// forms cost a 4096 x 2816 x 2048 product 15 of 55 us. The normal distribution's cumulative is erfc's
+// five-term approximation 7.1.26 of Abramowitz and Stegun, "Handbook of Mathematical Functions", on
+// the side where it is small. Its bound is absolute, 1.5e-7 (7.5e-8 of the cumulative); relative to a
+// cumulative that is small itself it is 1.6e-3 off at z = -5, 3.6e-3 at -6 and 2e-2 at -10, where a
+// bf16 result's own rounding is 2e-3 (the values are below 2e-6 there).
 __device__ __forceinline__ float logistic_fast(float z) { return __fdividef(1.f, 1.f + __expf(-z)); }
 // exp(-z^2 / 2) goes to `e`
 __device__ __forceinline__ float normal_cdf_fast(float z, float& e) {
@@ -48,7 +56,6 @@ __device__ __forceinline__ float normal_cdf_fast(float z, float& e) {
   const float tail = 0.5f * p * e;
   return z < 0.f ? tail : 1.f - tail;
 }
-__device__ __forceinline__ float gelu_u(float z) { return kGeluC * (z + kGeluA * z * z * z); }
 
 template <int ACT> __device__ __forceinline__ float act_fast(float z) {
   if constexpr (ACT == MOE_ACT_SILU) return z * logistic_fast(z);

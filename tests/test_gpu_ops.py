@@ -752,3 +752,45 @@ def test_decode_wait_that_runs_out(T, d, E, k, f, dtype):
     assert 0.9 < took < 3.0, took
     _close(layer.forward(xc), ref, dtype)
     assert A.get_device_error(layer.ws) == 0
+
+
+# ------------------------------------------------------------------ activations far out
+def _act_slope64(name, z):
+    """Value and derivative in 64 bits, by formulas that keep their relative accuracy in the tails."""
+    z = z.double()
+    if name == "gelu":
+        cdf = 0.5 * torch.special.erfc(-z / math.sqrt(2))
+        return z * cdf, cdf + z * torch.exp(-0.5 * z * z) / math.sqrt(2 * math.pi)
+    u = math.sqrt(2 / math.pi) * (z + 0.044715 * z ** 3)
+    s, r = torch.sigmoid(2 * u), torch.sigmoid(-2 * u)
+    return z * s, s + z * s * r * 2 * math.sqrt(2 / math.pi) * (1 + 3 * 0.044715 * z * z)
+
+
+def _through_layer(act, z, dtype=torch.float32):
+    """act(z) and act'(z) of every z by a layer of one input and one output: y = act(z * 1), dx = dy act'(z)."""
+    A = _api()
+    M = z.numel()
+    lin = A.Linear(torch.ones(1, 1, dtype=dtype, device="cuda"), None, act=act, max_rows=M)
+    x = z.to(dtype).reshape(M, 1).cuda()
+    y = lin.forward(x, save=True).clone()
+    dx = lin.backward(torch.ones(M, 1, dtype=dtype, device="cuda"), need=("dx",))["dx"]
+    return y.cpu().double().reshape(-1), dx.cpu().double().reshape(-1)
+
+
+@pytest.mark.parametrize("act", ["gelu", "gelu_tanh"])
+def test_fp32_gelu_keeps_its_accuracy_in_the_tail(act):
+    """Element by element. For z in [-6, -3] the function is e^(-t) times a factor of order 1 with t
+    up to 25; t is made by at most five fp32 operations, each off by 2^-24 of it, and the rest by ten
+    more: 25 * 5 * 6e-8 + 1e-6 = 8.5e-6; 2e-5 is twice that. The derivative is a sum of two
+    such terms, of which the larger is at most 1.15 times the result there: 4e-5."""
+    z = torch.linspace(-6, -3, 3001).float()
+    y, slope = _through_layer(act, z)
+    ry, rs = _act_slope64(act, z)
+    assert float(((y - ry) / ry).abs().max()) <= 2e-5
+    assert float(((slope - rs) / rs).abs().max()) <= 4e-5
+    # and around 0 and above, where nothing is small: 2^-24 of ten operations on values up to 6
+    z = torch.linspace(-3, 6, 3001).float()
+    y, slope = _through_layer(act, z)
+    ry, rs = _act_slope64(act, z)
+    assert float((y - ry).abs().max()) <= 6e-6
+    assert float((slope - rs).abs().max()) <= 6e-6

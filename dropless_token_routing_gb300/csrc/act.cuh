@@ -14,6 +14,8 @@ constexpr float kGeluA = 0.044715f;
 // distribution's cumulative is erfc, the tanh form z times the logistic of 2 u. Written as 1 + erf and
 // 1 + tanh they cancel there (4 % off at z = -5, everything at -6).
 __device__ __forceinline__ float gelu_u(float z) { return kGeluC * (z + kGeluA * z * z * z); }
+// The tanh form's slope is 0 or 1 to the last bit past 12; its polynomial would overflow further out.
+__device__ __forceinline__ float gelu_clamp(float z) { return z > 12.f ? 12.f : z < -12.f ? -12.f : z; }   // keeps NaN
 
 template <int ACT> __device__ __forceinline__ float act_f(float z) {
   if constexpr (ACT == MOE_ACT_RELU) return z < 0.f ? 0.f : z;   // keeps NaN
@@ -33,8 +35,8 @@ template <int ACT> __device__ __forceinline__ float act_slope(float z) {
     return 0.5f * erfcf(-z * kSqrtHalf) + z * kInvSqrt2Pi * expf(-0.5f * z * z);
   if constexpr (ACT == MOE_ACT_GELU_TANH) {
     // act = z s(2u), s' = s(2u) s(-2u)
-    const float u = 2.f * gelu_u(z), s = 1.f / (1.f + expf(-u)), r = 1.f / (1.f + expf(u));
-    return s + z * s * r * 2.f * kGeluC * (1.f + 3.f * kGeluA * z * z);
+    const float v = gelu_clamp(z), u = 2.f * gelu_u(v), s = 1.f / (1.f + expf(-u)), r = 1.f / (1.f + expf(u));
+    return s + v * s * r * 2.f * kGeluC * (1.f + 3.f * kGeluA * v * v);
   }
   return 1.f;
 }
@@ -79,8 +81,8 @@ template <int ACT> __device__ __forceinline__ float act_slope_fast(float z) {
   }
   if constexpr (ACT == MOE_ACT_GELU_TANH) {
     // act = z s(2u), s' = s (1 - s)
-    const float s = logistic_fast(2.f * gelu_u(z));
-    return s + z * s * (1.f - s) * 2.f * kGeluC * (1.f + 3.f * kGeluA * z * z);
+    const float v = gelu_clamp(z), s = logistic_fast(2.f * gelu_u(v));
+    return s + v * s * (1.f - s) * 2.f * kGeluC * (1.f + 3.f * kGeluA * v * v);
   }
   return act_slope<ACT>(z);
 }

@@ -794,3 +794,14 @@ def test_fp32_gelu_keeps_its_accuracy_in_the_tail(act):
     ry, rs = _act_slope64(act, z)
     assert float((y - ry).abs().max()) <= 6e-6
     assert float((slope - rs).abs().max()) <= 6e-6
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("act", ["silu", "gelu", "gelu_tanh"])
+def test_activations_of_huge_finite_values(act, dtype):
+    """Finite z, however large, have the function's limits: z and 0, slopes 1 and 0."""
+    z = torch.tensor([1e4, 1e10, 1e13, 1e18, 1e20, 1e25, 1e30, 3e38])
+    y, slope = _through_layer(act, torch.cat([z, -z]), dtype)
+    zd = z.to(dtype).double()
+    assert torch.equal(y[:8], zd) and float(y[8:].abs().max()) == 0.0
+    assert torch.equal(slope[:8], torch.ones(8).double()) and float(slope[8:].abs().max()) == 0.0

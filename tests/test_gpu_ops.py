@@ -805,3 +805,22 @@ def test_activations_of_huge_finite_values(act, dtype):
     zd = z.to(dtype).double()
     assert torch.equal(y[:8], zd) and float(y[8:].abs().max()) == 0.0
     assert torch.equal(slope[:8], torch.ones(8).double()) and float(slope[8:].abs().max()) == 0.0
+
+
+def test_linear_repeats_with_and_without_save_at_changing_rows():
+    """The result of every call, kept before the next one writes the layer's buffer: equal bits with
+    and without the pre-activation stored, and again after calls of other sizes."""
+    A = _api()
+    g = _gen(61)
+    N, K = 200, 128
+    w = _rand(g, N, K, std=0.1, dtype=torch.bfloat16)
+    lin = A.Linear(w.cuda(), None, act="silu", max_rows=700)
+    first = {}
+    for M in (700, 1, 64, 65, 3, 700, 65, 1, 64):
+        x = _rand(_gen(M), M, K, dtype=torch.bfloat16)
+        saved = lin.forward(x.cuda(), save=True).clone()
+        assert torch.equal(lin.forward(x.cuda()), saved)
+        lin.forward(-x.cuda())          # something else in the buffer
+        assert torch.equal(lin.forward(x.cuda()), saved)
+        _close(saved, _linear64(x, w, None, None, "silu")[0], torch.bfloat16, M)
+        assert torch.equal(saved, first.setdefault(M, saved))

@@ -304,7 +304,7 @@ def _matrix(t, name, dtype, rows, cols, device):
         if rows > 1:
             raise ValueError(f"{name}: rows of {cols} elements are {ld} apart (expanded? make it contiguous)")
         return cols
-    return ld
+    return ld if rows > 1 else min(ld, cols + 7 & ~7)   # one row: whole vectors, if there is room for them
 
 
 def _overlap(a, ld_a, b, ld_b):
@@ -551,15 +551,18 @@ class Linear:
         ld_x, xp, ld_w = _matrix(x, "x", self.dtype, M, self.K, self.device), x.data_ptr(), D.ld_w
         ld_y, yp = _matrix(dy, "dy", self.dtype, M, n, self.device), dy.data_ptr()
         dx = dw = db = dxp = dwp = dbp = None
-        if "dx" in need:   # rows of dx are as far apart as those of x
-            dx, dxp = self._view(("dx", ld_x), self.max_rows, ld_x, M, self.K)
+        # a call takes one distance for the rows of x and dx: where x's rows lie far apart (slices of
+        # something larger) dx is a call of its own, in dense rows
+        ld_dx = ld_x if ld_x <= 2 * self.K + 64 else self.K
+        if "dx" in need:
+            dx, dxp = self._view(("dx", ld_dx), self.max_rows, ld_dx, M, self.K)
         if "dw" in need:
             dw, dwp = self._view(("dw", ld_w), n, ld_w, n, self.K)
         if "db" in need and self.bias is not None:
             db, dbp = self._view("db", 1, n, 1, n)
         # dw's product reads x and dz last; dz is dy itself where it is not made first
         own_dz = self.act != 0 or (size == 2 and ld_y % 8 != 0)
-        for o, op, rows, ld_o in ((dx, dxp, M, ld_x), (dw, dwp, n, ld_w), (db, dbp, 1, n)):
+        for o, op, rows, ld_o in ((dx, dxp, M, ld_dx), (dw, dwp, n, ld_w), (db, dbp, 1, n)):
             if o is None:
                 continue
             end = op + rows * ld_o * size
@@ -567,11 +570,15 @@ class Linear:
                     dw is not None and xp < end and op < xp + M * ld_x * size and _overlap(x, ld_x, o, ld_o)):
                 raise ValueError("dy or x: overlaps a result of this layer that is written before it is read (pass a copy)")
         z = self._own("z", self.max_rows, n + 7 & ~7).data_ptr() if self.act != 0 else None
-        D.M, D.ld_x, D.ld_y, D.ld_res = M, ld_x, ld_y, 0
-        st = self._bwd(xp, self._w_ptr, z, yp, self._dims_ref, dxp, dwp, dbp, self.ws.ptr, self.ws.nbytes,
-                       _stream(stream, self._index))
-        if st:
-            N.check(st, "moe_linear_bwd")
+        D.M, D.ld_y, D.ld_res = M, ld_y, 0
+        parts = ((ld_x, dxp, dwp, dbp),)
+        if ld_dx != ld_x and dx is not None:
+            parts = ((ld_dx, dxp, None, None),) + (((ld_x, None, dwp, dbp),) if dw is not None or db is not None else ())
+        for D.ld_x, dxp, dwp, dbp in parts:
+            st = self._bwd(xp, self._w_ptr, z, yp, self._dims_ref, dxp, dwp, dbp, self.ws.ptr, self.ws.nbytes,
+                           _stream(stream, self._index))
+            if st:
+                N.check(st, "moe_linear_bwd")
         return dict(dx=dx, dw=dw, db=None if db is None else db[0])
 
 

@@ -824,3 +824,24 @@ def test_linear_repeats_with_and_without_save_at_changing_rows():
         assert torch.equal(lin.forward(x.cuda()), saved)
         _close(saved, _linear64(x, w, None, None, "silu")[0], torch.bfloat16, M)
         assert torch.equal(saved, first.setdefault(M, saved))
+
+
+@pytest.mark.parametrize("act", ["none", "gelu"])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("M,K", [(1, 67), (3, 72), (130, 65)])
+def test_linear_rows_far_apart(M, K, dtype, act):
+    """The last positions of sequences: rows of x a sequence apart, dx in rows of its own."""
+    A = _api()
+    N, far = 136, 5003
+    g = _gen(M + K)
+    x, w, b = _rand(g, M, K, dtype=dtype), _rand(g, N, K, std=K ** -0.5, dtype=dtype), _rand(g, N, dtype=dtype)
+    dy = _rand(g, M, N, dtype=dtype)
+    wide = torch.full((M, far), 3.0, dtype=dtype)
+    wide[:, 16:16 + K] = x
+    rows = wide.cuda()[:, 16:16 + K]
+    lin = A.Linear(w.cuda(), b.cuda(), act=act, max_rows=M + 1)
+    y, ref = _linear64(x, w, b, None, act, dy)
+    _close(lin.forward(rows, save=True), y, dtype)
+    grads = lin.backward(dy.cuda())
+    for name in ("dx", "dw", "db"):
+        _close(grads[name], ref[name], dtype, name)

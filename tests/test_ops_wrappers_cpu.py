@@ -388,3 +388,43 @@ def test_verify_refuses_its_results_as_inputs(lib):
     ver.verify(**{**good, "draft_len": accepted}, stream=ST)
     with pytest.raises(ValueError, match="draft_len"):
         ver.verify(**{**drafts(B_=2), "draft_len": accepted[1:3]}, stream=ST)
+
+
+# ------------------------------------------------------------------ rows far apart
+def test_linear_rows_far_apart_cost_no_memory(lib):
+    """The last positions of long sequences lie a sequence apart: neither the gradient nor anything
+    else of the layer's takes that distance."""
+    n, k, rows, far = 32, 64, 8, 100000
+    lin = linear(n, k, rows)
+    x = torch.zeros(3, far)[:, -k:]
+    dy = torch.zeros(3, n)
+    lin.forward(x, save=True, stream=ST)
+    assert lib.last("moe_linear_fwd")[4]["ld_x"] == far
+    for need in (("dx", "dw", "db"), ("dx",), ("dw",)):
+        lib.calls.clear()
+        grads = lin.backward(dy, need=need, stream=ST)
+        calls = [v for name, v in lib.calls if name == "moe_linear_bwd"]
+        assert len(calls) == min(2, len(need))
+        if "dx" in need:
+            assert grads["dx"].shape == (3, k) and grads["dx"].untyped_storage().nbytes() <= 4 * rows * 2 * k
+            (with_dx,) = [v for v in calls if v[5] is not None]
+            assert with_dx[4]["ld_x"] == grads["dx"].stride(0) and with_dx[6] is None
+        if "dw" in need:
+            (with_dw,) = [v for v in calls if v[6] is not None]
+            assert with_dw[4]["ld_x"] == far and with_dw[0] == x.data_ptr() and with_dw[5] is None
+    # a single row has no distance
+    one = torch.zeros(1, far)[:, :k]
+    lin.forward(one, save=True, stream=ST)
+    assert lib.last("moe_linear_fwd")[4]["ld_x"] == k
+    lib.calls.clear()
+    lin.backward(torch.zeros(1, n), stream=ST)
+    assert len(lib.calls) == 1
+
+
+def test_one_odd_row_keeps_its_whole_vectors(lib):
+    """One bf16 row that has room for whole 16-byte vectors is not copied for their sake."""
+    lin = A.Linear(torch.zeros(32, 72, dtype=torch.bfloat16)[:, :67], None, max_rows=8, device=DEV, stream=ST)
+    lin.forward(torch.zeros(1, 80, dtype=torch.bfloat16)[:, :67], stream=ST)
+    assert lib.last("moe_linear_fwd")[4]["ld_x"] == 72
+    lin.forward(torch.zeros(1, 67, dtype=torch.bfloat16), stream=ST)
+    assert lib.last("moe_linear_fwd")[4]["ld_x"] == 67

@@ -10,6 +10,7 @@ constexpr size_t kOpHeader = kOpFlags + 8 * 64 * kMaxK;   // and the selections 
 constexpr int kDecodeMaxT = 64;       // tokens of moe_layer_decode
 static_assert(kOpHeader == kOpFlags + 8 * kDecodeMaxT * kMaxK, "");
 
+constexpr int64_t kMaxLd = 1ll << 36;   // elements between rows
 inline size_t round256(size_t x) { return (x + 255) & ~size_t(255); }
 
 constexpr int kMaxStreamCtas = 160;   // CTAs of a weight stream

@@ -73,7 +73,8 @@ int check_decode(const moe_dims* d) {
   return check_layer_dims(d);
 }
 
-// Strides are checked with their defaults in place; no tensor is larger than 2^62 bytes.
+// Strides are checked with their defaults in place. M <= 2^30 rows 2^36 elements apart: offsets stay
+// within 64 bits for any tensor that exists, and a tensor map's strides (below 2^40 bytes) hold them.
 int resolve_linear(const moe_linear_dims* in, moe_linear_dims* d) {
   if (in == nullptr) return MOE_ERR_NULL_POINTER;
   *d = *in;
@@ -84,9 +85,8 @@ int resolve_linear(const moe_linear_dims* in, moe_linear_dims* d) {
   if (d->ld_w == 0) d->ld_w = d->K;
   if (d->ld_y == 0) d->ld_y = d->N;
   if (d->ld_res == 0) d->ld_res = d->N;
-  const int64_t most = 1ll << 28;
-  if (d->ld_x < d->K || d->ld_w < d->K || d->ld_y < d->N || d->ld_res < d->N || d->ld_x > most || d->ld_w > most ||
-      d->ld_y > most || d->ld_res > most)
+  if (d->ld_x < d->K || d->ld_w < d->K || d->ld_y < d->N || d->ld_res < d->N || d->ld_x > kMaxLd || d->ld_w > kMaxLd ||
+      d->ld_y > kMaxLd || d->ld_res > kMaxLd)
     return MOE_ERR_BAD_DIMS;
   return MOE_OK;
 }
@@ -269,7 +269,7 @@ int moe_verify_draft(const int32_t* draft_tokens, const int32_t* draft_len, cons
   if (dims->dtype != MOE_F32 && dims->dtype != MOE_BF16) return MOE_ERR_UNSUPPORTED_DTYPE;
   if (dims->B < 0 || dims->B > (1 << 26) || dims->n < 0 || dims->n > 1024 || dims->V < 1 || dims->V > (1 << 22) ||
       (dims->ld_draft != 0 && dims->ld_draft < dims->V) || (dims->ld_target != 0 && dims->ld_target < dims->V) ||
-      dims->ld_draft > (1 << 24) || dims->ld_target > (1 << 24))
+      dims->ld_draft > kMaxLd || dims->ld_target > kMaxLd)
     return MOE_ERR_BAD_DIMS;
   const bool some = dims->B > 0, drafts = some && dims->n > 0;
   OP_TRY(req_if(draft_tokens, drafts));

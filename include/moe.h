@@ -383,7 +383,7 @@ typedef struct moe_linear_dims {
   int32_t N, K;     /* output and input width, 1 .. 4194240 (65535 * 64) */
   int32_t act;      /* enum moe_act */
   int32_t dtype;    /* enum moe_dtype: x, w, bias, residual, y, z and every gradient */
-  int64_t ld_x;     /* elements between rows of x and dx (>= K), 0 = K */
+  int64_t ld_x;     /* elements between rows of x and dx (>= K, as all of these <= 2^36), 0 = K */
   int64_t ld_w;     /* ... of w and dw (>= K), 0 = K */
   int64_t ld_y;     /* ... of y and dy (>= N), 0 = N */
   int64_t ld_res;   /* ... of residual (>= N), 0 = N */
@@ -419,7 +419,7 @@ typedef struct moe_verify_dims {
   int32_t n;         /* drafted tokens per sequence, 0 <= n <= 1024 */
   int32_t V;         /* vocabulary, 1 <= V <= 2^22 */
   int32_t dtype;     /* enum moe_dtype of both probability tensors */
-  int64_t ld_draft;  /* elements between rows of draft_probs (>= V), 0 = V */
+  int64_t ld_draft;  /* elements between rows of draft_probs (>= V, <= 2^36), 0 = V */
   int64_t ld_target; /* ... of target_probs */
 } moe_verify_dims;
 

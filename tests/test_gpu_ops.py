@@ -845,3 +845,28 @@ def test_linear_rows_far_apart(M, K, dtype, act):
     grads = lin.backward(dy.cuda())
     for name in ("dx", "dw", "db"):
         _close(grads[name], ref[name], dtype, name)
+
+
+def test_rows_a_long_sequence_apart():
+    """Rows 2^28 elements and more apart (x) and 2^24 and more (probabilities of the last position)."""
+    A = _api()
+    M, N, K, far = 2, 40, 72, (1 << 28) + 64
+    g = _gen(71)
+    w = _rand(g, N, K, std=0.1, dtype=torch.bfloat16)
+    x, dy = _rand(g, M, K, dtype=torch.bfloat16), _rand(g, M, N, dtype=torch.bfloat16)
+    wide = torch.zeros(M, far, dtype=torch.bfloat16, device="cuda")
+    rows = wide[:, far - 80:far - 8]
+    rows.copy_(x)
+    lin = A.Linear(w.cuda(), None, max_rows=M)
+    y, ref = _linear64(x, w, None, None, "none", dy)
+    _close(lin.forward(rows, save=True), y, torch.bfloat16)
+    grads = lin.backward(dy.cuda())
+    _close(grads["dx"], ref["dx"], torch.bfloat16)
+    _close(grads["dw"], ref["dw"], torch.bfloat16)
+    B, S, V = 2, 40, 500000
+    p = torch.zeros(B, S, V, device="cuda")
+    p[0, -1, 123456] = 0.5
+    p[1, -1, 499999] = 0.25
+    got, acc = A.DraftVerifier(B, 0, V).verify(torch.zeros(B, 0, dtype=torch.int32).cuda(), torch.zeros(B, 0, V).cuda(),
+                                               p[:, -1:], torch.zeros(B, 0).cuda(), torch.tensor([0.1, 0.9]).cuda())
+    assert got[:, 0].tolist() == [123456, 499999] and acc.tolist() == [0, 0]

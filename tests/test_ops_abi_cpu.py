@@ -201,3 +201,16 @@ print({{"decode_bf16": lambda: decode(N.MOE_BF16), "decode_f32": lambda: decode(
     out = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, check=True,
                          env={**os.environ, "LD_PRELOAD": str(so), "CUDA_VISIBLE_DEVICES": ""})
     assert int(out.stdout) == C["MOE_ERR_UNSUPPORTED_DEVICE"], out.stdout
+
+
+def test_long_strides_are_allowed():
+    """The last positions of long sequences lie far apart: 2^36 elements and no more."""
+    far = 1 << 36
+    for name in ("ld_x", "ld_w", "ld_y", "ld_res"):
+        for ld, fits in ((1 << 30, True), (far, True), (far + 1, False), (1 << 62, False)):
+            assert (L.moe_linear_workspace_bytes(REF(linear_dims(**{name: ld}))) > 0) == fits, (name, ld)
+    null, bad = C["MOE_ERR_NULL_POINTER"], C["MOE_ERR_BAD_DIMS"]
+    for name in ("ld_draft", "ld_target"):
+        for ld, want in ((1 << 30, null), (far, null), (far + 1, bad), (1 << 62, bad)):
+            d = verify_dims(**{name: ld})
+            assert L.moe_verify_draft(None, None, GOOD, GOOD, GOOD, GOOD, REF(d), GOOD, GOOD, None) == want, (name, ld)

@@ -2,6 +2,7 @@
 every computation runs in libmoe's kernels.  Names follow include/moe.h."""
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import weakref
 from dataclasses import dataclass
@@ -259,6 +260,12 @@ class MoELayer:
 
 
 # ------------------------------------------------------------------ few-token operators
+def _on(stream, device):
+    """Memory made inside is the given stream's: what the allocator has of the current stream's may
+    still be read there."""
+    return torch.cuda.stream(stream) if stream is not None and device.type == "cuda" else contextlib.nullcontext()
+
+
 class OpWorkspace:
     """Device workspace of a few-token operator: its header is zeroed once, here."""
 
@@ -266,7 +273,8 @@ class OpWorkspace:
         if nbytes == 0:
             raise N.MoeError(N.STATUS_CODE["MOE_ERR_BAD_DIMS"], call)
         self.nbytes = int(nbytes)
-        self.buf = torch.empty(self.nbytes + 256, dtype=torch.uint8, device=device)
+        with _on(stream, torch.device(device)):
+            self.buf = torch.empty(self.nbytes + 256, dtype=torch.uint8, device=device)
         self.ptr = self.buf.data_ptr() + (-self.buf.data_ptr()) % 256
         N.check(N.lib().moe_op_workspace_init(self.ptr, self.nbytes, _s(stream)), "moe_op_workspace_init")
 
@@ -360,7 +368,8 @@ class MoEDecodeLayer:
     y [T, d], the layer's own buffer (overwritten by the next call) unless ``out`` is given
     (x and residual are allowed, a residual that only partly overlaps it is not). ``topk_idx`` and
     ``topk_w`` hold the last call's selection. Every call takes the weights that ``params`` holds
-    then (a captured graph those of the capture). One instance serves one stream at a time.
+    then (a captured graph those of the capture). One instance serves one stream at a time, which
+    waits for the one it was made on.
     """
 
     def __init__(self, params: LayerParams, max_tokens, d, E, k, f, S=0, f_s=0, dtype=torch.bfloat16,
@@ -457,7 +466,8 @@ class Linear:
     (written by the next call, which may therefore not read it: a result that goes through the
     layer again needs another ``out``) unless ``out`` is given; with ``save=True`` it keeps x and the
     pre-activation for ``backward(dy)``, which returns dict(dx, dw, db) (own buffers too; ``need``
-    names those to compute). The residual's gradient is dy itself. ``out`` may be the residual.
+    names those to compute). The residual's gradient is dy itself. ``out`` may be the residual. One
+    instance serves one stream at a time, which waits for the one it was made on.
     """
 
     def __init__(self, w, bias=None, act="none", max_rows=1, device=None, stream=None):
@@ -490,19 +500,20 @@ class Linear:
         self._w_ptr, self._b_ptr = w.data_ptr(), _p(bias)
         self._w_ref, self._b_ref = _ref(w), _ref(bias)
 
-    def _own(self, name, rows, cols):
-        """The layer's buffer ``name``, made at its first use."""
+    def _own(self, name, rows, cols, stream):
+        """The layer's buffer ``name``, made at its first use, of the call's stream."""
         t = self._bufs.get(name)
         if t is None:
-            t = self._bufs[name] = torch.empty(rows, cols, dtype=self.dtype, device=self.device)
+            with _on(stream, self.device):
+                t = self._bufs[name] = torch.empty(rows, cols, dtype=self.dtype, device=self.device)
         return t
 
-    def _view(self, name, rows, cols, M, width):
+    def _view(self, name, rows, cols, M, width, stream):
         """[M, width] of the buffer ``name`` [rows, cols], and its address."""
         key = (name, M, width)
         v = self._views.get(key)
         if v is None:
-            t = self._own(name, rows, cols)[:M, :width]
+            t = self._own(name, rows, cols, stream)[:M, :width]
             v = self._views[key] = t, t.data_ptr()
         return v
 
@@ -512,7 +523,7 @@ class Linear:
             raise ValueError(f"{M} rows, the layer was made for {self.max_rows}")
         ld_x, xp = _matrix(x, "x", dtype, M, self.K, dev), x.data_ptr()
         if out is None:
-            y, yp = self._view("y", self.max_rows, n, M, n)
+            y, yp = self._view("y", self.max_rows, n, M, n, stream)
             ld_y = n
         else:
             y, yp, ld_y = out, out.data_ptr(), _matrix(out, "out", dtype, M, n, dev)
@@ -532,7 +543,7 @@ class Linear:
         if out is not None and (_overlap(self.w, D.ld_w, y, ld_y) or
                                 (self.bias is not None and _overlap(self.bias[None], n, y, ld_y))):
             raise ValueError("out: overlaps the layer's weights")
-        z = self._own("z", self.max_rows, n + 7 & ~7).data_ptr() if save and self.act != 0 else None
+        z = self._own("z", self.max_rows, n + 7 & ~7, stream).data_ptr() if save and self.act != 0 else None
         self._x = x if save else None
         D.M, D.ld_x, D.ld_y, D.ld_res = M, ld_x, ld_y, ld_r
         st = self._fwd(xp, self._w_ptr, self._b_ptr, rp, self._dims_ref, z, yp, self.ws.ptr, self.ws.nbytes,
@@ -555,11 +566,11 @@ class Linear:
         # something larger) dx is a call of its own, in dense rows
         ld_dx = ld_x if ld_x <= 2 * self.K + 64 else self.K
         if "dx" in need:
-            dx, dxp = self._view(("dx", ld_dx), self.max_rows, ld_dx, M, self.K)
+            dx, dxp = self._view(("dx", ld_dx), self.max_rows, ld_dx, M, self.K, stream)
         if "dw" in need:
-            dw, dwp = self._view(("dw", ld_w), n, ld_w, n, self.K)
+            dw, dwp = self._view(("dw", ld_w), n, ld_w, n, self.K, stream)
         if "db" in need and self.bias is not None:
-            db, dbp = self._view("db", 1, n, 1, n)
+            db, dbp = self._view("db", 1, n, 1, n, stream)
         # dw's product reads x and dz last; dz is dy itself where it is not made first
         own_dz = self.act != 0 or (size == 2 and ld_y % 8 != 0)
         for o, op, rows, ld_o in ((dx, dxp, M, ld_dx), (dw, dwp, n, ld_w), (db, dbp, 1, n)):
@@ -569,7 +580,7 @@ class Linear:
             if (not own_dz and yp < end and op < yp + M * ld_y * size and _overlap(dy, ld_y, o, ld_o)) or (
                     dw is not None and xp < end and op < xp + M * ld_x * size and _overlap(x, ld_x, o, ld_o)):
                 raise ValueError("dy or x: overlaps a result of this layer that is written before it is read (pass a copy)")
-        z = self._own("z", self.max_rows, n + 7 & ~7).data_ptr() if self.act != 0 else None
+        z = self._own("z", self.max_rows, n + 7 & ~7, stream).data_ptr() if self.act != 0 else None
         D.M, D.ld_y, D.ld_res = M, ld_y, 0
         parts = ((ld_x, dxp, dwp, dbp),)
         if ld_dx != ld_x and dx is not None:

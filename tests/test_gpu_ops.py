@@ -870,3 +870,30 @@ def test_rows_a_long_sequence_apart():
     got, acc = A.DraftVerifier(B, 0, V).verify(torch.zeros(B, 0, dtype=torch.int32).cuda(), torch.zeros(B, 0, V).cuda(),
                                                p[:, -1:], torch.zeros(B, 0).cuda(), torch.tensor([0.1, 0.9]).cuda())
     assert got[:, 0].tolist() == [123456, 499999] and acc.tolist() == [0, 0]
+
+
+def test_linear_buffers_belong_to_the_call_s_stream():
+    """The layer's buffers are made in a call: memory that the current stream still reads (freed, but
+    with work pending) must not become the output of a call on another stream."""
+    A = _api()
+    M, N, K = 256, 4096, 64
+    g = _gen(81)
+    w, x = _rand(g, N, K, std=0.1, dtype=torch.bfloat16).cuda(), _rand(g, M, K, dtype=torch.bfloat16).cuda()
+    dy = _rand(g, M, N, dtype=torch.bfloat16).cuda()
+    side = torch.cuda.Stream()
+    lin = A.Linear(w, torch.zeros(N, dtype=torch.bfloat16, device="cuda"), act="silu", max_rows=M)
+    torch.cuda.synchronize()
+    shapes = ((M, N), (M, N), (M, K), (N, K), (1, N))      # y, z, dx, dw, db
+    freed = [torch.full(s, 1.0, dtype=torch.bfloat16, device="cuda") for s in shapes]
+    copies = [torch.empty_like(t) for t in freed]
+    torch.cuda.synchronize()
+    torch.cuda._sleep(100_000_000)      # tens of milliseconds on the current stream
+    for c, t in zip(copies, freed):
+        c.copy_(t)
+    del freed, t
+    lin.forward(x, save=True, stream=side)
+    grads = lin.backward(dy, stream=side)
+    torch.cuda.synchronize()
+    for c in copies:
+        assert bool((c == 1.0).all())
+    _close(grads["dw"], _linear64(x.cpu(), w.cpu(), None, None, "silu", dy.cpu())[1]["dw"], torch.bfloat16)

@@ -19,10 +19,10 @@
 // same product for its dW), y once. Scores, gates and all sums are fp32.
 //
 // Bound by the stream out of HBM, and with few bytes by the chain scores - selection - hidden rows -
-// output, whose steps each wait for all CTAs. Measured: T = 32, d = 7168, 81 experts read:
-// 7.16 GB in 1.06-1.10 ms, 6.5-6.7 TB/s (the copy rate is 6.8); T = 1, d = 7680, 9 experts:
-// 857 MB in 145 us, 5.9 TB/s; T = 5, d = 2048, 26 experts: 460 MB in 89 us, 5.2 TB/s; T = 10, d =
-// 448: 1.8 MB in 22 us, all of it the chain.
+// output, whose steps each wait for all CTAs. Measured: T = 32, d = 7168, 77 to 88 experts selected:
+// 6.9-7.8 GB in 1.04-1.17 ms, 6.7 TB/s (the copy rate is 6.8); T = 1, d = 7680, 8 experts and a shared
+// one: 857 MB in 145-151 us, 5.7-5.9 TB/s; T = 5, d = 2048, 22 to 27 experts and two shared ones: 416-502
+// MB in 89-100 us, 4.7-5.1 TB/s; T = 10, d = 448: 1.8 MB in 22 us, all of it the chain.
 #include <string.h>
 
 #include <mutex>

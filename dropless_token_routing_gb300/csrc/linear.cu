@@ -1,8 +1,9 @@
 // The linear layer's fp32 products, on the FMA pipes, and the elementwise half of its backward.
 //
 // The tensor cores have no fp32 type, and three bf16 parts would lose what fp32 keeps at the ends of
-// its range. The products are bound by the FMA pipe's issue (ncu, 2048 x 2048 x 512: pipe 55 % busy
-// while a block runs; the loop's shared-memory loads and copies take the other slots): 1024 x 1024 x
+// its range. The products are bound by latency that 16 warps on an SM do not hide (ncu, 2048 x 2048 x
+// 512: FMA pipe 55 % busy while a block runs, issue slots 39 %; a warp waits for fixed latencies, shared
+// and global memory and instructions, with a block-wide barrier for every 16 of K): 1024 x 1024 x
 // 1024: 51 us, 42 TFLOP/s; 900 x 900 x 4000: 162 us, 40 TFLOP/s (75 is the pipes' rate).
 #include "act.cuh"
 #include "launch.cuh"

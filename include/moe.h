@@ -393,7 +393,9 @@ typedef struct moe_linear_dims {
  *   z = x W^T + b,   y = act(z) + r        x [M, K], w [N][K], bias [N] or NULL, residual [M, N]
  * or NULL, z [M][N rounded up to a multiple of 8] receives the pre-activation for the backward, or
  * NULL.
- * fp32 accumulation, y rounded once (not from the rounded z). residual may be the buffer of y
+ * fp32 accumulation, y rounded once (not from the rounded z). In bf16 the activations (and their
+ * derivatives in the backward) use the hardware's exponential and reciprocal, a few 2^-22 off, and
+ * GELU a cumulative with an error of 7.5e-8, absolute. residual may be the buffer of y
  * (y updated in place) when their strides agree. y and z overlap no other input: the launch reads
  * all of x and w while it writes them. Base pointers are 16-byte aligned; strides and
  * widths may be odd (bf16 rows of x and w that are not whole 16-byte vectors are copied in every

@@ -214,3 +214,13 @@ def test_long_strides_are_allowed():
         for ld, want in ((1 << 30, null), (far, null), (far + 1, bad), (1 << 62, bad)):
             d = verify_dims(**{name: ld})
             assert L.moe_verify_draft(None, None, GOOD, GOOD, GOOD, GOOD, REF(d), GOOD, GOOD, None) == want, (name, ld)
+
+
+def test_decode_timeout_probe_is_checked():
+    p, d = N.LayerParams(GOOD, None, GOOD, GOOD, None, None), layer_dims()
+    n = L.moe_decode_workspace_bytes(REF(d))
+    call = L.moe_debug_decode_timeout_probe
+    assert call(None, GOOD, REF(d), GOOD, GOOD, n, None) == C["MOE_ERR_NULL_POINTER"]
+    assert call(REF(p), BAD, REF(d), GOOD, GOOD, n, None) == C["MOE_ERR_MISALIGNED"]
+    assert call(REF(p), GOOD, REF(d), GOOD, GOOD, n - 1, None) == C["MOE_ERR_WORKSPACE_TOO_SMALL"]
+    assert call(REF(p), GOOD, REF(layer_dims(T=65)), GOOD, GOOD, n, None) == C["MOE_ERR_BAD_DIMS"]

@@ -34,9 +34,9 @@ template <int ACT> __device__ __forceinline__ float act_slope(float z) {
   if constexpr (ACT == MOE_ACT_GELU)
     return 0.5f * erfcf(-z * kSqrtHalf) + z * kInvSqrt2Pi * expf(-0.5f * z * z);
   if constexpr (ACT == MOE_ACT_GELU_TANH) {
-    // act = z s(2u), s' = s(2u) s(-2u)
-    const float v = gelu_clamp(z), u = 2.f * gelu_u(v), s = 1.f / (1.f + expf(-u)), r = 1.f / (1.f + expf(u));
-    return s + v * s * r * 2.f * kGeluC * (1.f + 3.f * kGeluA * v * v);
+    // act = z s(2u), s' = s(2u) s(-2u); of these the one below 1/2 is e / (1 + e), the other 1 / (1 + e)
+    const float v = gelu_clamp(z), u = 2.f * gelu_u(v), e = expf(-fabsf(u)), big = 1.f / (1.f + e), small = e * big;
+    return (u > 0.f ? big : small) + v * big * small * 2.f * kGeluC * (1.f + 3.f * kGeluA * v * v);
   }
   return 1.f;
 }

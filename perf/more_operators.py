@@ -206,7 +206,7 @@ def _handle(api, c, s):
         return api.LayerNorm(s["weight"], s["bias"], eps=EPS, max_rows=c["M"], dtype=_dtype(c["dtype"]))
     if c["op"] == "logprob":
         return api.TokenLogprobs(c["M"], c["V"], top=c["top"], dtype=_dtype(c["dtype"]))
-    return api.GradClipper(len(s["grads"]))
+    return api.GradClipper(s["grads"], out=s.get("out"))
 
 
 # ------------------------------------------------------------------ one pass
@@ -242,9 +242,8 @@ def _own_logprob(c, s):
 
 def _own_clip(c, s):
     if c["dir"] == "norm":
-        return {"norm": s["handle"].norm(s["grads"])}
-    norm = s["handle"].clip(s["grads"], s["max_norm"], out=s["out"])
-    return {"norm": norm, "grads": s["flat"]}
+        return {"norm": s["handle"].norm()}
+    return {"norm": s["handle"].clip(s["max_norm"]), "grads": s["flat"]}
 
 
 def _plain_norm(c, s):

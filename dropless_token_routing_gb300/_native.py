@@ -27,6 +27,7 @@ STATUS = {
     0: "MOE_OK", -1: "MOE_ERR_NULL_POINTER", -2: "MOE_ERR_MISALIGNED", -3: "MOE_ERR_BAD_DIMS",
     -4: "MOE_ERR_BAD_TOPK", -5: "MOE_ERR_UNSUPPORTED_DTYPE", -6: "MOE_ERR_WORKSPACE_TOO_SMALL",
     -7: "MOE_ERR_LAUNCH", -8: "MOE_ERR_CUDA", -9: "MOE_ERR_UNSUPPORTED_DEVICE",
+    -10: "MOE_ERR_OVERLAP",
     -100: "MOE_ERR_DEVICE_EXPERT_ID", -101: "MOE_ERR_DEVICE_TIMEOUT",
 }
 STATUS_CODE = {v: k for k, v in STATUS.items()}
@@ -75,6 +76,20 @@ class VerifyDims(ctypes.Structure):
                 ("ld_target", c_int64)]
 
 
+class NormDims(ctypes.Structure):
+    _fields_ = [("M", c_int64), ("N", c_int32), ("dtype", c_int32), ("w_dtype", c_int32), ("eps", ctypes.c_float),
+                ("ld_x", c_int64), ("ld_res", c_int64), ("ld_sum", c_int64), ("ld_y", c_int64), ("ld_dx", c_int64)]
+
+
+class LogprobDims(ctypes.Structure):
+    _fields_ = [("M", c_int64), ("V", c_int32), ("n_top", c_int32), ("dtype", c_int32), ("ld", c_int64),
+                ("ld_grad", c_int64)]
+
+
+class Grad(ctypes.Structure):
+    _fields_ = [("g", c_void_p), ("out", c_void_p), ("n", c_int64), ("dtype", c_int32)]
+
+
 ACTS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}   # enum moe_act
 
 P = c_void_p
@@ -116,6 +131,13 @@ _SIGS = {
     "moe_linear_fwd": (c_int, [P, P, P, P, ctypes.POINTER(LinearDims), P, P, P, c_size_t, P]),
     "moe_linear_bwd": (c_int, [P, P, P, P, ctypes.POINTER(LinearDims), P, P, P, P, c_size_t, P]),
     "moe_verify_draft": (c_int, [P, P, P, P, P, P, ctypes.POINTER(VerifyDims), P, P, P]),
+    "moe_norm_fwd": (c_int, [P, P, P, P, ctypes.POINTER(NormDims), P, P, P, P]),
+    "moe_norm_workspace_bytes": (c_size_t, [ctypes.POINTER(NormDims)]),
+    "moe_norm_bwd": (c_int, [P, P, P, P, P, P, ctypes.POINTER(NormDims), P, P, P, P, c_size_t, P]),
+    "moe_token_logprob": (c_int, [P, P, ctypes.POINTER(LogprobDims), P, P, P, P, P, P]),
+    "moe_token_logprob_bwd": (c_int, [P, P, P, P, P, P, ctypes.POINTER(LogprobDims), P, P]),
+    "moe_clip_workspace_bytes": (c_size_t, [c_int64]),
+    "moe_clip_grads": (c_int, [P, c_int64, ctypes.c_float, P, P, P, c_size_t, P]),
     "moe_debug_timeout_probe": (c_int, [P, c_size_t, c_uint64, P]),
     "moe_debug_decode_timeout_probe": (c_int, [ctypes.POINTER(LayerParams), P, ctypes.POINTER(MoeDims), P, P, c_size_t, P]),
     "moe_trace_enable": (c_int, [c_int]),

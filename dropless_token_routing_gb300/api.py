@@ -15,7 +15,7 @@ from . import _native as N
 __all__ = ["make_dims", "Workspace", "router_logits", "route_topk", "permute", "permute_rows",
            "grouped_swiglu_fwd", "unpermute_combine", "grouped_bwd_dx", "grouped_bwd_dw",
            "route_topk_bwd", "LayerParams", "MoELayer", "get_device_error", "debug_timeout_probe",
-           "OpWorkspace", "MoEDecodeLayer", "Linear", "DraftVerifier"]
+           "OpWorkspace", "MoEDecodeLayer", "Linear", "DraftVerifier", "LayerNorm", "TokenLogprobs", "GradClipper"]
 
 
 def _p(t: Optional[torch.Tensor]):
@@ -663,3 +663,314 @@ class DraftVerifier:
         if st:
             N.check(st, "moe_verify_draft")
         return out
+
+
+# ------------------------------------------------------------------ around the layer in training
+def _in_place(name, t, ld, out, ld_out, what):
+    """Refuses an operand that overlaps a result unless it lies just where that does."""
+    M = t.shape[0]
+    if t.data_ptr() == out.data_ptr() and (ld == ld_out or M == 1):
+        return
+    if _overlap(t, ld, out, ld_out):
+        raise ValueError(f"{name}: overlaps {what} and does not lie where it does")
+
+
+class LayerNorm:
+    """y = (s - mean) rstd weight + bias with s = x + residual, and its gradients: moe_norm_fwd /
+    moe_norm_bwd on kept buffers for up to ``max_rows`` rows. ``dtype`` is the rows' (default the
+    weight's; bf16 rows may have fp32 weights). Every call takes the ``weight`` and ``bias`` that the
+    layer holds then.
+
+    ``forward(x, residual=None, save=False)`` returns y [M, N], or (y, s) with a residual: the layer's own
+    buffers (written by the next call) unless ``out`` and ``sum_out`` are given, which may be x or the
+    residual. With ``save=True`` it keeps what was normed (s, or x itself: unchanged until then) for
+    ``backward(dy, d_sum=None)``, which returns dict(dx, dw, db) (own buffers too; ``need`` names those to
+    compute; ``out`` takes dx and may be dy, d_sum or what was kept). d_sum is the gradient of s by its other
+    way; dx is the gradient of x and of the residual. bf16 rows with fp32 weights keep x and the residual
+    in place of s, whose rounding the gradient of the weight would show (s where a result has taken
+    the place of one of them). One instance serves one stream at a time, which waits for
+    the one it was made on.
+    """
+
+    def __init__(self, weight, bias=None, eps=1e-5, max_rows=1, dtype=None, device=None, stream=None):
+        self.weight, self.bias, self.eps, self.max_rows = weight, bias, eps, max_rows
+        self.dtype, self.w_dtype = dtype if dtype is not None else weight.dtype, weight.dtype
+        (self.N,) = weight.shape
+        self.device, self._index = _device(device if device is not None else weight.device)
+        self.dims = N.NormDims(int(max_rows), self.N, _dt(self.dtype), _dt(self.w_dtype), eps, 0, 0, 0, 0, 0)
+        self._bind()
+        self.ws = None
+        if N.lib().moe_norm_workspace_bytes(ctypes.byref(self.dims)) == 0:
+            raise N.MoeError(N.STATUS_CODE["MOE_ERR_BAD_DIMS"], "moe_norm_workspace_bytes")
+        self._bufs, self._views, self._s = {}, {}, None
+        self._dims_ref = ctypes.byref(self.dims)
+        self._fwd, self._bwd = N.lib().moe_norm_fwd, N.lib().moe_norm_bwd
+
+    def _bind(self):
+        self._w_ref = lambda: None      # nothing, should a check fail
+        _dense(self.weight, "weight", self.w_dtype, (self.N,), self.device)
+        if self.bias is not None:
+            _dense(self.bias, "bias", self.w_dtype, (self.N,), self.device)
+        self._w_ptr, self._b_ptr = self.weight.data_ptr(), _p(self.bias)
+        self._w_ref, self._b_ref = _ref(self.weight), _ref(self.bias)
+
+    def _view(self, name, M, stream):
+        """The first M rows of the layer's buffer ``name`` (made at its first use, of the call's stream), and
+        its address."""
+        v = self._views.get((name, M))
+        if v is None:
+            t = self._bufs.get(name)
+            if t is None:
+                shape, dt = {"stats": ((self.max_rows, 2), torch.float32), "dw": ((1, self.N), self.w_dtype),
+                             "db": ((1, self.N), self.w_dtype)}.get(name, ((self.max_rows, self.N), self.dtype))
+                with _on(stream, self.device):
+                    t = self._bufs[name] = torch.empty(shape, dtype=dt, device=self.device)
+            v = self._views[(name, M)] = t[:M], t.data_ptr()
+        return v
+
+    def _present(self):
+        if not (_same(self.weight, self._w_ref, self._w_ptr) and _same(self.bias, self._b_ref, self._b_ptr)):
+            self._bind()
+
+    def _result(self, name, given, M, stream):
+        """Tensor, address and row distance of a result: the layer's own buffer or the caller's."""
+        if given is None:
+            return (*self._view(name, M, stream), self.N)
+        ld = _matrix(given, name, self.dtype, M, self.N, self.device)
+        for wname, t in (("weight", self.weight), ("bias", self.bias)):
+            if t is not None and given.numel() and _bytes_meet(given, ld, t):
+                raise ValueError(f"{name}: overlaps the layer's {wname}")
+        return given, given.data_ptr(), ld
+
+    def forward(self, x, residual=None, save=False, out=None, sum_out=None, stream=None):
+        M, D, dev, dtype, n = x.shape[0], self.dims, self.device, self.dtype, self.N
+        if M > self.max_rows:
+            raise ValueError(f"{M} rows, the layer was made for {self.max_rows}")
+        ld_x = _matrix(x, "x", dtype, M, n, dev)
+        self._present()
+        y, yp, ld_y = self._result("y", out, M, stream)
+        _in_place("x", x, ld_x, y, ld_y, "the output")
+        s, sp, ld_s, rp, ld_r = x, None, 0, None, 0
+        if residual is not None:
+            ld_r, rp = _matrix(residual, "residual", dtype, M, n, dev), residual.data_ptr()
+            s, sp, ld_s = self._result("sum", sum_out, M, stream)
+            _in_place("residual", residual, ld_r, y, ld_y, "the output")
+            _in_place("residual", residual, ld_r, s, ld_s, "the sum")
+            _in_place("x", x, ld_x, s, ld_s, "the sum")
+            if (out is not None or sum_out is not None) and _overlap(y, ld_y, s, ld_s):
+                raise ValueError("out: overlaps the sum")
+        elif sum_out is not None:
+            raise ValueError("sum_out: there is no residual to add")
+        elif save and yp == x.data_ptr() and M:
+            raise ValueError("out: x is needed for the backward")
+        stats = self._view("stats", M, stream)[1] if save else None
+        if not save:
+            self._s = None
+        elif residual is None:
+            self._s = x, ld_x, None, 0
+        elif dtype != self.w_dtype and not ({x.data_ptr(), rp} & {sp, yp}):
+            self._s = x, ld_x, residual, ld_r
+        else:
+            self._s = s, ld_s, None, 0
+        D.M, D.ld_x, D.ld_res, D.ld_sum, D.ld_y = M, ld_x, ld_r, ld_s, ld_y
+        st = self._fwd(x.data_ptr(), rp, self._w_ptr, self._b_ptr, self._dims_ref, sp, yp, stats, _stream(stream, self._index))
+        if st:
+            N.check(st, "moe_norm_fwd")
+        return y if residual is None else (y, s)
+
+    def backward(self, dy, d_sum=None, need=("dx", "dw", "db"), out=None, stream=None):
+        if self._s is None:
+            raise ValueError("backward: the last forward did not save (save=True)")
+        (x, ld_x, res, ld_r), D, n = self._s, self.dims, self.N
+        M = x.shape[0]
+        self._present()
+        ld_y, ld_d = _matrix(dy, "dy", self.dtype, M, n, self.device), 0
+        dx = dw = db = dxp = dwp = dbp = None
+        ld_dx = n
+        if "dx" in need:
+            dx, dxp, ld_dx = self._result("dx", out, M, stream)
+            _in_place("dy", dy, ld_y, dx, ld_dx, "dx")
+            _in_place("x", x, ld_x, dx, ld_dx, "dx")
+            if res is not None:
+                _in_place("residual", res, ld_r, dx, ld_dx, "dx")
+        if d_sum is not None:
+            ld_d = _matrix(d_sum, "d_sum", self.dtype, M, n, self.device)
+            if dx is not None:
+                _in_place("d_sum", d_sum, ld_d, dx, ld_dx, "dx")
+        if "dw" in need:
+            dw, dwp = self._view("dw", 1, stream)
+        if "db" in need and self.bias is not None:
+            db, dbp = self._view("db", 1, stream)
+        if self.ws is None:
+            most = N.NormDims.from_buffer_copy(D)
+            most.M = self.max_rows
+            self.ws = OpWorkspace(N.lib().moe_norm_workspace_bytes(ctypes.byref(most)), "moe_norm_workspace_bytes", self.device,
+                                  stream)
+        D.M, D.ld_x, D.ld_res, D.ld_sum, D.ld_y, D.ld_dx = M, ld_x, ld_r, ld_d, ld_y, ld_dx
+        st = self._bwd(x.data_ptr(), _p(res), dy.data_ptr(), _p(d_sum), self._w_ptr, self._view("stats", M, stream)[1], self._dims_ref,
+                       dxp, dwp, dbp, self.ws.ptr, self.ws.nbytes, _stream(stream, self._index))
+        if st:
+            N.check(st, "moe_norm_bwd")
+        return dict(dx=dx, dw=None if dw is None else dw[0], db=None if db is None else db[0])
+
+
+def _bytes_meet(a, ld_a, b):
+    """Whether the span of matrix a's rows and the dense tensor b share a byte."""
+    end = a.data_ptr() + ((a.shape[0] - 1) * ld_a + a.shape[1]) * a.element_size()
+    return a.data_ptr() < b.data_ptr() + b.numel() * b.element_size() and b.data_ptr() < end
+
+
+class TokenLogprobs:
+    """Log probabilities of given tokens under the softmax of rows of scores [M, V], with entropy and
+    the ``top`` most probable alternatives, and the gradient of the scores: moe_token_logprob /
+    moe_token_logprob_bwd for up to ``max_rows`` rows.
+
+    ``forward(scores, tokens=None, entropy=False, save=False)`` returns a dict of ``logprob`` [M] (with
+    tokens), ``entropy`` [M] (if asked for), ``top_idx`` and ``top_logprob`` [M, top] (if top > 0): own
+    buffers, written by the next call. A token outside [0, V) is padding (0). With ``save=True`` it keeps
+    scores and tokens (unchanged until then) for ``backward(d_logprob=None, d_entropy=None)``, which returns the
+    gradient of the scores [M, V]: an own buffer unless ``out`` is given, which may be the scores. One instance
+    serves one stream at a time, which waits for the one it was made on.
+    """
+
+    def __init__(self, max_rows, V, top=0, dtype=torch.float32, device="cuda", stream=None):
+        self.max_rows, self.V, self.top, self.dtype = max_rows, V, top, dtype
+        self.dims = N.LogprobDims(int(max_rows), V, top, _dt(dtype), 0, 0)
+        if not (0 <= max_rows <= 1 << 30 and 1 <= V <= 1 << 22 and 0 <= top <= 32):
+            raise N.MoeError(N.STATUS_CODE["MOE_ERR_BAD_DIMS"], "moe_token_logprob")
+        self.device, self._index = _device(device)
+        with _on(stream, self.device):
+            self._logprob, self._entropy, self._stats = (torch.empty(max_rows, w, dtype=torch.float32, device=device) for w in (1, 1, 2))
+            top_idx = torch.empty(max_rows, top, dtype=torch.int32, device=device)
+            top_logprob = torch.empty(max_rows, top, dtype=torch.float32, device=device)
+        self._top = top_idx, top_logprob
+        self._grad, self._views, self._saved = None, {}, None
+        self._dims_ref = ctypes.byref(self.dims)
+        self._fwd, self._bwd = N.lib().moe_token_logprob, N.lib().moe_token_logprob_bwd
+
+    def forward(self, scores, tokens=None, entropy=False, save=False, stream=None):
+        M, D, dev = scores.shape[0], self.dims, self.device
+        if M > self.max_rows:
+            raise ValueError(f"{M} rows, made for {self.max_rows}")
+        ld = _matrix(scores, "scores", self.dtype, M, self.V, dev)
+        if tokens is not None:
+            _dense(tokens, "tokens", torch.int32, (M,), dev)
+        v = self._views.get(M)
+        if v is None:
+            v = self._views[M] = (self._logprob[:M, 0], self._entropy[:M, 0], self._top[0][:M], self._top[1][:M])
+        out = {}
+        if tokens is not None:
+            out["logprob"] = v[0]
+        if entropy:
+            out["entropy"] = v[1]
+        if self.top:
+            out["top_idx"], out["top_logprob"] = v[2], v[3]
+        self._saved = (scores, ld, tokens, entropy) if save else None
+        D.M, D.ld = M, ld
+        st = self._fwd(scores.data_ptr(), _p(tokens), self._dims_ref, v[0].data_ptr() if tokens is not None else None,
+                       v[1].data_ptr() if entropy else None, self._stats.data_ptr() if save else None, v[2].data_ptr() if self.top else None,
+                       v[3].data_ptr() if self.top else None, _stream(stream, self._index))
+        if st:
+            N.check(st, "moe_token_logprob")
+        return out
+
+    def backward(self, d_logprob=None, d_entropy=None, out=None, stream=None):
+        if self._saved is None:
+            raise ValueError("backward: the last forward did not save (save=True)")
+        (scores, ld, tokens, entropy), D, dev = self._saved, self.dims, self.device
+        M = scores.shape[0]
+        if d_logprob is not None:
+            if tokens is None:
+                raise ValueError("d_logprob: the last forward had no tokens")
+            _dense(d_logprob, "d_logprob", torch.float32, (M,), dev)
+        if d_entropy is not None:
+            if not entropy:
+                raise ValueError("d_entropy: the last forward took no entropy")
+            _dense(d_entropy, "d_entropy", torch.float32, (M,), dev)
+        if out is None:
+            if self._grad is None:
+                with _on(stream, dev):
+                    self._grad = torch.empty(self.max_rows, self.V, dtype=self.dtype, device=dev)
+            out, ld_g = self._grad[:M], self.V
+        else:
+            ld_g = _matrix(out, "out", self.dtype, M, self.V, dev)
+            for name, t in (("tokens", tokens), ("d_logprob", d_logprob), ("d_entropy", d_entropy)):
+                if t is not None and M and _bytes_meet(out, ld_g, t):
+                    raise ValueError(f"out: overlaps {name}")
+        _in_place("scores", scores, ld, out, ld_g, "their gradient")
+        D.M, D.ld, D.ld_grad = M, ld, ld_g
+        st = self._bwd(scores.data_ptr(), _p(tokens), self._stats.data_ptr(), self._entropy.data_ptr(), _p(d_logprob), _p(d_entropy),
+                       self._dims_ref, out.data_ptr(), _stream(stream, self._index))
+        if st:
+            N.check(st, "moe_token_logprob_bwd")
+        return out
+
+
+class GradClipper:
+    """The global norm of a list of gradients, and their clipping: moe_clip_grads on a kept list
+    (contiguous fp32 or bf16 tensors; those of None are left out).
+
+    ``norm()`` returns the norm, ``clip(max_norm)`` also scales the gradients by min(1, max_norm / (norm +
+    1e-6)), in place, or into ``out`` (a list of the same shape and types). Both return a tensor of one number
+    without waiting for it, an own buffer that the next call writes; ``scale`` holds the factor of the
+    last call. A tensor that has moved (``t.data = ...``) is taken where it is then; a captured graph takes those of
+    the capture. One instance serves one stream at a time, which waits for the one it was made on.
+    """
+
+    def __init__(self, grads, out=None, device=None, stream=None):
+        grads = list(grads)
+        outs = grads if out is None else list(out)
+        if len(outs) != len(grads):
+            raise ValueError(f"out: {len(outs)} tensors for {len(grads)} gradients")
+        if any((g is None) != (o is None) for g, o in zip(grads, outs)):
+            raise ValueError("out: None where a gradient is not, or the other way round")
+        self.grads = [g for g in grads if g is not None]
+        self.out = self.grads if out is None else [o for o in outs if o is not None]
+        if device is None:
+            device = self.grads[0].device if self.grads else "cuda"
+        self.device, self._index = _device(device)
+        self._places = None
+        n = len(self.grads)
+        self.ws = OpWorkspace(N.lib().moe_clip_workspace_bytes(n), "moe_clip_workspace_bytes", self.device, stream)
+        with _on(stream, self.device):
+            self._result = torch.empty(2, dtype=torch.float32, device=self.device)
+        self._norm, self.scale = self._result[0], self._result[1]
+        self._np, self._sp = self._norm.data_ptr(), self.scale.data_ptr()
+        self._clip_table, self._norm_table = (N.Grad * max(n, 1))(), (N.Grad * max(n, 1))()
+        self._call = N.lib().moe_clip_grads
+        self._bind()
+
+    def _bind(self):
+        """Checks the tensors and takes their present places."""
+        self._places = None
+        for i, (g, o) in enumerate(zip(self.grads, self.out)):
+            for name, t in (("gradient", g), ("out", o)):
+                if not t.is_contiguous() or t.dtype not in (torch.float32, torch.bfloat16):
+                    raise ValueError(f"{name} {i}: expected a contiguous fp32 or bf16 tensor, got {list(t.shape)} of {t.dtype}, "
+                                     f"strides {t.stride()}")
+                if t.device != self.device:
+                    _elsewhere(f"{name} {i}", self.device, t)
+            if o.dtype != g.dtype or o.shape != g.shape:
+                raise ValueError(f"out {i}: expected {list(g.shape)} of {g.dtype}, got {list(o.shape)} of {o.dtype}")
+            self._clip_table[i] = N.Grad(g.data_ptr(), o.data_ptr(), g.numel(), _dt(g.dtype))
+            self._norm_table[i] = N.Grad(g.data_ptr(), None, g.numel(), _dt(g.dtype))
+        self._places = self._now()
+
+    def _now(self):
+        now = [(t.data_ptr(), t.numel()) for t in self.grads]
+        return now if self.out is self.grads else now + [(t.data_ptr(), t.numel()) for t in self.out]
+
+    def _run(self, table, max_norm, stream):
+        if self._places != self._now():
+            self._bind()
+        st = self._call(table, len(self.grads), max_norm, self._np, self._sp, self.ws.ptr, self.ws.nbytes,
+                        _stream(stream, self._index))
+        if st:
+            N.check(st, "moe_clip_grads")
+        return self._norm
+
+    def norm(self, stream=None):
+        return self._run(self._norm_table, float("inf"), stream)
+
+    def clip(self, max_norm, stream=None):
+        return self._run(self._clip_table, max_norm, stream)

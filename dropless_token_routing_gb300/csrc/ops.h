@@ -111,4 +111,62 @@ struct VerifyArgs {
 };
 cudaError_t launch_verify(const VerifyArgs& v, int num_sms, cudaStream_t st);
 
+// ------------------------------------------------------------------ layer norm
+constexpr int kNormMaxN = 32768;   // a row in the registers of 1024 threads
+constexpr int kNormParts = 512;    // most partial sums of a column
+struct NormArgs {
+  const void *x, *res, *w, *b;
+  void *sum, *y;
+  float* stats;      // [M][2]: mean, rstd
+  int64_t M, ld_x, ld_res, ld_sum, ld_y;
+  int N;
+  float eps, inv_n;
+};
+struct NormBwdArgs {
+  const void *x, *res, *dy, *d_sum, *w;
+  const float* stats;
+  void *dx, *dw, *db;
+  float* part;       // [parts][2][N] partial sums of the columns
+  int64_t M, ld_x, ld_res, ld_dy, ld_ds, ld_dx;
+  int N;
+  float inv_n;
+};
+cudaError_t launch_norm_fwd(const NormArgs& a, int dtype, int w_dtype, cudaStream_t st);
+cudaError_t launch_norm_bwd(const NormBwdArgs& a, int dtype, int w_dtype, cudaStream_t st);
+
+// ------------------------------------------------------------------ log probabilities
+constexpr int kMaxTop = 32;   // alternatives
+struct LogprobArgs {
+  const void* x;
+  const int32_t* tokens;
+  float *logprob, *stats, *entropy;   // stats [M][2]: maximum, ln sum e^(x - maximum)
+  int32_t* top_idx;
+  float* top_logprob;
+  int64_t M, ld;
+  int V, n_top;
+};
+struct LogprobBwdArgs {
+  const void* x;
+  const int32_t* tokens;
+  const float *stats, *entropy, *d_logprob, *d_entropy;
+  void* dx;
+  int64_t M, ld, ld_dx;
+  int V;
+};
+cudaError_t launch_logprob(const LogprobArgs& a, int dtype, int num_sms, cudaStream_t st);
+cudaError_t launch_logprob_bwd(const LogprobBwdArgs& a, int dtype, cudaStream_t st);
+
+// ------------------------------------------------------------------ clipping
+constexpr int kClipFew = 16, kClipMany = 512;   // tensors of a launch (its parameters: 34 bytes for each)
+constexpr int kClipParts = 1024;                // most partial sums of a launch
+constexpr int64_t kClipMaxTotal = 1ll << 44;    // elements of all tensors
+struct ClipArgs {
+  const moe_grad* grads;   // host
+  int64_t count;
+  float max_norm;
+  float *norm, *scale;     // device, or NULL
+  double* part;
+};
+cudaError_t launch_clip(const ClipArgs& a, int num_sms, cudaStream_t st);
+
 }  // namespace moe

@@ -1,4 +1,6 @@
-// C ABI of the few-token operators: argument validation, workspace layouts and launches.
+// C ABI of the operators beside the layer: argument validation, workspace layouts and launches.
+#include <math.h>
+#include <stdlib.h>
 #include <string.h>
 
 #include "ops.h"
@@ -53,6 +55,9 @@ bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) ==
 int opt(const void* p) { return p == nullptr || aligned16(p) ? MOE_OK : MOE_ERR_MISALIGNED; }
 int req(const void* p) { return p == nullptr ? MOE_ERR_NULL_POINTER : opt(p); }
 int req_if(const void* p, bool needed) { return needed ? req(p) : opt(p); }
+// one number for each row: a batch's slice may begin anywhere
+int opt_rows(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0 ? MOE_OK : MOE_ERR_MISALIGNED; }
+int req_rows_if(const void* p, bool needed) { return needed && p == nullptr ? MOE_ERR_NULL_POINTER : opt_rows(p); }
 
 #define OP_TRY(x)                \
   do {                           \
@@ -154,6 +159,75 @@ int layer_decode(const moe_layer_params* params, const void* x, const float* log
   a.absent = absent;
   a.dm = *dims;
   return dims->dtype == MOE_BF16 ? launch_decode_tc(a, sms, st) : launch_decode_simt(a, sms, st);
+}
+
+int resolve_norm(const moe_norm_dims* in, moe_norm_dims* d) {
+  if (in == nullptr) return MOE_ERR_NULL_POINTER;
+  *d = *in;
+  if ((d->dtype != MOE_F32 && d->dtype != MOE_BF16) || (d->w_dtype != MOE_F32 && d->w_dtype != MOE_BF16) ||
+      (d->dtype == MOE_F32 && d->w_dtype != MOE_F32))
+    return MOE_ERR_UNSUPPORTED_DTYPE;
+  if (d->M < 0 || d->M > (1 << 30) || d->N < 1 || d->N > kNormMaxN || !(d->eps >= 0.f) || isinf(d->eps)) return MOE_ERR_BAD_DIMS;
+  for (int64_t* ld : {&d->ld_x, &d->ld_res, &d->ld_sum, &d->ld_y, &d->ld_dx}) {
+    if (*ld == 0) *ld = d->N;
+    if (*ld < d->N || *ld > kMaxLd) return MOE_ERR_BAD_DIMS;
+  }
+  return MOE_OK;
+}
+
+size_t norm_ws_bytes(const moe_norm_dims& d) {
+  return kOpHeader + round256((size_t)kNormParts * 2 * d.N * 4);
+}
+
+int resolve_logprob(const moe_logprob_dims* in, moe_logprob_dims* d) {
+  if (in == nullptr) return MOE_ERR_NULL_POINTER;
+  *d = *in;
+  if (d->dtype != MOE_F32 && d->dtype != MOE_BF16) return MOE_ERR_UNSUPPORTED_DTYPE;
+  if (d->M < 0 || d->M > (1 << 30) || d->V < 1 || d->V > (1 << 22) || d->n_top < 0 || d->n_top > kMaxTop) return MOE_ERR_BAD_DIMS;
+  for (int64_t* ld : {&d->ld, &d->ld_grad}) {
+    if (*ld == 0) *ld = d->V;
+    if (*ld < d->V || *ld > kMaxLd) return MOE_ERR_BAD_DIMS;
+  }
+  return MOE_OK;
+}
+
+// Memory that a clipping call reads or writes.
+struct Extent {
+  uintptr_t from, to;
+  bool out;
+};
+int by_start(const void* a, const void* b) {
+  const Extent *x = static_cast<const Extent*>(a), *y = static_cast<const Extent*>(b);
+  return x->from < y->from ? -1 : x->from > y->from;
+}
+
+// Whether an out overlaps another out, or a g other than its own in the same place. (No C++
+// allocation: an exception may not leave a C entry.)
+int check_overlap(const moe_grad* grads, int64_t count) {
+  int64_t n = 0;
+  bool any = false;
+  for (int64_t i = 0; i < count; ++i) any |= grads[i].out != nullptr && grads[i].n > 0;
+  if (!any) return MOE_OK;
+  Extent few[64];
+  Extent* e = 2 * count <= 64 ? few : static_cast<Extent*>(malloc(2 * (size_t)count * sizeof(Extent)));
+  if (e == nullptr) return MOE_ERR_CUDA;
+  for (int64_t i = 0; i < count; ++i) {
+    const moe_grad& g = grads[i];
+    if (g.n == 0) continue;
+    const uintptr_t bytes = (uintptr_t)g.n * elt_bytes(g.dtype), from = reinterpret_cast<uintptr_t>(g.g);
+    if (g.out != nullptr) e[n++] = {reinterpret_cast<uintptr_t>(g.out), reinterpret_cast<uintptr_t>(g.out) + bytes, true};
+    if (g.out != g.g) e[n++] = {from, from + bytes, false};
+  }
+  qsort(e, (size_t)n, sizeof(Extent), by_start);
+  int st = MOE_OK;
+  uintptr_t read = 0, written = 0;   // ends of what begins no later
+  for (int64_t i = 0; i < n && st == MOE_OK; ++i) {
+    if (e[i].from < written || (e[i].out && e[i].from < read)) st = MOE_ERR_OVERLAP;
+    uintptr_t& end = e[i].out ? written : read;
+    if (e[i].to > end) end = e[i].to;
+  }
+  if (e != few) free(e);
+  return st;
 }
 
 }  // namespace
@@ -287,6 +361,129 @@ int moe_verify_draft(const int32_t* draft_tokens, const int32_t* draft_len, cons
                   dims->B, dims->ld_draft != 0 ? dims->ld_draft : dims->V,
                   dims->ld_target != 0 ? dims->ld_target : dims->V, dims->n, dims->V, dims->dtype};
   return launch_verify(v, sms, (cudaStream_t)stream) == cudaSuccess ? MOE_OK : MOE_ERR_LAUNCH;
+}
+
+int moe_norm_fwd(const void* x, const void* residual, const void* weight, const void* bias, const moe_norm_dims* dims,
+                 void* sum, void* y, float* stats, moe_stream_t stream) {
+  moe_norm_dims d;
+  OP_TRY(resolve_norm(dims, &d));
+  const bool some = d.M > 0;
+  OP_TRY(req_if(x, some));
+  OP_TRY(opt(residual));
+  OP_TRY(req(weight));
+  OP_TRY(opt(bias));
+  OP_TRY(opt(sum));
+  OP_TRY(req_if(y, some));
+  OP_TRY(opt(stats));
+  if (!some) return MOE_OK;
+  int sms = 0;
+  OP_TRY(check_device(&sms));
+  const NormArgs a = {x, residual, weight, bias, residual != nullptr ? sum : nullptr, y, stats, d.M, d.ld_x, d.ld_res, d.ld_sum,
+                      d.ld_y, d.N, d.eps, 1.f / (float)d.N};
+  return launch_norm_fwd(a, d.dtype, d.w_dtype, (cudaStream_t)stream) == cudaSuccess ? MOE_OK : MOE_ERR_LAUNCH;
+}
+
+size_t moe_norm_workspace_bytes(const moe_norm_dims* dims) {
+  moe_norm_dims d;
+  return resolve_norm(dims, &d) == MOE_OK ? norm_ws_bytes(d) : 0;
+}
+
+int moe_norm_bwd(const void* x, const void* residual, const void* dy, const void* d_sum, const void* weight,
+                 const float* stats, const moe_norm_dims* dims, void* dx, void* dw, void* db, void* ws, size_t ws_bytes, moe_stream_t stream) {
+  moe_norm_dims d;
+  OP_TRY(resolve_norm(dims, &d));
+  OP_TRY(check_op_ws(ws, ws_bytes, norm_ws_bytes(d)));
+  const bool some = d.M > 0;
+  OP_TRY(req_if(x, some));
+  OP_TRY(opt(residual));
+  OP_TRY(req_if(dy, some));
+  OP_TRY(opt(d_sum));
+  OP_TRY(req_if(weight, dx != nullptr));
+  OP_TRY(req_if(stats, some));
+  OP_TRY(opt(dx));
+  OP_TRY(opt(dw));
+  OP_TRY(opt(db));
+  const cudaStream_t st = (cudaStream_t)stream;
+  if (!some) {
+    const size_t bytes = d.N * elt_bytes(d.w_dtype);
+    if (dw != nullptr && cudaMemsetAsync(dw, 0, bytes, st) != cudaSuccess) return MOE_ERR_CUDA;
+    if (db != nullptr && cudaMemsetAsync(db, 0, bytes, st) != cudaSuccess) return MOE_ERR_CUDA;
+    return MOE_OK;
+  }
+  int sms = 0;
+  OP_TRY(check_device(&sms));
+  const NormBwdArgs a = {x, residual, dy, d_sum, weight, stats, dx, dw, db,
+                         reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kOpHeader), d.M, d.ld_x, d.ld_res, d.ld_y, d.ld_sum,
+                         d.ld_dx, d.N, 1.f / (float)d.N};
+  return launch_norm_bwd(a, d.dtype, d.w_dtype, st) == cudaSuccess ? MOE_OK : MOE_ERR_LAUNCH;
+}
+
+int moe_token_logprob(const void* scores, const int32_t* tokens, const moe_logprob_dims* dims, float* logprob, float* entropy,
+                      float* stats, int32_t* top_idx, float* top_logprob, moe_stream_t stream) {
+  moe_logprob_dims d;
+  OP_TRY(resolve_logprob(dims, &d));
+  const bool some = d.M > 0;
+  OP_TRY(req_if(scores, some));
+  OP_TRY(req_rows_if(tokens, some && logprob != nullptr));
+  OP_TRY(opt_rows(logprob));
+  OP_TRY(opt_rows(entropy));
+  OP_TRY(opt(stats));
+  OP_TRY(req_if(top_idx, some && d.n_top > 0));
+  OP_TRY(req_if(top_logprob, some && d.n_top > 0));
+  if (!some) return MOE_OK;
+  int sms = 0;
+  OP_TRY(check_device(&sms));
+  const LogprobArgs a = {scores, tokens, logprob, stats, entropy, top_idx, top_logprob, d.M, d.ld, d.V, d.n_top};
+  return launch_logprob(a, d.dtype, sms, (cudaStream_t)stream) == cudaSuccess ? MOE_OK : MOE_ERR_LAUNCH;
+}
+
+int moe_token_logprob_bwd(const void* scores, const int32_t* tokens, const float* stats, const float* entropy,
+                          const float* d_logprob, const float* d_entropy, const moe_logprob_dims* dims, void* d_scores,
+                          moe_stream_t stream) {
+  moe_logprob_dims d;
+  OP_TRY(resolve_logprob(dims, &d));
+  const bool some = d.M > 0;
+  OP_TRY(req_if(scores, some));
+  OP_TRY(req_rows_if(tokens, some && d_logprob != nullptr));
+  OP_TRY(req_if(stats, some));
+  OP_TRY(req_rows_if(entropy, some && d_entropy != nullptr));
+  OP_TRY(opt_rows(d_logprob));
+  OP_TRY(opt_rows(d_entropy));
+  OP_TRY(req_if(d_scores, some));
+  if (!some) return MOE_OK;
+  int sms = 0;
+  OP_TRY(check_device(&sms));
+  const LogprobBwdArgs a = {scores, tokens, stats, entropy, d_logprob, d_entropy, d_scores, d.M, d.ld, d.ld_grad, d.V};
+  return launch_logprob_bwd(a, d.dtype, (cudaStream_t)stream) == cudaSuccess ? MOE_OK : MOE_ERR_LAUNCH;
+}
+
+size_t moe_clip_workspace_bytes(int64_t count) {
+  if (count < 0 || count > (1 << 24)) return 0;
+  return kOpHeader + 8 * (size_t)kClipParts * (size_t)(count / kClipMany + 1);
+}
+
+int moe_clip_grads(const moe_grad* grads, int64_t count, float max_norm, float* norm, float* scale, void* ws, size_t ws_bytes,
+                   moe_stream_t stream) {
+  const size_t need = moe_clip_workspace_bytes(count);
+  if (need == 0 || !(max_norm >= 0.f)) return MOE_ERR_BAD_DIMS;
+  if (grads == nullptr && count > 0) return MOE_ERR_NULL_POINTER;
+  OP_TRY(check_op_ws(ws, ws_bytes, need));
+  OP_TRY(opt_rows(norm));
+  OP_TRY(opt_rows(scale));
+  int64_t total = 0;
+  for (int64_t i = 0; i < count; ++i) {
+    const moe_grad& g = grads[i];
+    if (g.dtype != MOE_F32 && g.dtype != MOE_BF16) return MOE_ERR_UNSUPPORTED_DTYPE;
+    if (g.n < 0 || g.n > kClipMaxTotal - total) return MOE_ERR_BAD_DIMS;
+    total += g.n;
+    if (g.n > 0 && g.g == nullptr) return MOE_ERR_NULL_POINTER;
+    if (((reinterpret_cast<uintptr_t>(g.g) | reinterpret_cast<uintptr_t>(g.out)) & (elt_bytes(g.dtype) - 1)) != 0) return MOE_ERR_MISALIGNED;
+  }
+  OP_TRY(check_overlap(grads, count));
+  int sms = 0;
+  OP_TRY(check_device(&sms));
+  const ClipArgs a = {grads, count, max_norm, norm, scale, reinterpret_cast<double*>(static_cast<uint8_t*>(ws) + kOpHeader)};
+  return launch_clip(a, sms, (cudaStream_t)stream) == cudaSuccess ? MOE_OK : MOE_ERR_LAUNCH;
 }
 
 }  // extern "C"

@@ -14,7 +14,8 @@ const char* kPhaseNames[TP_COUNT] = {
     "gemm_fwd1",   "gemm_fwd2",   "combine",      "permute_rows", "gemm_bwd2t",
     "route_bwd",   "gemm_bwd1t",  "transpose",    "combine_bwd",  "gemm_dw2",
     "gemm_dw13",   "dwr",         "misc",         "decode",       "linear",
-    "linear_dz",   "verify"};
+    "linear_dz",   "verify",      "norm",         "norm_bwd",     "logprob",
+    "logprob_bwd", "clip"};
 
 struct Rec {
   int phase;

@@ -29,6 +29,11 @@ enum TracePhase : int {
   TP_LINEAR,
   TP_LINEAR_DZ,
   TP_VERIFY,
+  TP_NORM,
+  TP_NORM_BWD,
+  TP_LOGPROB,
+  TP_LOGPROB_BWD,
+  TP_CLIP,
   TP_COUNT
 };
 

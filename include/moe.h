@@ -63,7 +63,8 @@ enum moe_status {
   MOE_ERR_WORKSPACE_TOO_SMALL = -6, /* ws_bytes < moe_workspace_bytes(dims) */
   MOE_ERR_LAUNCH = -7,              /* a kernel launch failed */
   MOE_ERR_CUDA = -8,                /* another CUDA runtime/driver call failed */
-  MOE_ERR_UNSUPPORTED_DEVICE = -9,  /* bf16 grouped GEMM and the few-token operators: sm_103 (GB300) only */
+  MOE_ERR_UNSUPPORTED_DEVICE = -9,  /* bf16 grouped GEMM and the operators beside the layer: sm_103 (GB300) only */
+  MOE_ERR_OVERLAP = -10,            /* an output overlaps what is read while it is written, or another output */
   MOE_ERR_DEVICE_EXPERT_ID = -100,  /* device: expert id outside [0, E) or repeated in a row */
   MOE_ERR_DEVICE_TIMEOUT = -101     /* device: a bounded wait ran out */
 };
@@ -442,6 +443,101 @@ int moe_verify_draft(const int32_t* draft_tokens, const int32_t* draft_len, cons
                      const void* target_probs, const float* u_accept, const float* u_sample,
                      const moe_verify_dims* dims, int32_t* tokens, int32_t* accepted,
                      moe_stream_t stream);
+
+/* ---------------------------------------------------------------- around the layer in training */
+/* The calls below stand around a trained layer: the norm in front of it, what its head's scores say
+ * of given tokens (the loss, and what a served answer reports) and the clipping of the gradients. The
+ * pages name them only in passing; the formulas are written out here. */
+
+typedef struct moe_norm_dims {
+  int64_t M;        /* rows (tokens), 0 <= M <= 2^30 */
+  int32_t N;        /* width, 1 .. 32768 */
+  int32_t dtype;    /* enum moe_dtype: x, residual, sum, y and their gradients */
+  int32_t w_dtype;  /* ... weight, bias and their gradients (MOE_F32 if dtype is) */
+  float eps;        /* >= 0, finite */
+  int64_t ld_x;     /* elements between rows of x (>= N, as all of these <= 2^36), 0 = N */
+  int64_t ld_res;   /* ... of residual */
+  int64_t ld_sum;   /* ... of sum and d_sum */
+  int64_t ld_y;     /* ... of y and dy */
+  int64_t ld_dx;    /* ... of dx */
+} moe_norm_dims;
+
+/* Layer norm of rows, behind the residual's sum:
+ *   s = x (+ r),  y = (s - mean) rstd w (+ b),  mean = sum s / N,  rstd = 1 / sqrt(sum (s - mean)^2 / N + eps)
+ * x, residual (or NULL) [M, N], weight, bias (or NULL) [N] -> y [M, N], sum [M, N] = s (or NULL; not
+ * written without a residual), stats [M][2] fp32 = mean, rstd (or NULL). Sums are fp32, of the
+ * unrounded s; sum and y are rounded once. y, or sum, may be the buffer of x or residual when their
+ * strides agree; they overlap nothing else, nor each other. Base pointers are 16-byte aligned, strides
+ * and widths may be odd. M == 0 is a no-op. */
+int moe_norm_fwd(const void* x, const void* residual, const void* weight, const void* bias,
+                 const moe_norm_dims* dims, void* sum, void* y, float* stats, moe_stream_t stream);
+
+/* Its gradients from dy [M, N], and from d_sum [M, N] (the gradient of s by its other way, or NULL):
+ *   s = x (+ r),  u = dy w,  xh = (s - mean) rstd
+ *   dx = rstd (u - mean(u) - xh mean(u xh)) (+ d_sum)   (also the residual's gradient)
+ *   dw = sum_m dy xh,  db = sum_m dy
+ * x and residual are the forward's, or x is its sum and residual NULL (one operand less to read; in
+ * bf16 the sum was rounded, which costs dw about what rounding it to bf16 does). stats as moe_norm_fwd
+ * wrote them.
+ * dx [M, N], dw [N], db [N]: each may be NULL (not computed); weight is needed for dx. Sums are fp32 in
+ * a fixed order. dx may be the buffer of dy, x, residual or d_sum when their strides agree; the results overlap
+ * nothing else. With M == 0 dw and db are zeroed. A workspace for M rows serves fewer. ws:
+ * moe_op_workspace_init's. */
+size_t moe_norm_workspace_bytes(const moe_norm_dims* dims);
+int moe_norm_bwd(const void* x, const void* residual, const void* dy, const void* d_sum, const void* weight,
+                 const float* stats, const moe_norm_dims* dims, void* dx, void* dw, void* db, void* ws, size_t ws_bytes,
+                 moe_stream_t stream);
+
+typedef struct moe_logprob_dims {
+  int64_t M;        /* rows, 0 <= M <= 2^30 */
+  int32_t V;        /* vocabulary, 1 <= V <= 2^22 */
+  int32_t n_top;    /* alternatives, 0 .. 32 */
+  int32_t dtype;    /* enum moe_dtype: the scores and their gradient */
+  int64_t ld;       /* elements between rows of scores (>= V, <= 2^36), 0 = V */
+  int64_t ld_grad;  /* ... of d_scores */
+} moe_logprob_dims;
+
+/* Log probabilities under p = softmax of each row of scores [M, V]:
+ *   logprob[m] = ln p_m,token[m]; 0 for a token outside [0, V) (padding)
+ *   entropy[m] = - sum_j p_j ln p_j
+ *   top_idx, top_logprob [M][n_top]: the n_top most probable tokens, descending, equal scores by the
+ *     lower index, and their ln p; -1 and -inf where there are no more
+ *   stats [M][2]: the largest score and ln sum_j e^(x_j - largest), for the backward
+ * logprob, entropy and stats may each be NULL (not returned); tokens [M] int32 is read for logprob alone.
+ * What has one number for a row need only be aligned to it (a slice of a batch).
+ * A score of -inf is no token (p = 0, no alternative); in a row of nothing else every ln p is -inf and
+ * the entropy 0. NaN or +inf among the scores makes the row's results NaN (top_idx leaves out NaN). Sums are fp32 in
+ * a fixed order. M == 0 is a no-op. */
+int moe_token_logprob(const void* scores, const int32_t* tokens, const moe_logprob_dims* dims, float* logprob,
+                      float* entropy, float* stats, int32_t* top_idx, float* top_logprob, moe_stream_t stream);
+
+/* Gradient of sum_m (d_logprob[m] logprob[m] + d_entropy[m] entropy[m]) by the scores, written fully:
+ *   d_scores[m, j] = d_logprob[m] ([j = token[m]] - p_j) - d_entropy[m] p_j (ln p_j + entropy[m])
+ * A token outside [0, V) has no first term; a row of -inf, and one whose two gradients are 0, gets
+ * zeros (also where its scores are NaN). d_logprob or d_entropy may be NULL (zero; tokens, or entropy, is not read then). entropy
+ * and stats as moe_token_logprob wrote them. d_scores may be the buffer of scores when the strides
+ * agree; it overlaps nothing else. dims->n_top is not read. */
+int moe_token_logprob_bwd(const void* scores, const int32_t* tokens, const float* stats, const float* entropy,
+                          const float* d_logprob, const float* d_entropy, const moe_logprob_dims* dims,
+                          void* d_scores, moe_stream_t stream);
+
+typedef struct moe_grad {
+  const void* g;    /* device, n elements, aligned to the element */
+  void* out;        /* where they go when clipped: g itself, another tensor, or NULL (counted in the norm only) */
+  int64_t n;        /* >= 0 */
+  int32_t dtype;    /* enum moe_dtype of both */
+} moe_grad;
+
+/* The norm of many tensors together, and their clipping:
+ *   norm = sqrt(sum over all tensors of sum g^2),  scale = min(1, max_norm / (norm + 1e-6)),  out = g scale
+ * grads: HOST array of count entries (0 allowed: norm 0), read before the call returns. max_norm >= 0,
+ * or infinity (scale 1). norm, scale: device floats, or NULL. No outs: the norm alone. Sums of squares
+ * leave fp32's range neither way; a norm that is not finite gives the scale of the formula (0, or NaN). An out
+ * overlaps no other out and no other g, and its own g only as the whole of it (MOE_ERR_OVERLAP). All n
+ * together stay below 2^44. A workspace for count tensors serves fewer. ws: moe_op_workspace_init's. */
+size_t moe_clip_workspace_bytes(int64_t count);
+int moe_clip_grads(const moe_grad* grads, int64_t count, float max_norm, float* norm, float* scale, void* ws,
+                   size_t ws_bytes, moe_stream_t stream);
 
 /* ---------------------------------------------------------------- tracing */
 /* Per-phase launch timing: while enabled, every kernel launch of the library is bracketed by

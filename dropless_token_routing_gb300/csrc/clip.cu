@@ -3,10 +3,11 @@
 //   norm = sqrt(sum over all tensors of sum x^2),  scale = min(1, max_norm / (norm + 1e-6)),  out = x scale
 //
 // Two passes over the gradients (the scale is known after the first), both bound by HBM. The tensors
-// are cut into chunks of 16384 elements, which the blocks take in turn, whatever the tensors' sizes.
-// A thread adds the squares of 64 elements in fp32 and those sums in fp64; the blocks' sums are
+// are cut into chunks of 32 KB, which the blocks take in turn, whatever the tensors' sizes; the
+// second pass takes them from the last one back, so that it finds in L2 what the first one read last.
+// A thread adds the squares of its 128 bytes in fp32 and those sums in fp64; the blocks' sums are
 // written out and added in order, so a result does not depend on timing. Squares that leave fp32's
-// range (elements beyond 2^63, or a chunk below 2^-30) are taken in fp64 again.
+// range (elements beyond 2^63, or all of a thread's below 2^-33) are taken in fp64 again.
 #include <math.h>
 
 #include "common.cuh"
@@ -17,7 +18,9 @@
 namespace moe {
 namespace {
 
-constexpr int CT = 256, CE = CT * 64;   // threads of a block, elements of a chunk
+constexpr int CT = 256, CU = 8, CB = CT * CU * 16;   // threads of a block, 16-byte vectors of a thread, bytes of a chunk
+constexpr int kClipBlocks = 3;   // of an SM
+template <typename T> constexpr int kVec = 16 / sizeof(T);   // elements of a vector
 
 template <int CAP> struct ClipTable {
   const void* g[CAP];
@@ -44,46 +47,74 @@ template <typename T> __device__ __forceinline__ int head_of(const T* p, int64_t
   return h < n ? h : (int)n;
 }
 
-__device__ __forceinline__ double square(double x) { return x * x; }
+__device__ __forceinline__ void vec_floats(const uint4& v, float (&f)[4], float) {
+  f[0] = __uint_as_float(v.x);
+  f[1] = __uint_as_float(v.y);
+  f[2] = __uint_as_float(v.z);
+  f[3] = __uint_as_float(v.w);
+}
+__device__ __forceinline__ void vec_floats(const uint4& v, float (&f)[8], __nv_bfloat16) {
+  Vec8<__nv_bfloat16> b;
+  b.v = v;
+  b.to_float(f);
+}
+__device__ __forceinline__ uint4 floats_vec(const float (&f)[4], float) {
+  return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+}
+__device__ __forceinline__ uint4 floats_vec(const float (&f)[8], __nv_bfloat16) {
+  Vec8<__nv_bfloat16> b;
+  b.from_float(f);
+  return b.v;
+}
+
+// This thread's vectors of a chunk: vector u begins at element `at` + u * CT * kVec (zeros past n).
+template <typename T> __device__ __forceinline__ void load_chunk(uint4 (&v)[CU], const T* p, int64_t at, int64_t n) {
+  constexpr int W = kVec<T>;
+  if (at + (CU - 1) * CT * W + W <= n) {
+#pragma unroll
+    for (int u = 0; u < CU; ++u) v[u] = *reinterpret_cast<const uint4*>(p + at + u * CT * W);
+  } else {
+#pragma unroll
+    for (int u = 0; u < CU; ++u) {
+      const int64_t j = at + u * CT * W;
+      T* e = reinterpret_cast<T*>(&v[u]);
+#pragma unroll
+      for (int i = 0; i < W; ++i) e[i] = j + i < n ? p[j + i] : T(0.f);
+    }
+  }
+}
 
 // The squares of a chunk's elements, this thread's share.
 template <typename T> __device__ __forceinline__ double chunk_squares(const T* p, int64_t n, int64_t chunk) {
-  constexpr int U = 8;
+  constexpr int W = kVec<T>;
   const int h = head_of(p, n);
-  const int64_t at = h + chunk * CE;
-  Vec8<T> v[U];
-  float s = 0.f;
+  uint4 v[CU];
+  load_chunk(v, p, h + chunk * (CB / sizeof(T)) + threadIdx.x * W, n);
+  float s[2] = {0.f, 0.f};
 #pragma unroll
-  for (int u = 0; u < U; ++u) {
-    const int64_t j = at + (u * CT + threadIdx.x) * 8;
-    if (j + 8 <= n) {
-      v[u].load_plain(p + j);
-    } else {
-      T* e = reinterpret_cast<T*>(&v[u]);
+  for (int u = 0; u < CU; ++u) {
+    float f[W];
+    vec_floats(v[u], f, T());
 #pragma unroll
-      for (int i = 0; i < 8; ++i) e[i] = j + i < n ? p[j + i] : T(0.f);
-    }
+    for (int i = 0; i < W; ++i) s[i & 1] = fmaf(f[i], f[i], s[i & 1]);
   }
-#pragma unroll
-  for (int u = 0; u < U; ++u) {
-    float f[8];
-    v[u].to_float(f);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) s = fmaf(f[i], f[i], s);
-  }
-  double d = s;
-  if (!(s >= 0x1p-60f && s <= 0x1p126f)) {   // (s = 0 mostly because all of them are)
+  const float t = s[0] + s[1];
+  double d = t;
+  if (!(t >= 0x1p-60f && t <= 0x1p126f)) {   // (t = 0 mostly because all of them are)
     d = 0.0;
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      float f[8];
-      v[u].to_float(f);
+    for (int u = 0; u < CU; ++u) {
+      float f[W];
+      vec_floats(v[u], f, T());
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (f[i] != 0.f) d += square((double)f[i]);
+      for (int i = 0; i < W; ++i)
+        if (f[i] != 0.f) d = fma((double)f[i], (double)f[i], d);
     }
   }
-  if (chunk == 0 && threadIdx.x < h) d += square((double)to_f32(p[threadIdx.x]));
+  if (chunk == 0 && threadIdx.x < h) {
+    const double x = to_f32(p[threadIdx.x]);
+    d = fma(x, x, d);
+  }
   return d;
 }
 
@@ -99,7 +130,7 @@ __device__ __forceinline__ double block_sum(double d, double* s) {
   return d;
 }
 
-template <int CAP> __global__ void __launch_bounds__(CT) clip_squares_kernel(const __grid_constant__ ClipTable<CAP> t, double* part) {
+template <int CAP> __global__ void __launch_bounds__(CT, kClipBlocks) clip_squares_kernel(const __grid_constant__ ClipTable<CAP> t, double* part) {
   __shared__ double s[CT / 32];
   pdl_start();
   pdl_wait();
@@ -116,35 +147,24 @@ template <int CAP> __global__ void __launch_bounds__(CT) clip_squares_kernel(con
 }
 
 template <typename T> __device__ __forceinline__ void scale_chunk(const T* p, T* out, int64_t n, int64_t chunk, float scale) {
-  constexpr int U = 8;
+  constexpr int W = kVec<T>;
   const int h = head_of(p, n);
-  const int64_t at = h + chunk * CE;
+  const int64_t at = h + chunk * (CB / sizeof(T)) + threadIdx.x * W;
   const bool vec = ((reinterpret_cast<uintptr_t>(p) ^ reinterpret_cast<uintptr_t>(out)) & 15) == 0;
-  Vec8<T> v[U];
+  uint4 v[CU];
+  load_chunk(v, p, at, n);
 #pragma unroll
-  for (int u = 0; u < U; ++u) {
-    const int64_t j = at + (u * CT + threadIdx.x) * 8;
-    if (j + 8 <= n) {
-      v[u].load_plain(p + j);
-    } else {
-      T* e = reinterpret_cast<T*>(&v[u]);
+  for (int u = 0; u < CU; ++u) {
+    const int64_t j = at + u * CT * W;
+    float f[W];
+    vec_floats(v[u], f, T());
 #pragma unroll
-      for (int i = 0; i < 8; ++i) e[i] = j + i < n ? p[j + i] : T(0.f);
-    }
-  }
-#pragma unroll
-  for (int u = 0; u < U; ++u) {
-    const int64_t j = at + (u * CT + threadIdx.x) * 8;
-    float f[8];
-    v[u].to_float(f);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] *= scale;
-    if (vec && j + 8 <= n) {
-      v[u].from_float(f);
-      v[u].store(out + j);
+    for (int i = 0; i < W; ++i) f[i] *= scale;
+    if (vec && j + W <= n) {
+      *reinterpret_cast<uint4*>(out + j) = floats_vec(f, T());
     } else {
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
+      for (int i = 0; i < W; ++i)
         if (j + i < n) out[j + i] = from_f32<T>(f[i]);
     }
   }
@@ -153,7 +173,7 @@ template <typename T> __device__ __forceinline__ void scale_chunk(const T* p, T*
 
 // part: the blocks' sums of every launch of the first pass; block 0 writes norm and scale.
 template <int CAP>
-__global__ void __launch_bounds__(CT) clip_scale_kernel(const __grid_constant__ ClipTable<CAP> t, const double* part, int n_part, float max_norm,
+__global__ void __launch_bounds__(CT, kClipBlocks) clip_scale_kernel(const __grid_constant__ ClipTable<CAP> t, const double* part, int n_part, float max_norm,
                                                        float* norm, float* scale_out) {
   __shared__ double s[CT / 32];
   pdl_start();
@@ -168,7 +188,8 @@ __global__ void __launch_bounds__(CT) clip_scale_kernel(const __grid_constant__ 
     if (scale_out != nullptr) *scale_out = scale;
   }
   const uint32_t chunks = t.first[t.count];
-  for (uint32_t c = blockIdx.x; c < chunks; c += gridDim.x) {
+  for (uint32_t k = blockIdx.x; k < chunks; k += gridDim.x) {
+    const uint32_t c = chunks - 1 - k;
     const int i = tensor_of(t, c);
     if (t.out[i] == nullptr || (scale == 1.f && t.out[i] == t.g[i])) continue;
     const int64_t local = c - t.first[i];
@@ -189,7 +210,8 @@ template <int CAP> int64_t fill(ClipTable<CAP>& t, const moe_grad* grads, int64_
     t.out[k] = g.out;
     t.n[k] = g.n;
     t.f32[k] = g.dtype == MOE_F32;
-    t.first[k + 1] = t.first[k] + (uint32_t)((g.n + CE - 1) / CE);   // (below 2^31: kClipMaxTotal)
+    const int64_t e = CB / (int64_t)elt_bytes(g.dtype);
+    t.first[k + 1] = t.first[k] + (uint32_t)((g.n + e - 1) / e);   // (below 2^32: kClipMaxTotal)
   }
   return at;
 }
@@ -198,7 +220,7 @@ template <int CAP>
 cudaError_t clip(const ClipArgs& a, int num_sms, cudaStream_t st) {
   ClipTable<CAP> t;
   int n_part = 0;
-  const uint32_t most = (uint32_t)(num_sms * 4 < kClipParts ? num_sms * 4 : kClipParts);
+  const uint32_t most = (uint32_t)(num_sms * kClipBlocks < kClipParts ? num_sms * kClipBlocks : kClipParts);   // all at once
   bool write = false;
   for (int64_t at = 0; at < a.count;) {
     at = fill(t, a.grads, at, a.count);

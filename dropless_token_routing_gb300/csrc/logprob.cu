@@ -9,15 +9,19 @@
 // move to the new maximum when these hold one. Differences x - m are formed before the exponential,
 // so scores of any size (a mask of the type's lowest value among them) keep their meaning: -inf is no
 // token, a row of nothing else has no distribution (S = 0).
+#include "cluster.cuh"
 #include "common.cuh"
 #include "launch.cuh"
 #include "ops.h"
+#include "packed.cuh"
 #include "trace.h"
 
 namespace moe {
 namespace {
 
-constexpr int LT = 512, LW = LT / 32;   // threads and warps of a block
+constexpr int LT = 256, LW = LT / 32;   // threads and warps of a block
+constexpr int LU = 4, LC = LU * LT * 8;   // vectors of 8 scores that a thread takes at a time, and a block's scores then
+constexpr int kMaxCluster = 8;
 constexpr float kLog2e = 1.44269504088896340736f, kLowest = -3.402823466e38f, kInf = __builtin_huge_valf();
 
 // 2^x with an error of 2^-22 (numbers below 2^-126 count as 0)
@@ -44,12 +48,16 @@ struct Sums {
     S *= e;
     m = max;
   }
-  __device__ __forceinline__ void join(Sums o) {
-    const float max = fmaxf(m, o.m);
+  __device__ __forceinline__ void warp_join() {   // the warp's, in every lane
+    float max = m;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) max = fmaxf(max, __shfl_xor_sync(0xffffffffu, max, o));
     to(max);
-    o.to(max);
-    S += o.S;
-    D += o.D;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      S += __shfl_xor_sync(0xffffffffu, S, o);
+      D += __shfl_xor_sync(0xffffffffu, D, o);
+    }
   }
 };
 
@@ -63,129 +71,268 @@ __device__ __forceinline__ uint32_t index_of(unsigned long long key) { return 0x
 
 __device__ __forceinline__ unsigned long long max64(unsigned long long a, unsigned long long b) { return a > b ? a : b; }
 
+// 8 scores of a row from j on; those from `stop` on are not there.
 template <typename T, bool VEC>
-__device__ __forceinline__ void load_scores(float (&f)[8], const T* row, int j, int V, const T* end) {
-  const int n = V - j;
-  Vec8<T> v;
-  if (VEC && n >= 8) {
+__device__ __forceinline__ void load_scores(Vec8<T>& v, const T* row, int j, int stop, const T* end) {
+  if (VEC && j + 8 <= stop) {
     v.load_plain(row + j);
   } else if (!VEC) {
-    load8_unaligned(v, row + j, end, n);
+    load8_unaligned(v, row + j, end, stop - j);
   } else {
     T* e = reinterpret_cast<T*>(&v);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) e[i] = i < n ? row[j + i] : T(0.f);
-  }
-  v.to_float(f);
-  if (n < 8) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (i >= n) f[i] = -kInf;
+    for (int i = 0; i < 8; ++i) e[i] = j + i < stop ? row[j + i] : T(0.f);
   }
 }
-
-template <typename T, bool VEC, bool TOP>
-__global__ void __launch_bounds__(LT) logprob_kernel(const LogprobArgs a) {
-  __shared__ Sums s_sums[LW];
-  __shared__ unsigned long long s_key[2][LW];
-  constexpr int U = 4;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, V = a.V;
-  pdl_start();
-  pdl_wait();
-  const int64_t m = blockIdx.x;
-  const T* row = static_cast<const T*>(a.x) + m * a.ld;
-  const T* end = static_cast<const T*>(a.x) + (a.M - 1) * a.ld + V;
-  Sums s = {kLowest, 0.f, 0.f};
-  unsigned long long best = 0;
-  for (int j0 = threadIdx.x * 8; j0 < V; j0 += U * LT * 8) {
-    float f[U][8];
+// Adds a thread's LU vectors to its sums; ENT: D too.
+template <typename T, bool ENT> __device__ __forceinline__ void add_scores(Sums& s, const float (&f)[LU][8]) {
+  float max = s.m;
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int j = j0 + u * LT * 8;
-      if (j < V) {
-        load_scores<T, VEC>(f[u], row, j, V, end);
-      } else {
+  for (int u = 0; u < LU; ++u)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) f[u][i] = -kInf;
+    for (int i = 0; i < 8; ++i) max = fmaxf(max, f[u][i]);
+  if (max > s.m) s.to(max);
+  const uint64_t nm = both(-max), l2e = both(kLog2e);
+  uint64_t S[2] = {0, 0}, D[2] = {0, 0};   // two chains of additions
+#pragma unroll
+  for (int u = 0; u < LU; ++u)
+#pragma unroll
+    for (int i = 0; i < 8; i += 2) {
+      uint64_t d = add2(pack2(f[u][i], f[u][i + 1]), nm);
+      float a, b;
+      if (ENT) {
+        unpack2(d, a, b);
+        d = pack2(max_nan(a, -200.f), max_nan(b, -200.f));
       }
+      unpack2(mul2(d, l2e), a, b);
+      const uint64_t e = pack2(exp2_fast(a), exp2_fast(b));
+      S[u & 1] = add2(S[u & 1], e);
+      if (ENT) D[u & 1] = fma2(e, d, D[u & 1]);
     }
-    float max = s.m;
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-#pragma unroll
-      for (int i = 0; i < 8; ++i) max = fmaxf(max, f[u][i]);
-    s.to(max);
-#pragma unroll
-    for (int u = 0; u < U; ++u)
+  s.S += sum2(add2(S[0], S[1]));
+  if (ENT) s.D += sum2(add2(D[0], D[1]));
+}
+
+static_assert(kMaxCluster * kMaxTop == LT && LT / 4 == 64, "");
+struct TopShared {
+  unsigned long long key[LT];   // candidates, unordered
+  unsigned long long sorted[kMaxTop];              // this block's alternatives, descending
+  float group[64];                                 // maxima of 4 threads each
+  float bound;
+  int count;
+  unsigned long long warp[2][LW];
+};
+
+// The block's n highest keys among scores [j0, j1) of the row, descending, into t.sorted (0: no more).
+// `mine`: the highest score that this thread took (vectors threadIdx.x, + LT, ..). The n-th highest of
+// 64 groups' maxima is no higher than the n-th highest score, and few scores reach it (24 of 131072
+// in random order, n = 20): only the threads that hold one look at their scores again. Rows where
+// more than 256 reach it (in order, or of few values) are taken one key at a time.
+template <typename T> __device__ void block_top(TopShared& t, const T* row, int j0, int j1, float mine, int n) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  float g = mine;
+  g = fmaxf(g, __shfl_xor_sync(0xffffffffu, g, 1));
+  g = fmaxf(g, __shfl_xor_sync(0xffffffffu, g, 2));
+  if ((lane & 3) == 0) t.group[tid >> 2] = g;
+  if (tid == 0) t.count = 0;
+  if (tid < kMaxTop) t.sorted[tid] = 0;
+  __syncthreads();
+  if (tid < 64) {
+    g = t.group[tid];
+    int above = 0;
+#pragma unroll 16
+    for (int i = 0; i < 64; ++i) {
+      const float o = t.group[i];
+      above += o > g || (o == g && i < tid);
+    }
+    if (above == n - 1) t.bound = g;
+  }
+  __syncthreads();
+  const float bound = t.bound;
+  for (uint32_t who = __ballot_sync(0xffffffffu, mine >= bound); who != 0u; who &= who - 1) {
+    const int first = j0 + ((warp << 5) + __ffs((int)who) - 1) * 8;
+    for (int j = first + lane * LT * 8; j < j1; j += 32 * LT * 8)
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const float d = below(f[u][i], max), e = exp2_fast(d * kLog2e);
-        s.S += e;
-        s.D = fmaf(e, d, s.D);
-        if (TOP && f[u][i] > -kInf) best = max64(best, key_of(f[u][i], j0 + u * LT * 8 + i));
+        const float x = j + i < j1 ? to_f32(row[j + i]) : -kInf;
+        if (x >= bound && x > -kInf) {
+          const int at = atomicAdd(&t.count, 1);
+          if (at < LT) t.key[at] = key_of(x, j + i);
+        }
       }
   }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    Sums t;
-    t.m = __shfl_xor_sync(0xffffffffu, s.m, o);
-    t.S = __shfl_xor_sync(0xffffffffu, s.S, o);
-    t.D = __shfl_xor_sync(0xffffffffu, s.D, o);
-    s.join(t);
-  }
-  if (lane == 0) s_sums[warp] = s;
   __syncthreads();
-  s = s_sums[lane % LW];
-#pragma unroll
-  for (int o = LW / 2; o > 0; o >>= 1) {
-    Sums t;
-    t.m = __shfl_xor_sync(0xffffffffu, s.m, o);
-    t.S = __shfl_xor_sync(0xffffffffu, s.S, o);
-    t.D = __shfl_xor_sync(0xffffffffu, s.D, o);
-    s.join(t);
-  }
-  const float log_sum = s.S == 0.f ? -kInf : logf(s.S);   // a row without a distribution: -inf
-  if (threadIdx.x == 0) {
-    if (a.logprob != nullptr) {
-      const int t = a.tokens[m];
-      float lp = 0.f;
-      if (t >= 0 && t < V) lp = s.S == 0.f ? -kInf : (to_f32(row[t]) - s.m) - log_sum;
-      a.logprob[m] = lp;
+  const int count = t.count;
+  if (count <= LT) {
+    if (tid < count) {
+      const unsigned long long key = t.key[tid];
+      int above = 0;
+      for (int i = 0; i < count; ++i) above += t.key[i] > key;
+      if (above < n) t.sorted[above] = key;
     }
-    if (a.stats != nullptr) reinterpret_cast<float2*>(a.stats)[m] = make_float2(s.m, log_sum);
-    if (a.entropy != nullptr) a.entropy[m] = s.S == 0.f ? 0.f : log_sum - s.D / s.S;
+    __syncthreads();
+    return;
   }
-  if constexpr (TOP) {
-    // the block's largest key, n times; its owner then looks for its next one
-    for (int k = 0; k < a.n_top; ++k) {
-      unsigned long long top = best;
+  unsigned long long best = ~0ull, top = ~0ull;
+  for (int k = 0; k < n; ++k) {
+    if (best == top) {   // this thread's next key
+      best = 0;
+      for (int j = j0 + tid * 8; j < j1; j += LT * 8)
+        for (int i = 0; i < 8 && j + i < j1; ++i) {
+          const float x = to_f32(row[j + i]);
+          const unsigned long long key = key_of(x, j + i);
+          if (x > -kInf && key < top) best = max64(best, key);
+        }
+    }
+    top = best;
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) top = max64(top, __shfl_xor_sync(0xffffffffu, top, o));
-      if (lane == 0) s_key[k & 1][warp] = top;
+    for (int o = 16; o > 0; o >>= 1) top = max64(top, __shfl_xor_sync(0xffffffffu, top, o));
+    if (lane == 0) t.warp[k & 1][warp] = top;
+    __syncthreads();
+    top = t.warp[k & 1][lane % LW];
+#pragma unroll
+    for (int o = LW / 2; o > 0; o >>= 1) top = max64(top, __shfl_xor_sync(0xffffffffu, top, o));
+    if (top == 0) break;
+    if (tid == 0) t.sorted[k] = top;
+  }
+  __syncthreads();
+}
+
+// Keys of a descending list of n that are higher than `key`.
+__device__ __forceinline__ int above_in(const unsigned long long* list, int n, unsigned long long key) {
+  int lo = 0, hi = n;
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (list[mid] > key) lo = mid + 1;
+    else hi = mid;
+  }
+  return lo;
+}
+
+// A row is a cluster's (one block for many rows): every block takes a slice, the first one joins their sums.
+template <typename T, bool VEC, bool ENT, bool TOP>
+__global__ void __launch_bounds__(LT, 3) logprob_kernel(const LogprobArgs a) {
+  __shared__ Sums s_sums[LW];
+  __shared__ TopShared s_top[1];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, V = a.V;
+  const uint32_t rank = ctarank(), ranks = nctarank();
+  pdl_start();
+  pdl_wait();
+  const int64_t m = blockIdx.x / ranks;
+  const T* row = static_cast<const T*>(a.x) + m * a.ld;
+  const T* end = static_cast<const T*>(a.x) + (a.M - 1) * a.ld + V;
+  const int slice = (int)(((V + ranks - 1) / ranks + 7) & ~7u);
+  const int j0 = min((int)rank * slice, V), j1 = min(j0 + slice, V);
+  int token = -1;
+  float given = 0.f;
+  if (rank == 0 && threadIdx.x == 0 && a.logprob != nullptr) {
+    token = a.tokens[m];
+    if (token >= V) token = -1;
+    if (token >= 0) given = to_f32(row[token]);
+  }
+
+  Sums s = {kLowest, 0.f, 0.f};
+  const int mine = j0 + threadIdx.x * 8, whole = (j1 - j0) / LC;   // steps that need no bounds
+  Vec8<T> v[LU];
+  if (whole > 0) {
+#pragma unroll
+    for (int u = 0; u < LU; ++u) load_scores<T, VEC>(v[u], row, mine + u * LT * 8, V, end);
+  }
+  for (int k = 0; k < whole; ++k) {
+    float f[LU][8];
+#pragma unroll
+    for (int u = 0; u < LU; ++u) v[u].to_float(f[u]);
+    if (k + 1 < whole) {   // the next step's scores are under way while these are added
+#pragma unroll
+      for (int u = 0; u < LU; ++u) load_scores<T, VEC>(v[u], row, mine + (k + 1) * LC + u * LT * 8, V, end);
+    }
+    add_scores<T, ENT>(s, f);
+  }
+  if (j0 + whole * LC < j1) {
+    float f[LU][8];
+#pragma unroll
+    for (int u = 0; u < LU; ++u) {
+      const int j = mine + whole * LC + u * LT * 8;
+      if (j < j1) load_scores<T, VEC>(v[u], row, j, j1, end);
+    }
+#pragma unroll
+    for (int u = 0; u < LU; ++u) {
+      const int j = mine + whole * LC + u * LT * 8;
+      v[u].to_float(f[u]);
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (j + i >= j1) f[u][i] = -kInf;
+    }
+    add_scores<T, ENT>(s, f);
+  }
+  const float highest = s.m;
+  s.warp_join();
+  if (lane == 0) s_sums[warp] = s;
+  if constexpr (TOP) block_top(s_top[0], row, j0, j1, highest, a.n_top);
+  if (ranks > 1) {
+    cluster_arrive();
+    cluster_wait();
+  } else {
+    __syncthreads();
+  }
+  if (rank == 0) {
+    // the sums of up to 64 warps, in every warp
+    const int n = (int)ranks * LW;
+    s = {kLowest, 0.f, 0.f};
+    for (int r = lane; r < n; r += 32) {
+      const uint32_t at = smem_u32(&s_sums[r % LW]);
+      Sums o;
+      o.m = peer_ldf(at, r / LW);
+      o.S = peer_ldf(at + 4, r / LW);
+      o.D = peer_ldf(at + 8, r / LW);
+      const float max = fmaxf(s.m, o.m);
+      s.to(max);
+      o.to(max);
+      s.S += o.S;
+      s.D += o.D;
+    }
+    s.warp_join();
+    const float log_sum = s.S == 0.f ? -kInf : logf(s.S);   // a row without a distribution: -inf
+    if (threadIdx.x == 0) {
+      if (a.logprob != nullptr) a.logprob[m] = token < 0 ? 0.f : s.S == 0.f ? -kInf : (given - s.m) - log_sum;
+      if (a.stats != nullptr) reinterpret_cast<float2*>(a.stats)[m] = make_float2(s.m, log_sum);
+      if (ENT) a.entropy[m] = s.S == 0.f ? 0.f : log_sum - s.D / s.S;
+    }
+    if constexpr (TOP) {
+      TopShared& t = s_top[0];
+      const int r = threadIdx.x / kMaxTop, i = threadIdx.x % kMaxTop;
+      unsigned long long key = 0;
+      if (r < (int)ranks) key = ranks > 1 ? (unsigned long long)peer_ld64(smem_u32(&t.sorted[i]), r) : t.sorted[i];
+      t.key[threadIdx.x] = key;   // the blocks' lists in a row
       __syncthreads();
-      top = s_key[k & 1][lane % LW];
-#pragma unroll
-      for (int o = LW / 2; o > 0; o >>= 1) top = max64(top, __shfl_xor_sync(0xffffffffu, top, o));
-      const int j = top == 0 ? -1 : (int)index_of(top);
-      if (threadIdx.x == 0) {
-        a.top_idx[m * a.n_top + k] = j;
-        a.top_logprob[m * a.n_top + k] = j < 0 ? -kInf : (to_f32(row[j]) - s.m) - log_sum;
+      if (key != 0) {
+        int at = i;
+        for (int o = 0; o < (int)ranks; ++o)
+          if (o != r) at += above_in(t.key + o * kMaxTop, a.n_top, key);
+        if (at < a.n_top) {
+          const uint32_t b = (uint32_t)(key >> 32);
+          const float x = __uint_as_float(b & 0x80000000u ? b & 0x7fffffffu : ~b);
+          a.top_idx[m * a.n_top + at] = (int)index_of(key);
+          a.top_logprob[m * a.n_top + at] = (x - s.m) - log_sum;
+        }
       }
-      if (top != 0 && best == top) {
-        best = 0;
-        for (int j0 = threadIdx.x * 8; j0 < V; j0 += LT * 8)
-          for (int i = 0; i < 8 && j0 + i < V; ++i) {
-            const float x = to_f32(row[j0 + i]);
-            const unsigned long long key = key_of(x, j0 + i);
-            if (x > -kInf && key < top) best = max64(best, key);
-          }
+      // places that no key took
+      const int found = __syncthreads_count(key != 0);
+      if ((int)threadIdx.x >= found && (int)threadIdx.x < a.n_top) {
+        a.top_idx[m * a.n_top + threadIdx.x] = -1;
+        a.top_logprob[m * a.n_top + threadIdx.x] = -kInf;
       }
     }
+  }
+  if (ranks > 1) {   // the first block has read its peers' sums
+    __syncwarp();
+    cluster_arrive();
+    cluster_wait();
   }
 }
 
 template <typename T, bool VEC>
-__global__ void __launch_bounds__(256) logprob_bwd_kernel(const LogprobBwdArgs a) {
+__global__ void __launch_bounds__(LT) logprob_bwd_kernel(const LogprobBwdArgs a) {
   const int V = a.V;
   pdl_start();
   pdl_wait();
@@ -199,55 +346,80 @@ __global__ void __launch_bounds__(256) logprob_bwd_kernel(const LogprobBwdArgs a
   const float g = token >= 0 && token < V ? a.d_logprob[m] : 0.f;
   const float h = a.d_entropy != nullptr && some ? a.d_entropy[m] : 0.f, H = h != 0.f ? a.entropy[m] : 0.f;
   const bool zero = g == 0.f && h == 0.f;
-  for (int j = (blockIdx.y * 256 + threadIdx.x) * 8; j < V; j += gridDim.y * 2048) {
-    float f[8];
-    if (zero) {
+  for (int j0 = (blockIdx.y * LU * LT + threadIdx.x) * 8; j0 < V; j0 += gridDim.y * LC) {
+    Vec8<T> v[LU];
+    if (!zero) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) f[i] = 0.f;
-    } else {
-      load_scores<T, VEC>(f, row, j, V, end);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float lp = below(f[i], st.x) - st.y, p = exp2_fast(lp * kLog2e);
-        const float d = g * ((j + i == token ? 1.f : 0.f) - p);
-        f[i] = h != 0.f ? d - h * (p * (lp + H)) : d;
-      }
+      for (int u = 0; u < LU; ++u)
+        if (j0 + u * LT * 8 < V) load_scores<T, VEC>(v[u], row, j0 + u * LT * 8, V, end);
     }
-    if (VEC && j + 8 <= V) {
-      Vec8<T> v;
-      v.from_float(f);
-      v.store(out + j);
-    } else {
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (j + i < V) out[j + i] = from_f32<T>(f[i]);
+    for (int u = 0; u < LU; ++u) {
+      const int j = j0 + u * LT * 8;
+      if (j >= V) break;
+      float f[8];
+      if (zero) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] = 0.f;
+      } else {
+        v[u].to_float(f);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float lp = below(f[i], st.x) - st.y, p = exp2_fast(lp * kLog2e);
+          const float d = g * ((j + i == token ? 1.f : 0.f) - p);
+          f[i] = h != 0.f ? d - h * (p * (lp + H)) : d;
+        }
+      }
+      if (VEC && j + 8 <= V) {
+        v[u].from_float(f);
+        v[u].store(out + j);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (j + i < V) out[j + i] = from_f32<T>(f[i]);
+      }
     }
   }
 }
 
-template <typename T> cudaError_t logprob(const LogprobArgs& a, cudaStream_t st) {
-  const dim3 grid((unsigned)a.M);
-  const bool vec = a.M == 1 || a.ld % 8 == 0, top = a.n_top > 0;
-  if (top) return vec ? launch_pdl(logprob_kernel<T, true, true>, grid, LT, 0, 1, st, a) : launch_pdl(logprob_kernel<T, false, true>, grid, LT, 0, 1, st, a);
-  return vec ? launch_pdl(logprob_kernel<T, true, false>, grid, LT, 0, 1, st, a) : launch_pdl(logprob_kernel<T, false, false>, grid, LT, 0, 1, st, a);
+template <typename T, bool VEC> cudaError_t logprob_vec(const LogprobArgs& a, dim3 grid, int cluster, cudaStream_t st) {
+  const bool ent = a.entropy != nullptr;
+  if (a.n_top > 0)
+    return ent ? launch_pdl(logprob_kernel<T, VEC, true, true>, grid, LT, 0, cluster, st, a)
+               : launch_pdl(logprob_kernel<T, VEC, false, true>, grid, LT, 0, cluster, st, a);
+  return ent ? launch_pdl(logprob_kernel<T, VEC, true, false>, grid, LT, 0, cluster, st, a)
+             : launch_pdl(logprob_kernel<T, VEC, false, false>, grid, LT, 0, cluster, st, a);
 }
 
-template <typename T> cudaError_t logprob_bwd(const LogprobBwdArgs& a, cudaStream_t st) {
-  const dim3 grid((unsigned)a.M, (unsigned)((a.V + 8191) / 8192));
-  return a.M == 1 || (a.ld % 8 == 0 && a.ld_dx % 8 == 0) ? launch_pdl(logprob_bwd_kernel<T, true>, grid, 256, 0, 1, st, a)
-                                           : launch_pdl(logprob_bwd_kernel<T, false>, grid, 256, 0, 1, st, a);
+template <typename T> cudaError_t logprob(const LogprobArgs& a, int num_sms, cudaStream_t st) {
+  // Few rows: clusters, while the blocks stay within three on an SM and a slice keeps every thread at
+  // two vectors.
+  int c = 1;
+  while (c < kMaxCluster && a.M * c * 2 <= 3 * num_sms && a.V > c * LT * 16) c *= 2;
+  const dim3 grid((unsigned)(a.M * c));
+  return a.M == 1 || a.ld % 8 == 0 ? logprob_vec<T, true>(a, grid, c, st) : logprob_vec<T, false>(a, grid, c, st);
+}
+
+template <typename T> cudaError_t logprob_bwd(const LogprobBwdArgs& a, int num_sms, cudaStream_t st) {
+  // a block takes a row, or parts of it while there are fewer than 16 blocks for an SM
+  int64_t parts = (16 * num_sms + a.M - 1) / a.M;
+  const int64_t most = (a.V + LC - 1) / LC;
+  if (parts > most) parts = most;
+  const dim3 grid((unsigned)a.M, (unsigned)parts);
+  return a.M == 1 || (a.ld % 8 == 0 && a.ld_dx % 8 == 0) ? launch_pdl(logprob_bwd_kernel<T, true>, grid, LT, 0, 1, st, a)
+                                                         : launch_pdl(logprob_bwd_kernel<T, false>, grid, LT, 0, 1, st, a);
 }
 
 }  // namespace
 
 cudaError_t launch_logprob(const LogprobArgs& a, int dtype, int num_sms, cudaStream_t st) {
   TraceScope ts(TP_LOGPROB, st);
-  return dtype == MOE_F32 ? logprob<float>(a, st) : logprob<__nv_bfloat16>(a, st);
+  return dtype == MOE_F32 ? logprob<float>(a, num_sms, st) : logprob<__nv_bfloat16>(a, num_sms, st);
 }
 
-cudaError_t launch_logprob_bwd(const LogprobBwdArgs& a, int dtype, cudaStream_t st) {
+cudaError_t launch_logprob_bwd(const LogprobBwdArgs& a, int dtype, int num_sms, cudaStream_t st) {
   TraceScope ts(TP_LOGPROB_BWD, st);
-  return dtype == MOE_F32 ? logprob_bwd<float>(a, st) : logprob_bwd<__nv_bfloat16>(a, st);
+  return dtype == MOE_F32 ? logprob_bwd<float>(a, num_sms, st) : logprob_bwd<__nv_bfloat16>(a, num_sms, st);
 }
 
 }  // namespace moe

@@ -154,7 +154,7 @@ struct LogprobBwdArgs {
   int V;
 };
 cudaError_t launch_logprob(const LogprobArgs& a, int dtype, int num_sms, cudaStream_t st);
-cudaError_t launch_logprob_bwd(const LogprobBwdArgs& a, int dtype, cudaStream_t st);
+cudaError_t launch_logprob_bwd(const LogprobBwdArgs& a, int dtype, int num_sms, cudaStream_t st);
 
 // ------------------------------------------------------------------ clipping
 constexpr int kClipFew = 16, kClipMany = 512;   // tensors of a launch (its parameters: 34 bytes for each)

@@ -454,7 +454,7 @@ int moe_token_logprob_bwd(const void* scores, const int32_t* tokens, const float
   int sms = 0;
   OP_TRY(check_device(&sms));
   const LogprobBwdArgs a = {scores, tokens, stats, entropy, d_logprob, d_entropy, d_scores, d.M, d.ld, d.ld_grad, d.V};
-  return launch_logprob_bwd(a, d.dtype, (cudaStream_t)stream) == cudaSuccess ? MOE_OK : MOE_ERR_LAUNCH;
+  return launch_logprob_bwd(a, d.dtype, sms, (cudaStream_t)stream) == cudaSuccess ? MOE_OK : MOE_ERR_LAUNCH;
 }
 
 size_t moe_clip_workspace_bytes(int64_t count) {

@@ -11,6 +11,7 @@
 // their probabilities, the row, the sums, the drawn chunk, each a wait for the one before), by HBM
 // for many: B = 1, V = 32000: 5.2 us; B = 16, V = 50001: 8.1 us; B = 128, V = 131072 in fp32: 134 MB in
 // 34 us, 3.9 TB/s.
+#include "cluster.cuh"
 #include "common.cuh"
 #include "launch.cuh"
 #include "ops.h"
@@ -20,27 +21,6 @@ namespace moe {
 namespace {
 
 constexpr int VT = 512, VW = VT / 32;   // threads and warps per CTA
-
-__device__ __forceinline__ uint32_t ctarank() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
-__device__ __forceinline__ uint32_t nctarank() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
-  return r;
-}
-__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
-__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
-// The 64-bit word at shared address `a` of CTA `rank` of the cluster.
-__device__ __forceinline__ long long peer_ld64(uint32_t a, uint32_t rank) {
-  uint32_t p;
-  long long v;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(p) : "r"(a), "r"(rank));
-  asm volatile("ld.shared::cluster.s64 %0, [%1];" : "=l"(v) : "r"(p) : "memory");
-  return v;
-}
 
 // An fp32 weight as a whole number of 2^-40, added to two sums of 2^-20 and 2^-40 (32 bits each:
 // below 2^12 weights). fmaxf takes NaN to 0. Truncation by adding 2^23 towards zero: every step is

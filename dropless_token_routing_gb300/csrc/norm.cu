@@ -5,11 +5,20 @@
 //   u = dy w,  xh = (s - mean) rstd,  dx = rstd (u - mean(u) - xh mean(u xh)) (+ d_sum)
 //   dw = sum_m dy xh,  db = sum_m dy
 //
-// A row stays in registers between its sums and its way out, so every operand is read once; the
+// A row stays on the SM between its sums and its way out, so every operand is read once; the
 // variance is that of the centred values (no difference of large numbers). All of it is bound by HBM.
+//
+// Rows of up to 8192 elements are taken by groups of warps, two vectors of 8 elements to a thread, in a
+// persistent block of up to 16 warps; wider ones by a block each. A thread copies its own vectors of the
+// rows to come into its own places of shared memory (cp.async), several rows ahead, so that the loads of
+// a group go on through its barriers, and nobody waits for another thread's copies. The
+// columns being a thread's own for all its rows, the weight's gradient is summed in registers.
+#include <mutex>
+
 #include "common.cuh"
 #include "launch.cuh"
 #include "ops.h"
+#include "packed.cuh"
 #include "trace.h"
 
 namespace moe {
@@ -57,6 +66,7 @@ __device__ __forceinline__ void load_sum(float (&f)[8], const T* x, const T* r, 
     for (int j = 0; j < 8; ++j) f[j] += g[j];
   }
 }
+__host__ __device__ __forceinline__ int part_ld(int N) { return (N + 3) & ~3; }   // between rows of partial sums
 template <typename T> __device__ __forceinline__ const T* end_of(const void* p, int64_t M, int64_t ld, int N) {
   return static_cast<const T*>(p) + (M - 1) * ld + N;
 }
@@ -86,8 +96,398 @@ __device__ __forceinline__ float2 block_sums(float a, float b, float* s) {
   return make_float2(a, b);
 }
 
+// ------------------------------------------------------------------ rows of up to kRowsMaxN elements
+constexpr int kRowThreads = 512, kRowVecs = 2;   // most threads of a block; vectors of a thread
+constexpr int kRowsMaxN = kRowThreads * kRowVecs * 8;
+constexpr int kMaxStages = 6;
+constexpr int kRing = 200 * 1024;   // shared memory of an SM for the copies
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+// the first `bytes` of them, zeros behind
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// All but the last n of this thread's groups of copies have arrived.
+__device__ __forceinline__ void cp_wait(int n) {
+  switch (n) {
+    case 0: asm volatile("cp.async.wait_group 0;" ::: "memory"); break;
+    case 1: asm volatile("cp.async.wait_group 1;" ::: "memory"); break;
+    case 2: asm volatile("cp.async.wait_group 2;" ::: "memory"); break;
+    case 3: asm volatile("cp.async.wait_group 3;" ::: "memory"); break;
+    case 4: asm volatile("cp.async.wait_group 4;" ::: "memory"); break;
+    default: asm volatile("cp.async.wait_group 5;" ::: "memory"); break;
+  }
+}
+
+template <typename V> __device__ __forceinline__ void to_pairs(const V& v, uint64_t (&f)[4]) {
+  float g[8];
+  v.to_float(g);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) f[j] = pack2(g[2 * j], g[2 * j + 1]);
+}
+template <typename V> __device__ __forceinline__ void from_pairs(V& v, const uint64_t (&f)[4]) {
+  float g[8];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) unpack2(f[j], g[2 * j], g[2 * j + 1]);
+  v.from_float(g);
+}
+
+// A thread's place for one vector of 8 elements: 16-byte pieces, a block's threads side by side. Without
+// VEC (rows on 16-byte boundaries) a vector's pieces are the aligned ones around it, one more than its own
+// size. FULL: all of a group's vectors are whole ones (widths of 512 times its warps), which saves every
+// test for a row's end (8192 x 7680, two blocks on an SM: 95 us forward with them, 91 without).
+enum RowMode { UNALIGNED = 0, ALIGNED = 1, FULL = 2 };
+template <typename T, int MODE> struct Place {
+  static constexpr bool VEC = MODE != UNALIGNED;
+  static constexpr int kPieces = sizeof(T) / 2 + (VEC ? 0 : 1);
+  // p: the vector's first element; n: elements of the row from there on; end: the tensor's
+  static __device__ __forceinline__ void copy(uint32_t at, const T* p, int n, const T* end) {
+    if (MODE == FULL || (VEC && n >= 8)) {
+#pragma unroll
+      for (int q = 0; q < kPieces; ++q) cp_async16(at + q * blockDim.x * 16, p + q * (16 / sizeof(T)));
+      return;
+    }
+    const uintptr_t from = VEC ? reinterpret_cast<uintptr_t>(p) : reinterpret_cast<uintptr_t>(p) & ~uintptr_t(15);
+    // what there is: the row's elements, or all up to the tensor's end
+    const int64_t there = VEC ? n * (int)sizeof(T) : (int64_t)(reinterpret_cast<uintptr_t>(end) - from);
+#pragma unroll
+    for (int q = 0; q < kPieces; ++q) {
+      const int64_t left = there - 16 * q;
+      const int bytes = left >= 16 ? 16 : left > 0 ? (int)left : 0;
+      cp_async16(at + q * blockDim.x * 16, reinterpret_cast<const void*>(bytes > 0 ? from + 16 * q : from), bytes);
+    }
+  }
+  // The vector as four pairs; elements that the row has not (n < 8) are 0.
+  static __device__ __forceinline__ void read(uint64_t (&f)[4], const uint4* at, const T* row, int c, int n) {
+    Vec8<T> v;
+    if constexpr (VEC) {
+      uint4* d = reinterpret_cast<uint4*>(&v);
+#pragma unroll
+      for (int q = 0; q < kPieces; ++q) d[q] = at[q * blockDim.x];
+    } else {
+      uint32_t w[4 * kPieces];
+#pragma unroll
+      for (int q = 0; q < kPieces; ++q) {
+        const uint4 d = at[q * blockDim.x];
+        w[4 * q] = d.x;
+        w[4 * q + 1] = d.y;
+        w[4 * q + 2] = d.z;
+        w[4 * q + 3] = d.w;
+      }
+      shifted8(v, w, reinterpret_cast<uintptr_t>(row + c));
+    }
+    to_pairs(v, f);
+    if (!VEC && n < 8) keep(f, n);
+  }
+  // A vector's way out. Without VEC the warp's 32 vectors, which lie side by side in the row, are put in order in
+  // their first pieces (the lane's is at `at`; its operand has been read) and go out with
+  // neighbouring elements in neighbouring lanes: every lane of the warp takes part.
+  static __device__ __forceinline__ void write(const uint64_t (&f)[4], uint4* at, T* row, int c, int n) {
+    Vec8<T> v;
+    from_pairs(v, f);
+    if constexpr (VEC) {
+      if (MODE == FULL || n >= 8) {
+        v.store(row + c);
+      } else {
+        const T* e = reinterpret_cast<const T*>(&v);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (i < n) row[c + i] = e[i];
+      }
+    } else {
+      constexpr int kIn = 16 / sizeof(T);   // elements of a piece
+      const int lane = threadIdx.x & 31;
+      const uint4* d = reinterpret_cast<const uint4*>(&v);
+#pragma unroll
+      for (int q = 0; q < kPieces - 1; ++q) at[q * blockDim.x] = d[q];
+      __syncwarp();
+      const T* first = reinterpret_cast<const T*>(at - lane);
+      const int c0 = c - lane * 8, left = n + lane * 8;
+#pragma unroll
+      for (int s = 0; s < 8; ++s) {
+        const int e = s * 32 + lane;
+        if (e < left) row[c0 + e] = first[(e / kIn % (kPieces - 1)) * (int)blockDim.x * kIn + e / 8 * kIn + e % kIn];
+      }
+      __syncwarp();
+    }
+  }
+  static __device__ __forceinline__ void keep(uint64_t (&f)[4], int n) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      float lo, hi;
+      unpack2(f[j], lo, hi);
+      f[j] = pack2(2 * j < n ? lo : 0.f, 2 * j + 1 < n ? hi : 0.f);
+    }
+  }
+};
+
+// A group of warps that takes a row: sums over its threads.
+struct Group {
+  int index, warps;   // which of the block's, its warps
+  // Sums of one or two values, the same in every thread. `s`: the block's 16 pairs, not in use by the call before.
+  template <bool TWO> __device__ __forceinline__ float2 sums(float a, float b, float2* s) const {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      a += __shfl_xor_sync(0xffffffffu, a, o);
+      if (TWO) b += __shfl_xor_sync(0xffffffffu, b, o);
+    }
+    if (warps == 1) return make_float2(a, b);
+    const int lane = threadIdx.x & 31;
+    if (lane == 0) s[threadIdx.x >> 5] = make_float2(a, b);
+    asm volatile("bar.sync %0, %1;" ::"r"(1 + index), "r"(warps * 32) : "memory");
+    float2 t = make_float2(0.f, 0.f);
+    if ((lane & 15) < warps) t = s[index * warps + (lane & 15)];
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) {
+      t.x += __shfl_xor_sync(0xffffffffu, t.x, o);
+      if (TWO) t.y += __shfl_xor_sync(0xffffffffu, t.y, o);
+    }
+    return t;
+  }
+};
+
+template <typename T, typename W, int MODE, bool RES>
+__global__ void __launch_bounds__(kRowThreads, 1) norm_fwd_rows(const NormArgs a, int warps, int stages) {
+  extern __shared__ uint4 ring[];
+  __shared__ float2 s_sums[2][16];
+  using P = Place<T, MODE>;
+  constexpr int kOps = RES ? 2 : 1, kStep = kOps * kRowVecs * P::kPieces;   // places of a stage
+  pdl_start();
+  const int N = a.N, gt = warps * 32, groups = blockDim.x / gt, tg = threadIdx.x % gt;
+  const Group group = {(int)threadIdx.x / gt, warps};
+  const int64_t step = (int64_t)gridDim.x * groups;
+  const T *x0 = static_cast<const T*>(a.x), *r0 = static_cast<const T*>(a.res);
+  const T *x_end = end_of<T>(a.x, a.M, a.ld_x, N), *r_end = RES ? end_of<T>(a.res, a.M, a.ld_res, N) : nullptr;
+  pdl_wait();
+  int64_t next = (int64_t)blockIdx.x * groups + group.index;
+  const T *xp = x0 + next * a.ld_x + tg * 8, *rp = r0 + next * a.ld_res + tg * 8;   // this thread's part of row `next`
+  const int n0 = N - tg * 8;
+  auto fetch = [&](int stage) {
+    if (next < a.M) {
+      const uint32_t at = smem_u32(ring + stage * kStep * blockDim.x + threadIdx.x);
+#pragma unroll
+      for (int i = 0; i < kRowVecs; ++i) {
+        if (MODE == FULL || i * gt * 8 < n0) {
+          P::copy(at + i * P::kPieces * blockDim.x * 16, xp + i * gt * 8, n0 - i * gt * 8, x_end);
+          if (RES) P::copy(at + (kRowVecs + i) * P::kPieces * blockDim.x * 16, rp + i * gt * 8, n0 - i * gt * 8, r_end);
+        }
+      }
+    }
+    next += step;
+    xp += step * a.ld_x;
+    if (RES) rp += step * a.ld_res;
+    cp_commit();
+  };
+  for (int s = 0; s + 1 < stages; ++s) fetch(s);
+  Vec8<W> w[kRowVecs], b[kRowVecs];
+#pragma unroll
+  for (int i = 0; i < kRowVecs; ++i) {
+    const int c = (tg + i * gt) * 8;
+    if (MODE == FULL || c < N) {
+      load_row<W, true>(w[i], static_cast<const W*>(a.w), c, N - c, nullptr);
+      if (a.b != nullptr) load_row<W, true>(b[i], static_cast<const W*>(a.b), c, N - c, nullptr);
+    }
+  }
+  int stage = 0;
+  for (int64_t m = (int64_t)blockIdx.x * groups + group.index; m < a.M; m += step) {
+    fetch(stage == 0 ? stages - 1 : stage - 1);   // (the row before was taken from there)
+    cp_wait(stages - 1);
+    uint4* at = ring + (size_t)stage * kStep * blockDim.x + threadIdx.x;
+    if (++stage == stages) stage = 0;
+    uint64_t f[kRowVecs][4];
+    uint64_t t = 0;
+#pragma unroll
+    for (int i = 0; i < kRowVecs; ++i) {
+      const int c = (tg + i * gt) * 8, n = N - c;
+      uint4* place = at + i * P::kPieces * blockDim.x;
+      if (MODE == FULL || n > 0) {
+        P::read(f[i], place, x0 + m * a.ld_x, c, n);
+        if (RES) {
+          uint64_t g[4];
+          P::read(g, at + (kRowVecs + i) * P::kPieces * blockDim.x, r0 + m * a.ld_res, c, n);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) f[i][j] = add2(f[i][j], g[j]);
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) f[i][j] = 0;
+      }
+      if (RES && a.sum != nullptr && (MODE != ALIGNED || n > 0)) P::write(f[i], place, static_cast<T*>(a.sum) + m * a.ld_sum, c, n);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) t = add2(t, f[i][j]);
+    }
+    const float mean = group.sums<false>(sum2(t), 0.f, s_sums[0]).x * a.inv_n;
+    t = 0;
+#pragma unroll
+    for (int i = 0; i < kRowVecs; ++i) {
+      const int n = N - (tg + i * gt) * 8;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) f[i][j] = add2(f[i][j], both(-mean));
+      if (MODE != FULL && n < 8) P::keep(f[i], n);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) t = fma2(f[i][j], f[i][j], t);
+    }
+    const float rstd = 1.f / sqrtf(group.sums<false>(sum2(t), 0.f, s_sums[1]).x * a.inv_n + a.eps);
+    if (tg == 0 && a.stats != nullptr) reinterpret_cast<float2*>(a.stats)[m] = make_float2(mean, rstd);
+#pragma unroll
+    for (int i = 0; i < kRowVecs; ++i) {
+      const int c = (tg + i * gt) * 8, n = N - c;
+      uint64_t g[4], h[4] = {0, 0, 0, 0};
+      to_pairs(w[i], g);
+      if (a.b != nullptr) to_pairs(b[i], h);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) g[j] = fma2(f[i][j], mul2(g[j], both(rstd)), h[j]);
+      if (MODE != ALIGNED || n > 0) P::write(g, at + i * P::kPieces * blockDim.x, static_cast<T*>(a.y) + m * a.ld_y, c, n);
+    }
+  }
+  cp_wait(0);
+}
+
+// x, dy, then the residual (RES) and d_sum (DS) as further operands of a stage.
+template <typename T, typename W, int MODE, bool RES, bool DS>
+__global__ void __launch_bounds__(kRowThreads, 1) norm_bwd_rows(const NormBwdArgs a, int warps, int stages) {
+  extern __shared__ uint4 ring[];
+  __shared__ float2 s_sums[2][16];
+  using P = Place<T, MODE>;
+  constexpr int kOps = 2 + RES + DS, kOp = kRowVecs * P::kPieces;
+  pdl_start();
+  const int N = a.N, gt = warps * 32, groups = blockDim.x / gt, tg = threadIdx.x % gt;
+  const Group group = {(int)threadIdx.x / gt, warps};
+  const int64_t step = (int64_t)gridDim.x * groups;
+  const T* base[4] = {static_cast<const T*>(a.x), static_cast<const T*>(a.dy), static_cast<const T*>(RES ? a.res : a.d_sum),
+                      static_cast<const T*>(a.d_sum)};
+  const int64_t ld[4] = {a.ld_x, a.ld_dy, RES ? a.ld_res : a.ld_ds, a.ld_ds};
+  pdl_wait();
+  int64_t next = (int64_t)blockIdx.x * groups + group.index;
+  const T *p[kOps], *end[kOps];   // this thread's parts of row `next`
+#pragma unroll
+  for (int o = 0; o < kOps; ++o) {
+    p[o] = base[o] + next * ld[o] + tg * 8;
+    end[o] = end_of<T>(base[o], a.M, ld[o], N);
+  }
+  const int n0 = N - tg * 8;
+  auto fetch = [&](int stage) {
+    if (next < a.M) {
+      const uint32_t at = smem_u32(ring + stage * kOps * kOp * blockDim.x + threadIdx.x);
+#pragma unroll
+      for (int i = 0; i < kRowVecs; ++i) {
+        if (MODE == FULL || i * gt * 8 < n0) {
+#pragma unroll
+          for (int o = 0; o < kOps; ++o)
+            P::copy(at + (o * kOp + i * P::kPieces) * blockDim.x * 16, p[o] + i * gt * 8, n0 - i * gt * 8, end[o]);
+        }
+      }
+    }
+    next += step;
+#pragma unroll
+    for (int o = 0; o < kOps; ++o) p[o] += step * ld[o];
+    cp_commit();
+  };
+  for (int s = 0; s + 1 < stages; ++s) fetch(s);
+  Vec8<W> w[kRowVecs];
+  uint64_t dw[kRowVecs][4], db[kRowVecs][4];
+#pragma unroll
+  for (int i = 0; i < kRowVecs; ++i) {
+    const int c = (tg + i * gt) * 8;
+    if (c < N && a.dx != nullptr) load_row<W, true>(w[i], static_cast<const W*>(a.w), c, N - c, nullptr);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) dw[i][j] = db[i][j] = 0;
+  }
+  int stage = 0, buf = 0;
+  int64_t m = (int64_t)blockIdx.x * groups + group.index;
+  float2 coming = m < a.M ? reinterpret_cast<const float2*>(a.stats)[m] : make_float2(0.f, 0.f);
+  for (; m < a.M; m += step) {
+    const float2 st = coming;
+    if (m + step < a.M) coming = reinterpret_cast<const float2*>(a.stats)[m + step];
+    fetch(stage == 0 ? stages - 1 : stage - 1);
+    cp_wait(stages - 1);
+    uint4* at = ring + (size_t)stage * kOps * kOp * blockDim.x + threadIdx.x;
+    if (++stage == stages) stage = 0;
+    uint64_t u[kRowVecs][4], xh[kRowVecs][4];
+    uint64_t t = 0, tx = 0;
+#pragma unroll
+    for (int i = 0; i < kRowVecs; ++i) {
+      const int c = (tg + i * gt) * 8, n = N - c;
+      if (MODE == FULL || n > 0) {
+        P::read(xh[i], at + i * P::kPieces * blockDim.x, base[0] + m * ld[0], c, n);
+        P::read(u[i], at + (kOp + i * P::kPieces) * blockDim.x, base[1] + m * ld[1], c, n);
+        uint64_t g[4];
+        if (RES) {
+          P::read(g, at + (2 * kOp + i * P::kPieces) * blockDim.x, base[2] + m * ld[2], c, n);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) xh[i][j] = add2(xh[i][j], g[j]);
+        }
+        to_pairs(w[i], g);
+        // (past the row's end u is 0, and with it all that is added)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          xh[i][j] = mul2(add2(xh[i][j], both(-st.x)), both(st.y));
+          db[i][j] = add2(db[i][j], u[i][j]);
+          dw[i][j] = fma2(u[i][j], xh[i][j], dw[i][j]);
+          u[i][j] = mul2(u[i][j], g[j]);
+          t = add2(t, u[i][j]);
+          tx = fma2(u[i][j], xh[i][j], tx);
+        }
+      }
+    }
+    if (a.dx == nullptr) continue;
+    const float2 c12 = group.sums<true>(sum2(t), sum2(tx), s_sums[buf]);
+    buf ^= 1;
+    const uint64_t c1 = both(-c12.x * a.inv_n), c2 = both(-c12.y * a.inv_n), rstd = both(st.y);
+#pragma unroll
+    for (int i = 0; i < kRowVecs; ++i) {
+      const int c = (tg + i * gt) * 8, n = N - c;
+      uint64_t g[4] = {0, 0, 0, 0};
+      if (MODE == FULL || n > 0) {
+        if (DS) P::read(g, at + ((kOps - 1) * kOp + i * P::kPieces) * blockDim.x, base[kOps - 1] + m * ld[kOps - 1], c, n);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) g[j] = fma2(rstd, fma2(xh[i][j], c2, add2(u[i][j], c1)), g[j]);
+      }
+      if (MODE != ALIGNED || n > 0) P::write(g, at + i * P::kPieces * blockDim.x, static_cast<T*>(a.dx) + m * a.ld_dx, c, n);
+    }
+  }
+  cp_wait(0);
+  if (a.dw == nullptr && a.db == nullptr) return;
+  // the groups' sums, added in order: [group][dw, db][column], then a block's partial sums
+  __syncthreads();
+  ulonglong2* mine = reinterpret_cast<ulonglong2*>(ring) + ((size_t)group.index * 2 * gt * kRowVecs + tg) * 2;
+#pragma unroll
+  for (int i = 0; i < kRowVecs; ++i)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      mine[i * gt * 2 + h] = make_ulonglong2(dw[i][2 * h], dw[i][2 * h + 1]);
+      mine[(kRowVecs + i) * gt * 2 + h] = make_ulonglong2(db[i][2 * h], db[i][2 * h + 1]);
+    }
+  __syncthreads();
+  const float* all = reinterpret_cast<const float*>(ring);
+  const int cols = gt * kRowVecs * 8;
+#pragma unroll
+  for (int k = 0; k < 2; ++k)
+    for (int c = threadIdx.x; c < N; c += blockDim.x) {
+      float t = 0.f;
+      for (int g = 0; g < groups; ++g) t += all[(g * 2 + k) * cols + c];
+      a.part[((int64_t)blockIdx.x * 2 + k) * part_ld(N) + c] = t;
+    }
+}
+
+// Warps of a group and groups of a block for rows of N elements: no more groups than rows for an SM.
+struct RowShape {
+  int warps, groups;
+  RowShape(int N, int64_t M, int num_sms) : warps((N + 64 * 8 - 1) / (64 * 8)), groups(kRowThreads / 32 / warps) {
+    const int64_t rows = (M + num_sms - 1) / num_sms;
+    if (groups > rows) groups = (int)rows;
+  }
+  int threads() const { return warps * groups * 32; }
+  // vec: every row starts on a 16-byte boundary
+  static RowMode mode(int N, bool vec) { return !vec ? UNALIGNED : N % 512 == 0 ? FULL : ALIGNED; }
+};
+
+// ------------------------------------------------------------------ wide rows
 template <typename T, typename W, bool VEC>
-__global__ void __launch_bounds__(1024) norm_fwd_kernel(const NormArgs a) {
+__global__ void __launch_bounds__(1024) norm_fwd_wide(const NormArgs a) {
   __shared__ float sums[2][64];
   pdl_start();
   pdl_wait();
@@ -146,7 +546,7 @@ __global__ void __launch_bounds__(1024) norm_fwd_kernel(const NormArgs a) {
 }
 
 template <typename T, typename W, bool VEC>
-__global__ void __launch_bounds__(1024) norm_dx_kernel(const NormBwdArgs a) {
+__global__ void __launch_bounds__(1024) norm_dx_wide(const NormBwdArgs a) {
   __shared__ float sums[64];
   pdl_start();
   pdl_wait();
@@ -242,30 +642,39 @@ __global__ void __launch_bounds__(256) norm_columns_kernel(const NormBwdArgs a, 
     float t = 0.f;
 #pragma unroll
     for (int w = 0; w < 8; ++w) t += s[k][w][l][j];
-    a.part[((int64_t)blockIdx.y * 2 + k) * N + at] = t;
+    a.part[((int64_t)blockIdx.y * 2 + k) * part_ld(N) + at] = t;
   }
 }
 
-// dw and db from their partial sums, added in order.
+// dw (blockIdx.y 0) and db (1) from their partial sums, added in an order that their number alone sets:
+// 32 columns per block, four to a thread, 32 threads each.
 template <typename W>
 __global__ void __launch_bounds__(256) norm_join_kernel(const float* part, int n_part, int N, W* dw, W* db) {
-  __shared__ float s[8][33];
-  const int col = threadIdx.x & 31, r = threadIdx.x >> 5, n = blockIdx.x * 32 + col;
+  __shared__ float4 s[32][8];
+  const int v = threadIdx.x & 7, r = threadIdx.x >> 3, n = blockIdx.x * 32 + v * 4, ld = part_ld(N);
   W* out = blockIdx.y == 0 ? dw : db;
   pdl_start();
   pdl_wait();
   if (out == nullptr) return;
-  float t = 0.f;
+  float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
   if (n < N) {
-#pragma unroll 4
-    for (int i = r; i < n_part; i += 8) t += part[((int64_t)i * 2 + blockIdx.y) * N + n];
+#pragma unroll 5
+    for (int i = r; i < n_part; i += 32) {
+      const float4 p = *reinterpret_cast<const float4*>(part + ((int64_t)i * 2 + blockIdx.y) * ld + n);
+      t.x += p.x;
+      t.y += p.y;
+      t.z += p.z;
+      t.w += p.w;
+    }
   }
-  s[r][col] = t;
+  s[r][v] = t;
   __syncthreads();
-  if (r == 0 && n < N) {
+  if (threadIdx.x < 32 && blockIdx.x * 32 + threadIdx.x < N) {
+    const float* col = reinterpret_cast<const float*>(s) + threadIdx.x;
+    float sum = 0.f;
 #pragma unroll
-    for (int i = 1; i < 8; ++i) t += s[i][col];
-    out[n] = from_f32<W>(t);
+    for (int i = 0; i < 32; ++i) sum += col[i * 32];
+    out[blockIdx.x * 32 + threadIdx.x] = from_f32<W>(sum);
   }
 }
 
@@ -274,48 +683,116 @@ int norm_threads(int N) {
   return t;
 }
 
-template <typename T, typename W> cudaError_t norm_fwd(const NormArgs& a, cudaStream_t st) {
-  const bool vec = a.M == 1 || (a.ld_x % 8 == 0 && a.ld_y % 8 == 0 && (a.res == nullptr || a.ld_res % 8 == 0) &&
-                                (a.sum == nullptr || a.ld_sum % 8 == 0));
-  const dim3 grid((unsigned)a.M);
-  return vec ? launch_pdl(norm_fwd_kernel<T, W, true>, grid, norm_threads(a.N), 0, 1, st, a)
-             : launch_pdl(norm_fwd_kernel<T, W, false>, grid, norm_threads(a.N), 0, 1, st, a);
+// Shared memory above the default size has to be allowed, once for each kernel and device.
+template <auto Kernel> cudaError_t allow_ring(int bytes) {
+  static std::mutex mu;
+  static bool allowed[kMaxDevices];
+  int dev = 0;
+  const cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+  std::lock_guard<std::mutex> lk(mu);
+  if (allowed[dev]) return cudaSuccess;
+  const cudaError_t s = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  allowed[dev] = s == cudaSuccess;
+  return s;
 }
 
-template <typename T, typename W> cudaError_t norm_bwd(const NormBwdArgs& a, cudaStream_t st) {
-  const bool vec = a.M == 1 || (a.ld_x % 8 == 0 && a.ld_dy % 8 == 0 && (a.res == nullptr || a.ld_res % 8 == 0));
-  // columns first: dx may be the buffer of an operand
-  if (a.dw != nullptr || a.db != nullptr) {
-    const int nx = (a.N + 255) / 256;
-    int64_t rows = (a.M + kNormParts - 1) / kNormParts;
-    if (rows < 8) rows = 8;
-    const int parts = (int)((a.M + rows - 1) / rows);
-    const cudaError_t e = vec ? launch_pdl(norm_columns_kernel<T, true>, dim3(nx, parts), 256, 0, 1, st, a, rows)
-                              : launch_pdl(norm_columns_kernel<T, false>, dim3(nx, parts), 256, 0, 1, st, a, rows);
-    if (e != cudaSuccess) return e;
-    const cudaError_t j = launch_pdl(norm_join_kernel<W>, dim3((a.N + 31) / 32, 2), 256, 0, 1, st, (const float*)a.part, parts, a.N,
-                                     static_cast<W*>(a.dw), static_cast<W*>(a.db));
-    if (j != cudaSuccess) return j;
+// A persistent launch: one block on an SM (two with half the ring each: 90 us forward at 8192 x 7680, 77 by one).
+struct RowLaunch {
+  int grid, threads, warps, stages, smem;
+  // stage: bytes of a thread's places of a stage; join: of what it leaves behind the loop
+  RowLaunch(int64_t M, const RowShape& s, int stage, int join, int num_sms) : threads(s.threads()), warps(s.warps) {
+    const int64_t blocks = (M + s.groups - 1) / s.groups;
+    grid = (int)(blocks < num_sms ? blocks : num_sms);
+    const int64_t rows = (blocks + grid - 1) / grid;   // of a group
+    stages = kRing / (threads * stage);
+    if (stages > kMaxStages) stages = kMaxStages;
+    if (stages > rows) stages = (int)rows;
+    smem = threads * (stages * stage > join ? stages * stage : join);
   }
-  if (a.dx == nullptr) return cudaSuccess;
-  const bool vdx = a.M == 1 || (vec && a.ld_dx % 8 == 0 && (a.d_sum == nullptr || a.ld_ds % 8 == 0));
+};
+
+template <typename T, typename W, int MODE, bool RES> cudaError_t fwd_rows(const NormArgs& a, int num_sms, cudaStream_t st) {
+  const RowLaunch l(a.M, RowShape(a.N, a.M, num_sms), 16 * (1 + RES) * kRowVecs * Place<T, MODE>::kPieces, 0, num_sms);
+  const cudaError_t e = allow_ring<norm_fwd_rows<T, W, MODE, RES>>(kRing);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(norm_fwd_rows<T, W, MODE, RES>, dim3(l.grid), l.threads, l.smem, 1, st, a, l.warps, l.stages);
+}
+
+template <typename T, typename W> cudaError_t norm_fwd(const NormArgs& a, int num_sms, cudaStream_t st) {
+  const bool vec = a.M == 1 || (a.ld_x % 8 == 0 && a.ld_y % 8 == 0 && (a.res == nullptr || a.ld_res % 8 == 0) &&
+                                (a.sum == nullptr || a.ld_sum % 8 == 0));
+  if (a.N <= kRowsMaxN) {
+    const bool res = a.res != nullptr;
+    switch (RowShape::mode(a.N, vec)) {
+      case UNALIGNED: return res ? fwd_rows<T, W, UNALIGNED, true>(a, num_sms, st) : fwd_rows<T, W, UNALIGNED, false>(a, num_sms, st);
+      case ALIGNED: return res ? fwd_rows<T, W, ALIGNED, true>(a, num_sms, st) : fwd_rows<T, W, ALIGNED, false>(a, num_sms, st);
+      case FULL: return res ? fwd_rows<T, W, FULL, true>(a, num_sms, st) : fwd_rows<T, W, FULL, false>(a, num_sms, st);
+    }
+  }
   const dim3 grid((unsigned)a.M);
-  return vdx ? launch_pdl(norm_dx_kernel<T, W, true>, grid, norm_threads(a.N), 0, 1, st, a)
-             : launch_pdl(norm_dx_kernel<T, W, false>, grid, norm_threads(a.N), 0, 1, st, a);
+  return vec ? launch_pdl(norm_fwd_wide<T, W, true>, grid, norm_threads(a.N), 0, 1, st, a)
+             : launch_pdl(norm_fwd_wide<T, W, false>, grid, norm_threads(a.N), 0, 1, st, a);
+}
+
+template <typename T, typename W, int MODE, bool RES, bool DS>
+cudaError_t bwd_rows(const NormBwdArgs& a, int num_sms, int* parts, cudaStream_t st) {
+  const RowLaunch l(a.M, RowShape(a.N, a.M, num_sms), 16 * (2 + RES + DS) * kRowVecs * Place<T, MODE>::kPieces, 2 * kRowVecs * 8 * 4,
+                    num_sms);
+  const cudaError_t e = allow_ring<norm_bwd_rows<T, W, MODE, RES, DS>>(kRing);
+  if (e != cudaSuccess) return e;
+  *parts = l.grid;
+  return launch_pdl(norm_bwd_rows<T, W, MODE, RES, DS>, dim3(l.grid), l.threads, l.smem, 1, st, a, l.warps, l.stages);
+}
+
+template <typename T, typename W, int MODE> cudaError_t bwd_mode(const NormBwdArgs& a, int num_sms, int* parts, cudaStream_t st) {
+  const bool ds = a.d_sum != nullptr && a.dx != nullptr;
+  if (a.res != nullptr) return ds ? bwd_rows<T, W, MODE, true, true>(a, num_sms, parts, st) : bwd_rows<T, W, MODE, true, false>(a, num_sms, parts, st);
+  return ds ? bwd_rows<T, W, MODE, false, true>(a, num_sms, parts, st) : bwd_rows<T, W, MODE, false, false>(a, num_sms, parts, st);
+}
+
+template <typename T, typename W> cudaError_t norm_bwd(const NormBwdArgs& a, int num_sms, cudaStream_t st) {
+  const bool sums = a.dw != nullptr || a.db != nullptr, rows = a.N <= kRowsMaxN;
+  const bool vec = a.M == 1 || (a.ld_x % 8 == 0 && a.ld_dy % 8 == 0 && (a.res == nullptr || a.ld_res % 8 == 0));
+  const bool vdx = a.M == 1 || (vec && (a.dx == nullptr || a.ld_dx % 8 == 0) && (a.d_sum == nullptr || a.ld_ds % 8 == 0));
+  int parts = 0;
+  cudaError_t e = cudaSuccess;
+  if (rows) {
+    switch (RowShape::mode(a.N, vdx)) {
+      case UNALIGNED: e = bwd_mode<T, W, UNALIGNED>(a, num_sms, &parts, st); break;
+      case ALIGNED: e = bwd_mode<T, W, ALIGNED>(a, num_sms, &parts, st); break;
+      case FULL: e = bwd_mode<T, W, FULL>(a, num_sms, &parts, st); break;
+    }
+  } else if (sums) {   // columns first: dx may be the buffer of an operand
+    int64_t share = (a.M + kNormParts - 1) / kNormParts;
+    if (share < 8) share = 8;
+    parts = (int)((a.M + share - 1) / share);
+    const dim3 grid((a.N + 255) / 256, parts);
+    e = vec ? launch_pdl(norm_columns_kernel<T, true>, grid, 256, 0, 1, st, a, share)
+            : launch_pdl(norm_columns_kernel<T, false>, grid, 256, 0, 1, st, a, share);
+  }
+  if (e == cudaSuccess && sums)
+    e = launch_pdl(norm_join_kernel<W>, dim3((a.N + 31) / 32, 2), 256, 0, 1, st, (const float*)a.part, parts, a.N,
+                   static_cast<W*>(a.dw), static_cast<W*>(a.db));
+  if (e != cudaSuccess || rows || a.dx == nullptr) return e;
+  const dim3 grid((unsigned)a.M);
+  return vdx ? launch_pdl(norm_dx_wide<T, W, true>, grid, norm_threads(a.N), 0, 1, st, a)
+             : launch_pdl(norm_dx_wide<T, W, false>, grid, norm_threads(a.N), 0, 1, st, a);
 }
 
 }  // namespace
 
-cudaError_t launch_norm_fwd(const NormArgs& a, int dtype, int w_dtype, cudaStream_t st) {
+cudaError_t launch_norm_fwd(const NormArgs& a, int dtype, int w_dtype, int num_sms, cudaStream_t st) {
   TraceScope ts(TP_NORM, st);
-  if (dtype == MOE_F32) return norm_fwd<float, float>(a, st);
-  return w_dtype == MOE_F32 ? norm_fwd<__nv_bfloat16, float>(a, st) : norm_fwd<__nv_bfloat16, __nv_bfloat16>(a, st);
+  if (dtype == MOE_F32) return norm_fwd<float, float>(a, num_sms, st);
+  return w_dtype == MOE_F32 ? norm_fwd<__nv_bfloat16, float>(a, num_sms, st) : norm_fwd<__nv_bfloat16, __nv_bfloat16>(a, num_sms, st);
 }
 
-cudaError_t launch_norm_bwd(const NormBwdArgs& a, int dtype, int w_dtype, cudaStream_t st) {
+cudaError_t launch_norm_bwd(const NormBwdArgs& a, int dtype, int w_dtype, int num_sms, cudaStream_t st) {
   TraceScope ts(TP_NORM_BWD, st);
-  if (dtype == MOE_F32) return norm_bwd<float, float>(a, st);
-  return w_dtype == MOE_F32 ? norm_bwd<__nv_bfloat16, float>(a, st) : norm_bwd<__nv_bfloat16, __nv_bfloat16>(a, st);
+  if (dtype == MOE_F32) return norm_bwd<float, float>(a, num_sms, st);
+  return w_dtype == MOE_F32 ? norm_bwd<__nv_bfloat16, float>(a, num_sms, st) : norm_bwd<__nv_bfloat16, __nv_bfloat16>(a, num_sms, st);
 }
 
 }  // namespace moe

@@ -131,8 +131,8 @@ struct NormBwdArgs {
   int N;
   float inv_n;
 };
-cudaError_t launch_norm_fwd(const NormArgs& a, int dtype, int w_dtype, cudaStream_t st);
-cudaError_t launch_norm_bwd(const NormBwdArgs& a, int dtype, int w_dtype, cudaStream_t st);
+cudaError_t launch_norm_fwd(const NormArgs& a, int dtype, int w_dtype, int num_sms, cudaStream_t st);
+cudaError_t launch_norm_bwd(const NormBwdArgs& a, int dtype, int w_dtype, int num_sms, cudaStream_t st);
 
 // ------------------------------------------------------------------ log probabilities
 constexpr int kMaxTop = 32;   // alternatives

@@ -176,7 +176,7 @@ int resolve_norm(const moe_norm_dims* in, moe_norm_dims* d) {
 }
 
 size_t norm_ws_bytes(const moe_norm_dims& d) {
-  return kOpHeader + round256((size_t)kNormParts * 2 * d.N * 4);
+  return kOpHeader + round256((size_t)kNormParts * 2 * ((d.N + 3) & ~3) * 4);
 }
 
 int resolve_logprob(const moe_logprob_dims* in, moe_logprob_dims* d) {
@@ -380,7 +380,7 @@ int moe_norm_fwd(const void* x, const void* residual, const void* weight, const 
   OP_TRY(check_device(&sms));
   const NormArgs a = {x, residual, weight, bias, residual != nullptr ? sum : nullptr, y, stats, d.M, d.ld_x, d.ld_res, d.ld_sum,
                       d.ld_y, d.N, d.eps, 1.f / (float)d.N};
-  return launch_norm_fwd(a, d.dtype, d.w_dtype, (cudaStream_t)stream) == cudaSuccess ? MOE_OK : MOE_ERR_LAUNCH;
+  return launch_norm_fwd(a, d.dtype, d.w_dtype, sms, (cudaStream_t)stream) == cudaSuccess ? MOE_OK : MOE_ERR_LAUNCH;
 }
 
 size_t moe_norm_workspace_bytes(const moe_norm_dims* dims) {
@@ -415,7 +415,7 @@ int moe_norm_bwd(const void* x, const void* residual, const void* dy, const void
   const NormBwdArgs a = {x, residual, dy, d_sum, weight, stats, dx, dw, db,
                          reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kOpHeader), d.M, d.ld_x, d.ld_res, d.ld_y, d.ld_sum,
                          d.ld_dx, d.N, 1.f / (float)d.N};
-  return launch_norm_bwd(a, d.dtype, d.w_dtype, st) == cudaSuccess ? MOE_OK : MOE_ERR_LAUNCH;
+  return launch_norm_bwd(a, d.dtype, d.w_dtype, sms, st) == cudaSuccess ? MOE_OK : MOE_ERR_LAUNCH;
 }
 
 int moe_token_logprob(const void* scores, const int32_t* tokens, const moe_logprob_dims* dims, float* logprob, float* entropy,

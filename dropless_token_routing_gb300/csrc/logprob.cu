@@ -20,7 +20,8 @@ namespace moe {
 namespace {
 
 constexpr int LT = 256, LW = LT / 32;   // threads and warps of a block
-constexpr int LU = 4, LC = LU * LT * 8;   // vectors of 8 scores that a thread takes at a time, and a block's scores then
+constexpr int LU = 2, LC = LU * LT * 8;   // vectors of 8 scores that a thread takes at a time, and a block's scores then
+constexpr int kBlocks = 5;   // of an SM (4 vectors and 3 blocks: 4096 x 32000 fp32 93 us, 81 so; 8192 x 131072 bf16 313, 300)
 constexpr int kMaxCluster = 8;
 constexpr float kLog2e = 1.44269504088896340736f, kLowest = -3.402823466e38f, kInf = __builtin_huge_valf();
 
@@ -85,7 +86,7 @@ __device__ __forceinline__ void load_scores(Vec8<T>& v, const T* row, int j, int
   }
 }
 // Adds a thread's LU vectors to its sums; ENT: D too.
-template <typename T, bool ENT> __device__ __forceinline__ void add_scores(Sums& s, const float (&f)[LU][8]) {
+template <bool ENT> __device__ __forceinline__ void add_scores(Sums& s, const float (&f)[LU][8]) {
   float max = s.m;
 #pragma unroll
   for (int u = 0; u < LU; ++u)
@@ -114,52 +115,61 @@ template <typename T, bool ENT> __device__ __forceinline__ void add_scores(Sums&
 }
 
 static_assert(kMaxCluster * kMaxTop == LT && LT / 4 == 64, "");
-struct TopShared {
-  unsigned long long key[LT];   // candidates, unordered
-  unsigned long long sorted[kMaxTop];              // this block's alternatives, descending
-  float group[64];                                 // maxima of 4 threads each
-  float bound;
-  int count;
+struct alignas(16) TopShared {
+  unsigned long long key[LT];          // candidates, unordered
+  unsigned long long sorted[kMaxTop];  // this block's alternatives, descending
   unsigned long long warp[2][LW];
+  float group[64];                     // maxima of 4 threads each
+  int thread[LT];                      // threads that hold a candidate
+  float bound;
+  int threads, count;
 };
 
 // The block's n highest keys among scores [j0, j1) of the row, descending, into t.sorted (0: no more).
 // `mine`: the highest score that this thread took (vectors threadIdx.x, + LT, ..). The n-th highest of
 // 64 groups' maxima is no higher than the n-th highest score, and few scores reach it (24 of 131072
-// in random order, n = 20): only the threads that hold one look at their scores again. Rows where
-// more than 256 reach it (in order, or of few values) are taken one key at a time.
-template <typename T> __device__ void block_top(TopShared& t, const T* row, int j0, int j1, float mine, int n) {
+// in random order, n = 20): only the scores of threads that hold one are looked at again, by all of
+// the block's threads. Rows where more than 256 reach it (in order, or of few values) are taken one key at a time.
+template <typename T, bool VEC>
+__device__ __forceinline__ void block_top(TopShared& t, const T* row, int j0, int j1, const T* end, float mine, int n) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   float g = mine;
   g = fmaxf(g, __shfl_xor_sync(0xffffffffu, g, 1));
   g = fmaxf(g, __shfl_xor_sync(0xffffffffu, g, 2));
   if ((lane & 3) == 0) t.group[tid >> 2] = g;
-  if (tid == 0) t.count = 0;
+  if (tid == 0) t.threads = t.count = 0;
   if (tid < kMaxTop) t.sorted[tid] = 0;
   __syncthreads();
   if (tid < 64) {
     g = t.group[tid];
     int above = 0;
-#pragma unroll 16
-    for (int i = 0; i < 64; ++i) {
-      const float o = t.group[i];
-      above += o > g || (o == g && i < tid);
+#pragma unroll
+    for (int i = 0; i < 64; i += 4) {
+      const float4 o = *reinterpret_cast<const float4*>(&t.group[i]);
+      above += (o.x > g || (o.x == g && i < tid)) + (o.y > g || (o.y == g && i + 1 < tid)) + (o.z > g || (o.z == g && i + 2 < tid)) +
+               (o.w > g || (o.w == g && i + 3 < tid));
     }
     if (above == n - 1) t.bound = g;
   }
   __syncthreads();
   const float bound = t.bound;
-  for (uint32_t who = __ballot_sync(0xffffffffu, mine >= bound); who != 0u; who &= who - 1) {
-    const int first = j0 + ((warp << 5) + __ffs((int)who) - 1) * 8;
-    for (int j = first + lane * LT * 8; j < j1; j += 32 * LT * 8)
+  if (mine >= bound) t.thread[atomicAdd(&t.threads, 1)] = tid;
+  __syncthreads();
+  const int steps = (j1 - j0 + LT * 8 - 1) / (LT * 8), items = t.threads * steps;
+  for (int k = tid; k < items; k += LT) {
+    const int j = j0 + t.thread[k / steps] * 8 + k % steps * (LT * 8);
+    if (j < j1) {
+      Vec8<T> v;
+      float f[8];
+      load_scores<T, VEC>(v, row, j, j1, end);
+      v.to_float(f);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float x = j + i < j1 ? to_f32(row[j + i]) : -kInf;
-        if (x >= bound && x > -kInf) {
+      for (int i = 0; i < 8; ++i)
+        if (f[i] >= bound && f[i] > -kInf && j + i < j1) {
           const int at = atomicAdd(&t.count, 1);
-          if (at < LT) t.key[at] = key_of(x, j + i);
+          if (at < LT) t.key[at] = key_of(f[i], j + i);
         }
-      }
+    }
   }
   __syncthreads();
   const int count = t.count;
@@ -167,10 +177,10 @@ template <typename T> __device__ void block_top(TopShared& t, const T* row, int 
     if (tid < count) {
       const unsigned long long key = t.key[tid];
       int above = 0;
+#pragma unroll 4
       for (int i = 0; i < count; ++i) above += t.key[i] > key;
       if (above < n) t.sorted[above] = key;
     }
-    __syncthreads();
     return;
   }
   unsigned long long best = ~0ull, top = ~0ull;
@@ -195,23 +205,11 @@ template <typename T> __device__ void block_top(TopShared& t, const T* row, int 
     if (top == 0) break;
     if (tid == 0) t.sorted[k] = top;
   }
-  __syncthreads();
-}
-
-// Keys of a descending list of n that are higher than `key`.
-__device__ __forceinline__ int above_in(const unsigned long long* list, int n, unsigned long long key) {
-  int lo = 0, hi = n;
-  while (lo < hi) {
-    const int mid = (lo + hi) >> 1;
-    if (list[mid] > key) lo = mid + 1;
-    else hi = mid;
-  }
-  return lo;
 }
 
 // A row is a cluster's (one block for many rows): every block takes a slice, the first one joins their sums.
 template <typename T, bool VEC, bool ENT, bool TOP>
-__global__ void __launch_bounds__(LT, 3) logprob_kernel(const LogprobArgs a) {
+__global__ void __launch_bounds__(LT, TOP ? 3 : kBlocks) logprob_kernel(const LogprobArgs a) {
   __shared__ Sums s_sums[LW];
   __shared__ TopShared s_top[1];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, V = a.V;
@@ -246,7 +244,7 @@ __global__ void __launch_bounds__(LT, 3) logprob_kernel(const LogprobArgs a) {
 #pragma unroll
       for (int u = 0; u < LU; ++u) load_scores<T, VEC>(v[u], row, mine + (k + 1) * LC + u * LT * 8, V, end);
     }
-    add_scores<T, ENT>(s, f);
+    add_scores<ENT>(s, f);
   }
   if (j0 + whole * LC < j1) {
     float f[LU][8];
@@ -263,12 +261,12 @@ __global__ void __launch_bounds__(LT, 3) logprob_kernel(const LogprobArgs a) {
       for (int i = 0; i < 8; ++i)
         if (j + i >= j1) f[u][i] = -kInf;
     }
-    add_scores<T, ENT>(s, f);
+    add_scores<ENT>(s, f);
   }
   const float highest = s.m;
   s.warp_join();
   if (lane == 0) s_sums[warp] = s;
-  if constexpr (TOP) block_top(s_top[0], row, j0, j1, highest, a.n_top);
+  if constexpr (TOP) block_top<T, VEC>(s_top[0], row, j0, j1, end, highest, a.n_top);
   if (ranks > 1) {
     cluster_arrive();
     cluster_wait();
@@ -306,9 +304,15 @@ __global__ void __launch_bounds__(LT, 3) logprob_kernel(const LogprobArgs a) {
       t.key[threadIdx.x] = key;   // the blocks' lists in a row
       __syncthreads();
       if (key != 0) {
-        int at = i;
-        for (int o = 0; o < (int)ranks; ++o)
-          if (o != r) at += above_in(t.key + o * kMaxTop, a.n_top, key);
+        // its place: the higher keys of every list (its own among them), in the lists' 32 descending places
+        int higher[kMaxCluster] = {}, at = 0;
+#pragma unroll
+        for (int step = 16; step > 0; step >>= 1)
+#pragma unroll
+          for (int o = 0; o < kMaxCluster; ++o)
+            if (t.key[o * kMaxTop + higher[o] + step - 1] > key) higher[o] += step;
+#pragma unroll
+        for (int o = 0; o < kMaxCluster; ++o) at += higher[o] + (t.key[o * kMaxTop + higher[o]] > key);
         if (at < a.n_top) {
           const uint32_t b = (uint32_t)(key >> 32);
           const float x = __uint_as_float(b & 0x80000000u ? b & 0x7fffffffu : ~b);
@@ -331,6 +335,8 @@ __global__ void __launch_bounds__(LT, 3) logprob_kernel(const LogprobArgs a) {
   }
 }
 
+constexpr int GU = 4, GC = GU * LT * 8;   // the same of the gradient
+
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(LT) logprob_bwd_kernel(const LogprobBwdArgs a) {
   const int V = a.V;
@@ -346,15 +352,15 @@ __global__ void __launch_bounds__(LT) logprob_bwd_kernel(const LogprobBwdArgs a)
   const float g = token >= 0 && token < V ? a.d_logprob[m] : 0.f;
   const float h = a.d_entropy != nullptr && some ? a.d_entropy[m] : 0.f, H = h != 0.f ? a.entropy[m] : 0.f;
   const bool zero = g == 0.f && h == 0.f;
-  for (int j0 = (blockIdx.y * LU * LT + threadIdx.x) * 8; j0 < V; j0 += gridDim.y * LC) {
-    Vec8<T> v[LU];
+  for (int j0 = (blockIdx.y * GU * LT + threadIdx.x) * 8; j0 < V; j0 += gridDim.y * GC) {
+    Vec8<T> v[GU];
     if (!zero) {
 #pragma unroll
-      for (int u = 0; u < LU; ++u)
+      for (int u = 0; u < GU; ++u)
         if (j0 + u * LT * 8 < V) load_scores<T, VEC>(v[u], row, j0 + u * LT * 8, V, end);
     }
 #pragma unroll
-    for (int u = 0; u < LU; ++u) {
+    for (int u = 0; u < GU; ++u) {
       const int j = j0 + u * LT * 8;
       if (j >= V) break;
       float f[8];
@@ -403,7 +409,7 @@ template <typename T> cudaError_t logprob(const LogprobArgs& a, int num_sms, cud
 template <typename T> cudaError_t logprob_bwd(const LogprobBwdArgs& a, int num_sms, cudaStream_t st) {
   // a block takes a row, or parts of it while there are fewer than 16 blocks for an SM
   int64_t parts = (16 * num_sms + a.M - 1) / a.M;
-  const int64_t most = (a.V + LC - 1) / LC;
+  const int64_t most = (a.V + GC - 1) / GC;
   if (parts > most) parts = most;
   const dim3 grid((unsigned)a.M, (unsigned)parts);
   return a.M == 1 || (a.ld % 8 == 0 && a.ld_dx % 8 == 0) ? launch_pdl(logprob_bwd_kernel<T, true>, grid, LT, 0, 1, st, a)

@@ -159,13 +159,19 @@ cudaError_t launch_logprob_bwd(const LogprobBwdArgs& a, int dtype, int num_sms, 
 // ------------------------------------------------------------------ clipping
 constexpr int kClipFew = 16, kClipMany = 512;   // tensors of a launch (its parameters: 34 bytes for each)
 constexpr int kClipParts = 1024;                // most partial sums of a launch
+constexpr size_t kClipCounter = 64;             // in a workspace's header, where no other operator counts
 constexpr int64_t kClipMaxTotal = 1ll << 44;    // elements of all tensors
+struct alignas(16) ClipPart {   // a block's sum of squares: hi + lo + far
+  float hi, lo;
+  double far;
+};
 struct ClipArgs {
   const moe_grad* grads;   // host
   int64_t count;
   float max_norm;
   float *norm, *scale;     // device, or NULL
-  double* part;
+  ClipPart* part;
+  uint32_t* counter;       // 0 between calls
 };
 cudaError_t launch_clip(const ClipArgs& a, int num_sms, cudaStream_t st);
 

@@ -459,7 +459,7 @@ int moe_token_logprob_bwd(const void* scores, const int32_t* tokens, const float
 
 size_t moe_clip_workspace_bytes(int64_t count) {
   if (count < 0 || count > (1 << 24)) return 0;
-  return kOpHeader + 8 * (size_t)kClipParts * (size_t)(count / kClipMany + 1);
+  return kOpHeader + sizeof(ClipPart) * (size_t)kClipParts * (size_t)(count / kClipMany + 1);
 }
 
 int moe_clip_grads(const moe_grad* grads, int64_t count, float max_norm, float* norm, float* scale, void* ws, size_t ws_bytes,
@@ -482,7 +482,9 @@ int moe_clip_grads(const moe_grad* grads, int64_t count, float max_norm, float* 
   OP_TRY(check_overlap(grads, count));
   int sms = 0;
   OP_TRY(check_device(&sms));
-  const ClipArgs a = {grads, count, max_norm, norm, scale, reinterpret_cast<double*>(static_cast<uint8_t*>(ws) + kOpHeader)};
+  uint8_t* base = static_cast<uint8_t*>(ws);
+  const ClipArgs a = {grads, count, max_norm, norm, scale, reinterpret_cast<ClipPart*>(base + kOpHeader),
+                      reinterpret_cast<uint32_t*>(base + kClipCounter)};
   return launch_clip(a, sms, (cudaStream_t)stream) == cudaSuccess ? MOE_OK : MOE_ERR_LAUNCH;
 }
 

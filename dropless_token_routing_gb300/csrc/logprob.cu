@@ -21,7 +21,9 @@ namespace {
 
 constexpr int LT = 256, LW = LT / 32;   // threads and warps of a block
 constexpr int LU = 2, LC = LU * LT * 8;   // vectors of 8 scores that a thread takes at a time, and a block's scores then
-constexpr int kBlocks = 5;   // of an SM (4 vectors and 3 blocks: 4096 x 32000 fp32 93 us, 81 so; 8192 x 131072 bf16 313, 300)
+// Blocks of an SM. 4096 x 32000 fp32 with entropy: 79 us by 5, 81 by 4, 91 by 6; bf16: 52, 55, 48; 8192 x 131072 bf16
+// without: 300 by 5, 315 by 6; with alternatives, 1024 x 131072: 68 by 4, 86 by 3 (5 have no room for the registers).
+template <typename T, bool ENT, bool TOP> constexpr int kBlocks = TOP ? 4 : ENT && sizeof(T) == 2 ? 6 : 5;
 constexpr int kMaxCluster = 8;
 constexpr float kLog2e = 1.44269504088896340736f, kLowest = -3.402823466e38f, kInf = __builtin_huge_valf();
 
@@ -49,7 +51,7 @@ struct Sums {
     S *= e;
     m = max;
   }
-  __device__ __forceinline__ void warp_join() {   // the warp's, in every lane
+  template <bool ENT> __device__ __forceinline__ void warp_join() {   // the warp's, in every lane
     float max = m;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) max = fmaxf(max, __shfl_xor_sync(0xffffffffu, max, o));
@@ -57,7 +59,7 @@ struct Sums {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
       S += __shfl_xor_sync(0xffffffffu, S, o);
-      D += __shfl_xor_sync(0xffffffffu, D, o);
+      if (ENT) D += __shfl_xor_sync(0xffffffffu, D, o);
     }
   }
 };
@@ -72,28 +74,64 @@ __device__ __forceinline__ uint32_t index_of(unsigned long long key) { return 0x
 
 __device__ __forceinline__ unsigned long long max64(unsigned long long a, unsigned long long b) { return a > b ? a : b; }
 
-// 8 scores of a row from j on; those from `stop` on are not there.
-template <typename T, bool VEC>
-__device__ __forceinline__ void load_scores(Vec8<T>& v, const T* row, int j, int stop, const T* end) {
-  if (VEC && j + 8 <= stop) {
-    v.load_plain(row + j);
-  } else if (!VEC) {
-    load8_unaligned(v, row + j, end, stop - j);
-  } else {
-    T* e = reinterpret_cast<T*>(&v);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) e[i] = j + i < stop ? row[j + i] : T(0.f);
+// A row is read in 16-byte vectors wherever it starts: place k of it is the k-th element from the 16-byte
+// boundary at or below its first one, which is place `lead` (the tensor's own start is a boundary, so the places
+// before it are the row before's). (Vectors shifted into place instead: 2000 x 50001 bf16, forward 56 us,
+// 39 so; the gradient 276 us, 66.)
+template <typename T> struct Places {
+  const T* base;
+  int lead, end;   // the row's first place, and the one after its last
+  __device__ __forceinline__ Places(const T* row, int V) {
+    lead = (int)(reinterpret_cast<uintptr_t>(row) & 15) / (int)sizeof(T);
+    base = row - lead;
+    end = V + lead;
   }
+  // places k .. k + 7 (a multiple of 8); those past the end: not loaded
+  __device__ __forceinline__ void load(Vec8<T>& v, int k) const {
+    if (k + 8 <= end) {
+      v.load_plain(base + k);
+    } else {
+      T* e = reinterpret_cast<T*>(&v);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) e[i] = k + i < end ? base[k + i] : T(0.f);
+    }
+  }
+  // as numbers, -inf for those that are not the row's
+  __device__ __forceinline__ void scores(float (&f)[8], const Vec8<T>& v, int k) const {
+    v.to_float(f);
+    if (k < lead || k + 8 > end) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (k + i < lead || k + i >= end) f[i] = -kInf;
+    }
+  }
+};
+
+// The highest of a thread's vectors (NaN aside): two bf16 at a time
+__device__ __forceinline__ float highest(const Vec8<__nv_bfloat16> (&v)[LU]) {
+  const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(v);
+  __nv_bfloat162 m = h[0];
+#pragma unroll
+  for (int i = 1; i < 4 * LU; ++i) m = __hmax2(m, h[i]);
+  return fmaxf(__low2float(m), __high2float(m));
 }
-// Adds a thread's LU vectors to its sums; ENT: D too.
-template <bool ENT> __device__ __forceinline__ void add_scores(Sums& s, const float (&f)[LU][8]) {
-  float max = s.m;
+__device__ __forceinline__ float highest(const Vec8<float> (&v)[LU]) {
+  const float* h = reinterpret_cast<const float*>(v);
+  float m = h[0];
 #pragma unroll
-  for (int u = 0; u < LU; ++u)
+  for (int i = 1; i < 8 * LU; ++i) m = fmaxf(m, h[i]);
+  return m;
+}
+__device__ __forceinline__ float highest(const float (&f)[LU][8]) {
+  float m = f[0][0];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) max = fmaxf(max, f[u][i]);
-  if (max > s.m) s.to(max);
-  const uint64_t nm = both(-max), l2e = both(kLog2e);
+  for (int i = 1; i < 8 * LU; ++i) m = fmaxf(m, f[i / 8][i % 8]);
+  return m;
+}
+// Adds a thread's LU vectors, the highest of which is `top`, to its sums; ENT: D too.
+template <bool ENT> __device__ __forceinline__ void add_scores(Sums& s, const float (&f)[LU][8], float top) {
+  if (top > s.m) s.to(top);
+  const uint64_t nm = both(-s.m), l2e = both(kLog2e);
   uint64_t S[2] = {0, 0}, D[2] = {0, 0};   // two chains of additions
 #pragma unroll
   for (int u = 0; u < LU; ++u)
@@ -125,13 +163,13 @@ struct alignas(16) TopShared {
   int threads, count;
 };
 
-// The block's n highest keys among scores [j0, j1) of the row, descending, into t.sorted (0: no more).
+// The block's n highest keys among places [j0, j1) of the row, descending, into t.sorted (0: no more).
 // `mine`: the highest score that this thread took (vectors threadIdx.x, + LT, ..). The n-th highest of
 // 64 groups' maxima is no higher than the n-th highest score, and few scores reach it (24 of 131072
 // in random order, n = 20): only the scores of threads that hold one are looked at again, by all of
 // the block's threads. Rows where more than 256 reach it (in order, or of few values) are taken one key at a time.
-template <typename T, bool VEC>
-__device__ __forceinline__ void block_top(TopShared& t, const T* row, int j0, int j1, const T* end, float mine, int n) {
+template <typename T>
+__device__ __forceinline__ void block_top(TopShared& t, const Places<T>& row, int j0, int j1, float mine, int n) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   float g = mine;
   g = fmaxf(g, __shfl_xor_sync(0xffffffffu, g, 1));
@@ -161,13 +199,13 @@ __device__ __forceinline__ void block_top(TopShared& t, const T* row, int j0, in
     if (j < j1) {
       Vec8<T> v;
       float f[8];
-      load_scores<T, VEC>(v, row, j, j1, end);
-      v.to_float(f);
+      row.load(v, j);
+      row.scores(f, v, j);
 #pragma unroll
       for (int i = 0; i < 8; ++i)
-        if (f[i] >= bound && f[i] > -kInf && j + i < j1) {
+        if (f[i] >= bound && f[i] > -kInf) {
           const int at = atomicAdd(&t.count, 1);
-          if (at < LT) t.key[at] = key_of(f[i], j + i);
+          if (at < LT) t.key[at] = key_of(f[i], j + i - row.lead);
         }
     }
   }
@@ -187,12 +225,17 @@ __device__ __forceinline__ void block_top(TopShared& t, const T* row, int j0, in
   for (int k = 0; k < n; ++k) {
     if (best == top) {   // this thread's next key
       best = 0;
-      for (int j = j0 + tid * 8; j < j1; j += LT * 8)
-        for (int i = 0; i < 8 && j + i < j1; ++i) {
-          const float x = to_f32(row[j + i]);
-          const unsigned long long key = key_of(x, j + i);
-          if (x > -kInf && key < top) best = max64(best, key);
+      for (int j = j0 + tid * 8; j < j1; j += LT * 8) {
+        Vec8<T> v;
+        float f[8];
+        row.load(v, j);
+        row.scores(f, v, j);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const unsigned long long key = key_of(f[i], j + i - row.lead);
+          if (f[i] > -kInf && key < top) best = max64(best, key);
         }
+      }
     }
     top = best;
 #pragma unroll
@@ -208,65 +251,70 @@ __device__ __forceinline__ void block_top(TopShared& t, const T* row, int j0, in
 }
 
 // A row is a cluster's (one block for many rows): every block takes a slice, the first one joins their sums.
-template <typename T, bool VEC, bool ENT, bool TOP>
-__global__ void __launch_bounds__(LT, TOP ? 3 : kBlocks) logprob_kernel(const LogprobArgs a) {
+template <typename T, bool ENT, bool TOP>
+__global__ void __launch_bounds__(LT, (kBlocks<T, ENT, TOP>)) logprob_kernel(const LogprobArgs a) {
   __shared__ Sums s_sums[LW];
+  __shared__ float2 s_row;       // the row's maximum and ln S
   __shared__ TopShared s_top[1];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, V = a.V;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = ctarank(), ranks = nctarank();
   pdl_start();
   pdl_wait();
   const int64_t m = blockIdx.x / ranks;
-  const T* row = static_cast<const T*>(a.x) + m * a.ld;
-  const T* end = static_cast<const T*>(a.x) + (a.M - 1) * a.ld + V;
-  const int slice = (int)(((V + ranks - 1) / ranks + 7) & ~7u);
-  const int j0 = min((int)rank * slice, V), j1 = min(j0 + slice, V);
+  const T* first = static_cast<const T*>(a.x) + m * a.ld;
+  const Places<T> row(first, a.V);
+  const int slice = (int)(((row.end + ranks - 1) / ranks + 7) & ~7u);
+  const int j0 = min((int)rank * slice, row.end), j1 = min(j0 + slice, row.end);
   int token = -1;
   float given = 0.f;
   if (rank == 0 && threadIdx.x == 0 && a.logprob != nullptr) {
     token = a.tokens[m];
-    if (token >= V) token = -1;
-    if (token >= 0) given = to_f32(row[token]);
+    if (token >= a.V) token = -1;
+    if (token >= 0) given = to_f32(first[token]);
   }
 
   Sums s = {kLowest, 0.f, 0.f};
-  const int mine = j0 + threadIdx.x * 8, whole = (j1 - j0) / LC;   // steps that need no bounds
+  const int mine = j0 + threadIdx.x * 8, whole = (j1 - j0) / LC;   // steps that no thread ends in
   Vec8<T> v[LU];
   if (whole > 0) {
 #pragma unroll
-    for (int u = 0; u < LU; ++u) load_scores<T, VEC>(v[u], row, mine + u * LT * 8, V, end);
+    for (int u = 0; u < LU; ++u) v[u].load_plain(row.base + mine + u * LT * 8);
   }
   for (int k = 0; k < whole; ++k) {
     float f[LU][8];
 #pragma unroll
     for (int u = 0; u < LU; ++u) v[u].to_float(f[u]);
+    float top = highest(v);
     if (k + 1 < whole) {   // the next step's scores are under way while these are added
 #pragma unroll
-      for (int u = 0; u < LU; ++u) load_scores<T, VEC>(v[u], row, mine + (k + 1) * LC + u * LT * 8, V, end);
+      for (int u = 0; u < LU; ++u) v[u].load_plain(row.base + mine + (k + 1) * LC + u * LT * 8);
     }
-    add_scores<ENT>(s, f);
+    if (mine < row.lead && k == 0) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (i < row.lead) f[0][i] = -kInf;
+      top = highest(f);
+    }
+    add_scores<ENT>(s, f, top);
   }
   if (j0 + whole * LC < j1) {
     float f[LU][8];
 #pragma unroll
     for (int u = 0; u < LU; ++u) {
       const int j = mine + whole * LC + u * LT * 8;
-      if (j < j1) load_scores<T, VEC>(v[u], row, j, j1, end);
+      if (j < j1) row.load(v[u], j);
     }
 #pragma unroll
     for (int u = 0; u < LU; ++u) {
       const int j = mine + whole * LC + u * LT * 8;
-      v[u].to_float(f[u]);
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (j + i >= j1) f[u][i] = -kInf;
+      row.scores(f[u], v[u], j < j1 ? j : row.end);
     }
-    add_scores<ENT>(s, f);
+    add_scores<ENT>(s, f, highest(f));
   }
-  const float highest = s.m;
-  s.warp_join();
+  const float top = s.m;
+  s.warp_join<ENT>();
   if (lane == 0) s_sums[warp] = s;
-  if constexpr (TOP) block_top<T, VEC>(s_top[0], row, j0, j1, end, highest, a.n_top);
+  if constexpr (TOP) block_top(s_top[0], row, j0, j1, top, a.n_top);
   if (ranks > 1) {
     cluster_arrive();
     cluster_wait();
@@ -274,27 +322,32 @@ __global__ void __launch_bounds__(LT, TOP ? 3 : kBlocks) logprob_kernel(const Lo
     __syncthreads();
   }
   if (rank == 0) {
-    // the sums of up to 64 warps, in every warp
-    const int n = (int)ranks * LW;
-    s = {kLowest, 0.f, 0.f};
-    for (int r = lane; r < n; r += 32) {
-      const uint32_t at = smem_u32(&s_sums[r % LW]);
-      Sums o;
-      o.m = peer_ldf(at, r / LW);
-      o.S = peer_ldf(at + 4, r / LW);
-      o.D = peer_ldf(at + 8, r / LW);
-      const float max = fmaxf(s.m, o.m);
-      s.to(max);
-      o.to(max);
-      s.S += o.S;
-      s.D += o.D;
-    }
-    s.warp_join();
-    const float log_sum = s.S == 0.f ? -kInf : logf(s.S);   // a row without a distribution: -inf
-    if (threadIdx.x == 0) {
-      if (a.logprob != nullptr) a.logprob[m] = token < 0 ? 0.f : s.S == 0.f ? -kInf : (given - s.m) - log_sum;
-      if (a.stats != nullptr) reinterpret_cast<float2*>(a.stats)[m] = make_float2(s.m, log_sum);
-      if (ENT) a.entropy[m] = s.S == 0.f ? 0.f : log_sum - s.D / s.S;
+    if (warp == 0) {   // the sums of up to 64 warps
+      s = {kLowest, 0.f, 0.f};
+      for (int r = lane; r < (int)ranks * LW; r += 32) {
+        Sums o;
+        if (ranks > 1) {
+          const uint32_t at = smem_u32(&s_sums[r % LW]);
+          o.m = peer_ldf(at, r / LW);
+          o.S = peer_ldf(at + 4, r / LW);
+          o.D = peer_ldf(at + 8, r / LW);
+        } else {
+          o = s_sums[r];
+        }
+        const float max = fmaxf(s.m, o.m);
+        s.to(max);
+        o.to(max);
+        s.S += o.S;
+        s.D += o.D;
+      }
+      s.warp_join<ENT>();
+      const float log_sum = s.S == 0.f ? -kInf : logf(s.S);   // a row without a distribution: -inf
+      if (lane == 0) {
+        if (a.logprob != nullptr) a.logprob[m] = token < 0 ? 0.f : s.S == 0.f ? -kInf : (given - s.m) - log_sum;
+        if (a.stats != nullptr) reinterpret_cast<float2*>(a.stats)[m] = make_float2(s.m, log_sum);
+        if (ENT) a.entropy[m] = s.S == 0.f ? 0.f : log_sum - s.D / s.S;
+        if (TOP) s_row = make_float2(s.m, log_sum);
+      }
     }
     if constexpr (TOP) {
       TopShared& t = s_top[0];
@@ -317,7 +370,7 @@ __global__ void __launch_bounds__(LT, TOP ? 3 : kBlocks) logprob_kernel(const Lo
           const uint32_t b = (uint32_t)(key >> 32);
           const float x = __uint_as_float(b & 0x80000000u ? b & 0x7fffffffu : ~b);
           a.top_idx[m * a.n_top + at] = (int)index_of(key);
-          a.top_logprob[m * a.n_top + at] = (x - s.m) - log_sum;
+          a.top_logprob[m * a.n_top + at] = (x - s_row.x) - s_row.y;
         }
       }
       // places that no key took
@@ -337,32 +390,34 @@ __global__ void __launch_bounds__(LT, TOP ? 3 : kBlocks) logprob_kernel(const Lo
 
 constexpr int GU = 4, GC = GU * LT * 8;   // the same of the gradient
 
-template <typename T, bool VEC>
+template <typename T>
 __global__ void __launch_bounds__(LT) logprob_bwd_kernel(const LogprobBwdArgs a) {
-  const int V = a.V;
   pdl_start();
   pdl_wait();
   const int64_t m = blockIdx.x;
-  const T* row = static_cast<const T*>(a.x) + m * a.ld;
-  const T* end = static_cast<const T*>(a.x) + (a.M - 1) * a.ld + V;
-  T* out = static_cast<T*>(a.dx) + m * a.ld_dx;
+  const T* first = static_cast<const T*>(a.x) + m * a.ld;
+  const Places<T> row(first, a.V);
+  T* out = static_cast<T*>(a.dx) + m * a.ld_dx - row.lead;   // of place 0
+  const bool vec = (reinterpret_cast<uintptr_t>(out) & 15) == 0;
   const float2 st = reinterpret_cast<const float2*>(a.stats)[m];
   const bool some = !(st.y == -kInf);     // the row has a distribution
-  const int token = a.d_logprob != nullptr && some ? a.tokens[m] : -1;
-  const float g = token >= 0 && token < V ? a.d_logprob[m] : 0.f;
+  int token = a.d_logprob != nullptr && some ? a.tokens[m] : -1;
+  if (token >= a.V) token = -1;
+  const float g = token >= 0 ? a.d_logprob[m] : 0.f;
+  token += row.lead;                      // its place (no other place counts when g is 0)
   const float h = a.d_entropy != nullptr && some ? a.d_entropy[m] : 0.f, H = h != 0.f ? a.entropy[m] : 0.f;
   const bool zero = g == 0.f && h == 0.f;
-  for (int j0 = (blockIdx.y * GU * LT + threadIdx.x) * 8; j0 < V; j0 += gridDim.y * GC) {
+  for (int j0 = (blockIdx.y * GU * LT + threadIdx.x) * 8; j0 < row.end; j0 += gridDim.y * GC) {
     Vec8<T> v[GU];
     if (!zero) {
 #pragma unroll
       for (int u = 0; u < GU; ++u)
-        if (j0 + u * LT * 8 < V) load_scores<T, VEC>(v[u], row, j0 + u * LT * 8, V, end);
+        if (j0 + u * LT * 8 < row.end) row.load(v[u], j0 + u * LT * 8);
     }
 #pragma unroll
     for (int u = 0; u < GU; ++u) {
       const int j = j0 + u * LT * 8;
-      if (j >= V) break;
+      if (j >= row.end) break;
       float f[8];
       if (zero) {
 #pragma unroll
@@ -376,34 +431,28 @@ __global__ void __launch_bounds__(LT) logprob_bwd_kernel(const LogprobBwdArgs a)
           f[i] = h != 0.f ? d - h * (p * (lp + H)) : d;
         }
       }
-      if (VEC && j + 8 <= V) {
+      if (vec && j >= row.lead && j + 8 <= row.end) {
         v[u].from_float(f);
         v[u].store(out + j);
       } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-          if (j + i < V) out[j + i] = from_f32<T>(f[i]);
+          if (j + i >= row.lead && j + i < row.end) out[j + i] = from_f32<T>(f[i]);
       }
     }
   }
 }
 
-template <typename T, bool VEC> cudaError_t logprob_vec(const LogprobArgs& a, dim3 grid, int cluster, cudaStream_t st) {
-  const bool ent = a.entropy != nullptr;
-  if (a.n_top > 0)
-    return ent ? launch_pdl(logprob_kernel<T, VEC, true, true>, grid, LT, 0, cluster, st, a)
-               : launch_pdl(logprob_kernel<T, VEC, false, true>, grid, LT, 0, cluster, st, a);
-  return ent ? launch_pdl(logprob_kernel<T, VEC, true, false>, grid, LT, 0, cluster, st, a)
-             : launch_pdl(logprob_kernel<T, VEC, false, false>, grid, LT, 0, cluster, st, a);
-}
-
 template <typename T> cudaError_t logprob(const LogprobArgs& a, int num_sms, cudaStream_t st) {
-  // Few rows: clusters, while the blocks stay within three on an SM and a slice keeps every thread at
+  // Few rows: clusters, while the blocks stay within four on an SM and a slice keeps every thread at
   // two vectors.
   int c = 1;
-  while (c < kMaxCluster && a.M * c * 2 <= 3 * num_sms && a.V > c * LT * 16) c *= 2;
+  while (c < kMaxCluster && a.M * c * 2 <= 4 * num_sms && a.V > c * LT * 16) c *= 2;
   const dim3 grid((unsigned)(a.M * c));
-  return a.M == 1 || a.ld % 8 == 0 ? logprob_vec<T, true>(a, grid, c, st) : logprob_vec<T, false>(a, grid, c, st);
+  const bool ent = a.entropy != nullptr;
+  if (a.n_top > 0)
+    return ent ? launch_pdl(logprob_kernel<T, true, true>, grid, LT, 0, c, st, a) : launch_pdl(logprob_kernel<T, false, true>, grid, LT, 0, c, st, a);
+  return ent ? launch_pdl(logprob_kernel<T, true, false>, grid, LT, 0, c, st, a) : launch_pdl(logprob_kernel<T, false, false>, grid, LT, 0, c, st, a);
 }
 
 template <typename T> cudaError_t logprob_bwd(const LogprobBwdArgs& a, int num_sms, cudaStream_t st) {
@@ -411,9 +460,7 @@ template <typename T> cudaError_t logprob_bwd(const LogprobBwdArgs& a, int num_s
   int64_t parts = (16 * num_sms + a.M - 1) / a.M;
   const int64_t most = (a.V + GC - 1) / GC;
   if (parts > most) parts = most;
-  const dim3 grid((unsigned)a.M, (unsigned)parts);
-  return a.M == 1 || (a.ld % 8 == 0 && a.ld_dx % 8 == 0) ? launch_pdl(logprob_bwd_kernel<T, true>, grid, LT, 0, 1, st, a)
-                                                         : launch_pdl(logprob_bwd_kernel<T, false>, grid, LT, 0, 1, st, a);
+  return launch_pdl(logprob_bwd_kernel<T>, dim3((unsigned)a.M, (unsigned)parts), LT, 0, 1, st, a);
 }
 
 }  // namespace

@@ -72,20 +72,6 @@ template <> struct Vec8<float> {
   }
 };
 
-// The 8 elements that begin at byte `at` % 16 of the 16-byte vectors in w.
-template <typename T> __device__ __forceinline__ void shifted8(Vec8<T>& r, uint32_t (&w)[2 * sizeof(T) + 4], uintptr_t at) {
-  constexpr int W = 2 * sizeof(T);   // 32-bit words of the 8 elements
-  if (at & 8)
-#pragma unroll
-    for (int i = 0; i < W + 2; ++i) w[i] = w[i + 2];
-  if (at & 4)
-#pragma unroll
-    for (int i = 0; i < W + 1; ++i) w[i] = w[i + 1];
-  uint32_t* out = reinterpret_cast<uint32_t*>(&r);
-#pragma unroll
-  for (int i = 0; i < W; ++i) out[i] = at & 2 ? __funnelshift_r(w[i], w[i + 1], 16) : w[i];
-}
-
 // 8 consecutive elements from an address that is aligned to the element only: the aligned 16-byte
 // vectors around them, shifted into place (element by element where those reach past `end`, the
 // tensor's end; its beginning is 16-byte aligned).
@@ -103,7 +89,15 @@ __device__ __forceinline__ void load8_unaligned(Vec8<T>& r, const T* p, const T*
       w[4 * i + 2] = v.z;
       w[4 * i + 3] = v.w;
     }
-    shifted8(r, w, at);
+    if (at & 8)
+#pragma unroll
+      for (int i = 0; i < W + 2; ++i) w[i] = w[i + 2];
+    if (at & 4)
+#pragma unroll
+      for (int i = 0; i < W + 1; ++i) w[i] = w[i + 1];
+    uint32_t* out = reinterpret_cast<uint32_t*>(&r);
+#pragma unroll
+    for (int i = 0; i < W; ++i) out[i] = at & 2 ? __funnelshift_r(w[i], w[i + 1], 16) : w[i];
   } else {
     T* out = reinterpret_cast<T*>(&r);
 #pragma unroll

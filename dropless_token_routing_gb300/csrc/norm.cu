@@ -8,8 +8,8 @@
 // A row stays on the SM between its sums and its way out, so every operand is read once; the
 // variance is that of the centred values (no difference of large numbers). All of it is bound by HBM.
 //
-// Rows of up to 8192 elements are taken by groups of warps, two vectors of 8 elements to a thread, in a
-// persistent block of up to 16 warps; wider ones by a block each. A thread copies its own vectors of the
+// Rows of up to 8192 elements are taken by groups of warps, 16 elements to a thread, in a
+// persistent block of up to 16 warps; wider ones by a block each. A thread copies its own elements of the
 // rows to come into its own places of shared memory (cp.async), several rows ahead, so that the loads of
 // a group go on through its barriers, and nobody waits for another thread's copies. The
 // columns being a thread's own for all its rows, the weight's gradient is summed in registers.
@@ -97,9 +97,9 @@ __device__ __forceinline__ float2 block_sums(float a, float b, float* s) {
 }
 
 // ------------------------------------------------------------------ rows of up to kRowsMaxN elements
-constexpr int kRowThreads = 512, kRowVecs = 2;   // most threads of a block; vectors of a thread
-constexpr int kRowsMaxN = kRowThreads * kRowVecs * 8;
-constexpr int kMaxStages = 6;
+constexpr int kRowThreads = 512, kRowElements = 16;   // most threads of a block; elements of a row that a thread holds
+constexpr int kRowsMaxN = kRowThreads * kRowElements;
+constexpr int kMaxStages = 8;
 constexpr int kRing = 200 * 1024;   // shared memory of an SM for the copies
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
@@ -118,105 +118,148 @@ __device__ __forceinline__ void cp_wait(int n) {
     case 2: asm volatile("cp.async.wait_group 2;" ::: "memory"); break;
     case 3: asm volatile("cp.async.wait_group 3;" ::: "memory"); break;
     case 4: asm volatile("cp.async.wait_group 4;" ::: "memory"); break;
-    default: asm volatile("cp.async.wait_group 5;" ::: "memory"); break;
+    case 5: asm volatile("cp.async.wait_group 5;" ::: "memory"); break;
+    case 6: asm volatile("cp.async.wait_group 6;" ::: "memory"); break;
+    default: asm volatile("cp.async.wait_group 7;" ::: "memory"); break;
   }
 }
 
-template <typename V> __device__ __forceinline__ void to_pairs(const V& v, uint64_t (&f)[4]) {
-  float g[8];
-  v.to_float(g);
-#pragma unroll
-  for (int j = 0; j < 4; ++j) f[j] = pack2(g[2 * j], g[2 * j + 1]);
+__device__ __forceinline__ void word_floats(uint32_t w, float& lo, float& hi) {   // two bf16
+  lo = __uint_as_float(w << 16);
+  hi = __uint_as_float(w & 0xffff0000u);
 }
-template <typename V> __device__ __forceinline__ void from_pairs(V& v, const uint64_t (&f)[4]) {
+// 16 bytes of T as pairs, and back (rounded).
+__device__ __forceinline__ void unit_pairs(const uint4& v, uint64_t (&f)[2], float) {
+  f[0] = pack2(__uint_as_float(v.x), __uint_as_float(v.y));
+  f[1] = pack2(__uint_as_float(v.z), __uint_as_float(v.w));
+}
+__device__ __forceinline__ void unit_pairs(const uint4& v, uint64_t (&f)[4], __nv_bfloat16) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    float lo, hi;
+    word_floats(w[j], lo, hi);
+    f[j] = pack2(lo, hi);
+  }
+}
+__device__ __forceinline__ uint4 pairs_unit(const uint64_t (&f)[2], float) {
+  float v[4];
+  unpack2(f[0], v[0], v[1]);
+  unpack2(f[1], v[2], v[3]);
+  return make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+}
+__device__ __forceinline__ uint4 pairs_unit(const uint64_t (&f)[4], __nv_bfloat16) {
+  Vec8<__nv_bfloat16> v;
   float g[8];
 #pragma unroll
   for (int j = 0; j < 4; ++j) unpack2(f[j], g[2 * j], g[2 * j + 1]);
   v.from_float(g);
+  return v.v;
+}
+// The 16 bytes that begin `skip` bytes into two pieces (skip a multiple of 2).
+__device__ __forceinline__ uint4 window(const uint4& a, const uint4& b, uint32_t skip) {
+  uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+  if (skip & 8)
+#pragma unroll
+    for (int i = 0; i < 6; ++i) w[i] = w[i + 2];
+  if (skip & 4)
+#pragma unroll
+    for (int i = 0; i < 5; ++i) w[i] = w[i + 1];
+  if (skip & 2)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], 16);
+  return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// A thread's place for one vector of 8 elements: 16-byte pieces, a block's threads side by side. Without
-// VEC (rows on 16-byte boundaries) a vector's pieces are the aligned ones around it, one more than its own
-// size. FULL: all of a group's vectors are whole ones (widths of 512 times its warps), which saves every
+// A thread's weights for a unit of kIn elements of the row, as they are in memory.
+template <typename W, int kIn> struct Weights {
+  uint4 v[kIn * sizeof(W) / 16];
+  __device__ __forceinline__ void load(const W* p, int n) {
+    if (n >= kIn) {
+#pragma unroll
+      for (int q = 0; q < (int)(kIn * sizeof(W) / 16); ++q) v[q] = reinterpret_cast<const uint4*>(p)[q];
+    } else {
+      W* e = reinterpret_cast<W*>(v);
+#pragma unroll
+      for (int i = 0; i < kIn; ++i) e[i] = i < n ? p[i] : W(0.f);
+    }
+  }
+  __device__ __forceinline__ void pairs(uint64_t (&f)[kIn / 2]) const {
+    if constexpr (sizeof(W) == 4) {
+      const float* e = reinterpret_cast<const float*>(v);
+#pragma unroll
+      for (int j = 0; j < kIn / 2; ++j) f[j] = pack2(e[2 * j], e[2 * j + 1]);
+    } else {
+      unit_pairs(v[0], f, W());
+    }
+  }
+};
+
+// A thread's units of a row are 16 bytes each, neighbouring threads' side by side, in the row as in shared
+// memory. UNALIGNED (some row does not start on a 16-byte boundary): a unit's copy is the two aligned pieces
+// around it. FULL: all units of a group are whole ones (widths of 512 times its warps), which saves every
 // test for a row's end (8192 x 7680, two blocks on an SM: 95 us forward with them, 91 without).
 enum RowMode { UNALIGNED = 0, ALIGNED = 1, FULL = 2 };
-template <typename T, int MODE> struct Place {
-  static constexpr bool VEC = MODE != UNALIGNED;
-  static constexpr int kPieces = sizeof(T) / 2 + (VEC ? 0 : 1);
-  // p: the vector's first element; n: elements of the row from there on; end: the tensor's
+template <typename T, int MODE> struct Unit {
+  static constexpr int kIn = 16 / sizeof(T), kPairs = kIn / 2, kUnits = kRowElements / kIn;   // elements; pairs; of a thread
+  static constexpr int kPieces = MODE == UNALIGNED ? 2 : 1;
+  // p: the unit's first element; n: elements of the row from there on; end: the tensor's
   static __device__ __forceinline__ void copy(uint32_t at, const T* p, int n, const T* end) {
-    if (MODE == FULL || (VEC && n >= 8)) {
+    if (MODE == FULL || (MODE == ALIGNED && n >= kIn)) {
+      cp_async16(at, p);
+    } else if (MODE == ALIGNED) {
+      cp_async16(at, p, n * (int)sizeof(T));
+    } else {
+      const uintptr_t from = reinterpret_cast<uintptr_t>(p) & ~uintptr_t(15);
+      const int64_t there = (int64_t)(reinterpret_cast<uintptr_t>(end) - from);   // up to the tensor's end
 #pragma unroll
-      for (int q = 0; q < kPieces; ++q) cp_async16(at + q * blockDim.x * 16, p + q * (16 / sizeof(T)));
-      return;
-    }
-    const uintptr_t from = VEC ? reinterpret_cast<uintptr_t>(p) : reinterpret_cast<uintptr_t>(p) & ~uintptr_t(15);
-    // what there is: the row's elements, or all up to the tensor's end
-    const int64_t there = VEC ? n * (int)sizeof(T) : (int64_t)(reinterpret_cast<uintptr_t>(end) - from);
-#pragma unroll
-    for (int q = 0; q < kPieces; ++q) {
-      const int64_t left = there - 16 * q;
-      const int bytes = left >= 16 ? 16 : left > 0 ? (int)left : 0;
-      cp_async16(at + q * blockDim.x * 16, reinterpret_cast<const void*>(bytes > 0 ? from + 16 * q : from), bytes);
+      for (int q = 0; q < 2; ++q) {
+        const int64_t left = there - 16 * q;
+        const int bytes = left >= 16 ? 16 : left > 0 ? (int)left : 0;
+        cp_async16(at + q * blockDim.x * 16, reinterpret_cast<const void*>(bytes > 0 ? from + 16 * q : from), bytes);
+      }
     }
   }
-  // The vector as four pairs; elements that the row has not (n < 8) are 0.
-  static __device__ __forceinline__ void read(uint64_t (&f)[4], const uint4* at, const T* row, int c, int n) {
-    Vec8<T> v;
-    if constexpr (VEC) {
-      uint4* d = reinterpret_cast<uint4*>(&v);
-#pragma unroll
-      for (int q = 0; q < kPieces; ++q) d[q] = at[q * blockDim.x];
+  // As pairs; elements that the row has not (n < kIn) are 0.
+  static __device__ __forceinline__ void read(uint64_t (&f)[kPairs], const uint4* at, const T* p, int n) {
+    if constexpr (MODE == UNALIGNED) {
+      unit_pairs(window(at[0], at[blockDim.x], (uint32_t)(reinterpret_cast<uintptr_t>(p) & 15)), f, T());
+      if (n < kIn) keep(f, n);
     } else {
-      uint32_t w[4 * kPieces];
-#pragma unroll
-      for (int q = 0; q < kPieces; ++q) {
-        const uint4 d = at[q * blockDim.x];
-        w[4 * q] = d.x;
-        w[4 * q + 1] = d.y;
-        w[4 * q + 2] = d.z;
-        w[4 * q + 3] = d.w;
-      }
-      shifted8(v, w, reinterpret_cast<uintptr_t>(row + c));
+      unit_pairs(at[0], f, T());
     }
-    to_pairs(v, f);
-    if (!VEC && n < 8) keep(f, n);
   }
-  // A vector's way out. Without VEC the warp's 32 vectors, which lie side by side in the row, are put in order in
-  // their first pieces (the lane's is at `at`; its operand has been read) and go out with
-  // neighbouring elements in neighbouring lanes: every lane of the warp takes part.
-  static __device__ __forceinline__ void write(const uint64_t (&f)[4], uint4* at, T* row, int c, int n) {
-    Vec8<T> v;
-    from_pairs(v, f);
-    if constexpr (VEC) {
-      if (MODE == FULL || n >= 8) {
-        v.store(row + c);
-      } else {
-        const T* e = reinterpret_cast<const T*>(&v);
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          if (i < n) row[c + i] = e[i];
-      }
-    } else {
-      constexpr int kIn = 16 / sizeof(T);   // elements of a piece
+  // Its way out to p. UNALIGNED: the warp's 32 units go through their first pieces (the lane's is at `at`; its
+  // operand has been read) into whole vectors at the row's own 16-byte boundaries, and single elements at both
+  // ends; every lane of the warp takes part.
+  static __device__ __forceinline__ void write(const uint64_t (&f)[kPairs], uint4* at, T* p, int n) {
+    const uint4 v = pairs_unit(f, T());
+    if constexpr (MODE == UNALIGNED) {
       const int lane = threadIdx.x & 31;
-      const uint4* d = reinterpret_cast<const uint4*>(&v);
-#pragma unroll
-      for (int q = 0; q < kPieces - 1; ++q) at[q * blockDim.x] = d[q];
+      at[0] = v;
       __syncwarp();
-      const T* first = reinterpret_cast<const T*>(at - lane);
-      const int c0 = c - lane * 8, left = n + lane * 8;
-#pragma unroll
-      for (int s = 0; s < 8; ++s) {
-        const int e = s * 32 + lane;
-        if (e < left) row[c0 + e] = first[(e / kIn % (kPieces - 1)) * (int)blockDim.x * kIn + e / 8 * kIn + e % kIn];
-      }
+      const uint4* seg = at - lane;
+      T* first = p - lane * kIn;
+      const int left = n + lane * kIn, bytes = (left < 32 * kIn ? left : 32 * kIn) * (int)sizeof(T);   // of the warp's segment
+      const int skip = (int)((16 - (reinterpret_cast<uintptr_t>(first) & 15)) & 15), at16 = skip + 16 * lane;
+      if (at16 + 16 <= bytes) *reinterpret_cast<uint4*>(reinterpret_cast<char*>(first) + at16) = window(seg[lane], seg[skip ? lane + 1 : lane], skip);
+      // lanes 0 to 7: elements before the first boundary, 8 to 15: behind the last whole vector
+      const int tail = bytes > skip ? skip + ((bytes - skip) & ~15) : skip;   // (a segment may end before the boundary)
+      const int e = lane < 8 ? lane : tail / (int)sizeof(T) + lane - 8, stop = lane < 8 ? (skip < bytes ? skip : bytes) : bytes;
+      if (lane < 16 && e * (int)sizeof(T) < stop) first[e] = reinterpret_cast<const T*>(seg)[e];
       __syncwarp();
+    } else if (MODE == FULL || n >= kIn) {
+      *reinterpret_cast<uint4*>(p) = v;
+    } else {
+      const T* e = reinterpret_cast<const T*>(&v);
+#pragma unroll
+      for (int i = 0; i < kIn; ++i)
+        if (i < n) p[i] = e[i];
     }
   }
-  static __device__ __forceinline__ void keep(uint64_t (&f)[4], int n) {
+  static __device__ __forceinline__ void keep(uint64_t (&f)[kPairs], int n) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < kPairs; ++j) {
       float lo, hi;
       unpack2(f[j], lo, hi);
       f[j] = pack2(2 * j < n ? lo : 0.f, 2 * j + 1 < n ? hi : 0.f);
@@ -253,26 +296,27 @@ template <typename T, typename W, int MODE, bool RES>
 __global__ void __launch_bounds__(kRowThreads, 1) norm_fwd_rows(const NormArgs a, int warps, int stages) {
   extern __shared__ uint4 ring[];
   __shared__ float2 s_sums[2][16];
-  using P = Place<T, MODE>;
-  constexpr int kOps = RES ? 2 : 1, kStep = kOps * kRowVecs * P::kPieces;   // places of a stage
+  using P = Unit<T, MODE>;
+  constexpr int kIn = P::kIn, kUnits = P::kUnits, kPairs = P::kPairs, kOp = kUnits * P::kPieces, kStep = (1 + RES) * kOp;
   pdl_start();
   const int N = a.N, gt = warps * 32, groups = blockDim.x / gt, tg = threadIdx.x % gt;
   const Group group = {(int)threadIdx.x / gt, warps};
   const int64_t step = (int64_t)gridDim.x * groups;
-  const T *x0 = static_cast<const T*>(a.x), *r0 = static_cast<const T*>(a.res);
+  const int c0 = tg * kIn, n0 = N - c0, next_unit = gt * kIn;   // this thread's first column, elements from there on
+  const T *x0 = static_cast<const T*>(a.x) + c0, *r0 = RES ? static_cast<const T*>(a.res) + c0 : nullptr;
   const T *x_end = end_of<T>(a.x, a.M, a.ld_x, N), *r_end = RES ? end_of<T>(a.res, a.M, a.ld_res, N) : nullptr;
   pdl_wait();
   int64_t next = (int64_t)blockIdx.x * groups + group.index;
-  const T *xp = x0 + next * a.ld_x + tg * 8, *rp = r0 + next * a.ld_res + tg * 8;   // this thread's part of row `next`
-  const int n0 = N - tg * 8;
+  const T *xp = x0 + next * a.ld_x, *rp = RES ? r0 + next * a.ld_res : nullptr;   // row `next`
   auto fetch = [&](int stage) {
     if (next < a.M) {
       const uint32_t at = smem_u32(ring + stage * kStep * blockDim.x + threadIdx.x);
 #pragma unroll
-      for (int i = 0; i < kRowVecs; ++i) {
-        if (MODE == FULL || i * gt * 8 < n0) {
-          P::copy(at + i * P::kPieces * blockDim.x * 16, xp + i * gt * 8, n0 - i * gt * 8, x_end);
-          if (RES) P::copy(at + (kRowVecs + i) * P::kPieces * blockDim.x * 16, rp + i * gt * 8, n0 - i * gt * 8, r_end);
+      for (int i = 0; i < kUnits; ++i) {
+        const int n = n0 - i * next_unit;
+        if (MODE == FULL || n > 0) {
+          P::copy(at + i * P::kPieces * blockDim.x * 16, xp + i * next_unit, n, x_end);
+          if (RES) P::copy(at + (kOp + i * P::kPieces) * blockDim.x * 16, rp + i * next_unit, n, r_end);
         }
       }
     }
@@ -282,65 +326,66 @@ __global__ void __launch_bounds__(kRowThreads, 1) norm_fwd_rows(const NormArgs a
     cp_commit();
   };
   for (int s = 0; s + 1 < stages; ++s) fetch(s);
-  Vec8<W> w[kRowVecs], b[kRowVecs];
+  Weights<W, kIn> w[kUnits], b[kUnits];
 #pragma unroll
-  for (int i = 0; i < kRowVecs; ++i) {
-    const int c = (tg + i * gt) * 8;
-    if (MODE == FULL || c < N) {
-      load_row<W, true>(w[i], static_cast<const W*>(a.w), c, N - c, nullptr);
-      if (a.b != nullptr) load_row<W, true>(b[i], static_cast<const W*>(a.b), c, N - c, nullptr);
+  for (int i = 0; i < kUnits; ++i) {
+    const int n = n0 - i * next_unit;
+    if (MODE == FULL || n > 0) {
+      w[i].load(static_cast<const W*>(a.w) + c0 + i * next_unit, n);
+      if (a.b != nullptr) b[i].load(static_cast<const W*>(a.b) + c0 + i * next_unit, n);
     }
   }
   int stage = 0;
   for (int64_t m = (int64_t)blockIdx.x * groups + group.index; m < a.M; m += step) {
     fetch(stage == 0 ? stages - 1 : stage - 1);   // (the row before was taken from there)
     cp_wait(stages - 1);
-    uint4* at = ring + (size_t)stage * kStep * blockDim.x + threadIdx.x;
+    uint4* at = ring + stage * kStep * blockDim.x + threadIdx.x;
     if (++stage == stages) stage = 0;
-    uint64_t f[kRowVecs][4];
+    uint64_t f[kUnits][kPairs];
     uint64_t t = 0;
 #pragma unroll
-    for (int i = 0; i < kRowVecs; ++i) {
-      const int c = (tg + i * gt) * 8, n = N - c;
+    for (int i = 0; i < kUnits; ++i) {
+      const int n = n0 - i * next_unit;
       uint4* place = at + i * P::kPieces * blockDim.x;
       if (MODE == FULL || n > 0) {
-        P::read(f[i], place, x0 + m * a.ld_x, c, n);
+        P::read(f[i], place, x0 + m * a.ld_x + i * next_unit, n);
         if (RES) {
-          uint64_t g[4];
-          P::read(g, at + (kRowVecs + i) * P::kPieces * blockDim.x, r0 + m * a.ld_res, c, n);
+          uint64_t g[kPairs];
+          P::read(g, place + kOp * blockDim.x, r0 + m * a.ld_res + i * next_unit, n);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) f[i][j] = add2(f[i][j], g[j]);
+          for (int j = 0; j < kPairs; ++j) f[i][j] = add2(f[i][j], g[j]);
         }
       } else {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) f[i][j] = 0;
+        for (int j = 0; j < kPairs; ++j) f[i][j] = 0;
       }
-      if (RES && a.sum != nullptr && (MODE != ALIGNED || n > 0)) P::write(f[i], place, static_cast<T*>(a.sum) + m * a.ld_sum, c, n);
+      if (RES && a.sum != nullptr && (MODE != ALIGNED || n > 0))
+        P::write(f[i], place, static_cast<T*>(a.sum) + m * a.ld_sum + c0 + i * next_unit, n);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) t = add2(t, f[i][j]);
+      for (int j = 0; j < kPairs; ++j) t = add2(t, f[i][j]);
     }
     const float mean = group.sums<false>(sum2(t), 0.f, s_sums[0]).x * a.inv_n;
     t = 0;
 #pragma unroll
-    for (int i = 0; i < kRowVecs; ++i) {
-      const int n = N - (tg + i * gt) * 8;
+    for (int i = 0; i < kUnits; ++i) {
+      const int n = n0 - i * next_unit;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) f[i][j] = add2(f[i][j], both(-mean));
-      if (MODE != FULL && n < 8) P::keep(f[i], n);
+      for (int j = 0; j < kPairs; ++j) f[i][j] = add2(f[i][j], both(-mean));
+      if (MODE != FULL && n < kIn) P::keep(f[i], n);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) t = fma2(f[i][j], f[i][j], t);
+      for (int j = 0; j < kPairs; ++j) t = fma2(f[i][j], f[i][j], t);
     }
     const float rstd = 1.f / sqrtf(group.sums<false>(sum2(t), 0.f, s_sums[1]).x * a.inv_n + a.eps);
     if (tg == 0 && a.stats != nullptr) reinterpret_cast<float2*>(a.stats)[m] = make_float2(mean, rstd);
 #pragma unroll
-    for (int i = 0; i < kRowVecs; ++i) {
-      const int c = (tg + i * gt) * 8, n = N - c;
-      uint64_t g[4], h[4] = {0, 0, 0, 0};
-      to_pairs(w[i], g);
-      if (a.b != nullptr) to_pairs(b[i], h);
+    for (int i = 0; i < kUnits; ++i) {
+      const int n = n0 - i * next_unit;
+      uint64_t g[kPairs], h[kPairs] = {};
+      w[i].pairs(g);
+      if (a.b != nullptr) b[i].pairs(h);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) g[j] = fma2(f[i][j], mul2(g[j], both(rstd)), h[j]);
-      if (MODE != ALIGNED || n > 0) P::write(g, at + i * P::kPieces * blockDim.x, static_cast<T*>(a.y) + m * a.ld_y, c, n);
+      for (int j = 0; j < kPairs; ++j) g[j] = fma2(f[i][j], mul2(g[j], both(rstd)), h[j]);
+      if (MODE != ALIGNED || n > 0) P::write(g, at + i * P::kPieces * blockDim.x, static_cast<T*>(a.y) + m * a.ld_y + c0 + i * next_unit, n);
     }
   }
   cp_wait(0);
@@ -351,33 +396,33 @@ template <typename T, typename W, int MODE, bool RES, bool DS>
 __global__ void __launch_bounds__(kRowThreads, 1) norm_bwd_rows(const NormBwdArgs a, int warps, int stages) {
   extern __shared__ uint4 ring[];
   __shared__ float2 s_sums[2][16];
-  using P = Place<T, MODE>;
-  constexpr int kOps = 2 + RES + DS, kOp = kRowVecs * P::kPieces;
+  using P = Unit<T, MODE>;
+  constexpr int kIn = P::kIn, kUnits = P::kUnits, kPairs = P::kPairs, kOp = kUnits * P::kPieces, kOps = 2 + RES + DS;
   pdl_start();
   const int N = a.N, gt = warps * 32, groups = blockDim.x / gt, tg = threadIdx.x % gt;
   const Group group = {(int)threadIdx.x / gt, warps};
   const int64_t step = (int64_t)gridDim.x * groups;
-  const T* base[4] = {static_cast<const T*>(a.x), static_cast<const T*>(a.dy), static_cast<const T*>(RES ? a.res : a.d_sum),
-                      static_cast<const T*>(a.d_sum)};
+  const int c0 = tg * kIn, n0 = N - c0, next_unit = gt * kIn;   // this thread's first column, elements from there on
+  const void* const operand[4] = {a.x, a.dy, RES ? a.res : a.d_sum, a.d_sum};
   const int64_t ld[4] = {a.ld_x, a.ld_dy, RES ? a.ld_res : a.ld_ds, a.ld_ds};
   pdl_wait();
   int64_t next = (int64_t)blockIdx.x * groups + group.index;
-  const T *p[kOps], *end[kOps];   // this thread's parts of row `next`
+  const T *base[kOps], *p[kOps], *end[kOps];   // this thread's part of row 0 and of row `next`
 #pragma unroll
   for (int o = 0; o < kOps; ++o) {
-    p[o] = base[o] + next * ld[o] + tg * 8;
-    end[o] = end_of<T>(base[o], a.M, ld[o], N);
+    base[o] = static_cast<const T*>(operand[o]) + c0;
+    p[o] = base[o] + next * ld[o];
+    end[o] = end_of<T>(operand[o], a.M, ld[o], N);
   }
-  const int n0 = N - tg * 8;
   auto fetch = [&](int stage) {
     if (next < a.M) {
       const uint32_t at = smem_u32(ring + stage * kOps * kOp * blockDim.x + threadIdx.x);
 #pragma unroll
-      for (int i = 0; i < kRowVecs; ++i) {
-        if (MODE == FULL || i * gt * 8 < n0) {
+      for (int i = 0; i < kUnits; ++i) {
+        const int n = n0 - i * next_unit;
+        if (MODE == FULL || n > 0) {
 #pragma unroll
-          for (int o = 0; o < kOps; ++o)
-            P::copy(at + (o * kOp + i * P::kPieces) * blockDim.x * 16, p[o] + i * gt * 8, n0 - i * gt * 8, end[o]);
+          for (int o = 0; o < kOps; ++o) P::copy(at + (o * kOp + i * P::kPieces) * blockDim.x * 16, p[o] + i * next_unit, n, end[o]);
         }
       }
     }
@@ -387,14 +432,14 @@ __global__ void __launch_bounds__(kRowThreads, 1) norm_bwd_rows(const NormBwdArg
     cp_commit();
   };
   for (int s = 0; s + 1 < stages; ++s) fetch(s);
-  Vec8<W> w[kRowVecs];
-  uint64_t dw[kRowVecs][4], db[kRowVecs][4];
+  Weights<W, kIn> w[kUnits];
+  uint64_t dw[kUnits][kPairs], db[kUnits][kPairs];
 #pragma unroll
-  for (int i = 0; i < kRowVecs; ++i) {
-    const int c = (tg + i * gt) * 8;
-    if (c < N && a.dx != nullptr) load_row<W, true>(w[i], static_cast<const W*>(a.w), c, N - c, nullptr);
+  for (int i = 0; i < kUnits; ++i) {
+    const int n = n0 - i * next_unit;
+    if ((MODE == FULL || n > 0) && a.dx != nullptr) w[i].load(static_cast<const W*>(a.w) + c0 + i * next_unit, n);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) dw[i][j] = db[i][j] = 0;
+    for (int j = 0; j < kPairs; ++j) dw[i][j] = db[i][j] = 0;
   }
   int stage = 0, buf = 0;
   int64_t m = (int64_t)blockIdx.x * groups + group.index;
@@ -404,26 +449,27 @@ __global__ void __launch_bounds__(kRowThreads, 1) norm_bwd_rows(const NormBwdArg
     if (m + step < a.M) coming = reinterpret_cast<const float2*>(a.stats)[m + step];
     fetch(stage == 0 ? stages - 1 : stage - 1);
     cp_wait(stages - 1);
-    uint4* at = ring + (size_t)stage * kOps * kOp * blockDim.x + threadIdx.x;
+    uint4* at = ring + stage * kOps * kOp * blockDim.x + threadIdx.x;
     if (++stage == stages) stage = 0;
-    uint64_t u[kRowVecs][4], xh[kRowVecs][4];
+    uint64_t u[kUnits][kPairs], xh[kUnits][kPairs];
     uint64_t t = 0, tx = 0;
 #pragma unroll
-    for (int i = 0; i < kRowVecs; ++i) {
-      const int c = (tg + i * gt) * 8, n = N - c;
+    for (int i = 0; i < kUnits; ++i) {
+      const int n = n0 - i * next_unit;
+      const uint4* place = at + i * P::kPieces * blockDim.x;
       if (MODE == FULL || n > 0) {
-        P::read(xh[i], at + i * P::kPieces * blockDim.x, base[0] + m * ld[0], c, n);
-        P::read(u[i], at + (kOp + i * P::kPieces) * blockDim.x, base[1] + m * ld[1], c, n);
-        uint64_t g[4];
+        P::read(xh[i], place, base[0] + m * ld[0] + i * next_unit, n);
+        P::read(u[i], place + kOp * blockDim.x, base[1] + m * ld[1] + i * next_unit, n);
+        uint64_t g[kPairs];
         if (RES) {
-          P::read(g, at + (2 * kOp + i * P::kPieces) * blockDim.x, base[2] + m * ld[2], c, n);
+          P::read(g, place + 2 * kOp * blockDim.x, base[2] + m * ld[2] + i * next_unit, n);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) xh[i][j] = add2(xh[i][j], g[j]);
+          for (int j = 0; j < kPairs; ++j) xh[i][j] = add2(xh[i][j], g[j]);
         }
-        to_pairs(w[i], g);
+        w[i].pairs(g);
         // (past the row's end u is 0, and with it all that is added)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+        for (int j = 0; j < kPairs; ++j) {
           xh[i][j] = mul2(add2(xh[i][j], both(-st.x)), both(st.y));
           db[i][j] = add2(db[i][j], u[i][j]);
           dw[i][j] = fma2(u[i][j], xh[i][j], dw[i][j]);
@@ -438,32 +484,33 @@ __global__ void __launch_bounds__(kRowThreads, 1) norm_bwd_rows(const NormBwdArg
     buf ^= 1;
     const uint64_t c1 = both(-c12.x * a.inv_n), c2 = both(-c12.y * a.inv_n), rstd = both(st.y);
 #pragma unroll
-    for (int i = 0; i < kRowVecs; ++i) {
-      const int c = (tg + i * gt) * 8, n = N - c;
-      uint64_t g[4] = {0, 0, 0, 0};
+    for (int i = 0; i < kUnits; ++i) {
+      const int n = n0 - i * next_unit;
+      uint4* place = at + i * P::kPieces * blockDim.x;
+      uint64_t g[kPairs] = {};
       if (MODE == FULL || n > 0) {
-        if (DS) P::read(g, at + ((kOps - 1) * kOp + i * P::kPieces) * blockDim.x, base[kOps - 1] + m * ld[kOps - 1], c, n);
+        if (DS) P::read(g, place + (kOps - 1) * kOp * blockDim.x, base[kOps - 1] + m * ld[kOps - 1] + i * next_unit, n);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) g[j] = fma2(rstd, fma2(xh[i][j], c2, add2(u[i][j], c1)), g[j]);
+        for (int j = 0; j < kPairs; ++j) g[j] = fma2(rstd, fma2(xh[i][j], c2, add2(u[i][j], c1)), g[j]);
       }
-      if (MODE != ALIGNED || n > 0) P::write(g, at + i * P::kPieces * blockDim.x, static_cast<T*>(a.dx) + m * a.ld_dx, c, n);
+      if (MODE != ALIGNED || n > 0) P::write(g, place, static_cast<T*>(a.dx) + m * a.ld_dx + c0 + i * next_unit, n);
     }
   }
   cp_wait(0);
   if (a.dw == nullptr && a.db == nullptr) return;
   // the groups' sums, added in order: [group][dw, db][column], then a block's partial sums
   __syncthreads();
-  ulonglong2* mine = reinterpret_cast<ulonglong2*>(ring) + ((size_t)group.index * 2 * gt * kRowVecs + tg) * 2;
+  const int cols = gt * kRowElements;
+  float* mine = reinterpret_cast<float*>(ring) + group.index * 2 * cols + c0;
 #pragma unroll
-  for (int i = 0; i < kRowVecs; ++i)
+  for (int i = 0; i < kUnits; ++i)
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      mine[i * gt * 2 + h] = make_ulonglong2(dw[i][2 * h], dw[i][2 * h + 1]);
-      mine[(kRowVecs + i) * gt * 2 + h] = make_ulonglong2(db[i][2 * h], db[i][2 * h + 1]);
+    for (int h = 0; h < kPairs / 2; ++h) {
+      *reinterpret_cast<ulonglong2*>(mine + i * next_unit + 4 * h) = make_ulonglong2(dw[i][2 * h], dw[i][2 * h + 1]);
+      *reinterpret_cast<ulonglong2*>(mine + cols + i * next_unit + 4 * h) = make_ulonglong2(db[i][2 * h], db[i][2 * h + 1]);
     }
   __syncthreads();
   const float* all = reinterpret_cast<const float*>(ring);
-  const int cols = gt * kRowVecs * 8;
 #pragma unroll
   for (int k = 0; k < 2; ++k)
     for (int c = threadIdx.x; c < N; c += blockDim.x) {
@@ -476,13 +523,13 @@ __global__ void __launch_bounds__(kRowThreads, 1) norm_bwd_rows(const NormBwdArg
 // Warps of a group and groups of a block for rows of N elements: no more groups than rows for an SM.
 struct RowShape {
   int warps, groups;
-  RowShape(int N, int64_t M, int num_sms) : warps((N + 64 * 8 - 1) / (64 * 8)), groups(kRowThreads / 32 / warps) {
+  RowShape(int N, int64_t M, int num_sms) : warps((N + 32 * kRowElements - 1) / (32 * kRowElements)), groups(kRowThreads / 32 / warps) {
     const int64_t rows = (M + num_sms - 1) / num_sms;
     if (groups > rows) groups = (int)rows;
   }
   int threads() const { return warps * groups * 32; }
   // vec: every row starts on a 16-byte boundary
-  static RowMode mode(int N, bool vec) { return !vec ? UNALIGNED : N % 512 == 0 ? FULL : ALIGNED; }
+  static RowMode mode(int N, bool vec) { return !vec ? UNALIGNED : N % (32 * kRowElements) == 0 ? FULL : ALIGNED; }
 };
 
 // ------------------------------------------------------------------ wide rows
@@ -714,7 +761,7 @@ struct RowLaunch {
 };
 
 template <typename T, typename W, int MODE, bool RES> cudaError_t fwd_rows(const NormArgs& a, int num_sms, cudaStream_t st) {
-  const RowLaunch l(a.M, RowShape(a.N, a.M, num_sms), 16 * (1 + RES) * kRowVecs * Place<T, MODE>::kPieces, 0, num_sms);
+  const RowLaunch l(a.M, RowShape(a.N, a.M, num_sms), 16 * (1 + RES) * Unit<T, MODE>::kUnits * Unit<T, MODE>::kPieces, 0, num_sms);
   const cudaError_t e = allow_ring<norm_fwd_rows<T, W, MODE, RES>>(kRing);
   if (e != cudaSuccess) return e;
   return launch_pdl(norm_fwd_rows<T, W, MODE, RES>, dim3(l.grid), l.threads, l.smem, 1, st, a, l.warps, l.stages);
@@ -738,8 +785,8 @@ template <typename T, typename W> cudaError_t norm_fwd(const NormArgs& a, int nu
 
 template <typename T, typename W, int MODE, bool RES, bool DS>
 cudaError_t bwd_rows(const NormBwdArgs& a, int num_sms, int* parts, cudaStream_t st) {
-  const RowLaunch l(a.M, RowShape(a.N, a.M, num_sms), 16 * (2 + RES + DS) * kRowVecs * Place<T, MODE>::kPieces, 2 * kRowVecs * 8 * 4,
-                    num_sms);
+  const RowLaunch l(a.M, RowShape(a.N, a.M, num_sms), 16 * (2 + RES + DS) * Unit<T, MODE>::kUnits * Unit<T, MODE>::kPieces,
+                    2 * kRowElements * 4, num_sms);
   const cudaError_t e = allow_ring<norm_bwd_rows<T, W, MODE, RES, DS>>(kRing);
   if (e != cudaSuccess) return e;
   *parts = l.grid;

@@ -27,7 +27,6 @@ STATUS = {
     0: "MOE_OK", -1: "MOE_ERR_NULL_POINTER", -2: "MOE_ERR_MISALIGNED", -3: "MOE_ERR_BAD_DIMS",
     -4: "MOE_ERR_BAD_TOPK", -5: "MOE_ERR_UNSUPPORTED_DTYPE", -6: "MOE_ERR_WORKSPACE_TOO_SMALL",
     -7: "MOE_ERR_LAUNCH", -8: "MOE_ERR_CUDA", -9: "MOE_ERR_UNSUPPORTED_DEVICE",
-    -10: "MOE_ERR_OVERLAP",
     -100: "MOE_ERR_DEVICE_EXPERT_ID", -101: "MOE_ERR_DEVICE_TIMEOUT",
 }
 STATUS_CODE = {v: k for k, v in STATUS.items()}

@@ -697,17 +697,22 @@ class LayerNorm:
         self.dtype, self.w_dtype = dtype if dtype is not None else weight.dtype, weight.dtype
         (self.N,) = weight.shape
         self.device, self._index = _device(device if device is not None else weight.device)
-        self.dims = N.NormDims(int(max_rows), self.N, _dt(self.dtype), _dt(self.w_dtype), eps, 0, 0, 0, 0, 0)
+        self._size = torch.empty(0, dtype=self.dtype).element_size()
+        # one for each direction: a call sets what has changed since its last one
+        self.dims, self._bwd_dims = (N.NormDims(int(max_rows), self.N, _dt(self.dtype), _dt(self.w_dtype), eps, 0, 0, 0, 0, 0)
+                                     for _ in range(2))
+        self._set, self._bwd_set = None, None
         self._bind()
-        self.ws = None
-        if N.lib().moe_norm_workspace_bytes(ctypes.byref(self.dims)) == 0:
+        self._need = N.lib().moe_norm_workspace_bytes(ctypes.byref(self.dims))
+        if self._need == 0:
             raise N.MoeError(N.STATUS_CODE["MOE_ERR_BAD_DIMS"], "moe_norm_workspace_bytes")
-        self._bufs, self._views, self._s = {}, {}, None
-        self._dims_ref = ctypes.byref(self.dims)
+        self.ws = None
+        self._bufs, self._views, self._kept = {}, {}, None
+        self._dims_ref, self._bwd_ref = ctypes.byref(self.dims), ctypes.byref(self._bwd_dims)
         self._fwd, self._bwd = N.lib().moe_norm_fwd, N.lib().moe_norm_bwd
 
     def _bind(self):
-        self._w_ref = lambda: None      # nothing, should a check fail
+        self._w_ref = lambda: self      # none of them, should a check fail
         _dense(self.weight, "weight", self.w_dtype, (self.N,), self.device)
         if self.bias is not None:
             _dense(self.bias, "bias", self.w_dtype, (self.N,), self.device)
@@ -715,103 +720,128 @@ class LayerNorm:
         self._w_ref, self._b_ref = _ref(self.weight), _ref(self.bias)
 
     def _view(self, name, M, stream):
-        """The first M rows of the layer's buffer ``name`` (made at its first use, of the call's stream), and
-        its address."""
-        v = self._views.get((name, M))
-        if v is None:
-            t = self._bufs.get(name)
-            if t is None:
-                shape, dt = {"stats": ((self.max_rows, 2), torch.float32), "dw": ((1, self.N), self.w_dtype),
-                             "db": ((1, self.N), self.w_dtype)}.get(name, ((self.max_rows, self.N), self.dtype))
-                with _on(stream, self.device):
-                    t = self._bufs[name] = torch.empty(shape, dtype=dt, device=self.device)
-            v = self._views[(name, M)] = t[:M], t.data_ptr()
+        """The first M rows of the layer's buffer ``name`` (all of it: None), made at its first use, of the
+        call's stream, and its address."""
+        t = self._bufs.get(name)
+        if t is None:
+            shape, dt = {"stats": ((self.max_rows, 2), torch.float32), "dw": ((self.N,), self.w_dtype),
+                         "db": ((self.N,), self.w_dtype)}.get(name, ((self.max_rows, self.N), self.dtype))
+            with _on(stream, self.device):
+                t = self._bufs[name] = torch.empty(shape, dtype=dt, device=self.device)
+        v = self._views[(name, M)] = t if M is None else t[:M], t.data_ptr()
         return v
 
-    def _present(self):
-        if not (_same(self.weight, self._w_ref, self._w_ptr) and _same(self.bias, self._b_ref, self._b_ptr)):
-            self._bind()
-
-    def _result(self, name, given, M, stream):
-        """Tensor, address and row distance of a result: the layer's own buffer or the caller's."""
-        if given is None:
-            return (*self._view(name, M, stream), self.N)
-        ld = _matrix(given, name, self.dtype, M, self.N, self.device)
-        for wname, t in (("weight", self.weight), ("bias", self.bias)):
-            if t is not None and given.numel() and _bytes_meet(given, ld, t):
+    def _given(self, name, t, M):
+        """Checks a result's place that the caller gives; returns the stride between its rows."""
+        ld = _matrix(t, name, self.dtype, M, self.N, self.device)
+        for wname, w in (("weight", self.weight), ("bias", self.bias)):
+            if w is not None and M and _bytes_meet(t, ld, w):
                 raise ValueError(f"{name}: overlaps the layer's {wname}")
-        return given, given.data_ptr(), ld
+        return ld
 
     def forward(self, x, residual=None, save=False, out=None, sum_out=None, stream=None):
-        M, D, dev, dtype, n = x.shape[0], self.dims, self.device, self.dtype, self.N
+        M, n, dev, dt, size, views = x.shape[0], self.N, self.device, self.dtype, self._size, self._views
         if M > self.max_rows:
             raise ValueError(f"{M} rows, the layer was made for {self.max_rows}")
-        ld_x = _matrix(x, "x", dtype, M, n, dev)
-        self._present()
-        y, yp, ld_y = self._result("y", out, M, stream)
-        _in_place("x", x, ld_x, y, ld_y, "the output")
-        s, sp, ld_s, rp, ld_r = x, None, 0, None, 0
+        shape = (M, n)
+        # (checked here, and said there: a call's host time is near the kernel's own for one row)
+        ld_x = n if x.dtype is dt and x.shape == shape and x.is_contiguous() and x.device == dev else _matrix(x, "x", dt, M, n, dev)
+        w, b = self.weight, self.bias
+        if w is not self._w_ref() or b is not self._b_ref() or w.data_ptr() != self._w_ptr or (b is not None and b.data_ptr() != self._b_ptr):
+            self._bind()
+        if out is None:
+            y, yp = views.get(("y", M)) or self._view("y", M, stream)
+            ld_y = n
+        else:
+            y, yp, ld_y = out, out.data_ptr(), self._given("out", out, M)
+        xp, row = x.data_ptr(), M * size     # (row times a stride: the span of rows that far apart)
+        if xp < yp + row * ld_y and yp < xp + row * ld_x:
+            _in_place("x", x, ld_x, y, ld_y, "the output")
+        sp = rp = None
+        ld_s = ld_r = 0
         if residual is not None:
-            ld_r, rp = _matrix(residual, "residual", dtype, M, n, dev), residual.data_ptr()
-            s, sp, ld_s = self._result("sum", sum_out, M, stream)
-            _in_place("residual", residual, ld_r, y, ld_y, "the output")
-            _in_place("residual", residual, ld_r, s, ld_s, "the sum")
-            _in_place("x", x, ld_x, s, ld_s, "the sum")
+            r = residual
+            ld_r = n if r.dtype is dt and r.shape == shape and r.is_contiguous() and r.device == dev else _matrix(r, "residual", dt, M, n, dev)
+            if sum_out is None:
+                s, sp = views.get(("sum", M)) or self._view("sum", M, stream)
+                ld_s = n
+            else:
+                s, sp, ld_s = sum_out, sum_out.data_ptr(), self._given("sum_out", sum_out, M)
+            rp = r.data_ptr()
+            r_end, s_end = rp + row * ld_r, sp + row * ld_s
+            if rp < yp + row * ld_y and yp < r_end:
+                _in_place("residual", r, ld_r, y, ld_y, "the output")
+            if rp < s_end and sp < r_end:
+                _in_place("residual", r, ld_r, s, ld_s, "the sum")
+            if xp < s_end and sp < xp + row * ld_x:
+                _in_place("x", x, ld_x, s, ld_s, "the sum")
             if (out is not None or sum_out is not None) and _overlap(y, ld_y, s, ld_s):
                 raise ValueError("out: overlaps the sum")
         elif sum_out is not None:
             raise ValueError("sum_out: there is no residual to add")
-        elif save and yp == x.data_ptr() and M:
+        elif save and yp == xp and M:
             raise ValueError("out: x is needed for the backward")
-        stats = self._view("stats", M, stream)[1] if save else None
-        if not save:
-            self._s = None
-        elif residual is None:
-            self._s = x, ld_x, None, 0
-        elif dtype != self.w_dtype and not ({x.data_ptr(), rp} & {sp, yp}):
-            self._s = x, ld_x, residual, ld_r
-        else:
-            self._s = s, ld_s, None, 0
-        D.M, D.ld_x, D.ld_res, D.ld_sum, D.ld_y = M, ld_x, ld_r, ld_s, ld_y
-        st = self._fwd(x.data_ptr(), rp, self._w_ptr, self._b_ptr, self._dims_ref, sp, yp, stats, _stream(stream, self._index))
+        stats = None
+        self._kept = None
+        if save:
+            stats = (views.get(("stats", M)) or self._view("stats", M, stream))[1]
+            if residual is None:
+                self._kept = x, xp, ld_x, None, None, 0
+            elif dt is not self.w_dtype and xp != sp and xp != yp and rp != sp and rp != yp:
+                self._kept = x, xp, ld_x, residual, rp, ld_r
+            else:
+                self._kept = s, sp, ld_s, None, None, 0
+        key = M, ld_x, ld_r, ld_s, ld_y
+        if key != self._set:
+            D = self.dims
+            D.M, D.ld_x, D.ld_res, D.ld_sum, D.ld_y = self._set = key
+        st = self._fwd(xp, rp, self._w_ptr, self._b_ptr, self._dims_ref, sp, yp, stats, _stream(stream, self._index))
         if st:
             N.check(st, "moe_norm_fwd")
         return y if residual is None else (y, s)
 
     def backward(self, dy, d_sum=None, need=("dx", "dw", "db"), out=None, stream=None):
-        if self._s is None:
+        if self._kept is None:
             raise ValueError("backward: the last forward did not save (save=True)")
-        (x, ld_x, res, ld_r), D, n = self._s, self.dims, self.N
+        (x, xp, ld_x, res, rp, ld_r), n, dev, dt, views = self._kept, self.N, self.device, self.dtype, self._views
         M = x.shape[0]
-        self._present()
-        ld_y, ld_d = _matrix(dy, "dy", self.dtype, M, n, self.device), 0
-        dx = dw = db = dxp = dwp = dbp = None
-        ld_dx = n
-        if "dx" in need:
-            dx, dxp, ld_dx = self._result("dx", out, M, stream)
-            _in_place("dy", dy, ld_y, dx, ld_dx, "dx")
-            _in_place("x", x, ld_x, dx, ld_dx, "dx")
-            if res is not None:
-                _in_place("residual", res, ld_r, dx, ld_dx, "dx")
+        shape, row = (M, n), M * self._size
+        w, b = self.weight, self.bias
+        if w is not self._w_ref() or b is not self._b_ref() or w.data_ptr() != self._w_ptr or (b is not None and b.data_ptr() != self._b_ptr):
+            self._bind()
+        ld_y = n if dy.dtype is dt and dy.shape == shape and dy.is_contiguous() and dy.device == dev else _matrix(dy, "dy", dt, M, n, dev)
+        dx = dw = db = dxp = dwp = dbp = sp = None
+        ld_dx = ld_d = 0
         if d_sum is not None:
-            ld_d = _matrix(d_sum, "d_sum", self.dtype, M, n, self.device)
-            if dx is not None:
-                _in_place("d_sum", d_sum, ld_d, dx, ld_dx, "dx")
+            d = d_sum
+            ld_d = n if d.dtype is dt and d.shape == shape and d.is_contiguous() and d.device == dev else _matrix(d, "d_sum", dt, M, n, dev)
+            sp = d.data_ptr()
+        yp = dy.data_ptr()
+        if "dx" in need:
+            if out is None:
+                dx, dxp = views.get(("dx", M)) or self._view("dx", M, stream)
+                ld_dx = n
+            else:
+                dx, dxp, ld_dx = out, out.data_ptr(), self._given("out", out, M)
+            end = dxp + row * ld_dx
+            for name, t, p, ld in (("dy", dy, yp, ld_y), ("x", x, xp, ld_x), ("residual", res, rp, ld_r), ("d_sum", d_sum, sp, ld_d)):
+                if t is not None and p < end and dxp < p + row * ld:
+                    _in_place(name, t, ld, dx, ld_dx, "dx")
         if "dw" in need:
-            dw, dwp = self._view("dw", 1, stream)
-        if "db" in need and self.bias is not None:
-            db, dbp = self._view("db", 1, stream)
+            dw, dwp = views.get(("dw", None)) or self._view("dw", None, stream)
+        if "db" in need and b is not None:
+            db, dbp = views.get(("db", None)) or self._view("db", None, stream)
         if self.ws is None:
-            most = N.NormDims.from_buffer_copy(D)
-            most.M = self.max_rows
-            self.ws = OpWorkspace(N.lib().moe_norm_workspace_bytes(ctypes.byref(most)), "moe_norm_workspace_bytes", self.device,
-                                  stream)
-        D.M, D.ld_x, D.ld_res, D.ld_sum, D.ld_y, D.ld_dx = M, ld_x, ld_r, ld_d, ld_y, ld_dx
-        st = self._bwd(x.data_ptr(), _p(res), dy.data_ptr(), _p(d_sum), self._w_ptr, self._view("stats", M, stream)[1], self._dims_ref,
-                       dxp, dwp, dbp, self.ws.ptr, self.ws.nbytes, _stream(stream, self._index))
+            self.ws = OpWorkspace(self._need, "moe_norm_workspace_bytes", dev, stream)
+        key = M, ld_x, ld_r, ld_d, ld_y, ld_dx
+        if key != self._bwd_set:
+            D = self._bwd_dims
+            D.M, D.ld_x, D.ld_res, D.ld_sum, D.ld_y, D.ld_dx = self._bwd_set = key
+        st = self._bwd(xp, rp, yp, sp, self._w_ptr, views[("stats", M)][1], self._bwd_ref, dxp, dwp, dbp, self.ws.ptr, self.ws.nbytes,
+                       _stream(stream, self._index))
         if st:
             N.check(st, "moe_norm_bwd")
-        return dict(dx=dx, dw=None if dw is None else dw[0], db=None if db is None else db[0])
+        return dict(dx=dx, dw=dw, db=db)
 
 
 def _bytes_meet(a, ld_a, b):
@@ -844,6 +874,8 @@ class TokenLogprobs:
             top_idx = torch.empty(max_rows, top, dtype=torch.int32, device=device)
             top_logprob = torch.empty(max_rows, top, dtype=torch.float32, device=device)
         self._top = top_idx, top_logprob
+        self._ptrs = (self._logprob.data_ptr(), self._entropy.data_ptr(), self._stats.data_ptr(),
+                      top_idx.data_ptr() if top else None, top_logprob.data_ptr() if top else None)
         self._grad, self._views, self._saved = None, {}, None
         self._dims_ref = ctypes.byref(self.dims)
         self._fwd, self._bwd = N.lib().moe_token_logprob, N.lib().moe_token_logprob_bwd
@@ -852,24 +884,29 @@ class TokenLogprobs:
         M, D, dev = scores.shape[0], self.dims, self.device
         if M > self.max_rows:
             raise ValueError(f"{M} rows, made for {self.max_rows}")
-        ld = _matrix(scores, "scores", self.dtype, M, self.V, dev)
+        t = scores
+        ld = self.V if t.dtype is self.dtype and t.shape == (M, self.V) and t.is_contiguous() and t.device == dev else _matrix(
+            t, "scores", self.dtype, M, self.V, dev)
         if tokens is not None:
             _dense(tokens, "tokens", torch.int32, (M,), dev)
         v = self._views.get(M)
         if v is None:
             v = self._views[M] = (self._logprob[:M, 0], self._entropy[:M, 0], self._top[0][:M], self._top[1][:M])
         out = {}
+        lp, ep, sp, ip, vp = self._ptrs
         if tokens is not None:
-            out["logprob"] = v[0]
+            out["logprob"], tp = v[0], tokens.data_ptr()
+        else:
+            tp = lp = None
         if entropy:
             out["entropy"] = v[1]
+        else:
+            ep = None
         if self.top:
             out["top_idx"], out["top_logprob"] = v[2], v[3]
         self._saved = (scores, ld, tokens, entropy) if save else None
         D.M, D.ld = M, ld
-        st = self._fwd(scores.data_ptr(), _p(tokens), self._dims_ref, v[0].data_ptr() if tokens is not None else None,
-                       v[1].data_ptr() if entropy else None, self._stats.data_ptr() if save else None, v[2].data_ptr() if self.top else None,
-                       v[3].data_ptr() if self.top else None, _stream(stream, self._index))
+        st = self._fwd(scores.data_ptr(), tp, self._dims_ref, lp, ep, sp if save else None, ip, vp, _stream(stream, self._index))
         if st:
             N.check(st, "moe_token_logprob")
         return out
@@ -938,6 +975,8 @@ class GradClipper:
         self._np, self._sp = self._norm.data_ptr(), self.scale.data_ptr()
         self._clip_table, self._norm_table = (N.Grad * max(n, 1))(), (N.Grad * max(n, 1))()
         self._call = N.lib().moe_clip_grads
+        tensors = self.grads if self.out is self.grads else self.grads + self.out
+        self._ask = [t.data_ptr for t in tensors] + [t.numel for t in tensors]
         self._bind()
 
     def _bind(self):
@@ -954,14 +993,31 @@ class GradClipper:
                 raise ValueError(f"out {i}: expected {list(g.shape)} of {g.dtype}, got {list(o.shape)} of {o.dtype}")
             self._clip_table[i] = N.Grad(g.data_ptr(), o.data_ptr(), g.numel(), _dt(g.dtype))
             self._norm_table[i] = N.Grad(g.data_ptr(), None, g.numel(), _dt(g.dtype))
-        self._places = self._now()
+        self._check_places()
+        self._places = [ask() for ask in self._ask]
 
-    def _now(self):
-        now = [(t.data_ptr(), t.numel()) for t in self.grads]
-        return now if self.out is self.grads else now + [(t.data_ptr(), t.numel()) for t in self.out]
+    def _check_places(self):
+        """No result may overlap another one, or a gradient other than its own (that one only as a whole)."""
+        spans = []      # (first byte, behind the last, result's name or None, gradient's name)
+        for i, (g, o) in enumerate(zip(self.grads, self.out)):
+            a, b, size = g.data_ptr(), o.data_ptr(), g.numel() * g.element_size()
+            if size:
+                spans.append((b, b + size, f"out {i}", None))
+                if a != b:
+                    spans.append((a, a + size, None, f"gradient {i}"))
+        spans.sort(key=lambda s: s[0])
+        read = written = (0, None)      # the end that reaches furthest, and whose
+        for a, b, result, gradient in spans:
+            for end, name in ((written,) if gradient else (written, read)):
+                if a < end:
+                    raise ValueError(f"{result or gradient}: overlaps {name}")
+            if result:
+                written = max(written, (b, result))
+            else:
+                read = max(read, (b, gradient))
 
     def _run(self, table, max_norm, stream):
-        if self._places != self._now():
+        if self._places != [ask() for ask in self._ask]:
             self._bind()
         st = self._call(table, len(self.grads), max_norm, self._np, self._sp, self.ws.ptr, self.ws.nbytes,
                         _stream(stream, self._index))

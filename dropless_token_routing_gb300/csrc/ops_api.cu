@@ -1,6 +1,5 @@
 // C ABI of the operators beside the layer: argument validation, workspace layouts and launches.
 #include <math.h>
-#include <stdlib.h>
 #include <string.h>
 
 #include "ops.h"
@@ -189,45 +188,6 @@ int resolve_logprob(const moe_logprob_dims* in, moe_logprob_dims* d) {
     if (*ld < d->V || *ld > kMaxLd) return MOE_ERR_BAD_DIMS;
   }
   return MOE_OK;
-}
-
-// Memory that a clipping call reads or writes.
-struct Extent {
-  uintptr_t from, to;
-  bool out;
-};
-int by_start(const void* a, const void* b) {
-  const Extent *x = static_cast<const Extent*>(a), *y = static_cast<const Extent*>(b);
-  return x->from < y->from ? -1 : x->from > y->from;
-}
-
-// Whether an out overlaps another out, or a g other than its own in the same place. (No C++
-// allocation: an exception may not leave a C entry.)
-int check_overlap(const moe_grad* grads, int64_t count) {
-  int64_t n = 0;
-  bool any = false;
-  for (int64_t i = 0; i < count; ++i) any |= grads[i].out != nullptr && grads[i].n > 0;
-  if (!any) return MOE_OK;
-  Extent few[64];
-  Extent* e = 2 * count <= 64 ? few : static_cast<Extent*>(malloc(2 * (size_t)count * sizeof(Extent)));
-  if (e == nullptr) return MOE_ERR_CUDA;
-  for (int64_t i = 0; i < count; ++i) {
-    const moe_grad& g = grads[i];
-    if (g.n == 0) continue;
-    const uintptr_t bytes = (uintptr_t)g.n * elt_bytes(g.dtype), from = reinterpret_cast<uintptr_t>(g.g);
-    if (g.out != nullptr) e[n++] = {reinterpret_cast<uintptr_t>(g.out), reinterpret_cast<uintptr_t>(g.out) + bytes, true};
-    if (g.out != g.g) e[n++] = {from, from + bytes, false};
-  }
-  qsort(e, (size_t)n, sizeof(Extent), by_start);
-  int st = MOE_OK;
-  uintptr_t read = 0, written = 0;   // ends of what begins no later
-  for (int64_t i = 0; i < n && st == MOE_OK; ++i) {
-    if (e[i].from < written || (e[i].out && e[i].from < read)) st = MOE_ERR_OVERLAP;
-    uintptr_t& end = e[i].out ? written : read;
-    if (e[i].to > end) end = e[i].to;
-  }
-  if (e != few) free(e);
-  return st;
 }
 
 }  // namespace
@@ -479,7 +439,6 @@ int moe_clip_grads(const moe_grad* grads, int64_t count, float max_norm, float* 
     if (g.n > 0 && g.g == nullptr) return MOE_ERR_NULL_POINTER;
     if (((reinterpret_cast<uintptr_t>(g.g) | reinterpret_cast<uintptr_t>(g.out)) & (elt_bytes(g.dtype) - 1)) != 0) return MOE_ERR_MISALIGNED;
   }
-  OP_TRY(check_overlap(grads, count));
   int sms = 0;
   OP_TRY(check_device(&sms));
   uint8_t* base = static_cast<uint8_t*>(ws);

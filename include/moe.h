@@ -64,7 +64,6 @@ enum moe_status {
   MOE_ERR_LAUNCH = -7,              /* a kernel launch failed */
   MOE_ERR_CUDA = -8,                /* another CUDA runtime/driver call failed */
   MOE_ERR_UNSUPPORTED_DEVICE = -9,  /* bf16 grouped GEMM and the operators beside the layer: sm_103 (GB300) only */
-  MOE_ERR_OVERLAP = -10,            /* an output overlaps what is read while it is written, or another output */
   MOE_ERR_DEVICE_EXPERT_ID = -100,  /* device: expert id outside [0, E) or repeated in a row */
   MOE_ERR_DEVICE_TIMEOUT = -101     /* device: a bounded wait ran out */
 };
@@ -533,7 +532,7 @@ typedef struct moe_grad {
  * grads: HOST array of count entries (0 allowed: norm 0), read before the call returns. max_norm >= 0,
  * or infinity (scale 1). norm, scale: device floats, or NULL. No outs: the norm alone. Sums of squares
  * leave fp32's range neither way; a norm that is not finite gives the scale of the formula (0, or NaN). An out
- * overlaps no other out and no other g, and its own g only as the whole of it (MOE_ERR_OVERLAP). All n
+ * overlaps no other out and no other g, and its own g only as the whole of it. All n
  * together stay below 2^44. A workspace for count tensors serves fewer. ws: moe_op_workspace_init's. */
 size_t moe_clip_workspace_bytes(int64_t count);
 int moe_clip_grads(const moe_grad* grads, int64_t count, float max_norm, float* norm, float* scale, void* ws,

@@ -896,6 +896,8 @@ class TokenLogprobs:
         lp, ep, sp, ip, vp = self._ptrs
         if tokens is not None:
             out["logprob"], tp = v[0], tokens.data_ptr()
+            if save and ip is not None and ip - 4 * M < tp < ip + 4 * M * self.top:
+                raise ValueError("tokens: overlaps the result, and is needed for the backward")
         else:
             tp = lp = None
         if entropy:
@@ -944,7 +946,7 @@ class TokenLogprobs:
 
 
 class GradClipper:
-    """The global norm of a list of gradients, and their clipping: moe_clip_grads on a kept list
+    """The global norm of a list (or dict) of gradients, and their clipping: moe_clip_grads on a kept list
     (contiguous fp32 or bf16 tensors; those of None are left out).
 
     ``norm()`` returns the norm, ``clip(max_norm)`` also scales the gradients by min(1, max_norm / (norm +
@@ -955,8 +957,8 @@ class GradClipper:
     """
 
     def __init__(self, grads, out=None, device=None, stream=None):
-        grads = list(grads)
-        outs = grads if out is None else list(out)
+        grads = list(grads.values() if isinstance(grads, dict) else grads)
+        outs = grads if out is None else list(out.values() if isinstance(out, dict) else out)
         if len(outs) != len(grads):
             raise ValueError(f"out: {len(outs)} tensors for {len(grads)} gradients")
         if any((g is None) != (o is None) for g, o in zip(grads, outs)):

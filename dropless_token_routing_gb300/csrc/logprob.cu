@@ -390,11 +390,13 @@ __global__ void __launch_bounds__(LT, (kBlocks<T, ENT, TOP>)) logprob_kernel(con
 
 constexpr int GU = 4, GC = GU * LT * 8;   // the same of the gradient
 
+// Rows from the last one back: where the gradient follows the forward pass at once, as a loss's does, L2 still
+// holds the rows read last (4096 x 32000 fp32: both 236 us from the first row on, 233 so).
 template <typename T>
 __global__ void __launch_bounds__(LT) logprob_bwd_kernel(const LogprobBwdArgs a) {
   pdl_start();
   pdl_wait();
-  const int64_t m = blockIdx.x;
+  const int64_t m = a.M - 1 - blockIdx.x;
   const T* first = static_cast<const T*>(a.x) + m * a.ld;
   const Places<T> row(first, a.V);
   T* out = static_cast<T*>(a.dx) + m * a.ld_dx - row.lead;   // of place 0

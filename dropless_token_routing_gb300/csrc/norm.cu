@@ -693,6 +693,55 @@ __global__ void __launch_bounds__(256) norm_columns_kernel(const NormBwdArgs a, 
   }
 }
 
+// dw and db of few rows, from x and dy themselves: a block owns four vectors of columns, 64 threads each take rows
+// in turn, added in an order that M alone sets. One partial sum for every row or two would be as much
+// to write and read as the operands (backward of 64 x 8192 bf16 by those 10.4 us, 5.6 so; 100 x 256 5.9, 3.9; but
+// 200 x 100 5.6, 6.7, and 300 x 4096 11.2, 12.4).
+constexpr int kFewRows = 128;
+template <typename T, typename W, bool VEC>
+__global__ void __launch_bounds__(256) norm_sums_kernel(const NormBwdArgs a) {
+  __shared__ float s[2][64][4][9];
+  const int lane = threadIdx.x & 3, r = threadIdx.x >> 2, N = a.N, c = (blockIdx.x * 4 + lane) * 8, n = N - c;
+  pdl_start();
+  pdl_wait();
+  float dw[8], db[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) dw[j] = db[j] = 0.f;
+  if (n > 0) {
+    const T *x = static_cast<const T*>(a.x), *res = static_cast<const T*>(a.res), *dy = static_cast<const T*>(a.dy);
+    const T *x_end = end_of<T>(x, a.M, a.ld_x, N), *r_end = end_of<T>(res, a.M, a.ld_res, N), *y_end = end_of<T>(dy, a.M, a.ld_dy, N);
+#pragma unroll 4
+    for (int64_t m = r; m < a.M; m += 64) {
+      const float2 st = reinterpret_cast<const float2*>(a.stats)[m];
+      Vec8<T> v;
+      float f[8], g[8];
+      load_sum<T, VEC>(f, x + m * a.ld_x, res != nullptr ? res + m * a.ld_res : nullptr, c, n, x_end, r_end);
+      load_row<T, VEC>(v, dy + m * a.ld_dy, c, n, y_end);
+      v.to_float(g);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        dw[j] = fmaf(g[j], (f[j] - st.x) * st.y, dw[j]);
+        db[j] += g[j];
+      }
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    s[0][r][lane][j] = dw[j];
+    s[1][r][lane][j] = db[j];
+  }
+  __syncthreads();
+  // 64 sums, four threads each
+  const int sum = threadIdx.x >> 2, k = sum >> 5, col = sum & 31, at = blockIdx.x * 32 + col;
+  float t = 0.f;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) t += s[k][lane * 16 + i][col >> 3][col & 7];
+  t += __shfl_xor_sync(0xffffffffu, t, 1);
+  t += __shfl_xor_sync(0xffffffffu, t, 2);
+  W* out = static_cast<W*>(k ? a.db : a.dw);
+  if (lane == 0 && out != nullptr && at < N) out[at] = from_f32<W>(t);
+}
+
 // dw (blockIdx.y 0) and db (1) from their partial sums, added in an order that their number alone sets:
 // 32 columns per block, four to a thread, 32 threads each.
 template <typename W>
@@ -729,6 +778,9 @@ int norm_threads(int N) {
   const int t = ((N + 8 * kVecs - 1) / (8 * kVecs) + 31) & ~31;
   return t;
 }
+
+// Whether every row of an operand (if it is there) starts on a 16-byte boundary.
+template <typename T> bool whole(const void* p, int64_t ld) { return p == nullptr || ld % (16 / (int)sizeof(T)) == 0; }
 
 // Shared memory above the default size has to be allowed, once for each kernel and device.
 template <auto Kernel> cudaError_t allow_ring(int bytes) {
@@ -768,8 +820,7 @@ template <typename T, typename W, int MODE, bool RES> cudaError_t fwd_rows(const
 }
 
 template <typename T, typename W> cudaError_t norm_fwd(const NormArgs& a, int num_sms, cudaStream_t st) {
-  const bool vec = a.M == 1 || (a.ld_x % 8 == 0 && a.ld_y % 8 == 0 && (a.res == nullptr || a.ld_res % 8 == 0) &&
-                                (a.sum == nullptr || a.ld_sum % 8 == 0));
+  const bool vec = a.M == 1 || (whole<T>(a.x, a.ld_x) && whole<T>(a.y, a.ld_y) && whole<T>(a.res, a.ld_res) && whole<T>(a.sum, a.ld_sum));
   if (a.N <= kRowsMaxN) {
     const bool res = a.res != nullptr;
     switch (RowShape::mode(a.N, vec)) {
@@ -801,10 +852,18 @@ template <typename T, typename W, int MODE> cudaError_t bwd_mode(const NormBwdAr
 
 template <typename T, typename W> cudaError_t norm_bwd(const NormBwdArgs& a, int num_sms, cudaStream_t st) {
   const bool sums = a.dw != nullptr || a.db != nullptr, rows = a.N <= kRowsMaxN;
-  const bool vec = a.M == 1 || (a.ld_x % 8 == 0 && a.ld_dy % 8 == 0 && (a.res == nullptr || a.ld_res % 8 == 0));
-  const bool vdx = a.M == 1 || (vec && (a.dx == nullptr || a.ld_dx % 8 == 0) && (a.d_sum == nullptr || a.ld_ds % 8 == 0));
+  const bool vec = a.M == 1 || (whole<T>(a.x, a.ld_x) && whole<T>(a.dy, a.ld_dy) && whole<T>(a.res, a.ld_res));
+  const bool vdx = a.M == 1 || (vec && whole<T>(a.dx, a.ld_dx) && whole<T>(a.d_sum, a.ld_ds));
   int parts = 0;
   cudaError_t e = cudaSuccess;
+  if (sums && a.M <= kFewRows) {   // (before dx, which may be the buffer of an operand)
+    const dim3 grid((a.N + 31) / 32);
+    e = vec ? launch_pdl(norm_sums_kernel<T, W, true>, grid, 256, 0, 1, st, a) : launch_pdl(norm_sums_kernel<T, W, false>, grid, 256, 0, 1, st, a);
+    if (e != cudaSuccess || a.dx == nullptr) return e;
+    NormBwdArgs d = a;
+    d.dw = d.db = nullptr;
+    return norm_bwd<T, W>(d, num_sms, st);
+  }
   if (rows) {
     switch (RowShape::mode(a.N, vdx)) {
       case UNALIGNED: e = bwd_mode<T, W, UNALIGNED>(a, num_sms, &parts, st); break;

@@ -109,7 +109,7 @@ def test_norm_sizes(M, N, dtype, w_dtype):
 
 @pytest.mark.parametrize("dtype", [BF, F32])
 @pytest.mark.parametrize("residual", [False, True])
-@pytest.mark.parametrize("M,N,ld", [(20, 100, 104), (20, 104, 109), (7, 1001, 1016), (31, 2048, 4096), (6, 7680, 7683)])
+@pytest.mark.parametrize("M,N,ld", [(20, 100, 104), (20, 104, 109), (20, 100, 100), (9, 1004, 1004), (7, 1001, 1016), (31, 2048, 4096), (6, 7680, 7683)])
 def test_norm_strides(M, N, ld, dtype, residual):
     _check_norm(M, N, dtype, dtype, residual, True, seed=ld, ld=ld)
 
@@ -533,6 +533,20 @@ def test_clip_beyond_the_range_of_squares():
     mixed = torch.zeros(200_000)
     mixed[5], mixed[100_000], mixed[6] = 1e-30, 1e22, 1.0
     assert abs(float(_api().GradClipper([mixed.cuda()]).norm()) - 1e22) <= 4 * H * 1e22
+
+
+def test_clip_tensor_beyond_31_bits():
+    """More than 2^31 elements, the last ones counted and scaled like the first."""
+    n = (1 << 31) + 20001
+    t = torch.zeros(n, dtype=BF, device="cuda")
+    t[:3], t[n - 20000:] = 3.0, -2.0
+    ref = math.sqrt(3 * 9 + 20000 * 4)
+    c = _api().GradClipper([t])
+    assert abs(float(c.clip(1.0)) - ref) <= 40 * H * ref
+    scale = 1.0 / (ref + 1e-6)
+    _near(t[-4:], torch.full((4,), -2.0 * scale, dtype=torch.float64), BF, torch.full((4,), 2.0 * scale, dtype=torch.float64), steps=48)
+    _near(t[:4], torch.tensor([3.0, 3.0, 3.0, 0.0]).double() * scale, BF, torch.full((4,), 3.0 * scale, dtype=torch.float64), steps=48)
+    assert not t[3:n - 20000:99991].any()
 
 
 def test_clip_not_finite():

@@ -323,23 +323,26 @@ __global__ void __launch_bounds__(LT, (kBlocks<T, ENT, TOP>)) logprob_kernel(con
   }
   if (rank == 0) {
     if (warp == 0) {   // the sums of up to 64 warps
-      s = {kLowest, 0.f, 0.f};
-      for (int r = lane; r < (int)ranks * LW; r += 32) {
-        Sums o;
-        if (ranks > 1) {
+      Sums o[2];   // (both asked for at once)
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int r = lane + 32 * k;
+        o[k] = {kLowest, 0.f, 0.f};
+        if (ranks > 1 && r < (int)ranks * LW) {
           const uint32_t at = smem_u32(&s_sums[r % LW]);
-          o.m = peer_ldf(at, r / LW);
-          o.S = peer_ldf(at + 4, r / LW);
-          o.D = peer_ldf(at + 8, r / LW);
-        } else {
-          o = s_sums[r];
+          o[k].m = peer_ldf(at, r / LW);
+          o[k].S = peer_ldf(at + 4, r / LW);
+          if (ENT) o[k].D = peer_ldf(at + 8, r / LW);
+        } else if (r < LW) {
+          o[k] = s_sums[r];
         }
-        const float max = fmaxf(s.m, o.m);
-        s.to(max);
-        o.to(max);
-        s.S += o.S;
-        s.D += o.D;
       }
+      s = o[0];
+      const float max = fmaxf(o[0].m, o[1].m);
+      s.to(max);
+      o[1].to(max);
+      s.S += o[1].S;
+      s.D += o[1].D;
       s.warp_join<ENT>();
       const float log_sum = s.S == 0.f ? -kInf : logf(s.S);   // a row without a distribution: -inf
       if (lane == 0) {

@@ -695,9 +695,9 @@ __global__ void __launch_bounds__(256) norm_columns_kernel(const NormBwdArgs a, 
 
 // dw and db of few rows, from x and dy themselves: a block owns four vectors of columns, 64 threads each take rows
 // in turn, added in an order that M alone sets. One partial sum for every row or two would be as much
-// to write and read as the operands (backward of 64 x 8192 bf16 by those 10.4 us, 5.6 so; 100 x 256 5.9, 3.9; but
-// 200 x 100 5.6, 6.7, and 300 x 4096 11.2, 12.4).
-constexpr int kFewRows = 128;
+// to write and read as the operands (backward of 64 x 8192 bf16 by those 10.4 us, 5.4 so; 100 x 256 5.9, 3.7; 180 x
+// 7680 12.3, 9.6; with four rows for a thread, 250 x 1024 6.3, 5.5, but 200 x 100 4.7, 6.3).
+constexpr int kFewRows = 192;
 template <typename T, typename W, bool VEC>
 __global__ void __launch_bounds__(256) norm_sums_kernel(const NormBwdArgs a) {
   __shared__ float s[2][64][4][9];
@@ -710,20 +710,30 @@ __global__ void __launch_bounds__(256) norm_sums_kernel(const NormBwdArgs a) {
   if (n > 0) {
     const T *x = static_cast<const T*>(a.x), *res = static_cast<const T*>(a.res), *dy = static_cast<const T*>(a.dy);
     const T *x_end = end_of<T>(x, a.M, a.ld_x, N), *r_end = end_of<T>(res, a.M, a.ld_res, N), *y_end = end_of<T>(dy, a.M, a.ld_dy, N);
-#pragma unroll 4
-    for (int64_t m = r; m < a.M; m += 64) {
-      const float2 st = reinterpret_cast<const float2*>(a.stats)[m];
-      Vec8<T> v;
-      float f[8], g[8];
-      load_sum<T, VEC>(f, x + m * a.ld_x, res != nullptr ? res + m * a.ld_res : nullptr, c, n, x_end, r_end);
-      load_row<T, VEC>(v, dy + m * a.ld_dy, c, n, y_end);
-      v.to_float(g);
+    constexpr int U = kFewRows / 64;   // a thread's rows, all under way at once
+    float2 st[U];
+    float f[U][8];
+    Vec8<T> v[U];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        dw[j] = fmaf(g[j], (f[j] - st.x) * st.y, dw[j]);
-        db[j] += g[j];
+    for (int u = 0; u < U; ++u) {
+      const int64_t m = r + 64 * u;
+      if (m < a.M) {
+        st[u] = reinterpret_cast<const float2*>(a.stats)[m];
+        load_sum<T, VEC>(f[u], x + m * a.ld_x, res != nullptr ? res + m * a.ld_res : nullptr, c, n, x_end, r_end);
+        load_row<T, VEC>(v[u], dy + m * a.ld_dy, c, n, y_end);
       }
     }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (r + 64 * u < a.M) {
+        float g[8];
+        v[u].to_float(g);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          dw[j] = fmaf(g[j], (f[u][j] - st[u].x) * st[u].y, dw[j]);
+          db[j] += g[j];
+        }
+      }
   }
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
@@ -754,13 +764,21 @@ __global__ void __launch_bounds__(256) norm_join_kernel(const float* part, int n
   if (out == nullptr) return;
   float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
   if (n < N) {
-#pragma unroll 5
-    for (int i = r; i < n_part; i += 32) {
-      const float4 p = *reinterpret_cast<const float4*>(part + ((int64_t)i * 2 + blockIdx.y) * ld + n);
-      t.x += p.x;
-      t.y += p.y;
-      t.z += p.z;
-      t.w += p.w;
+    constexpr int U = 5;   // of a thread that are under way: all, with a block on each of 152 SMs
+    for (int i0 = r; i0 < n_part; i0 += 32 * U) {
+      float4 p[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int i = i0 + 32 * u;
+        p[u] = i < n_part ? *reinterpret_cast<const float4*>(part + ((int64_t)i * 2 + blockIdx.y) * ld + n) : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        t.x += p[u].x;
+        t.y += p[u].y;
+        t.z += p[u].z;
+        t.w += p[u].w;
+      }
     }
   }
   s[r][v] = t;

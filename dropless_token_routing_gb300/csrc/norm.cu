@@ -8,7 +8,7 @@
 // A row stays on the SM between its sums and its way out, so every operand is read once; the
 // variance is that of the centred values (no difference of large numbers). All of it is bound by HBM.
 //
-// Rows of up to 8192 elements are taken by groups of warps, 16 elements to a thread, in a
+// Rows of up to 8192 elements (bf16: 16384) are taken by groups of warps, 16 elements (32) to a thread, in a
 // persistent block of up to 16 warps; wider ones by a block each. A thread copies its own elements of the
 // rows to come into its own places of shared memory (cp.async), several rows ahead, so that the loads of
 // a group go on through its barriers, and nobody waits for another thread's copies. The
@@ -97,8 +97,10 @@ __device__ __forceinline__ float2 block_sums(float a, float b, float* s) {
 }
 
 // ------------------------------------------------------------------ rows of up to kRowsMaxN elements
-constexpr int kRowThreads = 512, kRowElements = 16;   // most threads of a block; elements of a row that a thread holds
-constexpr int kRowsMaxN = kRowThreads * kRowElements;
+constexpr int kRowThreads = 512;   // most threads of a block
+// Elements of a row that a thread holds: 16, or 32 of wider bf16 rows.
+constexpr int kThin = 16, kThick = 32;
+constexpr int kRowsMaxN = kRowThreads * kThin, kThickMaxN = kRowThreads * kThick;
 constexpr int kMaxStages = 8;
 constexpr int kRing = 200 * 1024;   // shared memory of an SM for the copies
 
@@ -197,11 +199,11 @@ template <typename W, int kIn> struct Weights {
 
 // A thread's units of a row are 16 bytes each, neighbouring threads' side by side, in the row as in shared
 // memory. UNALIGNED (some row does not start on a 16-byte boundary): a unit's copy is the two aligned pieces
-// around it. FULL: all units of a group are whole ones (widths of 512 times its warps), which saves every
+// around it. FULL: all units of a group are whole ones (widths of 32 E times its warps), which saves every
 // test for a row's end (8192 x 7680, two blocks on an SM: 95 us forward with them, 91 without).
 enum RowMode { UNALIGNED = 0, ALIGNED = 1, FULL = 2 };
-template <typename T, int MODE> struct Unit {
-  static constexpr int kIn = 16 / sizeof(T), kPairs = kIn / 2, kUnits = kRowElements / kIn;   // elements; pairs; of a thread
+template <typename T, int MODE, int E> struct Unit {
+  static constexpr int kIn = 16 / sizeof(T), kPairs = kIn / 2, kUnits = E / kIn;   // elements; pairs; of a thread
   static constexpr int kPieces = MODE == UNALIGNED ? 2 : 1;
   // p: the unit's first element; n: elements of the row from there on; end: the tensor's
   static __device__ __forceinline__ void copy(uint32_t at, const T* p, int n, const T* end) {
@@ -292,11 +294,11 @@ struct Group {
   }
 };
 
-template <typename T, typename W, int MODE, bool RES>
+template <typename T, typename W, int MODE, int E, bool RES>
 __global__ void __launch_bounds__(kRowThreads, 1) norm_fwd_rows(const NormArgs a, int warps, int stages) {
   extern __shared__ uint4 ring[];
   __shared__ float2 s_sums[2][16];
-  using P = Unit<T, MODE>;
+  using P = Unit<T, MODE, E>;
   constexpr int kIn = P::kIn, kUnits = P::kUnits, kPairs = P::kPairs, kOp = kUnits * P::kPieces, kStep = (1 + RES) * kOp;
   pdl_start();
   const int N = a.N, gt = warps * 32, groups = blockDim.x / gt, tg = threadIdx.x % gt;
@@ -326,14 +328,18 @@ __global__ void __launch_bounds__(kRowThreads, 1) norm_fwd_rows(const NormArgs a
     cp_commit();
   };
   for (int s = 0; s + 1 < stages; ++s) fetch(s);
-  Weights<W, kIn> w[kUnits], b[kUnits];
-#pragma unroll
-  for (int i = 0; i < kUnits; ++i) {
+  constexpr bool HOLD = E * sizeof(W) <= 64;   // the weights in registers; else read for every row
+  Weights<W, kIn> w[HOLD ? kUnits : 1], b[HOLD ? kUnits : 1];
+  auto weights = [&](int i, int to) {
     const int n = n0 - i * next_unit;
     if (MODE == FULL || n > 0) {
-      w[i].load(static_cast<const W*>(a.w) + c0 + i * next_unit, n);
-      if (a.b != nullptr) b[i].load(static_cast<const W*>(a.b) + c0 + i * next_unit, n);
+      w[to].load(static_cast<const W*>(a.w) + c0 + i * next_unit, n);
+      if (a.b != nullptr) b[to].load(static_cast<const W*>(a.b) + c0 + i * next_unit, n);
     }
+  };
+  if (HOLD) {
+#pragma unroll
+    for (int i = 0; i < kUnits; ++i) weights(i, i);
   }
   int stage = 0;
   for (int64_t m = (int64_t)blockIdx.x * groups + group.index; m < a.M; m += step) {
@@ -381,8 +387,9 @@ __global__ void __launch_bounds__(kRowThreads, 1) norm_fwd_rows(const NormArgs a
     for (int i = 0; i < kUnits; ++i) {
       const int n = n0 - i * next_unit;
       uint64_t g[kPairs], h[kPairs] = {};
-      w[i].pairs(g);
-      if (a.b != nullptr) b[i].pairs(h);
+      if (!HOLD) weights(i, 0);
+      w[HOLD ? i : 0].pairs(g);
+      if (a.b != nullptr) b[HOLD ? i : 0].pairs(h);
 #pragma unroll
       for (int j = 0; j < kPairs; ++j) g[j] = fma2(f[i][j], mul2(g[j], both(rstd)), h[j]);
       if (MODE != ALIGNED || n > 0) P::write(g, at + i * P::kPieces * blockDim.x, static_cast<T*>(a.y) + m * a.ld_y + c0 + i * next_unit, n);
@@ -392,11 +399,11 @@ __global__ void __launch_bounds__(kRowThreads, 1) norm_fwd_rows(const NormArgs a
 }
 
 // x, dy, then the residual (RES) and d_sum (DS) as further operands of a stage.
-template <typename T, typename W, int MODE, bool RES, bool DS>
+template <typename T, typename W, int MODE, int E, bool RES, bool DS>
 __global__ void __launch_bounds__(kRowThreads, 1) norm_bwd_rows(const NormBwdArgs a, int warps, int stages) {
   extern __shared__ uint4 ring[];
   __shared__ float2 s_sums[2][16];
-  using P = Unit<T, MODE>;
+  using P = Unit<T, MODE, E>;
   constexpr int kIn = P::kIn, kUnits = P::kUnits, kPairs = P::kPairs, kOp = kUnits * P::kPieces, kOps = 2 + RES + DS;
   pdl_start();
   const int N = a.N, gt = warps * 32, groups = blockDim.x / gt, tg = threadIdx.x % gt;
@@ -432,12 +439,17 @@ __global__ void __launch_bounds__(kRowThreads, 1) norm_bwd_rows(const NormBwdArg
     cp_commit();
   };
   for (int s = 0; s + 1 < stages; ++s) fetch(s);
-  Weights<W, kIn> w[kUnits];
+  // KEEP: u and xh stay in registers from the sums to dx; else they are formed again from the copies
+  constexpr bool KEEP = E == kThin, HOLD = KEEP;
+  Weights<W, kIn> w[HOLD ? kUnits : 1];
   uint64_t dw[kUnits][kPairs], db[kUnits][kPairs];
+  auto weights = [&](int i, int to) {
+    const int n = n0 - i * next_unit;
+    if ((MODE == FULL || n > 0) && a.dx != nullptr) w[to].load(static_cast<const W*>(a.w) + c0 + i * next_unit, n);
+  };
 #pragma unroll
   for (int i = 0; i < kUnits; ++i) {
-    const int n = n0 - i * next_unit;
-    if ((MODE == FULL || n > 0) && a.dx != nullptr) w[i].load(static_cast<const W*>(a.w) + c0 + i * next_unit, n);
+    if (HOLD) weights(i, i);
 #pragma unroll
     for (int j = 0; j < kPairs; ++j) dw[i][j] = db[i][j] = 0;
   }
@@ -451,56 +463,81 @@ __global__ void __launch_bounds__(kRowThreads, 1) norm_bwd_rows(const NormBwdArg
     cp_wait(stages - 1);
     uint4* at = ring + stage * kOps * kOp * blockDim.x + threadIdx.x;
     if (++stage == stages) stage = 0;
-    uint64_t u[kUnits][kPairs], xh[kUnits][kPairs];
+    // unit i: xh, and dy (past the row's end 0, and with it all that is added)
+    auto unit = [&](int i, uint64_t (&xh)[kPairs], uint64_t (&d)[kPairs]) {
+      const int n = n0 - i * next_unit;
+      const uint4* place = at + i * P::kPieces * blockDim.x;
+      P::read(xh, place, base[0] + m * ld[0] + i * next_unit, n);
+      P::read(d, place + kOp * blockDim.x, base[1] + m * ld[1] + i * next_unit, n);
+      if (RES) {
+        uint64_t g[kPairs];
+        P::read(g, place + 2 * kOp * blockDim.x, base[2] + m * ld[2] + i * next_unit, n);
+#pragma unroll
+        for (int j = 0; j < kPairs; ++j) xh[j] = add2(xh[j], g[j]);
+      }
+#pragma unroll
+      for (int j = 0; j < kPairs; ++j) xh[j] = mul2(add2(xh[j], both(-st.x)), both(st.y));
+    };
+    auto add_columns = [&](int i, const uint64_t (&xh)[kPairs], const uint64_t (&d)[kPairs]) {
+#pragma unroll
+      for (int j = 0; j < kPairs; ++j) {
+        db[i][j] = add2(db[i][j], d[j]);
+        dw[i][j] = fma2(d[j], xh[j], dw[i][j]);
+      }
+    };
+    uint64_t u[KEEP ? kUnits : 1][kPairs], xh[KEEP ? kUnits : 1][kPairs];
     uint64_t t = 0, tx = 0;
 #pragma unroll
     for (int i = 0; i < kUnits; ++i) {
-      const int n = n0 - i * next_unit;
-      const uint4* place = at + i * P::kPieces * blockDim.x;
-      if (MODE == FULL || n > 0) {
-        P::read(xh[i], place, base[0] + m * ld[0] + i * next_unit, n);
-        P::read(u[i], place + kOp * blockDim.x, base[1] + m * ld[1] + i * next_unit, n);
+      const int k = KEEP ? i : 0;
+      if (MODE == FULL || n0 - i * next_unit > 0) {
+        unit(i, xh[k], u[k]);
+        if (KEEP) add_columns(i, xh[k], u[k]);
         uint64_t g[kPairs];
-        if (RES) {
-          P::read(g, place + 2 * kOp * blockDim.x, base[2] + m * ld[2] + i * next_unit, n);
-#pragma unroll
-          for (int j = 0; j < kPairs; ++j) xh[i][j] = add2(xh[i][j], g[j]);
-        }
-        w[i].pairs(g);
-        // (past the row's end u is 0, and with it all that is added)
+        if (!HOLD) weights(i, 0);
+        w[HOLD ? i : 0].pairs(g);
 #pragma unroll
         for (int j = 0; j < kPairs; ++j) {
-          xh[i][j] = mul2(add2(xh[i][j], both(-st.x)), both(st.y));
-          db[i][j] = add2(db[i][j], u[i][j]);
-          dw[i][j] = fma2(u[i][j], xh[i][j], dw[i][j]);
-          u[i][j] = mul2(u[i][j], g[j]);
-          t = add2(t, u[i][j]);
-          tx = fma2(u[i][j], xh[i][j], tx);
+          u[k][j] = mul2(u[k][j], g[j]);
+          t = add2(t, u[k][j]);
+          tx = fma2(u[k][j], xh[k][j], tx);
         }
       }
     }
-    if (a.dx == nullptr) continue;
-    const float2 c12 = group.sums<true>(sum2(t), sum2(tx), s_sums[buf]);
+    if (KEEP && a.dx == nullptr) continue;
+    float2 c12 = make_float2(0.f, 0.f);
+    if (a.dx != nullptr) c12 = group.sums<true>(sum2(t), sum2(tx), s_sums[buf]);
     buf ^= 1;
     const uint64_t c1 = both(-c12.x * a.inv_n), c2 = both(-c12.y * a.inv_n), rstd = both(st.y);
 #pragma unroll
     for (int i = 0; i < kUnits; ++i) {
-      const int n = n0 - i * next_unit;
+      const int n = n0 - i * next_unit, k = KEEP ? i : 0;
       uint4* place = at + i * P::kPieces * blockDim.x;
       uint64_t g[kPairs] = {};
       if (MODE == FULL || n > 0) {
+        if (!KEEP) {
+          unit(i, xh[k], u[k]);
+          add_columns(i, xh[k], u[k]);
+          if (!HOLD) weights(i, 0);
+          w[HOLD ? i : 0].pairs(g);
+#pragma unroll
+          for (int j = 0; j < kPairs; ++j) {
+            u[k][j] = mul2(u[k][j], g[j]);
+            g[j] = 0;
+          }
+        }
         if (DS) P::read(g, place + (kOps - 1) * kOp * blockDim.x, base[kOps - 1] + m * ld[kOps - 1] + i * next_unit, n);
 #pragma unroll
-        for (int j = 0; j < kPairs; ++j) g[j] = fma2(rstd, fma2(xh[i][j], c2, add2(u[i][j], c1)), g[j]);
+        for (int j = 0; j < kPairs; ++j) g[j] = fma2(rstd, fma2(xh[k][j], c2, add2(u[k][j], c1)), g[j]);
       }
-      if (MODE != ALIGNED || n > 0) P::write(g, place, static_cast<T*>(a.dx) + m * a.ld_dx + c0 + i * next_unit, n);
+      if (a.dx != nullptr && (MODE != ALIGNED || n > 0)) P::write(g, place, static_cast<T*>(a.dx) + m * a.ld_dx + c0 + i * next_unit, n);
     }
   }
   cp_wait(0);
   if (a.dw == nullptr && a.db == nullptr) return;
   // the groups' sums, added in order: [group][dw, db][column], then a block's partial sums
   __syncthreads();
-  const int cols = gt * kRowElements;
+  const int cols = gt * E;
   float* mine = reinterpret_cast<float*>(ring) + group.index * 2 * cols + c0;
 #pragma unroll
   for (int i = 0; i < kUnits; ++i)
@@ -523,14 +560,18 @@ __global__ void __launch_bounds__(kRowThreads, 1) norm_bwd_rows(const NormBwdArg
 // Warps of a group and groups of a block for rows of N elements: no more groups than rows for an SM.
 struct RowShape {
   int warps, groups;
-  RowShape(int N, int64_t M, int num_sms) : warps((N + 32 * kRowElements - 1) / (32 * kRowElements)), groups(kRowThreads / 32 / warps) {
+  RowShape(int N, int64_t M, int num_sms, int each) : warps((N + 32 * each - 1) / (32 * each)), groups(kRowThreads / 32 / warps) {
     const int64_t rows = (M + num_sms - 1) / num_sms;
     if (groups > rows) groups = (int)rows;
   }
   int threads() const { return warps * groups * 32; }
-  // vec: every row starts on a 16-byte boundary
-  static RowMode mode(int N, bool vec) { return !vec ? UNALIGNED : N % (32 * kRowElements) == 0 ? FULL : ALIGNED; }
 };
+// vec: every row starts on a 16-byte boundary
+RowMode row_mode(int N, bool vec, int each) { return !vec ? UNALIGNED : N % (32 * each) == 0 ? FULL : ALIGNED; }
+// 32 elements to a thread: wider rows than 512 threads of 16 hold (4000 x 16384: 124 us forward and 265 backward by a block
+// each, 91 and 149 so; 8000 x 5120, where a block holds one group of 16 and three of 32: 61 and 69 by those of 16, 56 and
+// 79 by those of 32). fp32 rows would leave no room to copy ahead.
+template <typename T> bool thick(int N, bool vec) { return sizeof(T) == 2 && vec && N > kRowsMaxN && N <= kThickMaxN; }
 
 // ------------------------------------------------------------------ wide rows
 template <typename T, typename W, bool VEC>
@@ -830,21 +871,28 @@ struct RowLaunch {
   }
 };
 
-template <typename T, typename W, int MODE, bool RES> cudaError_t fwd_rows(const NormArgs& a, int num_sms, cudaStream_t st) {
-  const RowLaunch l(a.M, RowShape(a.N, a.M, num_sms), 16 * (1 + RES) * Unit<T, MODE>::kUnits * Unit<T, MODE>::kPieces, 0, num_sms);
-  const cudaError_t e = allow_ring<norm_fwd_rows<T, W, MODE, RES>>(kRing);
+template <typename T, typename W, int MODE, int E, bool RES> cudaError_t fwd_rows(const NormArgs& a, int num_sms, cudaStream_t st) {
+  using P = Unit<T, MODE, E>;
+  const RowLaunch l(a.M, RowShape(a.N, a.M, num_sms, E), 16 * (1 + RES) * P::kUnits * P::kPieces, 0, num_sms);
+  const cudaError_t e = allow_ring<norm_fwd_rows<T, W, MODE, E, RES>>(kRing);
   if (e != cudaSuccess) return e;
-  return launch_pdl(norm_fwd_rows<T, W, MODE, RES>, dim3(l.grid), l.threads, l.smem, 1, st, a, l.warps, l.stages);
+  return launch_pdl(norm_fwd_rows<T, W, MODE, E, RES>, dim3(l.grid), l.threads, l.smem, 1, st, a, l.warps, l.stages);
+}
+template <typename T, typename W, int MODE, int E> cudaError_t fwd_mode(const NormArgs& a, int num_sms, cudaStream_t st) {
+  return a.res != nullptr ? fwd_rows<T, W, MODE, E, true>(a, num_sms, st) : fwd_rows<T, W, MODE, E, false>(a, num_sms, st);
 }
 
 template <typename T, typename W> cudaError_t norm_fwd(const NormArgs& a, int num_sms, cudaStream_t st) {
   const bool vec = a.M == 1 || (whole<T>(a.x, a.ld_x) && whole<T>(a.y, a.ld_y) && whole<T>(a.res, a.ld_res) && whole<T>(a.sum, a.ld_sum));
+  if constexpr (sizeof(T) == 2) {
+    if (thick<T>(a.N, vec))
+      return row_mode(a.N, vec, kThick) == FULL ? fwd_mode<T, W, FULL, kThick>(a, num_sms, st) : fwd_mode<T, W, ALIGNED, kThick>(a, num_sms, st);
+  }
   if (a.N <= kRowsMaxN) {
-    const bool res = a.res != nullptr;
-    switch (RowShape::mode(a.N, vec)) {
-      case UNALIGNED: return res ? fwd_rows<T, W, UNALIGNED, true>(a, num_sms, st) : fwd_rows<T, W, UNALIGNED, false>(a, num_sms, st);
-      case ALIGNED: return res ? fwd_rows<T, W, ALIGNED, true>(a, num_sms, st) : fwd_rows<T, W, ALIGNED, false>(a, num_sms, st);
-      case FULL: return res ? fwd_rows<T, W, FULL, true>(a, num_sms, st) : fwd_rows<T, W, FULL, false>(a, num_sms, st);
+    switch (row_mode(a.N, vec, kThin)) {
+      case UNALIGNED: return fwd_mode<T, W, UNALIGNED, kThin>(a, num_sms, st);
+      case ALIGNED: return fwd_mode<T, W, ALIGNED, kThin>(a, num_sms, st);
+      case FULL: return fwd_mode<T, W, FULL, kThin>(a, num_sms, st);
     }
   }
   const dim3 grid((unsigned)a.M);
@@ -852,24 +900,25 @@ template <typename T, typename W> cudaError_t norm_fwd(const NormArgs& a, int nu
              : launch_pdl(norm_fwd_wide<T, W, false>, grid, norm_threads(a.N), 0, 1, st, a);
 }
 
-template <typename T, typename W, int MODE, bool RES, bool DS>
+template <typename T, typename W, int MODE, int E, bool RES, bool DS>
 cudaError_t bwd_rows(const NormBwdArgs& a, int num_sms, int* parts, cudaStream_t st) {
-  const RowLaunch l(a.M, RowShape(a.N, a.M, num_sms), 16 * (2 + RES + DS) * Unit<T, MODE>::kUnits * Unit<T, MODE>::kPieces,
-                    2 * kRowElements * 4, num_sms);
-  const cudaError_t e = allow_ring<norm_bwd_rows<T, W, MODE, RES, DS>>(kRing);
+  using P = Unit<T, MODE, E>;
+  const RowLaunch l(a.M, RowShape(a.N, a.M, num_sms, E), 16 * (2 + RES + DS) * P::kUnits * P::kPieces, 2 * E * 4, num_sms);
+  const cudaError_t e = allow_ring<norm_bwd_rows<T, W, MODE, E, RES, DS>>(kRing);
   if (e != cudaSuccess) return e;
   *parts = l.grid;
-  return launch_pdl(norm_bwd_rows<T, W, MODE, RES, DS>, dim3(l.grid), l.threads, l.smem, 1, st, a, l.warps, l.stages);
+  return launch_pdl(norm_bwd_rows<T, W, MODE, E, RES, DS>, dim3(l.grid), l.threads, l.smem, 1, st, a, l.warps, l.stages);
 }
 
-template <typename T, typename W, int MODE> cudaError_t bwd_mode(const NormBwdArgs& a, int num_sms, int* parts, cudaStream_t st) {
+template <typename T, typename W, int MODE, int E> cudaError_t bwd_mode(const NormBwdArgs& a, int num_sms, int* parts, cudaStream_t st) {
   const bool ds = a.d_sum != nullptr && a.dx != nullptr;
-  if (a.res != nullptr) return ds ? bwd_rows<T, W, MODE, true, true>(a, num_sms, parts, st) : bwd_rows<T, W, MODE, true, false>(a, num_sms, parts, st);
-  return ds ? bwd_rows<T, W, MODE, false, true>(a, num_sms, parts, st) : bwd_rows<T, W, MODE, false, false>(a, num_sms, parts, st);
+  if (a.res != nullptr)
+    return ds ? bwd_rows<T, W, MODE, E, true, true>(a, num_sms, parts, st) : bwd_rows<T, W, MODE, E, true, false>(a, num_sms, parts, st);
+  return ds ? bwd_rows<T, W, MODE, E, false, true>(a, num_sms, parts, st) : bwd_rows<T, W, MODE, E, false, false>(a, num_sms, parts, st);
 }
 
 template <typename T, typename W> cudaError_t norm_bwd(const NormBwdArgs& a, int num_sms, cudaStream_t st) {
-  const bool sums = a.dw != nullptr || a.db != nullptr, rows = a.N <= kRowsMaxN;
+  const bool sums = a.dw != nullptr || a.db != nullptr;
   const bool vec = a.M == 1 || (whole<T>(a.x, a.ld_x) && whole<T>(a.dy, a.ld_dy) && whole<T>(a.res, a.ld_res));
   const bool vdx = a.M == 1 || (vec && whole<T>(a.dx, a.ld_dx) && whole<T>(a.d_sum, a.ld_ds));
   int parts = 0;
@@ -882,11 +931,16 @@ template <typename T, typename W> cudaError_t norm_bwd(const NormBwdArgs& a, int
     d.dw = d.db = nullptr;
     return norm_bwd<T, W>(d, num_sms, st);
   }
-  if (rows) {
-    switch (RowShape::mode(a.N, vdx)) {
-      case UNALIGNED: e = bwd_mode<T, W, UNALIGNED>(a, num_sms, &parts, st); break;
-      case ALIGNED: e = bwd_mode<T, W, ALIGNED>(a, num_sms, &parts, st); break;
-      case FULL: e = bwd_mode<T, W, FULL>(a, num_sms, &parts, st); break;
+  const bool wide = !thick<T>(a.N, vdx) && a.N > kRowsMaxN;
+  if (thick<T>(a.N, vdx)) {
+    if constexpr (sizeof(T) == 2)
+      e = row_mode(a.N, vdx, kThick) == FULL ? bwd_mode<T, W, FULL, kThick>(a, num_sms, &parts, st)
+                                             : bwd_mode<T, W, ALIGNED, kThick>(a, num_sms, &parts, st);
+  } else if (!wide) {
+    switch (row_mode(a.N, vdx, kThin)) {
+      case UNALIGNED: e = bwd_mode<T, W, UNALIGNED, kThin>(a, num_sms, &parts, st); break;
+      case ALIGNED: e = bwd_mode<T, W, ALIGNED, kThin>(a, num_sms, &parts, st); break;
+      case FULL: e = bwd_mode<T, W, FULL, kThin>(a, num_sms, &parts, st); break;
     }
   } else if (sums) {   // columns first: dx may be the buffer of an operand
     int64_t share = (a.M + kNormParts - 1) / kNormParts;
@@ -899,7 +953,7 @@ template <typename T, typename W> cudaError_t norm_bwd(const NormBwdArgs& a, int
   if (e == cudaSuccess && sums)
     e = launch_pdl(norm_join_kernel<W>, dim3((a.N + 31) / 32, 2), 256, 0, 1, st, (const float*)a.part, parts, a.N,
                    static_cast<W*>(a.dw), static_cast<W*>(a.db));
-  if (e != cudaSuccess || rows || a.dx == nullptr) return e;
+  if (e != cudaSuccess || !wide || a.dx == nullptr) return e;
   const dim3 grid((unsigned)a.M);
   return vdx ? launch_pdl(norm_dx_wide<T, W, true>, grid, norm_threads(a.N), 0, 1, st, a)
              : launch_pdl(norm_dx_wide<T, W, false>, grid, norm_threads(a.N), 0, 1, st, a);

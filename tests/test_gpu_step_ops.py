@@ -102,7 +102,7 @@ TYPES = [(BF, BF), (BF, F32), (F32, F32)]
 @pytest.mark.parametrize("dtype,w_dtype", TYPES)
 @pytest.mark.parametrize("M,N", [(1, 1), (3, 2), (1, 7), (5, 8), (33, 9), (200, 64), (7, 65), (64, 127), (777, 1001), (1, 1001),
                                  (300, 1024), (41, 1032), (513, 2048), (19, 2056), (100, 4096), (9, 4097), (350, 7680), (3, 8191),
-                                 (77, 8192), (5, 8200), (6, 16384), (4, 32761), (3, 32768), (1500, 512), (2000, 200)])
+                                 (77, 8192), (5, 8200), (400, 12288), (6, 16384), (330, 9000), (5, 16392), (4, 32761), (3, 32768), (1500, 512), (2000, 200)])
 def test_norm_sizes(M, N, dtype, w_dtype):
     _check_norm(M, N, dtype, w_dtype, residual=(M + N) % 2 == 0, bias=M % 3 != 0, seed=M + N)
 

@@ -57,7 +57,8 @@ def test_gradients_of_a_step(T, dtype, bound):
     x64 = x.cpu().double().requires_grad_(True)
     want = _plain_loss(w, x64, tokens.cpu(), k, block.layer.saved["topk_idx"].cpu().long(), ex.ENTROPY)
     want.backward()
-    assert abs(float(loss) - float(want)) <= bound * abs(float(want))
+    want = float(want.detach())
+    assert abs(float(loss) - want) <= bound * abs(want)
     for name, ref in {**{n: t.grad for n, t in w.items()}, "x": x64.grad}.items():
         got = grads[name].cpu().double()
         assert float((got - ref).norm()) <= bound * float(ref.norm()), name

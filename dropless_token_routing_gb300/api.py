@@ -683,13 +683,13 @@ class LayerNorm:
 
     ``forward(x, residual=None, save=False)`` returns y [M, N], or (y, s) with a residual: the layer's own
     buffers (written by the next call) unless ``out`` and ``sum_out`` are given, which may be x or the
-    residual. With ``save=True`` it keeps what was normed (s, or x itself: unchanged until then) for
+    residual. With ``save=True`` it keeps what was normed (unchanged until then) for
     ``backward(dy, d_sum=None)``, which returns dict(dx, dw, db) (own buffers too; ``need`` names those to
     compute; ``out`` takes dx and may be dy, d_sum or what was kept). d_sum is the gradient of s by its other
-    way; dx is the gradient of x and of the residual. bf16 rows with fp32 weights keep x and the residual
-    in place of s, whose rounding the gradient of the weight would show (s where a result has taken
-    the place of one of them). One instance serves one stream at a time, which waits for
-    the one it was made on.
+    way; dx is the gradient of x and of the residual. What is kept is x and, in bf16, the residual: the
+    rounding of s would show in the gradient of the weight. It is s for fp32 rows, and where a result has taken
+    the place of x or the residual. One instance serves one stream at a time, which waits for the one it was
+    made on.
     """
 
     def __init__(self, weight, bias=None, eps=1e-5, max_rows=1, dtype=None, device=None, stream=None):
@@ -787,7 +787,7 @@ class LayerNorm:
             stats = (views.get(("stats", M)) or self._view("stats", M, stream))[1]
             if residual is None:
                 self._kept = x, xp, ld_x, None, None, 0
-            elif dt is not self.w_dtype and xp != sp and xp != yp and rp != sp and rp != yp:
+            elif size == 2 and xp != sp and xp != yp and rp != sp and rp != yp:
                 self._kept = x, xp, ld_x, residual, rp, ld_r
             else:
                 self._kept = s, sp, ld_s, None, None, 0

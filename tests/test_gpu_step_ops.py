@@ -76,8 +76,8 @@ def _check_norm(M, N, dtype, w_dtype, residual, bias, seed=0, eps=1e-5, shift=0.
     if residual:
         _near(s_got, s, dtype, s.abs(), steps=2, what="sum")
     grads = ln.backward(cuda(dy), d_sum=cuda(ds))
-    # what the backward reads: the sum as it was rounded, or (fp32 weights) x and the residual
-    kept = s if dtype != w_dtype else s_got.detach().cpu()
+    # what the backward reads: x and the residual in bf16, the sum as it was rounded in fp32
+    kept = s if dtype == BF else s_got.detach().cpu()
     xh, u, dx, dw, db = _norm_grads(kept, mean, rstd, w, dy, ds)
     dx_terms = rstd * terms(u) * (1 + terms(xh)) * (1 + spread) + (ds.double().abs() if ds is not None else 0)
     _near(grads["dx"], dx, dtype, dx_terms, what="dx")
@@ -156,7 +156,8 @@ def test_norm_in_place(dtype, N):
     x, r, dy, ds = (_rand(g, M, N, dtype=dtype).cuda() for _ in range(4))
     w, b = _rand(g, N, dtype=dtype).cuda(), _rand(g, N, dtype=dtype).cuda()
     ln, other = A.LayerNorm(w, b, max_rows=M), A.LayerNorm(w, b, max_rows=M)
-    y, s = ln.forward(x, residual=r, save=True)
+    r0 = r.clone()
+    y, s = ln.forward(x, residual=r0, sum_out=r0, save=True)     # (the sum is kept, as below)
     grads = ln.backward(dy, d_sum=ds)
     x1, r1 = x.clone(), r.clone()
     y1, s1 = other.forward(x1, residual=r1, out=x1, sum_out=r1, save=True)

@@ -301,12 +301,13 @@ def test_norm_hands_over_strides_and_what_it_kept(lib):
     assert v[0] == ln._bufs["sum"].data_ptr() and v[1] is None      # the sum
     d = v[6]
     assert (d["ld_x"], d["ld_res"], d["ld_sum"], d["ld_y"], d["ld_dx"]) == (n, 0, 66, 80, 96)
-    # fp32 weights beside bf16 rows: x and the residual, unless one of them was overwritten
-    ln = layer_norm(dtype=BF, w_dtype=F32)
+    # bf16 rows: x and the residual, unless one of them was overwritten
     x, r = z(4, n, dtype=BF), z(4, n, dtype=BF)
-    ln.forward(x, residual=r, save=True, stream=ST)
-    ln.backward(x, stream=ST)
-    assert lib.last("moe_norm_bwd")[:2] == [x.data_ptr(), r.data_ptr()]
+    for w_dtype in (BF, F32):
+        ln = layer_norm(dtype=BF, w_dtype=w_dtype)
+        ln.forward(x, residual=r, save=True, stream=ST)
+        ln.backward(x, stream=ST)
+        assert lib.last("moe_norm_bwd")[:2] == [x.data_ptr(), r.data_ptr()]
     ln.forward(x, residual=r, sum_out=r, save=True, stream=ST)
     ln.backward(x, stream=ST)
     assert lib.last("moe_norm_bwd")[:2] == [r.data_ptr(), None]

@@ -707,7 +707,7 @@ class LayerNorm:
         if self._need == 0:
             raise N.MoeError(N.STATUS_CODE["MOE_ERR_BAD_DIMS"], "moe_norm_workspace_bytes")
         self.ws = None
-        self._bufs, self._views, self._kept = {}, {}, None
+        self._bufs, self._views, self._shapes, self._kept = {}, {}, {}, None
         self._dims_ref, self._bwd_ref = ctypes.byref(self.dims), ctypes.byref(self._bwd_dims)
         self._fwd, self._bwd = N.lib().moe_norm_fwd, N.lib().moe_norm_bwd
 
@@ -731,6 +731,12 @@ class LayerNorm:
         v = self._views[(name, M)] = t if M is None else t[:M], t.data_ptr()
         return v
 
+    def _shape(self, M):
+        if M > self.max_rows:
+            raise ValueError(f"{M} rows, the layer was made for {self.max_rows}")
+        s = self._shapes[M] = torch.Size((M, self.N))
+        return s
+
     def _given(self, name, t, M):
         """Checks a result's place that the caller gives; returns the stride between its rows."""
         ld = _matrix(t, name, self.dtype, M, self.N, self.device)
@@ -740,40 +746,37 @@ class LayerNorm:
         return ld
 
     def forward(self, x, residual=None, save=False, out=None, sum_out=None, stream=None):
-        M, n, dev, dt, size, views = x.shape[0], self.N, self.device, self.dtype, self._size, self._views
-        if M > self.max_rows:
-            raise ValueError(f"{M} rows, the layer was made for {self.max_rows}")
-        shape = (M, n)
+        M, n, dev, dt, views = x.shape[0], self.N, self.device, self.dtype, self._views
         # (checked here, and said there: a call's host time is near the kernel's own for one row)
+        shape = self._shapes.get(M) or self._shape(M)
         ld_x = n if x.dtype is dt and x.shape == shape and x.is_contiguous() and x.device == dev else _matrix(x, "x", dt, M, n, dev)
         w, b = self.weight, self.bias
         if w is not self._w_ref() or b is not self._b_ref() or w.data_ptr() != self._w_ptr or (b is not None and b.data_ptr() != self._b_ptr):
             self._bind()
+        xp, row = x.data_ptr(), M * self._size     # (row times a stride: the span of rows that far apart)
         if out is None:
             y, yp = views.get(("y", M)) or self._view("y", M, stream)
             ld_y = n
         else:
             y, yp, ld_y = out, out.data_ptr(), self._given("out", out, M)
-        xp, row = x.data_ptr(), M * size     # (row times a stride: the span of rows that far apart)
-        if xp < yp + row * ld_y and yp < xp + row * ld_x:
+        if -row * ld_x < xp - yp < row * ld_y:
             _in_place("x", x, ld_x, y, ld_y, "the output")
-        sp = rp = None
+        sp = rp = stats = None
         ld_s = ld_r = 0
         if residual is not None:
             r = residual
             ld_r = n if r.dtype is dt and r.shape == shape and r.is_contiguous() and r.device == dev else _matrix(r, "residual", dt, M, n, dev)
+            rp = r.data_ptr()
             if sum_out is None:
                 s, sp = views.get(("sum", M)) or self._view("sum", M, stream)
                 ld_s = n
             else:
                 s, sp, ld_s = sum_out, sum_out.data_ptr(), self._given("sum_out", sum_out, M)
-            rp = r.data_ptr()
-            r_end, s_end = rp + row * ld_r, sp + row * ld_s
-            if rp < yp + row * ld_y and yp < r_end:
+            if -row * ld_r < rp - yp < row * ld_y:
                 _in_place("residual", r, ld_r, y, ld_y, "the output")
-            if rp < s_end and sp < r_end:
+            if -row * ld_r < rp - sp < row * ld_s:
                 _in_place("residual", r, ld_r, s, ld_s, "the sum")
-            if xp < s_end and sp < xp + row * ld_x:
+            if -row * ld_x < xp - sp < row * ld_s:
                 _in_place("x", x, ld_x, s, ld_s, "the sum")
             if (out is not None or sum_out is not None) and _overlap(y, ld_y, s, ld_s):
                 raise ValueError("out: overlaps the sum")
@@ -781,13 +784,12 @@ class LayerNorm:
             raise ValueError("sum_out: there is no residual to add")
         elif save and yp == xp and M:
             raise ValueError("out: x is needed for the backward")
-        stats = None
         self._kept = None
         if save:
             stats = (views.get(("stats", M)) or self._view("stats", M, stream))[1]
-            if residual is None:
+            if rp is None:
                 self._kept = x, xp, ld_x, None, None, 0
-            elif size == 2 and xp != sp and xp != yp and rp != sp and rp != yp:
+            elif self._size == 2 and xp != sp and xp != yp and rp != sp and rp != yp:
                 self._kept = x, xp, ld_x, residual, rp, ld_r
             else:
                 self._kept = s, sp, ld_s, None, None, 0
@@ -795,17 +797,18 @@ class LayerNorm:
         if key != self._set:
             D = self.dims
             D.M, D.ld_x, D.ld_res, D.ld_sum, D.ld_y = self._set = key
-        st = self._fwd(xp, rp, self._w_ptr, self._b_ptr, self._dims_ref, sp, yp, stats, _stream(stream, self._index))
+        st = self._fwd(xp, rp, self._w_ptr, self._b_ptr, self._dims_ref, sp, yp, stats,
+                       _raw_stream(self._index) if stream is None and _raw_stream is not None else _stream(stream, self._index))
         if st:
             N.check(st, "moe_norm_fwd")
-        return y if residual is None else (y, s)
+        return y if rp is None else (y, s)
 
     def backward(self, dy, d_sum=None, need=("dx", "dw", "db"), out=None, stream=None):
         if self._kept is None:
             raise ValueError("backward: the last forward did not save (save=True)")
         (x, xp, ld_x, res, rp, ld_r), n, dev, dt, views = self._kept, self.N, self.device, self.dtype, self._views
         M = x.shape[0]
-        shape, row = (M, n), M * self._size
+        shape, row = self._shapes[M], M * self._size
         w, b = self.weight, self.bias
         if w is not self._w_ref() or b is not self._b_ref() or w.data_ptr() != self._w_ptr or (b is not None and b.data_ptr() != self._b_ptr):
             self._bind()
@@ -823,10 +826,15 @@ class LayerNorm:
                 ld_dx = n
             else:
                 dx, dxp, ld_dx = out, out.data_ptr(), self._given("out", out, M)
-            end = dxp + row * ld_dx
-            for name, t, p, ld in (("dy", dy, yp, ld_y), ("x", x, xp, ld_x), ("residual", res, rp, ld_r), ("d_sum", d_sum, sp, ld_d)):
-                if t is not None and p < end and dxp < p + row * ld:
-                    _in_place(name, t, ld, dx, ld_dx, "dx")
+            end = row * ld_dx
+            if -row * ld_y < yp - dxp < end:
+                _in_place("dy", dy, ld_y, dx, ld_dx, "dx")
+            if -row * ld_x < xp - dxp < end:
+                _in_place("x", x, ld_x, dx, ld_dx, "dx")
+            if rp is not None and -row * ld_r < rp - dxp < end:
+                _in_place("residual", res, ld_r, dx, ld_dx, "dx")
+            if sp is not None and -row * ld_d < sp - dxp < end:
+                _in_place("d_sum", d_sum, ld_d, dx, ld_dx, "dx")
         if "dw" in need:
             dw, dwp = views.get(("dw", None)) or self._view("dw", None, stream)
         if "db" in need and b is not None:
@@ -876,39 +884,46 @@ class TokenLogprobs:
         self._top = top_idx, top_logprob
         self._ptrs = (self._logprob.data_ptr(), self._entropy.data_ptr(), self._stats.data_ptr(),
                       top_idx.data_ptr() if top else None, top_logprob.data_ptr() if top else None)
-        self._grad, self._views, self._saved = None, {}, None
+        self._grad, self._views, self._saved, self._set = None, {}, None, None
         self._dims_ref = ctypes.byref(self.dims)
         self._fwd, self._bwd = N.lib().moe_token_logprob, N.lib().moe_token_logprob_bwd
 
     def forward(self, scores, tokens=None, entropy=False, save=False, stream=None):
-        M, D, dev = scores.shape[0], self.dims, self.device
-        if M > self.max_rows:
-            raise ValueError(f"{M} rows, made for {self.max_rows}")
-        t = scores
-        ld = self.V if t.dtype is self.dtype and t.shape == (M, self.V) and t.is_contiguous() and t.device == dev else _matrix(
-            t, "scores", self.dtype, M, self.V, dev)
-        if tokens is not None:
-            _dense(tokens, "tokens", torch.int32, (M,), dev)
+        M, dev = scores.shape[0], self.device
         v = self._views.get(M)
         if v is None:
-            v = self._views[M] = (self._logprob[:M, 0], self._entropy[:M, 0], self._top[0][:M], self._top[1][:M])
+            if M > self.max_rows:
+                raise ValueError(f"{M} rows, made for {self.max_rows}")
+            v = self._views[M] = (torch.Size((M, self.V)), torch.Size((M,)), self._logprob[:M, 0], self._entropy[:M, 0],
+                                  self._top[0][:M], self._top[1][:M])
+        shape, of_rows, logprob, ent, top_idx, top_logprob = v
+        t = scores
+        ld = self.V if t.dtype is self.dtype and t.shape == shape and t.is_contiguous() and t.device == dev else _matrix(
+            t, "scores", self.dtype, M, self.V, dev)
         out = {}
         lp, ep, sp, ip, vp = self._ptrs
         if tokens is not None:
-            out["logprob"], tp = v[0], tokens.data_ptr()
-            if save and ip is not None and ip - 4 * M < tp < ip + 4 * M * self.top:
+            t = tokens
+            if t.dtype is not torch.int32 or t.shape != of_rows or not t.is_contiguous() or t.device != dev:
+                _dense(t, "tokens", torch.int32, of_rows, dev)
+            out["logprob"], tp = logprob, t.data_ptr()
+            if save and ip is not None and -4 * M < tp - ip < 4 * M * self.top:
                 raise ValueError("tokens: overlaps the result, and is needed for the backward")
         else:
             tp = lp = None
         if entropy:
-            out["entropy"] = v[1]
+            out["entropy"] = ent
         else:
             ep = None
-        if self.top:
-            out["top_idx"], out["top_logprob"] = v[2], v[3]
+        if ip is not None:
+            out["top_idx"], out["top_logprob"] = top_idx, top_logprob
         self._saved = (scores, ld, tokens, entropy) if save else None
-        D.M, D.ld = M, ld
-        st = self._fwd(scores.data_ptr(), tp, self._dims_ref, lp, ep, sp if save else None, ip, vp, _stream(stream, self._index))
+        key = M, ld
+        if key != self._set:
+            D = self.dims
+            D.M, D.ld = self._set = key
+        st = self._fwd(scores.data_ptr(), tp, self._dims_ref, lp, ep, sp if save else None, ip, vp,
+                       _raw_stream(self._index) if stream is None and _raw_stream is not None else _stream(stream, self._index))
         if st:
             N.check(st, "moe_token_logprob")
         return out
@@ -938,6 +953,7 @@ class TokenLogprobs:
                     raise ValueError(f"out: overlaps {name}")
         _in_place("scores", scores, ld, out, ld_g, "their gradient")
         D.M, D.ld, D.ld_grad = M, ld, ld_g
+        self._set = M, ld
         st = self._bwd(scores.data_ptr(), _p(tokens), self._stats.data_ptr(), self._entropy.data_ptr(), _p(d_logprob), _p(d_entropy),
                        self._dims_ref, out.data_ptr(), _stream(stream, self._index))
         if st:

@@ -241,7 +241,7 @@ const char* moe_status_string(int s) {
     case MOE_ERR_WORKSPACE_TOO_SMALL: return "workspace too small";
     case MOE_ERR_LAUNCH: return "kernel launch failed";
     case MOE_ERR_CUDA: return "CUDA call failed";
-    case MOE_ERR_UNSUPPORTED_DEVICE: return "bf16 grouped GEMM and the few-token operators need an sm_103 (GB300) device";
+    case MOE_ERR_UNSUPPORTED_DEVICE: return "bf16 grouped GEMM and the operators beside the layer need an sm_103 (GB300) device";
     case MOE_ERR_DEVICE_EXPERT_ID: return "device: expert id out of range or repeated in a row";
     case MOE_ERR_DEVICE_TIMEOUT: return "device: a bounded wait ran out";
     default: return "unknown status";

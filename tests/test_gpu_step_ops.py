@@ -414,6 +414,23 @@ def test_logprob_scores_beyond_31_bits():
     assert torch.equal(lp.backward(gl, out=scores), want)
 
 
+def test_logprob_of_more_than_31_bits_of_scores():
+    A, M, V = _api(), 17000, 131072
+    x = torch.randn(M, V, dtype=BF, device="cuda", generator=torch.Generator("cuda").manual_seed(1))
+    tokens = torch.randint(0, V, (M,), dtype=torch.int32, device="cuda")
+    lp = A.TokenLogprobs(M, V, top=2, dtype=BF)
+    out = lp.forward(x, tokens, save=True)
+    rows = torch.tensor([0, 1, 8191, 16383, 16384, 16385, M - 1])      # both sides of 2^31 elements
+    ref, p = _lp_ref(x[rows].cpu())
+    at = tokens[rows].cpu().long()[:, None]
+    _near(out["logprob"][rows], ref.gather(1, at)[:, 0], F32, 1 + ref.gather(1, at)[:, 0].abs())
+    assert torch.equal(out["top_idx"][rows].cpu(), _top_ref(x[rows].cpu(), 2))
+    g = torch.ones(M, device="cuda")
+    d = lp.backward(g, out=x)[rows].cpu()
+    want = torch.zeros_like(p).scatter_(1, at, 1.0) - p
+    _near(d, want, BF, torch.zeros_like(p).scatter_(1, at, 1.0) + p * (1 + ref.abs()), steps=160)
+
+
 def test_logprob_parts_on_their_own():
     """Alternatives without tokens; log probabilities alone; no rows."""
     A, g, V = _api(), _gen(5), 2000
@@ -623,6 +640,41 @@ def test_step_operators_in_a_graph():
         graph.replay()
         got = [t.clone() for t in outs]
         want, _ = step(*eager)
+        for a, e in zip(got, want):
+            assert torch.equal(a, e)
+
+
+def test_two_calls_at_once():
+    """Two sets of handles on two streams, their kernels interleaved: the results of each alone."""
+    A, M, N, V = _api(), 400, 1000, 6001
+    sets = []
+    for i in range(2):
+        g = _gen(30 + i)
+        w = _rand(g, N).cuda()
+        sets.append(dict(x=_rand(g, M, N).cuda(), dy=_rand(g, M, N).cuda(), scores=_rand(g, M, V).cuda(), gl=_rand(g, M).cuda(),
+                         tokens=torch.randint(0, V, (M,), generator=g, dtype=torch.int32).cuda(), ln=A.LayerNorm(w, max_rows=M),
+                         lp=A.TokenLogprobs(M, V, top=4), stream=torch.cuda.Stream()))
+    torch.cuda.synchronize()
+
+    def step(s):
+        y = s["ln"].forward(s["x"], save=True, stream=s["stream"])
+        grads = s["ln"].backward(s["dy"], stream=s["stream"])
+        out = s["lp"].forward(s["scores"], s["tokens"], save=True, stream=s["stream"])
+        d = s["lp"].backward(s["gl"], stream=s["stream"])
+        if "clip" not in s:
+            s["clip"] = A.GradClipper([grads["dx"], grads["dw"], d], stream=s["stream"])
+        return [y, grads["dx"], grads["dw"], *out.values(), d, s["clip"].norm(stream=s["stream"])]
+
+    alone = []
+    for s in sets:
+        results = step(s)
+        torch.cuda.synchronize()
+        alone.append([t.clone() for t in results])
+    torch.cuda.synchronize()
+    for _ in range(10):
+        both = [step(s) for s in sets]
+    torch.cuda.synchronize()
+    for got, want in zip(both, alone):
         for a, e in zip(got, want):
             assert torch.equal(a, e)
 

@@ -250,7 +250,9 @@ __device__ __forceinline__ void block_top(TopShared& t, const Places<T>& row, in
   }
 }
 
-// A row is a cluster's (one block for many rows): every block takes a slice, the first one joins their sums.
+// A row is a cluster's (one block for many rows): every block takes a slice, the first one joins their sums. Bound by HBM
+// for many rows (8192 x 131072 bf16: 301 us, 7.1 TB/s; 4096 x 32000 fp32 with entropy 79 us, 6.6 TB/s; the exponentials
+// alone would take 73 % of that time in bf16), by latency for few (one row of 131072 with 20 alternatives: 5.7 us).
 template <typename T, bool ENT, bool TOP>
 __global__ void __launch_bounds__(LT, (kBlocks<T, ENT, TOP>)) logprob_kernel(const LogprobArgs a) {
   __shared__ Sums s_sums[LW];
@@ -395,6 +397,7 @@ constexpr int GU = 4, GC = GU * LT * 8;   // the same of the gradient
 
 // Rows from the last one back: where the gradient follows the forward pass at once, as a loss's does, L2 still
 // holds the rows read last (4096 x 32000 fp32: both 236 us from the first row on, 233 so).
+// Bound by HBM: 8192 x 131072 bf16 599 us, 4096 x 32000 fp32 with entropy 150 us, both 7.0-7.2 TB/s.
 template <typename T>
 __global__ void __launch_bounds__(LT) logprob_bwd_kernel(const LogprobBwdArgs a) {
   pdl_start();

@@ -993,8 +993,9 @@ class GradClipper:
         self._np, self._sp = self._norm.data_ptr(), self.scale.data_ptr()
         self._clip_table, self._norm_table = (N.Grad * max(n, 1))(), (N.Grad * max(n, 1))()
         self._call = N.lib().moe_clip_grads
-        tensors = self.grads if self.out is self.grads else self.grads + self.out
-        self._ask = [t.data_ptr for t in tensors] + [t.numel for t in tensors]
+        # where the gradients and the results are, and how large
+        self._ask = [f for t in self.grads for f in (t.data_ptr, t.numel)]
+        self._ask_out = [] if self.out is self.grads else [f for t in self.out for f in (t.data_ptr, t.numel)]
         self._bind()
 
     def _bind(self):
@@ -1012,7 +1013,7 @@ class GradClipper:
             self._clip_table[i] = N.Grad(g.data_ptr(), o.data_ptr(), g.numel(), _dt(g.dtype))
             self._norm_table[i] = N.Grad(g.data_ptr(), None, g.numel(), _dt(g.dtype))
         self._check_places()
-        self._places = [ask() for ask in self._ask]
+        self._places, self._out_places = [f() for f in self._ask], [f() for f in self._ask_out]
 
     def _check_places(self):
         """No result may overlap another one, or a gradient other than its own (that one only as a whole)."""
@@ -1035,8 +1036,6 @@ class GradClipper:
                 read = max(read, (b, gradient))
 
     def _run(self, table, max_norm, stream):
-        if self._places != [ask() for ask in self._ask]:
-            self._bind()
         st = self._call(table, len(self.grads), max_norm, self._np, self._sp, self.ws.ptr, self.ws.nbytes,
                         _stream(stream, self._index))
         if st:
@@ -1044,7 +1043,11 @@ class GradClipper:
         return self._norm
 
     def norm(self, stream=None):
+        if [f() for f in self._ask] != self._places:
+            self._bind()
         return self._run(self._norm_table, float("inf"), stream)
 
     def clip(self, max_norm, stream=None):
+        if [f() for f in self._ask] != self._places or [f() for f in self._ask_out] != self._out_places:
+            self._bind()
         return self._run(self._clip_table, max_norm, stream)

@@ -20,10 +20,12 @@ namespace moe {
 namespace {
 
 constexpr int LT = 256, LW = LT / 32;   // threads and warps of a block
-constexpr int LU = 2, LC = LU * LT * 8;   // vectors of 8 scores that a thread takes at a time, and a block's scores then
-// Blocks of an SM. 4096 x 32000 fp32 with entropy: 79 us by 5, 81 by 4, 91 by 6; bf16: 52, 55, 48; 8192 x 131072 bf16
-// without: 300 by 5, 315 by 6; with alternatives, 1024 x 131072: 68 by 4, 86 by 3 (5 have no room for the registers).
-template <typename T, bool ENT, bool TOP> constexpr int kBlocks = TOP ? 4 : ENT && sizeof(T) == 2 ? 6 : 5;
+// A thread takes LU vectors of 8 scores at a time: 2, or 4 of few rows, whose blocks are three to an SM at most and have
+// long slices (30 x 131072 bf16: 5.8 us by 2, 4.5 by 4; 8 leave too much to a slice's last, partial step: 32000 scores 2.6, 3.4).
+// Blocks of an SM. LU = 2: 4096 x 32000 fp32 with entropy 79 us by 5, 81 by 4, 91 by 6; bf16 52, 55, 48; 8192 x 131072
+// bf16 without 300 by 5, 315 by 6; with alternatives, 1024 x 131072, 68 by 4, 86 by 3.
+template <typename T, int LU, bool ENT, bool TOP>
+constexpr int kBlocks = LU == 4 ? 3 : TOP ? 4 : ENT && sizeof(T) == 2 ? 6 : 5;
 constexpr int kMaxCluster = 8;
 constexpr float kLog2e = 1.44269504088896340736f, kLowest = -3.402823466e38f, kInf = __builtin_huge_valf();
 
@@ -108,28 +110,28 @@ template <typename T> struct Places {
 };
 
 // The highest of a thread's vectors (NaN aside): two bf16 at a time
-__device__ __forceinline__ float highest(const Vec8<__nv_bfloat16> (&v)[LU]) {
+template <int LU> __device__ __forceinline__ float highest(const Vec8<__nv_bfloat16> (&v)[LU]) {
   const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(v);
   __nv_bfloat162 m = h[0];
 #pragma unroll
   for (int i = 1; i < 4 * LU; ++i) m = __hmax2(m, h[i]);
   return fmaxf(__low2float(m), __high2float(m));
 }
-__device__ __forceinline__ float highest(const Vec8<float> (&v)[LU]) {
+template <int LU> __device__ __forceinline__ float highest(const Vec8<float> (&v)[LU]) {
   const float* h = reinterpret_cast<const float*>(v);
   float m = h[0];
 #pragma unroll
   for (int i = 1; i < 8 * LU; ++i) m = fmaxf(m, h[i]);
   return m;
 }
-__device__ __forceinline__ float highest(const float (&f)[LU][8]) {
+template <int LU> __device__ __forceinline__ float highest(const float (&f)[LU][8]) {
   float m = f[0][0];
 #pragma unroll
   for (int i = 1; i < 8 * LU; ++i) m = fmaxf(m, f[i / 8][i % 8]);
   return m;
 }
 // Adds a thread's LU vectors, the highest of which is `top`, to its sums; ENT: D too.
-template <bool ENT> __device__ __forceinline__ void add_scores(Sums& s, const float (&f)[LU][8], float top) {
+template <bool ENT, int LU> __device__ __forceinline__ void add_scores(Sums& s, const float (&f)[LU][8], float top) {
   if (top > s.m) s.to(top);
   const uint64_t nm = both(-s.m), l2e = both(kLog2e);
   uint64_t S[2] = {0, 0}, D[2] = {0, 0};   // two chains of additions
@@ -253,8 +255,9 @@ __device__ __forceinline__ void block_top(TopShared& t, const Places<T>& row, in
 // A row is a cluster's (one block for many rows): every block takes a slice, the first one joins their sums. Bound by HBM
 // for many rows (8192 x 131072 bf16: 301 us, 7.1 TB/s; 4096 x 32000 fp32 with entropy 79 us, 6.6 TB/s; the exponentials
 // alone would take 73 % of that time in bf16), by latency for few (one row of 131072 with 20 alternatives: 5.7 us).
-template <typename T, bool ENT, bool TOP>
-__global__ void __launch_bounds__(LT, (kBlocks<T, ENT, TOP>)) logprob_kernel(const LogprobArgs a) {
+template <typename T, int LU, bool ENT, bool TOP>
+__global__ void __launch_bounds__(LT, (kBlocks<T, LU, ENT, TOP>)) logprob_kernel(const LogprobArgs a) {
+  constexpr int LC = LU * LT * 8;   // scores that a block takes at a time
   __shared__ Sums s_sums[LW];
   __shared__ float2 s_row;       // the row's maximum and ln S
   __shared__ TopShared s_top[1];
@@ -451,6 +454,15 @@ __global__ void __launch_bounds__(LT) logprob_bwd_kernel(const LogprobBwdArgs a)
   }
 }
 
+template <typename T, int LU> cudaError_t logprob_lu(const LogprobArgs& a, dim3 grid, int c, cudaStream_t st) {
+  const bool ent = a.entropy != nullptr;
+  if (a.n_top > 0)
+    return ent ? launch_pdl(logprob_kernel<T, LU, true, true>, grid, LT, 0, c, st, a)
+               : launch_pdl(logprob_kernel<T, LU, false, true>, grid, LT, 0, c, st, a);
+  return ent ? launch_pdl(logprob_kernel<T, LU, true, false>, grid, LT, 0, c, st, a)
+             : launch_pdl(logprob_kernel<T, LU, false, false>, grid, LT, 0, c, st, a);
+}
+
 template <typename T> cudaError_t logprob(const LogprobArgs& a, int num_sms, cudaStream_t st) {
   // Few rows: clusters, while all blocks are resident (by their registers 4 on an SM with alternatives, 6 of bf16 without, 5 of
   // fp32) and a slice keeps every thread at two vectors. 200 x 131072 bf16: 18 us by 2, 11 by 4, 14 by 8; with 20
@@ -459,10 +471,7 @@ template <typename T> cudaError_t logprob(const LogprobArgs& a, int num_sms, cud
   int c = 1;
   while (c < kMaxCluster && a.M * c * 2 <= resident && a.V > c * LT * 16) c *= 2;
   const dim3 grid((unsigned)(a.M * c));
-  const bool ent = a.entropy != nullptr;
-  if (a.n_top > 0)
-    return ent ? launch_pdl(logprob_kernel<T, true, true>, grid, LT, 0, c, st, a) : launch_pdl(logprob_kernel<T, false, true>, grid, LT, 0, c, st, a);
-  return ent ? launch_pdl(logprob_kernel<T, true, false>, grid, LT, 0, c, st, a) : launch_pdl(logprob_kernel<T, false, false>, grid, LT, 0, c, st, a);
+  return a.M * c <= 3 * num_sms && a.V >= c * 6144 ? logprob_lu<T, 4>(a, grid, c, st) : logprob_lu<T, 2>(a, grid, c, st);
 }
 
 template <typename T> cudaError_t logprob_bwd(const LogprobBwdArgs& a, int num_sms, cudaStream_t st) {

@@ -361,28 +361,34 @@ __global__ void __launch_bounds__(LT, (kBlocks<T, LU, ENT, TOP>)) logprob_kernel
       TopShared& t = s_top[0];
       const int r = threadIdx.x / kMaxTop, i = threadIdx.x % kMaxTop;
       unsigned long long key = 0;
-      if (r < (int)ranks) key = ranks > 1 ? (unsigned long long)peer_ld64(smem_u32(&t.sorted[i]), r) : t.sorted[i];
-      t.key[threadIdx.x] = key;   // the blocks' lists in a row
-      __syncthreads();
-      if (key != 0) {
-        // its place: the higher keys of every list (its own among them), in the lists' 32 descending places
-        int higher[kMaxCluster] = {}, at = 0;
+      int at = i;   // the key's place
+      if (ranks > 1) {
+        if (r < (int)ranks) key = (unsigned long long)peer_ld64(smem_u32(&t.sorted[i]), r);
+        t.key[threadIdx.x] = key;   // the blocks' lists in a row
+        __syncthreads();
+        if (key != 0) {
+          // the higher keys of every list (its own among them), in the lists' 32 descending places
+          int higher[kMaxCluster] = {};
 #pragma unroll
-        for (int step = 16; step > 0; step >>= 1)
+          for (int step = 16; step > 0; step >>= 1)
 #pragma unroll
-          for (int o = 0; o < kMaxCluster; ++o)
-            if (t.key[o * kMaxTop + higher[o] + step - 1] > key) higher[o] += step;
+            for (int o = 0; o < kMaxCluster; ++o)
+              if (t.key[o * kMaxTop + higher[o] + step - 1] > key) higher[o] += step;
+          at = 0;
 #pragma unroll
-        for (int o = 0; o < kMaxCluster; ++o) at += higher[o] + (t.key[o * kMaxTop + higher[o]] > key);
-        if (at < a.n_top) {
-          const uint32_t b = (uint32_t)(key >> 32);
-          const float x = __uint_as_float(b & 0x80000000u ? b & 0x7fffffffu : ~b);
-          a.top_idx[m * a.n_top + at] = (int)index_of(key);
-          a.top_logprob[m * a.n_top + at] = (x - s_row.x) - s_row.y;
+          for (int o = 0; o < kMaxCluster; ++o) at += higher[o] + (t.key[o * kMaxTop + higher[o]] > key);
         }
+      } else if (r == 0) {
+        key = t.sorted[i];
+      }
+      const int found = __syncthreads_count(key != 0);   // (and s_row is there)
+      if (key != 0 && at < a.n_top) {
+        const uint32_t b = (uint32_t)(key >> 32);
+        const float x = __uint_as_float(b & 0x80000000u ? b & 0x7fffffffu : ~b);
+        a.top_idx[m * a.n_top + at] = (int)index_of(key);
+        a.top_logprob[m * a.n_top + at] = (x - s_row.x) - s_row.y;
       }
       // places that no key took
-      const int found = __syncthreads_count(key != 0);
       if ((int)threadIdx.x >= found && (int)threadIdx.x < a.n_top) {
         a.top_idx[m * a.n_top + threadIdx.x] = -1;
         a.top_logprob[m * a.n_top + threadIdx.x] = -kInf;

@@ -159,80 +159,56 @@ struct alignas(16) TopShared {
   unsigned long long key[LT];          // candidates, unordered
   unsigned long long sorted[kMaxTop];  // this block's alternatives, descending
   unsigned long long warp[2][LW];
+  int equal[2][LW];
   float group[64];                     // maxima of 4 threads each
   int thread[LT];                      // threads that hold a candidate
   float bound;
   int threads, count;
 };
 
-// The block's n highest keys among places [j0, j1) of the row, descending, into t.sorted (0: no more).
-// `mine`: the highest score that this thread took (vectors threadIdx.x, + LT, ..). The n-th highest of
-// 64 groups' maxima is no higher than the n-th highest score, and few scores reach it (24 of 131072
-// in random order, n = 20): only the scores of threads that hold one are looked at again, by all of
-// the block's threads. Rows where more than 256 reach it (in order, or of few values) are taken one key at a time.
+// The lowest number above x.
+__device__ __forceinline__ float next_above(float x) {
+  const int b = __float_as_int(x + 0.f);   // -0 is +0
+  return __int_as_float(b < 0 ? b - 1 : b + 1);
+}
+
+// Fills t.sorted from place `count` on with scores equal to x, in order.
 template <typename T>
-__device__ __forceinline__ void block_top(TopShared& t, const Places<T>& row, int j0, int j1, float mine, int n) {
+__device__ __forceinline__ void take_equal(TopShared& t, const Places<T> row, int j0, int j1, float x, int count, int n) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  float g = mine;
-  g = fmaxf(g, __shfl_xor_sync(0xffffffffu, g, 1));
-  g = fmaxf(g, __shfl_xor_sync(0xffffffffu, g, 2));
-  if ((lane & 3) == 0) t.group[tid >> 2] = g;
-  if (tid == 0) t.threads = t.count = 0;
-  if (tid < kMaxTop) t.sorted[tid] = 0;
-  __syncthreads();
-  if (tid < 64) {
-    g = t.group[tid];
-    int above = 0;
-#pragma unroll
-    for (int i = 0; i < 64; i += 4) {
-      const float4 o = *reinterpret_cast<const float4*>(&t.group[i]);
-      above += (o.x > g || (o.x == g && i < tid)) + (o.y > g || (o.y == g && i + 1 < tid)) + (o.z > g || (o.z == g && i + 2 < tid)) +
-               (o.w > g || (o.w == g && i + 3 < tid));
-    }
-    if (above == n - 1) t.bound = g;
-  }
-  __syncthreads();
-  const float bound = t.bound;
-  const uint32_t who = __ballot_sync(0xffffffffu, mine >= bound);
-  int first = 0;
-  if (lane == 0 && who != 0u) first = atomicAdd(&t.threads, __popc(who));
-  first = __shfl_sync(0xffffffffu, first, 0);
-  if (mine >= bound) t.thread[first + __popc(who & ((1u << lane) - 1))] = tid;
-  __syncthreads();
-  const int steps = (j1 - j0 + LT * 8 - 1) / (LT * 8), items = t.threads * steps;
-  for (int k = tid; k < items; k += LT) {
-    const int j = j0 + t.thread[k / steps] * 8 + k % steps * (LT * 8);
-    if (j < j1) {
+  for (int j = j0, step = 0; j < j1 && count < n; j += LT * 8, step ^= 1) {
+    const int k = j + tid * 8;
+    uint32_t equal = 0;
+    if (k < j1) {
       Vec8<T> v;
       float f[8];
-      row.load(v, j);
-      row.scores(f, v, j);
-      uint32_t high = 0;
+      row.load(v, k);
+      row.scores(f, v, k);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) high |= (uint32_t)(f[i] >= bound && f[i] > -kInf) << i;
-      if (high != 0u) {
-        int at = atomicAdd(&t.count, __popc(high));
+      for (int i = 0; i < 8; ++i) equal |= (uint32_t)(f[i] == x) << i;
+    }
+    int before = __popc(equal);   // the warp's, up to this thread's
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-          if (high >> i & 1) {
-            if (at < LT) t.key[at] = key_of(f[i], j + i - row.lead);
-            ++at;
-          }
-      }
+    for (int o = 1; o < 32; o <<= 1) {
+      const int w = __shfl_up_sync(0xffffffffu, before, o);
+      if (lane >= o) before += w;
     }
-  }
-  __syncthreads();
-  const int count = t.count;
-  if (count <= LT) {
-    if (tid < count) {
-      const unsigned long long key = t.key[tid];
-      int above = 0;
-#pragma unroll 4
-      for (int i = 0; i < count; ++i) above += t.key[i] > key;
-      if (above < n) t.sorted[above] = key;
+    if (lane == 31) t.equal[step][warp] = before;
+    __syncthreads();
+    before += count - __popc(equal);
+#pragma unroll
+    for (int w = 0; w < LW; ++w) {
+      const int o = t.equal[step][w];
+      count += o;
+      if (w < warp) before += o;
     }
-    return;
+    for (; equal != 0u && before < n; equal &= equal - 1, ++before) t.sorted[before] = key_of(x, k + __ffs(equal) - 1 - row.lead);
   }
+}
+
+// The n highest keys, one at a time.
+template <typename T> __device__ __forceinline__ void take_one_by_one(TopShared& t, const Places<T> row, int j0, int j1, int n) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   unsigned long long best = ~0ull, top = ~0ull;
   for (int k = 0; k < n; ++k) {
     if (best == top) {   // this thread's next key
@@ -262,9 +238,97 @@ __device__ __forceinline__ void block_top(TopShared& t, const Places<T>& row, in
   }
 }
 
+// The block's n highest keys among places [j0, j1) of the row, descending, into t.sorted (0: no more).
+// `mine`: the highest score that this thread took (vectors threadIdx.x, + LT, ..; -inf: none). The n-th highest of
+// 64 groups' maxima is no higher than the n-th highest score, and few scores reach it (24 of 131072
+// in random order, n = 20): only the scores of threads that hold one are looked at again, by all of
+// the block's threads. Where more than 256 reach it, mostly because they are equal to it (a finite mask that leaves
+// fewer than n tokens, a row of one value), those above it are taken, and then of those equal to it the first ones (one
+// row of 131072 with such a mask 7.2 us, 48 of them 10.6; by one key at a time 40 and 59). Rows where more than 256 are
+// above it (in order) are taken one key at a time.
+template <typename T>
+__device__ __forceinline__ void block_top(TopShared& t, const Places<T>& row, int j0, int j1, float mine, int n) {
+  const int tid = threadIdx.x, lane = tid & 31;
+  float g = mine;
+  g = fmaxf(g, __shfl_xor_sync(0xffffffffu, g, 1));
+  g = fmaxf(g, __shfl_xor_sync(0xffffffffu, g, 2));
+  if ((lane & 3) == 0) t.group[tid >> 2] = g;
+  if (tid == 0) t.threads = t.count = 0;
+  if (tid < kMaxTop) t.sorted[tid] = 0;
+  __syncthreads();
+  if (tid < 64) {
+    g = t.group[tid];
+    int higher = 0;
+#pragma unroll
+    for (int i = 0; i < 64; i += 4) {
+      const float4 o = *reinterpret_cast<const float4*>(&t.group[i]);
+      higher += (o.x > g || (o.x == g && i < tid)) + (o.y > g || (o.y == g && i + 1 < tid)) + (o.z > g || (o.z == g && i + 2 < tid)) +
+               (o.w > g || (o.w == g && i + 3 < tid));
+    }
+    if (higher == n - 1) t.bound = g;
+  }
+  __syncthreads();
+  const float bound = t.bound;
+  float least = bound;   // of a candidate
+  bool above = false;    // ... is above the bound
+  int count;
+  while (true) {
+    const bool holds = mine >= least && mine > -kInf;
+    const uint32_t who = __ballot_sync(0xffffffffu, holds);
+    int first = 0;
+    if (lane == 0 && who != 0u) first = atomicAdd(&t.threads, __popc(who));
+    first = __shfl_sync(0xffffffffu, first, 0);
+    if (holds) t.thread[first + __popc(who & ((1u << lane) - 1))] = tid;
+    __syncthreads();
+    const int steps = (j1 - j0 + LT * 8 - 1) / (LT * 8), items = t.threads * steps;
+    for (int k = tid; k < items; k += LT) {
+      const int j = j0 + t.thread[k / steps] * 8 + k % steps * (LT * 8);
+      if (j < j1) {
+        Vec8<T> v;
+        float f[8];
+        row.load(v, j);
+        row.scores(f, v, j);
+        uint32_t high = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) high |= (uint32_t)(f[i] >= least && f[i] > -kInf) << i;
+        if (high != 0u) {
+          int at = atomicAdd(&t.count, __popc(high));
+          if (at > LT) break;   // too many
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (high >> i & 1) {
+              if (at < LT) t.key[at] = key_of(f[i], j + i - row.lead);
+              ++at;
+            }
+        }
+      }
+    }
+    __syncthreads();
+    count = t.count;
+    if (count <= LT || above) break;
+    above = true;
+    least = next_above(bound);
+    __syncthreads();
+    if (tid == 0) t.threads = t.count = 0;
+    __syncthreads();
+  }
+  if (count > LT) {
+    take_one_by_one(t, row, j0, j1, n);
+    return;
+  }
+  if (tid < count) {
+    const unsigned long long key = t.key[tid];
+    int higher = 0;
+#pragma unroll 4
+    for (int i = 0; i < count; ++i) higher += t.key[i] > key;
+    if (higher < n) t.sorted[higher] = key;
+  }
+  if (above && bound > -kInf) take_equal(t, row, j0, j1, bound, count, n);
+}
+
 // A row is a cluster's (one block for many rows): every block takes a slice, the first one joins their sums. Bound by HBM
 // for many rows (8192 x 131072 bf16: 301 us, 7.1 TB/s; 4096 x 32000 fp32 with entropy 79 us, 6.6 TB/s; the exponentials
-// alone would take 73 % of that time in bf16), by latency for few (one row of 131072 with 20 alternatives: 5.6 us).
+// alone would take 73 % of that time in bf16), by latency for few (one row of 131072 with 20 alternatives: 5.8 us).
 template <typename T, int LU, bool ENT, bool TOP>
 __global__ void __launch_bounds__(LT, (kBlocks<T, LU, ENT, TOP>)) logprob_kernel(const LogprobArgs a) {
   constexpr int LC = LU * LT * 8;   // scores that a block takes at a time
@@ -326,7 +390,7 @@ __global__ void __launch_bounds__(LT, (kBlocks<T, LU, ENT, TOP>)) logprob_kernel
     }
     add_scores<ENT>(s, f, highest(f));
   }
-  const float top = s.m;
+  const float top = s.S == 0.f ? -kInf : s.m;
   s.warp_join<ENT>();
   if (lane == 0) s_sums[warp] = s;
   if constexpr (TOP) block_top(s_top[0], row, j0, j1, top, a.n_top);

@@ -384,6 +384,28 @@ def test_logprob_alternatives_of_rows_in_order(V, top, dtype):
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("M,V", [(9, 131071), (40, 20001), (700, 4099), (700, 1000)])
+def test_logprob_alternatives_among_equal_scores(M, V, dtype):
+    """A finite mask that leaves fewer tokens than are asked for, or as many; a value that many scores share at
+    the last places, alone or below some others; equal scores in the first or last part of a row only."""
+    g = _gen(M + V)
+    x = torch.full((M, V), -1e9, dtype=dtype)
+    for m in range(M):
+        kind, j = m % 9, torch.randperm(V, generator=g)
+        if kind < 4:
+            x[m, j[:(0, 1, 19, 20)[kind]]] = _rand(g, (0, 1, 19, 20)[kind], dtype=dtype)
+        elif kind < 6:
+            x[m] = _rand(g, V, dtype=dtype).clamp(max=(1.0, 0.0)[kind - 4])
+            x[m, j[:11]] = torch.arange(1, 12).to(dtype)
+        else:
+            x[m] = -math.inf
+            part = (slice(0, V // 3), slice(V - V // 3, V), slice(V // 2, V // 2 + 300))[kind - 6]
+            x[m, part] = 2.0
+            x[m, j[0]] = 3.0
+    _check_lp(x, torch.full((M,), V - 1, dtype=torch.int32), 20, bwd=False)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
 @pytest.mark.parametrize("V,ld", [(1000, 1008), (1001, 1003), (32000, 32001), (640, 5000)])
 def test_logprob_strides_and_in_place(V, ld, dtype):
     A, g, M = _api(), _gen(V + ld), 21

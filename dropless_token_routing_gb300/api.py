@@ -675,6 +675,9 @@ def _in_place(name, t, ld, out, ld_out, what):
         raise ValueError(f"{name}: overlaps {what} and does not lie where it does")
 
 
+_KEPT_VIEWS = 1024      # of results and shapes, one for each number of rows that came up
+
+
 class LayerNorm:
     """y = (s - mean) rstd weight + bias with s = x + residual, and its gradients: moe_norm_fwd /
     moe_norm_bwd on kept buffers for up to ``max_rows`` rows. ``dtype`` is the rows' (default the
@@ -685,7 +688,7 @@ class LayerNorm:
     buffers (written by the next call) unless ``out`` and ``sum_out`` are given, which may be x or the
     residual. With ``save=True`` it keeps what was normed (unchanged until then) for
     ``backward(dy, d_sum=None)``, which returns dict(dx, dw, db) (own buffers too; ``need`` names those to
-    compute; ``out`` takes dx and may be dy, d_sum or what was kept). d_sum is the gradient of s by its other
+    compute; ``out`` takes dx and may be dy, d_sum or what was kept, which is then gone). d_sum is the gradient of s by its other
     way; dx is the gradient of x and of the residual. What is kept is x and, in bf16, the residual: the
     rounding of s would show in the gradient of the weight. It is s for fp32 rows, and where a result has taken
     the place of x or the residual. One instance serves one stream at a time, which waits for the one it was
@@ -728,12 +731,16 @@ class LayerNorm:
                          "db": ((self.N,), self.w_dtype)}.get(name, ((self.max_rows, self.N), self.dtype))
             with _on(stream, self.device):
                 t = self._bufs[name] = torch.empty(shape, dtype=dt, device=self.device)
+        if len(self._views) >= _KEPT_VIEWS:
+            self._views.clear()
         v = self._views[(name, M)] = t if M is None else t[:M], t.data_ptr()
         return v
 
     def _shape(self, M):
         if M > self.max_rows:
             raise ValueError(f"{M} rows, the layer was made for {self.max_rows}")
+        if len(self._shapes) >= _KEPT_VIEWS:
+            self._shapes.clear()
         s = self._shapes[M] = torch.Size((M, self.N))
         return s
 
@@ -800,6 +807,7 @@ class LayerNorm:
         st = self._fwd(xp, rp, self._w_ptr, self._b_ptr, self._dims_ref, sp, yp, stats,
                        _raw_stream(self._index) if stream is None and _raw_stream is not None else _stream(stream, self._index))
         if st:
+            self._kept = None
             N.check(st, "moe_norm_fwd")
         return y if rp is None else (y, s)
 
@@ -808,13 +816,14 @@ class LayerNorm:
             raise ValueError("backward: the last forward did not save (save=True)")
         (x, xp, ld_x, res, rp, ld_r), n, dev, dt, views = self._kept, self.N, self.device, self.dtype, self._views
         M = x.shape[0]
-        shape, row = self._shapes[M], M * self._size
+        shape, row = x.shape, M * self._size
         w, b = self.weight, self.bias
         if w is not self._w_ref() or b is not self._b_ref() or w.data_ptr() != self._w_ptr or (b is not None and b.data_ptr() != self._b_ptr):
             self._bind()
         ld_y = n if dy.dtype is dt and dy.shape == shape and dy.is_contiguous() and dy.device == dev else _matrix(dy, "dy", dt, M, n, dev)
         dx = dw = db = dxp = dwp = dbp = sp = None
         ld_dx = ld_d = 0
+        gone = False        # what was kept
         if d_sum is not None:
             d = d_sum
             ld_d = n if d.dtype is dt and d.shape == shape and d.is_contiguous() and d.device == dev else _matrix(d, "d_sum", dt, M, n, dev)
@@ -831,8 +840,10 @@ class LayerNorm:
                 _in_place("dy", dy, ld_y, dx, ld_dx, "dx")
             if -row * ld_x < xp - dxp < end:
                 _in_place("x", x, ld_x, dx, ld_dx, "dx")
+                gone = xp == dxp
             if rp is not None and -row * ld_r < rp - dxp < end:
                 _in_place("residual", res, ld_r, dx, ld_dx, "dx")
+                gone = gone or rp == dxp
             if sp is not None and -row * ld_d < sp - dxp < end:
                 _in_place("d_sum", d_sum, ld_d, dx, ld_dx, "dx")
         if "dw" in need:
@@ -845,10 +856,12 @@ class LayerNorm:
         if key != self._bwd_set:
             D = self._bwd_dims
             D.M, D.ld_x, D.ld_res, D.ld_sum, D.ld_y, D.ld_dx = self._bwd_set = key
-        st = self._bwd(xp, rp, yp, sp, self._w_ptr, views[("stats", M)][1], self._bwd_ref, dxp, dwp, dbp, self.ws.ptr, self.ws.nbytes,
+        st = self._bwd(xp, rp, yp, sp, self._w_ptr, self._bufs["stats"].data_ptr(), self._bwd_ref, dxp, dwp, dbp, self.ws.ptr, self.ws.nbytes,
                        _stream(stream, self._index))
         if st:
             N.check(st, "moe_norm_bwd")
+        if gone:
+            self._kept = None
         return dict(dx=dx, dw=dw, db=db)
 
 
@@ -867,7 +880,8 @@ class TokenLogprobs:
     tokens), ``entropy`` [M] (if asked for), ``top_idx`` and ``top_logprob`` [M, top] (if top > 0): own
     buffers, written by the next call. A token outside [0, V) is padding (0). With ``save=True`` it keeps
     scores and tokens (unchanged until then) for ``backward(d_logprob=None, d_entropy=None)``, which returns the
-    gradient of the scores [M, V]: an own buffer unless ``out`` is given, which may be the scores. One instance
+    gradient of the scores [M, V]: an own buffer unless ``out`` is given, which may be the scores (what was kept is
+    then gone). One instance
     serves one stream at a time, which waits for the one it was made on.
     """
 
@@ -894,6 +908,8 @@ class TokenLogprobs:
         if v is None:
             if M > self.max_rows:
                 raise ValueError(f"{M} rows, made for {self.max_rows}")
+            if len(self._views) >= _KEPT_VIEWS:
+                self._views.clear()
             v = self._views[M] = (torch.Size((M, self.V)), torch.Size((M,)), self._logprob[:M, 0], self._entropy[:M, 0],
                                   self._top[0][:M], self._top[1][:M])
         shape, of_rows, logprob, ent, top_idx, top_logprob = v
@@ -907,8 +923,8 @@ class TokenLogprobs:
             if t.dtype is not torch.int32 or t.shape != of_rows or not t.is_contiguous() or t.device != dev:
                 _dense(t, "tokens", torch.int32, of_rows, dev)
             out["logprob"], tp = logprob, t.data_ptr()
-            if save and ip is not None and -4 * M < tp - ip < 4 * M * self.top:
-                raise ValueError("tokens: overlaps the result, and is needed for the backward")
+            if ip is not None and -4 * M < tp - ip < 4 * M * self.top and (save or tp != ip or self.top > 1):
+                raise ValueError("tokens: overlaps the result" + (", and is needed for the backward" if save else ""))
         else:
             tp = lp = None
         if entropy:
@@ -925,6 +941,7 @@ class TokenLogprobs:
         st = self._fwd(scores.data_ptr(), tp, self._dims_ref, lp, ep, sp if save else None, ip, vp,
                        _raw_stream(self._index) if stream is None and _raw_stream is not None else _stream(stream, self._index))
         if st:
+            self._saved = None
             N.check(st, "moe_token_logprob")
         return out
 
@@ -958,6 +975,8 @@ class TokenLogprobs:
                        self._dims_ref, out.data_ptr(), _stream(stream, self._index))
         if st:
             N.check(st, "moe_token_logprob_bwd")
+        if out.data_ptr() == scores.data_ptr():
+            self._saved = None
         return out
 
 
@@ -968,8 +987,8 @@ class GradClipper:
     ``norm()`` returns the norm, ``clip(max_norm)`` also scales the gradients by min(1, max_norm / (norm +
     1e-6)), in place, or into ``out`` (a list of the same shape and types). Both return a tensor of one number
     without waiting for it, an own buffer that the next call writes; ``scale`` holds the factor of the
-    last call. A tensor that has moved (``t.data = ...``) is taken where it is then; a captured graph takes those of
-    the capture. One instance serves one stream at a time, which waits for the one it was made on.
+    last call. A tensor that has moved (``t.data = ...``) is taken where it is then, another tensor in its place (a
+    parameter's new ``grad``) is not; a captured graph takes those of the capture. One instance serves one stream at a time, which waits for the one it was made on.
     """
 
     def __init__(self, grads, out=None, device=None, stream=None):

@@ -503,7 +503,8 @@ typedef struct moe_logprob_dims {
  *     lower index, and their ln p; -1 and -inf where there are no more
  *   stats [M][2]: the largest score and ln sum_j e^(x_j - largest), for the backward
  * logprob, entropy and stats may each be NULL (not returned); tokens [M] int32 is read for logprob alone.
- * What has one number for a row need only be aligned to it (a slice of a batch).
+ * What has one number for a row need only be aligned to it (a slice of a batch). The results overlap no operand,
+ * but for top_idx of one alternative, which may be the buffer of tokens.
  * A score of -inf is no token (p = 0, no alternative); in a row of nothing else every ln p is -inf and
  * the entropy 0. NaN or +inf among the scores makes the row's results NaN (top_idx leaves out NaN). Sums are fp32 in
  * a fixed order. M == 0 is a no-op. */

@@ -401,3 +401,52 @@ def test_results_are_views_of_kept_buffers(lib):
     assert a.data_ptr() == b.data_ptr() and b.shape == (3, 64)
     p, q = lp.forward(z(8, 30), stream=ST), lp.forward(z(2, 30), stream=ST)
     assert p["top_idx"].data_ptr() == q["top_idx"].data_ptr() and q["top_logprob"].shape == (2, 2)
+
+
+def test_what_a_gradient_overwrote_is_no_longer_kept(lib):
+    """A second backward would read the first one's result."""
+    x, r, s, dy = (z(4, 64, dtype=BF) for _ in range(4))
+    ln = layer_norm(dtype=BF)
+    for place, kw in ((x, {}), (x, dict(residual=r)), (r, dict(residual=r)), (s, dict(residual=r, out=x, sum_out=s))):
+        ln.forward(x, save=True, stream=ST, **kw)
+        ln.backward(dy, stream=ST)
+        ln.backward(dy, out=dy, stream=ST)
+        ln.backward(dy, out=place, need=("dw", "db"), stream=ST)     # not written
+        ln.backward(dy, out=place, stream=ST)
+        with pytest.raises(ValueError):
+            ln.backward(dy, stream=ST)
+    lp, x = A.TokenLogprobs(4, 50, device=DEV), z(4, 50)
+    lp.forward(x, torch.zeros(4, dtype=torch.int32), save=True, stream=ST)
+    lp.backward(z(4), stream=ST)
+    lp.backward(z(4), out=x, stream=ST)
+    with pytest.raises(ValueError):
+        lp.backward(z(4), stream=ST)
+
+
+def test_logprob_tokens_among_the_alternatives(lib):
+    """A row's alternatives would be written over the next rows' tokens."""
+    x = z(4, 50)
+    for top in (2, 5):
+        lp = A.TokenLogprobs(4, 50, top=top, device=DEV)
+        idx = lp.forward(x, stream=ST)["top_idx"].view(-1)
+        for i in (0, 1, 4 * top - 4):
+            with pytest.raises(ValueError):
+                lp.forward(x, idx[i:i + 4], stream=ST)
+    lp = A.TokenLogprobs(8, 50, top=1, device=DEV)
+    idx = lp.forward(z(8, 50), stream=ST)["top_idx"].view(-1)
+    lp.forward(x, idx[:4], stream=ST)
+    lp.forward(x, idx[4:], stream=ST)
+    with pytest.raises(ValueError):
+        lp.forward(x, idx[1:5], stream=ST)
+
+
+def test_views_of_many_numbers_of_rows(lib):
+    """What is kept for each number of rows that came up stays bounded, and a backward works all the same."""
+    rows = 3 * A._KEPT_VIEWS
+    ln, lp, x = layer_norm(n=1, rows=rows), A.TokenLogprobs(rows, 1, top=1, device=DEV), z(rows, 1)
+    for M in range(1, rows + 1):
+        y = ln.forward(x[:M], save=True, stream=ST)
+        assert y.shape == (M, 1) and ln.backward(x[:M], stream=ST)["dx"].shape == (M, 1)
+        assert lp.forward(x[:M], stream=ST)["top_idx"].shape == (M, 1)
+    assert max(map(len, (ln._views, ln._shapes, lp._views))) <= A._KEPT_VIEWS
+    assert lib.last("moe_norm_bwd")[5] == ln._bufs["stats"].data_ptr()

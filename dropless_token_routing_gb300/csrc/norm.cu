@@ -294,34 +294,37 @@ struct Group {
   }
 };
 
-// y (and the sum). Two sums for each row, the second of centred values, each a barrier of the row's group; 100 registers,
-// issue slots 43 % busy. 8192 x 7680 bf16 with a residual: 76 us, 6.6 TB/s, HBM; 4096 x 2048 14.3 us, of which 3 are
-// its two ends; one row 2.6 us.
-template <typename T, typename W, int MODE, int E, bool RES>
+// y (and the sum). Two sums for each row, the second of centred values, each a barrier of the row's group, which takes R
+// rows at a time; 100 to 126 registers. 8192 x 7680 bf16 with a residual: 76 us, 6.6 TB/s, HBM; 4096 x 2048 13.2 us, of
+// which 3 are its two ends; one row 2.6 us.
+template <typename T, typename W, int MODE, int E, bool RES, int R>
 __global__ void __launch_bounds__(kRowThreads, 1) norm_fwd_rows(const NormArgs a, int warps, int stages) {
   extern __shared__ uint4 ring[];
   __shared__ float2 s_sums[2][16];
   using P = Unit<T, MODE, E>;
-  constexpr int kIn = P::kIn, kUnits = P::kUnits, kPairs = P::kPairs, kOp = kUnits * P::kPieces, kStep = (1 + RES) * kOp;
+  constexpr int kIn = P::kIn, kUnits = P::kUnits, kPairs = P::kPairs, kOp = kUnits * P::kPieces, kRow = (1 + RES) * kOp;
   pdl_start();
   const int N = a.N, gt = warps * 32, groups = blockDim.x / gt, tg = threadIdx.x % gt;
   const Group group = {(int)threadIdx.x / gt, warps};
-  const int64_t step = (int64_t)gridDim.x * groups;
+  const int64_t step = (int64_t)gridDim.x * groups * R;
   const int c0 = tg * kIn, n0 = N - c0, next_unit = gt * kIn;   // this thread's first column, elements from there on
   const T *x0 = static_cast<const T*>(a.x) + c0, *r0 = RES ? static_cast<const T*>(a.res) + c0 : nullptr;
   const T *x_end = end_of<T>(a.x, a.M, a.ld_x, N), *r_end = RES ? end_of<T>(a.res, a.M, a.ld_res, N) : nullptr;
   pdl_wait();
-  int64_t next = (int64_t)blockIdx.x * groups + group.index;
+  int64_t next = ((int64_t)blockIdx.x * groups + group.index) * R;
   const T *xp = x0 + next * a.ld_x, *rp = RES ? r0 + next * a.ld_res : nullptr;   // row `next`
   auto fetch = [&](int stage) {
-    if (next < a.M) {
-      const uint32_t at = smem_u32(ring + stage * kStep * blockDim.x + threadIdx.x);
 #pragma unroll
-      for (int i = 0; i < kUnits; ++i) {
-        const int n = n0 - i * next_unit;
-        if (MODE == FULL || n > 0) {
-          P::copy(at + i * P::kPieces * blockDim.x * 16, xp + i * next_unit, n, x_end);
-          if (RES) P::copy(at + (kOp + i * P::kPieces) * blockDim.x * 16, rp + i * next_unit, n, r_end);
+    for (int r = 0; r < R; ++r) {
+      if (next + r < a.M) {
+        const uint32_t at = smem_u32(ring + (stage * R + r) * kRow * blockDim.x + threadIdx.x);
+#pragma unroll
+        for (int i = 0; i < kUnits; ++i) {
+          const int n = n0 - i * next_unit;
+          if (MODE == FULL || n > 0) {
+            P::copy(at + i * P::kPieces * blockDim.x * 16, xp + r * a.ld_x + i * next_unit, n, x_end);
+            if (RES) P::copy(at + (kOp + i * P::kPieces) * blockDim.x * 16, rp + r * a.ld_res + i * next_unit, n, r_end);
+          }
         }
       }
     }
@@ -345,47 +348,55 @@ __global__ void __launch_bounds__(kRowThreads, 1) norm_fwd_rows(const NormArgs a
     for (int i = 0; i < kUnits; ++i) weights(i, i);
   }
   int stage = 0;
-  for (int64_t m = (int64_t)blockIdx.x * groups + group.index; m < a.M; m += step) {
-    fetch(stage == 0 ? stages - 1 : stage - 1);   // (the row before was taken from there)
+  for (int64_t m = ((int64_t)blockIdx.x * groups + group.index) * R; m < a.M; m += step) {
+    fetch(stage == 0 ? stages - 1 : stage - 1);   // (the rows before were taken from there)
     cp_wait(stages - 1);
-    uint4* at = ring + stage * kStep * blockDim.x + threadIdx.x;
+    uint4* at = ring + stage * R * kRow * blockDim.x + threadIdx.x;
     if (++stage == stages) stage = 0;
-    uint64_t f[kUnits][kPairs];
-    uint64_t t = 0;
+    uint64_t f[R][kUnits][kPairs];
+    uint64_t t[R] = {};
 #pragma unroll
-    for (int i = 0; i < kUnits; ++i) {
-      const int n = n0 - i * next_unit;
-      uint4* place = at + i * P::kPieces * blockDim.x;
-      if (MODE == FULL || n > 0) {
-        P::read(f[i], place, x0 + m * a.ld_x + i * next_unit, n);
-        if (RES) {
-          uint64_t g[kPairs];
-          P::read(g, place + kOp * blockDim.x, r0 + m * a.ld_res + i * next_unit, n);
+    for (int r = 0; r < R; ++r)
 #pragma unroll
-          for (int j = 0; j < kPairs; ++j) f[i][j] = add2(f[i][j], g[j]);
+      for (int i = 0; i < kUnits; ++i) {
+        const int n = n0 - i * next_unit;
+        uint4* place = at + (r * kRow + i * P::kPieces) * blockDim.x;
+        if (MODE == FULL || n > 0) {
+          P::read(f[r][i], place, x0 + (m + r) * a.ld_x + i * next_unit, n);
+          if (RES) {
+            uint64_t g[kPairs];
+            P::read(g, place + kOp * blockDim.x, r0 + (m + r) * a.ld_res + i * next_unit, n);
+#pragma unroll
+            for (int j = 0; j < kPairs; ++j) f[r][i][j] = add2(f[r][i][j], g[j]);
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < kPairs; ++j) f[r][i][j] = 0;
         }
-      } else {
+        if (RES && a.sum != nullptr && (MODE != ALIGNED || n > 0) && (r == 0 || m + r < a.M))
+          P::write(f[r][i], place, static_cast<T*>(a.sum) + (m + r) * a.ld_sum + c0 + i * next_unit, n);
 #pragma unroll
-        for (int j = 0; j < kPairs; ++j) f[i][j] = 0;
+        for (int j = 0; j < kPairs; ++j) t[r] = add2(t[r], f[r][i][j]);
       }
-      if (RES && a.sum != nullptr && (MODE != ALIGNED || n > 0))
-        P::write(f[i], place, static_cast<T*>(a.sum) + m * a.ld_sum + c0 + i * next_unit, n);
+    float2 all = group.sums<(R > 1)>(sum2(t[0]), sum2(t[R - 1]), s_sums[0]);
+    const float mean[2] = {all.x * a.inv_n, all.y * a.inv_n};
 #pragma unroll
-      for (int j = 0; j < kPairs; ++j) t = add2(t, f[i][j]);
+    for (int r = 0; r < R; ++r) {
+      t[r] = 0;
+#pragma unroll
+      for (int i = 0; i < kUnits; ++i) {
+        const int n = n0 - i * next_unit;
+#pragma unroll
+        for (int j = 0; j < kPairs; ++j) f[r][i][j] = add2(f[r][i][j], both(-mean[r]));
+        if (MODE != FULL && n < kIn) P::keep(f[r][i], n);
+#pragma unroll
+        for (int j = 0; j < kPairs; ++j) t[r] = fma2(f[r][i][j], f[r][i][j], t[r]);
+      }
     }
-    const float mean = group.sums<false>(sum2(t), 0.f, s_sums[0]).x * a.inv_n;
-    t = 0;
-#pragma unroll
-    for (int i = 0; i < kUnits; ++i) {
-      const int n = n0 - i * next_unit;
-#pragma unroll
-      for (int j = 0; j < kPairs; ++j) f[i][j] = add2(f[i][j], both(-mean));
-      if (MODE != FULL && n < kIn) P::keep(f[i], n);
-#pragma unroll
-      for (int j = 0; j < kPairs; ++j) t = fma2(f[i][j], f[i][j], t);
-    }
-    const float rstd = 1.f / sqrtf(group.sums<false>(sum2(t), 0.f, s_sums[1]).x * a.inv_n + a.eps);
-    if (tg == 0 && a.stats != nullptr) reinterpret_cast<float2*>(a.stats)[m] = make_float2(mean, rstd);
+    all = group.sums<(R > 1)>(sum2(t[0]), sum2(t[R - 1]), s_sums[1]);
+    const float rstd[2] = {1.f / sqrtf(all.x * a.inv_n + a.eps), R > 1 ? 1.f / sqrtf(all.y * a.inv_n + a.eps) : 0.f};
+    if (tg < R && m + tg < a.M && a.stats != nullptr)
+      reinterpret_cast<float2*>(a.stats)[m + tg] = make_float2(tg == 0 ? mean[0] : mean[1], tg == 0 ? rstd[0] : rstd[1]);
 #pragma unroll
     for (int i = 0; i < kUnits; ++i) {
       const int n = n0 - i * next_unit;
@@ -394,8 +405,13 @@ __global__ void __launch_bounds__(kRowThreads, 1) norm_fwd_rows(const NormArgs a
       w[HOLD ? i : 0].pairs(g);
       if (a.b != nullptr) b[HOLD ? i : 0].pairs(h);
 #pragma unroll
-      for (int j = 0; j < kPairs; ++j) g[j] = fma2(f[i][j], mul2(g[j], both(rstd)), h[j]);
-      if (MODE != ALIGNED || n > 0) P::write(g, at + i * P::kPieces * blockDim.x, static_cast<T*>(a.y) + m * a.ld_y + c0 + i * next_unit, n);
+      for (int r = 0; r < R; ++r) {
+        uint64_t y[kPairs];
+#pragma unroll
+        for (int j = 0; j < kPairs; ++j) y[j] = fma2(f[r][i][j], mul2(g[j], both(rstd[r])), h[j]);
+        if ((MODE != ALIGNED || n > 0) && (r == 0 || m + r < a.M))
+          P::write(y, at + (r * kRow + i * P::kPieces) * blockDim.x, static_cast<T*>(a.y) + (m + r) * a.ld_y + c0 + i * next_unit, n);
+      }
     }
   }
   cp_wait(0);
@@ -868,11 +884,12 @@ template <auto Kernel> cudaError_t allow_ring(int bytes) {
 // A persistent launch: one block on an SM (two with half the ring each: 90 us forward at 8192 x 7680, 77 by one).
 struct RowLaunch {
   int grid, threads, warps, stages, smem;
-  // stage: bytes of a thread's places of a stage; join: of what it leaves behind the loop
-  RowLaunch(int64_t M, const RowShape& s, int stage, int join, int num_sms) : threads(s.threads()), warps(s.warps) {
-    const int64_t blocks = (M + s.groups - 1) / s.groups;
+  // each: rows that a group takes at a time; stage: bytes of a thread's places of a stage; join: of what it leaves
+  // behind the loop
+  RowLaunch(int64_t M, const RowShape& s, int each, int stage, int join, int num_sms) : threads(s.threads()), warps(s.warps) {
+    const int64_t blocks = (M + s.groups * each - 1) / (s.groups * each);
     grid = (int)(blocks < num_sms ? blocks : num_sms);
-    const int64_t rows = (blocks + grid - 1) / grid;   // of a group
+    const int64_t rows = (blocks + grid - 1) / grid;   // of a group, `each` at a time
     stages = kRing / (threads * stage);
     if (stages > kMaxStages) stages = kMaxStages;
     if (stages > rows) stages = (int)rows;
@@ -880,12 +897,24 @@ struct RowLaunch {
   }
 };
 
-template <typename T, typename W, int MODE, int E, bool RES> cudaError_t fwd_rows(const NormArgs& a, int num_sms, cudaStream_t st) {
+template <typename T, typename W, int MODE, int E, bool RES, int R> cudaError_t fwd_each(const NormArgs& a, int num_sms, cudaStream_t st) {
   using P = Unit<T, MODE, E>;
-  const RowLaunch l(a.M, RowShape(a.N, a.M, num_sms, E), 16 * (1 + RES) * P::kUnits * P::kPieces, 0, num_sms);
-  const cudaError_t e = allow_ring<norm_fwd_rows<T, W, MODE, E, RES>>(kRing);
+  static_assert(16 * R * (1 + RES) * P::kUnits * P::kPieces * kRowThreads <= kRing, "a stage at least");
+  const RowLaunch l(a.M, RowShape(a.N, a.M, num_sms, E), R, 16 * R * (1 + RES) * P::kUnits * P::kPieces, 0, num_sms);
+  const cudaError_t e = allow_ring<norm_fwd_rows<T, W, MODE, E, RES, R>>(kRing);
   if (e != cudaSuccess) return e;
-  return launch_pdl(norm_fwd_rows<T, W, MODE, E, RES>, dim3(l.grid), l.threads, l.smem, 1, st, a, l.warps, l.stages);
+  return launch_pdl(norm_fwd_rows<T, W, MODE, E, RES, R>, dim3(l.grid), l.threads, l.smem, 1, st, a, l.warps, l.stages);
+}
+template <typename T, typename W, int MODE, int E, bool RES> cudaError_t fwd_rows(const NormArgs& a, int num_sms, cudaStream_t st) {
+  // Two rows at a time of bf16, each group four times at least: a group's two barriers for them are the same (without a
+  // residual 8000 x 5120: 50 us by one, 41 by two; 10000 x 4096 41, 35; 40000 x 1024 35, 30; with one 8000 x 5120 61,
+  // 52; 4096 x 2048 14.4, 13.2). With a residual wider rows leave too few stages (5714 x 7168: 54 us by one, 57 by two), and
+  // narrow unaligned ones too much to do (52700 x 777: 109, 113).
+  if constexpr (sizeof(T) == 2 && E == kThin) {
+    const bool two = !RES || (a.N <= 5120 && (MODE != UNALIGNED || a.N > 4096));
+    if (two && a.M >= 4 * num_sms * RowShape(a.N, a.M, num_sms, E).groups) return fwd_each<T, W, MODE, E, RES, 2>(a, num_sms, st);
+  }
+  return fwd_each<T, W, MODE, E, RES, 1>(a, num_sms, st);
 }
 template <typename T, typename W, int MODE, int E> cudaError_t fwd_mode(const NormArgs& a, int num_sms, cudaStream_t st) {
   return a.res != nullptr ? fwd_rows<T, W, MODE, E, true>(a, num_sms, st) : fwd_rows<T, W, MODE, E, false>(a, num_sms, st);
@@ -912,7 +941,7 @@ template <typename T, typename W> cudaError_t norm_fwd(const NormArgs& a, int nu
 template <typename T, typename W, int MODE, int E, bool RES, bool DS>
 cudaError_t bwd_rows(const NormBwdArgs& a, int num_sms, int* parts, cudaStream_t st) {
   using P = Unit<T, MODE, E>;
-  const RowLaunch l(a.M, RowShape(a.N, a.M, num_sms, E), 16 * (2 + RES + DS) * P::kUnits * P::kPieces, 2 * E * 4, num_sms);
+  const RowLaunch l(a.M, RowShape(a.N, a.M, num_sms, E), 1, 16 * (2 + RES + DS) * P::kUnits * P::kPieces, 2 * E * 4, num_sms);
   const cudaError_t e = allow_ring<norm_bwd_rows<T, W, MODE, E, RES, DS>>(kRing);
   if (e != cudaSuccess) return e;
   *parts = l.grid;

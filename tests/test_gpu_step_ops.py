@@ -120,6 +120,14 @@ def test_norm_rows_far_from_zero(dtype):
     _check_norm(40, 1000, dtype, dtype, False, True, seed=3, shift=300.0)
 
 
+@pytest.mark.parametrize("residual", [False, True])
+@pytest.mark.parametrize("M,N,ld", [(1217, 4096, None), (611, 5120, None), (2435, 1544, 1552), (640, 5001, None), (4867, 999, None),
+                                    (609, 8192, None), (9729, 200, 203)])
+def test_norm_of_many_rows_two_at_a_time(M, N, ld, residual):
+    """Rows enough for every group of the device, an odd one at the end."""
+    _check_norm(M, N, BF, BF, residual, True, seed=M, ld=ld)
+
+
 def test_norm_many_rows():
     _check_norm(9001, 520, BF, F32, True, True, seed=4)
     _check_norm(20011, 72, F32, F32, False, True, seed=5)

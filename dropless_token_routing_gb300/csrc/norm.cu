@@ -886,8 +886,11 @@ struct RowLaunch {
   int grid, threads, warps, stages, smem;
   // each: rows that a group takes at a time; stage: bytes of a thread's places of a stage; join: of what it leaves
   // behind the loop
-  RowLaunch(int64_t M, const RowShape& s, int each, int stage, int join, int num_sms) : threads(s.threads()), warps(s.warps) {
-    const int64_t blocks = (M + s.groups * each - 1) / (s.groups * each);
+  RowLaunch(int64_t M, const RowShape& s, int each, int stage, int join, int num_sms) : warps(s.warps) {
+    int groups = s.groups;
+    while (groups > 1 && warps * 32 * groups * stage > kRing) --groups;   // (each takes a stage at least)
+    threads = warps * 32 * groups;
+    const int64_t blocks = (M + groups * each - 1) / (groups * each);
     grid = (int)(blocks < num_sms ? blocks : num_sms);
     const int64_t rows = (blocks + grid - 1) / grid;   // of a group, `each` at a time
     stages = kRing / (threads * stage);
@@ -941,6 +944,8 @@ template <typename T, typename W> cudaError_t norm_fwd(const NormArgs& a, int nu
 template <typename T, typename W, int MODE, int E, bool RES, bool DS>
 cudaError_t bwd_rows(const NormBwdArgs& a, int num_sms, int* parts, cudaStream_t st) {
   using P = Unit<T, MODE, E>;
+  static_assert(16 * (2 + RES + DS) * P::kUnits * P::kPieces * kRowThreads <= (MODE == UNALIGNED && sizeof(T) == 4 && RES && DS ? kRing * 4 / 3 : kRing),
+                "a stage at least");
   const RowLaunch l(a.M, RowShape(a.N, a.M, num_sms, E), 1, 16 * (2 + RES + DS) * P::kUnits * P::kPieces, 2 * E * 4, num_sms);
   const cudaError_t e = allow_ring<norm_bwd_rows<T, W, MODE, E, RES, DS>>(kRing);
   if (e != cudaSuccess) return e;
@@ -969,7 +974,9 @@ template <typename T, typename W> cudaError_t norm_bwd(const NormBwdArgs& a, int
     d.dw = d.db = nullptr;
     return norm_bwd<T, W>(d, num_sms, st);
   }
-  const bool wide = !thick<T>(a.N, vdx) && a.N > kRowsMaxN;
+  // (a stage of four unaligned fp32 operands, twice what they have, is more than the ring for 13 warps and up)
+  const bool four = sizeof(T) == 4 && !vdx && a.res != nullptr && a.d_sum != nullptr && a.dx != nullptr;
+  const bool wide = !thick<T>(a.N, vdx) && a.N > (four ? kRowsMaxN * 3 / 4 : kRowsMaxN);
   if (thick<T>(a.N, vdx)) {
     if constexpr (sizeof(T) == 2)
       e = row_mode(a.N, vdx, kThick) == FULL ? bwd_mode<T, W, FULL, kThick>(a, num_sms, &parts, st)

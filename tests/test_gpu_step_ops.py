@@ -226,6 +226,35 @@ def test_norm_rows_beyond_31_bits():
     assert torch.equal(got["dx"], grads["dx"]) and torch.equal(got["dw"], grads["dw"])
 
 
+@pytest.mark.parametrize("M,N,ld", [(1300, 1001, 1001), (2500, 777, 779), (700, 6145, 6145), (250, 8191, 8193), (40, 6401, 6401),
+                                    (900, 3001, 3001), (700, 8192, 8192), (5000, 100, 101)])
+def test_norm_gradients_of_fp32_rows_and_their_residual(M, N, ld):
+    """What the layer does not do, as it keeps the sum: all four operands of the backward in fp32."""
+    from dropless_token_routing_gb300 import _native as native
+    A, g = _api(), _gen(M + N)
+    x, r, dy, ds = (_rand(g, M, N) for _ in range(4))
+    w = 1 + _rand(g, N, std=0.3)
+    xd, rd, dyd, dsd, dx = (_strided(t.cuda(), ld) for t in (x, r, dy, ds, torch.zeros(M, N)))
+    ln = A.LayerNorm(w.cuda(), max_rows=M)
+    ln.forward(xd, residual=rd, save=True)
+    dims = native.NormDims(M, N, native.MOE_F32, native.MOE_F32, 1e-5, ld, ld, ld, ld, ld)
+    ws = A.OpWorkspace(native.lib().moe_norm_workspace_bytes(native.ctypes.byref(dims)), "moe_norm_workspace_bytes", "cuda")
+    dw, db = torch.empty(N, device="cuda"), torch.empty(N, device="cuda")
+    native.check(native.lib().moe_norm_bwd(xd.data_ptr(), rd.data_ptr(), dyd.data_ptr(), dsd.data_ptr(), ln.weight.data_ptr(),
+                                           ln._bufs["stats"].data_ptr(), native.ctypes.byref(dims), dx.data_ptr(), dw.data_ptr(),
+                                           db.data_ptr(), ws.ptr, ws.nbytes, torch.cuda.current_stream().cuda_stream), "moe_norm_bwd")
+    s, mean, rstd, _ = _norm_ref(x, r, w, None, 1e-5)
+    xh, u, want, want_dw, want_db = _norm_grads(s, mean, rstd, w, dy, ds)
+    spread = s.abs().amax(1, keepdim=True) * rstd + 1
+    big = lambda v: v.abs().amax(1, keepdim=True)  # noqa: E731
+    # (as _check_norm: and the sum's own rounding, half a step of it)
+    _near(dx, want, F32, rstd * big(u) * (1 + big(xh)) * (1 + spread) + ds.double().abs(), what="dx")
+    rows = 96 + M // 512
+    _near(dw, want_dw, F32, (dy.double().abs() * (xh.abs() + spread)).sum(0), steps=rows, what="dw")
+    _near(db, want_db, F32, dy.double().abs().sum(0), steps=rows, what="db")
+    assert ld == N or torch.isnan(dx._base[:, N:]).all()
+
+
 def test_norm_gradient_by_differences():
     """The gradients along a direction are the differences of the 64-bit form along it."""
     A, g, M, N, eps = _api(), _gen(11), 13, 72, 1e-3

@@ -292,6 +292,24 @@ struct Group {
     }
     return t;
   }
+  // ... of four.
+  __device__ __forceinline__ float4 sums(float4 v, float4* s) const {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v = add(v, o);
+    if (warps == 1) return v;
+    const int lane = threadIdx.x & 31;
+    if (lane == 0) s[threadIdx.x >> 5] = v;
+    asm volatile("bar.sync %0, %1;" ::"r"(1 + index), "r"(warps * 32) : "memory");
+    v = make_float4(0.f, 0.f, 0.f, 0.f);
+    if ((lane & 15) < warps) v = s[index * warps + (lane & 15)];
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) v = add(v, o);
+    return v;
+  }
+  static __device__ __forceinline__ float4 add(const float4& v, int o) {
+    return make_float4(v.x + __shfl_xor_sync(0xffffffffu, v.x, o), v.y + __shfl_xor_sync(0xffffffffu, v.y, o),
+                       v.z + __shfl_xor_sync(0xffffffffu, v.z, o), v.w + __shfl_xor_sync(0xffffffffu, v.w, o));
+  }
 };
 
 // y (and the sum). Two sums for each row, the second of centred values, each a barrier of the row's group, which takes R
@@ -418,23 +436,23 @@ __global__ void __launch_bounds__(kRowThreads, 1) norm_fwd_rows(const NormArgs a
 }
 
 // dx, and a block's partial sums of dw and db. x, dy, then the residual (RES) and d_sum (DS) are the operands of a
-// stage; the next row's mean and rstd are asked for a row ahead (86 us, 94 without, at 8192 x 7680 with three operands). One
-// barrier for each row. 8192 x 7680 bf16, four operands: 89 us, 7.0 TB/s, HBM; 97 with the sums' join.
-template <typename T, typename W, int MODE, int E, bool RES, bool DS>
+// stage; the next rows' mean and rstd are asked for a step ahead (86 us, 94 without, at 8192 x 7680 with three operands). One
+// barrier for R rows. 8192 x 7680 bf16, four operands: 89 us, 7.0 TB/s, HBM; 97 with the sums' join.
+template <typename T, typename W, int MODE, int E, bool RES, bool DS, int R>
 __global__ void __launch_bounds__(kRowThreads, 1) norm_bwd_rows(const NormBwdArgs a, int warps, int stages) {
   extern __shared__ uint4 ring[];
-  __shared__ float2 s_sums[2][16];
+  __shared__ float4 s_sums[2][16];
   using P = Unit<T, MODE, E>;
-  constexpr int kIn = P::kIn, kUnits = P::kUnits, kPairs = P::kPairs, kOp = kUnits * P::kPieces, kOps = 2 + RES + DS;
+  constexpr int kIn = P::kIn, kUnits = P::kUnits, kPairs = P::kPairs, kOp = kUnits * P::kPieces, kOps = 2 + RES + DS, kRow = kOps * kOp;
   pdl_start();
   const int N = a.N, gt = warps * 32, groups = blockDim.x / gt, tg = threadIdx.x % gt;
   const Group group = {(int)threadIdx.x / gt, warps};
-  const int64_t step = (int64_t)gridDim.x * groups;
+  const int64_t step = (int64_t)gridDim.x * groups * R;
   const int c0 = tg * kIn, n0 = N - c0, next_unit = gt * kIn;   // this thread's first column, elements from there on
   const void* const operand[4] = {a.x, a.dy, RES ? a.res : a.d_sum, a.d_sum};
   const int64_t ld[4] = {a.ld_x, a.ld_dy, RES ? a.ld_res : a.ld_ds, a.ld_ds};
   pdl_wait();
-  int64_t next = (int64_t)blockIdx.x * groups + group.index;
+  int64_t next = ((int64_t)blockIdx.x * groups + group.index) * R;
   const T *base[kOps], *p[kOps], *end[kOps];   // this thread's part of row 0 and of row `next`
 #pragma unroll
   for (int o = 0; o < kOps; ++o) {
@@ -443,14 +461,17 @@ __global__ void __launch_bounds__(kRowThreads, 1) norm_bwd_rows(const NormBwdArg
     end[o] = end_of<T>(operand[o], a.M, ld[o], N);
   }
   auto fetch = [&](int stage) {
-    if (next < a.M) {
-      const uint32_t at = smem_u32(ring + stage * kOps * kOp * blockDim.x + threadIdx.x);
 #pragma unroll
-      for (int i = 0; i < kUnits; ++i) {
-        const int n = n0 - i * next_unit;
-        if (MODE == FULL || n > 0) {
+    for (int r = 0; r < R; ++r) {
+      if (next + r < a.M) {
+        const uint32_t at = smem_u32(ring + (stage * R + r) * kRow * blockDim.x + threadIdx.x);
 #pragma unroll
-          for (int o = 0; o < kOps; ++o) P::copy(at + (o * kOp + i * P::kPieces) * blockDim.x * 16, p[o] + i * next_unit, n, end[o]);
+        for (int i = 0; i < kUnits; ++i) {
+          const int n = n0 - i * next_unit;
+          if (MODE == FULL || n > 0) {
+#pragma unroll
+            for (int o = 0; o < kOps; ++o) P::copy(at + (o * kOp + i * P::kPieces) * blockDim.x * 16, p[o] + r * ld[o] + i * next_unit, n, end[o]);
+          }
         }
       }
     }
@@ -460,8 +481,8 @@ __global__ void __launch_bounds__(kRowThreads, 1) norm_bwd_rows(const NormBwdArg
     cp_commit();
   };
   for (int s = 0; s + 1 < stages; ++s) fetch(s);
-  // KEEP: u and xh stay in registers from the sums to dx; else they are formed again from the copies
-  constexpr bool KEEP = E == kThin, HOLD = KEEP;
+  // KEEP: u and xh of one row stay in registers from the sums to dx; else they are formed again from the copies
+  constexpr bool KEEP = E == kThin && R == 1, HOLD = E == kThin;
   Weights<W, kIn> w[HOLD ? kUnits : 1];
   uint64_t dw[kUnits][kPairs], db[kUnits][kPairs];
   auto weights = [&](int i, int to) {
@@ -475,29 +496,35 @@ __global__ void __launch_bounds__(kRowThreads, 1) norm_bwd_rows(const NormBwdArg
     for (int j = 0; j < kPairs; ++j) dw[i][j] = db[i][j] = 0;
   }
   int stage = 0, buf = 0;
-  int64_t m = (int64_t)blockIdx.x * groups + group.index;
-  float2 coming = m < a.M ? reinterpret_cast<const float2*>(a.stats)[m] : make_float2(0.f, 0.f);
+  int64_t m = ((int64_t)blockIdx.x * groups + group.index) * R;
+  float2 coming[R];
+#pragma unroll
+  for (int r = 0; r < R; ++r) coming[r] = m + r < a.M ? reinterpret_cast<const float2*>(a.stats)[m + r] : make_float2(0.f, 0.f);
   for (; m < a.M; m += step) {
-    const float2 st = coming;
-    if (m + step < a.M) coming = reinterpret_cast<const float2*>(a.stats)[m + step];
+    float2 st[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      st[r] = coming[r];
+      if (m + step + r < a.M) coming[r] = reinterpret_cast<const float2*>(a.stats)[m + step + r];
+    }
     fetch(stage == 0 ? stages - 1 : stage - 1);
     cp_wait(stages - 1);
-    uint4* at = ring + stage * kOps * kOp * blockDim.x + threadIdx.x;
+    uint4* at = ring + stage * R * kRow * blockDim.x + threadIdx.x;
     if (++stage == stages) stage = 0;
-    // unit i: xh, and dy (past the row's end 0, and with it all that is added)
-    auto unit = [&](int i, uint64_t (&xh)[kPairs], uint64_t (&d)[kPairs]) {
+    // unit i of row r: xh, and dy (past the row's end 0, and with it all that is added)
+    auto unit = [&](int r, int i, uint64_t (&xh)[kPairs], uint64_t (&d)[kPairs]) {
       const int n = n0 - i * next_unit;
-      const uint4* place = at + i * P::kPieces * blockDim.x;
-      P::read(xh, place, base[0] + m * ld[0] + i * next_unit, n);
-      P::read(d, place + kOp * blockDim.x, base[1] + m * ld[1] + i * next_unit, n);
+      const uint4* place = at + (r * kRow + i * P::kPieces) * blockDim.x;
+      P::read(xh, place, base[0] + (m + r) * ld[0] + i * next_unit, n);
+      P::read(d, place + kOp * blockDim.x, base[1] + (m + r) * ld[1] + i * next_unit, n);
       if (RES) {
         uint64_t g[kPairs];
-        P::read(g, place + 2 * kOp * blockDim.x, base[2] + m * ld[2] + i * next_unit, n);
+        P::read(g, place + 2 * kOp * blockDim.x, base[2] + (m + r) * ld[2] + i * next_unit, n);
 #pragma unroll
         for (int j = 0; j < kPairs; ++j) xh[j] = add2(xh[j], g[j]);
       }
 #pragma unroll
-      for (int j = 0; j < kPairs; ++j) xh[j] = mul2(add2(xh[j], both(-st.x)), both(st.y));
+      for (int j = 0; j < kPairs; ++j) xh[j] = mul2(add2(xh[j], both(-st[r].x)), both(st[r].y));
     };
     auto add_columns = [&](int i, const uint64_t (&xh)[kPairs], const uint64_t (&d)[kPairs]) {
 #pragma unroll
@@ -507,51 +534,65 @@ __global__ void __launch_bounds__(kRowThreads, 1) norm_bwd_rows(const NormBwdArg
       }
     };
     uint64_t u[KEEP ? kUnits : 1][kPairs], xh[KEEP ? kUnits : 1][kPairs];
-    uint64_t t = 0, tx = 0;
+    uint64_t t[R] = {}, tx[R] = {};
 #pragma unroll
-    for (int i = 0; i < kUnits; ++i) {
-      const int k = KEEP ? i : 0;
-      if (MODE == FULL || n0 - i * next_unit > 0) {
-        unit(i, xh[k], u[k]);
-        if (KEEP) add_columns(i, xh[k], u[k]);
-        uint64_t g[kPairs];
-        if (!HOLD) weights(i, 0);
-        w[HOLD ? i : 0].pairs(g);
+    for (int r = 0; r < R; ++r)
 #pragma unroll
-        for (int j = 0; j < kPairs; ++j) {
-          u[k][j] = mul2(u[k][j], g[j]);
-          t = add2(t, u[k][j]);
-          tx = fma2(u[k][j], xh[k][j], tx);
-        }
-      }
-    }
-    if (KEEP && a.dx == nullptr) continue;
-    float2 c12 = make_float2(0.f, 0.f);
-    if (a.dx != nullptr) c12 = group.sums<true>(sum2(t), sum2(tx), s_sums[buf]);
-    buf ^= 1;
-    const uint64_t c1 = both(-c12.x * a.inv_n), c2 = both(-c12.y * a.inv_n), rstd = both(st.y);
-#pragma unroll
-    for (int i = 0; i < kUnits; ++i) {
-      const int n = n0 - i * next_unit, k = KEEP ? i : 0;
-      uint4* place = at + i * P::kPieces * blockDim.x;
-      uint64_t g[kPairs] = {};
-      if (MODE == FULL || n > 0) {
-        if (!KEEP) {
-          unit(i, xh[k], u[k]);
-          add_columns(i, xh[k], u[k]);
+      for (int i = 0; i < kUnits; ++i) {
+        const int k = KEEP ? i : 0;
+        if (MODE == FULL || n0 - i * next_unit > 0) {
+          unit(r, i, xh[k], u[k]);
+          if (KEEP) add_columns(i, xh[k], u[k]);
+          uint64_t g[kPairs];
           if (!HOLD) weights(i, 0);
           w[HOLD ? i : 0].pairs(g);
 #pragma unroll
           for (int j = 0; j < kPairs; ++j) {
             u[k][j] = mul2(u[k][j], g[j]);
-            g[j] = 0;
+            t[r] = add2(t[r], u[k][j]);
+            tx[r] = fma2(u[k][j], xh[k][j], tx[r]);
           }
         }
-        if (DS) P::read(g, place + (kOps - 1) * kOp * blockDim.x, base[kOps - 1] + m * ld[kOps - 1] + i * next_unit, n);
-#pragma unroll
-        for (int j = 0; j < kPairs; ++j) g[j] = fma2(rstd, fma2(xh[k][j], c2, add2(u[k][j], c1)), g[j]);
       }
-      if (a.dx != nullptr && (MODE != ALIGNED || n > 0)) P::write(g, place, static_cast<T*>(a.dx) + m * a.ld_dx + c0 + i * next_unit, n);
+    if (KEEP && a.dx == nullptr) continue;
+    float4 c = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (a.dx != nullptr) {
+      if constexpr (R > 1) {
+        c = group.sums(make_float4(sum2(t[0]), sum2(tx[0]), sum2(t[R - 1]), sum2(tx[R - 1])), s_sums[buf]);
+      } else {
+        const float2 one = group.sums<true>(sum2(t[0]), sum2(tx[0]), reinterpret_cast<float2*>(s_sums[buf]));
+        c.x = one.x;
+        c.y = one.y;
+      }
+    }
+    buf ^= 1;
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      if (r > 0 && m + r >= a.M) break;
+      const uint64_t c1 = both(-(r == 0 ? c.x : c.z) * a.inv_n), c2 = both(-(r == 0 ? c.y : c.w) * a.inv_n), rstd = both(st[r].y);
+#pragma unroll
+      for (int i = 0; i < kUnits; ++i) {
+        const int n = n0 - i * next_unit, k = KEEP ? i : 0;
+        uint4* place = at + (r * kRow + i * P::kPieces) * blockDim.x;
+        uint64_t g[kPairs] = {};
+        if (MODE == FULL || n > 0) {
+          if (!KEEP) {
+            unit(r, i, xh[k], u[k]);
+            add_columns(i, xh[k], u[k]);
+            if (!HOLD) weights(i, 0);
+            w[HOLD ? i : 0].pairs(g);
+#pragma unroll
+            for (int j = 0; j < kPairs; ++j) {
+              u[k][j] = mul2(u[k][j], g[j]);
+              g[j] = 0;
+            }
+          }
+          if (DS) P::read(g, place + (kOps - 1) * kOp * blockDim.x, base[kOps - 1] + (m + r) * ld[kOps - 1] + i * next_unit, n);
+#pragma unroll
+          for (int j = 0; j < kPairs; ++j) g[j] = fma2(rstd, fma2(xh[k][j], c2, add2(u[k][j], c1)), g[j]);
+        }
+        if (a.dx != nullptr && (MODE != ALIGNED || n > 0)) P::write(g, place, static_cast<T*>(a.dx) + (m + r) * a.ld_dx + c0 + i * next_unit, n);
+      }
     }
   }
   cp_wait(0);
@@ -941,16 +982,27 @@ template <typename T, typename W> cudaError_t norm_fwd(const NormArgs& a, int nu
              : launch_pdl(norm_fwd_wide<T, W, false>, grid, norm_threads(a.N), 0, 1, st, a);
 }
 
-template <typename T, typename W, int MODE, int E, bool RES, bool DS>
-cudaError_t bwd_rows(const NormBwdArgs& a, int num_sms, int* parts, cudaStream_t st) {
+template <typename T, typename W, int MODE, int E, bool RES, bool DS, int R>
+cudaError_t bwd_each(const NormBwdArgs& a, int num_sms, int* parts, cudaStream_t st) {
   using P = Unit<T, MODE, E>;
-  static_assert(16 * (2 + RES + DS) * P::kUnits * P::kPieces * kRowThreads <= (MODE == UNALIGNED && sizeof(T) == 4 && RES && DS ? kRing * 4 / 3 : kRing),
+
+  static_assert(16 * R * (2 + RES + DS) * P::kUnits * P::kPieces * kRowThreads <= (MODE == UNALIGNED && sizeof(T) == 4 && RES && DS ? kRing * 4 / 3 : kRing),
                 "a stage at least");
-  const RowLaunch l(a.M, RowShape(a.N, a.M, num_sms, E), 1, 16 * (2 + RES + DS) * P::kUnits * P::kPieces, 2 * E * 4, num_sms);
-  const cudaError_t e = allow_ring<norm_bwd_rows<T, W, MODE, E, RES, DS>>(kRing);
+  const RowLaunch l(a.M, RowShape(a.N, a.M, num_sms, E), R, 16 * R * (2 + RES + DS) * P::kUnits * P::kPieces, 2 * E * 4, num_sms);
+  const cudaError_t e = allow_ring<norm_bwd_rows<T, W, MODE, E, RES, DS, R>>(kRing);
   if (e != cudaSuccess) return e;
   *parts = l.grid;
-  return launch_pdl(norm_bwd_rows<T, W, MODE, E, RES, DS>, dim3(l.grid), l.threads, l.smem, 1, st, a, l.warps, l.stages);
+  return launch_pdl(norm_bwd_rows<T, W, MODE, E, RES, DS, R>, dim3(l.grid), l.threads, l.smem, 1, st, a, l.warps, l.stages);
+}
+
+template <typename T, typename W, int MODE, int E, bool RES, bool DS>
+cudaError_t bwd_rows(const NormBwdArgs& a, int num_sms, int* parts, cudaStream_t st) {
+  // Two rows at a time as the forward, unless they are four operands or unaligned ones, which leave one stage (8000 x 5120
+  // bf16: 59.3 us by one row, 53.9 by two; with a residual 72.1, 61.3; 20000 x 2048 46.5, 42.5; 4096 x 7168 42.8, 39.0).
+  if constexpr (sizeof(T) == 2 && E == kThin && !(RES && DS) && MODE != UNALIGNED) {
+    if (a.M >= 4 * num_sms * RowShape(a.N, a.M, num_sms, E).groups) return bwd_each<T, W, MODE, E, RES, DS, 2>(a, num_sms, parts, st);
+  }
+  return bwd_each<T, W, MODE, E, RES, DS, 1>(a, num_sms, parts, st);
 }
 
 template <typename T, typename W, int MODE, int E> cudaError_t bwd_mode(const NormBwdArgs& a, int num_sms, int* parts, cudaStream_t st) {

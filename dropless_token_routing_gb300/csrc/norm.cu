@@ -199,18 +199,17 @@ template <typename W, int kIn> struct Weights {
 
 // A thread's units of a row are 16 bytes each, neighbouring threads' side by side, in the row as in shared
 // memory. UNALIGNED (some row does not start on a 16-byte boundary): a unit's copy is the two aligned pieces
-// around it. FULL: all units of a group are whole ones (widths of 32 E times its warps), which saves every
-// test for a row's end (8192 x 7680, two blocks on an SM: 95 us forward with them, 91 without).
+// around it, and a row may end inside one. ALIGNED: a thread has each unit as a whole or not at all (5760 wide: 45 us
+// forward and 55 backward, 47 and 58 with tests for a row's end inside a unit). FULL: it has all of them (widths of 32 E
+// times the warps), which saves every test (8192 x 7680, two blocks on an SM: 95 us forward with them, 91 without).
 enum RowMode { UNALIGNED = 0, ALIGNED = 1, FULL = 2 };
 template <typename T, int MODE, int E> struct Unit {
   static constexpr int kIn = 16 / sizeof(T), kPairs = kIn / 2, kUnits = E / kIn;   // elements; pairs; of a thread
   static constexpr int kPieces = MODE == UNALIGNED ? 2 : 1;
   // p: the unit's first element; n: elements of the row from there on; end: the tensor's
   static __device__ __forceinline__ void copy(uint32_t at, const T* p, int n, const T* end) {
-    if (MODE == FULL || (MODE == ALIGNED && n >= kIn)) {
+    if (MODE != UNALIGNED) {
       cp_async16(at, p);
-    } else if (MODE == ALIGNED) {
-      cp_async16(at, p, n * (int)sizeof(T));
     } else {
       const uintptr_t from = reinterpret_cast<uintptr_t>(p) & ~uintptr_t(15);
       const int64_t there = (int64_t)(reinterpret_cast<uintptr_t>(end) - from);   // up to the tensor's end
@@ -250,13 +249,8 @@ template <typename T, int MODE, int E> struct Unit {
       const int e = lane < 8 ? lane : tail / (int)sizeof(T) + lane - 8, stop = lane < 8 ? (skip < bytes ? skip : bytes) : bytes;
       if (lane < 16 && e * (int)sizeof(T) < stop) first[e] = reinterpret_cast<const T*>(seg)[e];
       __syncwarp();
-    } else if (MODE == FULL || n >= kIn) {
-      *reinterpret_cast<uint4*>(p) = v;
     } else {
-      const T* e = reinterpret_cast<const T*>(&v);
-#pragma unroll
-      for (int i = 0; i < kIn; ++i)
-        if (i < n) p[i] = e[i];
+      *reinterpret_cast<uint4*>(p) = v;
     }
   }
   static __device__ __forceinline__ void keep(uint64_t (&f)[kPairs], int n) {
@@ -406,7 +400,11 @@ __global__ void __launch_bounds__(kRowThreads, 1) norm_fwd_rows(const NormArgs a
         const int n = n0 - i * next_unit;
 #pragma unroll
         for (int j = 0; j < kPairs; ++j) f[r][i][j] = add2(f[r][i][j], both(-mean[r]));
-        if (MODE != FULL && n < kIn) P::keep(f[r][i], n);
+        if (MODE == UNALIGNED && n < kIn) P::keep(f[r][i], n);
+        if (MODE == ALIGNED && n <= 0) {
+#pragma unroll
+          for (int j = 0; j < kPairs; ++j) f[r][i][j] = 0;
+        }
 #pragma unroll
         for (int j = 0; j < kPairs; ++j) t[r] = fma2(f[r][i][j], f[r][i][j], t[r]);
       }
@@ -628,12 +626,12 @@ struct RowShape {
   }
   int threads() const { return warps * groups * 32; }
 };
-// vec: every row starts on a 16-byte boundary
-RowMode row_mode(int N, bool vec, int each) { return !vec ? UNALIGNED : N % (32 * each) == 0 ? FULL : ALIGNED; }
+// vec: every row starts on a 16-byte boundary; unit: elements of 16 bytes
+RowMode row_mode(int N, bool vec, int unit, int each) { return !vec || N % unit != 0 ? UNALIGNED : N % (32 * each) == 0 ? FULL : ALIGNED; }
 // 32 elements to a thread: wider rows than 512 threads of 16 hold (4000 x 16384: 124 us forward and 265 backward by a block
 // each, 91 and 149 so; 8000 x 5120, where a block holds one group of 16 and three of 32: 61 and 69 by those of 16, 56 and
 // 79 by those of 32). fp32 rows would leave no room to copy ahead.
-template <typename T> bool thick(int N, bool vec) { return sizeof(T) == 2 && vec && N > kRowsMaxN && N <= kThickMaxN; }
+template <typename T> bool thick(int N, bool vec) { return sizeof(T) == 2 && vec && N % 8 == 0 && N > kRowsMaxN && N <= kThickMaxN; }
 
 // ------------------------------------------------------------------ wide rows
 // A block for a row, in registers. 4000 x 16384 bf16 (now with 32 elements to a thread above) took 124 us, 4.2 TB/s: a
@@ -968,10 +966,10 @@ template <typename T, typename W> cudaError_t norm_fwd(const NormArgs& a, int nu
   const bool vec = a.M == 1 || (whole<T>(a.x, a.ld_x) && whole<T>(a.y, a.ld_y) && whole<T>(a.res, a.ld_res) && whole<T>(a.sum, a.ld_sum));
   if constexpr (sizeof(T) == 2) {
     if (thick<T>(a.N, vec))
-      return row_mode(a.N, vec, kThick) == FULL ? fwd_mode<T, W, FULL, kThick>(a, num_sms, st) : fwd_mode<T, W, ALIGNED, kThick>(a, num_sms, st);
+      return row_mode(a.N, vec, 8, kThick) == FULL ? fwd_mode<T, W, FULL, kThick>(a, num_sms, st) : fwd_mode<T, W, ALIGNED, kThick>(a, num_sms, st);
   }
   if (a.N <= kRowsMaxN) {
-    switch (row_mode(a.N, vec, kThin)) {
+    switch (row_mode(a.N, vec, 16 / (int)sizeof(T), kThin)) {
       case UNALIGNED: return fwd_mode<T, W, UNALIGNED, kThin>(a, num_sms, st);
       case ALIGNED: return fwd_mode<T, W, ALIGNED, kThin>(a, num_sms, st);
       case FULL: return fwd_mode<T, W, FULL, kThin>(a, num_sms, st);
@@ -1027,14 +1025,14 @@ template <typename T, typename W> cudaError_t norm_bwd(const NormBwdArgs& a, int
     return norm_bwd<T, W>(d, num_sms, st);
   }
   // (a stage of four unaligned fp32 operands, twice what they have, is more than the ring for 13 warps and up)
-  const bool four = sizeof(T) == 4 && !vdx && a.res != nullptr && a.d_sum != nullptr && a.dx != nullptr;
+  const bool four = sizeof(T) == 4 && row_mode(a.N, vdx, 4, kThin) == UNALIGNED && a.res != nullptr && a.d_sum != nullptr && a.dx != nullptr;
   const bool wide = !thick<T>(a.N, vdx) && a.N > (four ? kRowsMaxN * 3 / 4 : kRowsMaxN);
   if (thick<T>(a.N, vdx)) {
     if constexpr (sizeof(T) == 2)
-      e = row_mode(a.N, vdx, kThick) == FULL ? bwd_mode<T, W, FULL, kThick>(a, num_sms, &parts, st)
+      e = row_mode(a.N, vdx, 8, kThick) == FULL ? bwd_mode<T, W, FULL, kThick>(a, num_sms, &parts, st)
                                              : bwd_mode<T, W, ALIGNED, kThick>(a, num_sms, &parts, st);
   } else if (!wide) {
-    switch (row_mode(a.N, vdx, kThin)) {
+    switch (row_mode(a.N, vdx, 16 / (int)sizeof(T), kThin)) {
       case UNALIGNED: e = bwd_mode<T, W, UNALIGNED, kThin>(a, num_sms, &parts, st); break;
       case ALIGNED: e = bwd_mode<T, W, ALIGNED, kThin>(a, num_sms, &parts, st); break;
       case FULL: e = bwd_mode<T, W, FULL, kThin>(a, num_sms, &parts, st); break;

@@ -980,6 +980,27 @@ class TokenLogprobs:
         return out
 
 
+_addresses_are = getattr(torch._C, "_tensors_data_ptrs_at_indices_equal", None)
+
+
+def _places(tensors):
+    """Where contiguous tensors lie, how large they are and their types."""
+    return [t.data_ptr() for t in tensors], list(range(len(tensors))), [t.numel() for t in tensors], [t.dtype for t in tensors]
+
+
+def _in_places(tensors, places):
+    """Whether tensors are what _places found. An address does not say that: the memory there may be another
+    tensor's by now, or the same one's with another type or order. (In one call for each property, as a list of
+    hundreds takes as long as the kernels do.)"""
+    if places is None:
+        return False
+    addresses, every, sizes, types = places
+    return ((_addresses_are(tensors, addresses, every) if _addresses_are is not None else
+             list(map(torch.Tensor.data_ptr, tensors)) == addresses) and
+            list(map(torch.Tensor.numel, tensors)) == sizes and [t.dtype for t in tensors] == types and
+            all(map(torch.Tensor.is_contiguous, tensors)))
+
+
 class GradClipper:
     """The global norm of a list (or dict) of gradients, and their clipping: moe_clip_grads on a kept list
     (contiguous fp32 or bf16 tensors; those of None are left out).
@@ -987,7 +1008,7 @@ class GradClipper:
     ``norm()`` returns the norm, ``clip(max_norm)`` also scales the gradients by min(1, max_norm / (norm +
     1e-6)), in place, or into ``out`` (a list of the same shape and types). Both return a tensor of one number
     without waiting for it, an own buffer that the next call writes; ``scale`` holds the factor of the
-    last call. A tensor that has moved (``t.data = ...``) is taken where it is then, another tensor in its place (a
+    last call. A tensor that has moved (``t.data = ...``) is taken where and as it is then, another tensor in its place (a
     parameter's new ``grad``) is not; a captured graph takes those of the capture. One instance serves one stream at a time, which waits for the one it was made on.
     """
 
@@ -1012,9 +1033,6 @@ class GradClipper:
         self._np, self._sp = self._norm.data_ptr(), self.scale.data_ptr()
         self._clip_table, self._norm_table = (N.Grad * max(n, 1))(), (N.Grad * max(n, 1))()
         self._call = N.lib().moe_clip_grads
-        # where the gradients and the results are, and how large
-        self._ask = [f for t in self.grads for f in (t.data_ptr, t.numel)]
-        self._ask_out = [] if self.out is self.grads else [f for t in self.out for f in (t.data_ptr, t.numel)]
         self._bind()
 
     def _bind(self):
@@ -1032,7 +1050,7 @@ class GradClipper:
             self._clip_table[i] = N.Grad(g.data_ptr(), o.data_ptr(), g.numel(), _dt(g.dtype))
             self._norm_table[i] = N.Grad(g.data_ptr(), None, g.numel(), _dt(g.dtype))
         self._check_places()
-        self._places, self._out_places = [f() for f in self._ask], [f() for f in self._ask_out]
+        self._places, self._out_places = _places(self.grads), _places(self.out)
 
     def _check_places(self):
         """No result may overlap another one, or a gradient other than its own (that one only as a whole)."""
@@ -1062,11 +1080,12 @@ class GradClipper:
         return self._norm
 
     def norm(self, stream=None):
-        if [f() for f in self._ask] != self._places:
+        if not _in_places(self.grads, self._places):
             self._bind()
         return self._run(self._norm_table, float("inf"), stream)
 
     def clip(self, max_norm, stream=None):
-        if [f() for f in self._ask] != self._places or [f() for f in self._ask_out] != self._out_places:
+        if not _in_places(self.grads, self._places) or not (
+                self.out is self.grads or _in_places(self.out, self._out_places)):
             self._bind()
         return self._run(self._clip_table, max_norm, stream)

@@ -450,3 +450,50 @@ def test_views_of_many_numbers_of_rows(lib):
         assert lp.forward(x[:M], stream=ST)["top_idx"].shape == (M, 1)
     assert max(map(len, (ln._views, ln._shapes, lp._views))) <= A._KEPT_VIEWS
     assert lib.last("moe_norm_bwd")[5] == ln._bufs["stats"].data_ptr()
+
+
+def test_clip_takes_tensors_of_another_type_or_order_at_the_same_address(lib):
+    """Address and number of elements alone do not say what lies there."""
+    a, o = z(100), z(100)
+    for out in (None, [o]):
+        for call in ("clip", "norm"):
+            a.data, o.data = z(100), z(100)
+            k = clipper([a], out=out)
+            run = (lambda: k.clip(1.0, stream=ST)) if call == "clip" else (lambda: k.norm(stream=ST))
+            run()
+            at, here = a.data_ptr(), a.data
+            a.data = here.view(BF)[:100]
+            if out is not None:
+                o.data = o.data.view(BF)[:100]
+            run()
+            assert lib.last("moe_clip_grads")[0][0] == (at, None if call == "norm" else k.out[0].data_ptr(), 100, N.MOE_BF16)
+            a.data = here.view(torch.int32)      # no type that it takes
+            with pytest.raises(ValueError):
+                run()
+            a.data = here
+            if out is not None:
+                with pytest.raises(ValueError):  # the result's type is still the other one
+                    run()
+
+
+def test_clip_refuses_tensors_that_were_transposed(lib):
+    a, o = z(4, 4), z(4, 4)
+    for out, t in ((None, a), ([o], a), ([o], o)):
+        k = clipper([a], out=out)
+        for run in (lambda: k.clip(1.0, stream=ST), lambda: k.norm(stream=ST)):
+            run()
+            t.data = t.data.t()
+            for _ in range(2):                   # (not the second time either)
+                with pytest.raises(ValueError):
+                    k.clip(1.0, stream=ST)
+            t.data = t.data.t()
+            run()
+
+
+def test_clip_takes_fewer_elements_at_the_same_address(lib):
+    a = z(100)
+    k = clipper([a])
+    k.clip(1.0, stream=ST)
+    a.data = a.data[:60]
+    k.clip(1.0, stream=ST)
+    assert lib.last("moe_clip_grads")[0][0] == (a.data_ptr(), a.data_ptr(), 60, 0)

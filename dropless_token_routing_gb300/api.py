@@ -361,6 +361,19 @@ def _same(t, ref, ptr):
     return t is ref() and (t.data_ptr() if t is not None else None) == ptr
 
 
+def _unchanged(*tensors):
+    """Says of the same tensors later on, all in one call, whether types, shapes and strides are the present ones: the
+    address alone does not, as the memory there may be another tensor's by then, or the same one's in another order.
+    It may say no where none of these has changed (a tensor now requires its gradient, another mode)."""
+    try:
+        return torch._C._dynamo.guards.TensorGuards(
+            *tensors, dynamic_dims_sizes=[list(t.shape) for t in tensors],
+            dynamic_dims_strides=[list(t.stride()) for t in tensors]).check
+    except Exception:       # (none, or another form of it)
+        were = [(t.dtype, t.shape, t.stride()) for t in tensors]
+        return lambda *tensors: [(t.dtype, t.shape, t.stride()) for t in tensors] == were
+
+
 class MoEDecodeLayer:
     """The whole MoE layer for a few tokens: moe_layer_decode on a kept workspace.
 
@@ -720,6 +733,7 @@ class LayerNorm:
         if self.bias is not None:
             _dense(self.bias, "bias", self.w_dtype, (self.N,), self.device)
         self._w_ptr, self._b_ptr = self.weight.data_ptr(), _p(self.bias)
+        self._like = _unchanged(self.weight) if self.bias is None else _unchanged(self.weight, self.bias)
         self._w_ref, self._b_ref = _ref(self.weight), _ref(self.bias)
 
     def _view(self, name, M, stream):
@@ -758,7 +772,8 @@ class LayerNorm:
         shape = self._shapes.get(M) or self._shape(M)
         ld_x = n if x.dtype is dt and x.shape == shape and x.is_contiguous() and x.device == dev else _matrix(x, "x", dt, M, n, dev)
         w, b = self.weight, self.bias
-        if w is not self._w_ref() or b is not self._b_ref() or w.data_ptr() != self._w_ptr or (b is not None and b.data_ptr() != self._b_ptr):
+        if w is not self._w_ref() or b is not self._b_ref() or w.data_ptr() != self._w_ptr or (
+                not self._like(w) if b is None else b.data_ptr() != self._b_ptr or not self._like(w, b)):
             self._bind()
         xp, row = x.data_ptr(), M * self._size     # (row times a stride: the span of rows that far apart)
         if out is None:
@@ -818,7 +833,8 @@ class LayerNorm:
         M = x.shape[0]
         shape, row = x.shape, M * self._size
         w, b = self.weight, self.bias
-        if w is not self._w_ref() or b is not self._b_ref() or w.data_ptr() != self._w_ptr or (b is not None and b.data_ptr() != self._b_ptr):
+        if w is not self._w_ref() or b is not self._b_ref() or w.data_ptr() != self._w_ptr or (
+                not self._like(w) if b is None else b.data_ptr() != self._b_ptr or not self._like(w, b)):
             self._bind()
         ld_y = n if dy.dtype is dt and dy.shape == shape and dy.is_contiguous() and dy.device == dev else _matrix(dy, "dy", dt, M, n, dev)
         dx = dw = db = dxp = dwp = dbp = sp = None
@@ -984,24 +1000,18 @@ _addresses_are = getattr(torch._C, "_tensors_data_ptrs_at_indices_equal", None)
 
 
 class _Places:
-    """Where contiguous tensors lie, how large they are and their types. An address does not say the rest: the
-    memory there may be another tensor's by now, or the same one's with another type or order.
+    """Where contiguous tensors lie, how large they are and their types.
 
     To ask hundreds of tensors takes as long as the kernels run (300 gradients clipped into as many others in 105 us: 124 us
     of host time with calls for each tensor and property), so torch is asked for all of them at once where it can be (73
-    us). That may say no where nothing has changed (a tensor now requires its gradient, another mode): then each is asked.
+    us), and for each when that says no.
     """
 
     def __init__(self, tensors):
         self.tensors = list(tensors)
         self.addresses, self.every = [t.data_ptr() for t in tensors], list(range(len(tensors)))
         self.sizes, self.types = [t.numel() for t in tensors], [t.dtype for t in tensors]
-        try:
-            self.unchanged = torch._C._dynamo.guards.TensorGuards(
-                *tensors, dynamic_dims_sizes=[list(t.shape) for t in tensors],
-                dynamic_dims_strides=[list(t.stride()) for t in tensors]).check
-        except Exception:       # (none, or another form of it)
-            self.unchanged = lambda *tensors: False
+        self.unchanged = _unchanged(*tensors)
 
     def hold(self):
         ts = self.tensors

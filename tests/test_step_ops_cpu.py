@@ -497,3 +497,37 @@ def test_clip_takes_fewer_elements_at_the_same_address(lib):
     a.data = a.data[:60]
     k.clip(1.0, stream=ST)
     assert lib.last("moe_clip_grads")[0][0] == (a.data_ptr(), a.data_ptr(), 60, 0)
+
+
+@pytest.mark.parametrize("change", [lambda t: t.view(BF)[:64], lambda t: t.view(torch.int32), lambda t: t[:63],
+                                    lambda t: t.as_strided((64,), (2,))])
+def test_norm_refuses_weights_of_another_type_size_or_stride_at_the_same_address(lib, change):
+    x, ln = z(4, 64), layer_norm()
+    for name in ("weight", "bias"):
+        t, here = getattr(ln, name), z(128)[:64]
+        t.data = here
+        ln.forward(x, save=True, stream=ST)
+        calls = len(lib.calls)
+        t.data = change(here)
+        assert t.data_ptr() == here.data_ptr()
+        for call in (lambda: ln.forward(x, stream=ST), lambda: ln.backward(x, stream=ST)) * 2:
+            with pytest.raises(ValueError):
+                call()
+        assert len(lib.calls) == calls
+        t.data = here
+        ln.backward(x, stream=ST)
+        ln.forward(x, stream=ST)
+
+
+def test_norm_weights_that_require_gradients_and_modes(lib):
+    """What else may change about a weight changes nothing."""
+    x, w = z(4, 64), torch.nn.Parameter(z(64))
+    for bias in (None, torch.nn.Parameter(z(64))):
+        ln = A.LayerNorm(w, bias, max_rows=4, device=DEV)
+        for needed in (True, False, True):
+            w.requires_grad_(needed)
+            for mode in (torch.enable_grad, torch.no_grad, torch.inference_mode, torch.enable_grad):
+                with mode():
+                    ln.forward(x, save=True, stream=ST)
+                    assert lib.last("moe_norm_fwd")[2] == w.data_ptr()
+                    ln.backward(x, stream=ST)

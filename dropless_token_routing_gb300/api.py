@@ -407,12 +407,14 @@ class MoEDecodeLayer:
         self._T = 0
 
     def _present(self):
-        p = self.params
+        p, there = self.params, []
         for name, ref, ptr in self._bound:
             t = getattr(p, name)
             if t is not ref() or (t.data_ptr() if t is not None else None) != ptr:
                 return False
-        return True
+            if t is not None:
+                there.append(t)
+        return self._like(*there)
 
     def _bind(self):
         """Takes the weights that params holds; those that are there have the layer's type, size and
@@ -428,7 +430,9 @@ class MoEDecodeLayer:
                 _elsewhere(name, self.device, t)
         for name, _ in c._fields_:
             setattr(c, name, _p(getattr(p, name)))
-        self._bound = tuple((name, _ref(getattr(p, name)), getattr(c, name)) for name, _, _ in self._weights)
+        there = [getattr(p, name) for name, _, _ in self._weights]
+        self._like = _unchanged(*[t for t in there if t is not None])
+        self._bound = tuple((name, _ref(t), getattr(c, name)) for (name, _, _), t in zip(self._weights, there))
 
     @property
     def topk_idx(self):
@@ -511,6 +515,7 @@ class Linear:
             self._workspaces.append(self.ws)
         D.ld_w = ld_w
         self._w_ptr, self._b_ptr = w.data_ptr(), _p(bias)
+        self._like = _unchanged(w) if bias is None else _unchanged(w, bias)
         self._w_ref, self._b_ref = _ref(w), _ref(bias)
 
     def _own(self, name, rows, cols, stream):
@@ -540,7 +545,8 @@ class Linear:
             ld_y = n
         else:
             y, yp, ld_y = out, out.data_ptr(), _matrix(out, "out", dtype, M, n, dev)
-        if not (_same(self.w, self._w_ref, self._w_ptr) and _same(self.bias, self._b_ref, self._b_ptr)):
+        if not (_same(self.w, self._w_ref, self._w_ptr) and _same(self.bias, self._b_ref, self._b_ptr) and
+                (self._like(self.w) if self.bias is None else self._like(self.w, self.bias))):
             self._bind(stream)
         # what is read may not lie where y is written, but for a residual in the same place
         end = yp + M * ld_y * size
@@ -570,7 +576,8 @@ class Linear:
         if x is None:
             raise ValueError("backward: the last forward did not save (save=True)")
         M = x.shape[0]
-        if not (_same(self.w, self._w_ref, self._w_ptr) and _same(self.bias, self._b_ref, self._b_ptr)):
+        if not (_same(self.w, self._w_ref, self._w_ptr) and _same(self.bias, self._b_ref, self._b_ptr) and
+                (self._like(self.w) if self.bias is None else self._like(self.w, self.bias))):
             self._bind(stream)
         ld_x, xp, ld_w = _matrix(x, "x", self.dtype, M, self.K, self.device), x.data_ptr(), D.ld_w
         ld_y, yp = _matrix(dy, "dy", self.dtype, M, n, self.device), dy.data_ptr()

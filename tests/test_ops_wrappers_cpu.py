@@ -428,3 +428,71 @@ def test_one_odd_row_keeps_its_whole_vectors(lib):
     assert lib.last("moe_linear_fwd")[4]["ld_x"] == 72
     lin.forward(torch.zeros(1, 67, dtype=torch.bfloat16), stream=ST)
     assert lib.last("moe_linear_fwd")[4]["ld_x"] == 67
+
+
+# ------------------------------------------------------------------ other tensors at a weight's address
+BF = torch.bfloat16
+
+
+@pytest.mark.parametrize("change", [lambda t: t.view(BF)[:, :32], lambda t: t.view(torch.int32), lambda t: t[:31], lambda t: t.t()])
+def test_linear_refuses_a_weight_of_another_type_size_or_order_at_the_same_address(lib, change):
+    lin, x, w = linear(N_=32, K=32), torch.zeros(4, 32), torch.zeros(32, 32)
+    lin.w.data = w
+    lin.forward(x, save=True, stream=ST)
+    calls = len(lib.calls)
+    lin.w.data = change(w)
+    assert lin.w.data_ptr() == w.data_ptr()
+    for call in (lambda: lin.forward(x, stream=ST), lambda: lin.backward(x, stream=ST)) * 2:
+        with pytest.raises(ValueError):
+            call()
+    assert len(lib.calls) == calls
+    lin.w.data = w
+    lin.backward(x, stream=ST)
+    lin.forward(x, stream=ST)
+
+
+def test_linear_takes_another_distance_of_rows_at_the_same_address(lib):
+    lin, buf = linear(N_=8, K=16), torch.zeros(8, 64)
+    lin.w.data = buf[:, :16]
+    lin.forward(torch.zeros(2, 16), stream=ST)
+    assert lib.last("moe_linear_fwd")[4]["ld_w"] == 64
+    lin.w.data = buf.view(-1)[:8 * 32].view(8, 32)[:, :16]
+    lin.forward(torch.zeros(2, 16), stream=ST)
+    assert lib.last("moe_linear_fwd")[4]["ld_w"] == 32
+
+
+@pytest.mark.parametrize("change", [lambda t: t.view(BF)[:32], lambda t: t.view(torch.int32), lambda t: t[:31], lambda t: t.as_strided((32,), (2,))])
+def test_linear_refuses_a_bias_of_another_type_size_or_stride_at_the_same_address(lib, change):
+    bias, here = torch.zeros(32), torch.zeros(64)[:32]
+    lin = A.Linear(torch.zeros(32, 16), bias, max_rows=4, device=DEV, stream=ST)
+    bias.data = here
+    lin.forward(torch.zeros(4, 16), stream=ST)
+    bias.data = change(here)
+    for _ in range(2):
+        with pytest.raises(ValueError):
+            lin.forward(torch.zeros(4, 16), stream=ST)
+    bias.data = here
+    lin.forward(torch.zeros(4, 16), stream=ST)
+
+
+@pytest.mark.parametrize("name", ["w13", "w2", "ws13", "ws2", "w_r", "bias"])
+@pytest.mark.parametrize("change", [lambda t: t.view(torch.int32), lambda t: t.view(BF).view(-1)[:t.numel()].view(t.shape),
+                                    lambda t: t.view(-1)[:-1], lambda t: t.as_strided(t.shape, t.stride()[:-1] + (2,))])
+def test_decode_refuses_weights_of_another_type_size_or_stride_at_the_same_address(lib, name, change):
+    d, E, k, f, S = 64, 4, 2, 64, 1
+    sizes = dict(w13=(E, 2 * f, d), w2=(E, d, f), w_r=(d, E), bias=(E,), ws13=(S, 2 * f, d), ws2=(S, d, f))
+    at = {n: torch.zeros(2 * torch.Size(s).numel()) for n, s in sizes.items()}
+    here = {n: at[n][:torch.Size(s).numel()].view(s) for n, s in sizes.items()}
+    params = A.LayerParams(**{n: t.view(t.shape) for n, t in here.items()})
+    layer = A.MoEDecodeLayer(params, 4, d, E, k, f, S, f, torch.float32, device=DEV, stream=ST)
+    x = torch.zeros(2, d)
+    layer.forward(x, stream=ST)
+    calls, t = len(lib.calls), getattr(params, name)
+    t.data = change(here[name])
+    assert t.data_ptr() == here[name].data_ptr()
+    for _ in range(2):
+        with pytest.raises(ValueError):
+            layer.forward(x, stream=ST)
+    assert len(lib.calls) == calls
+    t.data = here[name].reshape(-1)          # any shape of them
+    layer.forward(x, stream=ST)

@@ -82,7 +82,7 @@ class NormDims(ctypes.Structure):
 
 class LogprobDims(ctypes.Structure):
     _fields_ = [("M", c_int64), ("V", c_int32), ("n_top", c_int32), ("dtype", c_int32), ("ld", c_int64),
-                ("ld_grad", c_int64)]
+                ("ld_grad", c_int64), ("keep_entropy", c_int32)]
 
 
 class Grad(ctypes.Structure):

@@ -901,7 +901,7 @@ class TokenLogprobs:
 
     ``forward(scores, tokens=None, entropy=False, save=False)`` returns a dict of ``logprob`` [M] (with
     tokens), ``entropy`` [M] (if asked for), ``top_idx`` and ``top_logprob`` [M, top] (if top > 0): own
-    buffers, written by the next call. A token outside [0, V) is padding (0). With ``save=True`` it keeps
+    buffers, written by the next call (they may be changed, the backward does not read them). A token outside [0, V) is padding (0). With ``save=True`` it keeps
     scores and tokens (unchanged until then) for ``backward(d_logprob=None, d_entropy=None)``, which returns the
     gradient of the scores [M, V]: an own buffer unless ``out`` is given, which may be the scores (what was kept is
     then gone). One instance
@@ -910,12 +910,12 @@ class TokenLogprobs:
 
     def __init__(self, max_rows, V, top=0, dtype=torch.float32, device="cuda", stream=None):
         self.max_rows, self.V, self.top, self.dtype = max_rows, V, top, dtype
-        self.dims = N.LogprobDims(int(max_rows), V, top, _dt(dtype), 0, 0)
+        self.dims = N.LogprobDims(int(max_rows), V, top, _dt(dtype), 0, 0, 1)
         if not (0 <= max_rows <= 1 << 30 and 1 <= V <= 1 << 22 and 0 <= top <= 32):
             raise N.MoeError(N.STATUS_CODE["MOE_ERR_BAD_DIMS"], "moe_token_logprob")
         self.device, self._index = _device(device)
         with _on(stream, self.device):
-            self._logprob, self._entropy, self._stats = (torch.empty(max_rows, w, dtype=torch.float32, device=device) for w in (1, 1, 2))
+            self._logprob, self._entropy, self._stats = (torch.empty(max_rows, w, dtype=torch.float32, device=device) for w in (1, 1, 4))
             top_idx = torch.empty(max_rows, top, dtype=torch.int32, device=device)
             top_logprob = torch.empty(max_rows, top, dtype=torch.float32, device=device)
         self._top = top_idx, top_logprob
@@ -994,7 +994,7 @@ class TokenLogprobs:
         _in_place("scores", scores, ld, out, ld_g, "their gradient")
         D.M, D.ld, D.ld_grad = M, ld, ld_g
         self._set = M, ld
-        st = self._bwd(scores.data_ptr(), _p(tokens), self._stats.data_ptr(), self._entropy.data_ptr(), _p(d_logprob), _p(d_entropy),
+        st = self._bwd(scores.data_ptr(), _p(tokens), self._stats.data_ptr(), None, _p(d_logprob), _p(d_entropy),
                        self._dims_ref, out.data_ptr(), _stream(stream, self._index))
         if st:
             N.check(st, "moe_token_logprob_bwd")

@@ -426,8 +426,13 @@ __global__ void __launch_bounds__(LT, (kBlocks<T, LU, ENT, TOP>)) logprob_kernel
       const float log_sum = s.S == 0.f ? -kInf : logf(s.S);   // a row without a distribution: -inf
       if (lane == 0) {
         if (a.logprob != nullptr) a.logprob[m] = token < 0 ? 0.f : s.S == 0.f ? -kInf : (given - s.m) - log_sum;
-        if (a.stats != nullptr) reinterpret_cast<float2*>(a.stats)[m] = make_float2(s.m, log_sum);
-        if (ENT) a.entropy[m] = s.S == 0.f ? 0.f : log_sum - s.D / s.S;
+        const float H = ENT && s.S != 0.f ? log_sum - s.D / s.S : 0.f;
+        if (a.stats != nullptr) {
+          float2* st = reinterpret_cast<float2*>(a.stats) + (a.keep_entropy ? 2 * m : m);
+          st[0] = make_float2(s.m, log_sum);
+          if (ENT && a.keep_entropy) st[1].x = H;
+        }
+        if (ENT) a.entropy[m] = H;
         if (TOP) s_row = make_float2(s.m, log_sum);
       }
     }
@@ -490,13 +495,14 @@ __global__ void __launch_bounds__(LT) logprob_bwd_kernel(const LogprobBwdArgs a)
   const Places<T> row(first, a.V);
   T* out = static_cast<T*>(a.dx) + m * a.ld_dx - row.lead;   // of place 0
   const bool vec = (reinterpret_cast<uintptr_t>(out) & 15) == 0;
-  const float2 st = reinterpret_cast<const float2*>(a.stats)[m];
+  const float2* kept = reinterpret_cast<const float2*>(a.stats) + (a.keep_entropy ? 2 * m : m);
+  const float2 st = kept[0];
   const bool some = !(st.y == -kInf);     // the row has a distribution
   int token = a.d_logprob != nullptr && some ? a.tokens[m] : -1;
   if (token >= a.V) token = -1;
   const float g = token >= 0 ? a.d_logprob[m] : 0.f;
   token += row.lead;                      // its place (no other place counts when g is 0)
-  const float h = a.d_entropy != nullptr && some ? a.d_entropy[m] : 0.f, H = h != 0.f ? a.entropy[m] : 0.f;
+  const float h = a.d_entropy != nullptr && some ? a.d_entropy[m] : 0.f, H = h == 0.f ? 0.f : a.keep_entropy ? kept[1].x : a.entropy[m];
   const bool zero = g == 0.f && h == 0.f;
   for (int j0 = (blockIdx.y * GU * LT + threadIdx.x) * 8; j0 < row.end; j0 += gridDim.y * GC) {
     Vec8<T> v[GU];

@@ -139,11 +139,12 @@ constexpr int kMaxTop = 32;   // alternatives
 struct LogprobArgs {
   const void* x;
   const int32_t* tokens;
-  float *logprob, *stats, *entropy;   // stats [M][2]: maximum, ln sum e^(x - maximum)
+  float *logprob, *stats, *entropy;   // stats [M][2]: maximum, ln sum e^(x - maximum); [M][4] if kept: the entropy too
   int32_t* top_idx;
   float* top_logprob;
   int64_t M, ld;
   int V, n_top;
+  bool keep_entropy;
 };
 struct LogprobBwdArgs {
   const void* x;
@@ -152,6 +153,7 @@ struct LogprobBwdArgs {
   void* dx;
   int64_t M, ld, ld_dx;
   int V;
+  bool keep_entropy;   // entropy: not read, it is in stats
 };
 cudaError_t launch_logprob(const LogprobArgs& a, int dtype, int num_sms, cudaStream_t st);
 cudaError_t launch_logprob_bwd(const LogprobBwdArgs& a, int dtype, int num_sms, cudaStream_t st);

@@ -182,7 +182,9 @@ int resolve_logprob(const moe_logprob_dims* in, moe_logprob_dims* d) {
   if (in == nullptr) return MOE_ERR_NULL_POINTER;
   *d = *in;
   if (d->dtype != MOE_F32 && d->dtype != MOE_BF16) return MOE_ERR_UNSUPPORTED_DTYPE;
-  if (d->M < 0 || d->M > (1 << 30) || d->V < 1 || d->V > (1 << 22) || d->n_top < 0 || d->n_top > kMaxTop) return MOE_ERR_BAD_DIMS;
+  if (d->M < 0 || d->M > (1 << 30) || d->V < 1 || d->V > (1 << 22) || d->n_top < 0 || d->n_top > kMaxTop ||
+      d->keep_entropy < 0 || d->keep_entropy > 1)
+    return MOE_ERR_BAD_DIMS;
   for (int64_t* ld : {&d->ld, &d->ld_grad}) {
     if (*ld == 0) *ld = d->V;
     if (*ld < d->V || *ld > kMaxLd) return MOE_ERR_BAD_DIMS;
@@ -393,7 +395,7 @@ int moe_token_logprob(const void* scores, const int32_t* tokens, const moe_logpr
   if (!some) return MOE_OK;
   int sms = 0;
   OP_TRY(check_device(&sms));
-  const LogprobArgs a = {scores, tokens, logprob, stats, entropy, top_idx, top_logprob, d.M, d.ld, d.V, d.n_top};
+  const LogprobArgs a = {scores, tokens, logprob, stats, entropy, top_idx, top_logprob, d.M, d.ld, d.V, d.n_top, d.keep_entropy != 0};
   return launch_logprob(a, d.dtype, sms, (cudaStream_t)stream) == cudaSuccess ? MOE_OK : MOE_ERR_LAUNCH;
 }
 
@@ -406,14 +408,14 @@ int moe_token_logprob_bwd(const void* scores, const int32_t* tokens, const float
   OP_TRY(req_if(scores, some));
   OP_TRY(req_rows_if(tokens, some && d_logprob != nullptr));
   OP_TRY(req_if(stats, some));
-  OP_TRY(req_rows_if(entropy, some && d_entropy != nullptr));
+  OP_TRY(req_rows_if(entropy, some && d_entropy != nullptr && d.keep_entropy == 0));
   OP_TRY(opt_rows(d_logprob));
   OP_TRY(opt_rows(d_entropy));
   OP_TRY(req_if(d_scores, some));
   if (!some) return MOE_OK;
   int sms = 0;
   OP_TRY(check_device(&sms));
-  const LogprobBwdArgs a = {scores, tokens, stats, entropy, d_logprob, d_entropy, d_scores, d.M, d.ld, d.ld_grad, d.V};
+  const LogprobBwdArgs a = {scores, tokens, stats, entropy, d_logprob, d_entropy, d_scores, d.M, d.ld, d.ld_grad, d.V, d.keep_entropy != 0};
   return launch_logprob_bwd(a, d.dtype, sms, (cudaStream_t)stream) == cudaSuccess ? MOE_OK : MOE_ERR_LAUNCH;
 }
 

@@ -494,6 +494,7 @@ typedef struct moe_logprob_dims {
   int32_t dtype;    /* enum moe_dtype: the scores and their gradient */
   int64_t ld;       /* elements between rows of scores (>= V, <= 2^36), 0 = V */
   int64_t ld_grad;  /* ... of d_scores */
+  int32_t keep_entropy;  /* 1: stats has four numbers for a row and the entropy among them, 0: two */
 } moe_logprob_dims;
 
 /* Log probabilities under p = softmax of each row of scores [M, V]:
@@ -501,7 +502,9 @@ typedef struct moe_logprob_dims {
  *   entropy[m] = - sum_j p_j ln p_j
  *   top_idx, top_logprob [M][n_top]: the n_top most probable tokens, descending, equal scores by the
  *     lower index, and their ln p; -1 and -inf where there are no more
- *   stats [M][2]: the largest score and ln sum_j e^(x_j - largest), for the backward
+ *   stats [M][2]: the largest score and ln sum_j e^(x_j - largest), for the backward; with keep_entropy
+ *     [M][4]: these two and, if entropy is returned, it too, so that the returned one may be changed before
+ *     the backward
  * logprob, entropy and stats may each be NULL (not returned); tokens [M] int32 is read for logprob alone.
  * What has one number for a row need only be aligned to it (a slice of a batch). The results overlap no operand,
  * but for top_idx of one alternative, which may be the buffer of tokens.
@@ -515,7 +518,8 @@ int moe_token_logprob(const void* scores, const int32_t* tokens, const moe_logpr
  *   d_scores[m, j] = d_logprob[m] ([j = token[m]] - p_j) - d_entropy[m] p_j (ln p_j + entropy[m])
  * A token outside [0, V) has no first term; a row of -inf, and one whose two gradients are 0, gets
  * zeros (also where its scores are NaN). d_logprob or d_entropy may be NULL (zero; tokens, or entropy, is not read then). entropy
- * and stats as moe_token_logprob wrote them. d_scores may be the buffer of scores when the strides
+ * and stats as moe_token_logprob wrote them; with keep_entropy as there, the entropy is taken from stats
+ * (and entropy not read). d_scores may be the buffer of scores when the strides
  * agree; it overlaps nothing else. dims->n_top is not read. */
 int moe_token_logprob_bwd(const void* scores, const int32_t* tokens, const float* stats, const float* entropy,
                           const float* d_logprob, const float* d_entropy, const moe_logprob_dims* dims,

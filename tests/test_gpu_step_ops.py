@@ -757,3 +757,39 @@ def test_step_operators_on_another_stream():
         results.append([y, dx, *out.values(), d, norm])
     for a, e in zip(*results):
         assert torch.equal(a, e)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("M,V", [(1, 40000), (3, 777), (300, 1000)])
+def test_logprob_entropy_changed_before_the_backward(M, V, dtype):
+    """The gradient is that of the entropy that was taken, whatever has become of the results since."""
+    A, g = _api(), _gen(M + V)
+    x, tokens = _rand(g, M, V, std=2, dtype=dtype).cuda(), torch.randint(-1, V, (M,), generator=g, dtype=torch.int32).cuda()
+    gl, gh = _rand(g, M).cuda(), _rand(g, M).cuda()
+    lp = A.TokenLogprobs(M + 5, V, top=2, dtype=dtype)
+    lp.forward(x, tokens, entropy=True, save=True)
+    want = lp.backward(gl, d_entropy=gh).clone()
+    out = lp.forward(x, tokens, entropy=True, save=True)
+    out["entropy"].neg_().add_(7.0)
+    out["logprob"].zero_()
+    assert torch.equal(lp.backward(gl, d_entropy=gh), want)
+
+
+def test_logprob_entropy_where_the_caller_keeps_it():
+    """The library's calls with two statistics for a row and the entropy beside them: the wrapper's bits."""
+    from dropless_token_routing_gb300 import _native as native
+    A, g, M, V = _api(), _gen(8), 37, 1200
+    x, tokens = _rand(g, M, V, std=2).cuda(), torch.randint(-1, V, (M,), generator=g, dtype=torch.int32).cuda()
+    gl, gh = _rand(g, M).cuda(), _rand(g, M).cuda()
+    lp = A.TokenLogprobs(M, V)
+    out = lp.forward(x, tokens, entropy=True, save=True)
+    want = lp.backward(gl, d_entropy=gh)
+    dims = native.LogprobDims(M, V, 0, native.MOE_F32, 0, 0, 0)
+    ref, st = native.ctypes.byref(dims), torch.cuda.current_stream().cuda_stream
+    logprob, entropy, stats, d = (torch.full(s, float("nan"), device="cuda") for s in ((M,), (M,), (2 * M + 8,), (M, V)))
+    native.check(native.lib().moe_token_logprob(x.data_ptr(), tokens.data_ptr(), ref, logprob.data_ptr(), entropy.data_ptr(),
+                                                stats.data_ptr(), None, None, st), "moe_token_logprob")
+    native.check(native.lib().moe_token_logprob_bwd(x.data_ptr(), tokens.data_ptr(), stats.data_ptr(), entropy.data_ptr(),
+                                                    gl.data_ptr(), gh.data_ptr(), ref, d.data_ptr(), st), "moe_token_logprob_bwd")
+    assert torch.equal(logprob, out["logprob"]) and torch.equal(entropy, out["entropy"]) and torch.equal(d, want)
+    assert torch.isnan(stats[2 * M:]).all() and not torch.isnan(stats[:2 * M]).any()

@@ -531,3 +531,27 @@ def test_norm_weights_that_require_gradients_and_modes(lib):
                     ln.forward(x, save=True, stream=ST)
                     assert lib.last("moe_norm_fwd")[2] == w.data_ptr()
                     ln.backward(x, stream=ST)
+
+
+def test_logprob_backward_does_not_read_the_returned_entropy(lib):
+    """It may be changed between the passes (masked, weighted): the backward has its own."""
+    lp = A.TokenLogprobs(6, 50, device=DEV)
+    out = lp.forward(z(4, 50), torch.zeros(4, dtype=torch.int32), entropy=True, save=True, stream=ST)
+    stats = lib.last("moe_token_logprob")[5]
+    lp.backward(z(4), d_entropy=z(4), stream=ST)
+    _, _, kept, entropy, _, _, dims, _, _ = lib.last("moe_token_logprob_bwd")
+    assert kept == stats and entropy is None and dims["keep_entropy"] == lib.last("moe_token_logprob")[2]["keep_entropy"] == 1
+    assert not any(r.data_ptr() <= stats < r.data_ptr() + 4 * r.numel() for r in out.values())
+
+
+def test_logprob_entropy_among_the_statistics():
+    G = GOOD
+    for bad in (-1, 2):
+        d = logprob_dims(keep_entropy=bad)
+        assert L.moe_token_logprob(G, G, REF(d), G, G, G, G, G, None) == DIMS
+        assert L.moe_token_logprob_bwd(G, G, G, G, G, G, REF(d), G, None) == DIMS
+    with_own, kept = logprob_dims(M=0), logprob_dims(M=0, keep_entropy=1)
+    for d in (with_own, kept):
+        assert L.moe_token_logprob_bwd(G, G, G, None, G, G, REF(d), G, None) == 0
+    assert L.moe_token_logprob_bwd(G, G, G, None, G, G, REF(logprob_dims()), G, None) == NULL
+    assert L.moe_token_logprob_bwd(G, G, None, None, G, G, REF(logprob_dims(keep_entropy=1)), G, None) == NULL

@@ -720,7 +720,7 @@ class LayerNorm:
         self.dtype, self.w_dtype = dtype if dtype is not None else weight.dtype, weight.dtype
         (self.N,) = weight.shape
         self.device, self._index = _device(device if device is not None else weight.device)
-        self._size = torch.empty(0, dtype=self.dtype).element_size()
+        self._size, self._w_size = (torch.empty(0, dtype=t).element_size() for t in (self.dtype, self.w_dtype))
         # one for each direction: a call sets what has changed since its last one
         self.dims, self._bwd_dims = (N.NormDims(int(max_rows), self.N, _dt(self.dtype), _dt(self.w_dtype), eps, 0, 0, 0, 0, 0)
                                      for _ in range(2))
@@ -873,6 +873,11 @@ class LayerNorm:
             dw, dwp = views.get(("dw", None)) or self._view("dw", None, stream)
         if "db" in need and b is not None:
             db, dbp = views.get(("db", None)) or self._view("db", None, stream)
+        if 0 < M * self._size <= self._w_size:      # few enough rows to lie in an earlier call's dw or db
+            for name, t, ld in (("x", x, ld_x), ("residual", res, ld_r), ("dy", dy, ld_y), ("d_sum", d_sum, ld_d), ("out", dx, ld_dx)):
+                for g in (dw, db):
+                    if t is not None and g is not None and _bytes_meet(t, ld, g):
+                        raise ValueError(f"{name}: overlaps the weight's or bias's gradient (pass a copy)")
         if self.ws is None:
             self.ws = OpWorkspace(self._need, "moe_norm_workspace_bytes", dev, stream)
         key = M, ld_x, ld_r, ld_d, ld_y, ld_dx

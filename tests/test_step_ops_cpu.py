@@ -555,3 +555,31 @@ def test_logprob_entropy_among_the_statistics():
         assert L.moe_token_logprob_bwd(G, G, G, None, G, G, REF(d), G, None) == 0
     assert L.moe_token_logprob_bwd(G, G, G, None, G, G, REF(logprob_dims()), G, None) == NULL
     assert L.moe_token_logprob_bwd(G, G, None, None, G, G, REF(logprob_dims(keep_entropy=1)), G, None) == NULL
+
+
+def test_norm_refuses_operands_in_its_own_weight_gradients(lib):
+    """dw is written before dx is formed: an earlier call's dw as an operand would be read half overwritten."""
+    for w_dtype, rows in ((F32, 1), (BF, 1), (F32, 2)):
+        dtype = BF if rows == 2 else w_dtype
+        ln = A.LayerNorm(z(64, dtype=w_dtype), z(64, dtype=w_dtype), max_rows=4, dtype=dtype, device=DEV)
+        x, r, dy = (z(rows, 64, dtype=dtype) for _ in range(3))
+        ln.forward(x, save=True, stream=ST)
+        grads = ln.backward(dy, stream=ST)
+        for name in ("dw", "db"):
+            own = grads[name].view(dtype)[:rows * 64].view(rows, 64)
+            calls = len(lib.calls)
+            for kw in (dict(dy=own), dict(dy=dy, d_sum=own), dict(dy=dy, out=own)):
+                with pytest.raises(ValueError, match="gradient"):
+                    ln.backward(stream=ST, **kw)
+            assert len(lib.calls) == calls
+            ln.backward(own, need=("dx",), stream=ST)       # neither is written
+            ln.forward(own, save=True, stream=ST)
+            with pytest.raises(ValueError, match="gradient"):
+                ln.backward(dy, stream=ST)
+            ln.backward(dy, need=("dx",), stream=ST)
+            if dtype == BF:
+                ln.forward(x, residual=own, save=True, stream=ST)
+                with pytest.raises(ValueError, match="gradient"):
+                    ln.backward(dy, stream=ST)
+            ln.forward(x, save=True, stream=ST)
+            ln.backward(own.clone(), stream=ST)

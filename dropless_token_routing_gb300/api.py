@@ -725,12 +725,12 @@ class LayerNorm:
         self.dims, self._bwd_dims = (N.NormDims(int(max_rows), self.N, _dt(self.dtype), _dt(self.w_dtype), eps, 0, 0, 0, 0, 0)
                                      for _ in range(2))
         self._set, self._bwd_set = None, None
+        self._bufs, self._views, self._shapes, self._kept = {}, {}, {}, None
         self._bind()
         self._need = N.lib().moe_norm_workspace_bytes(ctypes.byref(self.dims))
         if self._need == 0:
             raise N.MoeError(N.STATUS_CODE["MOE_ERR_BAD_DIMS"], "moe_norm_workspace_bytes")
         self.ws = None
-        self._bufs, self._views, self._shapes, self._kept = {}, {}, {}, None
         self._dims_ref, self._bwd_ref = ctypes.byref(self.dims), ctypes.byref(self._bwd_dims)
         self._fwd, self._bwd = N.lib().moe_norm_fwd, N.lib().moe_norm_bwd
 
@@ -739,6 +739,10 @@ class LayerNorm:
         _dense(self.weight, "weight", self.w_dtype, (self.N,), self.device)
         if self.bias is not None:
             _dense(self.bias, "bias", self.w_dtype, (self.N,), self.device)
+        for name, t in (("weight", self.weight), ("bias", self.bias)):
+            for buf in self._bufs.values():     # (those made later are other memory)
+                if t is not None and buf.numel() and _bytes_meet(buf.view(1, -1), 0, t):
+                    raise ValueError(f"{name}: lies in a result of this layer (pass a copy)")
         self._w_ptr, self._b_ptr = self.weight.data_ptr(), _p(self.bias)
         self._like = _unchanged(self.weight) if self.bias is None else _unchanged(self.weight, self.bias)
         self._w_ref, self._b_ref = _ref(self.weight), _ref(self.bias)

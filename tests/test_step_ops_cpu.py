@@ -583,3 +583,20 @@ def test_norm_refuses_operands_in_its_own_weight_gradients(lib):
                     ln.backward(dy, stream=ST)
             ln.forward(x, save=True, stream=ST)
             ln.backward(own.clone(), stream=ST)
+
+
+def test_norm_refuses_weights_in_its_own_results(lib):
+    for name in ("weight", "bias"):
+        ln, x = layer_norm(), z(4, 64)
+        y = ln.forward(x, save=True, stream=ST)
+        grads = ln.backward(x, stream=ST)
+        good = getattr(ln, name)
+        for bad in (grads["dw"], grads["db"], y[1], grads["dx"][3]):
+            setattr(ln, name, bad)
+            for call in (lambda: ln.forward(x, stream=ST), lambda: ln.backward(x, stream=ST)):
+                with pytest.raises(ValueError, match="result"):
+                    call()
+            setattr(ln, name, bad.clone())
+            ln.forward(x, save=True, stream=ST)
+        setattr(ln, name, good)
+        ln.forward(x, stream=ST)

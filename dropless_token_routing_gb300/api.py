@@ -928,6 +928,9 @@ class TokenLogprobs:
             top_idx = torch.empty(max_rows, top, dtype=torch.int32, device=device)
             top_logprob = torch.empty(max_rows, top, dtype=torch.float32, device=device)
         self._top = top_idx, top_logprob
+        self._own = self._logprob, self._entropy, top_idx, top_logprob
+        self._most = 4 * max_rows * max(1, top)     # bytes of the largest of them
+        self._size = self.dims.dtype == N.MOE_BF16 and 2 or 4
         self._ptrs = (self._logprob.data_ptr(), self._entropy.data_ptr(), self._stats.data_ptr(),
                       top_idx.data_ptr() if top else None, top_logprob.data_ptr() if top else None)
         self._grad, self._views, self._saved, self._set = None, {}, None, None
@@ -948,6 +951,10 @@ class TokenLogprobs:
         t = scores
         ld = self.V if t.dtype is self.dtype and t.shape == shape and t.is_contiguous() and t.device == dev else _matrix(
             t, "scores", self.dtype, M, self.V, dev)
+        if 0 < M * self.V * self._size <= self._most:   # small enough to lie in an earlier call's results
+            for own in self._own:
+                if own.numel() and _bytes_meet(scores, ld, own):
+                    raise ValueError("scores: overlaps the result (pass a copy)")
         out = {}
         lp, ep, sp, ip, vp = self._ptrs
         if tokens is not None:

@@ -600,3 +600,17 @@ def test_norm_refuses_weights_in_its_own_results(lib):
             ln.forward(x, save=True, stream=ST)
         setattr(ln, name, good)
         ln.forward(x, stream=ST)
+
+
+def test_logprob_refuses_scores_in_its_own_results(lib):
+    lp, x = A.TokenLogprobs(8, 20, top=20, device=DEV), z(4, 20)
+    top = lp.forward(x, stream=ST)["top_logprob"]
+    for bad in (top, top[1:2], top[1:]):
+        with pytest.raises(ValueError, match="overlaps"):
+            lp.forward(bad, stream=ST)
+    lp.forward(top.clone(), stream=ST)
+    one = A.TokenLogprobs(8, 1, device=DEV)
+    out = one.forward(z(8, 1), torch.zeros(8, dtype=torch.int32), entropy=True, stream=ST)
+    for name in ("logprob", "entropy"):
+        with pytest.raises(ValueError, match="overlaps"):
+            one.forward(out[name][:, None], stream=ST)

@@ -1004,9 +1004,11 @@ class TokenLogprobs:
             out, ld_g = self._grad[:M], self.V
         else:
             ld_g = _matrix(out, "out", self.dtype, M, self.V, dev)
-            for name, t in (("tokens", tokens), ("d_logprob", d_logprob), ("d_entropy", d_entropy)):
-                if t is not None and M and _bytes_meet(out, ld_g, t):
-                    raise ValueError(f"out: overlaps {name}")
+        gp = out.data_ptr()     # (the own one may hold an earlier gradient, whose numbers are these)
+        end = gp + M * ld_g * self._size
+        for name, t in (("tokens", tokens), ("d_logprob", d_logprob), ("d_entropy", d_entropy)):
+            if t is not None and gp - 4 * M < t.data_ptr() < end and M and _bytes_meet(out, ld_g, t):
+                raise ValueError(f"{name}: overlaps the scores' gradient")
         _in_place("scores", scores, ld, out, ld_g, "their gradient")
         D.M, D.ld, D.ld_grad = M, ld, ld_g
         self._set = M, ld

@@ -614,3 +614,14 @@ def test_logprob_refuses_scores_in_its_own_results(lib):
     for name in ("logprob", "entropy"):
         with pytest.raises(ValueError, match="overlaps"):
             one.forward(out[name][:, None], stream=ST)
+
+
+def test_logprob_refuses_an_earlier_gradient_as_the_results_gradient(lib):
+    """The scores' gradient is written over it while other rows read it."""
+    lp, t = A.TokenLogprobs(4, 50, device=DEV), torch.zeros(4, dtype=torch.int32)
+    lp.forward(z(4, 50), t, entropy=True, save=True, stream=ST)
+    d = lp.backward(z(4), stream=ST)
+    for kw in (dict(d_logprob=d[0, :4]), dict(d_logprob=z(4), d_entropy=d[3, 46:]), dict(d_logprob=d[1, 3:7], out=d)):
+        with pytest.raises(ValueError, match="overlaps"):
+            lp.backward(stream=ST, **kw)
+    lp.backward(d[0, :4].clone(), d_entropy=d[1, :4], out=z(4, 50), stream=ST)

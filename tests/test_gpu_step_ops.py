@@ -793,3 +793,147 @@ def test_logprob_entropy_where_the_caller_keeps_it():
                                                     gl.data_ptr(), gh.data_ptr(), ref, d.data_ptr(), st), "moe_token_logprob_bwd")
     assert torch.equal(logprob, out["logprob"]) and torch.equal(entropy, out["entropy"]) and torch.equal(d, want)
     assert torch.isnan(stats[2 * M:]).all() and not torch.isnan(stats[:2 * M]).any()
+
+
+# ------------------------------------------------------------------ results in rows of their own distances
+def _nan_rows(M, N, ld, dtype):
+    return torch.full((M, ld), float("nan"), dtype=dtype, device="cuda")[:, :N]
+
+
+def _gaps_are_left(t):
+    M, N = t.shape
+    rest = t._base[:, N:]
+    return bool(torch.isnan(rest).all())
+
+
+ODD = dict(x=3, r=8, y=5, s=1, dy=2, ds=7, dx=9)
+WHOLE = dict(x=0, r=16, y=8, s=24, dy=40, ds=32, dx=48)     # on top of a multiple of 8
+
+
+@pytest.mark.parametrize("dtype,w_dtype", TYPES)
+@pytest.mark.parametrize("pads", [ODD, WHOLE], ids=["odd", "whole"])
+@pytest.mark.parametrize("M,N", [(1, 77), (20, 100), (37, 1001), (200, 264), (2000, 333), (640, 5001), (31, 2048), (9, 8191), (700, 8192),
+                                 (5, 8200), (250, 9000), (3, 12288), (4, 16392)])
+def test_norm_results_in_rows_of_other_distances(M, N, pads, dtype, w_dtype):
+    """Every operand and result has its own distance between rows, and so its own place within 16 bytes; what lies
+    between the results' rows is left as it was. Bounds as in _check_norm; a row of M / 152 to a group of warps adds one
+    rounding each to a column's sum."""
+    A, g = _api(), _gen(M + N)
+    dist = {k: (N + 7 & ~7 if pads is WHOLE else N) + p for k, p in pads.items()}
+    x, r, dy, ds = (_rand(g, M, N, std=std, dtype=dtype) for std in (1, 2, 1, 1))
+    w, b = (1 + 0.3 * _rand(g, N)).to(w_dtype), _rand(g, N, dtype=w_dtype)
+    ops = {k: _strided(t.cuda(), dist[k]) for k, t in dict(x=x, r=r, dy=dy, ds=ds).items()}
+    ln = A.LayerNorm(w.cuda(), b.cuda(), max_rows=M, dtype=dtype)
+    big = lambda v: v.abs().amax(1, keepdim=True)  # noqa: E731
+    rows = 96 + M // 152
+    for residual in (True, False):
+        y, sm, dx = (_nan_rows(M, N, dist[k], dtype) for k in ("y", "s", "dx"))
+        if residual:
+            got = ln.forward(ops["x"], residual=ops["r"], save=True, out=y, sum_out=sm)
+            assert got[0] is y and got[1] is sm
+        else:
+            assert ln.forward(ops["x"], save=True, out=y) is y
+        s, mean, rstd, ref = _norm_ref(x, r if residual else None, w, b, 1e-5)
+        spread = big(s) * rstd + 1
+        _near(y, ref, dtype, spread * w.double().abs() + b.double().abs(), what="y")
+        if residual:
+            _near(sm, s, dtype, s.abs(), steps=2, what="sum")
+        grads = ln.backward(ops["dy"], d_sum=ops["ds"] if residual else None, out=dx)
+        assert grads["dx"] is dx
+        kept = sm.cpu() if residual and dtype == F32 else s
+        xh, u, want, dw, db = _norm_grads(kept, mean, rstd, w, dy, ds if residual else None)
+        _near(dx, want, dtype, rstd * big(u) * (1 + big(xh)) * (1 + spread) + (ds.double().abs() if residual else 0), what="dx")
+        _near(grads["dw"], dw, w_dtype, (dy.double().abs() * (xh.abs() + spread)).sum(0), steps=rows, what="dw")
+        _near(grads["db"], db, w_dtype, dy.double().abs().sum(0), steps=rows, what="db")
+        assert all(map(_gaps_are_left, (y, sm, dx)))
+        # the same in the operands' places (rows of the same distances there: the same kernels, the same bits)
+        at = {k: _strided(t.cuda(), dist[k]) for k, t in dict(x=x, r=r, dy=dy, ds=ds).items()}
+        y2, sm2 = _nan_rows(M, N, dist["x"], dtype), _nan_rows(M, N, dist["r"], dtype)
+        if residual:
+            ln.forward(ops["x"], residual=ops["r"], out=y2, sum_out=sm2)
+            ln.forward(at["x"], residual=at["r"], out=at["x"], sum_out=at["r"])
+            assert torch.equal(at["r"], sm2) and _gaps_are_left(at["r"])
+        else:
+            ln.forward(ops["x"], out=y2)
+            ln.forward(at["x"], out=at["x"])
+        assert torch.equal(at["x"], y2) and _gaps_are_left(at["x"])
+        ln.forward(ops["x"], save=True)
+        dx2 = _nan_rows(M, N, dist["dy"], dtype)
+        d2 = ops["ds"] if residual else None
+        want = {k: v.clone() for k, v in ln.backward(ops["dy"], d_sum=d2, out=dx2).items()}
+        got = ln.backward(at["dy"], d_sum=d2, out=at["dy"])
+        assert all(torch.equal(got[k], want[k]) for k in want) and _gaps_are_left(at["dy"])
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("M,V,ld,ld_d", [(1, 1001, 1001, 1013), (5, 1000, 1008, 1003), (21, 1001, 1003, 1001), (9, 4099, 5000, 4101),
+                                         (3, 50001, 50048, 50001), (300, 777, 777, 784), (4, 131072, 131072, 131075)])
+def test_logprob_gradient_in_rows_of_another_distance(M, V, ld, ld_d, dtype):
+    """Each gradient is a function of its score and the row's statistics: the same bits wherever it goes."""
+    A, g = _api(), _gen(M + V)
+    x, tokens = _rand(g, M, V, std=2, dtype=dtype).cuda(), torch.randint(-1, V, (M,), generator=g, dtype=torch.int32).cuda()
+    gl, gh = _rand(g, M).cuda(), _rand(g, M).cuda()
+    gl[M // 2], gh[M // 2] = 0, 0       # a row that is not read
+    lp = A.TokenLogprobs(M, V, dtype=dtype)
+    lp.forward(_strided(x, ld), tokens, entropy=True, save=True)
+    want = lp.backward(gl, d_entropy=gh).clone()
+    out = _nan_rows(M, V, ld_d, dtype)
+    assert lp.backward(gl, d_entropy=gh, out=out) is out
+    assert torch.equal(out, want) and (ld_d == V or _gaps_are_left(out)) and not want[M // 2].any()
+
+
+@pytest.mark.parametrize("sign", [False, True])
+def test_norm_weight_gradients_of_many_rows_to_a_group(sign):
+    """60000 rows, 395 to a block: a column's sum takes that many roundings in a row, then one of each block and a
+    few; of gradients of one sign too, whose sums only grow."""
+    A, M, N = _api(), 60000, 5000
+    gen = torch.Generator("cuda").manual_seed(3)
+    x, dy = (torch.randn(M, N, dtype=BF, device="cuda", generator=gen) for _ in range(2))
+    if sign:
+        dy.abs_()
+    w = torch.ones(N, device="cuda")
+    ln = A.LayerNorm(w, w.clone(), max_rows=M, dtype=BF)
+    ln.forward(x, save=True)
+    grads = ln.backward(dy, need=("dw", "db"))
+    ref = [torch.zeros(N, dtype=torch.float64, device="cuda") for _ in range(4)]
+    for i in range(0, M, 4000):
+        s, d = x[i:i + 4000].double(), dy[i:i + 4000].double()
+        mean = s.mean(1, keepdim=True)
+        rstd = 1 / torch.sqrt(((s - mean) ** 2).mean(1, keepdim=True) + 1e-5)
+        xh, spread = (s - mean) * rstd, s.abs().amax(1, keepdim=True) * rstd + 1
+        for t, v in zip(ref, (d * xh, d, d.abs() * (xh.abs() + spread), d.abs())):
+            t += v.sum(0)
+    dw, db, dw_terms, db_terms = (t.cpu() for t in ref)
+    _near(grads["dw"], dw, F32, dw_terms, steps=96 + M // 152, what="dw")
+    _near(grads["db"], db, F32, db_terms, steps=96 + M // 152, what="db")
+
+
+def test_step_operators_look_at_their_tensors_again():
+    """Another type or order at the address of before: taken as it is, or refused; nothing behind it is touched."""
+    A = _api()
+    buf = torch.full((1000,), 3.0, device="cuda")
+    t = buf[:500]
+    clip = A.GradClipper([t])
+    clip.norm()
+    t.data = buf.view(BF)[:500]             # 1000 of the 4000 bytes
+    before = buf.clone()
+    ref = math.sqrt(float((t.double() ** 2).sum()))
+    assert abs(float(clip.clip(1.0)) - ref) <= 40 * H * ref
+    assert torch.equal(buf[250:], before[250:])
+    _near(t, before.view(BF)[:500].cpu().double() / (ref + 1e-6), BF, before.view(BF)[:500].cpu().double() / ref, steps=48)
+    m, out = torch.ones(64, 64, device="cuda"), torch.zeros(64, 64, device="cuda")
+    clip = A.GradClipper([m], out=[out])
+    clip.clip(1.0)
+    m.data = m.data.t()
+    with pytest.raises(ValueError):
+        clip.clip(1.0)
+    w, x = torch.ones(64, device="cuda"), torch.randn(3, 64, device="cuda")
+    ln = A.LayerNorm(w, max_rows=3)
+    ln.forward(x)
+    here = w.data
+    for other in (here[:63], here.view(torch.int32), here.view(BF)[:64]):
+        w.data = other
+        with pytest.raises(ValueError):
+            ln.forward(x)
+    w.data = here
+    ln.forward(x)

@@ -5,7 +5,7 @@
 //   ln p_j = x_j - m - ln S,  H = ln S - D / S
 //   d_x_j = g ([j = token] - p_j) - h p_j (ln p_j + H)      g, h: gradients of ln p_token and H
 //
-// One pass over a row with the running maximum: a thread takes 32 scores at a time, and its sums
+// One pass over a row with the running maximum: a thread takes 16 scores at a time (of few rows 32), and its sums
 // move to the new maximum when these hold one. Differences x - m are formed before the exponential,
 // so scores of any size (a mask of the type's lowest value among them) keep their meaning: -inf is no
 // token, a row of nothing else has no distribution (S = 0).
@@ -484,8 +484,11 @@ __global__ void __launch_bounds__(LT, (kBlocks<T, LU, ENT, TOP>)) logprob_kernel
 constexpr int GU = 4, GC = GU * LT * 8;   // the same of the gradient
 
 // Rows from the last one back: where the gradient follows the forward pass at once, as a loss's does, L2 still
-// holds the rows read last (4096 x 32000 fp32: both 236 us from the first row on, 233 so).
-// Bound by HBM: 8192 x 131072 bf16 599 us, 4096 x 32000 fp32 with entropy 150 us, both 7.0-7.2 TB/s.
+// holds some of the rows read last (4096 x 32000 fp32: both 236 us from the first row on, 233 so; of 2048 x 32000, 262 MB, 32
+// are not read again).
+// Bound by HBM: 8192 x 131072 bf16 627 us, 4096 x 32000 fp32 with entropy 156 us, both 6.7-6.9 TB/s; with a tenth of the rows
+// padding, which are not read, 599 and 150. Rows of the gradient that begin at another place within 16 bytes than the
+// scores' go out by single elements: 4096 x 50001 bf16 126 us, from rows 50048 apart 514.
 template <typename T>
 __global__ void __launch_bounds__(LT) logprob_bwd_kernel(const LogprobBwdArgs a) {
   pdl_start();

@@ -5,8 +5,10 @@
 //   u = dy w,  xh = (s - mean) rstd,  dx = rstd (u - mean(u) - xh mean(u xh)) (+ d_sum)
 //   dw = sum_m dy xh,  db = sum_m dy
 //
-// A row stays on the SM between its sums and its way out, so every operand is read once; the
-// variance is that of the centred values (no difference of large numbers). All of it is bound by HBM.
+// A row stays on the SM between its sums and its way out, so every operand is read once, but for the backward
+// of up to kFewRows rows and of the widest ones, where dw and db are another kernel's, which reads x, the residual and dy
+// again. The variance is that of the centred values (no difference of large numbers). Many rows that begin on 16 bytes are
+// bound by HBM; few rows, and those that begin anywhere, by latency.
 //
 // Rows of up to 8192 elements (bf16: 16384) are taken by groups of warps, 16 elements (32) to a thread, in a
 // persistent block of up to 16 warps; wider ones by a block each. A thread copies its own elements of the
@@ -307,8 +309,9 @@ struct Group {
 };
 
 // y (and the sum). Two sums for each row, the second of centred values, each a barrier of the row's group, which takes R
-// rows at a time; 100 to 126 registers. 8192 x 7680 bf16 with a residual: 76 us, 6.6 TB/s, HBM; 4096 x 2048 13.2 us, of
-// which 3 are its two ends; one row 2.6 us.
+// rows at a time; 94 to 128 registers. 8192 x 7680 bf16 with a residual: 76 us, 6.6 TB/s, HBM; 4096 x 2048 13.2 us, of
+// which 3 are its two ends; one row 2.6 us. Rows that begin anywhere: 8190 x 5001 with a residual 111 us, floor 48: issue
+// slots 47 % busy, DRAM 23 %, shared memory 31 %, ten warps on an SM that wait for one another and for their own shifts.
 template <typename T, typename W, int MODE, int E, bool RES, int R>
 __global__ void __launch_bounds__(kRowThreads, 1) norm_fwd_rows(const NormArgs a, int warps, int stages) {
   extern __shared__ uint4 ring[];
@@ -445,6 +448,10 @@ __global__ void __launch_bounds__(kRowThreads, 1) norm_fwd_rows(const NormArgs a
 // dx, and a block's partial sums of dw and db. x, dy, then the residual (RES) and d_sum (DS) are the operands of a
 // stage; the next rows' mean and rstd are asked for a step ahead (86 us, 94 without, at 8192 x 7680 with three operands). One
 // barrier for R rows. 8192 x 7680 bf16, four operands: 89 us, 7.0 TB/s, HBM; 97 with the sums' join.
+// Rows that begin anywhere: 8190 x 5001 152 us, floor 60, by latency as the forward's. A column's sum takes a group's rows one
+// after the other in fp32, M / (blocks x groups) roundings in a row at most, and one for each block in the join.
+// 126 to 128 registers, all that 512 threads have: 37 of the 64 forms spill, mostly 4 to 16 bytes a thread, those of 32
+// elements with every unit up to 160, that of four unaligned fp32 operands (no call of the Python layer) 256.
 template <typename T, typename W, int MODE, int E, bool RES, bool DS, int R>
 __global__ void __launch_bounds__(kRowThreads, 1) norm_bwd_rows(const NormBwdArgs a, int warps, int stages) {
   extern __shared__ uint4 ring[];
@@ -655,7 +662,8 @@ RowMode row_mode(int N, bool vec, int unit, int each) { return !vec || N % unit 
 template <typename T> bool thick(int N, bool vec) { return sizeof(T) == 2 && vec && N % 8 == 0 && N > kRowsMaxN && N <= kThickMaxN; }
 
 // ------------------------------------------------------------------ wide rows
-// A block for a row, in registers. 4000 x 16384 bf16 (now with 32 elements to a thread above) took 124 us, 4.2 TB/s: a
+// A block for a row, in registers: bf16 rows above 16384 elements, fp32 rows above 8192, unaligned ones above 8192. 2000 x
+// 32768 bf16 145 us with a residual (3.6 TB/s, floor 77), 90 without (39); 4000 x 12288 fp32 143 (116) and 107 (58): a
 // block's loads stop while it adds.
 template <typename T, typename W, bool VEC>
 __global__ void __launch_bounds__(1024) norm_fwd_wide(const NormArgs a) {
@@ -716,7 +724,9 @@ __global__ void __launch_bounds__(1024) norm_fwd_wide(const NormArgs a) {
   }
 }
 
-// dx alone, the same way: 139 us at that size, and 126 for the columns below.
+// dx alone, the same way. With the columns below, which read x, the residual and dy too: 2000 x 32768 bf16 332 us with a
+// residual (eight passes 155, the floor's five 97), 247 without; 4000 x 12288 fp32 264 and 223. 1024 threads have 64 registers
+// each: 76 to 308 bytes a thread are spilled.
 template <typename T, typename W, bool VEC>
 __global__ void __launch_bounds__(1024) norm_dx_wide(const NormBwdArgs a) {
   __shared__ float sums[64];

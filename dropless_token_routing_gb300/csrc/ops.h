@@ -126,7 +126,7 @@ struct NormBwdArgs {
   const void *x, *res, *dy, *d_sum, *w;
   const float* stats;
   void *dx, *dw, *db;
-  float* part;       // [parts][2][N] partial sums of the columns
+  float* part;       // [parts][2][N, rounded up to 4] partial sums of the columns
   int64_t M, ld_x, ld_res, ld_dy, ld_ds, ld_dx;
   int N;
   float inv_n;

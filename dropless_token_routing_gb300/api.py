@@ -878,11 +878,13 @@ class LayerNorm:
             dw, dwp = views.get(("dw", None)) or self._view("dw", None, stream)
         if "db" in need and b is not None:
             db, dbp = views.get(("db", None)) or self._view("db", None, stream)
-        if 0 < M * self._size <= self._w_size:      # few enough rows to lie in an earlier call's dw or db
-            for name, t, ld in (("x", x, ld_x), ("residual", res, ld_r), ("dy", dy, ld_y), ("d_sum", d_sum, ld_d), ("out", dx, ld_dx)):
-                for g in (dw, db):
-                    if t is not None and g is not None and _bytes_meet(t, ld, g):
-                        raise ValueError(f"{name}: overlaps the weight's or bias's gradient (pass a copy)")
+        if 0 < row <= self._w_size:     # few enough rows to lie in an earlier call's dw or db
+            end = n * self._w_size
+            for g in (dwp, dbp):
+                if g is not None and (-row * ld_x < xp - g < end or -row * ld_y < yp - g < end or (
+                        rp is not None and -row * ld_r < rp - g < end) or (sp is not None and -row * ld_d < sp - g < end) or (
+                        dxp is not None and -row * ld_dx < dxp - g < end)):
+                    raise ValueError("x, residual, dy, d_sum or out: lies in the weight's or bias's gradient (pass a copy)")
         if self.ws is None:
             self.ws = OpWorkspace(self._need, "moe_norm_workspace_bytes", dev, stream)
         key = M, ld_x, ld_r, ld_d, ld_y, ld_dx

@@ -625,3 +625,44 @@ def test_logprob_refuses_an_earlier_gradient_as_the_results_gradient(lib):
         with pytest.raises(ValueError, match="overlaps"):
             lp.backward(stream=ST, **kw)
     lp.backward(d[0, :4].clone(), d_entropy=d[1, :4], out=z(4, 50), stream=ST)
+
+
+@pytest.mark.parametrize("mode", [torch.no_grad, torch.inference_mode, lambda: torch.autocast("cpu", dtype=BF)])
+def test_kept_tensors_in_other_modes(lib, mode):
+    """Calls inside and outside of a mode, in turn: the same tensors, the same pointers."""
+    a, w, x = z(10), z(64), z(4, 64)
+    k, ln = clipper([a]), A.LayerNorm(w, w.clone(), max_rows=4, device=DEV)
+    for _ in range(2):
+        with mode():
+            k.clip(1.0, stream=ST)
+            ln.forward(x, save=True, stream=ST)
+            ln.backward(x, stream=ST)
+        k.norm(stream=ST)
+        ln.forward(x, save=True, stream=ST)
+        ln.backward(x, stream=ST)
+    a.requires_grad_()
+    k.clip(1.0, stream=ST)
+    assert {v[0][0][0] for n, v in lib.calls if n == "moe_clip_grads"} == {a.data_ptr()}
+    assert {v[2] for n, v in lib.calls if n == "moe_norm_fwd"} == {w.data_ptr()}
+
+
+def test_kept_tensors_where_torch_has_no_check_of_many(lib, monkeypatch):
+    """Each is asked then: a change is found as well, and none is where there is none."""
+    monkeypatch.delattr(torch._C._dynamo.guards, "TensorGuards")
+    monkeypatch.setattr(A, "_addresses_are", None)
+    a, w, x = z(10), z(64), z(4, 64)
+    k, ln = clipper([a]), A.LayerNorm(w, max_rows=4, device=DEV)
+    bound = k._places
+    for _ in range(2):
+        k.clip(1.0, stream=ST)
+        ln.forward(x, stream=ST)
+    assert k._places is bound
+    here = a.data
+    a.data = here.view(BF)[:10]
+    k.clip(1.0, stream=ST)
+    assert lib.last("moe_clip_grads")[0][0] == (a.data_ptr(), a.data_ptr(), 10, N.MOE_BF16)
+    a.data = z(20)[::2]
+    w.data = w.data[:63]
+    for call in (lambda: k.norm(stream=ST), lambda: ln.forward(x, stream=ST)):
+        with pytest.raises(ValueError):
+            call()

@@ -913,11 +913,11 @@ class TokenLogprobs:
 
     ``forward(scores, tokens=None, entropy=False, save=False)`` returns a dict of ``logprob`` [M] (with
     tokens), ``entropy`` [M] (if asked for), ``top_idx`` and ``top_logprob`` [M, top] (if top > 0): own
-    buffers, written by the next call (they may be changed, the backward does not read them). A token outside [0, V) is padding (0). With ``save=True`` it keeps
-    scores and tokens (unchanged until then) for ``backward(d_logprob=None, d_entropy=None)``, which returns the
+    buffers, written by the next call (they may be changed, the backward does not read them). A token outside
+    [0, V) is padding (0). With ``save=True`` it keeps scores and tokens (unchanged until then) for ``backward(d_logprob=None, d_entropy=None)``, which returns the
     gradient of the scores [M, V]: an own buffer unless ``out`` is given, which may be the scores (what was kept is
-    then gone). Scores and their gradient begin on 16 bytes, their rows anywhere (fastest where both do alike). One instance
-    serves one stream at a time, which waits for the one it was made on.
+    then gone). Scores and their gradient begin on 16 bytes, their rows anywhere (fastest where both
+    do alike). One instance serves one stream at a time, which waits for the one it was made on.
     """
 
     def __init__(self, max_rows, V, top=0, dtype=torch.float32, device="cuda", stream=None):
@@ -931,7 +931,7 @@ class TokenLogprobs:
             top_idx = torch.empty(max_rows, top, dtype=torch.int32, device=device)
             top_logprob = torch.empty(max_rows, top, dtype=torch.float32, device=device)
         self._top = top_idx, top_logprob
-        self._own = self._logprob, self._entropy, top_idx, top_logprob
+        self._own = tuple((t.data_ptr(), 4 * t.numel()) for t in (self._logprob, self._entropy, top_idx, top_logprob) if t.numel())
         self._most = 4 * max_rows * max(1, top)     # bytes of the largest of them
         self._size = 2 if self.dims.dtype == N.MOE_BF16 else 4
         self._ptrs = (self._logprob.data_ptr(), self._entropy.data_ptr(), self._stats.data_ptr(),
@@ -955,9 +955,10 @@ class TokenLogprobs:
         ld = self.V if t.dtype is self.dtype and t.shape == shape and t.is_contiguous() and t.device == dev else _matrix(
             t, "scores", self.dtype, M, self.V, dev)
         if 0 < M * self.V * self._size <= self._most:   # small enough to lie in an earlier call's results
-            for own in self._own:
-                if own.numel() and _bytes_meet(scores, ld, own):
-                    raise ValueError("scores: overlaps the result (pass a copy)")
+            xp, span = scores.data_ptr(), M * ld * self._size
+            for p, size in self._own:
+                if p - span < xp < p + size:
+                    raise ValueError("scores: lies in a result, or overlaps it (pass a copy)")
         out = {}
         lp, ep, sp, ip, vp = self._ptrs
         if tokens is not None:

@@ -479,8 +479,8 @@ int moe_norm_fwd(const void* x, const void* residual, const void* weight, const 
  * bf16 the sum was rounded, which costs dw about what rounding it to bf16 does). stats as moe_norm_fwd
  * wrote them.
  * dx [M, N], dw [N], db [N]: each may be NULL (not computed); weight is needed for dx. Sums are fp32 in
- * a fixed order (dw and db: up to M / 152 rows, those of an SM, one after the other, each rounded). dx may be the buffer of dy, x, residual or d_sum when their strides agree; the results overlap
- * nothing else. With M == 0 dw and db are zeroed. A workspace for M rows serves fewer. ws:
+ * a fixed order (dw and db: up to M / 152 rows, those of an SM, one after the other, each rounded). dx
+ * may be the buffer of dy, x, residual or d_sum when their strides agree; the results overlap nothing else. With M == 0 dw and db are zeroed. A workspace for M rows serves fewer. ws:
  * moe_op_workspace_init's. */
 size_t moe_norm_workspace_bytes(const moe_norm_dims* dims);
 int moe_norm_bwd(const void* x, const void* residual, const void* dy, const void* d_sum, const void* weight,
